@@ -76,7 +76,9 @@ typedef enum {
 #define SPD_DEV_BAD_LEN 0x8u   /* seq_lens[b] outside [0, max_pages_per_seq * page_size] (the row is
                                 * then treated as empty: nothing selected, o = 0, lse = -inf), or
                                 * too short for the tokens being appended */
-#define SPD_DEV_BAD_TOKEN 0x10u /* spec_accept: a drafted token outside [0, n_vocab) */
+#define SPD_DEV_BAD_TOKEN 0x10u /* spec_accept: a drafted token outside [0, n_vocab);
+                                 * token_logprobs: a target outside [-1, n_vocab) */
+#define SPD_DEV_BAD_POS 0x20u   /* a position outside the rotation's table */
 
 /*
  * Problem shape.  Supported: D in {64, 128}; page_size in {16, 32, 64};
@@ -392,6 +394,158 @@ spd_status spec_accept(int32_t B, int32_t k, int32_t n_vocab, const float *p_dra
  */
 spd_status lse_merge(int32_t S, int32_t rows, int32_t D, const float *part_o,
                      const float *part_lse, spd_bf16 *o, float *lse, void *stream);
+
+/*
+ * spd_rope -- norm of each head's row and position rotation of queries and keys
+ * (what the Qwen3 shapes of the rollout studies do between the projection and the
+ * attention).  A head row x of D channels becomes
+ *   y = x / sqrt(mean(x^2) + eps) * weight          (no norm where weight is NULL)
+ * and then, for i < rot_dim / 2 and the angle of the row's position and of i,
+ *   (y[a], y[b]) -> (y[a] cos - y[b] sin, y[b] cos + y[a] sin),
+ * (a, b) = (i, i + rot_dim / 2), or (2i, 2i + 1) with interleaved != 0; channels
+ * from rot_dim on are not rotated.  Everything is fp32, rounded to bf16 once.
+ * Supported: rot_dim a multiple of 8 in [0, D]; table fp32 [n_pos][2][rot_dim / 2],
+ * the cosines of a position and then its sines, 16-byte aligned (rot_dim = 0: not
+ * read, may be NULL); weights bf16 [D], 8-byte aligned; eps >= 0 and finite.
+ */
+typedef struct {
+    const float *table;
+    int32_t n_pos;
+    int32_t rot_dim;
+    int32_t interleaved;
+    float eps;
+    const spd_bf16 *q_weight; /* NULL: queries without a norm */
+    const spd_bf16 *k_weight; /* NULL: keys without a norm */
+} spd_rope;
+
+/*
+ * qk_norm_rope -- norm and rotation of the queries and keys of `rows` tokens in one
+ * pass: q_out[row][h] and k_out[row][h] from q and k at positions[row] (int32).
+ *
+ * q: rows of H_q * D contiguous bf16, q_stride elements apart (k likewise, H_kv and
+ * k_stride), so both may be views of one fused projection; strides multiples of 8,
+ * at least the row's length.  q or k may be NULL: that side is skipped.  q_out bf16
+ * [rows][H_q][D], k_out bf16 [rows][H_kv][D]; an output may be its own input where
+ * that is contiguous, and must not overlap an input otherwise.  Pointers 16-byte
+ * aligned.  A position outside [0, n_pos) sets SPD_DEV_BAD_POS and gives zero rows
+ * (with rot_dim = 0 the positions are not read and may be NULL).
+ * Supported: D in {64, 128}; any H_q, H_kv >= 1; rows >= 0 (0: no-op).
+ */
+spd_status qk_norm_rope(int64_t rows, int32_t H_q, int32_t H_kv, int32_t D, const spd_rope *rope,
+                        const spd_bf16 *q, int64_t q_stride, const spd_bf16 *k, int64_t k_stride,
+                        const int32_t *positions, spd_bf16 *q_out, spd_bf16 *k_out, void *stream);
+
+/*
+ * kv_append_rope -- kv_append_refresh of the normalised and rotated keys, and the
+ * queries of the same tokens, in one kernel: what a layer does between its projection
+ * and pages_score_select or dense_verify_attn.
+ *
+ * Token t (0 <= t < T) of sequence b is row b * T + t of q, k and v (strided rows as
+ * in qk_norm_rope; v_stride elements apart) and has position seq_lens[b] - T + t.
+ * K, V and summ afterwards, and q_out bf16 [B][T][H_q][D], are bit for bit what
+ * qk_norm_rope at those positions and kv_append_refresh give.  q and q_out may both
+ * be NULL (keys and values only).
+ * Supported: 1 <= T <= 4096.  A sequence with seq_lens[b] < T or seq_lens[b] >
+ * max_pages_per_seq * page_size sets SPD_DEV_BAD_LEN, one with seq_lens[b] > n_pos
+ * (where rot_dim > 0) sets SPD_DEV_BAD_POS: its cache is left as it was and its q_out
+ * rows are zeros.  A page id outside [0, num_phys_pages) sets SPD_DEV_BAD_PAGE and
+ * skips that page's tokens.  Sequences must not share the pages they append to.
+ */
+spd_status kv_append_rope(const spd_dims *dims, int32_t T, const spd_rope *rope, spd_bf16 *K,
+                          spd_bf16 *V, const int32_t *page_table, const int32_t *seq_lens,
+                          const spd_bf16 *q, int64_t q_stride, const spd_bf16 *k, int64_t k_stride,
+                          const spd_bf16 *v, int64_t v_stride, spd_bf16 *q_out, spd_bf16 *summ,
+                          void *stream);
+
+/*
+ * The 4-bit paged cache.  kv4 is bytes [num_phys_pages][H_kv][2][page_size * D * 9 / 16],
+ * 16-byte aligned: for each page and KV head the keys (0) and the values (1), each
+ * page_size rows of D / 2 code bytes (row-major, channel 2j in the low and channel
+ * 2j + 1 in the high four bits of byte j) and then page_size rows of D / 16 scale
+ * bytes, one for each group of 16 channels.  4.5 bits an element.
+ *
+ * A code is an e2m1 number (sign, 2 exponent bits, 1 mantissa bit: 0, 0.5, 1, 1.5, 2,
+ * 3, 4, 6), a scale an e4m3 number, and the value is code * scale * 2^exp, exp being
+ * k_exp for keys and v_exp for values: exact in bf16.  exp is the caller's, one for
+ * the whole cache, -64 <= exp <= 64; it should bring the values' largest magnitudes
+ * near 2^exp * 100, well inside the scales' range [2^-9, 448] (0 suits keys and values
+ * of unit size; a cache of small values wants a negative v_exp).
+ * Page tables, seq_lens and the summaries are those of the bf16 cache, so
+ * pages_score_select serves both.
+ */
+
+/*
+ * kv4_append -- quantises the T newest tokens of every sequence into the cache and
+ * rewrites the summaries of the pages they land in (min / max of the values as held,
+ * so the scores bound the logits of the 4-bit attention).
+ *
+ * k_new, v_new: bf16 [B][T][H_kv][D]; positions, errors and limits as
+ * kv_append_refresh.  A group's scale is amax / (6 * 2^exp) rounded to the nearest
+ * e4m3 number, at most 448; codes are x / (scale * 2^exp) rounded to the nearest e2m1
+ * number (ties to the even code), at most 6 in magnitude; a zero scale gives zeros.
+ * Infinities saturate; NaN counts as zero.
+ */
+spd_status kv4_append(const spd_dims *dims, int32_t T, uint8_t *kv4, int32_t k_exp, int32_t v_exp,
+                      const int32_t *page_table, const int32_t *seq_lens, const spd_bf16 *k_new,
+                      const spd_bf16 *v_new, spd_bf16 *summ, void *stream);
+
+/*
+ * kv4_read -- the T newest tokens of every sequence as the values that the cache
+ * holds: k_out, v_out bf16 [B][T][H_kv][D], exact.  For checks against the unquantised
+ * rows and for moving a cache to bf16.  Limits as kv4_append; the rows of a sequence
+ * or page that is skipped there are zeros.
+ */
+spd_status kv4_read(const spd_dims *dims, int32_t T, const uint8_t *kv4, int32_t k_exp, int32_t v_exp,
+                    const int32_t *page_table, const int32_t *seq_lens, spd_bf16 *k_out,
+                    spd_bf16 *v_out, void *stream);
+
+/*
+ * kv4_sparse_decode_attn / kv4_dense_verify_attn -- sparse_decode_attn and
+ * dense_verify_attn over the 4-bit cache: arguments, limits, errors and results as
+ * there, over the values that the cache stands for.  Workspaces by the sizes below
+ * (zero before the first use, left zero).
+ */
+size_t spd_kv4_sparse_decode_workspace_size(const spd_dims *dims, int32_t k_max, int32_t num_splits);
+size_t spd_kv4_dense_verify_workspace_size(const spd_dims *dims, int32_t T, int32_t num_splits);
+spd_status kv4_sparse_decode_attn(const spd_dims *dims, const spd_bf16 *q, const uint8_t *kv4,
+                                  int32_t k_exp, int32_t v_exp, const int32_t *page_table,
+                                  const int32_t *seq_lens, const int32_t *sel, const int32_t *nsel,
+                                  int32_t k_max, int32_t num_splits, float softmax_scale, spd_bf16 *o,
+                                  float *lse, void *ws, size_t ws_bytes, void *stream);
+spd_status kv4_dense_verify_attn(const spd_dims *dims, int32_t T, const spd_bf16 *q,
+                                 const uint8_t *kv4, int32_t k_exp, int32_t v_exp,
+                                 const int32_t *page_table, const int32_t *seq_lens,
+                                 int32_t num_splits, float softmax_scale, spd_bf16 *o, float *lse,
+                                 void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * token_logprobs -- log probabilities of given tokens, one pass over their logits: the
+ * sampled tokens' behaviour probabilities of a rollout, or those of spec_accept's
+ * output (tokens [B][k+1] against the target's logits [B][k+1][n_vocab]).
+ *
+ * logits: `rows` rows of n_vocab numbers (fp32, or bf16 with logits_bf16 != 0),
+ * row_stride elements apart, row_stride >= n_vocab.  With z = inv_temperature * logits:
+ *   lse[row] = log sum_x exp z(x),   logprob[row] = z(targets[row]) - lse[row],
+ *   entropy[row] = -sum_x p(x) log p(x),  p = exp(z - lse),
+ * and the top_k largest logits (ties: the lower token first) as top_ids int32
+ * [rows][top_k] with top_logprobs fp32 [rows][top_k], in descending order.
+ * logprob, entropy and lse are fp32 and may each be NULL; top_ids and top_logprobs go
+ * together and are NULL with top_k = 0.
+ * targets int32: -1 (no token, as behind spec_accept's last one) gives logprob 0; any
+ * other target outside [0, n_vocab) gives 0 too and sets SPD_DEV_BAD_TOKEN.  targets
+ * may be NULL with logprob.
+ * A logit of -inf (a masked token) has probability 0, logprob -inf and is never an
+ * alternative: where fewer than top_k logits are above -inf the rest is id -1, logprob
+ * -inf.  A row with no logit above -inf has lse = -inf, logprob = -inf, entropy = 0.
+ * A NaN makes its row's lse, logprob and entropy NaN and is never an alternative.
+ * Supported: 1 <= n_vocab <= 2^21, 0 <= top_k <= 32, inv_temperature > 0 and finite,
+ * 0 <= rows < 2^31 (0: no-op); logits aligned to their type.
+ */
+size_t spd_token_logprobs_workspace_size(int64_t rows, int32_t n_vocab, int32_t top_k);
+spd_status token_logprobs(int64_t rows, int32_t n_vocab, const void *logits, int32_t logits_bf16,
+                          int64_t row_stride, const int32_t *targets, float inv_temperature,
+                          float *logprob, float *entropy, float *lse, int32_t top_k, int32_t *top_ids,
+                          float *top_logprobs, void *ws, size_t ws_bytes, void *stream);
 
 /*
  * spd_round -- one S3R round captured as CUDA graphs: k sparse draft steps,

@@ -23,7 +23,11 @@ __all__ = [
     "lse_merge", "spec_accept", "spd_device_status", "spd_score_select_workspace_size",
     "spd_sparse_decode_workspace_size", "spd_dense_verify_workspace_size",
     "spd_sparse_decode_step_workspace_size", "spd_set_wait_limit_ns", "spd_wait_limit_ns",
-    "DEV_BAD_PAGE", "DEV_BAD_SEL", "DEV_TIMEOUT", "DEV_BAD_LEN", "DEV_BAD_TOKEN",
+    "DEV_BAD_PAGE", "DEV_BAD_SEL", "DEV_TIMEOUT", "DEV_BAD_LEN", "DEV_BAD_TOKEN", "DEV_BAD_POS",
+    "Rope", "qk_norm_rope", "kv_append_rope", "kv4_cache", "kv4_append", "kv4_read",
+    "kv4_sparse_decode_attn", "kv4_dense_verify_attn", "token_logprobs",
+    "spd_kv4_sparse_decode_workspace_size", "spd_kv4_dense_verify_workspace_size",
+    "spd_token_logprobs_workspace_size",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -31,6 +35,7 @@ LIB_PATH = os.path.join(_HERE, "libspd.so")
 
 # device status bits (SPD_DEV_* in include/spd.h)
 DEV_BAD_PAGE, DEV_BAD_SEL, DEV_TIMEOUT, DEV_BAD_LEN, DEV_BAD_TOKEN = 0x1, 0x2, 0x4, 0x8, 0x10
+DEV_BAD_POS = 0x20
 _STATUS = {0: "OK", 1: "INVALID_ARG", 2: "UNSUPPORTED", 3: "CUDA", 4: "WORKSPACE"}
 _MODES = {"fixed": 0, "linear": 1, "fraction": 2, "top_p": 3}
 
@@ -54,6 +59,12 @@ class Policy(ctypes.Structure):
                 ("frac_num", ctypes.c_int64), ("frac_den", ctypes.c_int64),
                 ("sink_pages", ctypes.c_int32), ("local_pages", ctypes.c_int32),
                 ("top_p", ctypes.c_float), ("score_scale", ctypes.c_float)]
+
+
+class Rope(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("n_pos", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p)]
 
 
 class RoundDesc(ctypes.Structure):
@@ -116,6 +127,20 @@ def lib():
         L.spd_sparse_decode_step_workspace_size.restype = sz
         L.sparse_decode_step.argtypes = [DP, P, P, P, P, P, P, P, P, PP, P, P, i32, ctypes.c_float, P, P,
                                          P, sz, P]
+        RP, i64, f32, u8 = ctypes.POINTER(Rope), ctypes.c_int64, ctypes.c_float, P
+        L.qk_norm_rope.argtypes = [i64, i32, i32, i32, RP, P, i64, P, i64, P, P, P, P]
+        L.kv_append_rope.argtypes = [DP, i32, RP, P, P, P, P, P, i64, P, i64, P, i64, P, P, P]
+        L.kv4_append.argtypes = [DP, i32, u8, i32, i32, P, P, P, P, P, P]
+        L.kv4_read.argtypes = [DP, i32, u8, i32, i32, P, P, P, P, P]
+        L.spd_kv4_sparse_decode_workspace_size.argtypes = [DP, i32, i32]
+        L.spd_kv4_sparse_decode_workspace_size.restype = sz
+        L.spd_kv4_dense_verify_workspace_size.argtypes = [DP, i32, i32]
+        L.spd_kv4_dense_verify_workspace_size.restype = sz
+        L.kv4_sparse_decode_attn.argtypes = [DP, P, u8, i32, i32, P, P, P, P, i32, i32, f32, P, P, P, sz, P]
+        L.kv4_dense_verify_attn.argtypes = [DP, i32, P, u8, i32, i32, P, P, i32, f32, P, P, P, sz, P]
+        L.spd_token_logprobs_workspace_size.argtypes = [i64, i32, i32]
+        L.spd_token_logprobs_workspace_size.restype = sz
+        L.token_logprobs.argtypes = [i64, i32, P, i32, i64, P, f32, P, P, P, i32, P, P, P, sz, P]
         L.spd_round_create.argtypes = [ctypes.POINTER(RoundDesc), ctypes.POINTER(ctypes.c_void_p)]
         L.spd_round_launch.argtypes = [P, i32, P]
         L.spd_round_destroy.argtypes = [P]
@@ -123,8 +148,9 @@ def lib():
         for f in ("spd_device_status", "spd_set_wait_limit_ns", "pages_summarize", "pages_score_select",
                   "sparse_decode_attn", "dense_verify_attn", "lse_merge",
                   "sparse_decode_attn_noalloc", "kv_append_refresh", "spec_accept",
-                  "pages_append_score_select", "sparse_decode_step",
-                  "spd_round_create", "spd_round_launch"):
+                  "pages_append_score_select", "sparse_decode_step", "qk_norm_rope", "kv_append_rope",
+                  "kv4_append", "kv4_read", "kv4_sparse_decode_attn", "kv4_dense_verify_attn",
+                  "token_logprobs", "spd_round_create", "spd_round_launch"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -302,6 +328,207 @@ def lse_merge(part_o, part_lse, o, lse=None, stream=None):
     S, rows, D = part_o.shape
     _check(lib().lse_merge(S, rows, D, _ptr(part_o), _ptr(part_lse), _ptr(o), _ptr(lse),
                            _stream(stream)))
+
+
+def _arg(t, dtypes, what: str, numel: int | None = None, rows: bool = False):
+    """The address of a tensor of the current device, its type and size checked (None passes).
+
+    rows: a [..., heads, D] view whose heads and channels are contiguous and whose leading
+    dimensions are one stride apart (a slice of a fused projection)."""
+    import torch
+    if t is None:
+        return None
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise SpdError(1, f"{what} is not on the current CUDA device")
+    if t.dtype not in dtypes:
+        raise SpdError(1, f"{what} is {t.dtype}, not {' or '.join(map(str, dtypes))}")
+    if numel is not None and t.numel() != numel:
+        raise SpdError(1, f"{what} has {t.numel()} elements, not {numel}")
+    if not rows and not t.is_contiguous():
+        raise SpdError(1, f"{what} is not contiguous")
+    return t.data_ptr()
+
+
+def _types():
+    import torch
+    return (torch.bfloat16, torch.uint16), (torch.int32,), (torch.float32,), (torch.uint8,)
+
+
+def _row_stride(t, D: int, what: str) -> int:
+    """Elements between the rows [heads][D] of a [..., heads, D] view (see _arg)."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) < 3 or shape[-1] != D:
+        raise SpdError(1, f"{what} must be [..., heads, {D}], not {list(shape)}")
+    if stride[-1] != 1 or (shape[-2] > 1 and stride[-2] != D):
+        raise SpdError(1, f"{what}: the heads and channels of a row must be contiguous")
+    step, n = None, 1
+    for size, s in zip(reversed(shape[:-2]), reversed(stride[:-2])):
+        if size == 1:
+            continue
+        if step is None:
+            step = s
+        elif s != step * n:
+            raise SpdError(1, f"{what}: the rows must be one stride apart")
+        n *= size
+    return step if step is not None else shape[-2] * D
+
+
+def _rope_of(rope, q_weight, k_weight, eps: float, interleaved: bool, D: int) -> Rope:
+    b16, _, f32, _ = _types()
+    if rope is None:
+        n_pos, rot = 0, 0
+    else:
+        if rope.dim() != 3 or rope.shape[1] != 2:
+            raise SpdError(1, f"rope must be [n_pos, 2, rot_dim / 2], not {list(rope.shape)}")
+        n_pos, rot = rope.shape[0], 2 * rope.shape[2]
+    return Rope(_arg(rope, f32, "rope"), n_pos, rot, 1 if interleaved else 0, eps,
+                _arg(q_weight, b16, "q_weight", D), _arg(k_weight, b16, "k_weight", D))
+
+
+def qk_norm_rope(q, k, positions, rope, q_out, k_out, q_weight=None, k_weight=None, eps: float = 1e-6,
+                 interleaved: bool = False, stream=None):
+    """Norm and rotation of query rows q [..., H_q, D] and key rows k [..., H_kv, D] (either may be
+    None) at positions [...]; rope fp32 [n_pos, 2, rot_dim / 2] (None: norm only)."""
+    b16, i32, _, _ = _types()
+    one = q if q is not None else k
+    if one is None:
+        raise SpdError(1, "q and k are both None")
+    D = one.shape[-1]
+    rows = one.numel() // max(1, one.shape[-2] * D)
+    r = _rope_of(rope, q_weight, k_weight, eps, interleaved, D)
+    args = []
+    for t, out, what in ((q, q_out, "q"), (k, k_out, "k")):
+        if t is None:
+            args.append((0, None, 0, None))
+            continue
+        step, heads = _row_stride(t, D, what), t.shape[-2]
+        args.append((heads, _arg(t, b16, what, rows * heads * D, rows=True), step,
+                     _arg(out, b16, what + "_out", rows * heads * D)))
+    (hq, qp, qs, qo), (hk, kp, ks, ko) = args
+    _check(lib().qk_norm_rope(rows, hq, hk, D, ctypes.byref(r), qp, qs, kp, ks,
+                              _arg(positions, i32, "positions", rows) if r.rot_dim else None, qo, ko,
+                              _stream(stream)))
+
+
+def kv_append_rope(dims: Dims, T: int, K, V, page_table, seq_lens, q, k, v, rope, q_out, summ, q_weight=None,
+                   k_weight=None, eps: float = 1e-6, interleaved: bool = False, stream=None):
+    """Norm and rotate the T newest tokens' keys into the paged cache (values as they are), rebuild
+    their pages' summaries, and write the rotated queries to q_out; q and q_out may be None."""
+    b16, i32, _, _ = _types()
+    B, D, n = dims.B, dims.D, dims.B * T
+    cache = dims.num_phys_pages * dims.H_kv * dims.page_size * D
+    r = _rope_of(rope, q_weight, k_weight, eps, interleaved, D)
+    qs = _row_stride(q, D, "q") if q is not None else 0
+    _check(lib().kv_append_rope(
+        ctypes.byref(dims), T, ctypes.byref(r), _arg(K, b16, "K", cache), _arg(V, b16, "V", cache),
+        _arg(page_table, i32, "page_table", B * dims.max_pages_per_seq), _arg(seq_lens, i32, "seq_lens", B),
+        _arg(q, b16, "q", n * dims.H_q * D, rows=True), qs,
+        _arg(k, b16, "k", n * dims.H_kv * D, rows=True), _row_stride(k, D, "k"),
+        _arg(v, b16, "v", n * dims.H_kv * D, rows=True), _row_stride(v, D, "v"),
+        _arg(q_out, b16, "q_out", n * dims.H_q * D),
+        _arg(summ, b16, "summ", B * dims.H_kv * dims.max_pages_per_seq * 2 * D), _stream(stream)))
+
+
+def kv4_cache(dims: Dims, device=None):
+    """An empty 4-bit cache for these dims: uint8 [num_phys_pages][H_kv][2][page_size * D * 9 / 16]."""
+    import torch
+    return torch.zeros((dims.num_phys_pages, dims.H_kv, 2, dims.page_size * dims.D * 9 // 16),
+                       dtype=torch.uint8, device=device or "cuda")
+
+
+def _kv4(dims: Dims, kv4):
+    return _arg(kv4, _types()[3], "kv4", dims.num_phys_pages * dims.H_kv * dims.page_size * dims.D * 9 // 8)
+
+
+def kv4_append(dims: Dims, T: int, kv4, page_table, seq_lens, k_new, v_new, summ, k_exp: int = 0,
+               v_exp: int = 0, stream=None):
+    """Quantise the T newest tokens into the 4-bit cache and rebuild the summaries of their pages."""
+    b16, i32, _, _ = _types()
+    B, D, n = dims.B, dims.D, dims.B * T * dims.H_kv * dims.D
+    _check(lib().kv4_append(
+        ctypes.byref(dims), T, _kv4(dims, kv4), k_exp, v_exp,
+        _arg(page_table, i32, "page_table", B * dims.max_pages_per_seq), _arg(seq_lens, i32, "seq_lens", B),
+        _arg(k_new, b16, "k_new", n), _arg(v_new, b16, "v_new", n),
+        _arg(summ, b16, "summ", B * dims.H_kv * dims.max_pages_per_seq * 2 * D), _stream(stream)))
+
+
+def kv4_read(dims: Dims, T: int, kv4, page_table, seq_lens, k_out, v_out, k_exp: int = 0, v_exp: int = 0,
+             stream=None):
+    """The T newest tokens of every sequence as the bf16 values that the 4-bit cache holds."""
+    b16, i32, _, _ = _types()
+    B, n = dims.B, dims.B * T * dims.H_kv * dims.D
+    _check(lib().kv4_read(
+        ctypes.byref(dims), T, _kv4(dims, kv4), k_exp, v_exp,
+        _arg(page_table, i32, "page_table", B * dims.max_pages_per_seq), _arg(seq_lens, i32, "seq_lens", B),
+        _arg(k_out, b16, "k_out", n), _arg(v_out, b16, "v_out", n), _stream(stream)))
+
+
+def spd_kv4_sparse_decode_workspace_size(dims: Dims, k_max: int, num_splits: int = 0) -> int:
+    """Bytes of workspace kv4_sparse_decode_attn needs."""
+    return _size(lib().spd_kv4_sparse_decode_workspace_size(ctypes.byref(dims), k_max, num_splits),
+                 "kv4_sparse_decode workspace")
+
+
+def spd_kv4_dense_verify_workspace_size(dims: Dims, T: int, num_splits: int = 0) -> int:
+    """Bytes of workspace kv4_dense_verify_attn needs for T positions."""
+    return _size(lib().spd_kv4_dense_verify_workspace_size(ctypes.byref(dims), T, num_splits),
+                 "kv4_dense_verify workspace")
+
+
+def kv4_sparse_decode_attn(dims: Dims, q, kv4, page_table, seq_lens, sel, nsel, k_max: int, o, ws, lse=None,
+                           num_splits: int = 0, softmax_scale: float | None = None, k_exp: int = 0,
+                           v_exp: int = 0, stream=None):
+    """sparse_decode_attn over the 4-bit cache."""
+    b16, i32, f32, u8 = _types()
+    scale = 1.0 / math.sqrt(dims.D) if softmax_scale is None else softmax_scale
+    B, rows = dims.B, dims.B * dims.H_q
+    _check(lib().kv4_sparse_decode_attn(
+        ctypes.byref(dims), _arg(q, b16, "q", rows * dims.D), _kv4(dims, kv4), k_exp, v_exp,
+        _arg(page_table, i32, "page_table", B * dims.max_pages_per_seq), _arg(seq_lens, i32, "seq_lens", B),
+        _arg(sel, i32, "sel", B * dims.H_kv * k_max), _arg(nsel, i32, "nsel", B * dims.H_kv), k_max,
+        num_splits, scale, _arg(o, b16, "o", rows * dims.D), _arg(lse, f32, "lse", rows),
+        _arg(ws, u8, "ws"), ws.numel(), _stream(stream)))
+
+
+def kv4_dense_verify_attn(dims: Dims, T: int, q, kv4, page_table, seq_lens, o, ws, lse=None,
+                          num_splits: int = 0, softmax_scale: float | None = None, k_exp: int = 0,
+                          v_exp: int = 0, stream=None):
+    """dense_verify_attn over the 4-bit cache."""
+    b16, i32, f32, u8 = _types()
+    scale = 1.0 / math.sqrt(dims.D) if softmax_scale is None else softmax_scale
+    B, rows = dims.B, dims.B * T * dims.H_q
+    _check(lib().kv4_dense_verify_attn(
+        ctypes.byref(dims), T, _arg(q, b16, "q", rows * dims.D), _kv4(dims, kv4), k_exp, v_exp,
+        _arg(page_table, i32, "page_table", B * dims.max_pages_per_seq), _arg(seq_lens, i32, "seq_lens", B),
+        num_splits, scale, _arg(o, b16, "o", rows * dims.D), _arg(lse, f32, "lse", rows),
+        _arg(ws, u8, "ws"), ws.numel(), _stream(stream)))
+
+
+def spd_token_logprobs_workspace_size(rows: int, n_vocab: int, top_k: int = 0) -> int:
+    """Bytes of workspace token_logprobs needs."""
+    return _size(lib().spd_token_logprobs_workspace_size(rows, n_vocab, top_k), "token_logprobs workspace")
+
+
+def token_logprobs(logits, targets, logprobs, ws, entropy=None, lse=None, top_ids=None, top_logprobs=None,
+                   inv_temperature: float = 1.0, stream=None):
+    """Log probabilities of targets [...] under logits [..., n_vocab] (fp32 or bf16; rows may be one
+    stride apart), with the optional entropy and lse [...] and the alternatives [..., top_k]."""
+    import torch
+    _, i32, f32, u8 = _types()
+    n = logits.shape[-1]
+    rows = logits.numel() // max(1, n)
+    step = n
+    if logits.dim() > 1:  # as rows of one "head" of n channels
+        step = _row_stride(logits.unsqueeze(-2), n, "logits")
+    elif n > 1 and logits.stride(0) != 1:
+        raise SpdError(1, "logits: a row must be contiguous")
+    top_k = 0 if top_ids is None else top_ids.shape[-1]
+    _check(lib().token_logprobs(
+        rows, n, _arg(logits, (torch.float32, torch.bfloat16), "logits", rows=True),
+        1 if logits.dtype == torch.bfloat16 else 0, step, _arg(targets, i32, "targets", rows),
+        inv_temperature, _arg(logprobs, f32, "logprobs", rows), _arg(entropy, f32, "entropy", rows),
+        _arg(lse, f32, "lse", rows), top_k, _arg(top_ids, i32, "top_ids", rows * top_k),
+        _arg(top_logprobs, f32, "top_logprobs", rows * top_k), _arg(ws, u8, "ws"), ws.numel(), _stream(stream)))
 
 
 class Round:

@@ -58,6 +58,101 @@ struct AppendArgs {
 };
 cudaError_t launch_append_refresh(const AppendArgs& a, cudaStream_t st);
 
+// Pages that T consecutive positions of a sequence can span.
+inline int append_touched(int T, int ps, int max_pages) {
+    const int n = (T - 1 + ps - 1) / ps + 1;
+    return n < max_pages ? n : max_pages;
+}
+
+struct RopeArgs {
+    const uint16_t* q;  // [rows] rows of H_q heads, q_stride elements apart (NULL: H_q = 0)
+    const uint16_t* k;  // [rows] rows of H_kv heads, k_stride elements apart (NULL: H_kv = 0)
+    long long q_stride, k_stride, rows;
+    int H_q, H_kv, D;
+    const int32_t* positions;  // [rows]
+    const float* table;        // [n_pos][2][rot / 2]
+    int n_pos, rot, interleaved;
+    const uint16_t* q_weight;  // [D] or NULL: no norm
+    const uint16_t* k_weight;
+    float eps;
+    uint16_t* q_out;  // [rows][H_q][D]
+    uint16_t* k_out;  // [rows][H_kv][D]
+    unsigned* status;
+};
+cudaError_t launch_qk_norm_rope(const RopeArgs& a, cudaStream_t st);
+
+struct AppendRopeArgs {
+    AppendArgs append;  // k_new and v_new are not used: the rows come from rope.k and v
+    RopeArgs rope;      // rows = B * T; positions come from seq_lens
+    const uint16_t* v;
+    long long v_stride;
+    int touched;  // set by the launch
+};
+cudaError_t launch_append_rope(const AppendRopeArgs& a, cudaStream_t st);
+// CTAs of its grid (to be kept below 2^31).
+long long append_rope_ctas(const AppendRopeArgs& a);
+
+// The 4-bit cache: [num_phys][H_kv][2][ps * D * 9 / 16] bytes (see include/spd.h).
+struct Kv4Args {
+    uint8_t* kv4;
+    const int32_t* page_table;
+    const int32_t* seq_lens;
+    const uint16_t* k_new;  // append: [B][T][H_kv][D]
+    const uint16_t* v_new;
+    uint16_t* summ;         // append: [B][H_kv][max_pages][2][D]
+    uint16_t* k_out;        // read: [B][T][H_kv][D]
+    uint16_t* v_out;
+    int B, T, H_kv, D, ps, max_pages;
+    long long num_phys;
+    int k_exp, v_exp;
+    unsigned* status;
+};
+cudaError_t launch_kv4_append(const Kv4Args& a, cudaStream_t st);
+cudaError_t launch_kv4_read(const Kv4Args& a, cudaStream_t st);
+
+struct Attn4Args {
+    const uint16_t* q;  // [B][T][H_q][D]
+    const uint8_t* kv4;
+    const int32_t* page_table;
+    const int32_t* seq_lens;
+    const int32_t* sel;   // sparse only
+    const int32_t* nsel;  // sparse only
+    int k_max;
+    int B, H_q, H_kv, D, ps, max_pages, T;
+    long long num_phys;
+    int pages_per_split, num_splits;
+    float scale_log2;  // softmax scale * log2(e) * 2^k_exp
+    float v_scale;     // 2^v_exp
+    uint16_t* o;
+    float* lse;
+    float* part_o;    // [B*H_kv][num_splits][R][D]
+    float* part_lse;  // [B*H_kv][num_splits][R]
+    int* counters;    // [B*H_kv] split tickets, zero on entry and on exit
+    unsigned* status;
+};
+cudaError_t launch_attn4(const Attn4Args& a, bool sparse, cudaStream_t st);
+// CTAs of the kernel that fit on one SM for this shape.
+int occ_attn4(int D, int ps, int R, bool sparse);
+
+struct LogprobArgs {
+    const void* logits;  // [rows][n], row_stride elements apart
+    bool bf16;
+    long long rows, row_stride;
+    int n;
+    const int32_t* targets;
+    float inv_t;
+    float* logprob;
+    float* entropy;  // may be NULL
+    float* lse;      // may be NULL
+    int top_k;
+    int32_t* top_ids;
+    float* top_logprobs;
+    void* ws;
+    unsigned* status;
+};
+cudaError_t launch_token_logprobs(const LogprobArgs& a, int num_sms, cudaStream_t st);
+size_t token_logprobs_ws(long long rows, int n, int top_k, int num_sms);
+
 // Default limit of every bounded wait in the kernels (spd_set_wait_limit_ns).
 constexpr unsigned long long kDefaultWaitNs = 2000000000ull;
 // The limit the next launches pass to their kernels.

@@ -783,3 +783,344 @@ SPD_API spd_status sparse_decode_attn_noalloc(const spd_dims* dims, const spd_bf
     return sparse_attn_launch(dims, q, K, V, page_table, seq_lens, sel, nsel, k_max, S, softmax_scale, o, lse,
                               scratch, SPD_NOALLOC_SCRATCH_BYTES, nullptr, nullptr, d, stream);
 }
+
+// ---------------------------------------------------------------- head norms and rotation
+
+// Checks a rotation's description and fills the kernel's arguments from it.
+static spd_status rope_setup(const spd_rope* rope, int32_t D, int32_t H_q, int32_t H_kv, const spd_bf16* q,
+                             int64_t q_stride, const spd_bf16* k, int64_t k_stride, RopeArgs& a) {
+    if (!rope) return fail(SPD_ERR_INVALID_ARG, "rope is NULL");
+    if (D != 64 && D != 128) return fail(SPD_ERR_UNSUPPORTED, "head dim %d (supported: 64, 128)", D);
+    if (rope->rot_dim < 0 || rope->rot_dim > D || rope->rot_dim % 8)
+        return fail(SPD_ERR_UNSUPPORTED, "rot_dim %d (need a multiple of 8 in [0, %d])", rope->rot_dim, D);
+    if (!(rope->eps >= 0.f) || !(rope->eps <= 3.4e38f)) return fail(SPD_ERR_INVALID_ARG, "eps must be >= 0 and finite");
+    if (rope->rot_dim > 0 && (!rope->table || rope->n_pos < 1 || !aligned16(rope->table)))
+        return fail(SPD_ERR_INVALID_ARG, "the angle table must be 16-byte aligned and hold at least one position");
+    if ((reinterpret_cast<uintptr_t>(rope->q_weight) | reinterpret_cast<uintptr_t>(rope->k_weight)) & 7u)
+        return fail(SPD_ERR_INVALID_ARG, "norm weights must be 8-byte aligned");
+    if ((q && (H_q < 1 || q_stride < (int64_t)H_q * D || q_stride % 8)) ||
+        (k && (H_kv < 1 || k_stride < (int64_t)H_kv * D || k_stride % 8)))
+        return fail(SPD_ERR_INVALID_ARG, "bad heads or row strides (H_q=%d q_stride=%lld H_kv=%d k_stride=%lld)", H_q,
+                    (long long)q_stride, H_kv, (long long)k_stride);
+    a = RopeArgs{};
+    a.q = q;
+    a.k = k;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.H_q = q ? H_q : 0;
+    a.H_kv = k ? H_kv : 0;
+    a.D = D;
+    a.table = rope->table;
+    a.n_pos = rope->n_pos;
+    a.rot = rope->rot_dim;
+    a.interleaved = rope->interleaved != 0;
+    a.q_weight = q ? rope->q_weight : nullptr;
+    a.k_weight = k ? rope->k_weight : nullptr;
+    a.eps = rope->eps;
+    return SPD_OK;
+}
+
+SPD_API spd_status qk_norm_rope(int64_t rows, int32_t H_q, int32_t H_kv, int32_t D, const spd_rope* rope,
+                                const spd_bf16* q, int64_t q_stride, const spd_bf16* k, int64_t k_stride,
+                                const int32_t* positions, spd_bf16* q_out, spd_bf16* k_out, void* stream) {
+    RopeArgs a;
+    spd_status st = rope_setup(rope, D, H_q, H_kv, q, q_stride, k, k_stride, a);
+    if (st != SPD_OK) return st;
+    if (rows < 0) return fail(SPD_ERR_INVALID_ARG, "rows < 0");
+    if (rows == 0 || (!q && !k)) return SPD_OK;
+    if ((q && !q_out) || (k && !k_out) || (a.rot > 0 && !positions))
+        return fail(SPD_ERR_INVALID_ARG, "NULL pointer argument");
+    if (!aligned16(q) || !aligned16(k) || !aligned16(q_out) || !aligned16(k_out))
+        return fail(SPD_ERR_INVALID_ARG, "q, k, q_out and k_out must be 16-byte aligned");
+    if (rows >= (1LL << 31) || rows * ((int64_t)a.H_q + a.H_kv) >= (1LL << 33))
+        return fail(SPD_ERR_UNSUPPORTED, "too many rows (%lld)", (long long)rows);
+    DevInfo* d = dev_info(&st);
+    if (!d) return st;
+    a.rows = rows;
+    a.positions = positions;
+    a.q_out = q_out;
+    a.k_out = k_out;
+    a.status = d->status;
+    cudaError_t e = launch_qk_norm_rope(a, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SPD_OK : cuda_fail(e, "qk_norm_rope launch");
+}
+
+SPD_API spd_status kv_append_rope(const spd_dims* dims, int32_t T, const spd_rope* rope, spd_bf16* K, spd_bf16* V,
+                                  const int32_t* page_table, const int32_t* seq_lens, const spd_bf16* q,
+                                  int64_t q_stride, const spd_bf16* k, int64_t k_stride, const spd_bf16* v,
+                                  int64_t v_stride, spd_bf16* q_out, spd_bf16* summ, void* stream) {
+    spd_status st = check_dims(dims);
+    if (st != SPD_OK) return st;
+    if (T < 1 || T > 4096) return fail(SPD_ERR_INVALID_ARG, "T = %d outside [1, 4096]", T);
+    AppendRopeArgs p;
+    st = rope_setup(rope, dims->D, dims->H_q, dims->H_kv, q, q_stride, k, k_stride, p.rope);
+    if (st != SPD_OK) return st;
+    if (dims->B == 0) return SPD_OK;
+    if (!K || !V || !page_table || !seq_lens || !k || !v || !summ || (q != nullptr) != (q_out != nullptr))
+        return fail(SPD_ERR_INVALID_ARG, "NULL pointer argument (q and q_out go together)");
+    if (v_stride < (int64_t)dims->H_kv * dims->D || v_stride % 8)
+        return fail(SPD_ERR_INVALID_ARG, "bad v_stride %lld", (long long)v_stride);
+    if (!aligned16(K) || !aligned16(V) || !aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) ||
+        !aligned16(summ))
+        return fail(SPD_ERR_INVALID_ARG, "K, V, q, k, v, q_out and summ must be 16-byte aligned");
+    DevInfo* d = dev_info(&st);
+    if (!d) return st;
+    AppendArgs& a = p.append;
+    a = AppendArgs{};
+    a.K = K;
+    a.V = V;
+    a.page_table = page_table;
+    a.seq_lens = seq_lens;
+    a.summ = summ;
+    a.B = dims->B;
+    a.T = T;
+    a.H_kv = dims->H_kv;
+    a.D = dims->D;
+    a.ps = dims->page_size;
+    a.max_pages = dims->max_pages_per_seq;
+    a.num_phys = dims->num_phys_pages;
+    a.status = d->status;
+    p.rope.rows = (long long)dims->B * T;
+    p.rope.q_out = q_out;
+    p.rope.status = d->status;
+    p.v = v;
+    p.v_stride = v_stride;
+    p.touched = 0;
+    if (append_rope_ctas(p) >= (1LL << 31)) return fail(SPD_ERR_UNSUPPORTED, "B * T * H_q too large");
+    cudaError_t e = launch_append_rope(p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SPD_OK : cuda_fail(e, "kv_append_rope launch");
+}
+
+// ---------------------------------------------------------------- the 4-bit cache
+
+static spd_status kv4_exps(int32_t k_exp, int32_t v_exp) {
+    if (k_exp < -64 || k_exp > 64 || v_exp < -64 || v_exp > 64)
+        return fail(SPD_ERR_INVALID_ARG, "k_exp (%d) and v_exp (%d) must lie in [-64, 64]", k_exp, v_exp);
+    return SPD_OK;
+}
+
+static spd_status kv4_rows_setup(const spd_dims* dims, int32_t T, const uint8_t* kv4, int32_t k_exp, int32_t v_exp,
+                                 const int32_t* page_table, const int32_t* seq_lens, const void* k, const void* v,
+                                 Kv4Args& a) {
+    spd_status st = check_dims(dims);
+    if (st != SPD_OK) return st;
+    if (T < 1 || T > 4096) return fail(SPD_ERR_INVALID_ARG, "T = %d outside [1, 4096]", T);
+    st = kv4_exps(k_exp, v_exp);
+    if (st != SPD_OK || dims->B == 0) return st;
+    if (!kv4 || !page_table || !seq_lens || !k || !v) return fail(SPD_ERR_INVALID_ARG, "NULL pointer argument");
+    if (!aligned16(kv4) || !aligned16(k) || !aligned16(v))
+        return fail(SPD_ERR_INVALID_ARG, "the cache and the rows must be 16-byte aligned");
+    if ((long long)dims->B * T * dims->H_kv >= (1LL << 33)) return fail(SPD_ERR_UNSUPPORTED, "B * T * H_kv too large");
+    DevInfo* d = dev_info(&st);
+    if (!d) return st;
+    a = Kv4Args{};
+    a.kv4 = const_cast<uint8_t*>(kv4);
+    a.page_table = page_table;
+    a.seq_lens = seq_lens;
+    a.B = dims->B;
+    a.T = T;
+    a.H_kv = dims->H_kv;
+    a.D = dims->D;
+    a.ps = dims->page_size;
+    a.max_pages = dims->max_pages_per_seq;
+    a.num_phys = dims->num_phys_pages;
+    a.k_exp = k_exp;
+    a.v_exp = v_exp;
+    a.status = d->status;
+    return SPD_OK;
+}
+
+SPD_API spd_status kv4_append(const spd_dims* dims, int32_t T, uint8_t* kv4, int32_t k_exp, int32_t v_exp,
+                              const int32_t* page_table, const int32_t* seq_lens, const spd_bf16* k_new,
+                              const spd_bf16* v_new, spd_bf16* summ, void* stream) {
+    Kv4Args a;
+    spd_status st = kv4_rows_setup(dims, T, kv4, k_exp, v_exp, page_table, seq_lens, k_new, v_new, a);
+    if (st != SPD_OK || dims->B == 0) return st;
+    if (!summ || !aligned16(summ)) return fail(SPD_ERR_INVALID_ARG, "summ must be 16-byte aligned and not NULL");
+    a.k_new = k_new;
+    a.v_new = v_new;
+    a.summ = summ;
+    cudaError_t e = launch_kv4_append(a, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SPD_OK : cuda_fail(e, "kv4_append launch");
+}
+
+SPD_API spd_status kv4_read(const spd_dims* dims, int32_t T, const uint8_t* kv4, int32_t k_exp, int32_t v_exp,
+                            const int32_t* page_table, const int32_t* seq_lens, spd_bf16* k_out, spd_bf16* v_out,
+                            void* stream) {
+    Kv4Args a;
+    spd_status st = kv4_rows_setup(dims, T, kv4, k_exp, v_exp, page_table, seq_lens, k_out, v_out, a);
+    if (st != SPD_OK || dims->B == 0) return st;
+    a.k_out = k_out;
+    a.v_out = v_out;
+    cudaError_t e = launch_kv4_read(a, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SPD_OK : cuda_fail(e, "kv4_read launch");
+}
+
+// Splits of a row of the 4-bit attention, as sparse_splits / dense_splits choose them.
+static int kv4_splits(const spd_dims* d, int T, int items, bool sparse, int req, int sms) {
+    const long long rows = (long long)d->B * d->H_kv;
+    const long long workers = (long long)sms * occ_attn4(d->D, d->page_size, T * (d->H_q / d->H_kv), sparse);
+    return splits_for(rows, items, workers, pages_per_split_floor(d->page_size), sparse ? 1 : 4, req);
+}
+
+static size_t kv4_attn_ws(const spd_dims* dims, int T, int items, bool sparse, int32_t num_splits) {
+    spd_status st = SPD_OK;
+    DevInfo* d = dev_info(&st);
+    if (!d) return 0;
+    const int S = kv4_splits(dims, T, items, sparse, num_splits, d->sms);
+    return attn_ws_layout(nullptr, (long long)dims->B * dims->H_kv, S, T * (dims->H_q / dims->H_kv), dims->D).bytes;
+}
+
+static spd_status kv4_check_T(const spd_dims* dims, int32_t T) {
+    if (T < 1 || (long long)T * (dims->H_q / dims->H_kv) > 64)
+        return fail(SPD_ERR_UNSUPPORTED, "T=%d with G=%d (need 1 <= T and T*G <= 64)", T, dims->H_q / dims->H_kv);
+    return SPD_OK;
+}
+
+SPD_API size_t spd_kv4_sparse_decode_workspace_size(const spd_dims* dims, int32_t k_max, int32_t num_splits) {
+    if (check_dims(dims) != SPD_OK) return 0;
+    if (k_max < 1) {
+        fail(SPD_ERR_INVALID_ARG, "k_max < 1");
+        return 0;
+    }
+    return kv4_attn_ws(dims, 1, k_max, true, num_splits);
+}
+
+SPD_API size_t spd_kv4_dense_verify_workspace_size(const spd_dims* dims, int32_t T, int32_t num_splits) {
+    if (check_dims(dims) != SPD_OK || kv4_check_T(dims, T) != SPD_OK) return 0;
+    return kv4_attn_ws(dims, T, dims->max_pages_per_seq, false, num_splits);
+}
+
+// The common body of the two calls (sel NULL: dense).  dims and T are checked.
+static spd_status kv4_attn(const spd_dims* dims, int32_t T, const spd_bf16* q, const uint8_t* kv4, int32_t k_exp,
+                           int32_t v_exp, const int32_t* page_table, const int32_t* seq_lens, const int32_t* sel,
+                           const int32_t* nsel, int32_t items, int32_t num_splits, float scale, spd_bf16* o,
+                           float* lse, void* ws, size_t ws_bytes, void* stream) {
+    const bool sparse = sel != nullptr;
+    spd_status st = kv4_exps(k_exp, v_exp);
+    if (st != SPD_OK) return st;
+    if (!(scale >= -3.4e38f && scale <= 3.4e38f)) return fail(SPD_ERR_INVALID_ARG, "softmax_scale is not finite");
+    if (num_splits < 0) return fail(SPD_ERR_INVALID_ARG, "num_splits < 0");
+    if (!q || !kv4 || !page_table || !seq_lens || !o) return fail(SPD_ERR_INVALID_ARG, "NULL pointer argument");
+    if (!aligned16(q) || !aligned16(kv4) || !aligned16(o))
+        return fail(SPD_ERR_INVALID_ARG, "q, kv4 and o must be 16-byte aligned");
+    DevInfo* d = dev_info(&st);
+    if (!d) return st;
+    const int R = T * (dims->H_q / dims->H_kv);
+    const int S = kv4_splits(dims, T, items, sparse, num_splits, d->sms);
+    const long long rows = (long long)dims->B * dims->H_kv;
+    if (rows * S >= (1LL << 31)) return fail(SPD_ERR_UNSUPPORTED, "B * H_kv * num_splits must be < 2^31");
+    const size_t need = attn_ws_layout(nullptr, rows, S, R, dims->D).bytes;
+    if (!ws || ws_bytes < need) return fail(SPD_ERR_WORKSPACE, "workspace %zu bytes < %zu", ws_bytes, need);
+    if (!aligned16(ws)) return fail(SPD_ERR_INVALID_ARG, "ws must be 16-byte aligned");
+    const AttnWs w = attn_ws_layout(ws, rows, S, R, dims->D);
+    Attn4Args a = {};
+    a.q = q;
+    a.kv4 = kv4;
+    a.page_table = page_table;
+    a.seq_lens = seq_lens;
+    a.sel = sel;
+    a.nsel = nsel;
+    a.k_max = items;
+    a.B = dims->B;
+    a.H_q = dims->H_q;
+    a.H_kv = dims->H_kv;
+    a.D = dims->D;
+    a.ps = dims->page_size;
+    a.max_pages = dims->max_pages_per_seq;
+    a.T = T;
+    a.num_phys = dims->num_phys_pages;
+    a.pages_per_split = (items + S - 1) / S;
+    a.num_splits = S;
+    a.scale_log2 = (float)((double)scale * 1.4426950408889634 * (double)exp2f((float)k_exp));
+    a.v_scale = exp2f((float)v_exp);
+    a.o = o;
+    a.lse = lse;
+    a.part_o = w.part_o;
+    a.part_lse = w.part_lse;
+    a.counters = w.counters;
+    a.status = d->status;
+    cudaError_t e = launch_attn4(a, sparse, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SPD_OK : cuda_fail(e, sparse ? "kv4_sparse_decode_attn launch" : "kv4_dense_verify_attn launch");
+}
+
+SPD_API spd_status kv4_sparse_decode_attn(const spd_dims* dims, const spd_bf16* q, const uint8_t* kv4, int32_t k_exp,
+                                          int32_t v_exp, const int32_t* page_table, const int32_t* seq_lens,
+                                          const int32_t* sel, const int32_t* nsel, int32_t k_max, int32_t num_splits,
+                                          float softmax_scale, spd_bf16* o, float* lse, void* ws, size_t ws_bytes,
+                                          void* stream) {
+    spd_status st = check_dims(dims);
+    if (st != SPD_OK) return st;
+    if (k_max < 1) return fail(SPD_ERR_INVALID_ARG, "k_max < 1");
+    if (dims->B == 0) return SPD_OK;
+    if (!sel || !nsel) return fail(SPD_ERR_INVALID_ARG, "NULL pointer argument");
+    return kv4_attn(dims, 1, q, kv4, k_exp, v_exp, page_table, seq_lens, sel, nsel, k_max, num_splits, softmax_scale, o,
+                    lse, ws, ws_bytes, stream);
+}
+
+SPD_API spd_status kv4_dense_verify_attn(const spd_dims* dims, int32_t T, const spd_bf16* q, const uint8_t* kv4,
+                                         int32_t k_exp, int32_t v_exp, const int32_t* page_table,
+                                         const int32_t* seq_lens, int32_t num_splits, float softmax_scale, spd_bf16* o,
+                                         float* lse, void* ws, size_t ws_bytes, void* stream) {
+    spd_status st = check_dims(dims);
+    if (st != SPD_OK) return st;
+    st = kv4_check_T(dims, T);
+    if (st != SPD_OK || dims->B == 0) return st;
+    return kv4_attn(dims, T, q, kv4, k_exp, v_exp, page_table, seq_lens, nullptr, nullptr, dims->max_pages_per_seq,
+                    num_splits, softmax_scale, o, lse, ws, ws_bytes, stream);
+}
+
+// ---------------------------------------------------------------- token log probabilities
+
+static spd_status logprob_shape(int64_t rows, int32_t n_vocab, int32_t top_k) {
+    if (rows < 0 || rows >= (1LL << 31)) return fail(SPD_ERR_INVALID_ARG, "rows = %lld outside [0, 2^31)", (long long)rows);
+    if (n_vocab < 1 || n_vocab > (1 << 21)) return fail(SPD_ERR_UNSUPPORTED, "n_vocab = %d outside [1, 2^21]", n_vocab);
+    if (top_k < 0 || top_k > 32) return fail(SPD_ERR_UNSUPPORTED, "top_k = %d outside [0, 32]", top_k);
+    return SPD_OK;
+}
+
+SPD_API size_t spd_token_logprobs_workspace_size(int64_t rows, int32_t n_vocab, int32_t top_k) {
+    spd_status st = logprob_shape(rows, n_vocab, top_k);
+    if (st != SPD_OK) return 0;
+    DevInfo* d = dev_info(&st);
+    return d ? token_logprobs_ws(rows, n_vocab, top_k, d->sms) : 0;
+}
+
+SPD_API spd_status token_logprobs(int64_t rows, int32_t n_vocab, const void* logits, int32_t logits_bf16,
+                                  int64_t row_stride, const int32_t* targets, float inv_temperature, float* logprob,
+                                  float* entropy, float* lse, int32_t top_k, int32_t* top_ids, float* top_logprobs,
+                                  void* ws, size_t ws_bytes, void* stream) {
+    spd_status st = logprob_shape(rows, n_vocab, top_k);
+    if (st != SPD_OK) return st;
+    if (row_stride < n_vocab) return fail(SPD_ERR_INVALID_ARG, "row_stride %lld < n_vocab %d", (long long)row_stride, n_vocab);
+    if (!(inv_temperature > 0.f && inv_temperature <= 3.4e38f))
+        return fail(SPD_ERR_INVALID_ARG, "inv_temperature must be > 0 and finite");
+    if (rows == 0) return SPD_OK;
+    if (!logits || (logprob && !targets) || (top_k > 0 && (!top_ids || !top_logprobs)))
+        return fail(SPD_ERR_INVALID_ARG, "NULL pointer argument");
+    if (reinterpret_cast<uintptr_t>(logits) % (logits_bf16 ? 2 : 4))
+        return fail(SPD_ERR_INVALID_ARG, "logits are not aligned to their type");
+    DevInfo* d = dev_info(&st);
+    if (!d) return st;
+    const size_t need = token_logprobs_ws(rows, n_vocab, top_k, d->sms);
+    if (!ws || ws_bytes < need) return fail(SPD_ERR_WORKSPACE, "workspace %zu bytes < %zu", ws_bytes, need);
+    if (!aligned16(ws)) return fail(SPD_ERR_INVALID_ARG, "ws must be 16-byte aligned");
+    LogprobArgs a = {};
+    a.logits = logits;
+    a.bf16 = logits_bf16 != 0;
+    a.rows = rows;
+    a.row_stride = row_stride;
+    a.n = n_vocab;
+    a.targets = targets;
+    a.inv_t = inv_temperature;
+    a.logprob = logprob;
+    a.entropy = entropy;
+    a.lse = lse;
+    a.top_k = top_k;
+    a.top_ids = top_ids;
+    a.top_logprobs = top_logprobs;
+    a.ws = ws;
+    a.status = d->status;
+    cudaError_t e = launch_token_logprobs(a, d->sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SPD_OK : cuda_fail(e, "token_logprobs launch");
+}

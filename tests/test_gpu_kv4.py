@@ -1,0 +1,451 @@
+"""The 4-bit paged cache on the GPU: its numbers bit for bit, its attention against the 64-bit form over them."""
+import numpy as np
+import pytest
+
+from tests import ops_reference as ref
+from tests.test_gpu_rope import dev, host, paged
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def spd():
+    import sparse_attention_decode_pages_gb300 as spd
+    spd.spd_device_status(clear=True)
+    return spd
+
+
+def rows_bf16(rng, *shape, spread=False):
+    """bf16 values as float64: normal, or over many powers of two with zeros, ties and tiny groups among them."""
+    x = rng.standard_normal(shape)
+    if spread:
+        x = x * 2.0 ** rng.integers(-14, 12, (*shape[:-1], 1))
+        flat = x.reshape(-1, 16)
+        flat[::7] = 0.0
+        flat[1::7] = np.round(flat[1::7] * 4) / 4  # many exact ties
+        flat[2::11] *= 2.0 ** -12                   # scales below the smallest e4m3 number
+        flat[3::11, 0] = 5000.0                     # scales past the largest
+    return ref.bf16(x)
+
+
+def to_dev(x):
+    import torch
+    return dev(x.astype(np.float32), torch.bfloat16)
+
+
+def append_reference(kv4, pt, lens, T, k, v, ps, k_exp, v_exp):
+    """kv4 (numpy bytes) with the T newest tokens written; the summaries' bf16 values of the touched pages."""
+    kv4 = kv4.copy()
+    H, D = k.shape[2], k.shape[3]
+    summ = {}
+    for b, n in enumerate(lens):
+        if n < T:
+            continue
+        for p in range((n - T) // ps, -(-n // ps)):
+            for h in range(H):
+                tile = kv4[pt[b, p], h]
+                for half, (rows, e) in enumerate(((k, k_exp), (v, v_exp))):
+                    codes, scale = (x.copy() for x in ref.kv4_unpack(tile[half], ps, D))
+                    for pos in range(max(p * ps, n - T), min((p + 1) * ps, n)):
+                        codes[pos % ps], scale[pos % ps] = ref.kv4_quantise(rows[b, pos - (n - T), h], e)
+                    tile[half] = ref.kv4_pack(codes, scale)
+                    if half == 0:
+                        val = ref.kv4_values(codes, scale, e)[: min(ps, n - p * ps)]
+                        summ[b, h, p] = (val.min(0), val.max(0))
+    return kv4, summ
+
+
+APPEND = [  # lens, T, ps, H, D, k_exp, v_exp
+    ([1, 17, 16, 130], 1, 16, 2, 128, 0, 0),
+    ([40, 33, 64], 33, 32, 1, 64, 3, -5),
+    ([100, 65, 71, 130], 65, 64, 3, 128, -2, 4),
+    ([500], 7, 16, 9, 64, 0, -1),
+]
+
+
+@pytest.mark.parametrize("lens,T,ps,H,D,k_exp,v_exp", APPEND)
+@pytest.mark.parametrize("spread", [False, True])
+def test_kv4_append_and_read_are_exact(spd, lens, T, ps, H, D, k_exp, v_exp, spread):
+    """Every byte of the cache (old slots and spare pages too), the summaries, and the values read back."""
+    import torch
+    rng = np.random.default_rng(T * 13 + D + spread)
+    lens, pt, mp, n, _, _ = paged(rng, lens, ps, H, D)
+    B = len(lens)
+    kv4 = rng.integers(0, 256, (n, H, 2, ps * D * 9 // 16)).astype(np.uint8)
+    # older tokens: scales without NaN
+    kv4[..., ps * D // 2:] &= 0x7F
+    kv4[..., ps * D // 2:][kv4[..., ps * D // 2:] == 0x7F] = 0x30
+    k, v = (rows_bf16(rng, B, T, H, D, spread=spread) for _ in range(2))
+    want, want_summ = append_reference(kv4, pt, lens, T, k, v, ps, k_exp, v_exp)
+    dims = spd.dims_of(B, H, H, D, ps, mp, n)
+    cache, summ = dev(kv4), torch.full((B, H, mp, 2, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    spd.kv4_append(dims, T, cache, dev(pt), dev(lens), to_dev(k), to_dev(v), summ, k_exp=k_exp, v_exp=v_exp)
+    ko, vo = (torch.full((B, T, H, D), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    spd.kv4_read(dims, T, cache, dev(pt), dev(lens), ko, vo, k_exp=k_exp, v_exp=v_exp)
+    torch.cuda.synchronize()
+    assert spd.spd_device_status(clear=True) == 0
+    assert np.array_equal(cache.cpu().numpy(), want)
+    got = host(summ)
+    expect = np.full(got.shape, 7.0)
+    for (b, h, p), (lo, hi) in want_summ.items():
+        expect[b, h, p, 0], expect[b, h, p, 1] = lo, hi
+    assert np.array_equal(got, expect)
+    for out, rows, e in ((ko, k, k_exp), (vo, v, v_exp)):
+        assert np.array_equal(host(out), ref.kv4_values(*ref.kv4_quantise(rows, e), e))
+
+
+def test_kv4_append_of_infinities_and_nan(spd):
+    import torch
+    rng = np.random.default_rng(5)
+    ps, H, D = 16, 2, 64
+    lens, pt, mp, n, _, _ = paged(rng, [16], ps, H, D)
+    k = rows_bf16(rng, 1, 16, H, D)
+    k[0, 0, 0, 3], k[0, 1, 0, 20], k[0, 2, 1, :16], k[0, 3, 1, 5] = np.inf, -np.inf, np.nan, np.nan
+    v = k[:, ::-1].copy()
+    dims = spd.dims_of(1, H, H, D, ps, mp, n)
+    cache, summ = spd.kv4_cache(dims), torch.zeros((1, H, mp, 2, D), dtype=torch.bfloat16, device="cuda")
+    ko, vo = (torch.empty((1, 16, H, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    spd.kv4_append(dims, 16, cache, dev(pt), dev(lens), to_dev(k), to_dev(v), summ)
+    spd.kv4_read(dims, 16, cache, dev(pt), dev(lens), ko, vo)
+    for out, rows in ((ko, k), (vo, v)):
+        assert np.array_equal(host(out), ref.kv4_values(*ref.kv4_quantise(rows, 0), 0))
+    assert host(ko)[0, 0, 0, 3] == 6 * 448 and host(ko)[0, 1, 0, 20] == -6 * 448
+    assert np.all(host(ko)[0, 2, 1, :16] == 0) and host(ko)[0, 3, 1, 5] == 0
+
+
+def test_kv4_append_skips_what_it_cannot_place(spd):
+    import torch
+    rng = np.random.default_rng(6)
+    T, ps, H, D = 3, 16, 2, 64
+    lens, pt, mp, n, _, _ = paged(rng, [20, 30, 40, 35], ps, H, D)
+    bad, pt_bad = lens.copy(), pt.copy()
+    bad[0], bad[1] = 2, mp * ps + 1
+    pt_bad[3, 2] = -5
+    kv4 = rng.integers(0, 120, (n, H, 2, ps * D * 9 // 16)).astype(np.uint8)
+    k, v = (rows_bf16(rng, 4, T, H, D) for _ in range(2))
+    dims = spd.dims_of(4, H, H, D, ps, mp, n)
+    cache, summ = dev(kv4), torch.full((4, H, mp, 2, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    spd.kv4_append(dims, T, cache, dev(pt_bad), dev(bad), to_dev(k), to_dev(v), summ)
+    assert spd.spd_device_status(clear=True) == spd.DEV_BAD_LEN | spd.DEV_BAD_PAGE
+    ko, vo = (torch.full((4, T, H, D), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    spd.kv4_read(dims, T, cache, dev(pt_bad), dev(bad), ko, vo)
+    assert spd.spd_device_status(clear=True) == spd.DEV_BAD_LEN | spd.DEV_BAD_PAGE
+    got = cache.cpu().numpy()
+    for b in range(4):
+        rows = pt[b, : -(-int(lens[b]) // ps)]
+        assert np.array_equal(got[rows], kv4[rows]) == (b != 2), b
+        assert bool(torch.count_nonzero(ko[b]) == 0) == (b != 2) and bool(torch.count_nonzero(vo[b]) == 0) == (b != 2)
+        assert bool((summ[b] == 7.0).all()) == (b != 2), b
+
+
+# ---------------------------------------------------------------- attention
+
+def make_cache(rng, lens, ps, H, D, k_exp=0, v_exp=0, poison=True):
+    """A page table and a cache of quantised normal rows; slots behind the lengths hold any bytes (NaN scales too)."""
+    lens, pt, mp, n, _, _ = paged(rng, lens, ps, H, D)
+    kv4 = rng.integers(0, 256, (n, H, 2, ps * D * 9 // 16)).astype(np.uint8)
+    if poison:
+        kv4[..., ps * D // 2:] = 0x7F
+    vals = []
+    for b, ln in enumerate(lens):
+        rows = [rows_bf16(rng, ln, H, D) * 2.0 ** e for e in (k_exp, v_exp)]
+        out = []
+        for half, (x, e) in enumerate(zip(rows, (k_exp, v_exp))):
+            codes, scale = ref.kv4_quantise(x, e)
+            out.append(ref.kv4_values(codes, scale, e))
+            for p in range(-(-ln // ps)):
+                lo, hi = p * ps, min((p + 1) * ps, ln)
+                for h in range(H):
+                    c, s = (y.copy() for y in ref.kv4_unpack(kv4[pt[b, p], h, half], ps, D))
+                    c[: hi - lo], s[: hi - lo] = codes[lo:hi, h], scale[lo:hi, h]
+                    kv4[pt[b, p], h, half] = ref.kv4_pack(c, s)
+        vals.append(out)
+    return lens, pt, mp, n, kv4, vals
+
+
+def check_row(o, lse, q, keys, values, scale, visible, what):
+    """o: one rounding to bf16 (2^-8), weights rounded to fp16 (2^-11 of sum p |v|; below 2^-32 of the largest
+    they are dropped), and logits that are off by d: D fp32 sums of products that add up to at most `mag`, the
+    query's channels kept to 2^-25 of the largest, and z itself rounded and raised by ex2 (2^-22): a weight's
+    relative error, once in the numerator and once in the sum."""
+    want, want_lse, pv, mag = ref.attention(q, keys, values, scale, visible)
+    d = mag * (len(q) + 4) * 2.0 ** -24 + 2.0 ** -21 + (abs(want_lse) * 2.0 ** -22 if np.isfinite(want_lse) else 0.0)
+    drop = len(keys) * 2.0 ** -32 * np.abs(values).max(0, initial=0.0)
+    tol = 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2 * d) * pv + drop
+    assert np.all(np.abs(o - want) <= tol), (what, float((np.abs(o - want) / np.maximum(tol, 1e-30)).max()))
+    if np.isneginf(want_lse):
+        assert np.isneginf(lse), what
+    else:
+        assert abs(lse - want_lse) <= d, (what, lse, want_lse)
+
+
+DENSE = [  # lens, T, H_q, H_kv, D, ps, splits
+    ([1, 16, 17, 100], 1, 8, 2, 128, 16, 0),
+    ([7, 64, 200], 7, 4, 1, 128, 16, 3),
+    ([33, 40, 129], 5, 6, 2, 64, 32, 0),
+    ([64, 63, 150], 8, 16, 2, 128, 64, 2),
+    ([300], 2, 7, 1, 64, 16, 5),
+    ([2000], 1, 3, 3, 128, 32, 0),
+    ([70, 31], 16, 4, 2, 64, 16, 0),
+    ([90, 65], 13, 1, 1, 128, 64, 1),
+]
+
+
+@pytest.mark.parametrize("lens,T,H_q,H_kv,D,ps,splits", DENSE)
+def test_kv4_dense_verify(spd, lens, T, H_q, H_kv, D, ps, splits):
+    import torch
+    rng = np.random.default_rng(len(lens) * 100 + T + D)
+    k_exp, v_exp = (2, -3) if T % 2 else (0, 0)
+    lens, pt, mp, n, kv4, vals = make_cache(rng, lens, ps, H_kv, D, k_exp, v_exp)
+    B, G = len(lens), H_q // H_kv
+    q = rows_bf16(rng, B, T, H_q, D) * 2.0 ** rng.integers(-3, 2, (B, T, H_q, 1))
+    dims = spd.dims_of(B, H_q, H_kv, D, ps, mp, n)
+    ws = spd.workspace(spd.spd_kv4_dense_verify_workspace_size(dims, T, splits))
+    o = torch.full((B, T, H_q, D), float("nan"), dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((B, T, H_q), float("nan"), device="cuda")
+    scale = 0.11
+    args = (dims, T, to_dev(q), dev(kv4), dev(pt), dev(lens), o, ws)
+    for _ in range(2):  # the workspace is left as it was found
+        spd.kv4_dense_verify_attn(*args, lse=lse, num_splits=splits, softmax_scale=scale, k_exp=k_exp, v_exp=v_exp)
+    torch.cuda.synchronize()
+    assert spd.spd_device_status(clear=True) == 0
+    og, lg = host(o), host(lse)
+    for b in range(B):
+        for t in range(T):
+            seen = np.arange(lens[b]) <= lens[b] - T + t
+            for hq in range(H_q):
+                check_row(og[b, t, hq], lg[b, t, hq], q[b, t, hq], vals[b][0][:, hq // G], vals[b][1][:, hq // G], scale,
+                          seen, (b, t, hq))
+    again = torch.empty_like(o)
+    spd.kv4_dense_verify_attn(*args[:6], again, ws, num_splits=splits, softmax_scale=scale, k_exp=k_exp, v_exp=v_exp)
+    assert torch.equal(again, o)  # and without lse
+
+
+SPARSE = [  # lens, H_q, H_kv, D, ps, k_max, splits
+    ([1, 16, 17, 100, 250], 8, 2, 128, 16, 5, 0),
+    ([600, 33, 129], 6, 2, 64, 32, 9, 3),
+    ([640, 63], 16, 2, 128, 64, 4, 2),
+    ([900], 7, 1, 64, 16, 40, 7),
+    ([500, 20], 3, 3, 128, 16, 31, 1),
+]
+
+
+@pytest.mark.parametrize("lens,H_q,H_kv,D,ps,k_max,splits", SPARSE)
+def test_kv4_sparse_decode(spd, lens, H_q, H_kv, D, ps, k_max, splits):
+    """Random selections in any order, a row with none, and one whose last page is not among its pages."""
+    import torch
+    rng = np.random.default_rng(k_max + D)
+    lens, pt, mp, n, kv4, vals = make_cache(rng, lens, ps, H_kv, D)
+    B, G = len(lens), H_q // H_kv
+    sel = np.full((B, H_kv, k_max), 1 << 20, np.int32)
+    nsel = np.zeros((B, H_kv), np.int32)
+    for b in range(B):
+        P = -(-int(lens[b]) // ps)
+        for h in range(H_kv):
+            nsel[b, h] = 0 if (b == 0 and h == 1) else rng.integers(1, min(P, k_max) + 1)
+            sel[b, h, : nsel[b, h]] = rng.permutation(P)[: nsel[b, h]]
+    q = rows_bf16(rng, B, H_q, D)
+    dims = spd.dims_of(B, H_q, H_kv, D, ps, mp, n)
+    ws = spd.workspace(spd.spd_kv4_sparse_decode_workspace_size(dims, k_max, splits))
+    o = torch.full((B, H_q, D), float("nan"), dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((B, H_q), float("nan"), device="cuda")
+    for _ in range(2):
+        spd.kv4_sparse_decode_attn(dims, to_dev(q), dev(kv4), dev(pt), dev(lens), dev(sel), dev(nsel), k_max, o, ws,
+                                   lse=lse, num_splits=splits)
+    torch.cuda.synchronize()
+    assert spd.spd_device_status(clear=True) == 0
+    og, lg = host(o), host(lse)
+    for b in range(B):
+        for hq in range(H_q):
+            h = hq // G
+            pages = set(sel[b, h, : nsel[b, h]].tolist())
+            seen = np.array([j // ps in pages for j in range(lens[b])])
+            check_row(og[b, hq], lg[b, hq], q[b, hq], vals[b][0][:, h], vals[b][1][:, h], D ** -0.5, seen, (b, hq))
+
+
+def test_kv4_attention_extremes(spd):
+    """Large and tiny queries, logits that grow along the sequence (the reference maximum moves again and again)
+    and one token that outweighs the rest."""
+    import torch
+    rng = np.random.default_rng(21)
+    H_q, H_kv, D, ps = 4, 1, 128, 16
+    lens, pt, mp, n, kv4, vals = make_cache(rng, [400], ps, H_kv, D)
+    q = rows_bf16(rng, 1, 1, H_q, D)
+    q[0, 0, 0] *= 2.0 ** 40
+    q[0, 0, 1] *= 2.0 ** -60
+    q[0, 0, 2] = 0.0
+    q[0, 0, 3, 1:] = 0.0
+    dims = spd.dims_of(1, H_q, H_kv, D, ps, mp, n)
+    for scale in (2.0 ** -42, 0.3):
+        qq = q.copy()
+        if scale == 0.3:
+            qq[0, 0, 0] = ref.bf16(vals[0][0][399, 0] * 4)  # the last key: far above the others
+        ws = spd.workspace(spd.spd_kv4_dense_verify_workspace_size(dims, 1, 0))
+        o = torch.empty((1, 1, H_q, D), dtype=torch.bfloat16, device="cuda")
+        lse = torch.empty((1, 1, H_q), device="cuda")
+        spd.kv4_dense_verify_attn(dims, 1, to_dev(qq), dev(kv4), dev(pt), dev(lens), o, ws, lse=lse, softmax_scale=scale)
+        for hq in range(H_q):
+            check_row(host(o)[0, 0, hq], host(lse)[0, 0, hq], qq[0, 0, hq], vals[0][0][:, 0], vals[0][1][:, 0], scale,
+                      np.ones(400, bool), (scale, hq))
+
+
+def test_kv4_attention_bad_entries(spd):
+    """Entries that point outside the sequence or the cache are skipped, lengths the table cannot hold give empty
+    rows, and the other rows are as without them."""
+    import torch
+    rng = np.random.default_rng(31)
+    H_q, H_kv, D, ps, k_max = 4, 2, 64, 16, 4
+    lens, pt, mp, n, kv4, vals = make_cache(rng, [70, 60, 50, 64], ps, H_kv, D)
+    sel = np.tile(np.arange(k_max, dtype=np.int32), (4, H_kv, 1))
+    nsel = np.full((4, H_kv), k_max, np.int32)
+    q = to_dev(rows_bf16(rng, 4, H_q, D))
+    dims = spd.dims_of(4, H_q, H_kv, D, ps, mp, n)
+    ws = spd.workspace(max(spd.spd_kv4_sparse_decode_workspace_size(dims, k_max), spd.spd_kv4_dense_verify_workspace_size(dims, 1)))
+
+    def run(pt, lens, sel, nsel):
+        o = torch.full((4, H_q, D), float("nan"), dtype=torch.bfloat16, device="cuda")
+        spd.kv4_sparse_decode_attn(dims, q, dev(kv4), dev(pt), dev(lens), dev(sel), dev(nsel), k_max, o, ws)
+        od = torch.full((4, 1, H_q, D), float("nan"), dtype=torch.bfloat16, device="cuda")
+        spd.kv4_dense_verify_attn(dims, 1, q.unsqueeze(1).contiguous(), dev(kv4), dev(pt), dev(lens), od, ws)
+        return o, od[:, 0], spd.spd_device_status(clear=True)
+
+    good, good_d, status = run(pt, lens, sel, nsel)
+    assert status == 0
+    sel2, nsel2, pt2, lens2 = sel.copy(), nsel.copy(), pt.copy(), lens.copy()
+    sel2[0, 0, 1], sel2[0, 1, 2] = -3, 1 << 20
+    nsel2[1, 0], nsel2[1, 1] = -1, k_max + 5
+    pt2[2, 1] = n + 7
+    lens2[3] = mp * ps + 1
+    o, od, status = run(pt2, lens2, sel2, nsel2)
+    assert status == spd.DEV_BAD_SEL | spd.DEV_BAD_PAGE | spd.DEV_BAD_LEN
+    assert not torch.isnan(o.float()).any() and not torch.isnan(od.float()).any()
+    assert torch.count_nonzero(o[3]) == 0 and torch.count_nonzero(od[3]) == 0
+    assert torch.count_nonzero(o[1, : H_q // H_kv]) == 0
+    assert torch.equal(o[1, H_q // H_kv:], good[1, H_q // H_kv:])
+    assert torch.equal(od[:2], good_d[:2])
+    # the skipped page of sequence 2: as a selection without it
+    sel3 = sel.copy()
+    sel3[2, :, 1:3] = sel[2, :, 2:4]
+    nsel3 = nsel.copy()
+    nsel3[2] = 3
+    less, _, _ = run(pt, lens, sel3, nsel3)
+    assert np.abs(host(o)[2] - host(less)[2]).max() <= 2 ** -7 * np.abs(host(less)[2]).max()
+
+
+def test_kv4_step_as_it_is_used(spd):
+    """Projection rows -> qk_norm_rope -> kv4_append -> pages_score_select -> kv4_sparse_decode_attn, the same
+    captured as a graph, and the verification of two positions over the same cache."""
+    import torch
+    rng = np.random.default_rng(41)
+    B, H_q, H_kv, D, ps, k_max = 3, 8, 2, 64, 16, 4
+    lens, pt, mp, n, kv4, vals = make_cache(rng, [100, 130, 75], ps, H_kv, D)
+    dims = spd.dims_of(B, H_q, H_kv, D, ps, mp, n)
+    cache = dev(kv4)
+    # summaries of the whole cache first: every token appended again, in one call per sequence length
+    summ = torch.zeros((B, H_kv, mp, 2, D), dtype=torch.bfloat16, device="cuda")
+    for b in range(B):
+        one = spd.dims_of(1, H_q, H_kv, D, ps, mp, n)
+        ln = int(lens[b])
+        kk, vv = (to_dev(vals[b][i][None]) for i in (0, 1))
+        spd.kv4_append(one, ln, cache, dev(pt[b: b + 1]), dev(lens[b: b + 1]), kk, vv, summ[b: b + 1])
+    before = cache.cpu().numpy()
+    for b in range(B):  # values that are representable are stored as they are
+        for p in range(-(-int(lens[b]) // ps)):
+            m = min(ps, int(lens[b]) - p * ps)
+            for h in range(H_kv):
+                for half in (0, 1):
+                    c, s = ref.kv4_unpack(before[pt[b, p], h, half], ps, D)
+                    assert np.array_equal(ref.kv4_values(c, s, 0)[:m], vals[b][half][p * ps: p * ps + m, h])
+    x = to_dev(rows_bf16(rng, B, H_q + 2 * H_kv, D))
+    q_in, k_in, v_in = torch.split(x, [H_q, H_kv, H_kv], 1)
+    w = to_dev(1 + 0.1 * rng.standard_normal(D))
+    table = dev(ref.rope_table(256, D))
+    pos = dev((lens - 1).astype(np.int32))
+    q, k = torch.empty((B, H_q, D), dtype=torch.bfloat16, device="cuda"), torch.empty((B, H_kv, D), dtype=torch.bfloat16, device="cuda")
+    v = v_in.contiguous()
+    sel = torch.zeros((B, H_kv, k_max), dtype=torch.int32, device="cuda")
+    nsel = torch.zeros((B, H_kv), dtype=torch.int32, device="cuda")
+    pol = spd.Policy(0, k_max, 0, 0, 1, 0, 1, 1, 1, 1)
+    ws = spd.workspace(max(spd.spd_score_select_workspace_size(dims), spd.spd_kv4_sparse_decode_workspace_size(dims, k_max),
+                           spd.spd_kv4_dense_verify_workspace_size(dims, 2)))
+    o = torch.empty((B, H_q, D), dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty((B, H_q), device="cuda")
+    d_pt, d_lens = dev(pt), dev(lens)
+
+    def step():
+        spd.qk_norm_rope(q_in, k_in, pos, table, q, k, q_weight=w, k_weight=w)
+        spd.kv4_append(dims, 1, cache, d_pt, d_lens, k, v, summ)
+        spd.pages_score_select(dims, q, summ, d_lens, pol, sel, nsel, k_max, ws)
+        spd.kv4_sparse_decode_attn(dims, q, cache, d_pt, d_lens, sel, nsel, k_max, o, ws, lse=lse)
+
+    step()
+    torch.cuda.synchronize()
+    assert spd.spd_device_status(clear=True) == 0
+    first = [t.clone() for t in (q, k, cache, summ, sel, nsel, o, lse)]
+    for b in range(B):
+        for i, rows in enumerate((k, v)):
+            vals[b][i][-1] = ref.kv4_values(*ref.kv4_quantise(host(rows)[b], 0), 0)
+        for h in range(H_kv):  # the selection by the score's definition over the values as held
+            P = -(-int(lens[b]) // ps)
+            lo = np.array([vals[b][0][p * ps: min((p + 1) * ps, lens[b]), h].min(0) for p in range(P)])
+            hi = np.array([vals[b][0][p * ps: min((p + 1) * ps, lens[b]), h].max(0) for p in range(P)])
+            qs = host(q)[b, h * 4: h * 4 + 4]
+            score = np.maximum(qs[:, None] * lo, qs[:, None] * hi).sum(-1).max(0)
+            chosen = sel[b, h].tolist()
+            assert chosen == sorted(set(chosen)) and 0 in chosen and P - 1 in chosen
+            worst = min(score[p] for p in chosen if p not in (0, P - 1))
+            rest = [score[p] for p in range(P) if p not in chosen]
+            assert max(rest) <= worst * (1 + 1e-5)
+            seen = np.array([j // ps in chosen for j in range(lens[b])])
+            for hq in range(h * 4, h * 4 + 4):
+                check_row(host(o)[b, hq], host(lse)[b, hq], host(q)[b, hq], vals[b][0][:, h], vals[b][1][:, h], D ** -0.5,
+                          seen, (b, hq))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for t in (q, k, o, lse):
+        t.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(first, (q, k, cache, summ, sel, nsel, o, lse)))
+    q2 = rows_bf16(rng, B, 2, H_q, D)
+    o2 = torch.empty((B, 2, H_q, D), dtype=torch.bfloat16, device="cuda")
+    lse2 = torch.empty((B, 2, H_q), device="cuda")
+    spd.kv4_dense_verify_attn(dims, 2, to_dev(q2), cache, d_pt, d_lens, o2, ws, lse=lse2)
+    for b in range(B):
+        for t in range(2):
+            for hq in range(H_q):
+                check_row(host(o2)[b, t, hq], host(lse2)[b, t, hq], q2[b, t, hq], vals[b][0][:, hq // 4], vals[b][1][:, hq // 4],
+                          D ** -0.5, np.arange(lens[b]) <= lens[b] - 2 + t, (b, t, hq))
+
+
+def test_kv4_cache_past_4_gib(spd):
+    """Pages whose byte offset in the cache passes 32 bits."""
+    import torch
+    rng = np.random.default_rng(51)
+    H, D, ps = 8, 128, 64
+    tile = ps * D * 9 // 8
+    n = (5 << 30) // (H * tile)
+    lens, pt, mp, m, kv4, vals = make_cache(rng, [150], ps, H, D)
+    cache = torch.zeros((n, H, 2, tile // 2), dtype=torch.uint8, device="cuda")
+    far = np.array([n - 1, 3, n - 5])
+    for p in range(3):
+        cache[int(far[p])] = dev(kv4[pt[0, p]])
+    pt2 = pt.copy()
+    pt2[0, :3] = far
+    dims = spd.dims_of(1, H, H, D, ps, mp, n)
+    q = rows_bf16(rng, 1, 1, H, D)
+    o, lse = torch.empty((1, 1, H, D), dtype=torch.bfloat16, device="cuda"), torch.empty((1, 1, H), device="cuda")
+    ws = spd.workspace(spd.spd_kv4_dense_verify_workspace_size(dims, 1))
+    spd.kv4_dense_verify_attn(dims, 1, to_dev(q), cache, dev(pt2), dev(lens), o, ws, lse=lse)
+    for h in range(H):
+        check_row(host(o)[0, 0, h], host(lse)[0, 0, h], q[0, 0, h], vals[0][0][:, h], vals[0][1][:, h], D ** -0.5,
+                  np.ones(150, bool), h)
+    k, v = (rows_bf16(rng, 1, 2, H, D) for _ in range(2))
+    summ = torch.zeros((1, H, mp, 2, D), dtype=torch.bfloat16, device="cuda")
+    ko, vo = (torch.empty((1, 2, H, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    spd.kv4_append(dims, 2, cache, dev(pt2), dev(lens), to_dev(k), to_dev(v), summ)
+    spd.kv4_read(dims, 2, cache, dev(pt2), dev(lens), ko, vo)
+    assert np.array_equal(host(ko), ref.kv4_values(*ref.kv4_quantise(k, 0), 0))
+    assert np.array_equal(host(vo), ref.kv4_values(*ref.kv4_quantise(v, 0), 0))
+    assert spd.spd_device_status(clear=True) == 0
