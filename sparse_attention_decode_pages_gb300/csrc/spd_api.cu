@@ -1076,6 +1076,7 @@ static spd_status logprob_shape(int64_t rows, int32_t n_vocab, int32_t top_k) {
     if (rows < 0 || rows >= (1LL << 31)) return fail(SPD_ERR_INVALID_ARG, "rows = %lld outside [0, 2^31)", (long long)rows);
     if (n_vocab < 1 || n_vocab > (1 << 21)) return fail(SPD_ERR_UNSUPPORTED, "n_vocab = %d outside [1, 2^21]", n_vocab);
     if (top_k < 0 || top_k > 32) return fail(SPD_ERR_UNSUPPORTED, "top_k = %d outside [0, 32]", top_k);
+    if (rows * ((n_vocab >> 10) + 1) >= (1LL << 31)) return fail(SPD_ERR_UNSUPPORTED, "rows * n_vocab too large");
     return SPD_OK;
 }
 
