@@ -8,14 +8,17 @@
 //                                   lowest value overflows nothing)
 // and M, S, T of two parts of a row join by shifting the smaller M's sums.
 //
-// A row is cut into parts that fit the registers of one CTA: every thread issues all
-// of its 16-byte loads at once and keeps the values, so the exact maximum is known
-// before the sums (no running rescale) and the alternatives need no second read.
-// The part's K-th largest of the 256 thread maxima bounds its K-th largest logit from
-// below; only threads whose maximum reaches that bound scan their values, and the few
-// dozen survivors are ranked by counting.  (Should more survive than the list holds --
-// rows of equal logits -- the K largest are taken one by one instead.)  The last part
-// of a row to finish (an atomic ticket; nothing waits) joins the parts.
+// A CTA streams one part of a row, a tile of 256 threads x 4 vectors at a time, the
+// next tile's loads in flight while it works on one.  Each thread keeps S and T
+// relative to a reference of its own, which moves only when a value exceeds it by
+// kLpHead, so nothing is exchanged per tile.  For the alternatives the CTA keeps a
+// list of candidates and a bound that at least K values reach: first the K-th largest
+// of the 256 thread maxima of the first tile, then, after 2, 4, 8, ... tiles, the K-th
+// largest of the list, which is cut to K at the same time; a thread looks at its
+// single values only where its tile's maximum reaches the bound.  (Should more values
+// pass than the list holds -- ascending rows, rows of equal logits -- the part's K
+// largest are taken one by one from memory instead.)  The last part of a row to
+// finish (an atomic ticket; nothing waits) joins the parts.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -24,6 +27,9 @@ namespace spd {
 constexpr int kLpThreads = 256;
 constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kLpList = 1024;  // survivors a CTA can hold
+constexpr int kLpU = 4;        // 16-byte vectors of a thread in a tile
+constexpr int kLpTile = kLpThreads * kLpU;
+constexpr float kLpHead = 6.f;  // log2 headroom before a thread's reference moves
 typedef unsigned long long u64;
 
 // The order of the alternatives as a whole number: the larger logit first (-0 as 0), the
@@ -65,24 +71,33 @@ struct LpStat {
 };
 
 struct LpPlan {
-    int nv;     // 16-byte vectors a thread holds
     int parts;  // of a row
-    int vecs;   // of a part
+    int vecs;   // 16-byte vectors of a part
 };
 
-// Rows are cut into the largest parts that still give every SM two CTAs, else into
-// parts a quarter as large: a single row of 151,936 fp32 logits takes 38 CTAs.
+// Parts of a row: the number whose CTAs, run kLpOcc to an SM, take the least time by
+// waves * (tiles of a part + kLpFixed).  kLpFixed stands for what a CTA does besides
+// streaming (the first bound, the joins), in tiles.  448 rows of 151,936 fp32 logits:
+// whole rows, one wave, 52 us; halves, two waves, 65 us; fifths 79 us.  One row: a part
+// for each tile.
+constexpr int kLpOcc = 3;
+constexpr int kLpFixed = 6;
+
 inline LpPlan lp_plan(long long rows, int n, bool bf16, int sms) {
-    const int ve = bf16 ? 8 : 4;
-    const int nvec = (n + 2 * ve - 2) / ve;  // a row that starts inside a vector touches one more
-    LpPlan p;
-    p.nv = 16;
-    p.parts = (nvec + p.nv * kLpThreads - 1) / (p.nv * kLpThreads);
-    if (rows * p.parts < 2LL * sms) {
-        p.nv = 4;
-        p.parts = (nvec + p.nv * kLpThreads - 1) / (p.nv * kLpThreads);
+    const int nvec = n / (bf16 ? 8 : 4) + 1;
+    const int most = (nvec + kLpTile - 1) / kLpTile;
+    const long long slots = (long long)kLpOcc * sms;
+    LpPlan p = {1, nvec};
+    long long best = -1;
+    for (int parts = 1; parts <= most; ++parts) {
+        const int vecs = (nvec + parts - 1) / parts;
+        const long long cost = (rows * parts + slots - 1) / slots * ((vecs + kLpTile - 1) / kLpTile + kLpFixed);
+        if (best < 0 || cost < best) {
+            best = cost;
+            p.parts = parts;
+            p.vecs = vecs;
+        }
     }
-    p.vecs = (nvec + p.parts - 1) / p.parts;
     return p;
 }
 
@@ -110,126 +125,220 @@ struct LpShared {
     unsigned tmax[kLpThreads];
     float a[kLpWarps], b[kLpWarps];
     u64 best[kLpWarps];
-    int count, flag;
-    unsigned bound;
+    int count, flag, over;
+    float bound;
+    unsigned join_bound;
 };
 
-// The K largest of the s.count keys of s.list, in order, into s.top (0 where there are
-// fewer); the keys differ from one another.
-__device__ __forceinline__ void lp_rank(LpShared& s, int K) {
-    for (int i = threadIdx.x; i < s.count; i += kLpThreads) {
+// The K largest of the first n keys of s.list, in order, into s.top (whose entries from
+// n on stay as they are); the keys differ from one another.
+__device__ __forceinline__ void lp_rank(LpShared& s, int n, int K) {
+    for (int i = threadIdx.x; i < n; i += kLpThreads) {
         const u64 mine = s.list[i];
         int r = 0;
-        for (int j = 0; j < s.count; ++j) r += s.list[j] > mine;
+        for (int j = 0; j < n; ++j) r += s.list[j] > mine;
         if (r < K) s.top[r] = mine;
     }
 }
 
-template <bool BF16, int NV>
-__global__ void __launch_bounds__(kLpThreads, NV >= 16 ? 2 : 3) logprob_kernel(const LogprobArgs a, const LpPlan plan, const LpWs w) {
-    constexpr int VE = BF16 ? 8 : 4;
+// Adds a candidate to the list.
+__device__ __forceinline__ void lp_push(LpShared& s, float x, int token) {
+    const int at = atomicAdd(&s.count, 1);
+    if (at < kLpList) s.list[at] = lp_key(lp_order(x), token);
+}
+
+// Cuts the list to its K largest and raises the bound to the last of them.  By all threads.
+__device__ __forceinline__ void lp_raise(LpShared& s, int K) {
+    __syncthreads();
+    const int n = min(s.count, kLpList);
+    if (n > K) lp_rank(s, n, K);
+    __syncthreads();
+    if (n > K) {
+        if (threadIdx.x < K) s.list[threadIdx.x] = s.top[threadIdx.x];
+        if (threadIdx.x == 0) {
+            if (s.count > kLpList) s.over = 1;
+            s.count = K;
+            s.bound = lp_key_value(s.top[K - 1]);
+        }
+    }
+    __syncthreads();
+}
+
+// One tile's kept values.
+struct LpRegs {
+    uint4 x[kLpU];
+};
+
+template <bool BF16>
+__global__ void __launch_bounds__(kLpThreads, kLpOcc) logprob_kernel(const LogprobArgs a, const LpPlan plan, const LpWs w) {
+    constexpr int VE = BF16 ? 8 : 4, SZ = BF16 ? 2 : 4;
+    constexpr uint32_t kNone = BF16 ? 0xff80ff80u : 0xff800000u;  // -inf
     __shared__ LpShared s;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const long long row = blockIdx.x / plan.parts;
     const int part = blockIdx.x % plan.parts;
     const int K = a.top_k;
     const float NEG_INF = __int_as_float(0xff800000);
-    const char* rowp = static_cast<const char*>(a.logits) + row * a.row_stride * (BF16 ? 2 : 4);
-    const int lead = (int)(reinterpret_cast<uintptr_t>(rowp) & 15) / (BF16 ? 2 : 4);  // elements before the row in its first vector
-    const uint4* vecs = reinterpret_cast<const uint4*>(rowp - lead * (BF16 ? 2 : 4));
-    const int v0 = part * plan.vecs, v1 = min(v0 + plan.vecs, (lead + a.n + VE - 1) / VE);
-    if (tid == 0) s.count = 0;
+    const char* rowp = static_cast<const char*>(a.logits) + row * a.row_stride * SZ;
+    // whole vectors of the row, and the tokens before and behind them
+    const int head = min(a.n, (int)((16 - (reinterpret_cast<uintptr_t>(rowp) & 15)) & 15) / SZ);
+    const uint4* vecs = reinterpret_cast<const uint4*>(rowp + head * SZ);
+    const int nvec = (a.n - head) / VE;
+    const int v0 = min(part * plan.vecs, nvec), v1 = part == plan.parts - 1 ? nvec : min(v0 + plan.vecs, nvec);
+    if (tid == 0) {
+        s.count = 0;
+        s.over = 0;
+    }
     if (tid < 32) s.top[tid] = 0ull;
     pdl_wait();
     pdl_trigger();
 
-    // all loads, then the thread's largest value
-    uint4 x[NV];
+    auto load = [&](int tile) {
+        LpRegs r;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int v = v0 + tid + j * kLpThreads;
-        const int i0 = v * VE - lead;  // token of the vector's first element
-        constexpr uint32_t kNone = BF16 ? 0xff80ff80u : 0xff800000u;  // -inf
-        x[j] = make_uint4(kNone, kNone, kNone, kNone);
-        if (v < v1) {
-            if (i0 >= 0 && i0 + VE <= a.n) {
-                x[j] = lp_load(vecs + v);
-            } else {  // a vector that the row fills in part
-                uint32_t t[4] = {kNone, kNone, kNone, kNone};
+        for (int j = 0; j < kLpU; ++j) {
+            const int v = v0 + tile * kLpTile + tid + j * kLpThreads;
+            r.x[j] = v < v1 ? lp_load(vecs + v) : make_uint4(kNone, kNone, kNone, kNone);
+        }
+        return r;
+    };
+    const float c2 = a.inv_t * kLog2e;
+    float ref = NEG_INF, S = 0.f, T = 0.f;
+    // sums of one tile; returns the thread's largest value in it
+    auto sums = [&](const LpRegs& r) {
+        float m = NEG_INF;
 #pragma unroll
-                for (int e = 0; e < VE; ++e)
-                    if (i0 + e >= 0 && i0 + e < a.n) {
-                        if (BF16) {
-                            const uint32_t h = reinterpret_cast<const uint16_t*>(rowp)[i0 + e];
-                            t[e >> 1] = e & 1 ? (t[e >> 1] & 0xffffu) | h << 16 : (t[e >> 1] & 0xffff0000u) | h;
-                        } else {
-                            t[e & 3] = reinterpret_cast<const uint32_t*>(rowp)[i0 + e];
-                        }
-                    }
-                x[j] = make_uint4(t[0], t[1], t[2], t[3]);
+        for (int j = 0; j < kLpU; ++j)
+#pragma unroll
+            for (int e = 0; e < VE; ++e) m = fmaxf(m, lp_elem<BF16>(r.x[j], e));
+        if ((m - ref) * c2 > kLpHead || (ref == NEG_INF && m > NEG_INF)) {
+            if (ref > NEG_INF) {
+                const float d = (ref - m) * c2, f = fast_exp2(d);
+                T = f * fmaf(fmaxf(d, -1e30f), S, T);
+                S *= f;
             }
+            ref = m;
+        }
+        const float base = ref == NEG_INF ? 0.f : ref;
+#pragma unroll
+        for (int j = 0; j < kLpU; ++j)
+#pragma unroll
+            for (int e = 0; e < VE; ++e) {
+                const float d = (lp_elem<BF16>(r.x[j], e) - base) * c2;
+                const float p = fast_exp2(d);
+                S += p;
+                T = fmaf(p, fmaxf(d, -1e30f), T);
+            }
+        return m;
+    };
+    auto scan = [&](const LpRegs& r, int tile, float bound) {
+#pragma unroll
+        for (int j = 0; j < kLpU; ++j)
+#pragma unroll
+            for (int e = 0; e < VE; ++e) {
+                const float x = lp_elem<BF16>(r.x[j], e);
+                if (x >= bound) lp_push(s, x, head + (v0 + tile * kLpTile + tid + j * kLpThreads) * VE + e);
+            }
+    };
+
+    const int tiles = (v1 - v0 + kLpTile - 1) / kLpTile;
+    LpRegs cur = load(0);
+    // the tokens outside the row's whole vectors: a thread each, of the first and the last part
+    float edge = NEG_INF;
+    int edge_token = 0;
+    {
+        const int tail0 = head + nvec * VE;
+        if (part == 0 && tid < head) {
+            edge_token = tid;
+            edge = lp_at<BF16>(rowp, tid);
+        } else if (part == plan.parts - 1 && tid >= 32 && tid - 32 < a.n - tail0) {
+            edge_token = tail0 + tid - 32;
+            edge = lp_at<BF16>(rowp, edge_token);
         }
     }
-    float m = NEG_INF;
+    {
+        LpRegs next = load(1);
+        float m = sums(cur);
+        if (!(edge == NEG_INF)) {  // NaN too
+            LpRegs one;
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+            for (int j = 0; j < kLpU; ++j) one.x[j] = make_uint4(kNone, kNone, kNone, kNone);
+            one.x[0].x = BF16 ? (__float_as_uint(edge) >> 16) | 0xff800000u : __float_as_uint(edge);
+            m = fmaxf(m, sums(one));
+        }
+        if (K > 0) {
+            // the first bound: the K-th largest thread maximum with its low bits cleared, found a
+            // bit at a time from the highest in which the maxima differ
+            s.tmax[tid] = lp_order(m);
+            __syncthreads();
+            if (warp == 0) {
+                unsigned t[kLpThreads / 32];
+                unsigned lo = 0xffffffffu, hi = 0;
 #pragma unroll
-        for (int e = 0; e < VE; ++e) m = fmaxf(m, lp_elem<BF16>(x[j], e));
-    const unsigned mine = lp_order(m);
-    s.tmax[tid] = mine;
+                for (int i = 0; i < kLpThreads / 32; ++i) {
+                    t[i] = s.tmax[lane + 32 * i];
+                    lo = min(lo, t[i]);
+                    hi = max(hi, t[i]);
+                }
+                lo = __reduce_min_sync(0xffffffffu, lo);
+                hi = __reduce_max_sync(0xffffffffu, hi);
+                const int top = hi == lo ? 0 : 32 - __clz(hi ^ lo);  // the bits that differ lie below 2^top
+                unsigned bound = top >= 32 ? 0u : hi >> top << top;
+                for (int bit = top - 1; bit >= max(0, top - 12); --bit) {
+                    const unsigned cand = bound | 1u << bit;
+                    int c = 0;
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-    if (lane == 0) s.a[warp] = m;
+                    for (int i = 0; i < kLpThreads / 32; ++i) c += t[i] >= cand;
+                    if ((int)__reduce_add_sync(0xffffffffu, (unsigned)c) >= K) bound = cand;
+                }
+                // at least the lowest finite value, so that nothing at -inf passes
+                const unsigned least = float_key(-3.402823466e+38f);
+                if (lane == 0) s.bound = lp_key_value((u64)max(bound, least) << 32);
+            }
+            __syncthreads();
+            const float bound = s.bound;
+            if (m >= bound) {
+                scan(cur, 0, bound);
+                if (edge >= bound) lp_push(s, edge, edge_token);
+            }
+        }
+        cur = next;
+    }
+    int raise = 1;
+    for (int t = 1; t < tiles; ++t) {
+        LpRegs next = load(t + 1);
+        if (K > 0 && t == raise) {
+            lp_raise(s, K);
+            raise *= 2;
+        }
+        const float m = sums(cur);
+        if (K > 0) {
+            const float bound = s.bound;
+            if (m >= bound) scan(cur, t, bound);
+        }
+        cur = next;
+    }
+
+    // the threads' sums relative to the part's largest reference
+    float M = ref;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    if (lane == 0) s.a[warp] = M;
     __syncthreads();
-    float M = s.a[0];
+    M = s.a[0];
 #pragma unroll
     for (int i = 1; i < kLpWarps; ++i) M = fmaxf(M, s.a[i]);
-    __syncthreads();
-
-    // the bound: the K-th largest thread maximum, its low bits cleared (one warp, a bit at a
-    // time from the highest in which the maxima can differ), while the others sum
-    if (K > 0 && warp == 0) {
-        unsigned t[kLpThreads / 32];
-        unsigned lo = 0xffffffffu;
-#pragma unroll
-        for (int i = 0; i < kLpThreads / 32; ++i) {
-            t[i] = s.tmax[lane + 32 * i];
-            lo = min(lo, t[i]);
-        }
-        lo = __reduce_min_sync(0xffffffffu, lo);
-        const unsigned hi = lp_order(M);
-        unsigned bound = 0;
-        if (hi != 0) {
-            const int top = hi == lo ? 0 : 32 - __clz(hi ^ lo);  // bits that differ: below 2^top
-            bound = top >= 32 ? 0u : hi >> top << top;
-            for (int bit = top - 1; bit >= max(0, top - 12); --bit) {
-                const unsigned cand = bound | 1u << bit;
-                int c = 0;
-#pragma unroll
-                for (int i = 0; i < kLpThreads / 32; ++i) c += t[i] >= cand;
-                if ((int)__reduce_add_sync(0xffffffffu, (unsigned)c) >= K) bound = cand;
-            }
-        }
-        if (lane == 0) s.bound = bound;
+    if (ref > NEG_INF) {
+        const float d = (ref - M) * c2, f = fast_exp2(d);
+        T = f * fmaf(fmaxf(d, -1e30f), S, T);
+        S *= f;
     }
-
-    const float c2 = a.inv_t * kLog2e;
-    const float ref = M == NEG_INF ? 0.f : M;
-    float S = 0.f, T = 0.f;
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int e = 0; e < VE; ++e) {
-            const float d = (lp_elem<BF16>(x[j], e) - ref) * c2;
-            const float p = fast_exp2(d);
-            S += p;
-            T = fmaf(p, fmaxf(d, -1e30f), T);
-        }
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
         S += __shfl_xor_sync(0xffffffffu, S, off);
         T += __shfl_xor_sync(0xffffffffu, T, off);
     }
+    __syncthreads();
     if (lane == 0) {
         s.a[warp] = S;
         s.b[warp] = T;
@@ -241,36 +350,20 @@ __global__ void __launch_bounds__(kLpThreads, NV >= 16 ? 2 : 3) logprob_kernel(c
         S += s.a[i];
         T += s.b[i];
     }
-
     if (K > 0) {
-        const unsigned bound = max(s.bound, 1u);
-        if (mine >= bound) {
-#pragma unroll
-            for (int j = 0; j < NV; ++j)
-#pragma unroll
-                for (int e = 0; e < VE; ++e) {
-                    const unsigned o = lp_order(lp_elem<BF16>(x[j], e));
-                    if (o >= bound) {
-                        const int at = atomicAdd(&s.count, 1);
-                        if (at < kLpList) s.list[at] = lp_key(o, (v0 + tid + j * kLpThreads) * VE - lead + e);
-                    }
-                }
-        }
-        __syncthreads();
-        if (s.count <= kLpList) {
-            lp_rank(s, K);
-        } else {  // one by one: each the largest below the last
+        const int n = s.count;
+        if (n <= kLpList && !s.over) {
+            lp_rank(s, n, K);
+        } else {  // one by one from memory: each the largest below the last
+            const int t0 = part == 0 ? 0 : head + v0 * VE, t1 = part == plan.parts - 1 ? a.n : head + v1 * VE;
             u64 last = ~0ull;
             for (int k = 0; k < K; ++k) {
                 u64 best = 0ull;
-#pragma unroll
-                for (int j = 0; j < NV; ++j)
-#pragma unroll
-                    for (int e = 0; e < VE; ++e) {
-                        const unsigned o = lp_order(lp_elem<BF16>(x[j], e));
-                        const u64 key = lp_key(o, (v0 + tid + j * kLpThreads) * VE - lead + e);
-                        if (o != 0 && key < last && key > best) best = key;
-                    }
+                for (int i = t0 + tid; i < t1; i += kLpThreads) {
+                    const unsigned o = lp_order(lp_at<BF16>(rowp, i));
+                    const u64 key = lp_key(o, i);
+                    if (o != 0 && key < last && key > best) best = key;
+                }
 #pragma unroll
                 for (int off = 1; off < 32; off <<= 1) {
                     const u64 y = __shfl_xor_sync(0xffffffffu, best, off);
@@ -300,7 +393,7 @@ __global__ void __launch_bounds__(kLpThreads, NV >= 16 ? 2 : 3) logprob_kernel(c
             if (s.flag) w.tickets[row] = 0;
             fence_acq_rel_gpu();
             s.count = 0;
-            s.bound = 0;
+            s.join_bound = 0;
         }
         __syncthreads();
         if (!s.flag) return;
@@ -344,7 +437,7 @@ __global__ void __launch_bounds__(kLpThreads, NV >= 16 ? 2 : 3) logprob_kernel(c
             for (int p = tid; p < plan.parts; p += kLpThreads)
                 bound = max(bound, (unsigned)(__ldcg(keys + (long long)p * K + K - 1) >> 32));
             bound = __reduce_max_sync(0xffffffffu, bound);
-            if (lane == 0) atomicMax(&s.bound, bound);
+            if (lane == 0) atomicMax(&s.join_bound, bound);
         }
         __syncthreads();
         S = T = 0.f;
@@ -354,7 +447,7 @@ __global__ void __launch_bounds__(kLpThreads, NV >= 16 ? 2 : 3) logprob_kernel(c
             T += s.b[i];
         }
         if (K > 0) {
-            const unsigned bound = max(s.bound, 1u);
+            const unsigned bound = max(s.join_bound, 1u);
             for (int i = tid; i < plan.parts * K; i += kLpThreads) {
                 const u64 key = __ldcg(keys + i);
                 if ((unsigned)(key >> 32) >= bound) {
@@ -364,7 +457,7 @@ __global__ void __launch_bounds__(kLpThreads, NV >= 16 ? 2 : 3) logprob_kernel(c
             }
             __syncthreads();
             if (s.count <= kLpList) {
-                lp_rank(s, K);
+                lp_rank(s, s.count, K);
             } else {
                 u64 last = ~0ull;
                 for (int k = 0; k < K; ++k) {
@@ -428,11 +521,8 @@ cudaError_t launch_token_logprobs(const LogprobArgs& a, int num_sms, cudaStream_
     LpWs w;
     lp_ws_layout(a.ws, a.rows, p.parts, a.top_k, &w);
     const dim3 grid((unsigned)(a.rows * p.parts)), block(kLpThreads);
-    if (a.bf16)
-        return p.nv == 16 ? launch_pdl(logprob_kernel<true, 16>, grid, block, 0, st, a, p, w)
-                          : launch_pdl(logprob_kernel<true, 4>, grid, block, 0, st, a, p, w);
-    return p.nv == 16 ? launch_pdl(logprob_kernel<false, 16>, grid, block, 0, st, a, p, w)
-                      : launch_pdl(logprob_kernel<false, 4>, grid, block, 0, st, a, p, w);
+    return a.bf16 ? launch_pdl(logprob_kernel<true>, grid, block, 0, st, a, p, w)
+                  : launch_pdl(logprob_kernel<false>, grid, block, 0, st, a, p, w);
 }
 
 }  // namespace spd
