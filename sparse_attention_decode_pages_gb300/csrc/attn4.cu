@@ -3,8 +3,12 @@
 //
 // A unit is a run of at most pages_per_split pages of one (sequence, KV head) row;
 // it holds all R = T * G query rows of the KV head in n-tiles of eight.  A CTA
-// takes one unit, its warps the unit's 16-token chunks in turn.  Per chunk, on the
-// tensor cores (mma.sync m16n8k16, fp16 in, fp32 out):
+// takes one unit; its warps take the unit's 16-token chunks in turn, each on its own:
+// lane i resolves the warp's i-th next chunk (selection entry, page-table entry), and
+// the warp keeps a ring of chunks filled by bulk copies, refilling a slot as soon as it
+// has read it, so no warp waits for another before the unit's end.
+//
+// Per chunk, on the tensor cores (mma.sync m16n8k16, fp16 in, fp32 out):
 //
 //   S^T = K Q^T   (rows: 16 tokens, columns: 8 query rows)
 //   O^T += V^T P^T
@@ -15,8 +19,8 @@
 // the D / 4 channels from c * D / 4 on of tokens g and g + 8, contiguous in memory,
 // and V's channels g * D / 8 ... of tokens 2c, 2c+1, 2c+8, 2c+9.  Queries are
 // scaled by a power of two into fp16's range (the factor goes into the logits'
-// scale).  Online softmax in fp32 in base 2; a column's reference maximum moves only
-// when a logit exceeds it by kHead4, and weights carry a factor 2^kBias4 so that what
+// scale).  Online softmax in fp32 in base 2; a column's reference moves only when a
+// logit exceeds it by kHead4, and weights carry a factor 2^kBias4 so that what
 // fp16 drops of a weight lies 2^-32 below the reference.
 #include "kv4.cuh"
 #include "kernels.h"
@@ -39,39 +43,52 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+constexpr float kLow4 = -3.0e38f;  // a column's reference before its first visible token
+
 template <int D, int NT>
 struct Attn4Cfg {
-    static constexpr int NTW = NT < 2 ? NT : 2;     // n-tiles of a warp
+    static constexpr int NTW = NT < 4 ? NT : 4;     // n-tiles of a warp
     static constexpr int NG = NT / NTW;             // warps that share a chunk's tokens
-    static constexpr int TW = NG <= 2 ? 4 : 2;      // chunks in work at once
+    static constexpr int TW = 4 / NG;               // chunks in work at once
     static constexpr int WARPS = NG * TW;
     static constexpr int THREADS = 32 * WARPS;
     static constexpr int COLS = NT * 8;
-    static constexpr int OFF_FAC = 0;                              // float [COLS]: logit scale of each query row
+    static constexpr int STAGES = 4;                // ring slots of a warp
+    static constexpr int CHUNK = kv4_tile_bytes(16, D);  // bytes of 16 tokens' keys and values
+    static constexpr int RING = WARPS * STAGES * CHUNK;
+    static constexpr int MERGE = TW * COLS * D * 4;  // float [TW][COLS][D], over the ring when it is done
+    static constexpr int OFF_Q = RING > MERGE ? RING : MERGE;      // half [COLS][D]
+    static constexpr int OFF_FAC = OFF_Q + COLS * D * 2;           // float [COLS]: logit scale of each query row
     static constexpr int OFF_M = OFF_FAC + COLS * 4;               // float [TW][COLS]
     static constexpr int OFF_L = OFF_M + TW * COLS * 4;            // float [TW][COLS]
-    static constexpr int OFF_Q = OFF_L + TW * COLS * 4;            // half [COLS][D]
-    static constexpr int OFF_O = OFF_Q + COLS * D * 2;             // float [TW][COLS][D]
-    static constexpr int SMEM = OFF_O + TW * COLS * D * 4;
+    static constexpr int OFF_BAR = OFF_L + TW * COLS * 4;          // uint64 [WARPS][STAGES]
+    static constexpr int OFF_META = OFF_BAR + WARPS * STAGES * 8;  // int [WARPS][STAGES]: first position or -1
+    static constexpr int SMEM = OFF_META + WARPS * STAGES * 4;
+    // CTAs that the registers leave room for on an SM
+    static constexpr int OCC = NT <= 1 ? 5 : (NT == 2 ? 3 : 2);
 };
 
 template <int D, int NT, bool SPARSE>
-__global__ void __launch_bounds__(Attn4Cfg<D, NT>::THREADS) attn4_kernel(const Attn4Args a) {
+__global__ void __launch_bounds__(Attn4Cfg<D, NT>::THREADS, Attn4Cfg<D, NT>::OCC) attn4_kernel(const Attn4Args a) {
     using C = Attn4Cfg<D, NT>;
-    constexpr int NTW = C::NTW, TW = C::TW, COLS = C::COLS;
+    constexpr int NTW = C::NTW, TW = C::TW, COLS = C::COLS, STAGES = C::STAGES;
     constexpr int KW = D / 32;  // 32-bit code words of a lane's share of a key row
     constexpr int VW = D / 64;  // and of a value row
     constexpr int MT = D / 16;  // 16-channel m-tiles of O^T
-    extern __shared__ __align__(16) uint8_t smem[];
+    constexpr int CODES = kv4_codes_bytes(16, D), HALF = kv4_half_bytes(16, D);  // of a chunk
+    extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int s_last;
     float* s_fac = reinterpret_cast<float*>(smem + C::OFF_FAC);
     float* s_m = reinterpret_cast<float*>(smem + C::OFF_M);
     float* s_l = reinterpret_cast<float*>(smem + C::OFF_L);
     __half* s_q = reinterpret_cast<__half*>(smem + C::OFF_Q);
-    float* s_o = reinterpret_cast<float*>(smem + C::OFF_O);
+    float* s_o = reinterpret_cast<float*>(smem);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, c = lane & 3;
     const int tw = warp % TW, ng = warp / TW;
+    uint8_t* ring = smem + warp * STAGES * C::CHUNK;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR) + warp * STAGES;
+    int* meta = reinterpret_cast<int*>(smem + C::OFF_META) + warp * STAGES;
     const int G = a.H_q / a.H_kv, R = a.T * G;
     const float NEG_INF = __int_as_float(0xff800000);
 
@@ -81,9 +98,21 @@ __global__ void __launch_bounds__(Attn4Cfg<D, NT>::THREADS) attn4_kernel(const A
         const int t = r / G;
         return ((long long)b * a.T + t) * a.H_q + h * G + (r - t * G);
     };
+    if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < STAGES; ++i) mbar_init(full + i, 1);
+        mbar_fence_init();
+    }
+    __syncwarp();
     pdl_wait();
     pdl_trigger();
 
+    const int start = split * a.pages_per_split;
+    const int cpp = a.ps >> 4;  // chunks per page
+    // chunk k of this warp is chunk tw + k * TW of the unit; the first selection entries
+    // are read together with the length and the count
+    int sel0 = 0;
+    if (SPARSE && start + (tw + lane * TW) / cpp < a.k_max) sel0 = a.sel[(long long)row * a.k_max + start + (tw + lane * TW) / cpp];
     const int len = a.seq_lens[b];
     int P = seq_pages(len, a.ps, a.max_pages);
     if (P < 0) {
@@ -98,7 +127,6 @@ __global__ void __launch_bounds__(Attn4Cfg<D, NT>::THREADS) attn4_kernel(const A
             n_items = n_items < 0 ? 0 : a.k_max;
         }
     }
-    const int start = split * a.pages_per_split;
     const int count = min(a.pages_per_split, n_items - start);
     if (count <= 0) {
         if (split == 0)
@@ -110,6 +138,57 @@ __global__ void __launch_bounds__(Attn4Cfg<D, NT>::THREADS) attn4_kernel(const A
         return;
     }
     const int nsplit = (n_items + a.pages_per_split - 1) / a.pages_per_split;
+    const int chunks = count * cpp;
+    const int mine = chunks > tw ? (chunks - tw + TW - 1) / TW : 0;  // of this warp
+
+    // this lane's chunk base + lane: its physical page and first position (-1: nothing to read)
+    auto resolve = [&](int base, int& phys, int& pos) {
+        phys = pos = -1;
+        const int k = base + lane;
+        if (k < mine) {
+            const int ci = tw + k * TW, item = ci / cpp;
+            const int lp = !SPARSE ? start + item : base == 0 ? sel0 : a.sel[(long long)row * a.k_max + start + item];
+            if (lp < 0 || lp >= P) {
+                raise_status(a.status, SPD_DEV_BAD_SEL);
+            } else {
+                const int at = lp * a.ps + (ci - item * cpp) * 16;
+                const int ph = a.page_table[(long long)b * a.max_pages + lp];
+                if (ph < 0 || ph >= a.num_phys) raise_status(a.status, SPD_DEV_BAD_PAGE);
+                else if (at < len) {
+                    phys = ph;
+                    pos = at;
+                }
+            }
+        }
+    };
+    int ph_cur, pos_cur, ph_next = -1, pos_next = -1;
+    resolve(0, ph_cur, pos_cur);
+    // issues chunk k into its slot (by the whole warp; the copies by lanes 0-3)
+    const int codes = kv4_codes_bytes(a.ps, D), half = kv4_half_bytes(a.ps, D);
+    auto issue = [&](int k) {
+        const int slot = k % STAGES;
+        const int phys = __shfl_sync(0xffffffffu, ph_cur, k & 31), pos = __shfl_sync(0xffffffffu, pos_cur, k & 31);
+        if (lane == 0) {
+            meta[slot] = pos;
+            mbar_arrive_expect_tx(full + slot, pos >= 0 ? C::CHUNK : 0);
+        }
+        __syncwarp();
+        if (pos >= 0) {
+            const uint8_t* tile = a.kv4 + ((long long)phys * a.H_kv + h) * (2LL * half);
+            uint8_t* dst = ring + slot * C::CHUNK;
+            if (a.ps == 16) {
+                if (lane == 0) bulk_load(dst, tile, C::CHUNK, full + slot);
+            } else if (lane < 4) {  // keys' codes and scales, values' codes and scales
+                const int t0 = pos & (a.ps - 1);
+                const uint8_t* src = tile + (lane >> 1) * half + (lane & 1 ? codes + t0 * (D / 16) : t0 * (D / 2));
+                bulk_load(dst + (lane >> 1) * HALF + (lane & 1) * CODES, src, lane & 1 ? HALF - CODES : CODES, full + slot);
+            }
+        }
+    };
+#pragma unroll
+    for (int k = 0; k < STAGES; ++k)
+        if (k < mine) issue(k);
+    if (mine > 32) resolve(32, ph_next, pos_next);
 
     // the query rows in fp16, each scaled by 2^-e so that its largest channel lies in [1, 2)
     for (int r = warp; r < COLS; r += C::WARPS) {
@@ -134,7 +213,6 @@ __global__ void __launch_bounds__(Attn4Cfg<D, NT>::THREADS) attn4_kernel(const A
 
     uint32_t qf[NTW][2 * KW][2];
     float fac[NTW][2], m[NTW][2], l[NTW][2];
-    int lim[NTW][2];
     float oacc[NTW][MT][4];
 #pragma unroll
     for (int n = 0; n < NTW; ++n) {
@@ -147,68 +225,80 @@ __global__ void __launch_bounds__(Attn4Cfg<D, NT>::THREADS) attn4_kernel(const A
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const int r = col0 + 2 * c + j;
-            fac[n][j] = s_fac[r];
-            m[n][j] = NEG_INF;
+            fac[n][j] = s_fac[col0 + 2 * c + j];
+            m[n][j] = kLow4;
             l[n][j] = 0.f;
-            lim[n][j] = r < R ? len - a.T + r / G : len - 1;
         }
 #pragma unroll
         for (int i = 0; i < MT; ++i) oacc[n][i][0] = oacc[n][i][1] = oacc[n][i][2] = oacc[n][i][3] = 0.f;
     }
 
-    const int cpp = a.ps >> 4;  // chunks per page
-    const int codes = kv4_codes_bytes(a.ps, D), half = kv4_half_bytes(a.ps, D);
-    for (int ci = tw; ci < count * cpp; ci += TW) {
-        const int item = ci / cpp, t0 = (ci - item * cpp) * 16;
-        const int lp = SPARSE ? a.sel[(long long)row * a.k_max + start + item] : start + item;
-        if (lp < 0 || lp >= P) {
-            if (lane == 0) raise_status(a.status, SPD_DEV_BAD_SEL);
-            continue;
+    for (int k = 0; k < mine; ++k) {
+        const int slot = k % STAGES;
+        if (!mbar_wait_bounded(full + slot, (uint32_t)(k / STAGES) & 1u, a.status, a.wait_ns)) {
+            // the chunks in flight land before the shared memory is used for anything else
+            for (int j = k + 1; j < min(k + STAGES, mine); ++j)
+                mbar_wait_bounded(full + j % STAGES, (uint32_t)(j / STAGES) & 1u, a.status, a.wait_ns);
+            break;
         }
-        const long long phys = a.page_table[(long long)b * a.max_pages + lp];
-        if (phys < 0 || phys >= a.num_phys) {
-            if (lane == 0) raise_status(a.status, SPD_DEV_BAD_PAGE);
-            continue;
-        }
-        const int pos0 = lp * a.ps + t0;
-        if (pos0 >= len) continue;
-        const uint8_t* kt = a.kv4 + (phys * a.H_kv + h) * (2LL * half);
-        const uint8_t* vt = kt + half;
+        const int pos0 = meta[slot];
+        const uint8_t* kt = ring + slot * C::CHUNK;
+        const uint8_t* vt = kt + HALF;
         uint32_t kw[2][KW], vw[4][VW];
         uint32_t ks[2], vs[4];
+        if (pos0 >= 0) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int t = t0 + g + 8 * j;
-            const uint32_t* p = reinterpret_cast<const uint32_t*>(kt + t * (D / 2) + c * (D / 8));
+            for (int j = 0; j < 2; ++j) {
+                const int t = g + 8 * j;
+                if constexpr (D == 128) {
+                    const uint4 x = *reinterpret_cast<const uint4*>(kt + t * 64 + c * 16);
+                    kw[j][0] = x.x;
+                    kw[j][1] = x.y;
+                    kw[j][KW - 2] = x.z;
+                    kw[j][KW - 1] = x.w;
+                    ks[j] = *reinterpret_cast<const uint16_t*>(kt + CODES + t * 8 + 2 * c);
+                } else {
+                    const uint2 x = *reinterpret_cast<const uint2*>(kt + t * 32 + c * 8);
+                    kw[j][0] = x.x;
+                    kw[j][1] = x.y;
+                    ks[j] = kt[CODES + t * 4 + c];
+                }
+            }
 #pragma unroll
-            for (int w = 0; w < KW; ++w) kw[j][w] = p[w];
-            if (D == 128)
-                ks[j] = *reinterpret_cast<const uint16_t*>(kt + codes + t * 8 + 2 * c);
-            else
-                ks[j] = kt[codes + t * 4 + c];
+            for (int j = 0; j < 4; ++j) {
+                const int t = 2 * c + (j & 1) + 8 * (j >> 1);
+                if constexpr (D == 128) {
+                    const uint2 x = *reinterpret_cast<const uint2*>(vt + t * 64 + g * 8);
+                    vw[j][0] = x.x;
+                    vw[j][VW - 1] = x.y;
+                } else {
+                    vw[j][0] = *reinterpret_cast<const uint32_t*>(vt + t * 32 + g * 4);
+                }
+                vs[j] = vt[CODES + t * (D / 16) + (D == 128 ? g : g >> 1)];
+            }
         }
-        const int valid = len - pos0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int tc = 2 * c + (j & 1) + 8 * (j >> 1), t = t0 + tc;
-            const uint32_t* p = reinterpret_cast<const uint32_t*>(vt + t * (D / 2) + g * (D / 16));
-#pragma unroll
-            for (int w = 0; w < VW; ++w) vw[j][w] = p[w];
-            // slots past the sequence's end may hold anything: their scale counts as 0
-            vs[j] = tc < valid ? vt[codes + t * (D / 16) + (D == 128 ? g : g >> 1)] : 0u;
+        __syncwarp();  // the slot has been read: refill it
+        const int kn = k + STAGES;
+        if (kn < mine) {
+            if ((kn & 31) == 0) {
+                ph_cur = ph_next;
+                pos_cur = pos_next;
+                resolve(kn + 32, ph_next, pos_next);
+            }
+            issue(kn);
         }
+        if (pos0 < 0) continue;
 
         float sc[NTW][4];
 #pragma unroll
         for (int n = 0; n < NTW; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
+        const uint32_t ks0 = e4m3x2_to_f16(ks[0]), ks1 = e4m3x2_to_f16(ks[1]);
 #pragma unroll
         for (int w = 0; w < KW; ++w) {
             uint32_t h0[4], h1[4];
             e2m1x8_to_f16(kw[0][w], h0);
             e2m1x8_to_f16(kw[1][w], h1);
-            const uint32_t b0 = (ks[0] >> (8 * (w / 2))) & 0xffu, b1 = (ks[1] >> (8 * (w / 2))) & 0xffu;
-            const uint32_t s0 = e4m3x2_to_f16(b0 * 0x101u), s1 = e4m3x2_to_f16(b1 * 0x101u);
+            const uint32_t s0 = __byte_perm(ks0, 0, w < 2 ? 0x1010 : 0x3232), s1 = __byte_perm(ks1, 0, w < 2 ? 0x1010 : 0x3232);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 h0[i] = hmul2(h0[i], s0);
@@ -221,17 +311,33 @@ __global__ void __launch_bounds__(Attn4Cfg<D, NT>::THREADS) attn4_kernel(const A
                 mma_f16(sc[n], a1, qf[n][2 * w + 1][0], qf[n][2 * w + 1][1]);
             }
         }
-        // logits in base 2, masked; the reference maximum; weights
+        // logits in base 2, relative to the reference and raised by kBias4; hidden tokens at -inf
+        if (pos0 + 15 > len - a.T) {
+            // slots past the sequence's end may hold anything: their scale counts as 0
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (pos0 + 2 * c + (j & 1) + 8 * (j >> 1) >= len) vs[j] = 0u;
+#pragma unroll
+            for (int n = 0; n < NTW; ++n) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int r = (ng * NTW + n) * 8 + 2 * c + (j & 1);
+                    const int lim = r < R ? len - a.T + r / G : len - 1;  // the last token that the row sees
+                    const float z = sc[n][j] * fac[n][j & 1];
+                    sc[n][j] = pos0 + g + 8 * (j >> 1) <= lim ? z : NEG_INF;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int n = 0; n < NTW; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) sc[n][j] *= fac[n][j & 1];
+        }
         bool move = false;
 #pragma unroll
-        for (int n = 0; n < NTW; ++n) {
+        for (int n = 0; n < NTW; ++n)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float z = sc[n][j] * fac[n][j & 1];
-                sc[n][j] = pos0 + g + 8 * (j >> 1) <= lim[n][j & 1] ? z : NEG_INF;
-                move |= sc[n][j] > m[n][j & 1] + kHead4;
-            }
-        }
+            for (int j = 0; j < 2; ++j) move |= fmaxf(sc[n][j], sc[n][j + 2]) > m[n][j] + kHead4;
         if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
             for (int n = 0; n < NTW; ++n) {
@@ -241,7 +347,7 @@ __global__ void __launch_bounds__(Attn4Cfg<D, NT>::THREADS) attn4_kernel(const A
 #pragma unroll
                     for (int off = 4; off < 32; off <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
                     x = fmaxf(x, m[n][j]);
-                    const float corr = x == NEG_INF ? 1.f : fast_exp2(m[n][j] - x);
+                    const float corr = fast_exp2(m[n][j] - x);
                     m[n][j] = x;
                     l[n][j] *= corr;
 #pragma unroll
@@ -258,8 +364,7 @@ __global__ void __launch_bounds__(Attn4Cfg<D, NT>::THREADS) attn4_kernel(const A
             float p[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float ref = m[n][j & 1] == NEG_INF ? 0.f : m[n][j & 1] - kBias4;
-                p[j] = fast_exp2(sc[n][j] - ref);
+                p[j] = fast_exp2(sc[n][j] - (m[n][j & 1] - kBias4));
                 l[n][j & 1] += p[j];
             }
             pf[n][0] = movmatrix_t(pack_f16(p[0], p[1]));
@@ -268,7 +373,7 @@ __global__ void __launch_bounds__(Attn4Cfg<D, NT>::THREADS) attn4_kernel(const A
         const uint32_t s01 = e4m3x2_to_f16(vs[0] | vs[1] << 8), s23 = e4m3x2_to_f16(vs[2] | vs[3] << 8);
 #pragma unroll
         for (int w = 0; w < VW; ++w) {
-            // byte i of the words below: channel 2i (first two words) or 2i + 1 of a token
+            // byte i of the words below: channel 2i (first and third word) or 2i + 1 of a token
             // pair, the earlier token in the low bits
             uint32_t x[4][4];
             e2m1x8_to_f16((vw[0][w] & 0x0f0f0f0fu) | ((vw[1][w] << 4) & 0xf0f0f0f0u), x[0]);
@@ -296,16 +401,16 @@ __global__ void __launch_bounds__(Attn4Cfg<D, NT>::THREADS) attn4_kernel(const A
             if (g == 0) s_m[tw * COLS + col] = m[n][j];
         }
     }
-    __syncthreads();
+    __syncthreads();  // and every warp is done with its ring
 #pragma unroll
     for (int n = 0; n < NTW; ++n) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int col = (ng * NTW + n) * 8 + 2 * c + j;
-            float top = NEG_INF;
+            float top = kLow4;
 #pragma unroll
             for (int i = 0; i < TW; ++i) top = fmaxf(top, s_m[i * COLS + col]);
-            const float f = m[n][j] == NEG_INF ? 0.f : fast_exp2(m[n][j] - top);
+            const float f = fast_exp2(m[n][j] - top);
             if (g == 0) s_l[tw * COLS + col] = l[n][j] * f;
             float* out = s_o + (tw * COLS + col) * D + g * (D / 8);
 #pragma unroll
@@ -384,26 +489,26 @@ namespace {
 
 typedef void (*Attn4Fn)(const Attn4Args);
 
-template <int D, int NT>
-void pick(bool sparse, Attn4Fn* fn, int* smem, int* threads) {
-    *fn = sparse ? attn4_kernel<D, NT, true> : attn4_kernel<D, NT, false>;
+template <int D, int NT, bool SPARSE>
+void pick(Attn4Fn* fn, int* smem, int* threads) {
+    *fn = attn4_kernel<D, NT, SPARSE>;
     *smem = Attn4Cfg<D, NT>::SMEM;
     *threads = Attn4Cfg<D, NT>::THREADS;
 }
 
+template <int D>
+void pick_R(int R, bool sparse, Attn4Fn* fn, int* smem, int* threads) {
+    if (sparse) pick<D, 1, true>(fn, smem, threads);  // one position: R = G <= 8
+    else if (R <= 8) pick<D, 1, false>(fn, smem, threads);
+    else if (R <= 16) pick<D, 2, false>(fn, smem, threads);
+    else if (R <= 32) pick<D, 4, false>(fn, smem, threads);
+    else pick<D, 8, false>(fn, smem, threads);
+}
+
 // The kernel for R query rows of a KV head, its dynamic shared memory and block.
 void attn4_variant(int D, int R, bool sparse, Attn4Fn* fn, int* smem, int* threads) {
-    if (D == 128) {
-        if (R <= 8) pick<128, 1>(sparse, fn, smem, threads);
-        else if (R <= 16) pick<128, 2>(sparse, fn, smem, threads);
-        else if (R <= 32) pick<128, 4>(sparse, fn, smem, threads);
-        else pick<128, 8>(sparse, fn, smem, threads);
-    } else {
-        if (R <= 8) pick<64, 1>(sparse, fn, smem, threads);
-        else if (R <= 16) pick<64, 2>(sparse, fn, smem, threads);
-        else if (R <= 32) pick<64, 4>(sparse, fn, smem, threads);
-        else pick<64, 8>(sparse, fn, smem, threads);
-    }
+    if (D == 128) pick_R<128>(R, sparse, fn, smem, threads);
+    else pick_R<64>(R, sparse, fn, smem, threads);
 }
 
 }  // namespace

@@ -129,6 +129,7 @@ struct Attn4Args {
     float* part_lse;  // [B*H_kv][num_splits][R]
     int* counters;    // [B*H_kv] split tickets, zero on entry and on exit
     unsigned* status;
+    unsigned long long wait_ns;  // limit of every bounded wait
 };
 cudaError_t launch_attn4(const Attn4Args& a, bool sparse, cudaStream_t st);
 // CTAs of the kernel that fit on one SM for this shape.

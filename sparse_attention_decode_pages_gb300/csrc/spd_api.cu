@@ -3,6 +3,7 @@
 // and dispatch to the kernels.  Nothing here allocates device memory or
 // synchronises (except spd_device_status).
 #include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -956,11 +957,44 @@ SPD_API spd_status kv4_read(const spd_dims* dims, int32_t T, const uint8_t* kv4,
     return e == cudaSuccess ? SPD_OK : cuda_fail(e, "kv4_read launch");
 }
 
-// Splits of a row of the 4-bit attention, as sparse_splits / dense_splits choose them.
+// Splits of a row of the 4-bit attention.  Its CTAs take one unit each, `slots` at a
+// time, and a unit costs about kv4_unit_fixed chunks of a warp besides its own (the
+// lengths, the queries, the first copies, the join).  Up to half a GPU of rows is cut
+// into one round of units.  More rows, selections (about equal): the count that takes
+// the least rounds * (chunks + fixed).  More rows, whole sequences (their lengths
+// differ, and only the GPU knows them): units + the longest one's tail,
+// rows * S * (c / S + fixed) / slots + c / S, is least at S = sqrt(c * slots / (rows * fixed)).
+constexpr int kv4_unit_fixed = 12;
+
 static int kv4_splits(const spd_dims* d, int T, int items, bool sparse, int req, int sms) {
     const long long rows = (long long)d->B * d->H_kv;
-    const long long workers = (long long)sms * occ_attn4(d->D, d->page_size, T * (d->H_q / d->H_kv), sparse);
-    return splits_for(rows, items, workers, pages_per_split_floor(d->page_size), sparse ? 1 : 4, req);
+    const int warps = 4;  // chunks in work at once
+    const long long slots = (long long)sms * occ_attn4(d->D, d->page_size, T * (d->H_q / d->H_kv), sparse);
+    int S = req;
+    if (S <= 0) {
+        S = 1;
+        const int most = (items + pages_per_split_floor(d->page_size) - 1) / pages_per_split_floor(d->page_size);
+        const double c = (double)items * (d->page_size / 16) / warps;  // chunks of a warp, row unsplit
+        if (rows > 0 && 2 * rows <= slots) {
+            S = (int)(slots / rows);
+        } else if (rows > 0 && !sparse) {
+            S = (int)(sqrt(c * slots / ((double)rows * kv4_unit_fixed)) + 0.5);
+        } else if (rows > 0) {
+            double best = 1e300;
+            for (int s = 1; s <= 16 && s <= most; ++s) {
+                const double cost = (double)((rows * s + slots - 1) / slots) * (c / s + kv4_unit_fixed);
+                if (cost < best) {
+                    best = cost;
+                    S = s;
+                }
+            }
+        }
+        if (S > most) S = most;
+    }
+    if (S > items) S = items;
+    if (S < 1) S = 1;
+    const int ips = (items + S - 1) / S;
+    return (items + ips - 1) / ips;
 }
 
 static size_t kv4_attn_ws(const spd_dims* dims, int T, int items, bool sparse, int32_t num_splits) {
@@ -1040,6 +1074,7 @@ static spd_status kv4_attn(const spd_dims* dims, int32_t T, const spd_bf16* q, c
     a.part_lse = w.part_lse;
     a.counters = w.counters;
     a.status = d->status;
+    a.wait_ns = wait_limit_ns();
     cudaError_t e = launch_attn4(a, sparse, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? SPD_OK : cuda_fail(e, sparse ? "kv4_sparse_decode_attn launch" : "kv4_dense_verify_attn launch");
 }
