@@ -2,26 +2,31 @@
 // pages and dense causal verification over the whole cache.
 //
 // A unit is a run of at most pages_per_split pages of one (sequence, KV head) row;
-// it holds all R = T * G query rows of the KV head in n-tiles of eight.  A CTA
-// takes one unit; its warps take the unit's 16-token chunks in turn, each on its own:
-// lane i resolves the warp's i-th next chunk (selection entry, page-table entry), and
-// the warp keeps a ring of chunks filled by bulk copies, refilling a slot as soon as it
-// has read it, so no warp waits for another before the unit's end.
+// it holds all R = T * G query rows of the KV head in n-tiles of eight.  A CTA of four
+// warps takes one unit, 64 tokens (a step) at a time from a ring that bulk copies fill.
+// On the tensor cores (mma.sync m16n8k16, fp16 in, fp32 out):
 //
-// Per chunk, on the tensor cores (mma.sync m16n8k16, fp16 in, fp32 out):
+//   S^T = K Q^T        warp w: the step's 16-token chunk w, every query row
+//   O^T += V^T P^T     warp w: channels (w & 1) * D / 2 ... of chunks 2 (w >> 1), + 1
 //
-//   S^T = K Q^T   (rows: 16 tokens, columns: 8 query rows)
-//   O^T += V^T P^T
+// so tokens and channels fill the MMA rows and the few query rows its columns, every
+// key and value is converted to fp16 once in the CTA, and a warp holds half of O (64
+// registers at 32 query rows; the two halves of the tokens are joined at the end); P
+// goes between the warps through shared memory as ready B fragments.  Two barriers a
+// step: one carries the vote on the references, one publishes P.
+// Warp k % 4 issues step k's copies, a lane for each piece, from what its lanes have
+// resolved (selection entry, page-table entry) for its next eight steps.
 //
-// so the tokens fill the MMA rows and the few query rows its columns.  code * scale
-// is exact in fp16, so the products are those of the values the cache stands for.
-// The contraction's channel order is free: lane (g, c) = (lane / 4, lane % 4) holds
-// the D / 4 channels from c * D / 4 on of tokens g and g + 8, contiguous in memory,
-// and V's channels g * D / 8 ... of tokens 2c, 2c+1, 2c+8, 2c+9.  Queries are
-// scaled by a power of two into fp16's range (the factor goes into the logits'
-// scale).  Online softmax in fp32 in base 2; a column's reference moves only when a
-// logit exceeds it by kHead4, and weights carry a factor 2^kBias4 so that what
-// fp16 drops of a weight lies 2^-32 below the reference.
+// code * scale is exact in fp16, so the products are those of the values the cache
+// stands for.  The contraction's channel order is free: lane (g, c) = (lane / 4,
+// lane % 4) holds the D / 4 channels from c * D / 4 on of tokens g and g + 8,
+// contiguous in memory; of V it holds D / 16 neighbouring channels of tokens 2c, 2c+1,
+// 2c+8, 2c+9 -- in a chunk's tokens taken in the order 0 1 3 2 4 5 7 6, 8 ..., with which
+// neither the 64-byte key rows nor the 32-byte slices of the value rows that are read
+// together share banks more than twice.  Queries are scaled by a power of two into fp16's range (the factor goes
+// into the logits' scale).  Online softmax in fp32 in base 2; a column's reference
+// moves only when a logit exceeds it by kHead4, and weights carry a factor 2^kBias4 so
+// that what fp16 drops of a weight lies 2^-32 below the reference.
 #include "kv4.cuh"
 #include "kernels.h"
 
@@ -30,12 +35,19 @@ namespace spd {
 constexpr float kHead4 = 8.f;  // log2 headroom before the running maximum moves
 constexpr float kBias4 = 7.f;  // 2^(kHead4 + kBias4) = 32768 stays within fp16
 
+// Without `volatile`: the compiler may order these among the conversions.
 __device__ __forceinline__ void mma_f16(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
@@ -43,52 +55,52 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// The token of MMA row r (0-7; r + 8 likewise) of a chunk.
+__device__ __forceinline__ int chunk_token(int r) { return r ^ ((r >> 1) & 1); }
+
 constexpr float kLow4 = -3.0e38f;  // a column's reference before its first visible token
 
 template <int D, int NT>
 struct Attn4Cfg {
-    static constexpr int NTW = NT < 4 ? NT : 4;     // n-tiles of a warp
-    static constexpr int NG = NT / NTW;             // warps that share a chunk's tokens
-    static constexpr int TW = 4 / NG;               // chunks in work at once
-    static constexpr int WARPS = NG * TW;
-    static constexpr int THREADS = 32 * WARPS;
+    static constexpr int WARPS = 4, THREADS = 128;
     static constexpr int COLS = NT * 8;
-    static constexpr int STAGES = 4;                // ring slots of a warp
-    static constexpr int CHUNK = kv4_tile_bytes(16, D);  // bytes of 16 tokens' keys and values
-    static constexpr int RING = WARPS * STAGES * CHUNK;
-    static constexpr int MERGE = TW * COLS * D * 4;  // float [TW][COLS][D], over the ring when it is done
-    static constexpr int OFF_Q = RING > MERGE ? RING : MERGE;      // half [COLS][D]
-    static constexpr int OFF_FAC = OFF_Q + COLS * D * 2;           // float [COLS]: logit scale of each query row
-    static constexpr int OFF_M = OFF_FAC + COLS * 4;               // float [TW][COLS]
-    static constexpr int OFF_L = OFF_M + TW * COLS * 4;            // float [TW][COLS]
-    static constexpr int OFF_BAR = OFF_L + TW * COLS * 4;          // uint64 [WARPS][STAGES]
-    static constexpr int OFF_META = OFF_BAR + WARPS * STAGES * 8;  // int [WARPS][STAGES]: first position or -1
-    static constexpr int SMEM = OFF_META + WARPS * STAGES * 4;
-    // CTAs that the registers leave room for on an SM
-    static constexpr int OCC = NT <= 1 ? 5 : (NT == 2 ? 3 : 2);
+    static constexpr int STAGES = 4;                      // steps in the ring
+    static constexpr int CHUNK = kv4_tile_bytes(16, D);   // bytes of 16 tokens' keys and values
+    static constexpr int STEP = WARPS * CHUNK;
+    static constexpr bool QREG = NT == 1;                 // Q's fragments stay in registers (else in shared memory)
+    // half [NT][D / 32][32 lanes][8]: B fragments of Q^T, 16 bytes for each lane and code word
+    static constexpr int OFF_Q = STAGES * STEP;
+    static constexpr int OFF_P = OFF_Q + COLS * D * 2;    // uint2 [WARPS][NT][32 lanes]: B fragments of P^T
+    static constexpr int OFF_FAC = OFF_P + WARPS * NT * 256;  // float [COLS]: logit scale of each query row
+    static constexpr int OFF_RED = OFF_FAC + COLS * 4;        // float [WARPS][COLS]: maxima, then sums
+    static constexpr int OFF_BAR = OFF_RED + WARPS * COLS * 4;  // uint64 [STAGES]
+    static constexpr int OFF_META = OFF_BAR + STAGES * 8;       // int4 [STAGES]: the chunks' first positions or -1
+    static constexpr int SMEM = OFF_META + STAGES * 16;
+    static constexpr int OCC = NT <= 2 ? 4 : (NT == 4 ? 3 : 2);  // CTAs on an SM
+    static_assert(COLS * D * 4 <= STAGES * STEP, "half of O is handed over in the ring");
+    static_assert(STAGES - 1 <= WARPS, "a warp issues one of the first steps");
+    static_assert(STAGES % 2 == 0, "meta is 16-byte aligned");
 };
 
 template <int D, int NT, bool SPARSE>
-__global__ void __launch_bounds__(Attn4Cfg<D, NT>::THREADS, Attn4Cfg<D, NT>::OCC) attn4_kernel(const Attn4Args a) {
+__global__ void __launch_bounds__(128, Attn4Cfg<D, NT>::OCC) attn4_kernel(const Attn4Args a) {
     using C = Attn4Cfg<D, NT>;
-    constexpr int NTW = C::NTW, TW = C::TW, COLS = C::COLS, STAGES = C::STAGES;
-    constexpr int KW = D / 32;  // 32-bit code words of a lane's share of a key row
-    constexpr int VW = D / 64;  // and of a value row
-    constexpr int MT = D / 16;  // 16-channel m-tiles of O^T
+    constexpr int COLS = C::COLS, STAGES = C::STAGES, WARPS = C::WARPS;
+    constexpr int KW = D / 32;   // 32-bit code words of a lane's share of a key row
+    constexpr int MT = D / 32;   // 16-channel m-tiles of a warp's half of O^T
     constexpr int CODES = kv4_codes_bytes(16, D), HALF = kv4_half_bytes(16, D);  // of a chunk
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int s_last;
+    __shared__ int s_last, s_late;
     float* s_fac = reinterpret_cast<float*>(smem + C::OFF_FAC);
-    float* s_m = reinterpret_cast<float*>(smem + C::OFF_M);
-    float* s_l = reinterpret_cast<float*>(smem + C::OFF_L);
+    float* s_red = reinterpret_cast<float*>(smem + C::OFF_RED);
     __half* s_q = reinterpret_cast<__half*>(smem + C::OFF_Q);
-    float* s_o = reinterpret_cast<float*>(smem);
+    uint2* s_p = reinterpret_cast<uint2*>(smem + C::OFF_P);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+    int4* meta = reinterpret_cast<int4*>(smem + C::OFF_META);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, c = lane & 3;
-    const int tw = warp % TW, ng = warp / TW;
-    uint8_t* ring = smem + warp * STAGES * C::CHUNK;
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR) + warp * STAGES;
-    int* meta = reinterpret_cast<int*>(smem + C::OFF_META) + warp * STAGES;
+    const int chalf = warp & 1, tpair = warp >> 1;  // this warp's half of the channels and pair of chunks of O
+    const int gt = chunk_token(g);  // the token of the lane's first key row; the second is 8 behind
     const int G = a.H_q / a.H_kv, R = a.T * G;
     const float NEG_INF = __int_as_float(0xff800000);
 
@@ -98,21 +110,22 @@ __global__ void __launch_bounds__(Attn4Cfg<D, NT>::THREADS, Attn4Cfg<D, NT>::OCC
         const int t = r / G;
         return ((long long)b * a.T + t) * a.H_q + h * G + (r - t * G);
     };
-    if (lane == 0) {
+    if (tid == 0) {
 #pragma unroll
         for (int i = 0; i < STAGES; ++i) mbar_init(full + i, 1);
         mbar_fence_init();
+        s_late = 0;
     }
-    __syncwarp();
     pdl_wait();
     pdl_trigger();
 
     const int start = split * a.pages_per_split;
     const int cpp = a.ps >> 4;  // chunks per page
-    // chunk k of this warp is chunk tw + k * TW of the unit; the first selection entries
-    // are read together with the length and the count
-    int sel0 = 0;
-    if (SPARSE && start + (tw + lane * TW) / cpp < a.k_max) sel0 = a.sel[(long long)row * a.k_max + start + (tw + lane * TW) / cpp];
+    // this warp issues steps 4 m + warp; lane i resolves chunk i % 4 of its step m = base + i / 4.
+    // The first selection entries are read together with the lengths.
+    auto chunk_of = [&](int m) { return 16 * (m + (lane >> 2)) + 4 * warp + (lane & 3); };
+    int lp_next = -1, ph_next = -1;  // the next eight steps' logical pages and page-table entries, unchecked
+    if (SPARSE && chunk_of(0) / cpp < a.k_max - start) lp_next = a.sel[(long long)row * a.k_max + start + chunk_of(0) / cpp];
     const int len = a.seq_lens[b];
     int P = seq_pages(len, a.ps, a.max_pages);
     if (P < 0) {
@@ -139,65 +152,77 @@ __global__ void __launch_bounds__(Attn4Cfg<D, NT>::THREADS, Attn4Cfg<D, NT>::OCC
     }
     const int nsplit = (n_items + a.pages_per_split - 1) / a.pages_per_split;
     const int chunks = count * cpp;
-    const int mine = chunks > tw ? (chunks - tw + TW - 1) / TW : 0;  // of this warp
+    const int steps = (chunks + WARPS - 1) / WARPS;
 
-    // this lane's chunk base + lane: its physical page and first position (-1: nothing to read)
-    auto resolve = [&](int base, int& phys, int& pos) {
-        phys = pos = -1;
-        const int k = base + lane;
-        if (k < mine) {
-            const int ci = tw + k * TW, item = ci / cpp;
-            const int lp = !SPARSE ? start + item : base == 0 ? sel0 : a.sel[(long long)row * a.k_max + start + item];
-            if (lp < 0 || lp >= P) {
+    auto next_pages = [&](int m) {
+        const int ci = chunk_of(m);
+        lp_next = -1;
+        if (ci < chunks) lp_next = SPARSE ? a.sel[(long long)row * a.k_max + start + ci / cpp] : start + ci / cpp;
+    };
+    auto next_entries = [&]() {
+        ph_next = lp_next >= 0 && lp_next < P ? a.page_table[(long long)b * a.max_pages + lp_next] : -1;
+    };
+    int ph_cur = -1, pos_cur = -1;  // physical page and first position (-1: nothing to read)
+    auto take_next = [&](int m) {
+        const int ci = chunk_of(m);
+        ph_cur = pos_cur = -1;
+        if (ci < chunks) {
+            if (lp_next < 0 || lp_next >= P) {
                 raise_status(a.status, SPD_DEV_BAD_SEL);
+            } else if (ph_next < 0 || ph_next >= a.num_phys) {
+                raise_status(a.status, SPD_DEV_BAD_PAGE);
             } else {
-                const int at = lp * a.ps + (ci - item * cpp) * 16;
-                const int ph = a.page_table[(long long)b * a.max_pages + lp];
-                if (ph < 0 || ph >= a.num_phys) raise_status(a.status, SPD_DEV_BAD_PAGE);
-                else if (at < len) {
-                    phys = ph;
-                    pos = at;
+                const int at = lp_next * a.ps + (ci - ci / cpp * cpp) * 16;
+                if (at < len) {
+                    ph_cur = ph_next;
+                    pos_cur = at;
                 }
             }
         }
     };
-    int ph_cur, pos_cur, ph_next = -1, pos_next = -1;
-    resolve(0, ph_cur, pos_cur);
-    // issues chunk k into its slot (by the whole warp; the copies by lanes 0-3)
+    // issues step k (k % 4 == warp): lane 4 q + i copies piece i of chunk q (keys' codes and
+    // scales, values' codes and scales), or lane 4 q the whole chunk where a page is one
     const int codes = kv4_codes_bytes(a.ps, D), half = kv4_half_bytes(a.ps, D);
     auto issue = [&](int k) {
-        const int slot = k % STAGES;
-        const int phys = __shfl_sync(0xffffffffu, ph_cur, k & 31), pos = __shfl_sync(0xffffffffu, pos_cur, k & 31);
-        if (lane == 0) {
-            meta[slot] = pos;
-            mbar_arrive_expect_tx(full + slot, pos >= 0 ? C::CHUNK : 0);
-        }
+        const int slot = k % STAGES, from = (k >> 2 & 7) * 4;
+        const int phys = __shfl_sync(0xffffffffu, ph_cur, from + (lane >> 2 & 3));
+        const int pos = __shfl_sync(0xffffffffu, pos_cur, from + (lane >> 2 & 3));
+        const unsigned there = __ballot_sync(0xffffffffu, pos >= 0 && (lane & 3) == 0 && lane < 16);
+        if (lane < 16 && (lane & 3) == 0) reinterpret_cast<int*>(meta + slot)[lane >> 2] = pos;
         __syncwarp();
-        if (pos >= 0) {
+        if (lane == 0) mbar_arrive_expect_tx(full + slot, __popc(there) * C::CHUNK);
+        __syncwarp();
+        if (lane < 16 && pos >= 0) {
+            const int i = lane & 3;
             const uint8_t* tile = a.kv4 + ((long long)phys * a.H_kv + h) * (2LL * half);
-            uint8_t* dst = ring + slot * C::CHUNK;
+            uint8_t* dst = smem + slot * C::STEP + (lane >> 2) * C::CHUNK;
             if (a.ps == 16) {
-                if (lane == 0) bulk_load(dst, tile, C::CHUNK, full + slot);
-            } else if (lane < 4) {  // keys' codes and scales, values' codes and scales
+                if (i == 0) bulk_load(dst, tile, C::CHUNK, full + slot);
+            } else {
                 const int t0 = pos & (a.ps - 1);
-                const uint8_t* src = tile + (lane >> 1) * half + (lane & 1 ? codes + t0 * (D / 16) : t0 * (D / 2));
-                bulk_load(dst + (lane >> 1) * HALF + (lane & 1) * CODES, src, lane & 1 ? HALF - CODES : CODES, full + slot);
+                const uint8_t* src = tile + (i >> 1) * half + (i & 1 ? codes + t0 * (D / 16) : t0 * (D / 2));
+                bulk_load(dst + (i >> 1) * HALF + (i & 1) * CODES, src, i & 1 ? HALF - CODES : CODES, full + slot);
             }
         }
     };
-#pragma unroll
-    for (int k = 0; k < STAGES; ++k)
-        if (k < mine) issue(k);
-    if (mine > 32) resolve(32, ph_next, pos_next);
+    if (!SPARSE) next_pages(0);
+    next_entries();
+    take_next(0);
+    __syncthreads();  // the barriers are initialised
+    if (warp < STAGES - 1 && warp < steps) issue(warp);
+    if (steps > 32) next_pages(8);
 
-    // the query rows in fp16, each scaled by 2^-e so that its largest channel lies in [1, 2)
-    for (int r = warp; r < COLS; r += C::WARPS) {
-        float x[D / 32];
+    // the query rows in fp16, each scaled by 2^-e so that its largest channel lies in [1, 2),
+    // stored as the lanes read them: two channels of a row for each lane and turn here
+    for (int r = warp; r < COLS; r += WARPS) {
+        float2 x[D / 64];
         float amax = 0.f;
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-            x[i] = r < R ? __bfloat162float(reinterpret_cast<const bf16*>(a.q)[out_index(r) * D + lane + 32 * i]) : 0.f;
-            amax = fmaxf(amax, fabsf(x[i]));
+        for (int i = 0; i < D / 64; ++i) {
+            x[i] = make_float2(0.f, 0.f);
+            if (r < R)
+                x[i] = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(a.q + out_index(r) * D + 2 * lane + 64 * i));
+            amax = fmaxf(amax, fmaxf(fabsf(x[i].x), fabsf(x[i].y)));
         }
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
@@ -206,149 +231,150 @@ __global__ void __launch_bounds__(Attn4Cfg<D, NT>::THREADS, Attn4Cfg<D, NT>::OCC
         if (amax == 0.f) e = 0;
         const float down = pow2f(-e);
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) s_q[r * D + lane + 32 * i] = __float2half_rn(x[i] * down);
+        for (int i = 0; i < D / 64; ++i) {
+            const int ch = 2 * lane + 64 * i, qc = ch / (D / 4), w = ch % (D / 4) / 8;
+            *reinterpret_cast<uint32_t*>(s_q + (((r >> 3) * KW + w) * 32 + (r & 7) * 4 + qc) * 8 + ch % 8) =
+                pack_f16(x[i].x * down, x[i].y * down);
+        }
         if (lane == 0) s_fac[r] = a.scale_log2 * pow2f(e);
     }
     __syncthreads();
 
-    uint32_t qf[NTW][2 * KW][2];
-    float fac[NTW][2], m[NTW][2], l[NTW][2];
-    float oacc[NTW][MT][4];
+    auto q_frag = [&](int n, int w) { return *reinterpret_cast<const uint4*>(s_q + ((n * KW + w) * 32 + lane) * 8); };
+    uint4 qf[C::QREG ? KW : 1];
+    if constexpr (C::QREG) {
 #pragma unroll
-    for (int n = 0; n < NTW; ++n) {
-        const int col0 = (ng * NTW + n) * 8;
+        for (int w = 0; w < KW; ++w) qf[w] = q_frag(0, w);
+    }
+    float fac[NT][2], ref[NT][2], l[NT][2];  // ref: the reference less kBias4
+    float oacc[NT][MT][4];
 #pragma unroll
-        for (int k = 0; k < 2 * KW; ++k) {
-            const uint2 q = *reinterpret_cast<const uint2*>(s_q + (col0 + g) * D + c * (D / 4) + 4 * k);
-            qf[n][k][0] = q.x;
-            qf[n][k][1] = q.y;
-        }
+    for (int n = 0; n < NT; ++n) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            fac[n][j] = s_fac[col0 + 2 * c + j];
-            m[n][j] = kLow4;
+            fac[n][j] = s_fac[n * 8 + 2 * c + j];
+            ref[n][j] = kLow4;
             l[n][j] = 0.f;
         }
 #pragma unroll
         for (int i = 0; i < MT; ++i) oacc[n][i][0] = oacc[n][i][1] = oacc[n][i][2] = oacc[n][i][3] = 0.f;
     }
 
-    for (int k = 0; k < mine; ++k) {
+    for (int k = 0; k < steps; ++k) {
         const int slot = k % STAGES;
-        if (!mbar_wait_bounded(full + slot, (uint32_t)(k / STAGES) & 1u, a.status, a.wait_ns)) {
-            // the chunks in flight land before the shared memory is used for anything else
-            for (int j = k + 1; j < min(k + STAGES, mine); ++j)
-                mbar_wait_bounded(full + j % STAGES, (uint32_t)(j / STAGES) & 1u, a.status, a.wait_ns);
-            break;
-        }
-        const int pos0 = meta[slot];
-        const uint8_t* kt = ring + slot * C::CHUNK;
-        const uint8_t* vt = kt + HALF;
-        uint32_t kw[2][KW], vw[4][VW];
-        uint32_t ks[2], vs[4];
+        const uint8_t* stage = smem + slot * C::STEP;
+        const bool landed = mbar_wait_bounded(full + slot, (uint32_t)(k / STAGES) & 1u, a.status, a.wait_ns);
+        const int4 firsts = meta[slot];
+        const int pos0 = warp == 0 ? firsts.x : warp == 1 ? firsts.y : warp == 2 ? firsts.z : firsts.w;
+        float sc[NT][4], y[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
+        float top = NEG_INF;
         if (pos0 >= 0) {
+            const uint8_t* kt = stage + warp * C::CHUNK;
+            uint32_t kw[2][KW], ks[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const int t = g + 8 * j;
+                const int t = gt + 8 * j;
                 if constexpr (D == 128) {
                     const uint4 x = *reinterpret_cast<const uint4*>(kt + t * 64 + c * 16);
                     kw[j][0] = x.x;
                     kw[j][1] = x.y;
                     kw[j][KW - 2] = x.z;
                     kw[j][KW - 1] = x.w;
-                    ks[j] = *reinterpret_cast<const uint16_t*>(kt + CODES + t * 8 + 2 * c);
+                    ks[j] = e4m3x2_to_f16(*reinterpret_cast<const uint16_t*>(kt + CODES + t * 8 + 2 * c));
                 } else {
                     const uint2 x = *reinterpret_cast<const uint2*>(kt + t * 32 + c * 8);
                     kw[j][0] = x.x;
                     kw[j][1] = x.y;
-                    ks[j] = kt[CODES + t * 4 + c];
+                    ks[j] = e4m3x2_to_f16(kt[CODES + t * 4 + c]);
                 }
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int t = 2 * c + (j & 1) + 8 * (j >> 1);
-                if constexpr (D == 128) {
-                    const uint2 x = *reinterpret_cast<const uint2*>(vt + t * 64 + g * 8);
-                    vw[j][0] = x.x;
-                    vw[j][VW - 1] = x.y;
-                } else {
-                    vw[j][0] = *reinterpret_cast<const uint32_t*>(vt + t * 32 + g * 4);
+            for (int w = 0; w < KW; ++w) {
+                uint32_t h0[4], h1[4];
+                e2m1x8_to_f16(kw[0][w], h0);
+                e2m1x8_to_f16(kw[1][w], h1);
+                const uint32_t s0 = __byte_perm(ks[0], 0, w < 2 ? 0x1010 : 0x3232), s1 = __byte_perm(ks[1], 0, w < 2 ? 0x1010 : 0x3232);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    h0[i] = hmul2(h0[i], s0);
+                    h1[i] = hmul2(h1[i], s1);
                 }
-                vs[j] = vt[CODES + t * (D / 16) + (D == 128 ? g : g >> 1)];
+                const uint32_t a0[4] = {h0[0], h1[0], h0[1], h1[1]}, a1[4] = {h0[2], h1[2], h0[3], h1[3]};
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const uint4 q = C::QREG ? qf[C::QREG ? w : 0] : q_frag(n, w);
+                    mma_f16(sc[n], a0, q.x, q.y);
+                    mma_f16(sc[n], a1, q.z, q.w);
+                }
             }
+            // y: logits in base 2 less ref, hidden tokens at -inf
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) y[n][j] = fmaf(sc[n][j], fac[n][j & 1], -ref[n][j & 1]);
+            if (pos0 + 15 > len - a.T) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int r = n * 8 + 2 * c + (j & 1);
+                        const int lim = r < R ? len - a.T + r / G : len - 1;  // the last token that the row sees
+                        if (pos0 + gt + 8 * (j >> 1) > lim) y[n][j] = NEG_INF;
+                    }
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) top = fmaxf(fmaxf(fmaxf(y[n][0], y[n][1]), fmaxf(y[n][2], y[n][3])), top);
+        } else {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) y[n][0] = y[n][1] = y[n][2] = y[n][3] = NEG_INF;
         }
-        __syncwarp();  // the slot has been read: refill it
-        const int kn = k + STAGES;
-        if (kn < mine) {
-            if ((kn & 31) == 0) {
-                ph_cur = ph_next;
-                pos_cur = pos_next;
-                resolve(kn + 32, ph_next, pos_next);
+        if (!landed) s_late = 1;
+        // every warp is done with step k - 1 behind this; the vote: some reference has to move
+        const bool move = __syncthreads_or(top > kHead4 + kBias4);
+        if (s_late) {  // the copies in flight land before the CTA ends; the row is given up
+            for (int j = k; j < min(k + STAGES - 1, steps); ++j)
+                mbar_wait_bounded(full + j % STAGES, (uint32_t)(j / STAGES) & 1u, a.status, a.wait_ns);
+            break;
+        }
+        const int kn = k + STAGES - 1;  // into the slot of step k - 1
+        if (kn < steps && (kn & 3) == warp) {
+            if (kn >= 32 && (kn & 28) == 0) {  // this warp's next eight steps
+                take_next(kn >> 2);
+                next_pages((kn >> 2) + 8);
+            } else if ((kn & 28) == 8) {
+                next_entries();
             }
             issue(kn);
         }
-        if (pos0 < 0) continue;
-
-        float sc[NTW][4];
+        if (move) {
+            // from the logits themselves: an unset reference leaves nothing of them in y
 #pragma unroll
-        for (int n = 0; n < NTW; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
-        const uint32_t ks0 = e4m3x2_to_f16(ks[0]), ks1 = e4m3x2_to_f16(ks[1]);
-#pragma unroll
-        for (int w = 0; w < KW; ++w) {
-            uint32_t h0[4], h1[4];
-            e2m1x8_to_f16(kw[0][w], h0);
-            e2m1x8_to_f16(kw[1][w], h1);
-            const uint32_t s0 = __byte_perm(ks0, 0, w < 2 ? 0x1010 : 0x3232), s1 = __byte_perm(ks1, 0, w < 2 ? 0x1010 : 0x3232);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                h0[i] = hmul2(h0[i], s0);
-                h1[i] = hmul2(h1[i], s1);
-            }
-            const uint32_t a0[4] = {h0[0], h1[0], h0[1], h1[1]}, a1[4] = {h0[2], h1[2], h0[3], h1[3]};
-#pragma unroll
-            for (int n = 0; n < NTW; ++n) {
-                mma_f16(sc[n], a0, qf[n][2 * w][0], qf[n][2 * w][1]);
-                mma_f16(sc[n], a1, qf[n][2 * w + 1][0], qf[n][2 * w + 1][1]);
-            }
-        }
-        // logits in base 2, relative to the reference and raised by kBias4; hidden tokens at -inf
-        if (pos0 + 15 > len - a.T) {
-            // slots past the sequence's end may hold anything: their scale counts as 0
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (pos0 + 2 * c + (j & 1) + 8 * (j >> 1) >= len) vs[j] = 0u;
-#pragma unroll
-            for (int n = 0; n < NTW; ++n) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int r = (ng * NTW + n) * 8 + 2 * c + (j & 1);
-                    const int lim = r < R ? len - a.T + r / G : len - 1;  // the last token that the row sees
-                    const float z = sc[n][j] * fac[n][j & 1];
-                    sc[n][j] = pos0 + g + 8 * (j >> 1) <= lim ? z : NEG_INF;
-                }
-            }
-        } else {
-#pragma unroll
-            for (int n = 0; n < NTW; ++n)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) sc[n][j] *= fac[n][j & 1];
-        }
-        bool move = false;
-#pragma unroll
-        for (int n = 0; n < NTW; ++n)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) move |= fmaxf(sc[n][j], sc[n][j + 2]) > m[n][j] + kHead4;
-        if (__any_sync(0xffffffffu, move)) {
-#pragma unroll
-            for (int n = 0; n < NTW; ++n) {
+            for (int n = 0; n < NT; ++n) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    float x = fmaxf(sc[n][j], sc[n][j + 2]);
+                    float x = fmaxf(y[n][j] == NEG_INF ? NEG_INF : sc[n][j] * fac[n][j],
+                                    y[n][j + 2] == NEG_INF ? NEG_INF : sc[n][j + 2] * fac[n][j]);
 #pragma unroll
                     for (int off = 4; off < 32; off <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
-                    x = fmaxf(x, m[n][j]);
-                    const float corr = fast_exp2(m[n][j] - x);
-                    m[n][j] = x;
+                    if (g == 0) s_red[warp * COLS + n * 8 + 2 * c + j] = x;
+                }
+            }
+            __syncthreads();
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    float x = NEG_INF;
+#pragma unroll
+                    for (int i = 0; i < WARPS; ++i) x = fmaxf(x, s_red[i * COLS + n * 8 + 2 * c + j]);
+                    x = fmaxf(ref[n][j], x - kBias4);
+                    const float corr = fast_exp2(ref[n][j] - x);
+                    ref[n][j] = x;
+                    if (y[n][j] != NEG_INF) y[n][j] = fmaf(sc[n][j], fac[n][j], -x);
+                    if (y[n][j + 2] != NEG_INF) y[n][j + 2] = fmaf(sc[n][j + 2], fac[n][j], -x);
                     l[n][j] *= corr;
 #pragma unroll
                     for (int i = 0; i < MT; ++i) {
@@ -358,95 +384,134 @@ __global__ void __launch_bounds__(Attn4Cfg<D, NT>::THREADS, Attn4Cfg<D, NT>::OCC
                 }
             }
         }
-        uint32_t pf[NTW][2];
 #pragma unroll
-        for (int n = 0; n < NTW; ++n) {
+        for (int n = 0; n < NT; ++n) {
             float p[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                p[j] = fast_exp2(sc[n][j] - (m[n][j & 1] - kBias4));
+                p[j] = fast_exp2(y[n][j]);
                 l[n][j & 1] += p[j];
             }
-            pf[n][0] = movmatrix_t(pack_f16(p[0], p[1]));
-            pf[n][1] = movmatrix_t(pack_f16(p[2], p[3]));
+            s_p[(warp * NT + n) * 32 + lane] = make_uint2(transpose8(pack_f16(p[0], p[1])), transpose8(pack_f16(p[2], p[3])));
         }
-        const uint32_t s01 = e4m3x2_to_f16(vs[0] | vs[1] << 8), s23 = e4m3x2_to_f16(vs[2] | vs[3] << 8);
+        __syncthreads();  // P is there (and, after a move, s_red has been read)
+        // this warp's half of the channels of two chunks
+        auto pv = [&](int q, int pos, bool whole) {
+            const uint8_t* vt = stage + q * C::CHUNK + HALF;
+            uint32_t v[4], vs[4];
 #pragma unroll
-        for (int w = 0; w < VW; ++w) {
-            // byte i of the words below: channel 2i (first and third word) or 2i + 1 of a token
-            // pair, the earlier token in the low bits
-            uint32_t x[4][4];
-            e2m1x8_to_f16((vw[0][w] & 0x0f0f0f0fu) | ((vw[1][w] << 4) & 0xf0f0f0f0u), x[0]);
-            e2m1x8_to_f16(((vw[0][w] >> 4) & 0x0f0f0f0fu) | (vw[1][w] & 0xf0f0f0f0u), x[1]);
-            e2m1x8_to_f16((vw[2][w] & 0x0f0f0f0fu) | ((vw[3][w] << 4) & 0xf0f0f0f0u), x[2]);
-            e2m1x8_to_f16(((vw[2][w] >> 4) & 0x0f0f0f0fu) | (vw[3][w] & 0xf0f0f0f0u), x[3]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t av[4] = {hmul2(x[0][i], s01), hmul2(x[1][i], s01), hmul2(x[2][i], s23),
-                                        hmul2(x[3][i], s23)};
-#pragma unroll
-                for (int n = 0; n < NTW; ++n) mma_f16(oacc[n][4 * w + i], av, pf[n][0], pf[n][1]);
+            for (int j = 0; j < 4; ++j) {
+                const int t = chunk_token(2 * c + (j & 1)) + 8 * (j >> 1);
+                if constexpr (D == 128) {
+                    v[j] = *reinterpret_cast<const uint32_t*>(vt + t * 64 + chalf * 32 + 4 * g);
+                    vs[j] = vt[CODES + t * 8 + chalf * 4 + (g >> 1)];
+                } else {
+                    v[j] = *reinterpret_cast<const uint16_t*>(vt + t * 32 + chalf * 16 + 2 * g);
+                    vs[j] = vt[CODES + t * 4 + chalf * 2 + (g >> 2)];
+                }
+                // slots past the sequence's end may hold anything: their scale counts as 0
+                if (!whole && pos + t >= len) vs[j] = 0u;
             }
+            const uint32_t s01 = e4m3x2_to_f16(vs[0] + vs[1] * 256u), s23 = e4m3x2_to_f16(vs[2] + vs[3] * 256u);
+            // byte i of a word: the lane's channel 2i (lo) or 2i + 1 (hi) of a token pair, the
+            // earlier token in the low bits
+            uint32_t lo01[4], hi01[4], lo23[4], hi23[4];
+            if constexpr (D == 128) {
+                e2m1x8_to_f16((v[0] & 0x0f0f0f0fu) | ((v[1] << 4) & 0xf0f0f0f0u), lo01);
+                e2m1x8_to_f16(((v[0] >> 4) & 0x0f0f0f0fu) | (v[1] & 0xf0f0f0f0u), hi01);
+                e2m1x8_to_f16((v[2] & 0x0f0f0f0fu) | ((v[3] << 4) & 0xf0f0f0f0u), lo23);
+                e2m1x8_to_f16(((v[2] >> 4) & 0x0f0f0f0fu) | (v[3] & 0xf0f0f0f0u), hi23);
+            } else {
+                const uint32_t v02 = v[0] | v[2] << 16, v13 = v[1] | v[3] << 16;
+                uint32_t lo[4], hi[4];
+                e2m1x8_to_f16((v02 & 0x0f0f0f0fu) | ((v13 << 4) & 0xf0f0f0f0u), lo);
+                e2m1x8_to_f16(((v02 >> 4) & 0x0f0f0f0fu) | (v13 & 0xf0f0f0f0u), hi);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    lo01[i] = lo[i];
+                    hi01[i] = hi[i];
+                    lo23[i] = lo[2 + i];
+                    hi23[i] = hi[2 + i];
+                }
+            }
+            uint2 pf[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) pf[n] = s_p[(q * NT + n) * 32 + lane];
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                const uint32_t av[4] = {hmul2(lo01[i], s01), hmul2(hi01[i], s01), hmul2(lo23[i], s23), hmul2(hi23[i], s23)};
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma_f16(oacc[n][i], av, pf[n].x, pf[n].y);
+            }
+        };
+        const int qa = tpair ? firsts.z : firsts.x, qb = tpair ? firsts.w : firsts.y;
+        if (qa >= 0 && qb >= 0 && max(qa, qb) + 16 <= len) {
+            pv(2 * tpair, qa, true);
+            pv(2 * tpair + 1, qb, true);
+        } else {
+            if (qa >= 0) pv(2 * tpair, qa, false);
+            if (qb >= 0) pv(2 * tpair + 1, qb, false);
         }
     }
 
-    // the warps' states joined: reference maxima, then sums and outputs relative to the largest
+    // the sums of the warps' chunks joined, and O of the second chunk pair handed to the first
+    __syncthreads();
+    float4* s_o = reinterpret_cast<float4*>(smem) + chalf * NT * MT * 32;
 #pragma unroll
-    for (int n = 0; n < NTW; ++n) {
+    for (int n = 0; n < NT; ++n) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) l[n][j] += __shfl_xor_sync(0xffffffffu, l[n][j], off);
-            const int col = (ng * NTW + n) * 8 + 2 * c + j;
-            if (g == 0) s_m[tw * COLS + col] = m[n][j];
+            if (g == 0) s_red[warp * COLS + n * 8 + 2 * c + j] = l[n][j];
         }
-    }
-    __syncthreads();  // and every warp is done with its ring
-#pragma unroll
-    for (int n = 0; n < NTW; ++n) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int col = (ng * NTW + n) * 8 + 2 * c + j;
-            float top = kLow4;
-#pragma unroll
-            for (int i = 0; i < TW; ++i) top = fmaxf(top, s_m[i * COLS + col]);
-            const float f = fast_exp2(m[n][j] - top);
-            if (g == 0) s_l[tw * COLS + col] = l[n][j] * f;
-            float* out = s_o + (tw * COLS + col) * D + g * (D / 8);
+        if (tpair) {
 #pragma unroll
             for (int i = 0; i < MT; ++i)
-                *reinterpret_cast<float2*>(out + 2 * i) = make_float2(oacc[n][i][j] * f, oacc[n][i][j + 2] * f);
+                s_o[(n * MT + i) * 32 + lane] = make_float4(oacc[n][i][0], oacc[n][i][1], oacc[n][i][2], oacc[n][i][3]);
         }
     }
     __syncthreads();
-    for (int i = tid; i < R * (D / 4); i += C::THREADS) {
-        const int r = i / (D / 4), d = (i % (D / 4)) * 4;
-        float top = NEG_INF, sum = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (!tpair) {
 #pragma unroll
-        for (int k = 0; k < TW; ++k) {
-            top = fmaxf(top, s_m[k * COLS + r]);
-            sum += s_l[k * COLS + r];
-            const float4 x = *reinterpret_cast<const float4*>(s_o + (k * COLS + r) * D + d);
-            o.x += x.x;
-            o.y += x.y;
-            o.z += x.z;
-            o.w += x.w;
-        }
-        const float inv = sum == 0.f ? 0.f : a.v_scale / sum;
-        o.x *= inv;
-        o.y *= inv;
-        o.z *= inv;
-        o.w *= inv;
-        const float lse = sum == 0.f ? NEG_INF : (top - kBias4 + log2f(sum)) * kLn2;
-        if (nsplit == 1) {
-            const long long oi = out_index(r);
-            *reinterpret_cast<uint2*>(a.o + oi * D + d) = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
-            if (d == 0 && a.lse) a.lse[oi] = lse;
-        } else {
-            const long long at = ((long long)row * a.num_splits + split) * R + r;
-            *reinterpret_cast<float4*>(a.part_o + at * D + d) = o;
-            if (d == 0) a.part_lse[at] = lse;
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                const float4 x = s_o[(n * MT + i) * 32 + lane];
+                oacc[n][i][0] += x.x;
+                oacc[n][i][1] += x.y;
+                oacc[n][i][2] += x.z;
+                oacc[n][i][3] += x.w;
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int r = n * 8 + 2 * c + j;
+                if (r >= R) continue;
+                float sum = 0.f;
+#pragma unroll
+                for (int i = 0; i < WARPS; ++i) sum += s_red[i * COLS + r];
+                const float inv = sum == 0.f ? 0.f : a.v_scale / sum;
+                const float lse = sum == 0.f ? NEG_INF : (ref[n][j] + log2f(sum)) * kLn2;
+                const int d = chalf * (D / 2) + g * (D / 16);  // the lane's 2 MT channels
+                const bool first = warp == 0 && g == 0;
+                if (nsplit == 1) {
+                    const long long oi = out_index(r);
+#pragma unroll
+                    for (int i = 0; i < MT; i += 2)
+                        *reinterpret_cast<uint2*>(a.o + oi * D + d + 2 * i) =
+                            make_uint2(pack_bf16(oacc[n][i][j] * inv, oacc[n][i][j + 2] * inv),
+                                       pack_bf16(oacc[n][i + 1][j] * inv, oacc[n][i + 1][j + 2] * inv));
+                    if (first && a.lse) a.lse[oi] = lse;
+                } else {
+                    const long long at = ((long long)row * a.num_splits + split) * R + r;
+#pragma unroll
+                    for (int i = 0; i < MT; i += 2)
+                        *reinterpret_cast<float4*>(a.part_o + at * D + d + 2 * i) =
+                            make_float4(oacc[n][i][j] * inv, oacc[n][i][j + 2] * inv, oacc[n][i + 1][j] * inv,
+                                        oacc[n][i + 1][j + 2] * inv);
+                    if (first) a.part_lse[at] = lse;
+                }
+            }
         }
     }
     if (nsplit == 1) return;
