@@ -330,28 +330,45 @@ def lse_merge(part_o, part_lse, o, lse=None, stream=None):
                            _stream(stream)))
 
 
-def _arg(t, dtypes, what: str, numel: int | None = None, rows: bool = False):
-    """The address of a tensor of the current device, its type and size checked (None passes).
+_B16 = _I32 = _F32 = _U8 = _LOGITS = ()  # accepted types, set with torch's first use
+_torch = None
+
+
+def _here(stream):
+    """The current device and the raw stream to launch on (the given one has to be of that device)."""
+    global _torch, _B16, _I32, _F32, _U8, _LOGITS
+    if _torch is None:
+        import torch
+        _B16, _I32, _F32, _U8 = (torch.bfloat16, torch.uint16), (torch.int32,), (torch.float32,), (torch.uint8,)
+        _LOGITS = (torch.float32, torch.bfloat16)
+        if not torch.cuda.is_available():
+            raise SpdError(3, "no CUDA device")
+        _torch = torch
+    dev = _torch.cuda.current_device()
+    if stream is None:
+        return dev, _torch.cuda.current_stream(dev).cuda_stream
+    if stream.device.index != dev:
+        raise SpdError(1, "the stream is not of the current CUDA device")
+    return dev, stream.cuda_stream
+
+
+def _arg(t, dtypes, what: str, dev: int, numel: int | None = None, rows: bool = False):
+    """The address of a tensor of device `dev`, its type and size checked (None passes).
 
     rows: a [..., heads, D] view whose heads and channels are contiguous and whose leading
-    dimensions are one stride apart (a slice of a fused projection)."""
-    import torch
+    dimensions are one stride apart (a slice of a fused projection; see _row_stride)."""
     if t is None:
         return None
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+    if (t.dtype in dtypes and t.get_device() == dev and (numel is None or t.numel() == numel)
+            and (rows or t.is_contiguous())):
+        return t.data_ptr()
+    if t.get_device() != dev:
         raise SpdError(1, f"{what} is not on the current CUDA device")
     if t.dtype not in dtypes:
         raise SpdError(1, f"{what} is {t.dtype}, not {' or '.join(map(str, dtypes))}")
     if numel is not None and t.numel() != numel:
         raise SpdError(1, f"{what} has {t.numel()} elements, not {numel}")
-    if not rows and not t.is_contiguous():
-        raise SpdError(1, f"{what} is not contiguous")
-    return t.data_ptr()
-
-
-def _types():
-    import torch
-    return (torch.bfloat16, torch.uint16), (torch.int32,), (torch.float32,), (torch.uint8,)
+    raise SpdError(1, f"{what} is not contiguous")
 
 
 def _row_stride(t, D: int, what: str) -> int:
@@ -359,8 +376,10 @@ def _row_stride(t, D: int, what: str) -> int:
     shape, stride = t.shape, t.stride()
     if len(shape) < 3 or shape[-1] != D:
         raise SpdError(1, f"{what} must be [..., heads, {D}], not {list(shape)}")
-    if stride[-1] != 1 or (shape[-2] > 1 and stride[-2] != D):
+    if stride[-1] != 1 or (stride[-2] != D and shape[-2] > 1):
         raise SpdError(1, f"{what}: the heads and channels of a row must be contiguous")
+    if len(shape) == 3:
+        return stride[0] if shape[0] > 1 else shape[-2] * D
     step, n = None, 1
     for size, s in zip(reversed(shape[:-2]), reversed(stride[:-2])):
         if size == 1:
@@ -373,60 +392,57 @@ def _row_stride(t, D: int, what: str) -> int:
     return step if step is not None else shape[-2] * D
 
 
-def _rope_of(rope, q_weight, k_weight, eps: float, interleaved: bool, D: int) -> Rope:
-    b16, _, f32, _ = _types()
+def _rope_of(rope, q_weight, k_weight, eps: float, interleaved: bool, D: int, dev: int) -> Rope:
     if rope is None:
-        n_pos, rot = 0, 0
+        n_pos, rot, table = 0, 0, None
     else:
         if rope.dim() != 3 or rope.shape[1] != 2:
             raise SpdError(1, f"rope must be [n_pos, 2, rot_dim / 2], not {list(rope.shape)}")
-        n_pos, rot = rope.shape[0], 2 * rope.shape[2]
-    return Rope(_arg(rope, f32, "rope"), n_pos, rot, 1 if interleaved else 0, eps,
-                _arg(q_weight, b16, "q_weight", D), _arg(k_weight, b16, "k_weight", D))
+        n_pos, rot, table = rope.shape[0], 2 * rope.shape[2], _arg(rope, _F32, "rope", dev)
+    return Rope(table, n_pos, rot, 1 if interleaved else 0, eps, _arg(q_weight, _B16, "q_weight", dev, D),
+                _arg(k_weight, _B16, "k_weight", dev, D))
 
 
 def qk_norm_rope(q, k, positions, rope, q_out, k_out, q_weight=None, k_weight=None, eps: float = 1e-6,
                  interleaved: bool = False, stream=None):
     """Norm and rotation of query rows q [..., H_q, D] and key rows k [..., H_kv, D] (either may be
     None) at positions [...]; rope fp32 [n_pos, 2, rot_dim / 2] (None: norm only)."""
-    b16, i32, _, _ = _types()
     one = q if q is not None else k
     if one is None:
         raise SpdError(1, "q and k are both None")
+    dev, st = _here(stream)
     D = one.shape[-1]
     rows = one.numel() // max(1, one.shape[-2] * D)
-    r = _rope_of(rope, q_weight, k_weight, eps, interleaved, D)
-    args = []
-    for t, out, what in ((q, q_out, "q"), (k, k_out, "k")):
-        if t is None:
-            args.append((0, None, 0, None))
-            continue
-        step, heads = _row_stride(t, D, what), t.shape[-2]
-        args.append((heads, _arg(t, b16, what, rows * heads * D, rows=True), step,
-                     _arg(out, b16, what + "_out", rows * heads * D)))
-    (hq, qp, qs, qo), (hk, kp, ks, ko) = args
-    _check(lib().qk_norm_rope(rows, hq, hk, D, ctypes.byref(r), qp, qs, kp, ks,
-                              _arg(positions, i32, "positions", rows) if r.rot_dim else None, qo, ko,
-                              _stream(stream)))
+    r = _rope_of(rope, q_weight, k_weight, eps, interleaved, D, dev)
+    hq = qs = hk = ks = 0
+    qp = qo = kp = ko = None
+    if q is not None:
+        hq, qs = q.shape[-2], _row_stride(q, D, "q")
+        qp = _arg(q, _B16, "q", dev, rows * hq * D, True)
+        qo = _arg(q_out, _B16, "q_out", dev, rows * hq * D)
+    if k is not None:
+        hk, ks = k.shape[-2], _row_stride(k, D, "k")
+        kp = _arg(k, _B16, "k", dev, rows * hk * D, True)
+        ko = _arg(k_out, _B16, "k_out", dev, rows * hk * D)
+    pos = _arg(positions, _I32, "positions", dev, rows) if r.rot_dim else None
+    _check(lib().qk_norm_rope(rows, hq, hk, D, ctypes.byref(r), qp, qs, kp, ks, pos, qo, ko, st))
 
 
 def kv_append_rope(dims: Dims, T: int, K, V, page_table, seq_lens, q, k, v, rope, q_out, summ, q_weight=None,
                    k_weight=None, eps: float = 1e-6, interleaved: bool = False, stream=None):
     """Norm and rotate the T newest tokens' keys into the paged cache (values as they are), rebuild
     their pages' summaries, and write the rotated queries to q_out; q and q_out may be None."""
-    b16, i32, _, _ = _types()
-    B, D, n = dims.B, dims.D, dims.B * T
-    cache = dims.num_phys_pages * dims.H_kv * dims.page_size * D
-    r = _rope_of(rope, q_weight, k_weight, eps, interleaved, D)
-    qs = _row_stride(q, D, "q") if q is not None else 0
+    dev, st = _here(stream)
+    B, D, H, pages = dims.B, dims.D, dims.H_kv, dims.max_pages_per_seq
+    n, cache = B * T, dims.num_phys_pages * H * dims.page_size * D
+    r = _rope_of(rope, q_weight, k_weight, eps, interleaved, D, dev)
     _check(lib().kv_append_rope(
-        ctypes.byref(dims), T, ctypes.byref(r), _arg(K, b16, "K", cache), _arg(V, b16, "V", cache),
-        _arg(page_table, i32, "page_table", B * dims.max_pages_per_seq), _arg(seq_lens, i32, "seq_lens", B),
-        _arg(q, b16, "q", n * dims.H_q * D, rows=True), qs,
-        _arg(k, b16, "k", n * dims.H_kv * D, rows=True), _row_stride(k, D, "k"),
-        _arg(v, b16, "v", n * dims.H_kv * D, rows=True), _row_stride(v, D, "v"),
-        _arg(q_out, b16, "q_out", n * dims.H_q * D),
-        _arg(summ, b16, "summ", B * dims.H_kv * dims.max_pages_per_seq * 2 * D), _stream(stream)))
+        ctypes.byref(dims), T, ctypes.byref(r), _arg(K, _B16, "K", dev, cache), _arg(V, _B16, "V", dev, cache),
+        _arg(page_table, _I32, "page_table", dev, B * pages), _arg(seq_lens, _I32, "seq_lens", dev, B),
+        _arg(q, _B16, "q", dev, n * dims.H_q * D, True), 0 if q is None else _row_stride(q, D, "q"),
+        _arg(k, _B16, "k", dev, n * H * D, True), _row_stride(k, D, "k"),
+        _arg(v, _B16, "v", dev, n * H * D, True), _row_stride(v, D, "v"),
+        _arg(q_out, _B16, "q_out", dev, n * dims.H_q * D), _arg(summ, _B16, "summ", dev, B * H * pages * 2 * D), st))
 
 
 def kv4_cache(dims: Dims, device=None):
@@ -436,31 +452,33 @@ def kv4_cache(dims: Dims, device=None):
                        dtype=torch.uint8, device=device or "cuda")
 
 
-def _kv4(dims: Dims, kv4):
-    return _arg(kv4, _types()[3], "kv4", dims.num_phys_pages * dims.H_kv * dims.page_size * dims.D * 9 // 8)
+def _kv4(dims: Dims, kv4, dev: int):
+    return _arg(kv4, _U8, "kv4", dev, dims.num_phys_pages * dims.H_kv * dims.page_size * dims.D * 9 // 8)
 
 
 def kv4_append(dims: Dims, T: int, kv4, page_table, seq_lens, k_new, v_new, summ, k_exp: int = 0,
                v_exp: int = 0, stream=None):
     """Quantise the T newest tokens into the 4-bit cache and rebuild the summaries of their pages."""
-    b16, i32, _, _ = _types()
-    B, D, n = dims.B, dims.D, dims.B * T * dims.H_kv * dims.D
+    dev, st = _here(stream)
+    B, pages = dims.B, dims.max_pages_per_seq
+    row = dims.H_kv * dims.D
     _check(lib().kv4_append(
-        ctypes.byref(dims), T, _kv4(dims, kv4), k_exp, v_exp,
-        _arg(page_table, i32, "page_table", B * dims.max_pages_per_seq), _arg(seq_lens, i32, "seq_lens", B),
-        _arg(k_new, b16, "k_new", n), _arg(v_new, b16, "v_new", n),
-        _arg(summ, b16, "summ", B * dims.H_kv * dims.max_pages_per_seq * 2 * D), _stream(stream)))
+        ctypes.byref(dims), T, _kv4(dims, kv4, dev), k_exp, v_exp,
+        _arg(page_table, _I32, "page_table", dev, B * pages), _arg(seq_lens, _I32, "seq_lens", dev, B),
+        _arg(k_new, _B16, "k_new", dev, B * T * row), _arg(v_new, _B16, "v_new", dev, B * T * row),
+        _arg(summ, _B16, "summ", dev, B * pages * 2 * row), st))
 
 
 def kv4_read(dims: Dims, T: int, kv4, page_table, seq_lens, k_out, v_out, k_exp: int = 0, v_exp: int = 0,
              stream=None):
     """The T newest tokens of every sequence as the bf16 values that the 4-bit cache holds."""
-    b16, i32, _, _ = _types()
+    dev, st = _here(stream)
     B, n = dims.B, dims.B * T * dims.H_kv * dims.D
     _check(lib().kv4_read(
-        ctypes.byref(dims), T, _kv4(dims, kv4), k_exp, v_exp,
-        _arg(page_table, i32, "page_table", B * dims.max_pages_per_seq), _arg(seq_lens, i32, "seq_lens", B),
-        _arg(k_out, b16, "k_out", n), _arg(v_out, b16, "v_out", n), _stream(stream)))
+        ctypes.byref(dims), T, _kv4(dims, kv4, dev), k_exp, v_exp,
+        _arg(page_table, _I32, "page_table", dev, B * dims.max_pages_per_seq),
+        _arg(seq_lens, _I32, "seq_lens", dev, B), _arg(k_out, _B16, "k_out", dev, n),
+        _arg(v_out, _B16, "v_out", dev, n), st))
 
 
 def spd_kv4_sparse_decode_workspace_size(dims: Dims, k_max: int, num_splits: int = 0) -> int:
@@ -479,29 +497,29 @@ def kv4_sparse_decode_attn(dims: Dims, q, kv4, page_table, seq_lens, sel, nsel, 
                            num_splits: int = 0, softmax_scale: float | None = None, k_exp: int = 0,
                            v_exp: int = 0, stream=None):
     """sparse_decode_attn over the 4-bit cache."""
-    b16, i32, f32, u8 = _types()
+    dev, st = _here(stream)
     scale = 1.0 / math.sqrt(dims.D) if softmax_scale is None else softmax_scale
-    B, rows = dims.B, dims.B * dims.H_q
+    B, D, H, rows = dims.B, dims.D, dims.H_kv, dims.B * dims.H_q
     _check(lib().kv4_sparse_decode_attn(
-        ctypes.byref(dims), _arg(q, b16, "q", rows * dims.D), _kv4(dims, kv4), k_exp, v_exp,
-        _arg(page_table, i32, "page_table", B * dims.max_pages_per_seq), _arg(seq_lens, i32, "seq_lens", B),
-        _arg(sel, i32, "sel", B * dims.H_kv * k_max), _arg(nsel, i32, "nsel", B * dims.H_kv), k_max,
-        num_splits, scale, _arg(o, b16, "o", rows * dims.D), _arg(lse, f32, "lse", rows),
-        _arg(ws, u8, "ws"), ws.numel(), _stream(stream)))
+        ctypes.byref(dims), _arg(q, _B16, "q", dev, rows * D), _kv4(dims, kv4, dev), k_exp, v_exp,
+        _arg(page_table, _I32, "page_table", dev, B * dims.max_pages_per_seq),
+        _arg(seq_lens, _I32, "seq_lens", dev, B), _arg(sel, _I32, "sel", dev, B * H * k_max),
+        _arg(nsel, _I32, "nsel", dev, B * H), k_max, num_splits, scale, _arg(o, _B16, "o", dev, rows * D),
+        _arg(lse, _F32, "lse", dev, rows), _arg(ws, _U8, "ws", dev), ws.numel(), st))
 
 
 def kv4_dense_verify_attn(dims: Dims, T: int, q, kv4, page_table, seq_lens, o, ws, lse=None,
                           num_splits: int = 0, softmax_scale: float | None = None, k_exp: int = 0,
                           v_exp: int = 0, stream=None):
     """dense_verify_attn over the 4-bit cache."""
-    b16, i32, f32, u8 = _types()
+    dev, st = _here(stream)
     scale = 1.0 / math.sqrt(dims.D) if softmax_scale is None else softmax_scale
-    B, rows = dims.B, dims.B * T * dims.H_q
+    B, D, rows = dims.B, dims.D, dims.B * T * dims.H_q
     _check(lib().kv4_dense_verify_attn(
-        ctypes.byref(dims), T, _arg(q, b16, "q", rows * dims.D), _kv4(dims, kv4), k_exp, v_exp,
-        _arg(page_table, i32, "page_table", B * dims.max_pages_per_seq), _arg(seq_lens, i32, "seq_lens", B),
-        num_splits, scale, _arg(o, b16, "o", rows * dims.D), _arg(lse, f32, "lse", rows),
-        _arg(ws, u8, "ws"), ws.numel(), _stream(stream)))
+        ctypes.byref(dims), T, _arg(q, _B16, "q", dev, rows * D), _kv4(dims, kv4, dev), k_exp, v_exp,
+        _arg(page_table, _I32, "page_table", dev, B * dims.max_pages_per_seq),
+        _arg(seq_lens, _I32, "seq_lens", dev, B), num_splits, scale, _arg(o, _B16, "o", dev, rows * D),
+        _arg(lse, _F32, "lse", dev, rows), _arg(ws, _U8, "ws", dev), ws.numel(), st))
 
 
 def spd_token_logprobs_workspace_size(rows: int, n_vocab: int, top_k: int = 0) -> int:
@@ -513,22 +531,23 @@ def token_logprobs(logits, targets, logprobs, ws, entropy=None, lse=None, top_id
                    inv_temperature: float = 1.0, stream=None):
     """Log probabilities of targets [...] under logits [..., n_vocab] (fp32 or bf16; rows may be one
     stride apart), with the optional entropy and lse [...] and the alternatives [..., top_k]."""
-    import torch
-    _, i32, f32, u8 = _types()
+    dev, st = _here(stream)
     n = logits.shape[-1]
     rows = logits.numel() // max(1, n)
     step = n
-    if logits.dim() > 1:  # as rows of one "head" of n channels
+    if logits.dim() == 2 and logits.stride(1) == 1:
+        step = logits.stride(0) if rows > 1 else n
+    elif logits.dim() > 1:  # as rows of one "head" of n channels
         step = _row_stride(logits.unsqueeze(-2), n, "logits")
     elif n > 1 and logits.stride(0) != 1:
         raise SpdError(1, "logits: a row must be contiguous")
     top_k = 0 if top_ids is None else top_ids.shape[-1]
     _check(lib().token_logprobs(
-        rows, n, _arg(logits, (torch.float32, torch.bfloat16), "logits", rows=True),
-        1 if logits.dtype == torch.bfloat16 else 0, step, _arg(targets, i32, "targets", rows),
-        inv_temperature, _arg(logprobs, f32, "logprobs", rows), _arg(entropy, f32, "entropy", rows),
-        _arg(lse, f32, "lse", rows), top_k, _arg(top_ids, i32, "top_ids", rows * top_k),
-        _arg(top_logprobs, f32, "top_logprobs", rows * top_k), _arg(ws, u8, "ws"), ws.numel(), _stream(stream)))
+        rows, n, _arg(logits, _LOGITS, "logits", dev, None, True), 1 if logits.dtype is _LOGITS[1] else 0, step,
+        _arg(targets, _I32, "targets", dev, rows), inv_temperature, _arg(logprobs, _F32, "logprobs", dev, rows),
+        _arg(entropy, _F32, "entropy", dev, rows), _arg(lse, _F32, "lse", dev, rows), top_k,
+        _arg(top_ids, _I32, "top_ids", dev, rows * top_k),
+        _arg(top_logprobs, _F32, "top_logprobs", dev, rows * top_k), _arg(ws, _U8, "ws", dev), ws.numel(), st))
 
 
 class Round:

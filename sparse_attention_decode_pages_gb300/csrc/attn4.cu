@@ -27,6 +27,8 @@
 // into the logits' scale).  Online softmax in fp32 in base 2; a column's reference
 // moves only when a logit exceeds it by kHead4, and weights carry a factor 2^kBias4 so
 // that what fp16 drops of a weight lies 2^-32 below the reference.
+#include <atomic>
+
 #include "kv4.cuh"
 #include "kernels.h"
 
@@ -578,20 +580,41 @@ void attn4_variant(int D, int R, bool sparse, Attn4Fn* fn, int* smem, int* threa
 
 }  // namespace
 
-int occ_attn4(int D, int ps, int R, bool sparse) {
-    Attn4Fn fn;
-    int smem, threads, n = 0;
-    attn4_variant(D, R, sparse, &fn, &smem, &threads);
-    cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, threads, smem);
-    return n < 1 ? 1 : n;
+// The kernel's attribute for its shared memory and its CTAs on an SM, asked of the driver
+// once for a device and a variant.
+static cudaError_t attn4_ready(int D, int R, bool sparse, int* occ) {
+    constexpr int kDevices = 64, kVariants = 10;
+    static std::atomic<int> known[kDevices][kVariants];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const int v = (D == 128 ? 5 : 0) + (sparse ? 4 : R <= 8 ? 0 : R <= 16 ? 1 : R <= 32 ? 2 : 3);
+    int n = dev < kDevices ? known[dev][v].load(std::memory_order_acquire) : 0;
+    if (n == 0) {
+        Attn4Fn fn;
+        int smem, threads;
+        attn4_variant(D, R, sparse, &fn, &smem, &threads);
+        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, threads, smem);
+        if (e != cudaSuccess) return e;
+        if (n < 1) n = 1;
+        if (dev < kDevices) known[dev][v].store(n, std::memory_order_release);
+    }
+    *occ = n;
+    return cudaSuccess;
+}
+
+int occ_attn4(int D, int R, bool sparse) {
+    int n = 1;
+    return attn4_ready(D, R, sparse, &n) == cudaSuccess ? n : 1;
 }
 
 cudaError_t launch_attn4(const Attn4Args& a, bool sparse, cudaStream_t st) {
     Attn4Fn fn;
-    int smem, threads;
-    attn4_variant(a.D, a.T * (a.H_q / a.H_kv), sparse, &fn, &smem, &threads);
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    int smem, threads, occ;
+    const int R = a.T * (a.H_q / a.H_kv);
+    attn4_variant(a.D, R, sparse, &fn, &smem, &threads);
+    cudaError_t e = attn4_ready(a.D, R, sparse, &occ);
     if (e != cudaSuccess) return e;
     return launch_pdl(fn, dim3((unsigned)((long long)a.B * a.H_kv * a.num_splits)), dim3(threads), smem, st, a);
 }

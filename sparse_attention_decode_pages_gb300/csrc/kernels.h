@@ -133,7 +133,7 @@ struct Attn4Args {
 };
 cudaError_t launch_attn4(const Attn4Args& a, bool sparse, cudaStream_t st);
 // CTAs of the kernel that fit on one SM for this shape.
-int occ_attn4(int D, int ps, int R, bool sparse);
+int occ_attn4(int D, int R, bool sparse);
 
 struct LogprobArgs {
     const void* logits;  // [rows][n], row_stride elements apart

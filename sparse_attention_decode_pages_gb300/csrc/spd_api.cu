@@ -969,7 +969,7 @@ constexpr int kv4_unit_fixed = 12;
 static int kv4_splits(const spd_dims* d, int T, int items, bool sparse, int req, int sms) {
     const long long rows = (long long)d->B * d->H_kv;
     const int warps = 4;  // chunks in work at once
-    const long long slots = (long long)sms * occ_attn4(d->D, d->page_size, T * (d->H_q / d->H_kv), sparse);
+    const long long slots = (long long)sms * occ_attn4(d->D, T * (d->H_q / d->H_kv), sparse);
     int S = req;
     if (S <= 0) {
         S = 1;
