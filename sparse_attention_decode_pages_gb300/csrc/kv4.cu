@@ -8,6 +8,10 @@
 namespace spd {
 
 constexpr int kKv4Threads = 256;
+constexpr int kNewBatch = 1;  // groups of new rows whose loads an appending lane keeps in flight
+constexpr int kOldBatch = 2;  // and of older ones
+constexpr int kPageHeads = 2;  // KV heads of an append's CTA
+constexpr int kPageParts = kKv4Threads / 32 / kPageHeads;  // warps of a head
 
 // The lane's eight channels of a row as four bf16 pairs, from its four bytes of codes
 // and its group's scale byte.
@@ -24,10 +28,17 @@ __device__ __forceinline__ uint4 kv4_values(uint32_t codes, uint32_t scale_byte,
     return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
+// a / s rounded correctly, r = 1 / s rounded correctly (Markstein: the quotient corrected by
+// its exact remainder); for the finite magnitudes met here.
+__device__ __forceinline__ float quotient(float a, float s, float r) {
+    const float q = a * r;
+    return fmaf(fmaf(-q, s, a), r, q);
+}
+
 // Quantises the lane's eight channels (its group's other eight are the neighbour
-// lane's): codes and the group's scale byte.  Divisions are rounded correctly, so the
+// lane's): codes and the group's scale byte.  Quotients are rounded correctly, so the
 // codes are those of the exact quotients: a border between codes times a scale has
-// few enough bits that no rounded quotient crosses it.
+// few enough bits that no rounded quotient crosses it, and a tie is met exactly.
 __device__ __forceinline__ uint32_t kv4_quantise(const uint4& u, float inv_exp2, uint32_t& scale_byte) {
     const __nv_bfloat162* e = reinterpret_cast<const __nv_bfloat162*>(&u);
     float x[8];
@@ -40,8 +51,10 @@ __device__ __forceinline__ uint32_t kv4_quantise(const uint4& u, float inv_exp2,
         amax = fmaxf(amax, fmaxf(fabsf(x[2 * i]), fabsf(x[2 * i + 1])));  // NaN counts as 0
     }
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    scale_byte = to_e4m3(__fdiv_rn(amax, 6.f));
+    constexpr float kTop = 6.f * 448.f;  // the largest value a group can hold
+    scale_byte = to_e4m3(quotient(fminf(amax, kTop), 6.f, 1.f / 6.f));
     const float s = e4m3_value(scale_byte);
+    const float r = s > 0.f ? __frcp_rn(s) : 0.f;  // scale 0: the codes are zeros
     uint32_t codes = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -49,23 +62,29 @@ __device__ __forceinline__ uint32_t kv4_quantise(const uint4& u, float inv_exp2,
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const float v = x[2 * i + j];
-            y[j] = s > 0.f ? __fdiv_rn(v, s) : copysignf(0.f, v);
-            if (!(v == v)) y[j] = 0.f;
+            // an infinity as the largest value (of its sign), NaN as 0; the sign of zeros stays
+            const float c = v == v ? fminf(fmaxf(v, -kTop), kTop) : 0.f;
+            y[j] = copysignf(quotient(c, s, r), c);
         }
         codes |= to_e2m1x2(y[0], y[1]) << (8 * i);
     }
     return codes;
 }
 
-// One CTA per (sequence, touched page), a warp per KV head, as in kv_append_refresh:
-// older rows are read back from the cache, new ones quantised and stored, and the
-// min / max of the values of all valid rows becomes the page's summary.
+// One CTA per (sequence, touched page, two KV heads), four warps a head: each takes
+// every fourth group of the page's rows, older ones read back from the cache, new ones
+// quantised and stored, and the min / max of the values of all valid rows, joined
+// through shared memory, becomes the page's summary.
 template <int D>
-__global__ void __launch_bounds__(kKv4Threads) kv4_append_kernel(const Kv4Args a) {
+__global__ void __launch_bounds__(kKv4Threads, 4) kv4_append_kernel(const Kv4Args a) {
     constexpr int L = D / 8;     // lanes per row
     constexpr int RPI = 32 / L;  // rows per warp instruction
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
-    const int b = blockIdx.x;
+    constexpr int STEP = kPageParts * RPI;
+    __shared__ uint4 s_mm[kKv4Threads / 32][L][2];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int head_ctas = (a.H_kv + kPageHeads - 1) / kPageHeads;
+    const int b = blockIdx.x / head_ctas, h = (blockIdx.x - b * head_ctas) * kPageHeads + warp / kPageParts;
+    const int part = warp % kPageParts;
     pdl_wait();
     pdl_trigger();
     const int len = a.seq_lens[b];
@@ -85,83 +104,114 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_append_kernel(const Kv4Args a
     const int r0 = lane / L, l = lane % L;
     const int half = kv4_half_bytes(a.ps, D), codes_bytes = kv4_codes_bytes(a.ps, D);
     const float k2 = pow2f(a.k_exp), ik2 = pow2f(-a.k_exp), iv2 = pow2f(-a.v_exp);
-    const __nv_bfloat162 pinf = __floats2bfloat162_rn(__int_as_float(0x7f800000), __int_as_float(0x7f800000));
-    const __nv_bfloat162 ninf = __floats2bfloat162_rn(__int_as_float(0xff800000), __int_as_float(0xff800000));
+    const __half2 pinf = __floats2half2_rn(__int_as_float(0x7f800000), __int_as_float(0x7f800000));
+    const __half2 ninf = __floats2half2_rn(__int_as_float(0xff800000), __int_as_float(0xff800000));
     const int nold = min(valid, max(0, first - p * a.ps));
-    for (int h = warp; h < a.H_kv; h += nwarps) {
+    __half2 mn[4], mx[4];  // of code * scale, exact in fp16
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        mn[i] = pinf;
+        mx[i] = ninf;
+    }
+    if (h < a.H_kv) {
         uint8_t* kt = a.kv4 + (phys * a.H_kv + h) * (2LL * half);
         uint8_t* vt = kt + half;
-        __nv_bfloat162 mn[4], mx[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            mn[i] = pinf;
-            mx[i] = ninf;
-        }
         auto fold = [&](uint32_t codes, uint32_t scale) {
-            const uint4 v = kv4_values(codes, scale, k2);
-            const __nv_bfloat162* e = reinterpret_cast<const __nv_bfloat162*>(&v);
+            uint32_t c4[4];
+            e2m1x8_to_f16(codes, c4);
+            const uint32_t s2 = e4m3x2_to_f16(scale * 0x101u);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                mn[i] = __hmin2(mn[i], e[i]);
-                mx[i] = __hmax2(mx[i], e[i]);
+                const uint32_t v = hmul2(c4[i], s2);
+                mn[i] = __hmin2(mn[i], *reinterpret_cast<const __half2*>(&v));
+                mx[i] = __hmax2(mx[i], *reinterpret_cast<const __half2*>(&v));
             }
         };
-        for (int t0 = r0; t0 < nold; t0 += kAppendBatch * RPI) {
-            uint32_t c[kAppendBatch], s[kAppendBatch];
+        for (int t0 = part * RPI + r0; t0 < nold; t0 += kOldBatch * STEP) {
+            uint32_t c[kOldBatch], s[kOldBatch];
 #pragma unroll
-            for (int u = 0; u < kAppendBatch; ++u)
-                if (t0 + u * RPI < nold) {
-                    c[u] = *reinterpret_cast<const uint32_t*>(kt + (t0 + u * RPI) * (D / 2) + 4 * l);
-                    s[u] = kt[codes_bytes + (t0 + u * RPI) * (D / 16) + l / 2];
+            for (int u = 0; u < kOldBatch; ++u)
+                if (t0 + u * STEP < nold) {
+                    c[u] = *reinterpret_cast<const uint32_t*>(kt + (t0 + u * STEP) * (D / 2) + 4 * l);
+                    s[u] = kt[codes_bytes + (t0 + u * STEP) * (D / 16) + l / 2];
                 }
 #pragma unroll
-            for (int u = 0; u < kAppendBatch; ++u)
-                if (t0 + u * RPI < nold) fold(c[u], s[u]);
+            for (int u = 0; u < kOldBatch; ++u)
+                if (t0 + u * STEP < nold) fold(c[u], s[u]);
         }
-        for (int tb = nold; tb < valid; tb += RPI) {  // by the whole warp: the groups' maxima are exchanged
-            const int t = tb + r0;
-            const bool live = t < valid;
-            uint4 k = make_uint4(0u, 0u, 0u, 0u), v = k;
-            if (live) {
-                const long long src = (((long long)b * a.T + (p * a.ps + t - first)) * a.H_kv + h) * (D / 8) + l;
-                k = __ldg(reinterpret_cast<const uint4*>(a.k_new) + src);
-                v = __ldg(reinterpret_cast<const uint4*>(a.v_new) + src);
-            }
-            uint32_t ks, vs;
-            const uint32_t kc = kv4_quantise(k, ik2, ks);
-            const uint32_t vc = kv4_quantise(v, iv2, vs);
-            if (live) {
-                *reinterpret_cast<uint32_t*>(kt + t * (D / 2) + 4 * l) = kc;
-                *reinterpret_cast<uint32_t*>(vt + t * (D / 2) + 4 * l) = vc;
-                if (!(l & 1)) {
-                    kt[codes_bytes + t * (D / 16) + l / 2] = (uint8_t)ks;
-                    vt[codes_bytes + t * (D / 16) + l / 2] = (uint8_t)vs;
+        // new rows: kNewBatch loads in flight a lane, then by the whole warp (the groups' maxima
+        // are exchanged)
+        const long long src = (((long long)b * a.T + (p * a.ps - first)) * a.H_kv + h) * (D / 8) + l;
+        for (int tb = nold + part * RPI; tb < valid; tb += kNewBatch * STEP) {
+            uint4 k[kNewBatch], v[kNewBatch];
+#pragma unroll
+            for (int u = 0; u < kNewBatch; ++u) {
+                const int t = tb + u * STEP + r0;
+                k[u] = v[u] = make_uint4(0u, 0u, 0u, 0u);
+                if (t < valid) {
+                    k[u] = __ldg(reinterpret_cast<const uint4*>(a.k_new) + src + (long long)t * a.H_kv * (D / 8));
+                    v[u] = __ldg(reinterpret_cast<const uint4*>(a.v_new) + src + (long long)t * a.H_kv * (D / 8));
                 }
-                fold(kc, ks);
+            }
+#pragma unroll
+            for (int u = 0; u < kNewBatch; ++u) {
+                const int t = tb + u * STEP + r0;
+                if (tb + u * STEP >= valid) break;
+                uint32_t ks, vs;
+                const uint32_t kc = kv4_quantise(k[u], ik2, ks);
+                const uint32_t vc = kv4_quantise(v[u], iv2, vs);
+                if (t < valid) {
+                    *reinterpret_cast<uint32_t*>(kt + t * (D / 2) + 4 * l) = kc;
+                    *reinterpret_cast<uint32_t*>(vt + t * (D / 2) + 4 * l) = vc;
+                    if (!(l & 1)) {
+                        kt[codes_bytes + t * (D / 16) + l / 2] = (uint8_t)ks;
+                        vt[codes_bytes + t * (D / 16) + l / 2] = (uint8_t)vs;
+                    }
+                    fold(kc, ks);
+                }
             }
         }
 #pragma unroll
         for (int off = L; off < 32; off <<= 1) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                uint32_t a_ = __shfl_xor_sync(0xffffffffu, *reinterpret_cast<uint32_t*>(&mn[i]), off);
-                uint32_t b_ = __shfl_xor_sync(0xffffffffu, *reinterpret_cast<uint32_t*>(&mx[i]), off);
-                mn[i] = __hmin2(mn[i], *reinterpret_cast<__nv_bfloat162*>(&a_));
-                mx[i] = __hmax2(mx[i], *reinterpret_cast<__nv_bfloat162*>(&b_));
+                mn[i] = __hmin2(mn[i], __shfl_xor_sync(0xffffffffu, mn[i], off));
+                mx[i] = __hmax2(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], off));
             }
         }
         if (r0 == 0) {
-            uint4* out = reinterpret_cast<uint4*>(
-                a.summ + (((long long)b * a.H_kv + h) * a.max_pages + p) * 2LL * D);
-            out[l] = *reinterpret_cast<uint4*>(mn);
-            out[L + l] = *reinterpret_cast<uint4*>(mx);
+            s_mm[warp][l][0] = *reinterpret_cast<uint4*>(mn);
+            s_mm[warp][l][1] = *reinterpret_cast<uint4*>(mx);
         }
+    }
+    __syncthreads();
+    if (part == 0 && r0 == 0 && h < a.H_kv) {
+#pragma unroll
+        for (int q = 1; q < kPageParts; ++q) {
+            const uint4 n = s_mm[warp + q][l][0], x = s_mm[warp + q][l][1];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                mn[i] = __hmin2(mn[i], reinterpret_cast<const __half2*>(&n)[i]);
+                mx[i] = __hmax2(mx[i], reinterpret_cast<const __half2*>(&x)[i]);
+            }
+        }
+        uint4* out = reinterpret_cast<uint4*>(a.summ + (((long long)b * a.H_kv + h) * a.max_pages + p) * 2LL * D);
+        uint32_t lo[4], hi[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 x = __half22float2(mn[i]), y = __half22float2(mx[i]);
+            lo[i] = pack_bf16(x.x * k2, x.y * k2);
+            hi[i] = pack_bf16(y.x * k2, y.y * k2);
+        }
+        out[l] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        out[L + l] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     }
 }
 
 cudaError_t launch_kv4_append(const Kv4Args& a, cudaStream_t st) {
-    dim3 grid((unsigned)a.B, (unsigned)append_touched(a.T, a.ps, a.max_pages));
-    dim3 block(32 * (a.H_kv < 8 ? a.H_kv : 8));
+    dim3 grid((unsigned)((long long)a.B * ((a.H_kv + kPageHeads - 1) / kPageHeads)),
+              (unsigned)append_touched(a.T, a.ps, a.max_pages));
+    dim3 block(kKv4Threads);
     if (a.D == 128) return launch_pdl(kv4_append_kernel<128>, grid, block, 0, st, a);
     return launch_pdl(kv4_append_kernel<64>, grid, block, 0, st, a);
 }

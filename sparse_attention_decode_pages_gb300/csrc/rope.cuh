@@ -60,13 +60,11 @@ __device__ __forceinline__ void rope_weights(const uint16_t* w, const RopeLane& 
 }
 
 // Normalises (when `norm`) and rotates the lane's eight channels in place.  cs and
-// sn are the lane's four angles (read only when turned).  `any_norm` is the same for
-// the whole warp, whose rows may differ in `norm` (a query and a key row): the sum of
-// squares is exchanged by all of its lanes or by none.
+// sn are the lane's four angles (read only when turned).  By whole warps.
 template <int D>
-__device__ __forceinline__ void rope_row(float* x, bool any_norm, bool norm, const float* wt, float eps,
-                                         const RopeLane& r, int interleaved, const float4& cs, const float4& sn) {
-    if (any_norm) {
+__device__ __forceinline__ void rope_row(float* x, bool norm, const float* wt, float eps, const RopeLane& r,
+                                         int interleaved, const float4& cs, const float4& sn) {
+    if (norm) {
         float ss = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss = __fmaf_rn(x[i], x[i], ss);
@@ -74,7 +72,7 @@ __device__ __forceinline__ void rope_row(float* x, bool any_norm, bool norm, con
         for (int off = 1; off < D / 8; off <<= 1) ss = __fadd_rn(ss, __shfl_xor_sync(0xffffffffu, ss, off));
         const float inv = rsqrtf(__fmaf_rn(ss, 1.f / D, eps));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = norm ? __fmul_rn(__fmul_rn(x[i], inv), wt[i]) : x[i];
+        for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(__fmul_rn(x[i], inv), wt[i]);
     }
     if (r.turned) {
         const float c[4] = {cs.x, cs.y, cs.z, cs.w}, s[4] = {sn.x, sn.y, sn.z, sn.w};

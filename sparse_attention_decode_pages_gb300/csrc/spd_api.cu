@@ -833,8 +833,8 @@ SPD_API spd_status qk_norm_rope(int64_t rows, int32_t H_q, int32_t H_kv, int32_t
         return fail(SPD_ERR_INVALID_ARG, "NULL pointer argument");
     if (!aligned16(q) || !aligned16(k) || !aligned16(q_out) || !aligned16(k_out))
         return fail(SPD_ERR_INVALID_ARG, "q, k, q_out and k_out must be 16-byte aligned");
-    if (rows >= (1LL << 31) || rows * ((int64_t)a.H_q + a.H_kv) >= (1LL << 33))
-        return fail(SPD_ERR_UNSUPPORTED, "too many rows (%lld)", (long long)rows);
+    if (rows >= (1LL << 31) || a.H_q > 65536 || a.H_kv > 65536)
+        return fail(SPD_ERR_UNSUPPORTED, "too many rows or heads (rows=%lld H_q=%d H_kv=%d)", (long long)rows, a.H_q, a.H_kv);
     DevInfo* d = dev_info(&st);
     if (!d) return st;
     a.rows = rows;
@@ -887,7 +887,7 @@ SPD_API spd_status kv_append_rope(const spd_dims* dims, int32_t T, const spd_rop
     p.v = v;
     p.v_stride = v_stride;
     p.touched = 0;
-    if (append_rope_ctas(p) >= (1LL << 31)) return fail(SPD_ERR_UNSUPPORTED, "B * T * H_q too large");
+    if (append_rope_ctas(p) >= (1LL << 28) || p.rope.rows >= (1LL << 31)) return fail(SPD_ERR_UNSUPPORTED, "B * T * H_q too large");
     cudaError_t e = launch_append_rope(p, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? SPD_OK : cuda_fail(e, "kv_append_rope launch");
 }
@@ -911,7 +911,7 @@ static spd_status kv4_rows_setup(const spd_dims* dims, int32_t T, const uint8_t*
     if (!kv4 || !page_table || !seq_lens || !k || !v) return fail(SPD_ERR_INVALID_ARG, "NULL pointer argument");
     if (!aligned16(kv4) || !aligned16(k) || !aligned16(v))
         return fail(SPD_ERR_INVALID_ARG, "the cache and the rows must be 16-byte aligned");
-    if ((long long)dims->B * T * dims->H_kv >= (1LL << 33)) return fail(SPD_ERR_UNSUPPORTED, "B * T * H_kv too large");
+    if ((long long)dims->B * T * dims->H_kv >= (1LL << 31)) return fail(SPD_ERR_UNSUPPORTED, "B * T * H_kv must be < 2^31");
     DevInfo* d = dev_info(&st);
     if (!d) return st;
     a = Kv4Args{};
