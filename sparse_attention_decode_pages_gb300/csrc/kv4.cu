@@ -36,37 +36,42 @@ __device__ __forceinline__ float quotient(float a, float s, float r) {
 }
 
 // Quantises the lane's eight channels (its group's other eight are the neighbour
-// lane's): codes and the group's scale byte.  Quotients are rounded correctly, so the
-// codes are those of the exact quotients: a border between codes times a scale has
-// few enough bits that no rounded quotient crosses it, and a tie is met exactly.
-__device__ __forceinline__ uint32_t kv4_quantise(const uint4& u, float inv_exp2, uint32_t& scale_byte) {
-    const __nv_bfloat162* e = reinterpret_cast<const __nv_bfloat162*>(&u);
-    float x[8];
-    float amax = 0.f;
+// lane's): codes and the group's scale byte, exp2 = 2^exp.  Quotients are rounded
+// correctly, so the codes are those of the exact quotients: a border between codes times a
+// scale has few enough bits that no rounded quotient crosses it, and a tie is met exactly.
+__device__ __forceinline__ uint32_t kv4_quantise(const uint4& u, float exp2, float inv_exp2, uint32_t& scale_byte) {
+    uint32_t e[4] = {u.x, u.y, u.z, u.w};
+    // the largest magnitude, in bf16 pairs (exact); NaN where there is one
+    __nv_bfloat162 m = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&e[0]));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 v = __bfloat1622float2(e[i]);
-        x[2 * i] = v.x * inv_exp2;
-        x[2 * i + 1] = v.y * inv_exp2;
-        amax = fmaxf(amax, fmaxf(fabsf(x[2 * i]), fabsf(x[2 * i + 1])));  // NaN counts as 0
+    for (int i = 1; i < 4; ++i) m = __hmax2_nan(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&e[i])));
+    m = __hmax2_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    const float2 mf = __bfloat1622float2(m);
+    constexpr float kTop = 6.f * 448.f;  // the largest value a group can hold, over exp2
+    float amax = fmaxf(mf.x, mf.y) + 0.f * mf.x + 0.f * mf.y;  // NaN where either is NaN or infinite
+    if (!(amax * inv_exp2 <= kTop)) {
+        // rare: what lies past the largest value that can be held becomes it, NaN zero
+        amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float2 v = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&e[i]));
+            v.x = v.x == v.x ? fminf(fmaxf(v.x, -kTop * exp2), kTop * exp2) : 0.f;
+            v.y = v.y == v.y ? fminf(fmaxf(v.y, -kTop * exp2), kTop * exp2) : 0.f;
+            amax = fmaxf(amax, fmaxf(fabsf(v.x), fabsf(v.y)));
+            e[i] = pack_bf16(v.x, v.y);
+        }
+        // the neighbour came here too: the two have looked at the same m
+        amax = fmaxf(amax, __shfl_xor_sync(3u << (threadIdx.x & 30), amax, 1));
     }
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    constexpr float kTop = 6.f * 448.f;  // the largest value a group can hold
-    scale_byte = to_e4m3(quotient(fminf(amax, kTop), 6.f, 1.f / 6.f));
-    const float s = e4m3_value(scale_byte);
-    const float r = s > 0.f ? __frcp_rn(s) : 0.f;  // scale 0: the codes are zeros
+    scale_byte = to_e4m3(quotient(amax * inv_exp2, 6.f, 1.f / 6.f));
+    const float s1 = e4m3_value(scale_byte);
+    const float s = s1 * exp2, r = s1 > 0.f ? __frcp_rn(s1) * inv_exp2 : 0.f;  // scale 0: the codes are zeros
     uint32_t codes = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        float y[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const float v = x[2 * i + j];
-            // an infinity as the largest value (of its sign), NaN as 0; the sign of zeros stays
-            const float c = v == v ? fminf(fmaxf(v, -kTop), kTop) : 0.f;
-            y[j] = copysignf(quotient(c, s, r), c);
-        }
-        codes |= to_e2m1x2(y[0], y[1]) << (8 * i);
+        const float lo = __uint_as_float(e[i] << 16), hi = __uint_as_float(e[i] & 0xffff0000u);
+        // (the sign of zeros stays)
+        codes |= to_e2m1x2(copysignf(quotient(lo, s, r), lo), copysignf(quotient(hi, s, r), hi)) << (8 * i);
     }
     return codes;
 }
@@ -103,7 +108,7 @@ __global__ void __launch_bounds__(kKv4Threads, 4) kv4_append_kernel(const Kv4Arg
     }
     const int r0 = lane / L, l = lane % L;
     const int half = kv4_half_bytes(a.ps, D), codes_bytes = kv4_codes_bytes(a.ps, D);
-    const float k2 = pow2f(a.k_exp), ik2 = pow2f(-a.k_exp), iv2 = pow2f(-a.v_exp);
+    const float k2 = pow2f(a.k_exp), ik2 = pow2f(-a.k_exp), v2 = pow2f(a.v_exp), iv2 = pow2f(-a.v_exp);
     const __half2 pinf = __floats2half2_rn(__int_as_float(0x7f800000), __int_as_float(0x7f800000));
     const __half2 ninf = __floats2half2_rn(__int_as_float(0xff800000), __int_as_float(0xff800000));
     const int nold = min(valid, max(0, first - p * a.ps));
@@ -158,8 +163,8 @@ __global__ void __launch_bounds__(kKv4Threads, 4) kv4_append_kernel(const Kv4Arg
                 const int t = tb + u * STEP + r0;
                 if (tb + u * STEP >= valid) break;
                 uint32_t ks, vs;
-                const uint32_t kc = kv4_quantise(k[u], ik2, ks);
-                const uint32_t vc = kv4_quantise(v[u], iv2, vs);
+                const uint32_t kc = kv4_quantise(k[u], k2, ik2, ks);
+                const uint32_t vc = kv4_quantise(v[u], v2, iv2, vs);
                 if (t < valid) {
                     *reinterpret_cast<uint32_t*>(kt + t * (D / 2) + 4 * l) = kc;
                     *reinterpret_cast<uint32_t*>(vt + t * (D / 2) + 4 * l) = vc;
@@ -216,45 +221,62 @@ cudaError_t launch_kv4_append(const Kv4Args& a, cudaStream_t st) {
     return launch_pdl(kv4_append_kernel<64>, grid, block, 0, st, a);
 }
 
-// D / 8 lanes per (token, KV head) row, the keys' and the values' eight channels each.
+// A warp takes one token's KV heads, D / 8 lanes a head and kReadTurns heads a lane group
+// whose loads are in flight together; its group of heads is blockIdx.y.
+constexpr int kReadTurns = 4;
+
 template <int D>
 __global__ void __launch_bounds__(kKv4Threads) kv4_read_kernel(const Kv4Args a) {
-    constexpr int L = D / 8;
+    constexpr int L = D / 8, HT = 32 / L;
     pdl_wait();
     pdl_trigger();
-    const long long unit = (long long)blockIdx.x * (kKv4Threads / L) + threadIdx.x / L;
-    const int l = threadIdx.x % L;
-    const long long row = unit / a.H_kv;  // b * T + t
-    const int h = (int)(unit - row * a.H_kv);
-    const int b = (int)(row / a.T), t = (int)(row - (long long)b * a.T);
-    if (b >= a.B) return;
-    const int len = a.seq_lens[b];
-    uint4 k = make_uint4(0u, 0u, 0u, 0u), v = k;
+    const int lane = threadIdx.x & 31, l = lane % L, h0 = blockIdx.y * (HT * kReadTurns) + lane / L;
+    const unsigned row = blockIdx.x * (kKv4Threads / 32) + (threadIdx.x >> 5);  // b * T + t
+    const unsigned b = row / (unsigned)a.T;
+    if (b >= (unsigned)a.B) return;
+    const int t = (int)(row - b * a.T), len = a.seq_lens[b];
+    long long phys = -1;
+    int slot = 0;
     if (len < a.T || len > (long long)a.max_pages * a.ps) {
-        if (l == 0) raise_status(a.status, SPD_DEV_BAD_LEN);
+        if (lane == 0) raise_status(a.status, SPD_DEV_BAD_LEN);
     } else {
-        const int pos = len - a.T + t, p = pos / a.ps, slot = pos % a.ps;
-        const long long phys = a.page_table[(long long)b * a.max_pages + p];
+        const unsigned pos = len - a.T + t, p = pos / (unsigned)a.ps;
+        slot = (int)(pos - p * a.ps);
+        phys = a.page_table[(long long)b * a.max_pages + p];
         if (phys < 0 || phys >= a.num_phys) {
-            if (l == 0) raise_status(a.status, SPD_DEV_BAD_PAGE);
-        } else {
-            const int half = kv4_half_bytes(a.ps, D), codes_bytes = kv4_codes_bytes(a.ps, D);
-            const uint8_t* kt = a.kv4 + (phys * a.H_kv + h) * (2LL * half);
-            const uint8_t* vt = kt + half;
-            const int co = slot * (D / 2) + 4 * l, so = codes_bytes + slot * (D / 16) + l / 2;
-            k = kv4_values(*reinterpret_cast<const uint32_t*>(kt + co), kt[so], pow2f(a.k_exp));
-            v = kv4_values(*reinterpret_cast<const uint32_t*>(vt + co), vt[so], pow2f(a.v_exp));
+            if (lane == 0) raise_status(a.status, SPD_DEV_BAD_PAGE);
+            phys = -1;
         }
     }
-    const long long at = (row * a.H_kv + h) * L + l;
-    reinterpret_cast<uint4*>(a.k_out)[at] = k;
-    reinterpret_cast<uint4*>(a.v_out)[at] = v;
+    const int half = kv4_half_bytes(a.ps, D), codes_bytes = kv4_codes_bytes(a.ps, D);
+    const uint8_t* tile = a.kv4 + (phys < 0 ? 0 : phys * a.H_kv + h0) * (2LL * half);
+    const int co = slot * (D / 2) + 4 * l, so = codes_bytes + slot * (D / 16) + l / 2;
+    uint32_t kc[kReadTurns], ks[kReadTurns], vc[kReadTurns], vs[kReadTurns];
+#pragma unroll
+    for (int i = 0; i < kReadTurns; ++i) {
+        kc[i] = ks[i] = vc[i] = vs[i] = 0u;
+        if (phys >= 0 && h0 + i * HT < a.H_kv) {
+            const uint8_t* kt = tile + i * HT * (2LL * half);
+            kc[i] = *reinterpret_cast<const uint32_t*>(kt + co);
+            ks[i] = kt[so];
+            vc[i] = *reinterpret_cast<const uint32_t*>(kt + half + co);
+            vs[i] = kt[half + so];
+        }
+    }
+    const float k2 = pow2f(a.k_exp), v2 = pow2f(a.v_exp);
+    const long long at = ((long long)row * a.H_kv + h0) * L + l;
+#pragma unroll
+    for (int i = 0; i < kReadTurns; ++i)
+        if (h0 + i * HT < a.H_kv) {
+            reinterpret_cast<uint4*>(a.k_out)[at + i * HT * L] = kv4_values(kc[i], ks[i], k2);
+            reinterpret_cast<uint4*>(a.v_out)[at + i * HT * L] = kv4_values(vc[i], vs[i], v2);
+        }
 }
 
 cudaError_t launch_kv4_read(const Kv4Args& a, cudaStream_t st) {
-    const long long units = (long long)a.B * a.T * a.H_kv;
-    const int upb = kKv4Threads / (a.D / 8);
-    dim3 grid((unsigned)((units + upb - 1) / upb)), block(kKv4Threads);
+    const long long rows = (long long)a.B * a.T;
+    const int warps = kKv4Threads / 32, heads = 32 / (a.D / 8) * kReadTurns;
+    dim3 grid((unsigned)((rows + warps - 1) / warps), (unsigned)((a.H_kv + heads - 1) / heads)), block(kKv4Threads);
     if (a.D == 128) return launch_pdl(kv4_read_kernel<128>, grid, block, 0, st, a);
     return launch_pdl(kv4_read_kernel<64>, grid, block, 0, st, a);
 }
