@@ -1,0 +1,580 @@
+// attn4_verify.cu -- dense causal attention over the 4-bit paged cache for 9 to 64 query
+// rows of a KV head (the T drafted positions times the grouped heads).
+//
+// A unit is a run of at most pages_per_split pages of one (sequence, KV head) row; it
+// holds all R = T * G query rows of the KV head.  A CTA of eight warps takes one unit, 128
+// tokens (a step: eight 16-token chunks) at a time from a ring that bulk copies fill, and
+// computes on the 5th-generation tensor cores (tcgen05, fp16 in, fp32 out)
+//
+//   S^T = K Q^T        M = 128 tokens, N = query rows (16, 32 or 64), K = channels
+//   O^T += V^T P^T     M = 128 channels, N = query rows, K = 128 tokens
+//
+// with S^T and O^T in tensor memory.  code * scale is exact in fp16, so the products
+// are those of the values the cache stands for.  What the threads do is convert:
+//   K: warp w converts chunk w in the layout of an mma fragment (lane (g, c) =
+//      (lane / 4, lane % 4): tokens g and g + 8, channels c * D / 4 ... -- 16 contiguous
+//      bytes a token, free of bank conflicts) and stores them to tensor memory, as the A
+//      operand of the first product.  The contraction's order of channels that this gives
+//      (position 16 i + 4 c + j is channel c * D / 4 + 4 i + j) is given to Q as well.
+//   V: rows of a token's channels to shared memory, as the M-major A operand of the second.
+//   P: a thread has one token (row token_row of its chunk) and half of the query rows: its
+//      weights, in fp16, into the token's row of the N-major B operand.
+// A ninth warp issues the copies and, one elected lane, the products, which run while the
+// others convert: S = K Q^T behind the conversion of V, and O += V^T P^T behind that of the
+// next step's K.  (mma.sync blocks its SM quarter's issue for 8 cycles each: the same
+// work took 502 us with it where this takes _VERIFY_.)
+//
+// Queries are scaled by a power of two into fp16's range (the factor goes into the
+// logits' scale).  Online softmax in fp32 in base 2; a column's reference moves only when a
+// logit exceeds it by kHead4 (attn4.cuh).  One barrier of the converting warps a step carries
+// the vote on the references.
+//
+// 64 sequences of 8K-16K tokens, 7 positions, 32 / 8 heads of 128: _VERIFY_, _VERIFYGB_ of keys
+// and values.  Bound by the handshake between conversions and products (a step of 128 tokens
+// takes ~1.45 us with two CTAs on an SM; without any conversion, softmax or product it
+// still took 1.2) and a unit's start and end (~8 us).
+#include <atomic>
+
+#include "attn4.cuh"
+#include "tcgen05.cuh"
+
+namespace spd {
+
+namespace {
+
+// CTAs on an SM (registers; shared memory and tensor memory hold them).  The driver's
+// occupancy query answers 1 for any kernel that allocates tensor memory.
+constexpr int kVerify4Occ = 2;
+
+template <int D, int N>
+struct Verify4Cfg {
+    static constexpr int WARPS = 8, THREADS = 32 * (WARPS + 1);  // converting warps, and the issuing one
+    static constexpr int NH = N / 2;                      // query rows of a thread
+    static constexpr int CHUNKS = 8;                      // of a step
+    static constexpr int CHUNK = kv4_tile_bytes(16, D);   // bytes of 16 tokens' keys and values
+    static constexpr int STEP = CHUNKS * CHUNK;
+    static constexpr int STAGES = N == 64 ? 2 : 3;        // steps in the ring
+    // V^T: 64-channel blocks of 128 rows (tokens) of 128 bytes, 128-byte swizzle
+    static constexpr int VBLOCK = 128 * 128;
+    static constexpr int OFF_V = 0;
+    // Q: 64-position blocks of N rows of 128 bytes, 128-byte swizzle
+    static constexpr int OFF_Q = OFF_V + D / 64 * VBLOCK;
+    // P: 128 rows (tokens) of N fp16, swizzled over the row's 32, 64 or 128 bytes
+    static constexpr int OFF_P = OFF_Q + N * D * 2;
+    static constexpr int OFF_RING = OFF_P + 128 * N * 2;
+    static constexpr int OFF_FR = OFF_RING + STAGES * STEP;  // float2 [N]: logit scale and -reference of each row
+    static constexpr int OFF_RED = OFF_FR + N * 8;           // float [4][N]: maxima, then sums
+    static constexpr int OFF_CORR = OFF_RED + 4 * N * 4;  // float [N]
+    static constexpr int OFF_OUT = OFF_CORR + N * 4;          // long long [N]: output rows
+    static constexpr int OFF_BAR = OFF_OUT + N * 8;           // uint64 [STAGES] and four more
+    static constexpr int OFF_META = OFF_BAR + (STAGES + 4) * 8;  // int [STAGES][CHUNKS]: first positions or -1
+    static constexpr int BODY = OFF_META + STAGES * CHUNKS * 4;
+    // tensor memory: K, S, O
+    static constexpr int COL_S = D / 2, COL_O = COL_S + N;
+    static constexpr int COLUMNS = COL_O + N <= 128 ? 128 : 256;
+    // at most 512 / COLUMNS CTAs fit on an SM (227 KB), so that none waits for columns
+    static constexpr int LEAST = 227 * 1024 / (512 / COLUMNS + 1);
+    static constexpr int SMEM = 1024 + (BODY > LEAST ? BODY : LEAST);
+    static constexpr int P_ROW = N * 2;
+    static constexpr uint64_t P_SWIZZLE = N == 16 ? kSwizzle32 : N == 32 ? kSwizzle64 : kSwizzle128;
+    static_assert(kVerify4Occ * (SMEM + 2048) <= 228 * 1024 && kVerify4Occ * COLUMNS <= 512, "they fit on an SM");
+    static_assert(STAGES <= 4, "the first steps are resolved at once");
+};
+
+// Tensor-memory lane of S (and row of V and P) of token i of chunk q: a warp reaches the 32
+// lanes of its number modulo 4, so warp q's chunk lies in those.
+__device__ __forceinline__ int token_row(int q, int i) { return 32 * (q & 3) + 16 * (q >> 2) + i; }
+
+__device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void load_columns(uint32_t taddr, uint32_t (&v)[N]) {
+    __syncwarp();
+    tmem_ld(taddr, v);
+    tmem_wait_ld();
+}
+
+template <int N>
+__device__ __forceinline__ void store_columns(uint32_t taddr, const uint32_t (&v)[N]) {
+    __syncwarp();
+    tmem_st(taddr, v);
+    tmem_wait_st();
+}
+
+// A place in a ring of S slots: the slot and the parity of its current round.
+template <int S>
+struct RingPos {
+    int slot = 0;
+    uint32_t parity = 0;
+    __device__ __forceinline__ void advance() {
+        if (++slot == S) {
+            slot = 0;
+            parity ^= 1u;
+        }
+    }
+};
+
+// Barriers of the T converting threads: a plain one, and one that says whether any of them
+// gave a true value.
+template <int T>
+__device__ __forceinline__ void converters_sync() {
+    asm volatile("barrier.cta.sync 1, %0;" ::"n"(T) : "memory");
+}
+template <int T>
+__device__ __forceinline__ bool converters_or(bool x) {
+    uint32_t any;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(any)
+        : "r"(x ? 1u : 0u), "n"(T)
+        : "memory");
+    return any != 0;
+}
+
+template <int D, int N>
+__global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify4_kernel(const Attn4Args a) {
+    using C = Verify4Cfg<D, N>;
+    constexpr int STAGES = C::STAGES, WARPS = C::WARPS, CHUNKS = C::CHUNKS, NH = C::NH;
+    constexpr int CODES = kv4_codes_bytes(16, D), HALF = kv4_half_bytes(16, D);  // of a chunk
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ int s_last, s_late;
+    __shared__ uint32_t s_tmem;
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    float2* s_fr = reinterpret_cast<float2*>(smem + C::OFF_FR);
+    float* s_red = reinterpret_cast<float*>(smem + C::OFF_RED);
+    float* s_corr = reinterpret_cast<float*>(smem + C::OFF_CORR);
+    long long* s_out = reinterpret_cast<long long*>(smem + C::OFF_OUT);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+    uint64_t* k_ready = full + STAGES;  // K of a step is in tensor memory
+    uint64_t* p_ready = k_ready + 1;    // V and P are in shared memory, and the step's codes are read
+    uint64_t* s_done = p_ready + 1;     // S is there
+    uint64_t* o_done = s_done + 1;      // O is there; V and P may be overwritten
+    int* meta = reinterpret_cast<int*>(smem + C::OFF_META);
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    const int g = lane >> 2, c = lane & 3;
+    const int G = a.H_q / a.H_kv, R = a.T * G;
+    const float NEG_INF = __int_as_float(0xff800000);
+
+    const int row = blockIdx.x / a.num_splits, split = blockIdx.x % a.num_splits;
+    const int b = row / a.H_kv, h = row - b * a.H_kv;
+    auto out_index = [&](int r) -> long long {
+        const int t = r / G;
+        return ((long long)b * a.T + t) * a.H_q + h * G + (r - t * G);
+    };
+    if (tid == 0) {
+#pragma unroll
+        for (int i = 0; i < STAGES + 4; ++i) mbar_init(full + i, i == STAGES ? WARPS : 1);
+        mbar_fence_init();
+        s_late = 0;
+    }
+    pdl_wait();
+    pdl_trigger();
+
+    const int start = split * a.pages_per_split;
+    const int cpp = a.ps >> 4;  // chunks per page
+    // the issuing warp's lane i resolves chunk 32 j + i of the unit, for four steps at a time
+    int lp_next = -1, ph_next = -1;  // the next four steps' logical pages and page-table entries, unchecked
+    const int len = a.seq_lens[b];
+    int P = seq_pages(len, a.ps, a.max_pages);
+    if (P < 0) {
+        if (tid == 0) raise_status(a.status, SPD_DEV_BAD_LEN);
+        P = 0;
+    }
+    const int n_items = P;
+    const int count = min(a.pages_per_split, n_items - start);
+    if (count <= 0) {
+        if (split == 0)
+            for (int i = tid; i < R * (D / 8); i += C::THREADS) {
+                const long long oi = out_index(i / (D / 8));
+                *reinterpret_cast<uint4*>(a.o + oi * D + (i % (D / 8)) * 8) = make_uint4(0, 0, 0, 0);
+                if (i % (D / 8) == 0 && a.lse) a.lse[oi] = NEG_INF;
+            }
+        return;
+    }
+    const int nsplit = (n_items + a.pages_per_split - 1) / a.pages_per_split;
+    const int chunks = count * cpp;
+    const int steps = (chunks + CHUNKS - 1) / CHUNKS;
+
+    auto next_pages = [&](int j) {
+        const int ci = 32 * j + lane;
+        lp_next = -1;
+        if (ci < chunks) lp_next = start + ci / cpp;
+    };
+    auto next_entries = [&]() {
+        ph_next = lp_next >= 0 ? a.page_table[(long long)b * a.max_pages + lp_next] : -1;
+    };
+    int ph_cur = -1, pos_cur = -1;  // physical page and first position (-1: nothing to read)
+    auto take_next = [&](int j) {
+        const int ci = 32 * j + lane;
+        ph_cur = pos_cur = -1;
+        if (ci < chunks) {
+            if (ph_next < 0 || ph_next >= a.num_phys) {
+                raise_status(a.status, SPD_DEV_BAD_PAGE);
+            } else {
+                const int at = lp_next * a.ps + (ci - ci / cpp * cpp) * 16;
+                if (at < len) {
+                    ph_cur = ph_next;
+                    pos_cur = at;
+                }
+            }
+        }
+    };
+    // issues step k's copies: lane 4 q + i copies piece i of chunk q (keys' codes and
+    // scales, values' codes and scales), or lane 4 q the whole chunk where a page is one
+    const int codes = kv4_codes_bytes(a.ps, D), half = kv4_half_bytes(a.ps, D);
+    auto issue = [&](int k) {
+        const int slot = k % STAGES, from = (k & 3) * 8;
+        const int phys = __shfl_sync(0xffffffffu, ph_cur, from + (lane >> 2));
+        const int pos = __shfl_sync(0xffffffffu, pos_cur, from + (lane >> 2));
+        const unsigned there = __ballot_sync(0xffffffffu, pos >= 0 && (lane & 3) == 0);
+        if ((lane & 3) == 0) meta[slot * CHUNKS + (lane >> 2)] = pos;
+        __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(full + slot, __popc(there) * C::CHUNK);
+        __syncwarp();
+        if (pos >= 0) {
+            const int i = lane & 3;
+            const uint8_t* tile = a.kv4 + ((long long)phys * a.H_kv + h) * (2LL * half);
+            uint8_t* dst = smem + C::OFF_RING + slot * C::STEP + (lane >> 2) * C::CHUNK;
+            if (a.ps == 16) {
+                if (i == 0) bulk_load(dst, tile, C::CHUNK, full + slot);
+            } else {
+                const int t0 = pos & (a.ps - 1);
+                const uint8_t* src = tile + (i >> 1) * half + (i & 1 ? codes + t0 * (D / 16) : t0 * (D / 2));
+                bulk_load(dst + (i >> 1) * HALF + (i & 1) * CODES, src, i & 1 ? HALF - CODES : CODES, full + slot);
+            }
+        }
+    };
+    __syncthreads();  // the barriers are initialised
+    if (warp == WARPS) {
+        next_pages(0);
+        next_entries();
+        take_next(0);
+        for (int k = 0; k < min(STAGES, steps); ++k) issue(k);
+        if (steps > 4) next_pages(1);
+        tmem_alloc(&s_tmem, C::COLUMNS);
+    }
+
+    // the query rows in fp16, each scaled by 2^-e so that its largest channel lies in [1, 2);
+    // channel qc * D / 4 + 4 i + j at position 16 i + 4 qc + j
+    for (int r = warp; r < N; r += WARPS + 1) {
+        float2 x[D / 64];
+        float amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+            x[i] = make_float2(0.f, 0.f);
+            if (r < R)
+                x[i] = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(a.q + out_index(r) * D + 2 * lane + 64 * i));
+            amax = fmaxf(amax, fmaxf(fabsf(x[i].x), fabsf(x[i].y)));
+        }
+        const int e = query_exponent(amax);
+        const float down = pow2f(-e);
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+            const int ch = 2 * lane + 64 * i, qc = ch / (D / 4), in = ch % (D / 4);
+            const int at = 16 * (in >> 2) + 4 * qc + (in & 3);
+            uint8_t* block = smem + C::OFF_Q + (at >> 6) * (N * 128);
+            *reinterpret_cast<uint32_t*>(block + r * 128 + (((at & 63) * 2) ^ ((r & 7) << 4))) = pack_f16(x[i].x * down, x[i].y * down);
+        }
+        if (lane == 0) {
+            s_fr[r] = make_float2(a.scale_log2 * pow2f(e), -kLow4);
+            s_out[r] = r < R ? out_index(r) : 0;
+        }
+    }
+    async_proxy_fence();
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tmem = s_tmem, tm_s = tmem + C::COL_S, tm_o = tmem + C::COL_O;
+    const uint32_t my_lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const int r0 = (warp >> 2) * NH;                 // this thread's query rows: r0 ... r0 + NH - 1
+    const int my_row = (warp & 3) * 32 + lane;       // and its token's row
+    const int my_chunk = (warp & 3) + 4 * (lane >> 4);
+    const uint32_t v_smem = smem_u32(smem + C::OFF_V), q_smem = smem_u32(smem + C::OFF_Q), p_smem = smem_u32(smem + C::OFF_P);
+    constexpr uint32_t kIdescS = umma_idesc_f16(128, N, false, false);
+    constexpr uint32_t kIdescO = umma_idesc_f16(128, N, true, true);
+    // this thread's row of P: 16-byte pieces in swizzled order
+    const int p_xor = N == 16 ? my_row >> 2 & 1 : N == 32 ? my_row >> 1 & 3 : my_row & 7;
+
+    if (warp == WARPS) {
+        // ============================================================ copies and products
+        for (int k = 0; k < steps; ++k) {
+            if (!__all_sync(0xffffffffu, mbar_sleep_bounded(k_ready, (uint32_t)k & 1u, a.status, a.wait_ns))) break;
+            tmem_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i)
+                    umma_f16_ts(tm_s, tmem + 8 * i, umma_desc(q_smem + (i >> 2) * (N * 128) + (i & 3) * 32, 0, 1024, kSwizzle128),
+                                kIdescS, i > 0);
+                umma_commit(s_done);
+            }
+            __syncwarp();
+            const int kn = k + STAGES;  // the next step into this one's slot
+            if (kn < steps && (kn & 3) == 0) {
+                next_entries();
+                take_next(kn >> 2);
+                next_pages((kn >> 2) + 1);
+            }
+            if (!__all_sync(0xffffffffu, mbar_sleep_bounded(p_ready, (uint32_t)k & 1u, a.status, a.wait_ns))) break;
+            tmem_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    umma_f16_ss(tm_o, umma_desc(v_smem + i * 2048, D == 128 ? C::VBLOCK : 0, 1024, kSwizzle128),
+                                umma_desc(p_smem + i * 16 * C::P_ROW, 0, 8 * C::P_ROW, C::P_SWIZZLE), kIdescO, k > 0 || i > 0);
+                umma_commit(o_done);
+            }
+            __syncwarp();
+            if (kn < steps) issue(kn);
+        }
+    } else {
+    // ================================================================ conversions and softmax
+    // V of this warp's chunk: this lane's token (and the one 8 behind) and 32 channels; the eight
+    // lanes that store together cover every bank
+    const int piece = D == 128 ? (lane >> 2 & 1) + 2 * (lane >> 3 & 1) : lane >> 2 & 1;
+    const int v_token = D == 128 ? (lane & 3) + 4 * (lane >> 4) : (lane & 3) + 4 * (lane >> 3);
+    const int v_src = warp * C::CHUNK + HALF + v_token * (D / 2) + piece * 16;
+    const int v_scale_src = warp * C::CHUNK + HALF + CODES + v_token * (D / 16) + piece * 2;
+    const uint32_t v_dst = v_smem + (piece >> 1) * C::VBLOCK + token_row(warp, v_token) * 128 +
+                           ((((piece & 1) * 4) ^ (v_token & 7)) << 4);
+    const uint32_t p_dst = p_smem + my_row * C::P_ROW + (((r0 / 8) ^ p_xor) << 4);
+
+    float l[NH];  // sums of this thread's weights
+#pragma unroll
+    for (int r = 0; r < NH; ++r) l[r] = 0.f;
+    bool gone = false;  // a wait ran out
+    int done = 0;       // steps whose second product was issued
+    RingPos<STAGES> ring;
+
+    for (int k = 0; k < steps; ++k) {
+        const int slot = ring.slot;
+        const uint8_t* stage = smem + C::OFF_RING + slot * C::STEP;
+        bool ok = mbar_sleep_bounded(full + slot, ring.parity, a.status, a.wait_ns);
+        ring.advance();
+
+        // K: this warp's chunk to tensor memory (one that is not there: whatever the ring holds;
+        // its tokens are hidden)
+        {
+            const uint8_t* kt = stage + warp * C::CHUNK;
+            uint32_t f[D / 4];  // [column group][row g: two columns, row g + 8: two]
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int t = g + 8 * j;
+                uint32_t w[D / 32], s;
+                if constexpr (D == 128) {
+                    const uint4 x = *reinterpret_cast<const uint4*>(kt + t * 64 + c * 16);
+                    w[0] = x.x;
+                    w[1] = x.y;
+                    w[D / 32 - 2] = x.z;
+                    w[D / 32 - 1] = x.w;
+                    s = e4m3x2_to_f16(*reinterpret_cast<const uint16_t*>(kt + CODES + t * 8 + 2 * c));
+                } else {
+                    const uint2 x = *reinterpret_cast<const uint2*>(kt + t * 32 + c * 8);
+                    w[0] = x.x;
+                    w[1] = x.y;
+                    s = e4m3x2_to_f16(kt[CODES + t * 4 + c]);
+                }
+#pragma unroll
+                for (int x = 0; x < D / 32; ++x) {
+                    uint32_t v[4];
+                    e2m1x8_to_f16(w[x], v);
+                    const uint32_t s2 = __byte_perm(s, 0, x < 2 ? 0x1010 : 0x3232);
+                    f[8 * x + 2 * j] = hmul2(v[0], s2);
+                    f[8 * x + 2 * j + 1] = hmul2(v[1], s2);
+                    f[8 * x + 4 + 2 * j] = hmul2(v[2], s2);
+                    f[8 * x + 4 + 2 * j + 1] = hmul2(v[3], s2);
+                }
+            }
+            __syncwarp();
+            tmem_st_frag(tmem + ((uint32_t)token_row(warp, 0) << 16), f);
+        }
+        tmem_wait_st();
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(k_ready);
+
+        // V: this warp's chunk to shared memory, 32 channels of a token at a time; the eight lanes
+        // that store together cover every bank
+        if (k > 0) ok &= mbar_sleep_bounded(o_done, (uint32_t)(k - 1) & 1u, a.status, a.wait_ns);
+        const int warp_first = meta[slot * CHUNKS + warp];
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+            const uint8_t* vt = stage + v_src + i * (8 * (D / 2));
+            const uint4 x = *reinterpret_cast<const uint4*>(vt);
+            uint32_t two = *reinterpret_cast<const uint16_t*>(stage + v_scale_src + i * (8 * (D / 16)));
+            if (warp_first < 0 || warp_first + v_token + 8 * i >= len) two = 0u;  // no token: its bytes may be anything, its scale counts as 0
+            const uint32_t s = e4m3x2_to_f16(two);
+            const uint32_t s_lo = __byte_perm(s, 0, 0x1010), s_hi = __byte_perm(s, 0, 0x3232);
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t v[4];
+                e2m1x8_to_f16(w[j], v);
+                const uint32_t s2 = j < 2 ? s_lo : s_hi;
+                st_shared16((v_dst ^ (j << 4)) + i * 1024, hmul2(v[0], s2), hmul2(v[1], s2), hmul2(v[2], s2), hmul2(v[3], s2));
+            }
+        }
+
+        // softmax of this thread's token, for its query rows
+        ok &= mbar_sleep_bounded(s_done, (uint32_t)k & 1u, a.status, a.wait_ns);
+        tmem_fence_after();
+        const int chunk_first = meta[slot * CHUNKS + my_chunk];
+        const int pos = chunk_first < 0 ? 0x7fffffff : chunk_first + (lane & 15);
+        const bool all = __all_sync(0xffffffffu, pos <= len - a.T);  // every row sees every token of the warp
+        auto last_seen = [&](int r) { return r < R ? len - a.T + r / G : len - 1; };
+        float p[NH];
+        auto weights = [&](const uint32_t (&s)[NH]) {
+#pragma unroll
+            for (int r = 0; r < NH; r += 2) {
+                const float4 fr = *reinterpret_cast<const float4*>(s_fr + r0 + r);
+                p[r] = fast_exp2(fmaf(__uint_as_float(s[r]), fr.x, fr.y));
+                p[r + 1] = fast_exp2(fmaf(__uint_as_float(s[r + 1]), fr.z, fr.w));
+            }
+            if (!all) {
+#pragma unroll
+                for (int r = 0; r < NH; ++r)
+                    if (pos > last_seen(r0 + r)) p[r] = 0.f;
+            }
+        };
+        auto put_p = [&]() {
+#pragma unroll
+            for (int i = 0; i < NH / 8; ++i)
+                st_shared16(p_dst ^ (i << 4), pack_f16(p[8 * i], p[8 * i + 1]), pack_f16(p[8 * i + 2], p[8 * i + 3]),
+                            pack_f16(p[8 * i + 4], p[8 * i + 5]), pack_f16(p[8 * i + 6], p[8 * i + 7]));
+        };
+        float top = 0.f;
+        {
+            uint32_t s[NH];
+            load_columns<NH>(tm_s + r0 + my_lanes, s);
+            weights(s);
+        }
+#pragma unroll
+        for (int r = 0; r < NH; ++r) top = fmaxf(top, p[r]);
+        put_p();
+        async_proxy_fence();
+        tmem_fence_before();
+        if (!ok) s_late = 1;
+        const bool move = converters_or<32 * WARPS>(top > kMost4);
+        if (s_late) {
+            gone = true;
+            break;
+        }
+        if (move) {
+            // the largest logit of each row among this step's tokens
+            uint32_t s[NH];
+            load_columns<NH>(tm_s + r0 + my_lanes, s);
+#pragma unroll
+            for (int r = 0; r < NH; ++r) {
+                const float z = pos > last_seen(r0 + r) ? NEG_INF : __uint_as_float(s[r]) * s_fr[r0 + r].x;
+                const unsigned top_key = __reduce_max_sync(0xffffffffu, z == z ? float_key(z) : 0u);
+                if (lane == 0) s_red[(warp & 3) * N + r0 + r] = __uint_as_float(top_key & 0x80000000u ? top_key & 0x7fffffffu : ~top_key);
+            }
+            converters_sync<32 * WARPS>();
+            if (tid < N) {
+                float x = NEG_INF;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x = fmaxf(x, s_red[i * N + tid]);
+                const float old = -s_fr[tid].y, now = fmaxf(old, x - kBias4);
+                s_corr[tid] = fast_exp2(old - now);
+                s_fr[tid].y = -now;
+            }
+            converters_sync<32 * WARPS>();
+            if (k > 0) {
+                uint32_t o[NH];
+                load_columns<NH>(tm_o + r0 + my_lanes, o);
+#pragma unroll
+                for (int r = 0; r < NH; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * s_corr[r0 + r]);
+                store_columns<NH>(tm_o + r0 + my_lanes, o);
+            }
+#pragma unroll
+            for (int r = 0; r < NH; ++r) l[r] *= s_corr[r0 + r];
+            weights(s);
+            put_p();
+            async_proxy_fence();
+            tmem_fence_before();
+            converters_sync<32 * WARPS>();
+        }
+        if (tid == 0) mbar_arrive(p_ready);
+        done = k + 1;
+#pragma unroll
+        for (int r = 0; r < NH; ++r) l[r] += p[r];
+    }
+
+    // the copies in flight land, and the products end, before their memory is given back
+    if (gone)
+        for (int j = done; j < min(done + STAGES, steps); ++j)
+            mbar_sleep_bounded(full + j % STAGES, (uint32_t)(j / STAGES) & 1u, a.status, a.wait_ns);
+    if (done > 0) mbar_sleep_bounded(o_done, (uint32_t)(done - 1) & 1u, a.status, a.wait_ns);
+    tmem_fence_after();
+    uint32_t o[NH];
+    load_columns<NH>(tm_o + r0 + my_lanes, o);  // channel my_row of this thread's query rows
+#pragma unroll
+    for (int r = 0; r < NH; ++r) {
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], off);
+        if (lane == 0) s_red[(warp & 3) * N + r0 + r] = l[r];
+    }
+    tmem_fence_before();
+    converters_sync<32 * WARPS>();
+    if (my_row < D) {
+#pragma unroll
+        for (int i = 0; i < NH; ++i) {
+            const int r = r0 + i;
+            if (r >= R) break;
+            const float sum = s_red[r] + s_red[N + r] + s_red[2 * N + r] + s_red[3 * N + r];
+            const float x = sum == 0.f ? 0.f : __uint_as_float(o[i]) * (a.v_scale / sum);
+            const float lse = sum == 0.f ? NEG_INF : (log2f(sum) - s_fr[r].y) * kLn2;
+            if (nsplit == 1) {
+                reinterpret_cast<bf16*>(a.o)[s_out[r] * D + my_row] = __float2bfloat16_rn(x);
+                if (my_row == 0 && a.lse) a.lse[s_out[r]] = lse;
+            } else {
+                const long long at = ((long long)row * a.num_splits + split) * R + r;
+                a.part_o[at * D + my_row] = x;
+                if (my_row == 0) a.part_lse[at] = lse;
+            }
+        }
+    }
+    }
+    __syncthreads();
+    tmem_fence_after();
+    if (warp == WARPS) tmem_free(tmem, C::COLUMNS);
+    if (nsplit == 1 || !last_split(a, row, nsplit, &s_last)) return;
+    join_splits<D, C::THREADS>(a, row, nsplit, R, out_index);
+}
+
+typedef void (*Verify4Fn)(const Attn4Args);
+
+template <int D>
+void pick(int R, Verify4Fn* fn, int* smem) {
+    *fn = R <= 16 ? verify4_kernel<D, 16> : R <= 32 ? verify4_kernel<D, 32> : verify4_kernel<D, 64>;
+    *smem = R <= 16 ? Verify4Cfg<D, 16>::SMEM : R <= 32 ? Verify4Cfg<D, 32>::SMEM : Verify4Cfg<D, 64>::SMEM;
+}
+
+}  // namespace
+
+int occ_attn4_verify() { return kVerify4Occ; }
+
+cudaError_t launch_attn4_verify(const Attn4Args& a, cudaStream_t st) {
+    // the kernel's attributes for its shared memory, set once for a device and a variant
+    constexpr int kDevices = 64, kVariants = 6;
+    static std::atomic<bool> known[kDevices][kVariants];
+    const int R = a.T * (a.H_q / a.H_kv);
+    Verify4Fn fn;
+    int smem, dev = 0;
+    if (a.D == 128) pick<128>(R, &fn, &smem);
+    else pick<64>(R, &fn, &smem);
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const int v = (a.D == 128 ? 3 : 0) + (R <= 16 ? 0 : R <= 32 ? 1 : 2);
+    if (dev >= kDevices || !known[dev][v].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+        if (e != cudaSuccess) return e;
+        if (dev < kDevices) known[dev][v].store(true, std::memory_order_release);
+    }
+    return launch_pdl(fn, dim3((unsigned)((long long)a.B * a.H_kv * a.num_splits)), dim3(Verify4Cfg<128, 16>::THREADS), smem, st, a);
+}
+
+}  // namespace spd

@@ -131,9 +131,13 @@ struct Attn4Args {
     unsigned* status;
     unsigned long long wait_ns;  // limit of every bounded wait
 };
-cudaError_t launch_attn4(const Attn4Args& a, bool sparse, cudaStream_t st);
-// CTAs of the kernel that fit on one SM for this shape.
-int occ_attn4(int D, int R, bool sparse);
+// Up to 8 query rows of a KV head (T * G), dense or sparse; 9 to 64, dense.
+cudaError_t launch_attn4_decode(const Attn4Args& a, bool sparse, cudaStream_t st);
+cudaError_t launch_attn4_verify(const Attn4Args& a, cudaStream_t st);
+constexpr int kAttn4DecodeRows = 8;
+// Their CTAs on one SM.
+int occ_attn4_decode();
+int occ_attn4_verify();
 
 struct LogprobArgs {
     const void* logits;  // [rows][n], row_stride elements apart

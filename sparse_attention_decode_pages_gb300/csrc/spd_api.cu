@@ -957,32 +957,34 @@ SPD_API spd_status kv4_read(const spd_dims* dims, int32_t T, const uint8_t* kv4,
     return e == cudaSuccess ? SPD_OK : cuda_fail(e, "kv4_read launch");
 }
 
-// Splits of a row of the 4-bit attention.  Its CTAs take one unit each, `slots` at a
-// time, and a unit costs about kv4_unit_fixed chunks of a warp besides its own (the
-// lengths, the queries, the first copies, the join).  Up to half a GPU of rows is cut
-// into one round of units.  More rows, selections (about equal): the count that takes
-// the least rounds * (chunks + fixed).  More rows, whole sequences (their lengths
-// differ, and only the GPU knows them): units + the longest one's tail,
-// rows * S * (c / S + fixed) / slots + c / S, is least at S = sqrt(c * slots / (rows * fixed)).
-constexpr int kv4_unit_fixed = 12;
-
+// Splits of a row of the 4-bit attention.  Its CTAs take one unit each, `slots` at a time, in
+// turns of 128 tokens, and a unit costs about `fixed` turns besides its own (the lengths, the
+// queries, the first copies, the join).  Up to half a GPU of rows is cut into one round of
+// units.  More rows, selections (about equal): the count that takes the least rounds *
+// (turns + fixed).  More rows, whole sequences (their lengths differ, and only the GPU knows
+// them): units + the longest one's tail, rows * S * (turns / S + fixed) / slots + turns / S, is
+// least at S = sqrt(turns * slots / (rows * fixed)).  Measured: 64 sequences of 8K-16K tokens, 8 KV heads,
+// 28 query rows: S = 1 / 2 / 3 / 4 / 8: 457 / 447 / 459 / 470 / 545 us; 64 selections of 64 pages of
+// 16: 1 / 2 / 4: 28 / 37 / 44 us.
 static int kv4_splits(const spd_dims* d, int T, int items, bool sparse, int req, int sms) {
     const long long rows = (long long)d->B * d->H_kv;
-    const int warps = 4;  // chunks in work at once
-    const long long slots = (long long)sms * occ_attn4(d->D, T * (d->H_q / d->H_kv), sparse);
+    const bool few = T * (d->H_q / d->H_kv) <= kAttn4DecodeRows;
+    const double fixed = few ? 6 : 16;
+    const long long slots = (long long)sms * (few ? occ_attn4_decode() : occ_attn4_verify());
     int S = req;
     if (S <= 0) {
         S = 1;
-        const int most = (items + pages_per_split_floor(d->page_size) - 1) / pages_per_split_floor(d->page_size);
-        const double c = (double)items * (d->page_size / 16) / warps;  // chunks of a warp, row unsplit
+        const int floor_items = 128 / d->page_size;
+        const int most = (items + floor_items - 1) / floor_items;
+        const double turns = (double)items * d->page_size / 128;
         if (rows > 0 && 2 * rows <= slots) {
             S = (int)(slots / rows);
         } else if (rows > 0 && !sparse) {
-            S = (int)(sqrt(c * slots / ((double)rows * kv4_unit_fixed)) + 0.5);
+            S = (int)(sqrt(turns * slots / (rows * fixed)) + 0.5);
         } else if (rows > 0) {
             double best = 1e300;
             for (int s = 1; s <= 16 && s <= most; ++s) {
-                const double cost = (double)((rows * s + slots - 1) / slots) * (c / s + kv4_unit_fixed);
+                const double cost = (double)((rows * s + slots - 1) / slots) * (turns / s + fixed);
                 if (cost < best) {
                     best = cost;
                     S = s;
@@ -1075,7 +1077,8 @@ static spd_status kv4_attn(const spd_dims* dims, int32_t T, const spd_bf16* q, c
     a.counters = w.counters;
     a.status = d->status;
     a.wait_ns = wait_limit_ns();
-    cudaError_t e = launch_attn4(a, sparse, static_cast<cudaStream_t>(stream));
+    cudaError_t e = R <= kAttn4DecodeRows ? launch_attn4_decode(a, sparse, static_cast<cudaStream_t>(stream))
+                                          : launch_attn4_verify(a, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? SPD_OK : cuda_fail(e, sparse ? "kv4_sparse_decode_attn launch" : "kv4_dense_verify_attn launch");
 }
 
