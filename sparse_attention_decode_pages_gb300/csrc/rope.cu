@@ -19,73 +19,93 @@ constexpr int kRopeTurns = 2;
 
 __host__ __device__ constexpr int rope_heads_per_warp(int D) { return kRopeTurns * 32 / (D / 8); }
 
-// One side (queries or keys) of one token by one warp: heads h0 ... of `heads`.  pos < 0: the
-// token's position is not one of the table's (or its sequence is skipped): zero rows.
+// Tokens of a warp: the second shares the first one's weights, addresses and rotation, and its
+// loads are in flight with the first one's.  (16,381 rows: 1 / 2 / 4 tokens 70 / 67 / 106 us.)
+constexpr int kRopeTokens = 2;
+
+// One side (queries or keys) of kRopeTokens tokens by one warp: heads h0 ... of `heads` of rows
+// row ... that lie below a.rows.  pos < 0: the token's position is not one of the table's (or
+// its sequence is skipped): zero rows.
 template <int D>
-__device__ __forceinline__ void rope_warp(const RopeArgs& a, const uint16_t* src, uint16_t* dst, const uint16_t* weight,
-                                          int h0, int heads, int pos) {
+__device__ __forceinline__ void rope_warp(const RopeArgs& a, const uint16_t* src, long long stride, uint16_t* dst,
+                                          const uint16_t* weight, int h0, int heads, long long row,
+                                          const int (&pos)[kRopeTokens]) {
     constexpr int L = D / 8, HT = 32 / L;
     const int lane = threadIdx.x & 31, l = lane % L, h = h0 + lane / L;
     const RopeLane r = rope_lane<D>(l, a.rot, a.interleaved);
-    uint2 x0[kRopeTurns], x1[kRopeTurns];
+    const int there = (heads - h + HT - 1) / HT;  // turns of this lane
+    uint2 x0[kRopeTokens][kRopeTurns], x1[kRopeTokens][kRopeTurns];
+    float4 cs[kRopeTokens], sn[kRopeTokens];
+    const uint16_t* p = src + row * stride + h * D;
 #pragma unroll
-    for (int i = 0; i < kRopeTurns; ++i) {
-        x0[i] = x1[i] = make_uint2(0u, 0u);
-        if (pos >= 0 && h + i * HT < heads) {
-            x0[i] = *reinterpret_cast<const uint2*>(src + (h + i * HT) * D + r.o0);
-            x1[i] = *reinterpret_cast<const uint2*>(src + (h + i * HT) * D + r.o1);
+    for (int t = 0; t < kRopeTokens; ++t) {
+        const bool live = pos[t] >= 0 && row + t < a.rows;
+#pragma unroll
+        for (int i = 0; i < kRopeTurns; ++i) {
+            x0[t][i] = x1[t][i] = make_uint2(0u, 0u);
+            if (live && i < there) {
+                x0[t][i] = *reinterpret_cast<const uint2*>(p + i * HT * D + r.o0);
+                x1[t][i] = *reinterpret_cast<const uint2*>(p + i * HT * D + r.o1);
+            }
         }
-    }
-    float4 cs = make_float4(1.f, 1.f, 1.f, 1.f), sn = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (pos >= 0 && r.turned) {
-        const float* t = a.table + (long long)pos * a.rot + 4 * l;
-        cs = __ldg(reinterpret_cast<const float4*>(t));
-        sn = __ldg(reinterpret_cast<const float4*>(t + (a.rot >> 1)));
+        cs[t] = sn[t] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (live && r.turned) {
+            const float* table = a.table + (long long)pos[t] * a.rot + 4 * l;
+            cs[t] = __ldg(reinterpret_cast<const float4*>(table));
+            sn[t] = __ldg(reinterpret_cast<const float4*>(table + (a.rot >> 1)));
+        }
+        p += stride;
     }
     float w[8];
     rope_weights(weight, r, w);
+    uint16_t* q = dst + (row * heads + h) * D;
 #pragma unroll
-    for (int i = 0; i < kRopeTurns; ++i) {
-        float x[8];
-        unpack4(x0[i], x);
-        unpack4(x1[i], x + 4);
-        rope_row<D>(x, weight != nullptr, w, a.eps, r, a.interleaved, cs, sn);
-        if (h + i * HT < heads) {
-            *reinterpret_cast<uint2*>(dst + (h + i * HT) * D + r.o0) = pos >= 0 ? pack4(x) : make_uint2(0u, 0u);
-            *reinterpret_cast<uint2*>(dst + (h + i * HT) * D + r.o1) = pos >= 0 ? pack4(x + 4) : make_uint2(0u, 0u);
+    for (int t = 0; t < kRopeTokens; ++t) {
+        const int turns = row + t < a.rows ? there : 0;
+#pragma unroll
+        for (int i = 0; i < kRopeTurns; ++i) {
+            float x[8];
+            unpack4(x0[t][i], x);
+            unpack4(x1[t][i], x + 4);
+            rope_row<D>(x, weight != nullptr, w, a.eps, r, a.interleaved, cs[t], sn[t]);
+            if (i < turns) {
+                *reinterpret_cast<uint2*>(q + i * HT * D + r.o0) = pos[t] >= 0 ? pack4(x) : make_uint2(0u, 0u);
+                *reinterpret_cast<uint2*>(q + i * HT * D + r.o1) = pos[t] >= 0 ? pack4(x + 4) : make_uint2(0u, 0u);
+            }
         }
+        q += heads * D;
     }
 }
 
-// A warp's token is row blockIdx.x * kRopeWarps + warp, its heads group blockIdx.y: the
-// query heads' groups, then the key heads'.
+// A warp's tokens are kRopeTokens from kRopeTokens * (blockIdx.x * kRopeWarps + warp) on, its
+// heads group blockIdx.y: the query heads' groups, then the key heads'.
 template <int D>
 __global__ void __launch_bounds__(kRopeThreads, 4) qk_norm_rope_kernel(const RopeArgs a) {
     constexpr int HW = rope_heads_per_warp(D);
     pdl_wait();
     pdl_trigger();
-    const long long row = (long long)blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
+    const long long row = ((long long)blockIdx.x * kRopeWarps + (threadIdx.x >> 5)) * kRopeTokens;
     if (row >= a.rows) return;
-    int pos = 0;
-    if (a.rot > 0) {
-        pos = a.positions[row];
-        if (pos < 0 || pos >= a.n_pos) {
+    int pos[kRopeTokens];
+#pragma unroll
+    for (int t = 0; t < kRopeTokens; ++t) {
+        pos[t] = a.rot > 0 && row + t < a.rows ? a.positions[row + t] : 0;
+        if (a.rot > 0 && (pos[t] < 0 || pos[t] >= a.n_pos)) {
             if ((threadIdx.x & 31) == 0) raise_status(a.status, SPD_DEV_BAD_POS);
-            pos = -1;
+            pos[t] = -1;
         }
     }
     const int q_groups = (a.H_q + HW - 1) / HW;
     if ((int)blockIdx.y < q_groups)
-        rope_warp<D>(a, a.q + row * a.q_stride, a.q_out + row * a.H_q * D, a.q_weight, blockIdx.y * HW, a.H_q, pos);
+        rope_warp<D>(a, a.q, a.q_stride, a.q_out, a.q_weight, blockIdx.y * HW, a.H_q, row, pos);
     else
-        rope_warp<D>(a, a.k + row * a.k_stride, a.k_out + row * a.H_kv * D, a.k_weight, (blockIdx.y - q_groups) * HW,
-                     a.H_kv, pos);
+        rope_warp<D>(a, a.k, a.k_stride, a.k_out, a.k_weight, (blockIdx.y - q_groups) * HW, a.H_kv, row, pos);
 }
 
 cudaError_t launch_qk_norm_rope(const RopeArgs& a, cudaStream_t st) {
     const int hw = rope_heads_per_warp(a.D);
     const dim3 block(kRopeThreads);
-    const dim3 grid((unsigned)((a.rows + kRopeWarps - 1) / kRopeWarps),
+    const dim3 grid((unsigned)((a.rows + kRopeWarps * kRopeTokens - 1) / (kRopeWarps * kRopeTokens)),
                     (unsigned)((a.H_q + hw - 1) / hw + (a.H_kv + hw - 1) / hw));
     if (a.D == 128) return launch_pdl(qk_norm_rope_kernel<128>, grid, block, 0, st, a);
     return launch_pdl(qk_norm_rope_kernel<64>, grid, block, 0, st, a);
@@ -115,19 +135,26 @@ __global__ void __launch_bounds__(kRopeThreads, 4) append_rope_kernel(const Appe
     const int head_ctas = (a.H_kv + kPageHeads - 1) / kPageHeads;
     const int page_ctas = a.B * p.touched * head_ctas;
     if ((int)blockIdx.x >= page_ctas) {
-        // a warp: one group of the query heads of token row = b * T + t, at position len - T + t
+        // a warp: one group of the query heads of tokens row ... of all B * T, row = b * T + t at
+        // position len - T + t
         constexpr int HW = rope_heads_per_warp(D);
         const unsigned groups = (ro.H_q + HW - 1) / HW;
         const unsigned unit = (blockIdx.x - page_ctas) * kRopeWarps + warp;  // below 2^31 + kRopeWarps (checked by the host)
-        const unsigned row = unit / groups;
+        const unsigned row = unit / groups * kRopeTokens;
         if (row >= ro.rows) return;
-        const int b = (int)(row / (unsigned)a.T), t = (int)(row - (unsigned)b * a.T);
-        const int len = a.seq_lens[b];
-        int pos = len - a.T + t;
-        // a sequence that is skipped gets zero rows (the page CTAs report it)
-        if (len < a.T || len > a.max_pages * (long long)a.ps || (ro.rot > 0 && len > ro.n_pos)) pos = -1;
-        rope_warp<D>(ro, ro.q + (long long)row * ro.q_stride, ro.q_out + (long long)row * ro.H_q * D, ro.q_weight,
-                     (unit - row * groups) * HW, ro.H_q, pos);
+        int pos[kRopeTokens];
+#pragma unroll
+        for (int i = 0; i < kRopeTokens; ++i) {
+            pos[i] = -1;
+            if (row + i < ro.rows) {
+                const int b = (int)((row + i) / (unsigned)a.T), t = (int)(row + i - (unsigned)b * a.T);
+                const int len = a.seq_lens[b];
+                // a sequence that is skipped gets zero rows (the page CTAs report it)
+                const bool skipped = len < a.T || len > a.max_pages * (long long)a.ps || (ro.rot > 0 && len > ro.n_pos);
+                pos[i] = skipped ? -1 : len - a.T + t;
+            }
+        }
+        rope_warp<D>(ro, ro.q, ro.q_stride, ro.q_out, ro.q_weight, (unit - unit / groups * groups) * HW, ro.H_q, row, pos);
         return;
     }
     const int page_cta = blockIdx.x / head_ctas, h = (blockIdx.x - page_cta * head_ctas) * kPageHeads + warp / kPageParts;
@@ -269,7 +296,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) append_rope_kernel(const Appe
 
 long long append_rope_ctas(const AppendRopeArgs& p) {
     const int hw = rope_heads_per_warp(p.append.D);
-    const long long units = p.rope.q ? p.rope.rows * ((p.rope.H_q + hw - 1) / hw) : 0;
+    const long long units = p.rope.q ? (p.rope.rows + kRopeTokens - 1) / kRopeTokens * ((p.rope.H_q + hw - 1) / hw) : 0;
     return (long long)p.append.B * append_touched(p.append.T, p.append.ps, p.append.max_pages) *
                ((p.append.H_kv + kPageHeads - 1) / kPageHeads) +
            (units + kRopeWarps - 1) / kRopeWarps;
