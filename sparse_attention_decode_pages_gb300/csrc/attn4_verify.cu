@@ -66,7 +66,8 @@ struct Verify4Cfg {
     static constexpr int OFF_RED = OFF_FR + N * 8;           // float [4][N]: maxima, then sums
     static constexpr int OFF_CORR = OFF_RED + 4 * N * 4;  // float [N]
     static constexpr int OFF_OUT = OFF_CORR + N * 4;          // long long [N]: output rows
-    static constexpr int OFF_BAR = OFF_OUT + N * 8;           // uint64 [STAGES] and four more
+    static constexpr int OFF_LIM = OFF_OUT + N * 8;           // int [N]: the last position that a row sees
+    static constexpr int OFF_BAR = OFF_LIM + N * 4;           // uint64 [STAGES] and four more
     static constexpr int OFF_META = OFF_BAR + (STAGES + 4) * 8;  // int [STAGES][CHUNKS]: first positions or -1
     static constexpr int BODY = OFF_META + STAGES * CHUNKS * 4;
     // tensor memory: K, S, O
@@ -75,6 +76,7 @@ struct Verify4Cfg {
     // at most 512 / COLUMNS CTAs fit on an SM (227 KB), so that none waits for columns
     static constexpr int LEAST = 227 * 1024 / (512 / COLUMNS + 1);
     static constexpr int SMEM = 1024 + (BODY > LEAST ? BODY : LEAST);
+    static_assert(128 * (N + 1) * 4 <= OFF_FR - OFF_V && OFF_LIM % 8 == 0 && OFF_BAR % 8 == 0, "the sums fit over V, Q and P");
     static constexpr int P_ROW = N * 2;
     static constexpr uint64_t P_SWIZZLE = N == 16 ? kSwizzle32 : N == 32 ? kSwizzle64 : kSwizzle128;
     static_assert(kVerify4Occ * (SMEM + 2048) <= 228 * 1024 && kVerify4Occ * COLUMNS <= 512, "they fit on an SM");
@@ -147,6 +149,7 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
     float* s_red = reinterpret_cast<float*>(smem + C::OFF_RED);
     float* s_corr = reinterpret_cast<float*>(smem + C::OFF_CORR);
     long long* s_out = reinterpret_cast<long long*>(smem + C::OFF_OUT);
+    int* s_lim = reinterpret_cast<int*>(smem + C::OFF_LIM);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
     uint64_t* k_ready = full + STAGES;  // K of a step is in tensor memory
     uint64_t* p_ready = k_ready + 1;    // V and P are in shared memory, and the step's codes are read
@@ -173,6 +176,19 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
     pdl_wait();
     pdl_trigger();
 
+    // this warp's query rows, read together with the length
+    constexpr int RW = (N + WARPS) / (WARPS + 1);
+    float2 qx[RW][D / 64];
+#pragma unroll
+    for (int j = 0; j < RW; ++j) {
+        const int r = warp + (WARPS + 1) * j;
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+            qx[j][i] = make_float2(0.f, 0.f);
+            if (r < R)
+                qx[j][i] = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(a.q + out_index(r) * D + 2 * lane + 64 * i));
+        }
+    }
     const int start = split * a.pages_per_split;
     const int cpp = a.ps >> 4;  // chunks per page
     // the issuing warp's lane i resolves chunk 32 j + i of the unit, for four steps at a time
@@ -259,16 +275,13 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
 
     // the query rows in fp16, each scaled by 2^-e so that its largest channel lies in [1, 2);
     // channel qc * D / 4 + 4 i + j at position 16 i + 4 qc + j
-    for (int r = warp; r < N; r += WARPS + 1) {
-        float2 x[D / 64];
+#pragma unroll
+    for (int j = 0; j < RW; ++j) {
+        const int r = warp + (WARPS + 1) * j;
+        if (r >= N) break;
         float amax = 0.f;
 #pragma unroll
-        for (int i = 0; i < D / 64; ++i) {
-            x[i] = make_float2(0.f, 0.f);
-            if (r < R)
-                x[i] = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(a.q + out_index(r) * D + 2 * lane + 64 * i));
-            amax = fmaxf(amax, fmaxf(fabsf(x[i].x), fabsf(x[i].y)));
-        }
+        for (int i = 0; i < D / 64; ++i) amax = fmaxf(amax, fmaxf(fabsf(qx[j][i].x), fabsf(qx[j][i].y)));
         const int e = query_exponent(amax);
         const float down = pow2f(-e);
 #pragma unroll
@@ -276,12 +289,13 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
             const int ch = 2 * lane + 64 * i, qc = ch / (D / 4), in = ch % (D / 4);
             const int at = 16 * (in >> 2) + 4 * qc + (in & 3);
             uint8_t* block = smem + C::OFF_Q + (at >> 6) * (N * 128);
-            *reinterpret_cast<uint32_t*>(block + r * 128 + (((at & 63) * 2) ^ ((r & 7) << 4))) = pack_f16(x[i].x * down, x[i].y * down);
+            *reinterpret_cast<uint32_t*>(block + r * 128 + (((at & 63) * 2) ^ ((r & 7) << 4))) = pack_f16(qx[j][i].x * down, qx[j][i].y * down);
         }
-        if (lane == 0) {
-            s_fr[r] = make_float2(a.scale_log2 * pow2f(e), -kLow4);
-            s_out[r] = r < R ? out_index(r) : 0;
-        }
+        if (lane == 0) s_fr[r] = make_float2(a.scale_log2 * pow2f(e), -kLow4);
+    }
+    if (tid < N) {
+        s_out[tid] = tid < R ? out_index(tid) : 0;
+        s_lim[tid] = tid < R ? len - a.T + tid / G : len - 1;
     }
     async_proxy_fence();
     tmem_fence_before();
@@ -423,53 +437,48 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
         const int chunk_first = meta[slot * CHUNKS + my_chunk];
         const int pos = chunk_first < 0 ? 0x7fffffff : chunk_first + (lane & 15);
         const bool all = __all_sync(0xffffffffu, pos <= len - a.T);  // every row sees every token of the warp
-        auto last_seen = [&](int r) { return r < R ? len - a.T + r / G : len - 1; };
         float p[NH];
-        auto weights = [&](const uint32_t (&s)[NH]) {
+        // (what runs once a unit is kept short: a unit's first pass through straight code is bound by
+        // fetching it)
+        bool late = false;
+#pragma unroll 1
+        for (bool moved = false;; moved = true) {
+            {
+                uint32_t s[NH];
+                load_columns<NH>(tm_s + r0 + my_lanes, s);
 #pragma unroll
-            for (int r = 0; r < NH; r += 2) {
-                const float4 fr = *reinterpret_cast<const float4*>(s_fr + r0 + r);
-                p[r] = fast_exp2(fmaf(__uint_as_float(s[r]), fr.x, fr.y));
-                p[r + 1] = fast_exp2(fmaf(__uint_as_float(s[r + 1]), fr.z, fr.w));
+                for (int r = 0; r < NH; r += 2) {
+                    const float4 fr = *reinterpret_cast<const float4*>(s_fr + r0 + r);
+                    p[r] = fast_exp2(fmaf(__uint_as_float(s[r]), fr.x, fr.y));
+                    p[r + 1] = fast_exp2(fmaf(__uint_as_float(s[r + 1]), fr.z, fr.w));
+                }
             }
             if (!all) {
 #pragma unroll
                 for (int r = 0; r < NH; ++r)
-                    if (pos > last_seen(r0 + r)) p[r] = 0.f;
+                    if (pos > s_lim[r0 + r]) p[r] = 0.f;
             }
-        };
-        auto put_p = [&]() {
+            float top = 0.f;
+#pragma unroll
+            for (int r = 0; r < NH; ++r) top = fmaxf(top, p[r]);
 #pragma unroll
             for (int i = 0; i < NH / 8; ++i)
                 st_shared16(p_dst ^ (i << 4), pack_f16(p[8 * i], p[8 * i + 1]), pack_f16(p[8 * i + 2], p[8 * i + 3]),
                             pack_f16(p[8 * i + 4], p[8 * i + 5]), pack_f16(p[8 * i + 6], p[8 * i + 7]));
-        };
-        float top = 0.f;
-        {
-            uint32_t s[NH];
-            load_columns<NH>(tm_s + r0 + my_lanes, s);
-            weights(s);
-        }
-#pragma unroll
-        for (int r = 0; r < NH; ++r) top = fmaxf(top, p[r]);
-        put_p();
-        async_proxy_fence();
-        tmem_fence_before();
-        if (!ok) s_late = 1;
-        const bool move = converters_or<32 * WARPS>(top > kMost4);
-        if (s_late) {
-            gone = true;
-            break;
-        }
-        if (move) {
-            // the largest logit of each row among this step's tokens
-            uint32_t s[NH];
-            load_columns<NH>(tm_s + r0 + my_lanes, s);
-#pragma unroll
+            async_proxy_fence();
+            tmem_fence_before();
+            if (!ok) s_late = 1;
+            const bool move = converters_or<32 * WARPS>(top > kMost4);  // some weight is too large
+            late = s_late != 0;
+            if (!move || moved || late) break;
+            // the references move to the largest logit of each row among this step's tokens
+#pragma unroll 1
             for (int r = 0; r < NH; ++r) {
-                const float z = pos > last_seen(r0 + r) ? NEG_INF : __uint_as_float(s[r]) * s_fr[r0 + r].x;
-                const unsigned top_key = __reduce_max_sync(0xffffffffu, z == z ? float_key(z) : 0u);
-                if (lane == 0) s_red[(warp & 3) * N + r0 + r] = __uint_as_float(top_key & 0x80000000u ? top_key & 0x7fffffffu : ~top_key);
+                uint32_t s[1];
+                load_columns<1>(tm_s + r0 + r + my_lanes, s);
+                const float z = pos > s_lim[r0 + r] ? NEG_INF : __uint_as_float(s[0]) * s_fr[r0 + r].x;
+                const unsigned key = __reduce_max_sync(0xffffffffu, z == z ? float_key(z) : 0u);
+                if (lane == 0) s_red[(warp & 3) * N + r0 + r] = __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
             }
             converters_sync<32 * WARPS>();
             if (tid < N) {
@@ -482,19 +491,21 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
             }
             converters_sync<32 * WARPS>();
             if (k > 0) {
-                uint32_t o[NH];
-                load_columns<NH>(tm_o + r0 + my_lanes, o);
+#pragma unroll 1
+                for (int r = 0; r < NH; r += 8) {
+                    uint32_t o[8];
+                    load_columns<8>(tm_o + r0 + r + my_lanes, o);
 #pragma unroll
-                for (int r = 0; r < NH; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * s_corr[r0 + r]);
-                store_columns<NH>(tm_o + r0 + my_lanes, o);
+                    for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * s_corr[r0 + r + i]);
+                    store_columns<8>(tm_o + r0 + r + my_lanes, o);
+                }
             }
 #pragma unroll
             for (int r = 0; r < NH; ++r) l[r] *= s_corr[r0 + r];
-            weights(s);
-            put_p();
-            async_proxy_fence();
-            tmem_fence_before();
-            converters_sync<32 * WARPS>();
+        }
+        if (late) {
+            gone = true;
+            break;
         }
         if (tid == 0) mbar_arrive(p_ready);
         done = k + 1;
@@ -510,29 +521,39 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
     tmem_fence_after();
     uint32_t o[NH];
     load_columns<NH>(tm_o + r0 + my_lanes, o);  // channel my_row of this thread's query rows
-#pragma unroll
-    for (int r = 0; r < NH; ++r) {
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], off);
-        if (lane == 0) s_red[(warp & 3) * N + r0 + r] = l[r];
-    }
     tmem_fence_before();
+    // the sums of the rows, over the 128 threads that hold parts of each: through shared memory
+    // (over V, with a column of padding), 128 / PARTS of them a thread
+    float* s_sum = reinterpret_cast<float*>(smem + C::OFF_V);
+#pragma unroll
+    for (int r = 0; r < NH; ++r) s_sum[my_row * (N + 1) + r0 + r] = l[r];
+    converters_sync<32 * WARPS>();
+    constexpr int PARTS = 4;
+    if (tid < N * PARTS) {
+        float sum = 0.f;
+        for (int i = 0; i < 128 / PARTS; ++i) sum += s_sum[(tid / N * (128 / PARTS) + i) * (N + 1) + tid % N];
+        s_red[tid] = sum;
+    }
+    converters_sync<32 * WARPS>();
+    if (tid < N) {
+        const float sum = s_red[tid] + s_red[N + tid] + s_red[2 * N + tid] + s_red[3 * N + tid];
+        s_corr[tid] = sum == 0.f ? 0.f : a.v_scale / sum;
+        const float lse = sum == 0.f ? NEG_INF : (log2f(sum) - s_fr[tid].y) * kLn2;
+        const long long at = ((long long)row * a.num_splits + split) * R + tid;
+        if (tid < R && nsplit > 1) a.part_lse[at] = lse;
+        if (tid < R && nsplit == 1 && a.lse) a.lse[s_out[tid]] = lse;
+    }
     converters_sync<32 * WARPS>();
     if (my_row < D) {
 #pragma unroll
         for (int i = 0; i < NH; ++i) {
             const int r = r0 + i;
-            if (r >= R) break;
-            const float sum = s_red[r] + s_red[N + r] + s_red[2 * N + r] + s_red[3 * N + r];
-            const float x = sum == 0.f ? 0.f : __uint_as_float(o[i]) * (a.v_scale / sum);
-            const float lse = sum == 0.f ? NEG_INF : (log2f(sum) - s_fr[r].y) * kLn2;
-            if (nsplit == 1) {
-                reinterpret_cast<bf16*>(a.o)[s_out[r] * D + my_row] = __float2bfloat16_rn(x);
-                if (my_row == 0 && a.lse) a.lse[s_out[r]] = lse;
-            } else {
-                const long long at = ((long long)row * a.num_splits + split) * R + r;
-                a.part_o[at * D + my_row] = x;
-                if (my_row == 0) a.part_lse[at] = lse;
+            const float inv = s_corr[r], x = inv == 0.f ? 0.f : __uint_as_float(o[i]) * inv;
+            if (r < R) {
+                if (nsplit == 1)
+                    reinterpret_cast<bf16*>(a.o)[s_out[r] * D + my_row] = __float2bfloat16_rn(x);
+                else
+                    a.part_o[(((long long)row * a.num_splits + split) * R + r) * D + my_row] = x;
             }
         }
     }
