@@ -178,16 +178,13 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
 
     // this warp's query rows, read together with the length
     constexpr int RW = (N + WARPS) / (WARPS + 1);
-    float2 qx[RW][D / 64];
+    uint32_t qx[RW][D / 64];
 #pragma unroll
     for (int j = 0; j < RW; ++j) {
         const int r = warp + (WARPS + 1) * j;
+        const long long at = out_index(r < R ? r : 0) * D + 2 * lane;
 #pragma unroll
-        for (int i = 0; i < D / 64; ++i) {
-            qx[j][i] = make_float2(0.f, 0.f);
-            if (r < R)
-                qx[j][i] = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(a.q + out_index(r) * D + 2 * lane + 64 * i));
-        }
+        for (int i = 0; i < D / 64; ++i) qx[j][i] = r < R ? *reinterpret_cast<const uint32_t*>(a.q + at + 64 * i) : 0u;
     }
     const int start = split * a.pages_per_split;
     const int cpp = a.ps >> 4;  // chunks per page
@@ -279,9 +276,13 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
     for (int j = 0; j < RW; ++j) {
         const int r = warp + (WARPS + 1) * j;
         if (r >= N) break;
+        float2 x[D / 64];
         float amax = 0.f;
 #pragma unroll
-        for (int i = 0; i < D / 64; ++i) amax = fmaxf(amax, fmaxf(fabsf(qx[j][i].x), fabsf(qx[j][i].y)));
+        for (int i = 0; i < D / 64; ++i) {
+            x[i] = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&qx[j][i]));
+            amax = fmaxf(amax, fmaxf(fabsf(x[i].x), fabsf(x[i].y)));
+        }
         const int e = query_exponent(amax);
         const float down = pow2f(-e);
 #pragma unroll
@@ -289,7 +290,7 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
             const int ch = 2 * lane + 64 * i, qc = ch / (D / 4), in = ch % (D / 4);
             const int at = 16 * (in >> 2) + 4 * qc + (in & 3);
             uint8_t* block = smem + C::OFF_Q + (at >> 6) * (N * 128);
-            *reinterpret_cast<uint32_t*>(block + r * 128 + (((at & 63) * 2) ^ ((r & 7) << 4))) = pack_f16(qx[j][i].x * down, qx[j][i].y * down);
+            *reinterpret_cast<uint32_t*>(block + r * 128 + (((at & 63) * 2) ^ ((r & 7) << 4))) = pack_f16(x[i].x * down, x[i].y * down);
         }
         if (lane == 0) s_fr[r] = make_float2(a.scale_log2 * pow2f(e), -kLow4);
     }
@@ -473,12 +474,20 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
             if (!move || moved || late) break;
             // the references move to the largest logit of each row among this step's tokens
 #pragma unroll 1
-            for (int r = 0; r < NH; ++r) {
-                uint32_t s[1];
-                load_columns<1>(tm_s + r0 + r + my_lanes, s);
-                const float z = pos > s_lim[r0 + r] ? NEG_INF : __uint_as_float(s[0]) * s_fr[r0 + r].x;
-                const unsigned key = __reduce_max_sync(0xffffffffu, z == z ? float_key(z) : 0u);
-                if (lane == 0) s_red[(warp & 3) * N + r0 + r] = __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
+            for (int r = 0; r < NH; r += 8) {
+                uint32_t s[8];
+                load_columns<8>(tm_s + r0 + r + my_lanes, s);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float z = pos > s_lim[r0 + r + i] ? NEG_INF : __uint_as_float(s[i]) * s_fr[r0 + r + i].x;
+                    s[i] = __reduce_max_sync(0xffffffffu, z == z ? float_key(z) : 0u);
+                }
+                if (lane < 8) {
+                    uint32_t key = s[0];
+#pragma unroll
+                    for (int i = 1; i < 8; ++i) key = lane == i ? s[i] : key;
+                    s_red[(warp & 3) * N + r0 + r + lane] = __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
+                }
             }
             converters_sync<32 * WARPS>();
             if (tid < N) {

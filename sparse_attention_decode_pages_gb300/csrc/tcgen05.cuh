@@ -104,12 +104,6 @@ __device__ __forceinline__ void umma_commit(uint64_t* bar) {
 
 // A warp's 32 lanes of tensor memory (32 * (warp % 4) on), n 32-bit columns from taddr: lane i's
 // registers are lane i's columns.
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[1]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];"
-        : "=r"(v[0])
-        : "r"(taddr));
-}
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[8]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
