@@ -256,56 +256,10 @@ __global__ void __launch_bounds__(kLpThreads, kLpOcc) logprob_kernel(const Logpr
             edge = lp_at<BF16>(rowp, edge_token);
         }
     }
-    {
-        LpRegs next = load(1);
-        float m = sums(cur);
-        if (!(edge == NEG_INF)) {  // NaN too
-            LpRegs one;
-#pragma unroll
-            for (int j = 0; j < kLpU; ++j) one.x[j] = make_uint4(kNone, kNone, kNone, kNone);
-            one.x[0].x = BF16 ? (__float_as_uint(edge) >> 16) | 0xff800000u : __float_as_uint(edge);
-            m = fmaxf(m, sums(one));
-        }
-        if (K > 0) {
-            // the first bound: the K-th largest thread maximum with its low bits cleared, found a
-            // bit at a time from the highest in which the maxima differ
-            s.tmax[tid] = lp_order(m);
-            __syncthreads();
-            if (warp == 0) {
-                unsigned t[kLpThreads / 32];
-                unsigned lo = 0xffffffffu, hi = 0;
-#pragma unroll
-                for (int i = 0; i < kLpThreads / 32; ++i) {
-                    t[i] = s.tmax[lane + 32 * i];
-                    lo = min(lo, t[i]);
-                    hi = max(hi, t[i]);
-                }
-                lo = __reduce_min_sync(0xffffffffu, lo);
-                hi = __reduce_max_sync(0xffffffffu, hi);
-                const int top = hi == lo ? 0 : 32 - __clz(hi ^ lo);  // the bits that differ lie below 2^top
-                unsigned bound = top >= 32 ? 0u : hi >> top << top;
-                for (int bit = top - 1; bit >= max(0, top - 12); --bit) {
-                    const unsigned cand = bound | 1u << bit;
-                    int c = 0;
-#pragma unroll
-                    for (int i = 0; i < kLpThreads / 32; ++i) c += t[i] >= cand;
-                    if ((int)__reduce_add_sync(0xffffffffu, (unsigned)c) >= K) bound = cand;
-                }
-                // at least the lowest finite value, so that nothing at -inf passes
-                const unsigned least = float_key(-3.402823466e+38f);
-                if (lane == 0) s.bound = lp_key_value((u64)max(bound, least) << 32);
-            }
-            __syncthreads();
-            const float bound = s.bound;
-            if (m >= bound) {
-                scan(cur, 0, bound);
-                if (edge >= bound) lp_push(s, edge, edge_token);
-            }
-        }
-        cur = next;
-    }
+    // (one loop for the first tile and the others: straight code that runs once costs its fetching)
     int raise = 1;
-    for (int t = 1; t < tiles; ++t) {
+#pragma unroll 1
+    for (int t = 0; t == 0 || t < tiles; ++t) {
         LpRegs next = load(t + 1);
         if (K > 0 && t == raise) {
             lp_raise(s, K);
@@ -313,10 +267,49 @@ __global__ void __launch_bounds__(kLpThreads, kLpOcc) logprob_kernel(const Logpr
         }
         const float m = sums(cur);
         if (K > 0) {
+            if (t == 0) {
+                // the first bound: the K-th largest thread maximum with its low bits cleared, found a
+                // bit at a time from the highest in which the maxima differ
+                s.tmax[tid] = lp_order(fmaxf(m, edge));
+                __syncthreads();
+                if (warp == 0) {
+                    unsigned v[kLpThreads / 32];
+                    unsigned lo = 0xffffffffu, hi = 0;
+#pragma unroll
+                    for (int i = 0; i < kLpThreads / 32; ++i) {
+                        v[i] = s.tmax[lane + 32 * i];
+                        lo = min(lo, v[i]);
+                        hi = max(hi, v[i]);
+                    }
+                    lo = __reduce_min_sync(0xffffffffu, lo);
+                    hi = __reduce_max_sync(0xffffffffu, hi);
+                    const int top = hi == lo ? 0 : 32 - __clz(hi ^ lo);  // the bits that differ lie below 2^top
+                    unsigned bound = top >= 32 ? 0u : hi >> top << top;
+                    for (int bit = top - 1; bit >= max(0, top - 12); --bit) {
+                        const unsigned cand = bound | 1u << bit;
+                        int c = 0;
+#pragma unroll
+                        for (int i = 0; i < kLpThreads / 32; ++i) c += v[i] >= cand;
+                        if ((int)__reduce_add_sync(0xffffffffu, (unsigned)c) >= K) bound = cand;
+                    }
+                    // at least the lowest finite value, so that nothing at -inf passes
+                    const unsigned least = float_key(-3.402823466e+38f);
+                    if (lane == 0) s.bound = lp_key_value((u64)max(bound, least) << 32);
+                }
+                __syncthreads();
+                if (edge >= s.bound) lp_push(s, edge, edge_token);
+            }
             const float bound = s.bound;
             if (m >= bound) scan(cur, t, bound);
         }
         cur = next;
+    }
+    if (!(edge == NEG_INF)) {  // the thread's single token, NaN too
+        const float m = fmaxf(ref, edge);
+        const float d = ref == NEG_INF ? -1e30f : (ref - m) * c2, f = fast_exp2(d), de = (edge - m) * c2, fe = fast_exp2(de);
+        T = fmaf(f, fmaf(d, S, T), fe * fmaxf(de, -1e30f));
+        S = fmaf(f, S, fe);
+        ref = m;
     }
 
     // the threads' sums relative to the part's largest reference
@@ -432,12 +425,25 @@ __global__ void __launch_bounds__(kLpThreads, kLpOcc) logprob_kernel(const Logpr
         if (tid < 32) s.top[tid] = 0ull;
         const u64* keys = w.keys + row * plan.parts * K;
         if (K > 0) {
-            // the K-th key of any part bounds the row's K-th from below
-            unsigned bound = 0;
-            for (int p = tid; p < plan.parts; p += kLpThreads)
-                bound = max(bound, (unsigned)(__ldcg(keys + (long long)p * K + K - 1) >> 32));
-            bound = __reduce_max_sync(0xffffffffu, bound);
-            if (lane == 0) atomicMax(&s.join_bound, bound);
+            // a bound that at least K keys reach: the m-th largest of the parts' j-th keys, m * j >= K
+            // (with more parts than threads the largest of their K-th keys)
+            if (plan.parts <= kLpThreads) {
+                const int j = (K + plan.parts - 1) / plan.parts, m = (K + j - 1) / j;
+                if (tid < plan.parts) s.list[tid] = __ldcg(keys + (long long)tid * K + j - 1) & ~0xffffffffull | (unsigned)tid;
+                __syncthreads();
+                if (tid < plan.parts) {
+                    const u64 mine = s.list[tid];
+                    int rank = 0;
+                    for (int p = 0; p < plan.parts; ++p) rank += s.list[p] > mine;
+                    if (rank == m - 1) s.join_bound = (unsigned)(mine >> 32);
+                }
+            } else {
+                unsigned bound = 0;
+                for (int p = tid; p < plan.parts; p += kLpThreads)
+                    bound = max(bound, (unsigned)(__ldcg(keys + (long long)p * K + K - 1) >> 32));
+                bound = __reduce_max_sync(0xffffffffu, bound);
+                if (lane == 0) atomicMax(&s.join_bound, bound);
+            }
         }
         __syncthreads();
         S = T = 0.f;
