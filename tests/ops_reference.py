@@ -61,7 +61,7 @@ def _nearest_even(v, grid):
 
 def kv4_quantise(x, exp):
     """Codes (0..15) and scale bytes of x [..][D] (float64 bf16 values)."""
-    g = np.asarray(x, np.float64).reshape(*x.shape[:-1], -1, 16) / 2.0 ** exp
+    g = np.asarray(x, np.float64).reshape(*x.shape[:-1], x.shape[-1] // 16, 16) / 2.0 ** exp
     mag = np.where(np.isnan(g), 0.0, np.abs(g))
     grid = e4m3_values()
     scale = _nearest_even(np.minimum(mag.max(-1) / 6, grid[-1]), grid)

@@ -188,6 +188,7 @@ DENSE = [  # lens, T, H_q, H_kv, D, ps, splits
     ([2000], 1, 3, 3, 128, 32, 0),
     ([70, 31], 16, 4, 2, 64, 16, 0),
     ([90, 65], 13, 1, 1, 128, 64, 1),
+    ([140, 12], 12, 8, 2, 64, 32, 0),
 ]
 
 
@@ -261,6 +262,106 @@ def test_kv4_sparse_decode(spd, lens, H_q, H_kv, D, ps, k_max, splits):
             pages = set(sel[b, h, : nsel[b, h]].tolist())
             seen = np.array([j // ps in pages for j in range(lens[b])])
             check_row(og[b, hq], lg[b, hq], q[b, hq], vals[b][0][:, h], vals[b][1][:, h], D ** -0.5, seen, (b, hq))
+
+
+LONG = [  # len, T, H_q, H_kv, D, ps, splits
+    (9001, 1, 4, 1, 128, 16, 1),
+    (9001, 2, 8, 2, 64, 64, 2),
+    (5003, 7, 4, 1, 128, 16, 1),
+    (5003, 7, 4, 1, 64, 32, 2),
+    (4500, 9, 7, 1, 128, 64, 1),
+]
+
+
+@pytest.mark.parametrize("length,T,H_q,H_kv,D,ps,splits", LONG)
+def test_kv4_long_sequences(spd, length, T, H_q, H_kv, D, ps, splits):
+    """Many turns of every ring and of the page lookups, in few splits; and, for one position, the same tokens
+    as a selection of every page."""
+    import torch
+    rng = np.random.default_rng(length + T)
+    lens, pt, mp, n, kv4, vals = make_cache(rng, [length, 40], ps, H_kv, D)
+    G = H_q // H_kv
+    q = rows_bf16(rng, 2, T, H_q, D)
+    dims = spd.dims_of(2, H_q, H_kv, D, ps, mp, n)
+    ws = spd.workspace(spd.spd_kv4_dense_verify_workspace_size(dims, T, splits))
+    o = torch.full((2, T, H_q, D), float("nan"), dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((2, T, H_q), float("nan"), device="cuda")
+    spd.kv4_dense_verify_attn(dims, T, to_dev(q), dev(kv4), dev(pt), dev(lens), o, ws, lse=lse, num_splits=splits)
+    assert spd.spd_device_status(clear=True) == 0
+    for b in range(2):
+        for t in range(T):
+            seen = np.arange(lens[b]) <= lens[b] - T + t
+            for hq in range(H_q):
+                check_row(host(o)[b, t, hq], host(lse)[b, t, hq], q[b, t, hq], vals[b][0][:, hq // G], vals[b][1][:, hq // G],
+                          D ** -0.5, seen, (b, t, hq))
+    if T == 1:
+        k_max = mp
+        sel = np.zeros((2, H_kv, k_max), np.int32)
+        nsel = np.zeros((2, H_kv), np.int32)
+        for b in range(2):
+            P = -(-int(lens[b]) // ps)
+            for h in range(H_kv):
+                sel[b, h, :P], nsel[b, h] = rng.permutation(P), P
+        ws = spd.workspace(spd.spd_kv4_sparse_decode_workspace_size(dims, k_max, splits))
+        spd.kv4_sparse_decode_attn(dims, to_dev(q), dev(kv4), dev(pt), dev(lens), dev(sel), dev(nsel), k_max, o, ws, lse=lse,
+                                   num_splits=splits)
+        assert spd.spd_device_status(clear=True) == 0
+        for b in range(2):
+            for hq in range(H_q):
+                check_row(host(o)[b, 0, hq], host(lse)[b, 0, hq], q[b, 0, hq], vals[b][0][:, hq // G], vals[b][1][:, hq // G],
+                          D ** -0.5, np.ones(lens[b], bool), (b, hq))
+
+
+@pytest.mark.parametrize("T,H_q", [(1, 4), (4, 8), (7, 4), (8, 8)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_kv4_empty_and_short_sequences(spd, T, H_q, D):
+    """Idle slots of a padded batch: no tokens at all, and fewer tokens than positions (rows that see nothing give
+    zeros and -inf), beside ordinary sequences."""
+    import torch
+    rng = np.random.default_rng(T + D)
+    lens, pt, mp, n, kv4, vals = make_cache(rng, [0, 3, 50, 0, 129], 16, 1, D)
+    q = rows_bf16(rng, 5, T, H_q, D)
+    dims = spd.dims_of(5, H_q, 1, D, 16, mp, n)
+    ws = spd.workspace(spd.spd_kv4_dense_verify_workspace_size(dims, T, 0))
+    o = torch.full((5, T, H_q, D), float("nan"), dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((5, T, H_q), float("nan"), device="cuda")
+    spd.kv4_dense_verify_attn(dims, T, to_dev(q), dev(kv4), dev(pt), dev(lens), o, ws, lse=lse)
+    assert spd.spd_device_status(clear=True) == 0
+    for b in range(5):
+        for t in range(T):
+            seen = np.arange(lens[b]) <= lens[b] - T + t
+            for hq in range(H_q):
+                check_row(host(o)[b, t, hq], host(lse)[b, t, hq], q[b, t, hq], vals[b][0][:, 0], vals[b][1][:, 0], D ** -0.5,
+                          seen, (b, t, hq))
+    assert torch.count_nonzero(o[0]) == 0 and torch.count_nonzero(o[3]) == 0
+
+
+@pytest.mark.parametrize("T", [1, 3, 8])
+@pytest.mark.parametrize("D", [64, 128])
+def test_kv4_logits_that_grow_along_the_sequence(spd, T, D):
+    """The largest logit moves up by tens of nats, again and again: every rescaling of what was summed before.
+    Some rows fall instead, and some heads see the growth from the other side."""
+    import torch
+    rng = np.random.default_rng(T * D)
+    H_q, length, ps = 4, 1500, 32
+    lens, pt, mp, n, _, _ = paged(rng, [length], ps, 1, D)
+    u = np.where(rng.random(D) < 0.5, 1.0, -1.0)
+    k = ref.bf16(np.linspace(0.5, 6.0, length)[:, None, None] * u + 0.1 * rng.standard_normal((length, 1, D)))
+    v = rows_bf16(rng, length, 1, D)
+    dims = spd.dims_of(1, H_q, 1, D, ps, mp, n)
+    cache, summ = spd.kv4_cache(dims), torch.zeros((1, 1, mp, 2, D), dtype=torch.bfloat16, device="cuda")
+    spd.kv4_append(dims, length, cache, dev(pt), dev(lens), to_dev(k[None]), to_dev(v[None]), summ)
+    kd, vd = ref.kv4_values(*ref.kv4_quantise(k, 0), 0)[:, 0], ref.kv4_values(*ref.kv4_quantise(v, 0), 0)[:, 0]
+    q = ref.bf16(np.array([3.0, -2.0, 0.7, 8.0])[None, None, :, None] * u + 0.2 * rng.standard_normal((1, T, H_q, D)))
+    for splits in (1, 3):
+        ws = spd.workspace(spd.spd_kv4_dense_verify_workspace_size(dims, T, splits))
+        o, lse = torch.empty((1, T, H_q, D), dtype=torch.bfloat16, device="cuda"), torch.empty((1, T, H_q), device="cuda")
+        spd.kv4_dense_verify_attn(dims, T, to_dev(q), cache, dev(pt), dev(lens), o, ws, lse=lse, num_splits=splits)
+        assert spd.spd_device_status(clear=True) == 0
+        for t in range(T):
+            for hq in range(H_q):
+                check_row(host(o)[0, t, hq], host(lse)[0, t, hq], q[0, t, hq], kd, vd, D ** -0.5,
+                          np.arange(length) <= length - T + t, (splits, t, hq))
 
 
 def test_kv4_attention_extremes(spd):
@@ -441,6 +542,13 @@ def test_kv4_cache_past_4_gib(spd):
     for h in range(H):
         check_row(host(o)[0, 0, h], host(lse)[0, 0, h], q[0, 0, h], vals[0][0][:, h], vals[0][1][:, h], D ** -0.5,
                   np.ones(150, bool), h)
+    q9 = rows_bf16(rng, 1, 9, H, D)  # the kernel for more query rows
+    o9, lse9 = torch.empty((1, 9, H, D), dtype=torch.bfloat16, device="cuda"), torch.empty((1, 9, H), device="cuda")
+    ws9 = spd.workspace(spd.spd_kv4_dense_verify_workspace_size(dims, 9))
+    spd.kv4_dense_verify_attn(dims, 9, to_dev(q9), cache, dev(pt2), dev(lens), o9, ws9, lse=lse9)
+    for t in range(9):
+        check_row(host(o9)[0, t, 3], host(lse9)[0, t, 3], q9[0, t, 3], vals[0][0][:, 3], vals[0][1][:, 3], D ** -0.5,
+                  np.arange(150) <= 150 - 9 + t, t)
     k, v = (rows_bf16(rng, 1, 2, H, D) for _ in range(2))
     summ = torch.zeros((1, H, mp, 2, D), dtype=torch.bfloat16, device="cuda")
     ko, vo = (torch.empty((1, 2, H, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
