@@ -377,12 +377,15 @@ def _arg(t, dtypes, what: str, dev: int, numel: int | None = None, rows: bool = 
 def _row_stride(t, D: int, what: str) -> int:
     """Elements between the rows [heads][D] of a [..., heads, D] view (see _arg)."""
     shape, stride = t.shape, t.stride()
-    if len(shape) < 3 or shape[-1] != D:
+    dims = len(shape)
+    if dims < 3 or shape[-1] != D:
         raise SpdError(1, f"{what} must be [..., heads, {D}], not {list(shape)}")
     if stride[-1] != 1 or (stride[-2] != D and shape[-2] > 1):
         raise SpdError(1, f"{what}: the heads and channels of a row must be contiguous")
-    if len(shape) == 3:
-        return stride[0] if shape[0] > 1 else shape[-2] * D
+    if dims == 3:
+        return stride[0] if shape[0] > 1 else shape[1] * D
+    if dims == 4 and shape[0] > 1 and (shape[1] == 1 or stride[0] == stride[1] * shape[1]):
+        return stride[0] if shape[1] == 1 else stride[1]
     step, n = None, 1
     for size, s in zip(reversed(shape[:-2]), reversed(stride[:-2])):
         if size == 1:
@@ -396,14 +399,15 @@ def _row_stride(t, D: int, what: str) -> int:
 
 
 def _rope_of(rope, q_weight, k_weight, eps: float, interleaved: bool, D: int, dev: int) -> Rope:
-    if rope is None:
-        n_pos, rot, table = 0, 0, None
-    else:
-        if rope.dim() != 3 or rope.shape[1] != 2:
-            raise SpdError(1, f"rope must be [n_pos, 2, rot_dim / 2], not {list(rope.shape)}")
-        n_pos, rot, table = rope.shape[0], 2 * rope.shape[2], _arg(rope, _F32, "rope", dev)
-    return Rope(table, n_pos, rot, 1 if interleaved else 0, eps, _arg(q_weight, _B16, "q_weight", dev, D),
-                _arg(k_weight, _B16, "k_weight", dev, D))
+    n_pos, rot, table = 0, 0, None
+    if rope is not None:
+        shape = rope.shape
+        if len(shape) != 3 or shape[1] != 2:
+            raise SpdError(1, f"rope must be [n_pos, 2, rot_dim / 2], not {list(shape)}")
+        n_pos, rot, table = shape[0], 2 * shape[2], _arg(rope, _F32, "rope", dev)
+    return Rope(table, n_pos, rot, 1 if interleaved else 0, eps,
+                None if q_weight is None else _arg(q_weight, _B16, "q_weight", dev, D),
+                None if k_weight is None else _arg(k_weight, _B16, "k_weight", dev, D))
 
 
 def qk_norm_rope(q, k, positions, rope, q_out, k_out, q_weight=None, k_weight=None, eps: float = 1e-6,
