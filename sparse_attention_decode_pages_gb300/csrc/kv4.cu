@@ -29,10 +29,11 @@ __device__ __forceinline__ uint4 kv4_values(uint32_t codes, uint32_t scale_byte,
 }
 
 // a / s rounded correctly, r = 1 / s rounded correctly (Markstein: the quotient corrected by
-// its exact remainder); for the finite magnitudes met here.
+// its exact remainder); for the finite magnitudes met here.  With the remainder taken as
+// q s - a a zero quotient keeps a's sign, for a = -0 and for s = r = 0 too.
 __device__ __forceinline__ float quotient(float a, float s, float r) {
     const float q = a * r;
-    return fmaf(fmaf(-q, s, a), r, q);
+    return fmaf(-fmaf(q, s, -a), r, q);
 }
 
 // Quantises the lane's eight channels (its group's other eight are the neighbour
@@ -66,14 +67,13 @@ __device__ __forceinline__ uint32_t kv4_quantise(const uint4& u, float exp2, flo
     scale_byte = to_e4m3(quotient(amax * inv_exp2, 6.f, 1.f / 6.f));
     const float s1 = e4m3_value(scale_byte);
     const float s = s1 * exp2, r = s1 > 0.f ? __frcp_rn(s1) * inv_exp2 : 0.f;  // scale 0: the codes are zeros
-    uint32_t codes = 0;
+    float y[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float lo = __uint_as_float(e[i] << 16), hi = __uint_as_float(e[i] & 0xffff0000u);
-        // (the sign of zeros stays)
-        codes |= to_e2m1x2(copysignf(quotient(lo, s, r), lo), copysignf(quotient(hi, s, r), hi)) << (8 * i);
+        y[2 * i] = quotient(__uint_as_float(e[i] << 16), s, r);
+        y[2 * i + 1] = quotient(__uint_as_float(e[i] & 0xffff0000u), s, r);
     }
-    return codes;
+    return to_e2m1x8(y);
 }
 
 // One CTA per (sequence, touched page, two KV heads), four warps a head: each takes

@@ -52,16 +52,19 @@ __device__ __forceinline__ float e4m3_value(uint32_t byte) {
     return __half2float(__ushort_as_half((unsigned short)(h & 0xffffu)));
 }
 
-// Two floats as a byte of e2m1 codes (lo in the low bits): nearest, ties to the even
-// code, saturating at 6.
-__device__ __forceinline__ uint32_t to_e2m1x2(float lo, float hi) {
-    uint32_t b;
-    asm("{\n\t.reg .b8 t, z;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\t"
-        "mov.b32 %0, {t, t, t, t};\n\t}"
-        : "=r"(b)
-        : "f"(hi), "f"(lo));
-    return b & 0xffu;
+// Eight floats as e2m1 codes, the first in the lowest bits: nearest, ties to the even code,
+// saturating at 6.
+__device__ __forceinline__ uint32_t to_e2m1x8(const float* y) {
+    uint32_t codes;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(codes)
+        : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
+    return codes;
 }
 
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
