@@ -98,8 +98,7 @@ __device__ __forceinline__ void load_columns(uint32_t taddr, uint32_t (&v)[N]) {
     tmem_wait_ld();
 }
 
-template <int N>
-__device__ __forceinline__ void store_columns(uint32_t taddr, const uint32_t (&v)[N]) {
+__device__ __forceinline__ void store_columns(uint32_t taddr, const uint32_t (&v)[8]) {
     __syncwarp();
     tmem_st(taddr, v);
     tmem_wait_st();
@@ -506,7 +505,7 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
                     load_columns<8>(tm_o + r0 + r + my_lanes, o);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * s_corr[r0 + r + i]);
-                    store_columns<8>(tm_o + r0 + r + my_lanes, o);
+                    store_columns(tm_o + r0 + r + my_lanes, o);
                 }
             }
 #pragma unroll
