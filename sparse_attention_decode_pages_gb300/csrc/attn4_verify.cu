@@ -22,17 +22,18 @@
 // A ninth warp issues the copies and, one elected lane, the products, which run while the
 // others convert: S = K Q^T behind the conversion of V, and O += V^T P^T behind that of the
 // next step's K.  (mma.sync blocks its SM quarter's issue for 8 cycles each: the same
-// work took 502 us with it where this takes _VERIFY_.)
+// work took 502 us with it where this takes 393.)
 //
 // Queries are scaled by a power of two into fp16's range (the factor goes into the
 // logits' scale).  Online softmax in fp32 in base 2; a column's reference moves only when a
 // logit exceeds it by kHead4 (attn4.cuh).  One barrier of the converting warps a step carries
 // the vote on the references.
 //
-// 64 sequences of 8K-16K tokens, 7 positions, 32 / 8 heads of 128: _VERIFY_, _VERIFYGB_ of keys
-// and values.  Bound by the handshake between conversions and products (a step of 128 tokens
-// takes ~1.45 us with two CTAs on an SM; without any conversion, softmax or product it
-// still took 1.2) and a unit's start and end (~8 us).
+// 64 sequences of 8K-16K tokens, 7 positions, 32 / 8 heads of 128: 393 us, 2.3 TB/s of keys and
+// values, 34 % of the measured copy peak.  Bound by the chain of a step (a wait for the copy, the
+// conversions, two hand-overs to the products and back, the vote): 1.8 us for 128 tokens
+// in each of the two CTAs of an SM, hardly less with the conversions, the softmax or the products
+// taken out one at a time; and by a unit's start and end, 9 to 12 us.
 #include <atomic>
 
 #include "attn4.cuh"

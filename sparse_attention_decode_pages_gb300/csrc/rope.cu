@@ -4,7 +4,10 @@
 // cache and the touched pages' key summaries rebuilt (kv_append_rope).
 //
 // Both read every element once and write it once; what bounds them is memory
-// for long prompts and the launch for single tokens.
+// for long prompts and the launch for single tokens.  Measured, heads of 128:
+// qk_norm_rope of 32 / 8 heads, 16,381 tokens: 67.2 us, 5.1 TB/s, 75 % of the measured copy
+// peak; one token 2.2 us.  kv_append_rope of 16 / 8 heads, 4 x 4,095 tokens: 54.7 us,
+// 5.0 TB/s, 74 %; 64 sequences' single tokens 3.1 us.
 #include "rope.cuh"
 
 namespace spd {
@@ -14,13 +17,14 @@ constexpr int kRopeWarps = kRopeThreads / 32;
 // A warp takes kRopeTurns rows of heads a lane group at a time from one token: four
 // (D = 128) or eight (D = 64) heads whose loads are in flight together and share the
 // token's angles and the weights.  (32 + 8 heads of 128, one row / 16,381 rows: 2 turns
-// 1.5 / 72.7 us, 4 turns 2.2 / 72.2 us, 8 turns 3.4 / 90.9 us.)
+// 2.2 / 67.2 us, 4 turns 3.8 / 113 us.)
 constexpr int kRopeTurns = 2;
 
 __host__ __device__ constexpr int rope_heads_per_warp(int D) { return kRopeTurns * 32 / (D / 8); }
 
 // Tokens of a warp: the second shares the first one's weights, addresses and rotation, and its
-// loads are in flight with the first one's.  (16,381 rows: 1 / 2 / 4 tokens 70 / 67 / 106 us.)
+// loads are in flight with the first one's.  (One row / 16,381 rows: 1 token
+// 1.6 / 70.3 us, 2 tokens 2.2 / 67.2; 4 tokens 106.)
 constexpr int kRopeTokens = 2;
 
 // One side (queries or keys) of kRopeTokens tokens by one warp: heads h0 ... of `heads` of rows
@@ -117,8 +121,11 @@ cudaError_t launch_qk_norm_rope(const RopeArgs& a, cudaStream_t st) {
 // rotated and stored, and the channel-wise min / max of all valid rows, as rounded,
 // joined through shared memory, becomes the page's summary.  The CTAs behind them take
 // the query heads as qk_norm_rope does.
-constexpr int kNewBatch = 1;     // groups of new rows whose loads a lane keeps in flight
-constexpr int kPageHeads = 2;    // KV heads of an append's CTA
+// Groups of new rows whose loads a lane keeps in flight (1 / 2: 54.7 / 56.2 us for the 4 x 4,095
+// tokens, 3.1 / 3.5 for 64 single ones), and KV heads of an append's CTA (1 / 2 / 4: 57.7 /
+// 54.7 / 52.9 and 3.5 / 3.1 / 3.3 us; four leave half of the warps idle where there are two).
+constexpr int kNewBatch = 1;
+constexpr int kPageHeads = 2;
 constexpr int kPageParts = kRopeWarps / kPageHeads;
 
 template <int D>

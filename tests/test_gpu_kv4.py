@@ -94,6 +94,34 @@ def test_kv4_append_and_read_are_exact(spd, lens, T, ps, H, D, k_exp, v_exp, spr
         assert np.array_equal(host(out), ref.kv4_values(*ref.kv4_quantise(rows, e), e))
 
 
+@pytest.mark.parametrize("k_exp,v_exp", [(0, 7), (-64, 64)])
+def test_kv4_codes_of_every_quotient(spd, k_exp, v_exp):
+    """Every scale against every bf16 magnitude from 2^-5 scales to the largest code, both signs, and zeros of both."""
+    import torch
+    ps, H, D = 64, 1, 128
+    scales = ref.e4m3_values()[1:]
+    mags = np.outer(np.arange(128, 256), 2.0 ** np.arange(-12, -4)).reshape(-1)  # [2^-5, 16) times a power of two
+    groups = []
+    for s in scales:
+        x = mags * 2.0 ** np.floor(np.log2(s))
+        x = np.concatenate([x[x < 6 * s], [0.0, -0.0]])
+        x = np.concatenate([x, -x])
+        x = np.append(x, np.zeros(-len(x) % 15)).reshape(-1, 15)
+        groups.append(np.concatenate([np.full((len(x), 1), 6 * s), x], 1))  # 6 s: the group's scale is s
+    g = np.concatenate(groups)
+    g = np.concatenate([g, np.zeros((-len(g) % (D // 16), 16))])
+    T = len(g) * 16 // D
+    lens, pt, mp, n, _, _ = paged(np.random.default_rng(1), [T], ps, H, D)
+    k, v = (g.reshape(1, T, H, D) * 2.0 ** e for e in (k_exp, v_exp))
+    assert np.array_equal(k, ref.bf16(k)) and np.array_equal(v, ref.bf16(v))
+    want, _ = append_reference(np.zeros((n, H, 2, ps * D * 9 // 16), np.uint8), pt, lens, T, k, v, ps, k_exp, v_exp)
+    dims = spd.dims_of(1, H, H, D, ps, mp, n)
+    cache, summ = spd.kv4_cache(dims), torch.zeros((1, H, mp, 2, D), dtype=torch.bfloat16, device="cuda")
+    spd.kv4_append(dims, T, cache, dev(pt), dev(lens), to_dev(k), to_dev(v), summ, k_exp=k_exp, v_exp=v_exp)
+    assert spd.spd_device_status(clear=True) == 0
+    assert np.array_equal(cache.cpu().numpy(), want)
+
+
 def test_kv4_append_of_infinities_and_nan(spd):
     import torch
     rng = np.random.default_rng(5)
