@@ -40,8 +40,11 @@
  *    calls keep in it (unit queue, split tickets, the step's chain) MUST be
  *    zero before the first call that uses the buffer (zero the whole buffer
  *    once); every successful call leaves them zero again, so a buffer can be
- *    reused by any later call on the same stream.  Calls that overlap on the
- *    GPU must use different workspaces.
+ *    reused by any later call with the same dims on the same stream (zero it again
+ *    before a call with a larger B * H_kv than the call before; the calls over the
+ *    4-bit cache and token_logprobs keep their tickets apart, so a buffer that serves
+ *    those alone needs no zeroing, whatever their sizes).  Calls that overlap on
+ *    the GPU must use different workspaces.
  *  - Errors: argument problems are reported synchronously by the returned
  *    status (nothing is launched); spd_last_error() gives a message.  Problems
  *    only the GPU can see (a page id outside [0, num_phys_pages), a selection
@@ -502,8 +505,9 @@ spd_status kv4_read(const spd_dims *dims, int32_t T, const uint8_t *kv4, int32_t
 /*
  * kv4_sparse_decode_attn / kv4_dense_verify_attn -- sparse_decode_attn and
  * dense_verify_attn over the 4-bit cache: arguments, limits, errors and results as
- * there, over the values that the cache stands for.  Workspaces by the sizes below
- * (zero before the first use, left zero).
+ * there, over the values that the cache stands for; softmax_scale * 2^k_exp finite in
+ * fp32, num_splits ignored where B * H_kv > 16384 (no row is split then).  Workspaces
+ * by the sizes below (tickets zero before the first use, left zero).
  */
 size_t spd_kv4_sparse_decode_workspace_size(const spd_dims *dims, int32_t k_max, int32_t num_splits);
 size_t spd_kv4_dense_verify_workspace_size(const spd_dims *dims, int32_t T, int32_t num_splits);

@@ -110,6 +110,11 @@ struct Kv4Args {
 cudaError_t launch_kv4_append(const Kv4Args& a, cudaStream_t st);
 cudaError_t launch_kv4_read(const Kv4Args& a, cudaStream_t st);
 
+// Split tickets at the start (16 bytes on) of the workspaces of the 4-bit attention and of
+// token_logprobs, the same for every call; more rows than that are not split.
+constexpr int kTickets = 16384;
+constexpr size_t kTicketBytes = (16 + kTickets * sizeof(int) + 255) / 256 * 256;
+
 struct Attn4Args {
     const uint16_t* q;  // [B][T][H_q][D]
     const uint8_t* kv4;

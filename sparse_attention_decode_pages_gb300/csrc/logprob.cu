@@ -93,6 +93,7 @@ inline LpPlan lp_plan(long long rows, int n, bool bf16, int sms) {
     const int most = (nvec + kLpTile - 1) / kLpTile;
     const long long slots = (long long)kLpOcc * sms;
     LpPlan p = {1, nvec};
+    if (rows > kTickets) return p;  // many times the rows that fill the GPU
     long long best = -1;
     for (int parts = 1; parts <= most; ++parts) {
         const int vecs = (nvec + parts - 1) / parts;
@@ -107,7 +108,7 @@ inline LpPlan lp_plan(long long rows, int n, bool bf16, int sms) {
 }
 
 struct LpWs {
-    int* tickets;  // [rows], zero on entry and on exit
+    int* tickets;   // [kTickets], zero on entry and on exit: no call's other data lie on another's
     LpStat* stats;  // [rows][parts]
     u64* keys;      // [rows][parts][top_k]
 };
@@ -115,9 +116,9 @@ struct LpWs {
 __host__ __device__ inline size_t lp_align(size_t x) { return (x + 255) & ~size_t(255); }
 
 inline size_t lp_ws_layout(void* ws, long long rows, int parts, int top_k, LpWs* w) {
-    const size_t o1 = lp_align((size_t)rows * sizeof(int)), o2 = lp_align(o1 + (size_t)rows * parts * sizeof(LpStat));
+    const size_t o1 = kTicketBytes, o2 = lp_align(o1 + (size_t)rows * parts * sizeof(LpStat));
     if (w) {
-        w->tickets = static_cast<int*>(ws);
+        w->tickets = static_cast<int*>(ws) + 4;
         w->stats = reinterpret_cast<LpStat*>(static_cast<char*>(ws) + o1);
         w->keys = reinterpret_cast<u64*>(static_cast<char*>(ws) + o2);
     }

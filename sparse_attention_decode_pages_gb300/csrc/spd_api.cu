@@ -970,6 +970,7 @@ SPD_API spd_status kv4_read(const spd_dims* dims, int32_t T, const uint8_t* kv4,
 // (9 taken).
 static int kv4_splits(const spd_dims* d, int T, int items, bool sparse, int req, int sms) {
     const long long rows = (long long)d->B * d->H_kv;
+    if (rows > kTickets) return 1;  // many times the rows that fill the GPU
     const bool few = T * (d->H_q / d->H_kv) <= kAttn4DecodeRows;
     const double fixed = few ? 6 : 16;
     const long long slots = (long long)sms * (few ? occ_attn4_decode() : occ_attn4_verify());
@@ -1001,12 +1002,28 @@ static int kv4_splits(const spd_dims* d, int T, int items, bool sparse, int req,
     return (items + ips - 1) / ips;
 }
 
+// The workspace: tickets at its start, where the bf16 attention's are, with room for the rows of any
+// call that splits them, so that no partials lie where another call's tickets are.
+static AttnWs kv4_ws_layout(void* ws, long long rows, int S, int R, int D) {
+    AttnWs w;
+    char* base = static_cast<char*>(ws);
+    w.queue = nullptr;
+    w.counters = reinterpret_cast<int*>(base + 16);
+    size_t off = kTicketBytes;
+    w.part_lse = reinterpret_cast<float*>(base + off);
+    if (S > 1) off += align256((size_t)rows * S * R * sizeof(float));
+    w.part_o = reinterpret_cast<float*>(base + off);
+    if (S > 1) off += (size_t)rows * S * R * D * sizeof(float);
+    w.bytes = off;
+    return w;
+}
+
 static size_t kv4_attn_ws(const spd_dims* dims, int T, int items, bool sparse, int32_t num_splits) {
     spd_status st = SPD_OK;
     DevInfo* d = dev_info(&st);
     if (!d) return 0;
     const int S = kv4_splits(dims, T, items, sparse, num_splits, d->sms);
-    return attn_ws_layout(nullptr, (long long)dims->B * dims->H_kv, S, T * (dims->H_q / dims->H_kv), dims->D).bytes;
+    return kv4_ws_layout(nullptr, (long long)dims->B * dims->H_kv, S, T * (dims->H_q / dims->H_kv), dims->D).bytes;
 }
 
 static spd_status kv4_check_T(const spd_dims* dims, int32_t T) {
@@ -1037,7 +1054,9 @@ static spd_status kv4_attn(const spd_dims* dims, int32_t T, const spd_bf16* q, c
     const bool sparse = sel != nullptr;
     spd_status st = kv4_exps(k_exp, v_exp);
     if (st != SPD_OK) return st;
-    if (!(scale >= -3.4e38f && scale <= 3.4e38f)) return fail(SPD_ERR_INVALID_ARG, "softmax_scale is not finite");
+    const double scale_log2 = (double)scale * 1.4426950408889634 * (double)exp2f((float)k_exp);
+    if (!(scale_log2 >= -3.4e38 && scale_log2 <= 3.4e38))
+        return fail(SPD_ERR_INVALID_ARG, "softmax_scale (times 2^k_exp) is not finite in 32 bits");
     if (num_splits < 0) return fail(SPD_ERR_INVALID_ARG, "num_splits < 0");
     if (!q || !kv4 || !page_table || !seq_lens || !o) return fail(SPD_ERR_INVALID_ARG, "NULL pointer argument");
     if (!aligned16(q) || !aligned16(kv4) || !aligned16(o))
@@ -1048,10 +1067,9 @@ static spd_status kv4_attn(const spd_dims* dims, int32_t T, const spd_bf16* q, c
     const int S = kv4_splits(dims, T, items, sparse, num_splits, d->sms);
     const long long rows = (long long)dims->B * dims->H_kv;
     if (rows * S >= (1LL << 31)) return fail(SPD_ERR_UNSUPPORTED, "B * H_kv * num_splits must be < 2^31");
-    const size_t need = attn_ws_layout(nullptr, rows, S, R, dims->D).bytes;
-    if (!ws || ws_bytes < need) return fail(SPD_ERR_WORKSPACE, "workspace %zu bytes < %zu", ws_bytes, need);
+    const AttnWs w = kv4_ws_layout(ws, rows, S, R, dims->D);
+    if (!ws || ws_bytes < w.bytes) return fail(SPD_ERR_WORKSPACE, "workspace %zu bytes < %zu", ws_bytes, w.bytes);
     if (!aligned16(ws)) return fail(SPD_ERR_INVALID_ARG, "ws must be 16-byte aligned");
-    const AttnWs w = attn_ws_layout(ws, rows, S, R, dims->D);
     Attn4Args a = {};
     a.q = q;
     a.kv4 = kv4;
@@ -1070,7 +1088,7 @@ static spd_status kv4_attn(const spd_dims* dims, int32_t T, const spd_bf16* q, c
     a.num_phys = dims->num_phys_pages;
     a.pages_per_split = (items + S - 1) / S;
     a.num_splits = S;
-    a.scale_log2 = (float)((double)scale * 1.4426950408889634 * (double)exp2f((float)k_exp));
+    a.scale_log2 = (float)scale_log2;
     a.v_scale = exp2f((float)v_exp);
     a.o = o;
     a.lse = lse;

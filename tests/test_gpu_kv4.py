@@ -585,3 +585,38 @@ def test_kv4_cache_past_4_gib(spd):
     assert np.array_equal(host(ko), ref.kv4_values(*ref.kv4_quantise(k, 0), 0))
     assert np.array_equal(host(vo), ref.kv4_values(*ref.kv4_quantise(v, 0), 0))
     assert spd.spd_device_status(clear=True) == 0
+
+
+def test_one_workspace_for_calls_of_different_sizes(spd):
+    """Split calls of few and of many rows and scored rows through one buffer, in turn: the bits of buffers of their own."""
+    import torch
+    rng = np.random.default_rng(77)
+    calls = []
+    for lens, T, H_q, H_kv, splits in (([200, 90, 310], 3, 16, 8, 3), ([400], 1, 2, 1, 4), ([250, 130], 1, 32, 16, 2)):
+        lens, pt, mp, n, kv4, _ = make_cache(rng, lens, 16, H_kv, 64)
+        dims, B = spd.dims_of(len(lens), H_q, H_kv, 64, 16, mp, n), len(lens)
+        q, args = to_dev(rows_bf16(rng, B, T, H_q, 64)), (dev(kv4), dev(pt), dev(lens))
+
+        def attend(ws, dims=dims, T=T, q=q, args=args, splits=splits):
+            o = torch.full(q.shape, float("nan"), dtype=torch.bfloat16, device="cuda")
+            lse = torch.full(q.shape[:-1], float("nan"), device="cuda")
+            spd.kv4_dense_verify_attn(dims, T, q, *args, o, ws, lse=lse, num_splits=splits)
+            return o, lse
+
+        calls.append((spd.spd_kv4_dense_verify_workspace_size(dims, T, splits), attend))
+    for rows in (3, 70):
+        x, t = dev(rng.standard_normal((rows, 20001)).astype(np.float32)), dev(rng.integers(0, 20001, rows).astype(np.int32))
+
+        def score(ws, rows=rows, x=x, t=t):
+            out = [torch.full((rows,), float("nan"), device="cuda") for _ in range(3)]
+            ids, top = torch.full((rows, 5), -9, dtype=torch.int32, device="cuda"), torch.zeros((rows, 5), device="cuda")
+            spd.token_logprobs(x, t, out[0], ws, entropy=out[1], lse=out[2], top_ids=ids, top_logprobs=top)
+            return (*out, ids, top)
+
+        calls.append((spd.spd_token_logprobs_workspace_size(rows, 20001, 5), score))
+    want = [f(spd.workspace(size)) for size, f in calls]
+    ws = spd.workspace(max(size for size, _ in calls))
+    for i in (0, 1, 0, 3, 2, 4, 1, 3, 0, 2, 3, 4, 0):
+        for got, ref_ in zip(calls[i][1](ws), want[i]):
+            assert torch.equal(got, ref_), i
+    assert spd.spd_device_status(clear=True) == 0

@@ -91,6 +91,7 @@ def test_kv4_refusals(spd):
     assert sparse(k_max=0) == INVALID and sparse(sel=None) == INVALID and sparse(q=None) == INVALID
     assert sparse(c=ODD) == INVALID and sparse(o=ODD) == INVALID and sparse(ke=99) == INVALID
     assert sparse(scale=float("nan")) == INVALID and sparse(splits=-1) == INVALID
+    assert sparse(scale=1e30, ke=64) == INVALID
     assert sparse(dims=z) == OK and dense(dims=z) == OK
     assert dense(T=0) == UNSUPPORTED and dense(T=33) == UNSUPPORTED
     assert dense(q=ODD) == INVALID and dense(ve=-99) == INVALID and dense(scale=float("inf")) == INVALID
