@@ -28,6 +28,12 @@ __device__ __forceinline__ int query_exponent(float amax) {
     return amax == 0.f ? 0 : e > 126 ? 126 : e < -126 ? -126 : e;
 }
 
+// A CTA whose wait ran out still waits for its own copies and products in flight, whatever limit
+// the caller has set: the memory that they write is another CTA's after it.
+__device__ __forceinline__ unsigned long long drain_limit(const Attn4Args& a) {
+    return a.wait_ns > 2000000000ull ? a.wait_ns : 2000000000ull;
+}
+
 // Called by every thread of the CTA behind its partials' stores: whether this was the last of the
 // row's nsplit units to finish (its ticket is then reset for the next call).
 __device__ __forceinline__ bool last_split(const Attn4Args& a, int row, int nsplit, int* s_last) {

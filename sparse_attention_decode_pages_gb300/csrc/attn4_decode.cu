@@ -248,10 +248,11 @@ __global__ void __launch_bounds__(128, DecodeCfg<D>::OCC) decode4_kernel(const A
     int slot = 0;
     uint32_t parity = 0;
     for (int m = 0; m < pairs; ++m) {
-        if (!mbar_wait_bounded(full + slot, parity, a.status, a.wait_ns)) {
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(full + slot, parity, a.status, a.wait_ns))) {
             // the pairs in flight land before the shared memory is used for anything else
-            for (int j = m + 1; j < min(m + STAGES, pairs); ++j)
-                mbar_wait_bounded(full + j % STAGES, (uint32_t)(j / STAGES) & 1u, a.status, a.wait_ns);
+            for (int j = m; j < min(m + STAGES, pairs); ++j)
+                mbar_wait_bounded(full + j % STAGES, (uint32_t)(j / STAGES) & 1u, a.status, drain_limit(a));
+            __syncwarp();
             break;
         }
         const int2 first = meta[slot];

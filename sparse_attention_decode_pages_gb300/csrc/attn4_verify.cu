@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
     constexpr int STAGES = C::STAGES, WARPS = C::WARPS, CHUNKS = C::CHUNKS, NH = C::NH;
     constexpr int CODES = kv4_codes_bytes(16, D), HALF = kv4_half_bytes(16, D);  // of a chunk
     extern __shared__ uint8_t smem_raw[];
-    __shared__ int s_last, s_late;
+    __shared__ int s_last, s_late[2];  // s_late: of even and of odd steps, so that a thread that is a step ahead tells no other
     __shared__ uint32_t s_tmem;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float2* s_fr = reinterpret_cast<float2*>(smem + C::OFF_FR);
@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
 #pragma unroll
         for (int i = 0; i < STAGES + 4; ++i) mbar_init(full + i, i == STAGES ? WARPS : 1);
         mbar_fence_init();
-        s_late = 0;
+        s_late[0] = s_late[1] = 0;
     }
     pdl_wait();
     pdl_trigger();
@@ -315,9 +315,11 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
 
     if (warp == WARPS) {
         // ============================================================ copies and products
+        int issued = min(STAGES, steps), s_issued = 0, o_issued = 0;  // steps copied, and multiplied
         for (int k = 0; k < steps; ++k) {
             if (!__all_sync(0xffffffffu, mbar_sleep_bounded(k_ready, (uint32_t)k & 1u, a.status, a.wait_ns))) break;
             tmem_fence_after();
+            s_issued = k + 1;
             if (elect_one()) {
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i)
@@ -334,6 +336,7 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
             }
             if (!__all_sync(0xffffffffu, mbar_sleep_bounded(p_ready, (uint32_t)k & 1u, a.status, a.wait_ns))) break;
             tmem_fence_after();
+            o_issued = k + 1;
             if (elect_one()) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
@@ -342,8 +345,16 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
                 umma_commit(o_done);
             }
             __syncwarp();
-            if (kn < steps) issue(kn);
+            if (kn < steps) {
+                issue(kn);
+                issued = kn + 1;
+            }
         }
+        // the copies in flight land, and the products end, before their memory is given back
+        for (int j = max(0, issued - STAGES); j < issued; ++j)
+            mbar_sleep_bounded(full + j % STAGES, (uint32_t)(j / STAGES) & 1u, a.status, drain_limit(a));
+        if (s_issued > 0) mbar_sleep_bounded(s_done, (uint32_t)(s_issued - 1) & 1u, a.status, drain_limit(a));
+        if (o_issued > 0) mbar_sleep_bounded(o_done, (uint32_t)(o_issued - 1) & 1u, a.status, drain_limit(a));
     } else {
     // ================================================================ conversions and softmax
     // V of this warp's chunk: this lane's token (and the one 8 behind) and 32 channels; the eight
@@ -359,7 +370,6 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
     float l[NH];  // sums of this thread's weights
 #pragma unroll
     for (int r = 0; r < NH; ++r) l[r] = 0.f;
-    bool gone = false;  // a wait ran out
     int done = 0;       // steps whose second product was issued
     RingPos<STAGES> ring;
 
@@ -468,9 +478,9 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
                             pack_f16(p[8 * i + 4], p[8 * i + 5]), pack_f16(p[8 * i + 6], p[8 * i + 7]));
             async_proxy_fence();
             tmem_fence_before();
-            if (!ok) s_late = 1;
+            if (!ok) s_late[k & 1] = 1;
             const bool move = converters_or<32 * WARPS>(top > kMost4);  // some weight is too large
-            late = s_late != 0;
+            late = s_late[k & 1] != 0;
             if (!move || moved || late) break;
             // the references move to the largest logit of each row among this step's tokens
 #pragma unroll 1
@@ -512,20 +522,13 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
 #pragma unroll
             for (int r = 0; r < NH; ++r) l[r] *= s_corr[r0 + r];
         }
-        if (late) {
-            gone = true;
-            break;
-        }
+        if (late) break;
         if (tid == 0) mbar_arrive(p_ready);
         done = k + 1;
 #pragma unroll
         for (int r = 0; r < NH; ++r) l[r] += p[r];
     }
 
-    // the copies in flight land, and the products end, before their memory is given back
-    if (gone)
-        for (int j = done; j < min(done + STAGES, steps); ++j)
-            mbar_sleep_bounded(full + j % STAGES, (uint32_t)(j / STAGES) & 1u, a.status, a.wait_ns);
     if (done > 0) mbar_sleep_bounded(o_done, (uint32_t)(done - 1) & 1u, a.status, a.wait_ns);
     tmem_fence_after();
     uint32_t o[NH];

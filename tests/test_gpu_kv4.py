@@ -620,3 +620,36 @@ def test_one_workspace_for_calls_of_different_sizes(spd):
         for got, ref_ in zip(calls[i][1](ws), want[i]):
             assert torch.equal(got, ref_), i
     assert spd.spd_device_status(clear=True) == 0
+
+
+@pytest.mark.parametrize("T,H_q,D,splits", [(1, 8, 128, 2), (1, 8, 64, 1), (6, 16, 128, 2), (7, 8, 64, 1)])
+def test_kv4_attention_with_waits_that_run_out(spd, T, H_q, D, splits):
+    """A limit that no copy meets: the calls return with the timeout bit (or, should every copy be early, clean), all
+    of their waits over, and later calls with the usual limit are those of before."""
+    import torch
+    rng = np.random.default_rng(T + D)
+    lens, pt, mp, n, kv4, _ = make_cache(rng, [700, 300], 16, 2, D)
+    dims = spd.dims_of(2, H_q, 2, D, 16, mp, n)
+    q, cache, d_pt, d_lens = to_dev(rows_bf16(rng, 2, T, H_q, D)), dev(kv4), dev(pt), dev(lens)
+    size = spd.spd_kv4_dense_verify_workspace_size(dims, T, splits)
+
+    def run():
+        o = torch.full((2, T, H_q, D), float("nan"), dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((2, T, H_q), float("nan"), device="cuda")
+        spd.kv4_dense_verify_attn(dims, T, q, cache, d_pt, d_lens, o, spd.workspace(size), lse=lse, num_splits=splits)
+        torch.cuda.synchronize()
+        return o, lse
+
+    first = run()
+    assert spd.spd_device_status(clear=True) == 0
+    usual = spd.spd_wait_limit_ns()
+    try:
+        spd.spd_set_wait_limit_ns(1)
+        for _ in range(3):
+            run()
+            assert spd.spd_device_status(clear=True) & ~spd.DEV_TIMEOUT == 0
+    finally:
+        spd.spd_set_wait_limit_ns(usual)
+    for got, want in zip(run(), first):
+        assert torch.equal(got, want)
+    assert spd.spd_device_status(clear=True) == 0
