@@ -55,6 +55,10 @@ struct Verify4Cfg {
     static constexpr int CHUNK = kv4_tile_bytes(16, D);   // bytes of 16 tokens' keys and values
     static constexpr int STEP = CHUNKS * CHUNK;
     static constexpr int STAGES = N == 64 ? 2 : 3;        // steps in the ring
+    // Whether a step's keys are converted, and multiplied, before the softmax of the step before:
+    // a second place for K and S in tensor memory, and a third step in the ring
+    static constexpr bool AHEAD = N < 64;
+    static constexpr int NB = AHEAD ? 2 : 1;              // places of K and S
     // V^T: 64-channel blocks of 128 rows (tokens) of 128 bytes, 128-byte swizzle
     static constexpr int VBLOCK = 128 * 128;
     static constexpr int OFF_V = 0;
@@ -68,11 +72,11 @@ struct Verify4Cfg {
     static constexpr int OFF_CORR = OFF_RED + 4 * N * 4;  // float [N]
     static constexpr int OFF_OUT = OFF_CORR + N * 4;          // long long [N]: output rows
     static constexpr int OFF_LIM = OFF_OUT + N * 8;           // int [N]: the last position that a row sees
-    static constexpr int OFF_BAR = OFF_LIM + N * 4;           // uint64 [STAGES] and four more
-    static constexpr int OFF_META = OFF_BAR + (STAGES + 4) * 8;  // int [STAGES][CHUNKS]: first positions or -1
+    static constexpr int OFF_BAR = OFF_LIM + N * 4;           // uint64 [STAGES] and six more
+    static constexpr int OFF_META = OFF_BAR + (STAGES + 6) * 8;  // int [STAGES][CHUNKS]: first positions or -1
     static constexpr int BODY = OFF_META + STAGES * CHUNKS * 4;
     // tensor memory: K, S, O
-    static constexpr int COL_S = D / 2, COL_O = COL_S + N;
+    static constexpr int COL_S = NB * D / 2, COL_O = COL_S + NB * N;
     static constexpr int COLUMNS = COL_O + N <= 128 ? 128 : 256;
     // at most 512 / COLUMNS CTAs fit on an SM (227 KB), so that none waits for columns
     static constexpr int LEAST = 227 * 1024 / (512 / COLUMNS + 1);
@@ -151,10 +155,10 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
     long long* s_out = reinterpret_cast<long long*>(smem + C::OFF_OUT);
     int* s_lim = reinterpret_cast<int*>(smem + C::OFF_LIM);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
-    uint64_t* k_ready = full + STAGES;  // K of a step is in tensor memory
-    uint64_t* p_ready = k_ready + 1;    // V and P are in shared memory, and the step's codes are read
-    uint64_t* s_done = p_ready + 1;     // S is there
-    uint64_t* o_done = s_done + 1;      // O is there; V and P may be overwritten
+    uint64_t* k_ready = full + STAGES;  // [2] K of a step is in tensor memory (of even and of odd steps)
+    uint64_t* s_done = k_ready + 2;     // [2] S is there
+    uint64_t* p_ready = s_done + 2;     // V and P are in shared memory, and the step's codes are read
+    uint64_t* o_done = p_ready + 1;     // O is there; V and P may be overwritten
     int* meta = reinterpret_cast<int*>(smem + C::OFF_META);
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int g = lane >> 2, c = lane & 3;
@@ -169,7 +173,7 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
     };
     if (tid == 0) {
 #pragma unroll
-        for (int i = 0; i < STAGES + 4; ++i) mbar_init(full + i, i == STAGES ? WARPS : 1);
+        for (int i = 0; i < STAGES + 6; ++i) mbar_init(full + i, i == STAGES || i == STAGES + 1 ? WARPS : 1);
         mbar_fence_init();
         s_late[0] = s_late[1] = 0;
     }
@@ -316,18 +320,25 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
     if (warp == WARPS) {
         // ============================================================ copies and products
         int issued = min(STAGES, steps), s_issued = 0, o_issued = 0;  // steps copied, and multiplied
-        for (int k = 0; k < steps; ++k) {
-            if (!__all_sync(0xffffffffu, mbar_sleep_bounded(k_ready, (uint32_t)k & 1u, a.status, a.wait_ns))) break;
+        auto multiply_keys = [&](int k) {
+            if (!__all_sync(0xffffffffu, mbar_sleep_bounded(k_ready + (k & 1), (uint32_t)k >> 1 & 1u, a.status, a.wait_ns))) return false;
             tmem_fence_after();
             s_issued = k + 1;
             if (elect_one()) {
+                const int place = k & (C::NB - 1);
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i)
-                    umma_f16_ts(tm_s, tmem + 8 * i, umma_desc(q_smem + (i >> 2) * (N * 128) + (i & 3) * 32, 0, 1024, kSwizzle128),
-                                kIdescS, i > 0);
-                umma_commit(s_done);
+                    umma_f16_ts(tm_s + place * N, tmem + place * (D / 2) + 8 * i,
+                                umma_desc(q_smem + (i >> 2) * (N * 128) + (i & 3) * 32, 0, 1024, kSwizzle128), kIdescS, i > 0);
+                umma_commit(s_done + (k & 1));
             }
             __syncwarp();
+            return true;
+        };
+        for (int k = C::AHEAD ? -1 : 0; k < steps; ++k) {
+            const int ahead = k + (C::AHEAD ? 1 : 0);
+            if (ahead < steps && !multiply_keys(ahead)) break;
+            if (k < 0) continue;
             const int kn = k + STAGES;  // the next step into this one's slot
             if (kn < steps && (kn & 3) == 0) {
                 next_entries();
@@ -353,13 +364,13 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
         // the copies in flight land, and the products end, before their memory is given back
         for (int j = max(0, issued - STAGES); j < issued; ++j)
             mbar_sleep_bounded(full + j % STAGES, (uint32_t)(j / STAGES) & 1u, a.status, drain_limit(a));
-        if (s_issued > 0) mbar_sleep_bounded(s_done, (uint32_t)(s_issued - 1) & 1u, a.status, drain_limit(a));
+        if (s_issued > 0) mbar_sleep_bounded(s_done + (s_issued - 1 & 1), (uint32_t)(s_issued - 1) >> 1 & 1u, a.status, drain_limit(a));
         if (o_issued > 0) mbar_sleep_bounded(o_done, (uint32_t)(o_issued - 1) & 1u, a.status, drain_limit(a));
     } else {
     // ================================================================ conversions and softmax
     // V of this warp's chunk: this lane's token (and the one 8 behind) and 32 channels; the eight
     // lanes that store together cover every bank
-    const int piece = D == 128 ? (lane >> 2 & 1) + 2 * (lane >> 3 & 1) : lane >> 2 & 1;
+    const int piece = D == 128 ? (lane >> 2 & 1) + 2 * ((lane >> 3 ^ lane >> 1) & 1) : lane >> 2 & 1;
     const int v_token = D == 128 ? (lane & 3) + 4 * (lane >> 4) : (lane & 3) + 4 * (lane >> 3);
     const int v_src = warp * C::CHUNK + HALF + v_token * (D / 2) + piece * 16;
     const int v_scale_src = warp * C::CHUNK + HALF + CODES + v_token * (D / 16) + piece * 2;
@@ -371,18 +382,15 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
 #pragma unroll
     for (int r = 0; r < NH; ++r) l[r] = 0.f;
     int done = 0;       // steps whose second product was issued
-    RingPos<STAGES> ring;
+    RingPos<STAGES> ring;  // of the next step whose keys are converted
 
-    for (int k = 0; k < steps; ++k) {
-        const int slot = ring.slot;
-        const uint8_t* stage = smem + C::OFF_RING + slot * C::STEP;
-        bool ok = mbar_sleep_bounded(full + slot, ring.parity, a.status, a.wait_ns);
-        ring.advance();
-
-        // K: this warp's chunk to tensor memory (one that is not there: whatever the ring holds;
-        // its tokens are hidden)
+    // K of step k: this warp's chunk to tensor memory (one that is not there: whatever the ring
+    // holds; its tokens are hidden)
+    auto convert_keys = [&](int k) {
+        const bool there = mbar_sleep_bounded(full + ring.slot, ring.parity, a.status, a.wait_ns);
         {
-            const uint8_t* kt = stage + warp * C::CHUNK;
+            const uint8_t* kt = smem + C::OFF_RING + ring.slot * C::STEP + warp * C::CHUNK;
+            ring.advance();
             uint32_t f[D / 4];  // [column group][row g: two columns, row g + 8: two]
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -413,12 +421,22 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
                 }
             }
             __syncwarp();
-            tmem_st_frag(tmem + ((uint32_t)token_row(warp, 0) << 16), f);
+            tmem_st_frag(tmem + ((uint32_t)token_row(warp, 0) << 16) + (k & (C::NB - 1)) * (D / 2), f);
         }
         tmem_wait_st();
         tmem_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(k_ready);
+        if (lane == 0) mbar_arrive(k_ready + (k & 1));
+        return there;
+    };
+    bool ok = true;
+    int slot = 0;  // of step k
+
+    for (int k = C::AHEAD ? -1 : 0; k < steps; ++k) {
+        const uint8_t* stage = smem + C::OFF_RING + slot * C::STEP;
+        const int ahead = k + (C::AHEAD ? 1 : 0);
+        if (ahead < steps) ok &= convert_keys(ahead);
+        if (k < 0) continue;
 
         // V: this warp's chunk to shared memory, 32 channels of a token at a time; the eight lanes
         // that store together cover every bank
@@ -443,8 +461,9 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
         }
 
         // softmax of this thread's token, for its query rows
-        ok &= mbar_sleep_bounded(s_done, (uint32_t)k & 1u, a.status, a.wait_ns);
+        ok &= mbar_sleep_bounded(s_done + (k & 1), (uint32_t)k >> 1 & 1u, a.status, a.wait_ns);
         tmem_fence_after();
+        const uint32_t my_s = tm_s + (k & (C::NB - 1)) * N + r0 + my_lanes;
         const int chunk_first = meta[slot * CHUNKS + my_chunk];
         const int pos = chunk_first < 0 ? 0x7fffffff : chunk_first + (lane & 15);
         const bool all = __all_sync(0xffffffffu, pos <= len - a.T);  // every row sees every token of the warp
@@ -456,7 +475,7 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
         for (bool moved = false;; moved = true) {
             {
                 uint32_t s[NH];
-                load_columns<NH>(tm_s + r0 + my_lanes, s);
+                load_columns<NH>(my_s, s);
 #pragma unroll
                 for (int r = 0; r < NH; r += 2) {
                     const float4 fr = *reinterpret_cast<const float4*>(s_fr + r0 + r);
@@ -486,7 +505,7 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
 #pragma unroll 1
             for (int r = 0; r < NH; r += 8) {
                 uint32_t s[8];
-                load_columns<8>(tm_s + r0 + r + my_lanes, s);
+                load_columns<8>(my_s + r, s);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const float z = pos > s_lim[r0 + r + i] ? NEG_INF : __uint_as_float(s[i]) * s_fr[r0 + r + i].x;
@@ -525,6 +544,7 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
         if (late) break;
         if (tid == 0) mbar_arrive(p_ready);
         done = k + 1;
+        slot = slot + 1 == STAGES ? 0 : slot + 1;
 #pragma unroll
         for (int r = 0; r < NH; ++r) l[r] += p[r];
     }
