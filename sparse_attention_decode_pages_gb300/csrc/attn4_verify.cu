@@ -72,8 +72,8 @@ struct Verify4Cfg {
     static constexpr int OFF_CORR = OFF_RED + 4 * N * 4;  // float [N]
     static constexpr int OFF_OUT = OFF_CORR + N * 4;          // long long [N]: output rows
     static constexpr int OFF_LIM = OFF_OUT + N * 8;           // int [N]: the last position that a row sees
-    static constexpr int OFF_BAR = OFF_LIM + N * 4;           // uint64 [STAGES] and six more
-    static constexpr int OFF_META = OFF_BAR + (STAGES + 6) * 8;  // int [STAGES][CHUNKS]: first positions or -1
+    static constexpr int OFF_BAR = OFF_LIM + N * 4;           // uint64 [STAGES] and eight more
+    static constexpr int OFF_META = OFF_BAR + (STAGES + 8) * 8;  // int [STAGES][CHUNKS]: first positions or -1
     static constexpr int BODY = OFF_META + STAGES * CHUNKS * 4;
     // tensor memory: K, S, O
     static constexpr int COL_S = NB * D / 2, COL_O = COL_S + NB * N;
@@ -122,22 +122,10 @@ struct RingPos {
     }
 };
 
-// Barriers of the T converting threads: a plain one, and one that says whether any of them
-// gave a true value.
+// A barrier of the T converting threads.
 template <int T>
 __device__ __forceinline__ void converters_sync() {
     asm volatile("barrier.cta.sync 1, %0;" ::"n"(T) : "memory");
-}
-template <int T>
-__device__ __forceinline__ bool converters_or(bool x) {
-    uint32_t any;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(any)
-        : "r"(x ? 1u : 0u), "n"(T)
-        : "memory");
-    return any != 0;
 }
 
 template <int D, int N>
@@ -146,9 +134,10 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
     constexpr int STAGES = C::STAGES, WARPS = C::WARPS, CHUNKS = C::CHUNKS, NH = C::NH;
     constexpr int CODES = kv4_codes_bytes(16, D), HALF = kv4_half_bytes(16, D);  // of a chunk
     extern __shared__ uint8_t smem_raw[];
-    __shared__ int s_last, s_late[2];  // s_late: of even and of odd steps, so that a thread that is a step ahead tells no other
+    __shared__ int s_last, s_move[2];  // s_move: a weight is too large, in an even or an odd step
     __shared__ uint32_t s_tmem;
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    // (an offset to the array, not a rounded address: its accesses stay shared-memory ones)
+    uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
     float2* s_fr = reinterpret_cast<float2*>(smem + C::OFF_FR);
     float* s_red = reinterpret_cast<float*>(smem + C::OFF_RED);
     float* s_corr = reinterpret_cast<float*>(smem + C::OFF_CORR);
@@ -156,9 +145,11 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
     int* s_lim = reinterpret_cast<int*>(smem + C::OFF_LIM);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
     uint64_t* k_ready = full + STAGES;  // [2] K of a step is in tensor memory (of even and of odd steps)
-    uint64_t* s_done = k_ready + 2;     // [2] S is there
-    uint64_t* p_ready = s_done + 2;     // V and P are in shared memory, and the step's codes are read
-    uint64_t* o_done = p_ready + 1;     // O is there; V and P may be overwritten
+    uint64_t* p_ready = k_ready + 2;    // V and P are in shared memory, and the step's codes are read
+    uint64_t* voted = p_ready + 1;      // every warp has said whether its weights are too large
+    uint64_t* level = voted + 1;        // and is as far as the others, where references move
+    uint64_t* s_done = level + 1;       // [2] S is there
+    uint64_t* o_done = s_done + 2;      // O is there; V and P may be overwritten
     int* meta = reinterpret_cast<int*>(smem + C::OFF_META);
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int g = lane >> 2, c = lane & 3;
@@ -173,9 +164,9 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
     };
     if (tid == 0) {
 #pragma unroll
-        for (int i = 0; i < STAGES + 6; ++i) mbar_init(full + i, i == STAGES || i == STAGES + 1 ? WARPS : 1);
+        for (int i = 0; i < STAGES + 8; ++i) mbar_init(full + i, i >= STAGES && i < STAGES + 5 ? WARPS : 1);
         mbar_fence_init();
-        s_late[0] = s_late[1] = 0;
+        s_move[0] = s_move[1] = 0;
     }
     pdl_wait();
     pdl_trigger();
@@ -429,6 +420,15 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
         if (lane == 0) mbar_arrive(k_ready + (k & 1));
         return there;
     };
+    // A barrier of the converting warps that no warp can be held at: false where the wait ran out.
+    uint32_t level_parity = 0;
+    auto all_level = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(level);
+        const bool there = __all_sync(0xffffffffu, mbar_sleep_bounded(level, level_parity, a.status, a.wait_ns));
+        level_parity ^= 1u;
+        return there;
+    };
     bool ok = true;
     int slot = 0;  // of step k
 
@@ -438,39 +438,16 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
         if (ahead < steps) ok &= convert_keys(ahead);
         if (k < 0) continue;
 
-        // V: this warp's chunk to shared memory, 32 channels of a token at a time; the eight lanes
-        // that store together cover every bank
-        if (k > 0) ok &= mbar_sleep_bounded(o_done, (uint32_t)(k - 1) & 1u, a.status, a.wait_ns);
-        const int warp_first = meta[slot * CHUNKS + warp];
-#pragma unroll
-        for (int i = 0; i < D / 64; ++i) {
-            const uint8_t* vt = stage + v_src + i * (8 * (D / 2));
-            const uint4 x = *reinterpret_cast<const uint4*>(vt);
-            uint32_t two = *reinterpret_cast<const uint16_t*>(stage + v_scale_src + i * (8 * (D / 16)));
-            if (warp_first < 0 || warp_first + v_token + 8 * i >= len) two = 0u;  // no token: its bytes may be anything, its scale counts as 0
-            const uint32_t s = e4m3x2_to_f16(two);
-            const uint32_t s_lo = __byte_perm(s, 0, 0x1010), s_hi = __byte_perm(s, 0, 0x3232);
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t v[4];
-                e2m1x8_to_f16(w[j], v);
-                const uint32_t s2 = j < 2 ? s_lo : s_hi;
-                st_shared16((v_dst ^ (j << 4)) + i * 1024, hmul2(v[0], s2), hmul2(v[1], s2), hmul2(v[2], s2), hmul2(v[3], s2));
-            }
-        }
-
         // softmax of this thread's token, for its query rows
         ok &= mbar_sleep_bounded(s_done + (k & 1), (uint32_t)k >> 1 & 1u, a.status, a.wait_ns);
         tmem_fence_after();
         const uint32_t my_s = tm_s + (k & (C::NB - 1)) * N + r0 + my_lanes;
-        const int chunk_first = meta[slot * CHUNKS + my_chunk];
+        const int warp_first = meta[slot * CHUNKS + warp], chunk_first = meta[slot * CHUNKS + my_chunk];
         const int pos = chunk_first < 0 ? 0x7fffffff : chunk_first + (lane & 15);
         const bool all = __all_sync(0xffffffffu, pos <= len - a.T);  // every row sees every token of the warp
         float p[NH];
         // (what runs once a unit is kept short: a unit's first pass through straight code is bound by
         // fetching it)
-        bool late = false;
 #pragma unroll 1
         for (bool moved = false;; moved = true) {
             {
@@ -488,19 +465,44 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
                 for (int r = 0; r < NH; ++r)
                     if (pos > s_lim[r0 + r]) p[r] = 0.f;
             }
-            float top = 0.f;
+            if (!moved) {
+                float top = 0.f;
 #pragma unroll
-            for (int r = 0; r < NH; ++r) top = fmaxf(top, p[r]);
+                for (int r = 0; r < NH; ++r) top = fmaxf(top, p[r]);
+                const bool large = __any_sync(0xffffffffu, top > kMost4);  // some weight is too large
+                if (lane == 0) {
+                    if (large) s_move[k & 1] = 1;
+                    mbar_arrive(voted);
+                }
+                if (k > 0) ok &= mbar_sleep_bounded(o_done, (uint32_t)(k - 1) & 1u, a.status, a.wait_ns);
+            }
 #pragma unroll
             for (int i = 0; i < NH / 8; ++i)
                 st_shared16(p_dst ^ (i << 4), pack_f16(p[8 * i], p[8 * i + 1]), pack_f16(p[8 * i + 2], p[8 * i + 3]),
                             pack_f16(p[8 * i + 4], p[8 * i + 5]), pack_f16(p[8 * i + 6], p[8 * i + 7]));
-            async_proxy_fence();
-            tmem_fence_before();
-            if (!ok) s_late[k & 1] = 1;
-            const bool move = converters_or<32 * WARPS>(top > kMost4);  // some weight is too large
-            late = s_late[k & 1] != 0;
-            if (!move || moved || late) break;
+            if (moved) break;
+
+            // V: this warp's chunk to shared memory, 32 channels of a token at a time
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) {
+                const uint8_t* vt = stage + v_src + i * (8 * (D / 2));
+                const uint4 x = *reinterpret_cast<const uint4*>(vt);
+                uint32_t two = *reinterpret_cast<const uint16_t*>(stage + v_scale_src + i * (8 * (D / 16)));
+                if (warp_first < 0 || warp_first + v_token + 8 * i >= len) two = 0u;  // no token: its bytes may be anything, its scale counts as 0
+                const uint32_t s = e4m3x2_to_f16(two);
+                const uint32_t s_lo = __byte_perm(s, 0, 0x1010), s_hi = __byte_perm(s, 0, 0x3232);
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t v[4];
+                    e2m1x8_to_f16(w[j], v);
+                    const uint32_t s2 = j < 2 ? s_lo : s_hi;
+                    st_shared16((v_dst ^ (j << 4)) + i * 1024, hmul2(v[0], s2), hmul2(v[1], s2), hmul2(v[2], s2), hmul2(v[3], s2));
+                }
+            }
+            ok &= mbar_sleep_bounded(voted, (uint32_t)k & 1u, a.status, a.wait_ns);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok || !*reinterpret_cast<volatile int*>(s_move + (k & 1))) break;
             // the references move to the largest logit of each row among this step's tokens
 #pragma unroll 1
             for (int r = 0; r < NH; r += 8) {
@@ -518,7 +520,8 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
                     s_red[(warp & 3) * N + r0 + r + lane] = __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
                 }
             }
-            converters_sync<32 * WARPS>();
+            ok = all_level();
+            if (!ok) break;
             if (tid < N) {
                 float x = NEG_INF;
 #pragma unroll
@@ -527,7 +530,9 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
                 s_corr[tid] = fast_exp2(old - now);
                 s_fr[tid].y = -now;
             }
-            converters_sync<32 * WARPS>();
+            if (tid == 0) s_move[k & 1] = 0;  // every warp has read it
+            ok = all_level();
+            if (!ok) break;
             if (k > 0) {
 #pragma unroll 1
                 for (int r = 0; r < NH; r += 8) {
@@ -541,8 +546,11 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
 #pragma unroll
             for (int r = 0; r < NH; ++r) l[r] *= s_corr[r0 + r];
         }
-        if (late) break;
-        if (tid == 0) mbar_arrive(p_ready);
+        if (!ok) break;  // a wait ran out: the others' waits for this warp will, too
+        async_proxy_fence();
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_ready);
         done = k + 1;
         slot = slot + 1 == STAGES ? 0 : slot + 1;
 #pragma unroll
