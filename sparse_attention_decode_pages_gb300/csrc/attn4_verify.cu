@@ -67,7 +67,7 @@ struct Verify4Cfg {
     // P: 128 rows (tokens) of N fp16, swizzled over the row's 32, 64 or 128 bytes
     static constexpr int OFF_P = OFF_Q + N * D * 2;
     static constexpr int OFF_RING = OFF_P + 128 * N * 2;
-    static constexpr int OFF_FR = OFF_RING + STAGES * STEP;  // float2 [N]: logit scale and -reference of each row
+    static constexpr int OFF_FR = OFF_RING + STAGES * STEP;  // float [N]: logit scales, then [N]: -references
     static constexpr int OFF_RED = OFF_FR + N * 8;           // float [4][N]: maxima, then sums
     static constexpr int OFF_CORR = OFF_RED + 4 * N * 4;  // float [N]
     static constexpr int OFF_OUT = OFF_CORR + N * 4;          // long long [N]: output rows
@@ -94,6 +94,24 @@ __device__ __forceinline__ int token_row(int q, int i) { return 32 * (q & 3) + 1
 
 __device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+// Two multiply-adds, and two sums, as one instruction.
+__device__ __forceinline__ unsigned long long pair_of(float2 x) {
+    return (unsigned long long)__float_as_uint(x.y) << 32 | __float_as_uint(x.x);
+}
+__device__ __forceinline__ float2 of_pair(unsigned long long x) {
+    return make_float2(__uint_as_float((uint32_t)x), __uint_as_float((uint32_t)(x >> 32)));
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    unsigned long long d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(pair_of(a)), "l"(pair_of(b)), "l"(pair_of(c)));
+    return of_pair(d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    unsigned long long d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(pair_of(a)), "l"(pair_of(b)));
+    return of_pair(d);
 }
 
 template <int N>
@@ -138,7 +156,8 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
     __shared__ uint32_t s_tmem;
     // (an offset to the array, not a rounded address: its accesses stay shared-memory ones)
     uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
-    float2* s_fr = reinterpret_cast<float2*>(smem + C::OFF_FR);
+    float* s_fac = reinterpret_cast<float*>(smem + C::OFF_FR);
+    float* s_neg = s_fac + N;
     float* s_red = reinterpret_cast<float*>(smem + C::OFF_RED);
     float* s_corr = reinterpret_cast<float*>(smem + C::OFF_CORR);
     long long* s_out = reinterpret_cast<long long*>(smem + C::OFF_OUT);
@@ -287,7 +306,10 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
             uint8_t* block = smem + C::OFF_Q + (at >> 6) * (N * 128);
             *reinterpret_cast<uint32_t*>(block + r * 128 + (((at & 63) * 2) ^ ((r & 7) << 4))) = pack_f16(x[i].x * down, x[i].y * down);
         }
-        if (lane == 0) s_fr[r] = make_float2(a.scale_log2 * pow2f(e), -kLow4);
+        if (lane == 0) {
+            s_fac[r] = a.scale_log2 * pow2f(e);
+            s_neg[r] = -kLow4;
+        }
     }
     if (tid < N) {
         s_out[tid] = tid < R ? out_index(tid) : 0;
@@ -312,7 +334,7 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
         // ============================================================ copies and products
         int issued = min(STAGES, steps), s_issued = 0, o_issued = 0;  // steps copied, and multiplied
         auto multiply_keys = [&](int k) {
-            if (!__all_sync(0xffffffffu, mbar_sleep_bounded(k_ready + (k & 1), (uint32_t)k >> 1 & 1u, a.status, a.wait_ns))) return false;
+            if (!__all_sync(0xffffffffu, mbar_wait_bounded(k_ready + (k & 1), (uint32_t)k >> 1 & 1u, a.status, a.wait_ns))) return false;
             tmem_fence_after();
             s_issued = k + 1;
             if (elect_one()) {
@@ -336,7 +358,7 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
                 take_next(kn >> 2);
                 next_pages((kn >> 2) + 1);
             }
-            if (!__all_sync(0xffffffffu, mbar_sleep_bounded(p_ready, (uint32_t)k & 1u, a.status, a.wait_ns))) break;
+            if (!__all_sync(0xffffffffu, mbar_wait_bounded(p_ready, (uint32_t)k & 1u, a.status, a.wait_ns))) break;
             async_proxy_fence();  // here, behind the barrier, for what all the others have written
             tmem_fence_after();
             o_issued = k + 1;
@@ -355,9 +377,9 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
         }
         // the copies in flight land, and the products end, before their memory is given back
         for (int j = max(0, issued - STAGES); j < issued; ++j)
-            mbar_sleep_bounded(full + j % STAGES, (uint32_t)(j / STAGES) & 1u, a.status, drain_limit(a));
-        if (s_issued > 0) mbar_sleep_bounded(s_done + (s_issued - 1 & 1), (uint32_t)(s_issued - 1) >> 1 & 1u, a.status, drain_limit(a));
-        if (o_issued > 0) mbar_sleep_bounded(o_done, (uint32_t)(o_issued - 1) & 1u, a.status, drain_limit(a));
+            mbar_wait_bounded(full + j % STAGES, (uint32_t)(j / STAGES) & 1u, a.status, drain_limit(a));
+        if (s_issued > 0) mbar_wait_bounded(s_done + (s_issued - 1 & 1), (uint32_t)(s_issued - 1) >> 1 & 1u, a.status, drain_limit(a));
+        if (o_issued > 0) mbar_wait_bounded(o_done, (uint32_t)(o_issued - 1) & 1u, a.status, drain_limit(a));
     } else {
     // ================================================================ conversions and softmax
     // V of this warp's chunk: this lane's token (and the one 8 behind) and 32 channels; the eight
@@ -379,7 +401,7 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
     // K of step k: this warp's chunk to tensor memory (one that is not there: whatever the ring
     // holds; its tokens are hidden)
     auto convert_keys = [&](int k) {
-        const bool there = mbar_sleep_bounded(full + ring.slot, ring.parity, a.status, a.wait_ns);
+        const bool there = mbar_wait_bounded(full + ring.slot, ring.parity, a.status, a.wait_ns);
         {
             const uint8_t* kt = smem + C::OFF_RING + ring.slot * C::STEP + warp * C::CHUNK;
             ring.advance();
@@ -426,7 +448,7 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
     auto all_level = [&]() {
         __syncwarp();
         if (lane == 0) mbar_arrive(level);
-        const bool there = __all_sync(0xffffffffu, mbar_sleep_bounded(level, level_parity, a.status, a.wait_ns));
+        const bool there = __all_sync(0xffffffffu, mbar_wait_bounded(level, level_parity, a.status, a.wait_ns));
         level_parity ^= 1u;
         return there;
     };
@@ -440,7 +462,7 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
         if (k < 0) continue;
 
         // softmax of this thread's token, for its query rows
-        ok &= mbar_sleep_bounded(s_done + (k & 1), (uint32_t)k >> 1 & 1u, a.status, a.wait_ns);
+        ok &= mbar_wait_bounded(s_done + (k & 1), (uint32_t)k >> 1 & 1u, a.status, a.wait_ns);
         tmem_fence_after();
         const uint32_t my_s = tm_s + (k & (C::NB - 1)) * N + r0 + my_lanes;
         const int warp_first = meta[slot * CHUNKS + warp], chunk_first = meta[slot * CHUNKS + my_chunk];
@@ -455,10 +477,17 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
                 uint32_t s[NH];
                 load_columns<NH>(my_s, s);
 #pragma unroll
-                for (int r = 0; r < NH; r += 2) {
-                    const float4 fr = *reinterpret_cast<const float4*>(s_fr + r0 + r);
-                    p[r] = fast_exp2(fmaf(__uint_as_float(s[r]), fr.x, fr.y));
-                    p[r + 1] = fast_exp2(fmaf(__uint_as_float(s[r + 1]), fr.z, fr.w));
+                for (int r = 0; r < NH; r += 4) {
+                    const float4 f = *reinterpret_cast<const float4*>(s_fac + r0 + r);
+                    const float4 n = *reinterpret_cast<const float4*>(s_neg + r0 + r);
+                    const float2 y0 = fma2(make_float2(__uint_as_float(s[r]), __uint_as_float(s[r + 1])), make_float2(f.x, f.y),
+                                           make_float2(n.x, n.y));
+                    const float2 y1 = fma2(make_float2(__uint_as_float(s[r + 2]), __uint_as_float(s[r + 3])),
+                                           make_float2(f.z, f.w), make_float2(n.z, n.w));
+                    p[r] = fast_exp2(y0.x);
+                    p[r + 1] = fast_exp2(y0.y);
+                    p[r + 2] = fast_exp2(y1.x);
+                    p[r + 3] = fast_exp2(y1.y);
                 }
             }
             if (!all) {
@@ -475,7 +504,7 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
                     if (large) s_move[k & 1] = 1;
                     mbar_arrive(voted);
                 }
-                if (k > 0) ok &= mbar_sleep_bounded(o_done, (uint32_t)(k - 1) & 1u, a.status, a.wait_ns);
+                if (k > 0) ok &= mbar_wait_bounded(o_done, (uint32_t)(k - 1) & 1u, a.status, a.wait_ns);
             }
 #pragma unroll
             for (int i = 0; i < NH / 8; ++i)
@@ -501,7 +530,7 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
                     st_shared16((v_dst ^ (j << 4)) + i * 1024, hmul2(v[0], s2), hmul2(v[1], s2), hmul2(v[2], s2), hmul2(v[3], s2));
                 }
             }
-            ok &= mbar_sleep_bounded(voted, (uint32_t)k & 1u, a.status, a.wait_ns);
+            ok &= mbar_wait_bounded(voted, (uint32_t)k & 1u, a.status, a.wait_ns);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok || !*reinterpret_cast<volatile int*>(s_move + (k & 1))) break;
             // the references move to the largest logit of each row among this step's tokens
@@ -511,7 +540,7 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
                 load_columns<8>(my_s + r, s);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float z = pos > s_lim[r0 + r + i] ? NEG_INF : __uint_as_float(s[i]) * s_fr[r0 + r + i].x;
+                    const float z = pos > s_lim[r0 + r + i] ? NEG_INF : __uint_as_float(s[i]) * s_fac[r0 + r + i];
                     s[i] = __reduce_max_sync(0xffffffffu, z == z ? float_key(z) : 0u);
                 }
                 if (lane < 8) {
@@ -527,9 +556,9 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
                 float x = NEG_INF;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) x = fmaxf(x, s_red[i * N + tid]);
-                const float old = -s_fr[tid].y, now = fmaxf(old, x - kBias4);
+                const float old = -s_neg[tid], now = fmaxf(old, x - kBias4);
                 s_corr[tid] = fast_exp2(old - now);
-                s_fr[tid].y = -now;
+                s_neg[tid] = -now;
             }
             if (tid == 0) s_move[k & 1] = 0;  // every warp has read it
             ok = all_level();
@@ -554,10 +583,14 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
         done = k + 1;
         slot = slot + 1 == STAGES ? 0 : slot + 1;
 #pragma unroll
-        for (int r = 0; r < NH; ++r) l[r] += p[r];
+        for (int r = 0; r < NH; r += 2) {
+            const float2 x = add2(make_float2(l[r], l[r + 1]), make_float2(p[r], p[r + 1]));
+            l[r] = x.x;
+            l[r + 1] = x.y;
+        }
     }
 
-    if (done > 0) mbar_sleep_bounded(o_done, (uint32_t)(done - 1) & 1u, a.status, a.wait_ns);
+    if (done > 0) mbar_wait_bounded(o_done, (uint32_t)(done - 1) & 1u, a.status, a.wait_ns);
     tmem_fence_after();
     uint32_t o[NH];
     load_columns<NH>(tm_o + r0 + my_lanes, o);  // channel my_row of this thread's query rows
@@ -578,7 +611,7 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
     if (tid < N) {
         const float sum = s_red[tid] + s_red[N + tid] + s_red[2 * N + tid] + s_red[3 * N + tid];
         s_corr[tid] = sum == 0.f ? 0.f : a.v_scale / sum;
-        const float lse = sum == 0.f ? NEG_INF : (log2f(sum) - s_fr[tid].y) * kLn2;
+        const float lse = sum == 0.f ? NEG_INF : (log2f(sum) - s_neg[tid]) * kLn2;
         const long long at = ((long long)row * a.num_splits + split) * R + tid;
         if (tid < R && nsplit > 1) a.part_lse[at] = lse;
         if (tid < R && nsplit == 1 && a.lse) a.lse[s_out[tid]] = lse;

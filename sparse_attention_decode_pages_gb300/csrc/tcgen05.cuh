@@ -28,31 +28,6 @@ __device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence
 // Makes this thread's shared-memory writes visible to the products (and bulk copies) issued later.
 __device__ __forceinline__ void async_proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// mbar_wait_bounded for waits that are long as a rule: the hardware holds the thread for up to
-// 20 us at a time, so that waiting warps leave the issue slots to the others.
-__device__ __forceinline__ bool mbar_sleep_bounded(uint64_t* bar, uint32_t parity, unsigned* status,
-         unsigned long long limit) {
-    auto landed = [&]() {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
-            : "memory");
-        return ok != 0;
-    };
-    if (landed()) return true;
-    const unsigned long long t0 = globaltimer_ns();
-    while (!landed())
-        if (globaltimer_ns() - t0 > limit) {
-            raise_status(status, SPD_DEV_TIMEOUT);
-            return false;
-        }
-    return true;
-}
-
 enum : uint64_t { kSwizzle128 = 2, kSwizzle64 = 4, kSwizzle32 = 6 };
 
 // Shared-memory matrix descriptor: byte strides as the layouts define them.
