@@ -68,8 +68,8 @@ struct Verify4Cfg {
     static constexpr int OFF_P = OFF_Q + N * D * 2;
     static constexpr int OFF_RING = OFF_P + 128 * N * 2;
     static constexpr int OFF_FR = OFF_RING + STAGES * STEP;  // float [N]: logit scales, then [N]: -references
-    static constexpr int OFF_RED = OFF_FR + N * 8;           // float [4][N]: maxima, then sums
-    static constexpr int OFF_CORR = OFF_RED + 4 * N * 4;  // float [N]
+    static constexpr int OFF_RED = OFF_FR + N * 8;           // float [WARPS][N]: maxima, then sums
+    static constexpr int OFF_CORR = OFF_RED + WARPS * N * 4;  // float [N]
     static constexpr int OFF_OUT = OFF_CORR + N * 4;          // long long [N]: output rows
     static constexpr int OFF_LIM = OFF_OUT + N * 8;           // int [N]: the last position that a row sees
     static constexpr int OFF_BAR = OFF_LIM + N * 4;           // uint64 [STAGES] and eight more
@@ -81,7 +81,7 @@ struct Verify4Cfg {
     // at most 512 / COLUMNS CTAs fit on an SM (227 KB), so that none waits for columns
     static constexpr int LEAST = 227 * 1024 / (512 / COLUMNS + 1);
     static constexpr int SMEM = 1024 + (BODY > LEAST ? BODY : LEAST);
-    static_assert(128 * (N + 1) * 4 <= OFF_FR - OFF_V && OFF_LIM % 8 == 0 && OFF_BAR % 8 == 0, "the sums fit over V, Q and P");
+    static_assert(OFF_LIM % 8 == 0 && OFF_BAR % 8 == 0, "aligned");
     static constexpr int P_ROW = N * 2;
     static constexpr uint64_t P_SWIZZLE = N == 16 ? kSwizzle32 : N == 32 ? kSwizzle64 : kSwizzle128;
     static_assert(kVerify4Occ * (SMEM + 2048) <= 228 * 1024 && kVerify4Occ * COLUMNS <= 512, "they fit on an SM");
@@ -119,6 +119,20 @@ __device__ __forceinline__ void load_columns(uint32_t taddr, uint32_t (&v)[N]) {
     __syncwarp();
     tmem_ld(taddr, v);
     tmem_wait_ld();
+}
+
+template <int N>
+__device__ __forceinline__ void load_frag(uint32_t taddr, uint32_t (&v)[N]) {
+    __syncwarp();
+    tmem_ld_frag(taddr, v);
+    tmem_wait_ld();
+}
+
+// Four 8 x 8 matrices of 16-bit elements, as mma accumulators lie in a warp; lane i gives the
+// address of row i % 8 of matrix i / 8.
+__device__ __forceinline__ void store_matrices(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w)
+                 : "memory");
 }
 
 __device__ __forceinline__ void store_columns(uint32_t taddr, const uint32_t (&v)[8]) {
@@ -323,12 +337,9 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
     const uint32_t my_lanes = (uint32_t)((warp & 3) * 32) << 16;
     const int r0 = (warp >> 2) * NH;                 // this thread's query rows: r0 ... r0 + NH - 1
     const int my_row = (warp & 3) * 32 + lane;       // and its token's row
-    const int my_chunk = (warp & 3) + 4 * (lane >> 4);
     const uint32_t v_smem = smem_u32(smem + C::OFF_V), q_smem = smem_u32(smem + C::OFF_Q), p_smem = smem_u32(smem + C::OFF_P);
     constexpr uint32_t kIdescS = umma_idesc_f16(128, N, false, false);
     constexpr uint32_t kIdescO = umma_idesc_f16(128, N, true, true);
-    // this thread's row of P: 16-byte pieces in swizzled order
-    const int p_xor = N == 16 ? my_row >> 2 & 1 : N == 32 ? my_row >> 1 & 3 : my_row & 7;
 
     if (warp == WARPS) {
         // ============================================================ copies and products
@@ -390,11 +401,16 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
     const int v_scale_src = warp * C::CHUNK + HALF + CODES + v_token * (D / 16) + piece * 2;
     const uint32_t v_dst = v_smem + (piece >> 1) * C::VBLOCK + token_row(warp, v_token) * 128 +
                            ((((piece & 1) * 4) ^ (v_token & 7)) << 4);
-    const uint32_t p_dst = p_smem + my_row * C::P_ROW + (((r0 / 8) ^ p_xor) << 4);
+    // P: matrices of 8 tokens by 8 query rows, four a store, a row of one a lane: tokens 0 to 7 and
+    // 8 to 15 of the warp's chunk, two 16-byte pieces, in the rows' swizzled order
+    const int p_row = token_row(warp, lane & 15);
+    const int p_xor = N == 16 ? p_row >> 2 & 1 : N == 32 ? p_row >> 1 & 3 : p_row & 7;
+    const uint32_t p_dst = p_smem + p_row * C::P_ROW + (((lane >> 4) ^ p_xor) << 4);
 
-    float l[NH];  // sums of this thread's weights
+    // this thread has tokens g and g + 8 of the warp's chunk and query rows 8 j + 2 c, 8 j + 2 c + 1
+    float2 l[N / 8];  // sums of the rows' weights
 #pragma unroll
-    for (int r = 0; r < NH; ++r) l[r] = 0.f;
+    for (int j = 0; j < N / 8; ++j) l[j] = make_float2(0.f, 0.f);
     int done = 0;       // steps whose second product was issued
     RingPos<STAGES> ring;  // of the next step whose keys are converted
 
@@ -464,52 +480,57 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
         // softmax of this thread's token, for its query rows
         ok &= mbar_wait_bounded(s_done + (k & 1), (uint32_t)k >> 1 & 1u, a.status, a.wait_ns);
         tmem_fence_after();
-        const uint32_t my_s = tm_s + (k & (C::NB - 1)) * N + r0 + my_lanes;
-        const int warp_first = meta[slot * CHUNKS + warp], chunk_first = meta[slot * CHUNKS + my_chunk];
-        const int pos = chunk_first < 0 ? 0x7fffffff : chunk_first + (lane & 15);
-        const bool all = __all_sync(0xffffffffu, pos <= len - a.T);  // every row sees every token of the warp
-        float p[NH];
+        const uint32_t my_s = tm_s + (k & (C::NB - 1)) * N + ((uint32_t)token_row(warp, 0) << 16);
+        const int first = meta[slot * CHUNKS + warp];
+        const int pos = first < 0 ? 0x7ffffff0 : first + g;  // of this thread's first token
+        const bool all = first >= 0 && first + 15 <= len - a.T;  // every row sees every token of the warp
+        float2 p[N / 8][2];
         // (what runs once a unit is kept short: a unit's first pass through straight code is bound by
         // fetching it)
 #pragma unroll 1
         for (bool moved = false;; moved = true) {
             {
-                uint32_t s[NH];
-                load_columns<NH>(my_s, s);
+                uint32_t s[N / 2];
+                load_frag(my_s, s);
 #pragma unroll
-                for (int r = 0; r < NH; r += 4) {
-                    const float4 f = *reinterpret_cast<const float4*>(s_fac + r0 + r);
-                    const float4 n = *reinterpret_cast<const float4*>(s_neg + r0 + r);
-                    const float2 y0 = fma2(make_float2(__uint_as_float(s[r]), __uint_as_float(s[r + 1])), make_float2(f.x, f.y),
-                                           make_float2(n.x, n.y));
-                    const float2 y1 = fma2(make_float2(__uint_as_float(s[r + 2]), __uint_as_float(s[r + 3])),
-                                           make_float2(f.z, f.w), make_float2(n.z, n.w));
-                    p[r] = fast_exp2(y0.x);
-                    p[r + 1] = fast_exp2(y0.y);
-                    p[r + 2] = fast_exp2(y1.x);
-                    p[r + 3] = fast_exp2(y1.y);
+                for (int j = 0; j < N / 8; ++j) {
+                    const float2 f = *reinterpret_cast<const float2*>(s_fac + 8 * j + 2 * c);
+                    const float2 n = *reinterpret_cast<const float2*>(s_neg + 8 * j + 2 * c);
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const float2 y = fma2(make_float2(__uint_as_float(s[4 * j + 2 * t]), __uint_as_float(s[4 * j + 2 * t + 1])), f, n);
+                        p[j][t] = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+                    }
                 }
             }
             if (!all) {
 #pragma unroll
-                for (int r = 0; r < NH; ++r)
-                    if (pos > s_lim[r0 + r]) p[r] = 0.f;
+                for (int j = 0; j < N / 8; ++j) {
+                    const int2 lim = *reinterpret_cast<const int2*>(s_lim + 8 * j + 2 * c);
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        if (pos + 8 * t > lim.x) p[j][t].x = 0.f;
+                        if (pos + 8 * t > lim.y) p[j][t].y = 0.f;
+                    }
+                }
             }
             if (!moved) {
                 float top = 0.f;
 #pragma unroll
-                for (int r = 0; r < NH; ++r) top = fmaxf(top, p[r]);
+                for (int j = 0; j < N / 8; ++j)
+                    top = fmaxf(fmaxf(top, fmaxf(p[j][0].x, p[j][0].y)), fmaxf(p[j][1].x, p[j][1].y));
                 const bool large = __any_sync(0xffffffffu, top > kMost4);  // some weight is too large
                 if (lane == 0) {
                     if (large) s_move[k & 1] = 1;
                     mbar_arrive(voted);
                 }
                 if (k > 0) ok &= mbar_wait_bounded(o_done, (uint32_t)(k - 1) & 1u, a.status, a.wait_ns);
+                __syncwarp();
             }
 #pragma unroll
-            for (int i = 0; i < NH / 8; ++i)
-                st_shared16(p_dst ^ (i << 4), pack_f16(p[8 * i], p[8 * i + 1]), pack_f16(p[8 * i + 2], p[8 * i + 3]),
-                            pack_f16(p[8 * i + 4], p[8 * i + 5]), pack_f16(p[8 * i + 6], p[8 * i + 7]));
+            for (int j = 0; j < N / 8; j += 2)
+                store_matrices(p_dst ^ (j << 4), pack_f16(p[j][0].x, p[j][0].y), pack_f16(p[j][1].x, p[j][1].y),
+                               pack_f16(p[j + 1][0].x, p[j + 1][0].y), pack_f16(p[j + 1][1].x, p[j + 1][1].y));
             if (moved) break;
 
             // V: this warp's chunk to shared memory, 32 channels of a token at a time
@@ -518,7 +539,7 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
                 const uint8_t* vt = stage + v_src + i * (8 * (D / 2));
                 const uint4 x = *reinterpret_cast<const uint4*>(vt);
                 uint32_t two = *reinterpret_cast<const uint16_t*>(stage + v_scale_src + i * (8 * (D / 16)));
-                if (warp_first < 0 || warp_first + v_token + 8 * i >= len) two = 0u;  // no token: its bytes may be anything, its scale counts as 0
+                if (first < 0 || first + v_token + 8 * i >= len) two = 0u;  // no token: its bytes may be anything, its scale counts as 0
                 const uint32_t s = e4m3x2_to_f16(two);
                 const uint32_t s_lo = __byte_perm(s, 0, 0x1010), s_hi = __byte_perm(s, 0, 0x3232);
                 const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -534,20 +555,25 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
             ok = __all_sync(0xffffffffu, ok);
             if (!ok || !*reinterpret_cast<volatile int*>(s_move + (k & 1))) break;
             // the references move to the largest logit of each row among this step's tokens
-#pragma unroll 1
-            for (int r = 0; r < NH; r += 8) {
-                uint32_t s[8];
-                load_columns<8>(my_s + r, s);
+            {
+                uint32_t s[N / 2];
+                load_frag(my_s, s);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float z = pos > s_lim[r0 + r + i] ? NEG_INF : __uint_as_float(s[i]) * s_fac[r0 + r + i];
-                    s[i] = __reduce_max_sync(0xffffffffu, z == z ? float_key(z) : 0u);
-                }
-                if (lane < 8) {
-                    uint32_t key = s[0];
+                for (int j = 0; j < N / 8; ++j) {
+                    const float2 f = *reinterpret_cast<const float2*>(s_fac + 8 * j + 2 * c);
+                    const int2 lim = *reinterpret_cast<const int2*>(s_lim + 8 * j + 2 * c);
+                    float2 m = make_float2(NEG_INF, NEG_INF);
 #pragma unroll
-                    for (int i = 1; i < 8; ++i) key = lane == i ? s[i] : key;
-                    s_red[(warp & 3) * N + r0 + r + lane] = __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
+                    for (int t = 0; t < 2; ++t) {
+                        if (pos + 8 * t <= lim.x) m.x = fmaxf(m.x, __uint_as_float(s[4 * j + 2 * t]) * f.x);
+                        if (pos + 8 * t <= lim.y) m.y = fmaxf(m.y, __uint_as_float(s[4 * j + 2 * t + 1]) * f.y);
+                    }
+#pragma unroll
+                    for (int off = 4; off < 32; off <<= 1) {
+                        m.x = fmaxf(m.x, __shfl_xor_sync(0xffffffffu, m.x, off));
+                        m.y = fmaxf(m.y, __shfl_xor_sync(0xffffffffu, m.y, off));
+                    }
+                    if (g == 0) *reinterpret_cast<float2*>(s_red + warp * N + 8 * j + 2 * c) = m;
                 }
             }
             ok = all_level();
@@ -555,7 +581,7 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
             if (tid < N) {
                 float x = NEG_INF;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) x = fmaxf(x, s_red[i * N + tid]);
+                for (int i = 0; i < WARPS; ++i) x = fmaxf(x, s_red[i * N + tid]);
                 const float old = -s_neg[tid], now = fmaxf(old, x - kBias4);
                 s_corr[tid] = fast_exp2(old - now);
                 s_neg[tid] = -now;
@@ -574,7 +600,11 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
                 }
             }
 #pragma unroll
-            for (int r = 0; r < NH; ++r) l[r] *= s_corr[r0 + r];
+            for (int j = 0; j < N / 8; ++j) {
+                const float2 corr = *reinterpret_cast<const float2*>(s_corr + 8 * j + 2 * c);
+                l[j].x *= corr.x;
+                l[j].y *= corr.y;
+            }
         }
         if (!ok) break;  // a wait ran out: the others' waits for this warp will, too
         tmem_fence_before();
@@ -583,11 +613,7 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
         done = k + 1;
         slot = slot + 1 == STAGES ? 0 : slot + 1;
 #pragma unroll
-        for (int r = 0; r < NH; r += 2) {
-            const float2 x = add2(make_float2(l[r], l[r + 1]), make_float2(p[r], p[r + 1]));
-            l[r] = x.x;
-            l[r + 1] = x.y;
-        }
+        for (int j = 0; j < N / 8; ++j) l[j] = add2(l[j], add2(p[j][0], p[j][1]));
     }
 
     if (done > 0) mbar_wait_bounded(o_done, (uint32_t)(done - 1) & 1u, a.status, a.wait_ns);
@@ -595,21 +621,21 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
     uint32_t o[NH];
     load_columns<NH>(tm_o + r0 + my_lanes, o);  // channel my_row of this thread's query rows
     tmem_fence_before();
-    // the sums of the rows, over the 128 threads that hold parts of each: through shared memory
-    // (over V, with a column of padding), 128 / PARTS of them a thread
-    float* s_sum = reinterpret_cast<float*>(smem + C::OFF_V);
+    // the sums of the rows, over the eight lanes of a warp and the warps that hold parts of each
 #pragma unroll
-    for (int r = 0; r < NH; ++r) s_sum[my_row * (N + 1) + r0 + r] = l[r];
-    converters_sync<32 * WARPS>();
-    constexpr int PARTS = 4;
-    if (tid < N * PARTS) {
-        float sum = 0.f;
-        for (int i = 0; i < 128 / PARTS; ++i) sum += s_sum[(tid / N * (128 / PARTS) + i) * (N + 1) + tid % N];
-        s_red[tid] = sum;
+    for (int j = 0; j < N / 8; ++j) {
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) {
+            l[j].x += __shfl_xor_sync(0xffffffffu, l[j].x, off);
+            l[j].y += __shfl_xor_sync(0xffffffffu, l[j].y, off);
+        }
+        if (g == 0) *reinterpret_cast<float2*>(s_red + warp * N + 8 * j + 2 * c) = l[j];
     }
     converters_sync<32 * WARPS>();
     if (tid < N) {
-        const float sum = s_red[tid] + s_red[N + tid] + s_red[2 * N + tid] + s_red[3 * N + tid];
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < WARPS; ++i) sum += s_red[i * N + tid];
         s_corr[tid] = sum == 0.f ? 0.f : a.v_scale / sum;
         const float lse = sum == 0.f ? NEG_INF : (log2f(sum) - s_neg[tid]) * kLn2;
         const long long at = ((long long)row * a.num_splits + split) * R + tid;
