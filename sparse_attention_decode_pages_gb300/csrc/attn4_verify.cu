@@ -17,23 +17,30 @@
 //      operand of the first product.  The contraction's order of channels that this gives
 //      (position 16 i + 4 c + j is channel c * D / 4 + 4 i + j) is given to Q as well.
 //   V: rows of a token's channels to shared memory, as the M-major A operand of the second.
-//   P: a thread has one token (row token_row of its chunk) and half of the query rows: its
-//      weights, in fp16, into the token's row of the N-major B operand.
+//   P: a warp weighs the 16 tokens of its chunk for every query row, S loaded and the weights,
+//      in fp16, stored (8 x 8 matrices, the N-major B operand) as an mma fragment lies.
 // A ninth warp issues the copies and, one elected lane, the products, which run while the
-// others convert: S = K Q^T behind the conversion of V, and O += V^T P^T behind that of the
-// next step's K.  (mma.sync blocks its SM quarter's issue for 8 cycles each: the same
-// work took 502 us with it where this takes 393.)
+// others convert.  mma.sync blocks its SM quarter's issue for 8 cycles each: the same work
+// took 502 us with it where this takes 334.
+//
+// In a step k a converting warp stores K of step k + 1, weighs step k (whose S was begun a step
+// ago), says whether a weight is too large for the references (below), waits for O of step
+// k - 1, stores P and V of step k, and only then waits for what the others said: no barrier of
+// the CTA, and every wait has other work before it.  (Up to 32 query rows: for more, two
+// places for K and S exceed tensor memory, so K of step k is stored in step k.)
 //
 // Queries are scaled by a power of two into fp16's range (the factor goes into the
-// logits' scale).  Online softmax in fp32 in base 2; a column's reference moves only when a
-// logit exceeds it by kHead4 (attn4.cuh).  One barrier of the converting warps a step carries
-// the vote on the references.
+// logits' scale).  Online softmax in fp32 in base 2; a query row's reference moves only when a
+// logit exceeds it by kHead4 (attn4.cuh), for all warps at once.
 //
-// 64 sequences of 8K-16K tokens, 7 positions, 32 / 8 heads of 128: 393 us, 2.3 TB/s of keys and
-// values, 34 % of the measured copy peak.  Bound by the chain of a step (a wait for the copy, the
-// conversions, two hand-overs to the products and back, the vote): 1.8 us for 128 tokens
-// in each of the two CTAs of an SM, hardly less with the conversions, the softmax or the products
-// taken out one at a time; and by a unit's start and end, 9 to 12 us.
+// 64 sequences of 8K-16K tokens, 7 positions, 32 / 8 heads of 128: 334 us, 2.7 TB/s of keys and
+// values, 40 % of the measured copy peak.  What it was before, step by step: a barrier for the
+// vote and K of its own step 393; K ahead 380; the vote waited for later, and shared memory
+// addressed as such, 359; waits that poll, multiply-adds in pairs 347; weights by fragments, their
+// factors in registers 337; three splits of a row instead of two 334.  Bound by the instructions
+// of the conversions (issue ~60 % of an SM with two CTAs, half of it at two cycles an
+// instruction) and by shared memory (V written and read by the product, ~70 %), in a step of
+// 1.5 us for 128 tokens in each of two CTAs; and by a unit's start and end, 9 to 12 us.
 #include <atomic>
 
 #include "attn4.cuh"
@@ -411,6 +418,7 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
     float2 l[N / 8];  // sums of the rows' weights
 #pragma unroll
     for (int j = 0; j < N / 8; ++j) l[j] = make_float2(0.f, 0.f);
+    float2 fac[N / 8], neg[N / 8];
     int done = 0;       // steps whose second product was issued
     RingPos<STAGES> ring;  // of the next step whose keys are converted
 
@@ -494,11 +502,13 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
                 load_frag(my_s, s);
 #pragma unroll
                 for (int j = 0; j < N / 8; ++j) {
-                    const float2 f = *reinterpret_cast<const float2*>(s_fac + 8 * j + 2 * c);
-                    const float2 n = *reinterpret_cast<const float2*>(s_neg + 8 * j + 2 * c);
+                    if (N == 64 || moved || k == 0) {
+                        fac[j] = *reinterpret_cast<const float2*>(s_fac + 8 * j + 2 * c);
+                        neg[j] = *reinterpret_cast<const float2*>(s_neg + 8 * j + 2 * c);
+                    }
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
-                        const float2 y = fma2(make_float2(__uint_as_float(s[4 * j + 2 * t]), __uint_as_float(s[4 * j + 2 * t + 1])), f, n);
+                        const float2 y = fma2(make_float2(__uint_as_float(s[4 * j + 2 * t]), __uint_as_float(s[4 * j + 2 * t + 1])), fac[j], neg[j]);
                         p[j][t] = make_float2(fast_exp2(y.x), fast_exp2(y.y));
                     }
                 }
