@@ -17,8 +17,9 @@
 //   O^T += V^T P^T
 //
 // so the tokens fill the MMA rows and the few query rows its columns.  tcgen05 would
-// spend 16 columns and a handshake of ~2 us a step of 128 tokens on them (41 us for the
-// batch below); for more rows it wins, see attn4_verify.cu.  code * scale is exact in fp16,
+// spend 16 columns and a hand-over between conversions and products on them (41 us for the
+// batch below, tried; two CTAs on an SM take 1.1 us for 128 tokens each here, 1.5 with
+// attn4_verify.cu's 32 columns); for more rows it wins.  code * scale is exact in fp16,
 // so the products are those of the values the cache stands for.  The contraction's
 // channel order is free: lane (g, c) = (lane / 4, lane % 4) holds the D / 4 channels from
 // c * D / 4 on of tokens g and g + 8, contiguous in memory, and V's channels g * D / 8 ...

@@ -37,10 +37,10 @@
 // values, 40 % of the measured copy peak.  What it was before, step by step: a barrier for the
 // vote and K of its own step 393; K ahead 380; the vote waited for later, and shared memory
 // addressed as such, 359; waits that poll, multiply-adds in pairs 347; weights by fragments, their
-// factors in registers 337; three splits of a row instead of two 334.  Bound by the instructions
-// of the conversions (issue ~60 % of an SM with two CTAs, half of it at two cycles an
-// instruction) and by shared memory (V written and read by the product, ~70 %), in a step of
-// 1.5 us for 128 tokens in each of two CTAs; and by a unit's start and end, 9 to 12 us.
+// factors in registers 337; three splits of a row instead of two 334.  Bound by the latency of a
+// step's instructions, 1.3 us for 128 tokens with one CTA on an SM, 1.5 with two (issue slots
+// 52 % busy, and a quarter of the instructions hold their pipe for two cycles; shared memory
+// 42 %), of which registers allow no third CTA; and by a unit's start and end, 8 to 11 us.
 #include <atomic>
 
 #include "attn4.cuh"

@@ -964,15 +964,17 @@ SPD_API spd_status kv4_read(const spd_dims* dims, int32_t T, const uint8_t* kv4,
 // (turns + fixed).  More rows, whole sequences (their lengths differ, and only the GPU knows
 // them): units + the longest one's tail, rows * S * (turns / S + fixed) / slots + turns / S, is
 // least at S = sqrt(turns * slots / (rows * fixed)).  Measured: 64 sequences of 8K-16K tokens, 8 KV heads,
-// 28 query rows: S = 1 / 2 / 3 / 4 / 8: 344 / 337 / 333 / 342 / 377 us (3 taken); 64 selections of 64
+// 28 query rows: S = 1 / 2 / 3 / 4 / 8: 344 / 337 / 333 / 342 / 377 us (3 taken); 40 of
+// 2K-6K, 64 query rows: 1 / 2 / 3: 136 / 150 / 159 us (1 taken); 64 selections of 64
 // pages of 16: 1 / 2 / 4: 23 / 32 / 40 us (1 taken); one sequence of 131,072 tokens: 25 / 38 / 57 /
 // 76: 54 / 40 / 45 / 39 us (76 taken); 8 selections of 256 pages of 32: 4 / 7 / 9 / 14: 29 / 30 / 26 / 33 us
 // (9 taken).
 static int kv4_splits(const spd_dims* d, int T, int items, bool sparse, int req, int sms) {
     const long long rows = (long long)d->B * d->H_kv;
     if (rows > kTickets) return 1;  // many times the rows that fill the GPU
-    const bool few = T * (d->H_q / d->H_kv) <= kAttn4DecodeRows;
-    const double fixed = few ? 6 : 10;
+    const int R = T * (d->H_q / d->H_kv);
+    const bool few = R <= kAttn4DecodeRows;
+    const double fixed = few ? 6 : R <= 32 ? 10 : 20;
     const long long slots = (long long)sms * (few ? occ_attn4_decode() : occ_attn4_verify());
     int S = req;
     if (S <= 0) {
