@@ -377,7 +377,6 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
                 next_pages((kn >> 2) + 1);
             }
             if (!__all_sync(0xffffffffu, mbar_wait_bounded(p_ready, (uint32_t)k & 1u, a.status, a.wait_ns))) break;
-            async_proxy_fence();  // here, behind the barrier, for what all the others have written
             tmem_fence_after();
             o_issued = k + 1;
             if (elect_one()) {
@@ -617,6 +616,7 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
             }
         }
         if (!ok) break;  // a wait ran out: the others' waits for this warp will, too
+        async_proxy_fence();
         tmem_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(p_ready);
