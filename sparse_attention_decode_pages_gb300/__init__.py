@@ -331,28 +331,34 @@ def lse_merge(part_o, part_lse, o, lse=None, stream=None):
 
 
 _B16 = _I32 = _F32 = _U8 = _LOGITS = ()  # accepted types, set with torch's first use
-_torch = _raw_stream = None
+_raw_stream = _device = None
 
 
 def _here(stream):
     """The current device and the raw stream to launch on (the given one has to be of that device)."""
-    global _torch, _raw_stream, _B16, _I32, _F32, _U8, _LOGITS
-    if _torch is None:
-        import torch
-        _B16, _I32, _F32, _U8 = (torch.bfloat16, torch.uint16), (torch.int32,), (torch.float32,), (torch.uint8,)
-        _LOGITS = (torch.float32, torch.bfloat16)
-        if not torch.cuda.is_available():
-            raise SpdError(3, "no CUDA device")
-        # the current stream's handle without a Stream object around it (1 us less a call)
-        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-            lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-        _torch = torch
-    dev = _torch.cuda.current_device()
+    if _device is None:
+        _first_use()
+    dev = _device()
     if stream is None:
         return dev, _raw_stream(dev)
     if stream.device.index != dev:
         raise SpdError(1, "the stream is not of the current CUDA device")
     return dev, stream.cuda_stream
+
+
+def _first_use():
+    global _raw_stream, _device, _B16, _I32, _F32, _U8, _LOGITS
+    import torch
+    _B16, _I32, _F32, _U8 = (torch.bfloat16, torch.uint16), (torch.int32,), (torch.float32,), (torch.uint8,)
+    _LOGITS = (torch.float32, torch.bfloat16)
+    if not torch.cuda.is_available():
+        raise SpdError(3, "no CUDA device")
+    torch.cuda.init()
+    # the current device, and its stream's handle without a Stream object around it, as plain
+    # numbers (1 us less a call)
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+    _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _arg(t, dtypes, what: str, dev: int, numel: int | None = None, rows: bool = False):
