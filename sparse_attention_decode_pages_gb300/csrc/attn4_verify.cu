@@ -50,7 +50,7 @@ namespace spd {
 
 namespace {
 
-// CTAs on an SM (registers; shared memory and tensor memory hold them).  The driver's
+// CTAs on an SM (registers; shared memory and tensor memory hold them).  The runtime's
 // occupancy query answers 1 for any kernel that allocates tensor memory.
 constexpr int kVerify4Occ = 2;
 

@@ -1,5 +1,5 @@
 // kv4.cuh -- the 4-bit paged cache's number format, shared by the kernels that
-// write it (kv4.cu) and attend over it (attn4.cu).
+// write it (kv4.cu) and attend over it (attn4_decode.cu, attn4_verify.cu).
 //
 // A row of D channels is held in groups of 16: a scale s = e4m3(amax / (6 * 2^e))
 // and sixteen e2m1 codes (sign, two exponent bits, one mantissa bit: 0, 0.5, 1,
