@@ -8,7 +8,7 @@
 // entry), and the warp keeps a ring of pairs filled by bulk copies, refilling a slot as soon
 // as it has read it, so no warp waits for another before the unit's end.  (With barriers
 // between the warps -- keys and values split over them -- the same products took 28 us
-// where this takes 22.8; one pair at a time instead of one chunk saves a wait, a vote and
+// where this takes 22.6; one pair at a time instead of one chunk saves a wait, a vote and
 // a refill.)
 //
 // Per chunk, on the tensor cores (mma.sync m16n8k16, fp16 in, fp32 out):
@@ -28,9 +28,9 @@
 // Measured on the pipes: a chunk costs an SM quarter 64 conversions (2 cycles each), 64
 // fp16 products and 16 mma (8 cycles each, during which nothing else issues), so
 // arithmetic, not the 2,304 bytes, bounds it: 64 sequences x 64 pages of 16 tokens, 32 / 8
-// heads of 128: 22.8 us, 3.35 TB/s of keys and values, 49 % of the measured copy peak (and 512
+// heads of 128: 22.6 us, 3.4 TB/s of keys and values, 50 % of the measured copy peak (and 512
 // units on 152 SMs: the SMs that get four of them end last); one sequence of 131,072
-// tokens in 76 splits: 38.9 us, 3.9 TB/s, 57 %.
+// tokens in 76 splits: 39.2 us, 3.85 TB/s, 57 %.
 #include <atomic>
 
 #include "attn4.cuh"
@@ -449,13 +449,12 @@ __global__ void __launch_bounds__(128, DecodeCfg<D>::OCC) decode4_kernel(const A
             *reinterpret_cast<uint2*>(a.o + oi * D + d) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
             if (d == 0 && a.lse) a.lse[oi] = lse;
         } else {
-            const long long at = ((long long)row * a.num_splits + split) * R + r;
+            const long long at = ((long long)row * a.parts + split) * R + r;
             *reinterpret_cast<float4*>(a.part_o + at * D + d) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
             if (d == 0) a.part_lse[at] = lse;
         }
     }
-    if (nsplit == 1 || !last_split(a, row, nsplit, &s_last)) return;
-    join_splits<D, C::THREADS>(a, row, nsplit, R, out_index);
+    join_splits<D, C::THREADS, false>(a, row, split, nsplit, R, &s_last, out_index);
 }
 
 template <int D>

@@ -648,7 +648,7 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
         for (int i = 0; i < WARPS; ++i) sum += s_red[i * N + tid];
         s_corr[tid] = sum == 0.f ? 0.f : a.v_scale / sum;
         const float lse = sum == 0.f ? NEG_INF : (log2f(sum) - s_neg[tid]) * kLn2;
-        const long long at = ((long long)row * a.num_splits + split) * R + tid;
+        const long long at = ((long long)row * a.parts + split) * R + tid;
         if (tid < R && nsplit > 1) a.part_lse[at] = lse;
         if (tid < R && nsplit == 1 && a.lse) a.lse[s_out[tid]] = lse;
     }
@@ -662,7 +662,7 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
                 if (nsplit == 1)
                     reinterpret_cast<bf16*>(a.o)[s_out[r] * D + my_row] = __float2bfloat16_rn(x);
                 else
-                    a.part_o[(((long long)row * a.num_splits + split) * R + r) * D + my_row] = x;
+                    a.part_o[(((long long)row * a.parts + split) * R + r) * D + my_row] = x;
             }
         }
     }
@@ -670,8 +670,7 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
     __syncthreads();
     tmem_fence_after();
     if (warp == WARPS) tmem_free(tmem, C::COLUMNS);
-    if (nsplit == 1 || !last_split(a, row, nsplit, &s_last)) return;
-    join_splits<D, C::THREADS>(a, row, nsplit, R, out_index);
+    join_splits<D, C::THREADS, true>(a, row, split, nsplit, R, &s_last, out_index);
 }
 
 typedef void (*Verify4Fn)(const Attn4Args);

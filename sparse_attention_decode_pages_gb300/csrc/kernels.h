@@ -130,9 +130,11 @@ struct Attn4Args {
     float v_scale;     // 2^v_exp
     uint16_t* o;
     float* lse;
-    float* part_o;    // [B*H_kv][num_splits][R][D]
-    float* part_lse;  // [B*H_kv][num_splits][R]
-    int* counters;    // [B*H_kv] split tickets, zero on entry and on exit
+    float* part_o;    // [B*H_kv][parts][R][D]: the splits' outputs, then those of groups of splits
+    float* part_lse;  // [B*H_kv][parts][R]
+    int* counters;    // tickets of the rows, then of their groups, zero on entry and on exit
+    int parts;        // num_splits and the groups, if there are any
+    int group;        // splits of a group (num_splits: no groups)
     unsigned* status;
     unsigned long long wait_ns;  // limit of every bounded wait
 };

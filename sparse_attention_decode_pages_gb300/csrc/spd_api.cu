@@ -969,6 +969,8 @@ SPD_API spd_status kv4_read(const spd_dims* dims, int32_t T, const uint8_t* kv4,
 // pages of 16: 1 / 2 / 4: 23 / 32 / 40 us (1 taken); one sequence of 131,072 tokens: 25 / 38 / 57 /
 // 76: 54 / 40 / 45 / 39 us (76 taken); 8 selections of 256 pages of 32: 4 / 7 / 9 / 14: 29 / 30 / 26 / 33 us
 // (9 taken).
+constexpr long long kJoinBytes = 256 << 10;
+
 static int kv4_splits(const spd_dims* d, int T, int items, bool sparse, int req, int sms) {
     const long long rows = (long long)d->B * d->H_kv;
     if (rows > kTickets) return 1;  // many times the rows that fill the GPU
@@ -1004,9 +1006,28 @@ static int kv4_splits(const spd_dims* d, int T, int items, bool sparse, int req,
     return (items + ips - 1) / ips;
 }
 
+// Groups of splits that are joined first.  One CTA reads a row's partials at ~50 GB/s, so the join
+// of many splits of many query rows goes in two steps of about sqrt(S) partials where they
+// are more than 256 KB.  One sequence of 131,000 tokens, one KV head, 64 / 24 / 8 query rows:
+// 232 / 92 / 77 us in one step, 94 / 46 / 22 in two; 8 KV heads of 4 rows (156 KB): 39.0 in one, 38.2
+// to 40.1 in two.
+struct Kv4Groups {
+    int group, groups;  // splits of a group; groups of a row (0: no groups)
+};
+static Kv4Groups kv4_groups(long long rows, int S, int R, int D) {
+    Kv4Groups g = {S, 0};
+    if ((long long)S * R * D * 4 <= kJoinBytes) return g;
+    const int group = (int)ceil(sqrt((double)S)), groups = (S + group - 1) / group;
+    if (rows * (1 + groups) > kTickets) return g;
+    g.group = group;
+    g.groups = groups;
+    return g;
+}
+
 // The workspace: tickets at its start, where the bf16 attention's are, with room for the rows of any
 // call that splits them, so that no partials lie where another call's tickets are.
 static AttnWs kv4_ws_layout(void* ws, long long rows, int S, int R, int D) {
+    S += kv4_groups(rows, S, R, D).groups;
     AttnWs w;
     char* base = static_cast<char*>(ws);
     w.queue = nullptr;
@@ -1090,6 +1111,9 @@ static spd_status kv4_attn(const spd_dims* dims, int32_t T, const spd_bf16* q, c
     a.num_phys = dims->num_phys_pages;
     a.pages_per_split = (items + S - 1) / S;
     a.num_splits = S;
+    const Kv4Groups g = kv4_groups(rows, S, R, dims->D);
+    a.group = g.group;
+    a.parts = S + g.groups;
     a.scale_log2 = (float)scale_log2;
     a.v_scale = exp2f((float)v_exp);
     a.o = o;

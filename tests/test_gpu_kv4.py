@@ -653,3 +653,35 @@ def test_kv4_attention_with_waits_that_run_out(spd, T, H_q, D, splits):
     for got, want in zip(run(), first):
         assert torch.equal(got, want)
     assert spd.spd_device_status(clear=True) == 0
+
+
+@pytest.mark.parametrize("lens,T,H_q,H_kv,D,splits", [
+    ([6000], 8, 8, 1, 128, 40), ([5000, 900, 0], 6, 8, 1, 64, 33), ([4100, 8200], 1, 8, 1, 128, 100), ([6500, 70], 2, 8, 2, 64, 136),
+])
+def test_kv4_splits_joined_in_groups(spd, lens, T, H_q, H_kv, D, splits):
+    """So many partials that they are joined in two steps: against one unit a row, and twice through one workspace."""
+    import torch
+    rng = np.random.default_rng(splits)
+    lens, pt, mp, n, kv4, vals = make_cache(rng, lens, 16, H_kv, D)
+    B = len(lens)
+    dims = spd.dims_of(B, H_q, H_kv, D, 16, mp, n)
+    items = mp
+    units = -(-items // -(-items // splits))  # of a row, as the call cuts it
+    assert units * T * (H_q // H_kv) * D * 4 > 256 << 10
+    q, cache, d_pt, d_lens = rows_bf16(rng, B, T, H_q, D), dev(kv4), dev(pt), dev(lens)
+    ws = spd.workspace(spd.spd_kv4_dense_verify_workspace_size(dims, T, splits))
+    got = []
+    for s in (splits, splits, 1):
+        o = torch.full((B, T, H_q, D), float("nan"), dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((B, T, H_q), float("nan"), device="cuda")
+        spd.kv4_dense_verify_attn(dims, T, to_dev(q), cache, d_pt, d_lens, o, ws, lse=lse, num_splits=s)
+        got.append((host(o), host(lse)))
+    assert spd.spd_device_status(clear=True) == 0
+    assert all(np.array_equal(x, y) for x, y in zip(got[0], got[1]))
+    G = H_q // H_kv
+    for b in range(B):
+        for t in range(T):
+            seen = np.arange(lens[b]) <= lens[b] - T + t
+            for hq in (0, H_q - 1):
+                for og, lg in (got[0], got[2]):
+                    check_row(og[b, t, hq], lg[b, t, hq], q[b, t, hq], vals[b][0][:, hq // G], vals[b][1][:, hq // G], D ** -0.5, seen, (b, t, hq))
