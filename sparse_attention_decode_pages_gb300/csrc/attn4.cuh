@@ -131,7 +131,7 @@ __device__ __forceinline__ void join_groups(const Attn4Args& a, int row, int spl
 
 template <int D, int THREADS>
 __device__ __noinline__ void join_groups_apart(const Attn4Args& a, int row, int split, int nsplit, int R, int* s_last) {
-    join_groups<D, THREADS, 8>(a, row, split, nsplit, R, s_last);  // (16 spill: 94 -> 136 us for 304 splits of 64 rows)
+    join_groups<D, THREADS, 8>(a, row, split, nsplit, R, s_last);  // (16 spill: 96 -> 136 us for 304 splits of 64 rows)
 }
 
 // A unit's end: the last of a row's nsplit units joins them, or, where that would be much for one

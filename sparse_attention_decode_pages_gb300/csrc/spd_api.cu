@@ -960,7 +960,9 @@ SPD_API spd_status kv4_read(const spd_dims* dims, int32_t T, const uint8_t* kv4,
 // Splits of a row of the 4-bit attention.  Its CTAs take one unit each, `slots` at a time, in
 // turns of 128 tokens, and a unit costs about `fixed` turns besides its own (the lengths, the
 // queries, the first copies, the join).  Up to half a GPU of rows is cut into one round of
-// units.  More rows, selections (about equal): the count that takes the least rounds *
+// units, or, with more than eight query rows, into fewer where the join would take longer (one KV
+// head, 64 query rows, 131,000 / 20,000 tokens: 304 / 157 units 95.6 / 68.0 us, 162 / 46 units 79.6 /
+// 49.3 us).  More rows, selections (about equal): the count that takes the least rounds *
 // (turns + fixed).  More rows, whole sequences (their lengths differ, and only the GPU knows
 // them): units + the longest one's tail, rows * S * (turns / S + fixed) / slots + turns / S, is
 // least at S = sqrt(turns * slots / (rows * fixed)).  Measured: 64 sequences of 8K-16K tokens, 8 KV heads,
@@ -986,6 +988,12 @@ static int kv4_splits(const spd_dims* d, int T, int items, bool sparse, int req,
         const double turns = (double)items * d->page_size / 128;
         if (rows > 0 && 2 * rows <= slots) {
             S = (int)(slots / rows);
+            if (!few) {
+                // turns / S * 1.3 us + 2 sqrt(S) partials of the join at 50 GB/s
+                const double part = (double)R * d->D * 4 / 50e3;
+                const int least = (int)cbrt(turns * 1.3 / part * (turns * 1.3 / part)) + 1;
+                if (S > least) S = least;
+            }
         } else if (rows > 0 && !sparse) {
             S = (int)(sqrt(turns * slots / (rows * fixed)) + 0.5);
         } else if (rows > 0) {
@@ -1009,7 +1017,7 @@ static int kv4_splits(const spd_dims* d, int T, int items, bool sparse, int req,
 // Groups of splits that are joined first.  One CTA reads a row's partials at ~50 GB/s, so the join
 // of many splits of many query rows goes in two steps of about sqrt(S) partials where they
 // are more than 256 KB.  One sequence of 131,000 tokens, one KV head, 64 / 24 / 8 query rows:
-// 232 / 92 / 77 us in one step, 94 / 46 / 22 in two; 8 KV heads of 4 rows (156 KB): 39.0 in one, 38.2
+// 232 / 92 / 77 us in one step, 96 / 46 / 22 in two (304 splits each); 8 KV heads of 4 rows (156 KB): 39.0 in one, 38.2
 // to 40.1 in two.
 struct Kv4Groups {
     int group, groups;  // splits of a group; groups of a row (0: no groups)
