@@ -961,7 +961,7 @@ SPD_API spd_status kv4_read(const spd_dims* dims, int32_t T, const uint8_t* kv4,
 // turns of 128 tokens, and a unit costs about `fixed` turns besides its own (the lengths, the
 // queries, the first copies, the join).  Up to half a GPU of rows is cut into one round of
 // units, or, with more than eight query rows, into fewer where the join would take longer (one KV
-// head, 64 query rows, 131,000 / 20,000 tokens: 304 / 157 units 95.6 / 68.0 us, 162 / 46 units 79.6 /
+// head, 64 query rows, 131,000 / 20,000 tokens: 304 / 157 units 95.6 / 68.0 us, 161 / 46 units 79.6 /
 // 49.3 us).  More rows, selections (about equal): the count that takes the least rounds *
 // (turns + fixed).  More rows, whole sequences (their lengths differ, and only the GPU knows
 // them): units + the longest one's tail, rows * S * (turns / S + fixed) / slots + turns / S, is
