@@ -599,6 +599,7 @@ __global__ void __launch_bounds__(Verify4Cfg<D, N>::THREADS, kVerify4Occ) verify
             ok = all_level();
             if (!ok) break;
             if (k > 0) {
+                tmem_fence_after();  // O of step k - 1, whose end this thread has waited for above
 #pragma unroll 1
                 for (int r = 0; r < NH; r += 8) {
                     uint32_t o[8];

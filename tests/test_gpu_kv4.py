@@ -392,6 +392,46 @@ def test_kv4_logits_that_grow_along_the_sequence(spd, T, D):
                           np.arange(length) <= length - T + t, (splits, t, hq))
 
 
+@pytest.mark.parametrize("T,H_q", [(5, 7), (8, 8), (9, 7)])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("splits", [1, 3])
+def test_kv4_logits_that_grow_under_many_query_rows(spd, T, H_q, D, splits):
+    """33 to 64 query rows of a KV head whose largest logit moves up again and again, rows that fall among them: what was
+    summed before is rescaled at many steps, in units that start with and without a visible token."""
+    import torch
+    rng = np.random.default_rng(T * D + splits)
+    length, ps = 1500, 16
+    lens, pt, mp, n, _, _ = paged(rng, [length, T - 2], ps, 1, D)
+    u = np.where(rng.random(D) < 0.5, 1.0, -1.0)
+    k = ref.bf16(np.linspace(0.5, 6.0, length)[:, None, None] * u + 0.1 * rng.standard_normal((length, 1, D)))
+    v = rows_bf16(rng, length, 1, D)
+    dims = spd.dims_of(2, H_q, 1, D, ps, mp, n)
+    one = spd.dims_of(1, H_q, 1, D, ps, mp, n)
+    cache, summ = spd.kv4_cache(dims), torch.zeros((1, 1, mp, 2, D), dtype=torch.bfloat16, device="cuda")
+    for b in range(2):
+        m = int(lens[b])
+        spd.kv4_append(one, m, cache, dev(pt[b: b + 1]), dev(lens[b: b + 1]), to_dev(k[None, :m]), to_dev(v[None, :m]), summ)
+    kd, vd = ref.kv4_values(*ref.kv4_quantise(k, 0), 0)[:, 0], ref.kv4_values(*ref.kv4_quantise(v, 0), 0)[:, 0]
+    size = np.resize(np.array([3.0, -2.0, 0.7, 8.0, 1.5]), H_q)
+    q = ref.bf16(size[None, None, :, None] * u + 0.2 * rng.standard_normal((2, T, H_q, D)))
+    ws = spd.workspace(spd.spd_kv4_dense_verify_workspace_size(dims, T, splits))
+    got = []
+    for _ in range(2):
+        o = torch.full((2, T, H_q, D), float("nan"), dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((2, T, H_q), float("nan"), device="cuda")
+        spd.kv4_dense_verify_attn(dims, T, to_dev(q), cache, dev(pt), dev(lens), o, ws, lse=lse, num_splits=splits)
+        got.append((o, lse))
+    assert spd.spd_device_status(clear=True) == 0
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    og, lg = host(o), host(lse)
+    for b in range(2):
+        m = int(lens[b])
+        for t in range(T):
+            for hq in range(H_q):
+                check_row(og[b, t, hq], lg[b, t, hq], q[b, t, hq], kd[:m], vd[:m], D ** -0.5, np.arange(m) <= m - T + t,
+                          (b, t, hq))
+
+
 def test_kv4_attention_extremes(spd):
     """Large and tiny queries, logits that grow along the sequence (the reference maximum moves again and again)
     and one token that outweighs the rest."""
