@@ -312,7 +312,9 @@ __global__ void __launch_bounds__(kLpThreads, kLpOcc) logprob_kernel(const Logpr
     }
     if (!(edge == NEG_INF)) {  // the thread's single token, NaN too
         const float m = fmaxf(ref, edge);
-        const float d = ref == NEG_INF ? -1e30f : (ref - m) * c2, f = fast_exp2(d), de = (edge - m) * c2, fe = fast_exp2(de);
+        // (d bounded as everywhere: f is 0 far above the bound, and 0 times an infinite product would be NaN)
+        const float d = ref == NEG_INF ? -1e30f : fmaxf((ref - m) * c2, -1e30f), f = fast_exp2(d);
+        const float de = (edge - m) * c2, fe = fast_exp2(de);
         T = fmaf(f, fmaf(d, S, T), fe * fmaxf(de, -1e30f));
         S = fmaf(f, S, fe);
         ref = m;

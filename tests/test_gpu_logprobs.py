@@ -126,6 +126,32 @@ def test_masked_infinite_and_nan_logits(spd):
     assert np.all(got[0] == 0)
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("n", [601, 1001, 50257])
+@pytest.mark.parametrize("offset", [0, 1])
+@pytest.mark.parametrize("inv_t", [0.5, 1.0, 2.0])
+def test_one_token_left_under_a_finite_mask(spd, dtype, n, offset, inv_t):
+    """Masks of the type's lowest value and of -1e38 that leave a row's first, last or any token, in rows whose ends lie
+    outside their whole vectors.  A masked token's weight is exactly 0, so the tolerances are those of the few
+    that are left: z to 2^-24 of 9 at most, exp and the sums by 2^-20."""
+    import torch
+    t_dtype = torch.bfloat16 if dtype == "bf16" else torch.float32
+    lowest = torch.finfo(t_dtype).min
+    left = [{n - 1: 2.5}, {0: -3.0}, {0: 1.0, n - 1: 4.0}, {n // 2: 0.5}, {n - 1: 2.0, n - 2: 2.0, 1: 3.0}, {n - 1: 0.0}]
+    buf = torch.full((offset + len(left) * n,), lowest, dtype=t_dtype, device="cuda")
+    x = buf[offset:].view(len(left), n)
+    x[4:] = -1e38
+    for r, tokens in enumerate(left):
+        for token, logit in tokens.items():
+            x[r, token] = logit
+    t = np.array([max(tokens) for tokens in left])
+    got = call(spd, x, t, 0, inv_t)
+    lp, ent, lse, _, _ = ref.logprobs(host(x), t, inv_t, 0)
+    for a, b in zip(got, (lp, ent, lse)):
+        assert np.all(np.abs(a - b) <= 2.0 ** -20 * (1 + 8 * np.abs(b)) + 9 * 2.0 ** -22), (a, b)
+    assert spd.spd_device_status(clear=True) == 0
+
+
 def test_targets_outside_the_vocabulary(spd):
     rng = np.random.default_rng(4)
     x = rng.standard_normal((4, 50)).astype(np.float32)
