@@ -39,12 +39,14 @@
  *    matching *_workspace_size function returns.  The counters and flags some
  *    calls keep in it (unit queue, split tickets, the step's chain) MUST be
  *    zero before the first call that uses the buffer (zero the whole buffer
- *    once); every successful call leaves them zero again, so a buffer can be
- *    reused by any later call with the same dims on the same stream (zero it again
- *    before a call with a larger B * H_kv than the call before; the calls over the
- *    4-bit cache and token_logprobs keep their tickets apart, so a buffer that serves
- *    those alone needs no zeroing, whatever their sizes).  Calls that overlap on
- *    the GPU must use different workspaces.
+ *    once); every successful call leaves them zero again.  The queue and the tickets
+ *    of every call lie in the buffer's first bytes, where no call writes anything
+ *    else, so a buffer can be reused by any later call, whatever its kind and
+ *    dims, on the same stream.  Two calls keep more, and want the whole buffer
+ *    zeroed again if it has served other calls, or themselves with other sizes:
+ *    sparse_decode_step (its chain lies behind its scores), and sparse_decode_attn
+ *    or dense_verify_attn told to split (num_splits > 1) more than 16,384 rows
+ *    B * H_kv.  Calls that overlap on the GPU must use different workspaces.
  *  - Errors: argument problems are reported synchronously by the returned
  *    status (nothing is launched); spd_last_error() gives a message.  Problems
  *    only the GPU can see (a page id outside [0, num_phys_pages), a selection
@@ -295,8 +297,10 @@ spd_status sparse_decode_attn(const spd_dims *dims, const spd_bf16 *q, const spd
  * rows) as soon as its selection is published (release / acquire flags in the
  * workspace; every wait is bounded and reports SPD_DEV_TIMEOUT).  The
  * workspace (spd_sparse_decode_step_workspace_size bytes) must be zero before
- * its first use and is left zero; calls that overlap on the GPU need separate
- * workspaces.  Errors as the separate calls.
+ * its first use, and before a step with other dims or k_max or behind other calls
+ * that used it; a step leaves it as it needs it, and other calls may follow one.
+ * Calls that overlap on the GPU need separate workspaces.  Errors as the separate
+ * calls.
  */
 size_t spd_sparse_decode_step_workspace_size(const spd_dims *dims, int32_t k_max);
 spd_status sparse_decode_step(const spd_dims *dims, spd_bf16 *K, spd_bf16 *V, const int32_t *page_table,

@@ -110,8 +110,9 @@ struct Kv4Args {
 cudaError_t launch_kv4_append(const Kv4Args& a, cudaStream_t st);
 cudaError_t launch_kv4_read(const Kv4Args& a, cudaStream_t st);
 
-// Split tickets at the start (16 bytes on) of the workspaces of the 4-bit attention and of
-// token_logprobs, the same for every call; more rows than that are not split.
+// Split tickets at the start (16 bytes on) of every workspace, the same for every call: no call's
+// scores or partials lie before kTicketBytes.  (The 4-bit attention and token_logprobs split no
+// more rows than that; where the bf16 attention is told to, its tickets go on behind them.)
 constexpr int kTickets = 16384;
 constexpr size_t kTicketBytes = (16 + kTickets * sizeof(int) + 255) / 256 * 256;
 

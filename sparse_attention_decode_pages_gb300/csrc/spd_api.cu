@@ -195,25 +195,23 @@ struct AttnWs {
 };
 
 // [queue: 16 B][row tickets][partial lse][partial o]; the first two must start zeroed.
-// The scores of pages_score_select start after a prefix as long as the attention
-// calls' counters (queue + tickets) and stay clear of it, so the prefix stays zero
-// and one buffer can serve the calls of a step in turn.
-static size_t score_ws_prefix(const spd_dims* dims) {
-    return align256(16 + (size_t)dims->B * dims->H_kv * sizeof(int));
+// Bytes of the queue and the tickets of these rows alone, as in scratch that no other call shares.
+size_t ticket_bytes(long long rows) { return align256(16 + (size_t)rows * sizeof(int)); }
+
+// The same in a caller's workspace: the place of every call's queue and tickets (those of the
+// 4-bit attention and of token_logprobs too), which scores and partials of any call stay clear
+// of, so it stays zero and one buffer serves calls of any kind and size in turn.
+size_t ws_prefix(long long rows) {
+    const size_t own = ticket_bytes(rows);
+    return own > kTicketBytes ? own : kTicketBytes;
 }
 
-// Bytes of attn_ws_layout the kernel touches: with one unit per row (S = 1) only
-// the queue and the tickets (no partials).
-size_t attn_ws_needed(long long rows, int S, int R, int D);
-
-AttnWs attn_ws_layout(void* ws, long long rows, int S, int R, int D) {
+AttnWs attn_ws_layout(void* ws, long long rows, int S, int R, int D, size_t prefix) {
     AttnWs w;
-    size_t off = 0;
+    size_t off = prefix;
     char* base = static_cast<char*>(ws);
     w.queue = reinterpret_cast<int*>(base);
-    off += 16;
-    w.counters = reinterpret_cast<int*>(base + off);
-    off = align256(off + rows * sizeof(int));
+    w.counters = reinterpret_cast<int*>(base + 16);
     w.part_lse = reinterpret_cast<float*>(base + off);
     off += align256((size_t)rows * S * R * sizeof(float));
     w.part_o = reinterpret_cast<float*>(base + off);
@@ -222,9 +220,11 @@ AttnWs attn_ws_layout(void* ws, long long rows, int S, int R, int D) {
     return w;
 }
 
-size_t attn_ws_needed(long long rows, int S, int R, int D) {
-    if (S == 1) return align256(16 + (size_t)rows * sizeof(int));
-    return attn_ws_layout(nullptr, rows, S, R, D).bytes;
+// Bytes of attn_ws_layout the kernel touches: with one unit per row (S = 1) only
+// the queue and the tickets (no partials).
+size_t attn_ws_needed(long long rows, int S, int R, int D, size_t prefix) {
+    if (S == 1) return ticket_bytes(rows);
+    return attn_ws_layout(nullptr, rows, S, R, D, prefix).bytes;
 }
 
 }  // namespace
@@ -263,7 +263,8 @@ SPD_API spd_status spd_device_status(uint32_t* out, int32_t clear) {
 
 SPD_API size_t spd_score_select_workspace_size(const spd_dims* dims) {
     if (check_dims(dims) != SPD_OK) return 0;
-    return score_ws_prefix(dims) + (size_t)dims->B * dims->H_kv * dims->max_pages_per_seq * sizeof(float);
+    const long long rows = (long long)dims->B * dims->H_kv;
+    return ws_prefix(rows) + (size_t)rows * dims->max_pages_per_seq * sizeof(float);
 }
 
 SPD_API size_t spd_sparse_decode_workspace_size(const spd_dims* dims, int32_t k_max, int32_t num_splits) {
@@ -276,7 +277,8 @@ SPD_API size_t spd_sparse_decode_workspace_size(const spd_dims* dims, int32_t k_
     DevInfo* d = dev_info(&st);
     if (!d) return 0;
     const int S = sparse_splits(dims, k_max, num_splits, d->sms);
-    return attn_ws_layout(nullptr, (long long)dims->B * dims->H_kv, S, dims->H_q / dims->H_kv, dims->D).bytes;
+    const long long rows = (long long)dims->B * dims->H_kv;
+    return attn_ws_layout(nullptr, rows, S, dims->H_q / dims->H_kv, dims->D, ws_prefix(rows)).bytes;
 }
 
 SPD_API size_t spd_dense_verify_workspace_size(const spd_dims* dims, int32_t T, int32_t num_splits) {
@@ -289,7 +291,8 @@ SPD_API size_t spd_dense_verify_workspace_size(const spd_dims* dims, int32_t T, 
     DevInfo* d = dev_info(&st);
     if (!d) return 0;
     const int S = dense_splits(dims, T, num_splits, d->sms);
-    return attn_ws_layout(nullptr, (long long)dims->B * dims->H_kv, S, T * (dims->H_q / dims->H_kv), dims->D).bytes;
+    const long long rows = (long long)dims->B * dims->H_kv;
+    return attn_ws_layout(nullptr, rows, S, T * (dims->H_q / dims->H_kv), dims->D, ws_prefix(rows)).bytes;
 }
 
 SPD_API spd_status pages_summarize(const spd_dims* dims, const spd_bf16* K, const int32_t* page_table,
@@ -426,7 +429,7 @@ static spd_status score_select_setup(const spd_dims* dims, const spd_bf16* q, co
     a.sel = sel;
     a.nsel = nsel;
     a.k_max = k_max;
-    a.scores = scores ? scores : reinterpret_cast<float*>(static_cast<char*>(ws) + score_ws_prefix(dims));
+    a.scores = scores ? scores : reinterpret_cast<float*>(static_cast<char*>(ws) + ws_prefix((long long)dims->B * dims->H_kv));
     a.B = dims->B;
     a.H_q = dims->H_q;
     a.H_kv = dims->H_kv;
@@ -485,17 +488,18 @@ static spd_status attn_common(const spd_dims* dims, const spd_bf16* q, const spd
 }
 
 // Validates and launches the sparse attention kernel with S units per row (S >= 1
-// already chosen); sel_done != NULL chains it behind the selection of each row.
+// already chosen) and `prefix` bytes for the queue and the tickets; sel_done != NULL chains
+// it behind the selection of each row.
 static spd_status sparse_attn_launch(const spd_dims* dims, const spd_bf16* q, const spd_bf16* K, const spd_bf16* V,
                                      const int32_t* page_table, const int32_t* seq_lens, const int32_t* sel,
                                      const int32_t* nsel, int32_t k_max, int S, float softmax_scale, spd_bf16* o,
-                                     float* lse, void* ws, size_t ws_bytes, unsigned* sel_done,
+                                     float* lse, void* ws, size_t ws_bytes, size_t prefix, unsigned* sel_done,
                                      const int32_t* sel_phys, DevInfo* d, void* stream) {
     spd_status st;
     const int G = dims->H_q / dims->H_kv;
     const long long rows = (long long)dims->B * dims->H_kv;
-    AttnWs w = attn_ws_layout(ws, rows, S, G, dims->D);
-    const size_t need = attn_ws_needed(rows, S, G, dims->D);
+    AttnWs w = attn_ws_layout(ws, rows, S, G, dims->D, prefix);
+    const size_t need = attn_ws_needed(rows, S, G, dims->D, prefix);
     if (!ws || ws_bytes < need) return fail(SPD_ERR_WORKSPACE, "workspace %zu bytes < %zu", ws_bytes, need);
     if (!aligned16(ws)) return fail(SPD_ERR_INVALID_ARG, "ws must be 16-byte aligned");
     CUtensorMap tk, tv;
@@ -549,7 +553,7 @@ SPD_API spd_status sparse_decode_attn(const spd_dims* dims, const spd_bf16* q, c
     if (!d) return st;
     return sparse_attn_launch(dims, q, K, V, page_table, seq_lens, sel, nsel, k_max,
                               sparse_splits(dims, k_max, num_splits, d->sms), softmax_scale, o, lse, ws, ws_bytes,
-                              nullptr, nullptr, d, stream);
+                              ws_prefix((long long)dims->B * dims->H_kv), nullptr, nullptr, d, stream);
 }
 
 // The chained step's workspace: [score / select][chain: two tile counters, warps
@@ -574,7 +578,7 @@ static bool step_ws_layout(const spd_dims* dims, int32_t k_max, StepWs* w, DevIn
     w->keys = align256(32 + 2 * (size_t)rows * sizeof(unsigned));  // offset of the keys in the chain part
     w->phys = w->keys + align256((size_t)rows * dims->max_pages_per_seq * sizeof(unsigned));
     w->chain = w->phys + align256((size_t)rows * k_max * sizeof(int32_t));
-    w->attn = attn_ws_layout(nullptr, rows, S, dims->H_q / dims->H_kv, dims->D).bytes;
+    w->attn = attn_ws_layout(nullptr, rows, S, dims->H_q / dims->H_kv, dims->D, ticket_bytes(rows)).bytes;
     w->bytes = w->score + w->chain + w->attn;
     return w->score != 0;
 }
@@ -642,7 +646,7 @@ SPD_API spd_status sparse_decode_step(const spd_dims* dims, spd_bf16* K, spd_bf1
     cudaError_t e = launch_score_select(a, d->sms, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "sparse_decode_step scoring launch");
     return sparse_attn_launch(dims, q, K, V, page_table, seq_lens, sel, nsel, k_max, S, softmax_scale, o, lse,
-                              base + w.score + w.chain, w.attn, sel_done, a.sel_phys, d, stream);
+                              base + w.score + w.chain, w.attn, ticket_bytes(rows), sel_done, a.sel_phys, d, stream);
 }
 
 SPD_API spd_status dense_verify_attn(const spd_dims* dims, int32_t T, const spd_bf16* q, const spd_bf16* K,
@@ -660,7 +664,7 @@ SPD_API spd_status dense_verify_attn(const spd_dims* dims, int32_t T, const spd_
     if (!d) return st;
     const int S = dense_splits(dims, T, num_splits, d->sms);
     const long long rows = (long long)dims->B * dims->H_kv;
-    AttnWs w = attn_ws_layout(ws, rows, S, T * G, dims->D);
+    AttnWs w = attn_ws_layout(ws, rows, S, T * G, dims->D, ws_prefix(rows));
     if (!ws || ws_bytes < w.bytes) return fail(SPD_ERR_WORKSPACE, "workspace %zu bytes < %zu", ws_bytes, w.bytes);
     if (!aligned16(ws)) return fail(SPD_ERR_INVALID_ARG, "ws must be 16-byte aligned");
     CUtensorMap tk, tv;
@@ -765,24 +769,23 @@ SPD_API spd_status sparse_decode_attn_noalloc(const spd_dims* dims, const spd_bf
     if (!scratch) return st;
     const int G = dims->H_q / dims->H_kv;
     const long long rows = (long long)dims->B * dims->H_kv;
+    const size_t prefix = ticket_bytes(rows);
     int S = sparse_splits(dims, k_max, num_splits, d->sms);
     if (num_splits == 0) {
         // automatic: the usual split count, or fewer until the partials fit
-        while (S > 1 && attn_ws_needed(rows, S, G, dims->D) > SPD_NOALLOC_SCRATCH_BYTES)
+        while (S > 1 && attn_ws_needed(rows, S, G, dims->D, prefix) > SPD_NOALLOC_SCRATCH_BYTES)
             S = sparse_splits(dims, k_max, S - 1, d->sms);
     }
-    const size_t need = attn_ws_needed(rows, S, G, dims->D);
+    const size_t need = attn_ws_needed(rows, S, G, dims->D, prefix);
     if (need > SPD_NOALLOC_SCRATCH_BYTES)
         return fail(SPD_ERR_UNSUPPORTED,
                     "sparse_decode_attn_noalloc needs %zu bytes of scratch for %d split(s); the fixed array holds %zu",
                     need, S, (size_t)SPD_NOALLOC_SCRATCH_BYTES);
     // the queue and the split tickets must start at zero
-    const AttnWs w = attn_ws_layout(scratch, rows, S, G, dims->D);
-    const size_t zero_bytes = reinterpret_cast<char*>(w.part_lse) - static_cast<char*>(scratch);
-    cudaError_t e = cudaMemsetAsync(scratch, 0, zero_bytes, static_cast<cudaStream_t>(stream));
+    cudaError_t e = cudaMemsetAsync(scratch, 0, prefix, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "clearing the fixed scratch array");
     return sparse_attn_launch(dims, q, K, V, page_table, seq_lens, sel, nsel, k_max, S, softmax_scale, o, lse,
-                              scratch, SPD_NOALLOC_SCRATCH_BYTES, nullptr, nullptr, d, stream);
+                              scratch, SPD_NOALLOC_SCRATCH_BYTES, prefix, nullptr, nullptr, d, stream);
 }
 
 // ---------------------------------------------------------------- head norms and rotation
@@ -1032,8 +1035,8 @@ static Kv4Groups kv4_groups(long long rows, int S, int R, int D) {
     return g;
 }
 
-// The workspace: tickets at its start, where the bf16 attention's are, with room for the rows of any
-// call that splits them, so that no partials lie where another call's tickets are.
+// The workspace: tickets at its start, the rows' where the bf16 attention's are and the groups'
+// behind them, within the place that no call's scores or partials reach (ws_prefix).
 static AttnWs kv4_ws_layout(void* ws, long long rows, int S, int R, int D) {
     S += kv4_groups(rows, S, R, D).groups;
     AttnWs w;

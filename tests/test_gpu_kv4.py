@@ -662,6 +662,80 @@ def test_one_workspace_for_calls_of_different_sizes(spd):
     assert spd.spd_device_status(clear=True) == 0
 
 
+def test_one_workspace_for_every_call(spd):
+    """Scoring, attention over both caches (in few splits, in many, joined in groups) and scored rows, of several sizes, in
+    any order through one buffer that a step has used before: the bits of buffers of their own."""
+    import torch
+    rng = np.random.default_rng(99)
+    calls, steps = [], []
+    for lens, T, H_q, H_kv, D, ps, k_max in (([16384, 9000], 7, 32, 8, 128, 16, 64), ([16400], 1, 64, 8, 128, 16, 1024),
+                                             ([700, 40, 0, 333, 512], 2, 8, 4, 64, 32, 8), ([90] * 70, 3, 4, 4, 64, 16, 4)):
+        lens, pt, mp, n, K, V = paged(rng, lens, ps, H_kv, D)
+        B = len(lens)
+        dims, d_pt, d_lens = spd.dims_of(B, H_q, H_kv, D, ps, mp, n), dev(pt), dev(lens)
+        kv4 = rng.integers(0, 256, (n, H_kv, 2, ps * D * 9 // 16)).astype(np.uint8)
+        kv4[..., ps * D // 2:] = rng.integers(0x30, 0x3C, kv4[..., ps * D // 2:].shape)
+        kv4 = dev(kv4)
+        lo = rng.standard_normal((B, H_kv, mp, 1, D))
+        summ = to_dev(ref.bf16(np.concatenate([lo, lo + 1], 3)))
+        q = to_dev(rows_bf16(rng, B, T, H_q, D))
+        q1 = q[:, 0].contiguous()
+        pol = spd.Policy(0, k_max, 0, 0, 1, 0, 1, 1, 1, 1)
+        sel = torch.zeros((B, H_kv, k_max), dtype=torch.int32, device="cuda")
+        nsel = torch.zeros((B, H_kv), dtype=torch.int32, device="cuda")
+
+        def select(ws, q1=q1, dims=dims, summ=summ, d_lens=d_lens, pol=pol, sel=sel, nsel=nsel, k_max=k_max):
+            a, b = torch.full_like(sel, -1), torch.full_like(nsel, -1)
+            spd.pages_score_select(dims, q1, summ, d_lens, pol, a, b, k_max, ws)
+            a[torch.arange(k_max, device="cuda") >= b[..., None]] = 0
+            return a, b
+
+        first = select(spd.workspace(spd.spd_score_select_workspace_size(dims)))
+        sel.copy_(first[0])
+        nsel.copy_(first[1])
+
+        def attend(f, *args, like=None):
+            def run(ws):
+                o = torch.full_like(like, float("nan"))
+                lse = torch.full(like.shape[:-1], float("nan"), device="cuda")
+                f(*args, o, ws, lse=lse)
+                return o, lse
+            return run
+
+        steps.append((spd.spd_sparse_decode_step_workspace_size(dims, k_max),
+                      lambda ws, a=(dims, K, V, d_pt, d_lens, None, None, q1, summ, pol, sel.clone(), nsel.clone(), k_max):
+                      spd.sparse_decode_step(*a, torch.empty_like(a[7]), ws)))
+        calls += [
+            (spd.spd_score_select_workspace_size(dims), select),
+            (spd.spd_sparse_decode_workspace_size(dims, k_max),
+             attend(spd.sparse_decode_attn, dims, q1, K, V, d_pt, d_lens, sel, nsel, k_max, like=q1)),
+            (spd.spd_dense_verify_workspace_size(dims, T), attend(spd.dense_verify_attn, dims, T, q, K, V, d_pt, d_lens, like=q)),
+            (spd.spd_kv4_sparse_decode_workspace_size(dims, k_max),
+             attend(spd.kv4_sparse_decode_attn, dims, q1, kv4, d_pt, d_lens, sel, nsel, k_max, like=q1)),
+            (spd.spd_kv4_dense_verify_workspace_size(dims, T),
+             attend(spd.kv4_dense_verify_attn, dims, T, q, kv4, d_pt, d_lens, like=q)),
+        ]
+    for rows, n in ((70, 20001), (3, 151936)):
+        x, t = dev(rng.standard_normal((rows, n)).astype(np.float32)), dev(rng.integers(0, n, rows).astype(np.int32))
+
+        def score(ws, rows=rows, x=x, t=t):
+            out = [torch.full((rows,), float("nan"), device="cuda") for _ in range(3)]
+            ids, top = torch.full((rows, 5), -9, dtype=torch.int32, device="cuda"), torch.zeros((rows, 5), device="cuda")
+            spd.token_logprobs(x, t, out[0], ws, entropy=out[1], lse=out[2], top_ids=ids, top_logprobs=top)
+            return (*out, ids, top)
+
+        calls.append((spd.spd_token_logprobs_workspace_size(rows, n, 5), score))
+    want = [f(spd.workspace(size)) for size, f in calls]
+    ws = spd.workspace(max(size for size, _ in calls + steps))
+    steps[2][1](ws)
+    order = np.concatenate([np.arange(len(calls)), *(rng.permutation(len(calls)) for _ in range(8))])
+    wrong = []
+    for before, i in zip([-1, *order], order):
+        wrong += [(int(before), int(i)) for got, own in zip(calls[i][1](ws), want[i]) if not torch.equal(got, own)]
+    assert not wrong, wrong
+    assert spd.spd_device_status(clear=True) == 0
+
+
 @pytest.mark.parametrize("T,H_q,D,splits", [(1, 8, 128, 2), (1, 8, 64, 1), (6, 16, 128, 2), (7, 8, 64, 1)])
 def test_kv4_attention_with_waits_that_run_out(spd, T, H_q, D, splits):
     """A limit that no copy meets: the calls return with the timeout bit (or, should every copy be early, clean), all

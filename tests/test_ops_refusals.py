@@ -99,6 +99,14 @@ def test_kv4_refusals(spd):
     assert L.spd_kv4_dense_verify_workspace_size(B(d), 33, 0) == 0
 
 
+@pytest.mark.parametrize("B,H_kv", [(1, 1), (2, 8), (2048, 8), (5000, 8)])
+def test_scores_lie_behind_every_calls_tickets(spd, B, H_kv):
+    """A queue of 16 bytes and the tickets of 16,384 rows, or of the call's own where they are more."""
+    d = spd.dims_of(B, H_kv, H_kv, 64, 16, 9, 16)
+    size = spd.lib().spd_score_select_workspace_size(ctypes.byref(d))
+    assert size - B * H_kv * 9 * 4 >= 16 + 4 * max(16384, B * H_kv)
+
+
 def test_token_logprobs_refusals(spd):
     def call(rows=2, n=50, x=A, bf=0, stride=50, t=A, inv=1.0, lp=A, k=0, ids=None, tops=None):
         return spd.lib().token_logprobs(rows, n, x, bf, stride, t, inv, lp, None, None, k, ids, tops, A, 1 << 20, None)
