@@ -546,8 +546,9 @@ spd_status kv4_dense_verify_attn(const spd_dims *dims, int32_t T, const spd_bf16
  * alternative: where fewer than top_k logits are above -inf the rest is id -1, logprob
  * -inf.  A row with no logit above -inf has lse = -inf, logprob = -inf, entropy = 0.
  * A NaN makes its row's lse, logprob and entropy NaN and is never an alternative.
- * Supported: 1 <= n_vocab <= 2^21, 0 <= top_k <= 32, inv_temperature > 0 and finite,
- * 0 <= rows < 2^31 (0: no-op); logits aligned to their type.
+ * Supported: 1 <= n_vocab <= 2^21, 0 <= top_k <= 32, inv_temperature > 0 and
+ * finite, times log2(e) too (up to 2.35e38), 0 <= rows < 2^31 (0: no-op); logits aligned
+ * to their type.
  */
 size_t spd_token_logprobs_workspace_size(int64_t rows, int32_t n_vocab, int32_t top_k);
 spd_status token_logprobs(int64_t rows, int32_t n_vocab, const void *logits, int32_t logits_bf16,

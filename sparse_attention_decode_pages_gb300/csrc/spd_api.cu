@@ -1189,8 +1189,8 @@ SPD_API spd_status token_logprobs(int64_t rows, int32_t n_vocab, const void* log
     spd_status st = logprob_shape(rows, n_vocab, top_k);
     if (st != SPD_OK) return st;
     if (row_stride < n_vocab) return fail(SPD_ERR_INVALID_ARG, "row_stride %lld < n_vocab %d", (long long)row_stride, n_vocab);
-    if (!(inv_temperature > 0.f && inv_temperature <= 3.4e38f))
-        return fail(SPD_ERR_INVALID_ARG, "inv_temperature must be > 0 and finite");
+    if (!(inv_temperature > 0.f && inv_temperature * kLog2e <= 3.4e38f))
+        return fail(SPD_ERR_INVALID_ARG, "inv_temperature must be > 0 and finite, times log2(e) too");
     if (rows == 0) return SPD_OK;
     if (!logits || (logprob && !targets) || (top_k > 0 && (!top_ids || !top_logprobs)))
         return fail(SPD_ERR_INVALID_ARG, "NULL pointer argument");

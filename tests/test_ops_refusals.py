@@ -124,6 +124,12 @@ def test_token_logprobs_refusals(spd):
     assert spd.lib().spd_token_logprobs_workspace_size(1, 0, 0) == 0
 
 
+def test_token_logprobs_refuses_a_temperature_past_its_exponents(spd):
+    """Differences of logits are scaled by inv_temperature * log2(e): where that is infinite, 0 times it is NaN."""
+    for inv in (2.4e38, 3e38, 3.4028e38):
+        assert spd.lib().token_logprobs(2, 50, A, 0, 50, A, inv, A, None, None, 0, None, None, A, 1 << 20, None) == INVALID
+
+
 def test_the_binding_checks_its_tensors(spd):
     """Host tensors are refused before anything is called (types, sizes and strides need a device tensor)."""
     import torch
