@@ -279,7 +279,7 @@ __device__ __forceinline__ uint32_t swz128(int r, int c) {
 // SPD_DEV_BAD_LEN raised by the caller).
 __device__ __forceinline__ int seq_pages(int len, int ps, int max_pages) {
     if (len < 0 || (long long)len > (long long)max_pages * ps) return -1;
-    return (len + ps - 1) / ps;
+    return (int)(((unsigned)len + ps - 1) / ps);
 }
 
 // Order-preserving map of fp32 to uint32 (larger float -> larger key).

@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kKv4Threads, 4) kv4_append_kernel(const Kv4Arg
     }
     const int first = len - a.T;
     const int p = first / a.ps + (int)blockIdx.y;
-    if (p >= a.max_pages || p * a.ps >= len) return;
+    if (p >= a.max_pages || (long long)p * a.ps >= len) return;
     const int valid = min(a.ps, len - p * a.ps);
     const long long phys = a.page_table[(long long)b * a.max_pages + p];
     if (phys < 0 || phys >= a.num_phys) {

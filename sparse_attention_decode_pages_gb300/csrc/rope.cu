@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) append_rope_kernel(const Appe
     }
     const int first = len - a.T;  // position of the first new token
     const int pg = first / a.ps + (page_cta - b * p.touched);
-    if (pg * a.ps >= len) return;
+    if ((long long)pg * a.ps >= len) return;  // (the page behind a sequence of 2^31 - 1 tokens starts past 32 bits)
     const int valid = min(a.ps, len - pg * a.ps);
     const long long phys = a.page_table[(long long)b * a.max_pages + pg];
     if (phys < 0 || phys >= a.num_phys) {

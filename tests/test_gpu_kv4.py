@@ -340,6 +340,43 @@ def test_kv4_long_sequences(spd, length, T, H_q, H_kv, D, ps, splits):
                           D ** -0.5, np.ones(lens[b], bool), (b, hq))
 
 
+def test_kv4_the_longest_sequence(spd):
+    """2^31 - 1 tokens, every page of them the same physical page of zero keys and of ones (33/32 as held) as values: the
+    two newest tokens appended, with their summary, read back, and attended to by one query row."""
+    import torch
+    D, ps, mp, length = 64, 16, 1 << 27, (1 << 31) - 1
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GB of device memory")
+    dims = spd.dims_of(1, 1, 1, D, ps, mp, 2)
+    pt, lens = torch.ones((1, mp), dtype=torch.int32, device="cuda"), torch.tensor([length], dtype=torch.int32, device="cuda")
+    pt[0, -1] = 0
+    summ = torch.empty((1, 1, mp, 2, D), dtype=torch.bfloat16, device="cuda")
+    summ[0, 0, -2:] = 7.0
+    zeros, ones = (torch.full((1, 16, 1, D), x, dtype=torch.bfloat16, device="cuda") for x in (0.0, 1.0))
+    cache = spd.kv4_cache(dims)
+    small = spd.dims_of(2, 1, 1, D, ps, 1, 2)
+    spd.kv4_append(small, 16, cache, torch.tensor([[0], [1]], dtype=torch.int32, device="cuda"),
+                   torch.tensor([16, 16], dtype=torch.int32, device="cuda"), zeros.repeat(2, 1, 1, 1), ones.repeat(2, 1, 1, 1),
+                   torch.empty((2, 1, 1, 2, D), dtype=torch.bfloat16, device="cuda"))
+    before = cache.clone()
+    rng = np.random.default_rng(8)
+    k, v = (to_dev(ref.bf16(rng.standard_normal((1, 2, 1, D)))) for _ in range(2))
+    spd.kv4_append(dims, 2, cache, pt, lens, k, v, summ)
+    ko, vo = torch.empty_like(k), torch.empty_like(v)
+    spd.kv4_read(dims, 2, cache, pt, lens, ko, vo)
+    want = ref.kv4_values(*ref.kv4_quantise(host(k), 0), 0)
+    assert np.array_equal(host(ko), want) and np.array_equal(host(vo), ref.kv4_values(*ref.kv4_quantise(host(v), 0), 0))
+    assert np.array_equal(host(summ[0, 0, -1]), np.stack([np.minimum(want[0, :, 0].min(0), 0), np.maximum(want[0, :, 0].max(0), 0)]))
+    assert torch.all(summ[0, 0, -2] == 7.0) and torch.equal(cache[1], before[1])
+    cache.copy_(before)
+    q = to_dev(rows_bf16(rng, 1, 1, 1, D))
+    o, lse = torch.full_like(q, float("nan")), torch.full((1, 1, 1), float("nan"), device="cuda")
+    spd.kv4_dense_verify_attn(dims, 1, q, cache, pt, lens, o, spd.workspace(spd.spd_kv4_dense_verify_workspace_size(dims, 1)), lse=lse)
+    assert spd.spd_device_status(clear=True) == 0
+    assert np.all(host(o) == ref.kv4_values(*ref.kv4_quantise(np.ones(16), 0), 0)[0])
+    assert np.all(np.abs(host(lse) - np.log(float(length))) <= 32 * 2.0 ** -22)
+
+
 @pytest.mark.parametrize("T,H_q", [(1, 4), (4, 8), (7, 4), (8, 8)])
 @pytest.mark.parametrize("D", [64, 128])
 def test_kv4_empty_and_short_sequences(spd, T, H_q, D):

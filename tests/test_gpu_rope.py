@@ -129,6 +129,30 @@ def paged(rng, lens, ps, H_kv, D, spare=2):
     return lens, pt, mp, n, K, V
 
 
+def test_kv_append_rope_to_the_longest_sequence(spd):
+    """The newest two of 2^31 - 1 tokens, in the last page of a table of 2^27."""
+    import torch
+    D, ps, mp = 64, 16, 1 << 27
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GB of device memory")
+    rng = np.random.default_rng(9)
+    dims = spd.dims_of(1, 1, 1, D, ps, mp, 2)
+    pt, lens = torch.ones((1, mp), dtype=torch.int32, device="cuda"), torch.tensor([(1 << 31) - 1], dtype=torch.int32, device="cuda")
+    pt[0, -1] = 0
+    summ = torch.empty((1, 1, mp, 2, D), dtype=torch.bfloat16, device="cuda")
+    summ[0, 0, -2:] = 7.0
+    K, V = (dev(rng.standard_normal((2, 1, ps, D)).astype(np.float32), torch.bfloat16) for _ in range(2))
+    want_K, want_V = K.clone(), V.clone()
+    k, v = (dev(rng.standard_normal((1, 2, 1, D)).astype(np.float32), torch.bfloat16) for _ in range(2))
+    spd.kv_append_rope(dims, 2, K, V, pt, lens, None, k, v, None, None, summ)
+    torch.cuda.synchronize()
+    assert spd.spd_device_status(clear=True) == 0
+    want_K[0, 0, 13:15], want_V[0, 0, 13:15] = k[0, :, 0], v[0, :, 0]
+    assert torch.equal(K, want_K) and torch.equal(V, want_V)
+    held = want_K[0, 0, :15]
+    assert torch.equal(summ[0, 0, -1], torch.stack([held.amin(0), held.amax(0)])) and torch.all(summ[0, 0, -2] == 7.0)
+
+
 APPEND = [  # lens, T, ps, H_q, H_kv, D, rot, interleaved, norm
     ([1, 17, 16, 130], 1, 16, 8, 2, 128, 128, False, True),
     ([40, 33, 64], 33, 32, 7, 1, 64, 32, True, True),
