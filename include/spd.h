@@ -545,7 +545,8 @@ spd_status kv4_dense_verify_attn(const spd_dims *dims, int32_t T, const spd_bf16
  * A logit of -inf (a masked token) has probability 0, logprob -inf and is never an
  * alternative: where fewer than top_k logits are above -inf the rest is id -1, logprob
  * -inf.  A row with no logit above -inf has lse = -inf, logprob = -inf, entropy = 0.
- * A NaN makes its row's lse, logprob and entropy NaN and is never an alternative.
+ * A NaN makes its row's lse, logprob and entropy NaN and is never an alternative.  So does
+ * +inf (it leaves no distribution), which is the first alternative with logprob NaN.
  * Supported: 1 <= n_vocab <= 2^21, 0 <= top_k <= 32, inv_temperature > 0 and
  * finite, times log2(e) too (up to 2.35e38), 0 <= rows < 2^31 (0: no-op); logits aligned
  * to their type.

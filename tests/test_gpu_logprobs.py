@@ -152,6 +152,24 @@ def test_one_token_left_under_a_finite_mask(spd, dtype, n, offset, inv_t):
     assert spd.spd_device_status(clear=True) == 0
 
 
+@pytest.mark.parametrize("n", [600, 601, 20003])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_an_infinite_logit(spd, n, dtype):
+    """+inf in a vector, as a row's single first or last token, beside a second one, and with all else masked."""
+    import torch
+    rng = np.random.default_rng(n)
+    x = (rng.standard_normal((6, n)) * 3).astype(np.float32)
+    x[0, 5], x[1, 0], x[2, n - 1], x[3, [7, n // 2]] = np.inf, np.inf, np.inf, np.inf
+    x[4], x[4, n - 1] = -np.inf, np.inf
+    d = dev(x, torch.bfloat16 if dtype == "bf16" else torch.float32)
+    t = np.array([5, 3, n - 1, 0, n - 1, 2])
+    with np.errstate(invalid="ignore"):
+        check(call(spd, d, t, 6), host(d), t, 1.0, 6)
+    got = call(spd, d, t, 6)
+    assert np.isnan(np.stack(got[:3])[:, :5]).all() and not np.isnan(np.stack(got[:3])[:, 5]).any()
+    assert np.array_equal(got[3][:5, 0], [5, 0, n - 1, 7, n - 1]) and got[3][3, 1] == n // 2 and np.all(got[3][4, 1:] == -1)
+
+
 def test_targets_outside_the_vocabulary(spd):
     rng = np.random.default_rng(4)
     x = rng.standard_normal((4, 50)).astype(np.float32)
