@@ -26,13 +26,13 @@
 // of tokens 2c, 2c+1, 2c+8, 2c+9.
 //
 // Measured on the pipes: a chunk costs an SM quarter 64 conversions (2 cycles each), 64
-// fp16 products and 16 mma (8 cycles each, during which nothing else issues), so
-// arithmetic, not the 2,304 bytes, bounds it: 64 sequences x 64 pages of 16 tokens, 32 / 8
-// heads of 128: 22.6 us, 3.4 TB/s of keys and values, 50 % of the measured copy peak (and 512
-// units on 152 SMs: the SMs that get four of them end last); one sequence of 131,072
-// tokens in 76 splits: 39.2 us, 3.85 TB/s, 57 %.
-#include <atomic>
-
+// fp16 products and 16 mma (8 cycles each, during which nothing else issues), 320 to 390
+// cycles in all.  64 sequences x 64 pages of 16 tokens, 32 / 8 heads of 128: 22.6 us, 3.4 TB/s of
+// keys and values, 50 % of the measured copy peak.  Half of that is those cycles (54 chunks an SM
+// quarter: 9 to 11 us); the other half is a unit's start (length, selection, page table, first copy,
+// one behind the other, and the queries' scaling) and the join of its warps, about 9 us, which
+// overlap no other work of the unit, and 512 units on 152 SMs, of which those with four end
+// last.  One sequence of 131,072 tokens in 76 splits: 39.5 us, 3.8 TB/s, 56 %.
 #include "attn4.cuh"
 
 namespace spd {

@@ -971,9 +971,13 @@ SPD_API spd_status kv4_read(const spd_dims* dims, int32_t T, const uint8_t* kv4,
 // least at S = sqrt(turns * slots / (rows * fixed)).  Measured: 64 sequences of 8K-16K tokens, 8 KV heads,
 // 28 query rows: S = 1 / 2 / 3 / 4 / 8: 344 / 337 / 333 / 342 / 377 us (3 taken); 40 of
 // 2K-6K, 64 query rows: 1 / 2 / 3: 136 / 150 / 159 us (1 taken); 64 selections of 64
-// pages of 16: 1 / 2 / 4: 23 / 32 / 40 us (1 taken); one sequence of 131,072 tokens: 25 / 38 / 57 /
-// 76: 54 / 40 / 45 / 39 us (76 taken); 8 selections of 256 pages of 32: 4 / 7 / 9 / 14: 29 / 30 / 26 / 33 us
-// (9 taken).
+// pages of 16: 1 / 2 / 4: 23 / 32 / 40 us (1 taken); one sequence of 131,072 tokens, 8 KV heads: 25 / 38 / 44 / 57 /
+// 76 / 90: 57 / 42 / 55 / 46 / 40 / 52 us (76 taken: 38, 57 and 76 are two, three and four units on each of 152 SMs,
+// the counts between them leave some SMs one unit more than others, and 90 takes a second round); 8 selections of
+// 256 pages of 32: 4 / 7 / 9 / 14: 29 / 30 / 26 / 33 us (9 taken).
+// A dense row's units are planned by the page table's width, since only the GPU knows the length; in a table
+// much wider than the sequence fewer of them have work (one of 2,048 / 16,384 / 65,536 tokens in a table for 131,072
+// against one of its own width: 19 / 26 / 37 us against 8 / 17 / 27).
 constexpr long long kJoinBytes = 256 << 10;
 
 static int kv4_splits(const spd_dims* d, int T, int items, bool sparse, int req, int sms) {
