@@ -233,7 +233,6 @@ def prepare(case, seed):
         s["w"] = w * (torch.rand(w.shape, generator=gen, device="cuda") > 0.2)  # some tokens have never been looked at
         s["w_out"] = torch.zeros_like(s["w"])
         s["kept"] = torch.full((b, h_kv, case["budget"]), -1, dtype=torch.int32, device="cuda")
-        s["ws"] = torch.zeros(64 << 20, dtype=torch.uint8, device="cuda")
     return s
 
 
@@ -433,8 +432,7 @@ def _own(s):
                               n_path=s.get("n_path"), sel=s.get("sel"), nsel=s.get("nsel"))
         return s["w_out"]
     sink, recent = _evict_rule(s)
-    spd.kv_evict(dims, s["budget"], sink, recent, s["K"], s["V"], s["table"], s["lens"], s["w"], s["dst_table"], s["kept"], s["w_out"], s["summ"],
-                 s["new_lens"], s["ws"])
+    spd.kv_evict(dims, s["budget"], sink, recent, s["K"], s["V"], s["table"], s["lens"], s["w"], s["dst_table"], s["kept"], s["w_out"], s["summ"], s["new_lens"])
     return s["K"][s["n_src"]:], s["V"][s["n_src"]:], s["w_out"], s["kept"], s["summ"], s["new_lens"]
 
 
