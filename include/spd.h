@@ -84,6 +84,8 @@ typedef enum {
 #define SPD_DEV_BAD_TOKEN 0x10u /* spec_accept: a drafted token outside [0, n_vocab);
                                  * token_logprobs: a target outside [-1, n_vocab) */
 #define SPD_DEV_BAD_POS 0x20u   /* a position outside the rotation's table */
+#define SPD_DEV_BAD_TREE 0x40u  /* a parent that is not before its node, a path entry outside [0, T) or a
+                                 * path length outside [0, T] */
 
 /*
  * Problem shape.  Supported: D in {64, 128}; page_size in {16, 32, 64};
@@ -560,6 +562,139 @@ spd_status token_logprobs(int64_t rows, int32_t n_vocab, const void *logits, int
                           int64_t row_stride, const int32_t *targets, float inv_temperature,
                           float *logprob, float *entropy, float *lse, int32_t top_k, int32_t *top_ids,
                           float *top_logprobs, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Trees of drafted tokens.  A tree of T <= 64 nodes is parents int32 [B][T]: node 0 is
+ * the root (the last token of the sequence, whose keys and values are not in the cache
+ * yet), parents[b][v] the node that v follows, smaller than v, and -1 for a root; a node
+ * with parent -2, or one below such a node, is no node (trees of fewer than T nodes).  Any
+ * other parent sets SPD_DEV_BAD_TREE and makes v no node.  A chain of drafted tokens is
+ * parents = -1, 0, 1, 2, ...
+ * seq_lens counts the cache alone: the nodes' keys and values are rows of their own, and
+ * only an accepted path reaches the cache (kv_append_path), so no page holds a rejected
+ * token and no summary has to be taken back.
+ */
+
+/*
+ * tree_verify_attn -- attention of every node of a tree of drafted tokens over the whole
+ * cache, its ancestors and itself (dense_verify_attn for drafts with alternatives).
+ *
+ * q: bf16 rows of H_q * D, node v of sequence b at row b * T + v, q_stride elements apart;
+ * k_tree, v_tree likewise (H_kv * D), so all three may be views of one projection: strides
+ * multiples of 8, at least the row's length.  Row (b, v) attends over cache tokens
+ * 0 .. seq_lens[b] - 1 and over tree rows u for u = v and v's ancestors.  Outputs o bf16
+ * [B][T][H_q][D] and lse fp32 [B][T][H_q] (may be NULL); the rows of what is no node are
+ * o = 0, lse = -inf.  seq_lens[b] = 0 (a tree on an empty cache) is valid; a length that the
+ * page table has no room for sets SPD_DEV_BAD_LEN and gives such rows to the whole sequence.  A page
+ * id outside [0, num_phys_pages) sets SPD_DEV_BAD_PAGE and its tokens are not seen.
+ * Supported: 1 <= T <= 64, B * H_kv <= 16384, max_pages_per_seq * page_size <= 2^30.  The workspace needs no zeros.
+ */
+size_t spd_tree_verify_workspace_size(const spd_dims *dims, int32_t T);
+spd_status tree_verify_attn(const spd_dims *dims, int32_t T, const spd_bf16 *q, int64_t q_stride,
+                            const spd_bf16 *K, const spd_bf16 *V, const int32_t *page_table,
+                            const int32_t *seq_lens, const spd_bf16 *k_tree, int64_t k_stride,
+                            const spd_bf16 *v_tree, int64_t v_stride, const int32_t *parents,
+                            float softmax_scale, spd_bf16 *o, float *lse, void *ws, size_t ws_bytes,
+                            void *stream);
+
+/*
+ * spec_accept_tree -- a path through a tree of drafted tokens, accepted from given random
+ * numbers so that the tokens follow the target's distribution whatever the tree proposes
+ * (spec_accept for drafts with alternatives that were picked, not drawn: the most likely
+ * tokens of a drafter, as many at a node as one likes).
+ *
+ * q_target fp32 [B][T][n_vocab]: the target's distribution behind each node (rows need not
+ * be normalised); draft int32 [B][T]: the nodes' tokens (the root's is not read);
+ * u_acc fp32 [B][T] and u_res fp32 [B]: uniform numbers in [0, 1).
+ * The walk starts at node 0.  At a node with row q, weights are whole numbers on a 2^-40
+ * grid, W(x) = floor(2^40 * min(q(x), 1)) (0 for q(x) <= 0 or NaN), R = sum W.  Its children c
+ * are tried in ascending order, with token x = draft[c]: c is taken iff
+ * floor(u_acc[c] * R) < W(x); otherwise R -= W(x) and W(x) = 0.  The walk goes on from the
+ * taken child; where none is taken, the last token is the smallest x whose running sum of W
+ * exceeds floor(u_res * R) (-1 where R = 0; u_res >= 1 draws the last x of positive
+ * weight).  Every sum is exact, so results do not depend on any order.
+ * Outputs: n_path int32 [B], the nodes walked, the root among them; path int32 [B][T], these
+ * nodes, then -1; tokens int32 [B][T], what follows each of them (the next one's draft, at last
+ * the drawn token), then -1.  Where node 0 is not a root, n_path = 0 and all else is -1.
+ * A draft outside [0, n_vocab) that is tried is not taken and sets SPD_DEV_BAD_TOKEN.
+ * Supported: 1 <= T <= 64, 1 <= n_vocab <= 2^21, B * 16 < 2^31; q_target 16-byte aligned.
+ */
+spd_status spec_accept_tree(int32_t B, int32_t T, int32_t n_vocab, const float *q_target,
+                            const int32_t *draft, const int32_t *parents, const float *u_acc,
+                            const float *u_res, int32_t *n_path, int32_t *path, int32_t *tokens,
+                            void *stream);
+
+/*
+ * kv_append_path -- appends the accepted path's keys and values to the paged cache and
+ * rebuilds the summaries of the pages they land in, in one kernel.
+ *
+ * For i < n_path[b]: row path[b][i] of k_tree and v_tree (rows as in tree_verify_attn) goes to
+ * position seq_lens[b] + i, bit for bit; summ as kv_append_refresh leaves it; new_lens[b] =
+ * seq_lens[b] + n_path[b] (new_lens int32 [B], not seq_lens itself).  A sequence with a path length
+ * outside [0, T] or an entry outside [0, T) sets SPD_DEV_BAD_TREE, one with a length below 0 or no room
+ * in the page table SPD_DEV_BAD_LEN: its cache is left as it was and new_lens[b] = seq_lens[b].  A page
+ * id outside [0, num_phys_pages) sets SPD_DEV_BAD_PAGE and skips that page's tokens.
+ * Supported: 1 <= T <= 64.  Sequences must not share the pages they append to.
+ */
+spd_status kv_append_path(const spd_dims *dims, int32_t T, spd_bf16 *K, spd_bf16 *V,
+                          const int32_t *page_table, const int32_t *seq_lens, const spd_bf16 *k_tree,
+                          int64_t k_stride, const spd_bf16 *v_tree, int64_t v_stride,
+                          const int32_t *path, const int32_t *n_path, spd_bf16 *summ,
+                          int32_t *new_lens, void *stream);
+
+/*
+ * kv_weights_update -- adds to every cached token the attention weight that the newest
+ * queries gave it: what kv_evict goes by.
+ *
+ * w_in, w_out: fp32 [B][H_kv][max_pages_per_seq * page_size], one weight for a token of a KV
+ * head.  q bf16 [B][T][H_q][D] and lse fp32 [B][T][H_q] are the inputs and the output of the
+ * attention of the newest tokens (dense_verify_attn, sparse_decode_attn with T = 1, or
+ * tree_verify_attn: then path and n_path tell which rows were accepted, and the cache
+ * holds them already).  Sequence b has N = n_path[b] query rows path[b][0 .. N) (without path and n_path:
+ * N = T rows in order), the i-th at position seq_lens[b] - N + i.  For t < seq_lens[b]:
+ *   w_out[b][h][t] = (t < seq_lens[b] - N ? decay * w_in[b][h][t] : 0)
+ *                  + sum over i, g with t <= position i of exp(softmax_scale * q . K[t] - lse)
+ * (hq = h * G + g); other places of w_out are left as they were.  w_in may be w_out, or NULL (all
+ * weights start from 0).  Rows with lse = -inf add nothing.
+ * sel, nsel (both or neither; [B][H_kv][k_max] and [B][H_kv] as pages_score_select writes them): only
+ * tokens of the selected pages get the sum, and only these pages are read.
+ * A length outside the page table's room, or below N, sets SPD_DEV_BAD_LEN, a path entry or length
+ * outside its range SPD_DEV_BAD_TREE: that sequence's weights are left as they were.  A page id outside
+ * [0, num_phys_pages) sets SPD_DEV_BAD_PAGE and its tokens get no sum; a selection entry outside the
+ * sequence's pages, or nsel outside [0, k_max], sets SPD_DEV_BAD_SEL and is passed over (nsel clamped).
+ * Supported: 1 <= T <= 64; path and n_path go together; decay and softmax_scale finite; max_pages_per_seq *
+ * page_size <= 2^30.
+ */
+spd_status kv_weights_update(const spd_dims *dims, int32_t T, const spd_bf16 *q, const float *lse,
+                             const spd_bf16 *K, const int32_t *page_table, const int32_t *seq_lens,
+                             const int32_t *path, const int32_t *n_path, const int32_t *sel,
+                             const int32_t *nsel, int32_t k_max, float decay, float softmax_scale,
+                             const float *w_in, float *w_out, void *stream);
+
+/*
+ * kv_evict -- shortens every sequence to `budget` tokens of each KV head: the first n_sink, the newest
+ * n_recent, and of the others those of the largest weights.
+ *
+ * new_lens[b] = min(seq_lens[b], budget).  Each KV head keeps that many tokens of its own choice (weights fp32
+ * [B][H_kv][max_pages_per_seq * page_size], compared as numbers, NaN below all; the lower position among
+ * equals), in the order of their positions: the j-th kept one, kept[b][h][j] (int32 [B][H_kv][budget], its
+ * old position), has its key and value copied from its page to slot j % page_size of page
+ * dst_table[b][j / page_size], its weight to weights_out[b][h][j], and summ gets the new pages' minima and
+ * maxima.  Places behind new_lens[b] are left as they were, and the old pages too: with dst_table as the
+ * page table and new_lens as the lengths every call goes on over the shortened cache (rotated keys
+ * keep their rotation), and the old pages are free.
+ * dst_table is int32 [B][max_pages_per_seq]; its first ceil(new_lens[b] / page_size) pages must be pages that no
+ * sequence of the call reads or writes otherwise (old pages may be shared by sequences).  weights_out is not
+ * weights, new_lens not seq_lens.  A length that the page table has no room for sets SPD_DEV_BAD_LEN: nothing is
+ * written for it but new_lens[b] = 0.  A page id outside [0, num_phys_pages) sets SPD_DEV_BAD_PAGE: tokens
+ * read from it become zeros, a new page is skipped.
+ * Supported: 1 <= budget, 0 <= n_sink, n_recent, n_sink + n_recent <= budget, max_pages_per_seq * page_size
+ * <= 2^30, B * H_kv * max_pages_per_seq < 2^31.
+ */
+spd_status kv_evict(const spd_dims *dims, int32_t budget, int32_t n_sink, int32_t n_recent, spd_bf16 *K,
+                    spd_bf16 *V, const int32_t *page_table, const int32_t *seq_lens,
+                    const float *weights, const int32_t *dst_table, int32_t *kept, float *weights_out,
+                    spd_bf16 *summ, int32_t *new_lens, void *stream);
 
 /*
  * spd_round -- one S3R round captured as CUDA graphs: k sparse draft steps,

@@ -27,7 +27,8 @@ __all__ = [
     "Rope", "qk_norm_rope", "kv_append_rope", "kv4_cache", "kv4_append", "kv4_read",
     "kv4_sparse_decode_attn", "kv4_dense_verify_attn", "token_logprobs",
     "spd_kv4_sparse_decode_workspace_size", "spd_kv4_dense_verify_workspace_size",
-    "spd_token_logprobs_workspace_size",
+    "spd_token_logprobs_workspace_size", "DEV_BAD_TREE", "tree_verify_attn", "spec_accept_tree",
+    "kv_append_path", "kv_weights_update", "kv_evict", "spd_tree_verify_workspace_size",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -35,7 +36,7 @@ LIB_PATH = os.path.join(_HERE, "libspd.so")
 
 # device status bits (SPD_DEV_* in include/spd.h)
 DEV_BAD_PAGE, DEV_BAD_SEL, DEV_TIMEOUT, DEV_BAD_LEN, DEV_BAD_TOKEN = 0x1, 0x2, 0x4, 0x8, 0x10
-DEV_BAD_POS = 0x20
+DEV_BAD_POS, DEV_BAD_TREE = 0x20, 0x40
 _STATUS = {0: "OK", 1: "INVALID_ARG", 2: "UNSUPPORTED", 3: "CUDA", 4: "WORKSPACE"}
 _MODES = {"fixed": 0, "linear": 1, "fraction": 2, "top_p": 3}
 
@@ -141,6 +142,13 @@ def lib():
         L.spd_token_logprobs_workspace_size.argtypes = [i64, i32, i32]
         L.spd_token_logprobs_workspace_size.restype = sz
         L.token_logprobs.argtypes = [i64, i32, P, i32, i64, P, f32, P, P, P, i32, P, P, P, sz, P]
+        L.spd_tree_verify_workspace_size.argtypes = [DP, i32]
+        L.spd_tree_verify_workspace_size.restype = sz
+        L.tree_verify_attn.argtypes = [DP, i32, P, i64, P, P, P, P, P, i64, P, i64, P, f32, P, P, P, sz, P]
+        L.spec_accept_tree.argtypes = [i32, i32, i32, P, P, P, P, P, P, P, P, P]
+        L.kv_append_path.argtypes = [DP, i32, P, P, P, P, P, i64, P, i64, P, P, P, P, P]
+        L.kv_weights_update.argtypes = [DP, i32, P, P, P, P, P, P, P, P, P, i32, f32, f32, P, P, P]
+        L.kv_evict.argtypes = [DP, i32, i32, i32, P, P, P, P, P, P, P, P, P, P, P]
         L.spd_round_create.argtypes = [ctypes.POINTER(RoundDesc), ctypes.POINTER(ctypes.c_void_p)]
         L.spd_round_launch.argtypes = [P, i32, P]
         L.spd_round_destroy.argtypes = [P]
@@ -150,7 +158,8 @@ def lib():
                   "sparse_decode_attn_noalloc", "kv_append_refresh", "spec_accept",
                   "pages_append_score_select", "sparse_decode_step", "qk_norm_rope", "kv_append_rope",
                   "kv4_append", "kv4_read", "kv4_sparse_decode_attn", "kv4_dense_verify_attn",
-                  "token_logprobs", "spd_round_create", "spd_round_launch"):
+                  "token_logprobs", "tree_verify_attn", "spec_accept_tree", "kv_append_path",
+                  "kv_weights_update", "kv_evict", "spd_round_create", "spd_round_launch"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -561,6 +570,95 @@ def token_logprobs(logits, targets, logprobs, ws, entropy=None, lse=None, top_id
         _arg(entropy, _F32, "entropy", dev, rows), _arg(lse, _F32, "lse", dev, rows), top_k,
         _arg(top_ids, _I32, "top_ids", dev, rows * top_k),
         _arg(top_logprobs, _F32, "top_logprobs", dev, rows * top_k), _arg(ws, _U8, "ws", dev), ws.numel(), st))
+
+
+def spd_tree_verify_workspace_size(dims: Dims, T: int) -> int:
+    """Bytes of workspace tree_verify_attn needs for trees of T nodes."""
+    return _size(lib().spd_tree_verify_workspace_size(ctypes.byref(dims), T), "tree_verify workspace")
+
+
+def tree_verify_attn(dims: Dims, T: int, q, K, V, page_table, seq_lens, k_tree, v_tree, parents, o, ws, lse=None,
+                     softmax_scale: float | None = None, stream=None):
+    """Attention of every node of a tree of drafted tokens over the cache, its ancestors and itself.
+
+    q [B, T, H_q, D], k_tree and v_tree [B, T, H_kv, D] may be views of one projection; parents int32 [B, T];
+    seq_lens counts the cache without the tree."""
+    dev, st = _here(stream)
+    scale = 1.0 / math.sqrt(dims.D) if softmax_scale is None else softmax_scale
+    B, D, H, n = dims.B, dims.D, dims.H_kv, dims.B * T
+    cache = dims.num_phys_pages * H * dims.page_size * D
+    _check(lib().tree_verify_attn(
+        ctypes.byref(dims), T, _arg(q, _B16, "q", dev, n * dims.H_q * D, True), _row_stride(q, D, "q"),
+        _arg(K, _B16, "K", dev, cache), _arg(V, _B16, "V", dev, cache),
+        _arg(page_table, _I32, "page_table", dev, B * dims.max_pages_per_seq),
+        _arg(seq_lens, _I32, "seq_lens", dev, B), _arg(k_tree, _B16, "k_tree", dev, n * H * D, True),
+        _row_stride(k_tree, D, "k_tree"), _arg(v_tree, _B16, "v_tree", dev, n * H * D, True),
+        _row_stride(v_tree, D, "v_tree"), _arg(parents, _I32, "parents", dev, n), scale,
+        _arg(o, _B16, "o", dev, n * dims.H_q * D), _arg(lse, _F32, "lse", dev, n * dims.H_q),
+        _arg(ws, _U8, "ws", dev), ws.numel(), st))
+
+
+def spec_accept_tree(q_target, draft, parents, u_acc, u_res, n_path, path, tokens, stream=None):
+    """The accepted path through a tree: q_target fp32 [B, T, n], draft and parents int32 [B, T], u_acc [B, T],
+    u_res [B]; writes n_path [B], path and tokens [B, T]."""
+    dev, st = _here(stream)
+    if q_target.dim() != 3:
+        raise SpdError(1, f"q_target must be [B, T, n_vocab], not {list(q_target.shape)}")
+    B, T, n = q_target.shape
+    _check(lib().spec_accept_tree(
+        B, T, n, _arg(q_target, _F32, "q_target", dev), _arg(draft, _I32, "draft", dev, B * T),
+        _arg(parents, _I32, "parents", dev, B * T), _arg(u_acc, _F32, "u_acc", dev, B * T),
+        _arg(u_res, _F32, "u_res", dev, B), _arg(n_path, _I32, "n_path", dev, B), _arg(path, _I32, "path", dev, B * T),
+        _arg(tokens, _I32, "tokens", dev, B * T), st))
+
+
+def kv_append_path(dims: Dims, T: int, K, V, page_table, seq_lens, k_tree, v_tree, path, n_path, summ, new_lens,
+                   stream=None):
+    """Append the accepted nodes' keys and values (rows path[b, :n_path[b]] of k_tree, v_tree [B, T, H_kv, D]) to
+    the cache, rebuild their pages' summaries, and write the new lengths."""
+    dev, st = _here(stream)
+    B, D, H, pages = dims.B, dims.D, dims.H_kv, dims.max_pages_per_seq
+    n, cache = B * T * H * D, dims.num_phys_pages * H * dims.page_size * D
+    _check(lib().kv_append_path(
+        ctypes.byref(dims), T, _arg(K, _B16, "K", dev, cache), _arg(V, _B16, "V", dev, cache),
+        _arg(page_table, _I32, "page_table", dev, B * pages), _arg(seq_lens, _I32, "seq_lens", dev, B),
+        _arg(k_tree, _B16, "k_tree", dev, n, True), _row_stride(k_tree, D, "k_tree"),
+        _arg(v_tree, _B16, "v_tree", dev, n, True), _row_stride(v_tree, D, "v_tree"),
+        _arg(path, _I32, "path", dev, B * T), _arg(n_path, _I32, "n_path", dev, B),
+        _arg(summ, _B16, "summ", dev, B * H * pages * 2 * D), _arg(new_lens, _I32, "new_lens", dev, B), st))
+
+
+def kv_weights_update(dims: Dims, T: int, q, lse, K, page_table, seq_lens, w_out, w_in=None, path=None, n_path=None,
+                      sel=None, nsel=None, decay: float = 1.0, softmax_scale: float | None = None, stream=None):
+    """Add the newest queries' attention weights to those of the cached tokens, w [B, H_kv, max_pages * page_size]
+    (w_in may be w_out, or None for weights that start at 0)."""
+    dev, st = _here(stream)
+    scale = 1.0 / math.sqrt(dims.D) if softmax_scale is None else softmax_scale
+    B, D, H, pages, rows = dims.B, dims.D, dims.H_kv, dims.max_pages_per_seq, dims.B * T * dims.H_q
+    n_w = B * H * pages * dims.page_size
+    k_max = 0 if sel is None else sel.shape[-1]
+    _check(lib().kv_weights_update(
+        ctypes.byref(dims), T, _arg(q, _B16, "q", dev, rows * D), _arg(lse, _F32, "lse", dev, rows),
+        _arg(K, _B16, "K", dev, dims.num_phys_pages * H * dims.page_size * D),
+        _arg(page_table, _I32, "page_table", dev, B * pages), _arg(seq_lens, _I32, "seq_lens", dev, B),
+        _arg(path, _I32, "path", dev, B * T), _arg(n_path, _I32, "n_path", dev, B),
+        _arg(sel, _I32, "sel", dev, B * H * k_max), _arg(nsel, _I32, "nsel", dev, B * H), k_max, decay, scale,
+        _arg(w_in, _F32, "w_in", dev, n_w), _arg(w_out, _F32, "w_out", dev, n_w), st))
+
+
+def kv_evict(dims: Dims, budget: int, n_sink: int, n_recent: int, K, V, page_table, seq_lens, weights, dst_table,
+             kept, weights_out, summ, new_lens, stream=None):
+    """Copy the `budget` tokens of each KV head that stay (the first n_sink, the newest n_recent, and those of the
+    largest weights) to the pages of dst_table; kept int32 [B, H_kv, budget] gets their old positions."""
+    dev, st = _here(stream)
+    B, D, H, pages = dims.B, dims.D, dims.H_kv, dims.max_pages_per_seq
+    n_w, cache = B * H * pages * dims.page_size, dims.num_phys_pages * H * dims.page_size * D
+    _check(lib().kv_evict(
+        ctypes.byref(dims), budget, n_sink, n_recent, _arg(K, _B16, "K", dev, cache), _arg(V, _B16, "V", dev, cache),
+        _arg(page_table, _I32, "page_table", dev, B * pages), _arg(seq_lens, _I32, "seq_lens", dev, B),
+        _arg(weights, _F32, "weights", dev, n_w), _arg(dst_table, _I32, "dst_table", dev, B * pages),
+        _arg(kept, _I32, "kept", dev, B * H * budget), _arg(weights_out, _F32, "weights_out", dev, n_w),
+        _arg(summ, _B16, "summ", dev, B * H * pages * 2 * D), _arg(new_lens, _I32, "new_lens", dev, B), st))
 
 
 class Round:

@@ -1,0 +1,285 @@
+// evict.cu -- shortens the cache to the tokens of the largest attention weights.
+//
+// Two kernels.  The first chooses: of a (sequence, KV head)'s tokens the first n_sink, the newest
+// n_recent, and the k others of the largest weights.  A weight becomes a 32-bit key in the
+// order of the numbers; the key of the k-th largest is found two bits at a time, from the highest, by
+// counting the keys that reach each of three candidates.  The keys stay in registers meanwhile: 16 a thread,
+// 16,384 tokens a CTA, and a cluster of CTAs for longer rows (the counts are joined through
+// distributed shared memory); rows beyond that are read anew for each count.  Tokens with a larger
+// key stay, and of those with that very key the lowest positions.  A warp holds consecutive tokens, 32 a
+// register, so one scan of the warps' counts and ballots give every kept token its place.
+//
+// The second moves: a warp takes a new page of a KV head, 16 tokens at a time, all their keys' and values' rows in flight at
+// once, and forms the page's minima and maxima on the way.  It is bound by memory: each kept row
+// is read once and written once.
+#include <cooperative_groups.h>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace cg = cooperative_groups;
+
+namespace spd {
+namespace {
+
+constexpr int kThreads = 1024, kWarps = kThreads / 32;
+constexpr int kKeys = 16;                     // keys of a thread
+constexpr int kMaxCluster = 8;
+constexpr int kHeld = kThreads * kKeys;       // tokens that a CTA holds
+
+// Larger weight, larger key; -0 as 0; NaN 0, below every number.
+__device__ __forceinline__ uint32_t weight_key(float w) { return w != w ? 0u : float_key(w + 0.f); }
+
+// HELD: the cluster's registers hold the row.  Otherwise its CTAs go over parts of the row again and again.
+template <bool HELD>
+__global__ void __launch_bounds__(kThreads) choose_kernel(const EvictArgs a) {
+    __shared__ unsigned s_count[2][kMaxCluster][4];  // the CTAs' counts, in turn
+    __shared__ unsigned s_warp[kWarps][4];
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = (int)cluster.block_rank(), size = (int)cluster.num_blocks();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int row = blockIdx.x / size, b = row / a.H_kv;
+    pdl_wait();
+    pdl_trigger();
+    const int len = a.seq_lens[b];
+    const bool head = rank == 0 && tid == 0 && row == b * a.H_kv;
+    if (seq_pages(len, a.ps, a.max_pages) < 0) {  // the same for the whole cluster
+        if (head) {
+            raise_status(a.status, SPD_DEV_BAD_LEN);
+            a.new_lens[b] = 0;
+        }
+        return;
+    }
+    if (head) a.new_lens[b] = min(len, a.budget);
+    int32_t* kept = a.kept + (long long)row * a.budget;
+    if (len <= a.budget) {  // all of them
+        for (long long i = (long long)rank * kThreads + tid; i < len; i += (long long)size * kThreads) kept[i] = (int)i;
+        return;
+    }
+    const int lo = a.n_sink, hi = len - a.n_recent;  // tokens that are chosen by their weights
+    const unsigned k = (unsigned)(a.budget - a.n_sink - a.n_recent);
+    const float* w = a.w + (long long)row * a.max_pages * a.ps;
+
+    // this warp's tokens: `per` times 32 consecutive ones
+    const int warps = size * kWarps;
+    const int per = HELD ? kKeys : (int)(((long long)len + 32LL * warps - 1) / (32LL * warps));
+    const long long base = (long long)(rank * kWarps + warp) * per * 32 + lane;
+    uint32_t key[kKeys];
+    auto key_at = [&](int i) {  // of the warp's i-th 32 tokens; what is not chosen by its weight has none (0)
+        const long long t = base + 32LL * i;
+        return t >= lo && t < hi ? weight_key(__ldg(w + t)) : 0u;
+    };
+    if (HELD) {
+#pragma unroll
+        for (int i = 0; i < kKeys; ++i) key[i] = key_at(i);
+    }
+    // the cluster's counts of four kinds; the warps' own stay in s_warp
+    int turn = 0;
+    auto join = [&](unsigned (&n)[4]) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) n[j] = __reduce_add_sync(0xffffffffu, n[j]);
+        if (lane == 0)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s_warp[warp][j] = n[j];
+        __syncthreads();
+        if (warp < 4) {
+            const unsigned sum = __reduce_add_sync(0xffffffffu, s_warp[lane][warp]);
+            if (size == 1) {
+                if (lane == 0) s_count[turn][0][warp] = sum;
+            } else if (lane < size) {
+                *cluster.map_shared_rank(&s_count[turn][rank][warp], lane) = sum;
+            }
+        }
+        if (size == 1) __syncthreads();
+        else cluster.sync();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            n[j] = 0;
+            for (int r = 0; r < size; ++r) n[j] += s_count[turn][r][j];
+        }
+        turn ^= 1;
+    };
+    if (size > 1) cluster.sync();  // the other CTAs' shared memory is there
+
+    // the largest key that at least k tokens reach
+    uint32_t found = 0;
+    if (k > 0) {
+#pragma unroll 1
+        for (int bit = 30; bit >= 0; bit -= 2) {
+            const uint32_t c1 = found | 1u << bit, c2 = found | 2u << bit, c3 = found | 3u << bit;
+            unsigned n[4] = {0, 0, 0, 0};
+            if (HELD) {
+#pragma unroll
+                for (int i = 0; i < kKeys; ++i) {
+                    n[1] += key[i] >= c1;
+                    n[2] += key[i] >= c2;
+                    n[3] += key[i] >= c3;
+                }
+            } else {
+                for (int i = 0; i < per; ++i) {
+                    const uint32_t x = key_at(i);
+                    n[1] += x >= c1;
+                    n[2] += x >= c2;
+                    n[3] += x >= c3;
+                }
+            }
+            join(n);
+            if (n[3] >= k) found = c3;
+            else if (n[2] >= k) found = c2;
+            else if (n[1] >= k) found = c1;
+        }
+    } else {
+        found = 0xffffffffu;  // no key reaches it: float_key gives at most 0xff800000 for a number
+    }
+
+    // how many stay without regard to ties, and how many tie, up to each warp
+    unsigned n[4] = {0, 0, 0, 0};
+    auto classify = [&](int i, uint32_t x, bool& stays, bool& ties) {
+        const long long t = base + 32LL * i;
+        const bool inner = t >= lo && t < hi;
+        stays = (t < len && !inner) || (inner && x > found);
+        ties = inner && k > 0 && x == found;
+    };
+    auto tally = [&](int i, uint32_t x) {
+        bool stays, ties;
+        classify(i, x, stays, ties);
+        n[0] += stays;
+        n[1] += ties;
+    };
+    if (HELD) {
+#pragma unroll
+        for (int i = 0; i < kKeys; ++i) tally(i, key[i]);
+    } else {
+        for (int i = 0; i < per; ++i) tally(i, key_at(i));
+    }
+    join(n);
+    const unsigned need = (unsigned)a.budget - n[0];  // ties that stay: the first ones
+    unsigned stay_before = 0, tie_before = 0;
+    for (int r = 0; r < rank; ++r) {
+        stay_before += s_count[turn ^ 1][r][0];
+        tie_before += s_count[turn ^ 1][r][1];
+    }
+    for (int i = 0; i < warp; ++i) {
+        stay_before += s_warp[i][0];
+        tie_before += s_warp[i][1];
+    }
+    const unsigned below = (1u << lane) - 1u;
+    auto place = [&](int i, uint32_t x) {
+        bool stays, ties;
+        classify(i, x, stays, ties);
+        const unsigned ms = __ballot_sync(0xffffffffu, stays), mt = __ballot_sync(0xffffffffu, ties);
+        const unsigned my_tie = tie_before + __popc(mt & below);
+        // kept ones before this token: those that stay, and ties up to `need`
+        if (stays || (ties && my_tie < need)) kept[stay_before + __popc(ms & below) + min(my_tie, need)] = (int)(base + 32LL * i);
+        stay_before += __popc(ms);
+        tie_before += __popc(mt);
+    };
+    if (HELD) {
+#pragma unroll
+        for (int i = 0; i < kKeys; ++i) place(i, key[i]);
+    } else {
+        for (int i = 0; i < per; ++i) place(i, key_at(i));
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(128) move_kernel(const EvictArgs a, int pages, long long items) {
+    constexpr int LPR = D * 2 / 16, RPI = 32 / LPR;  // lanes of a row, rows of an access
+    constexpr int ACC = 16 / RPI;                    // accesses for 16 tokens
+    const int lane = threadIdx.x & 31;
+    const long long item = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+    pdl_wait();
+    pdl_trigger();
+    if (item >= items) return;
+    const int page = (int)(item % pages);
+    const long long row = item / pages;  // (sequence, KV head)
+    const int b = (int)(row / a.H_kv), h = (int)(row - (long long)b * a.H_kv);
+    const int m = a.new_lens[b];
+    const int j0 = page * a.ps;
+    if (j0 >= m) return;
+    const int phys = a.dst_table[(long long)b * a.max_pages + page];
+    if (phys < 0 || phys >= a.num_phys) {
+        if (lane == 0) raise_status(a.status, SPD_DEV_BAD_PAGE);
+        return;
+    }
+    const int r0 = lane / LPR, ch = lane % LPR;
+    const long long dst = ((long long)phys * a.H_kv + h) * a.ps;
+    const float* w = a.w + row * a.max_pages * a.ps;
+    float* w_out = a.w_out + row * a.max_pages * a.ps;
+    __nv_bfloat162 mn[4], mx[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        mn[i] = __floats2bfloat162_rn(__int_as_float(0x7f800000), __int_as_float(0x7f800000));
+        mx[i] = __floats2bfloat162_rn(__int_as_float(0xff800000), __int_as_float(0xff800000));
+    }
+    for (int s0 = 0; s0 < a.ps && j0 + s0 < m; s0 += 16) {
+        const int n = min(16, m - j0 - s0);
+        // lane i < n: the i-th token's old row
+        long long from = -1;
+        if (lane < n) {
+            const int t = a.kept[row * a.budget + j0 + s0 + lane];
+            const int p = a.page_table[(long long)b * a.max_pages + t / a.ps];
+            if (p < 0 || p >= a.num_phys) raise_status(a.status, SPD_DEV_BAD_PAGE);
+            else from = ((long long)p * a.H_kv + h) * a.ps + t % a.ps;
+            w_out[j0 + s0 + lane] = w[t];
+        }
+        uint4 k[ACC], v[ACC];
+#pragma unroll
+        for (int i = 0; i < ACC; ++i) {
+            const long long src = __shfl_sync(0xffffffffu, from, i * RPI + r0);
+            k[i] = v[i] = make_uint4(0, 0, 0, 0);
+            if (src >= 0) {
+                k[i] = *(reinterpret_cast<const uint4*>(a.K) + src * LPR + ch);
+                v[i] = *(reinterpret_cast<const uint4*>(a.V) + src * LPR + ch);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < ACC; ++i) {
+            if (i * RPI + r0 >= n) continue;
+            const long long to = (dst + s0 + i * RPI + r0) * LPR + ch;
+            reinterpret_cast<uint4*>(a.K)[to] = k[i];
+            reinterpret_cast<uint4*>(a.V)[to] = v[i];
+            const __nv_bfloat162* e = reinterpret_cast<const __nv_bfloat162*>(&k[i]);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                mn[x] = __hmin2(mn[x], e[x]);
+                mx[x] = __hmax2(mx[x], e[x]);
+            }
+        }
+    }
+#pragma unroll
+    for (int off = LPR; off < 32; off <<= 1) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t x = __shfl_xor_sync(0xffffffffu, *reinterpret_cast<uint32_t*>(&mn[i]), off);
+            const uint32_t y = __shfl_xor_sync(0xffffffffu, *reinterpret_cast<uint32_t*>(&mx[i]), off);
+            mn[i] = __hmin2(mn[i], *reinterpret_cast<const __nv_bfloat162*>(&x));
+            mx[i] = __hmax2(mx[i], *reinterpret_cast<const __nv_bfloat162*>(&y));
+        }
+    }
+    if (r0 == 0) {
+        uint4* out = reinterpret_cast<uint4*>(a.summ + (row * a.max_pages + page) * 2LL * D);
+        out[ch] = *reinterpret_cast<uint4*>(mn);
+        out[LPR + ch] = *reinterpret_cast<uint4*>(mx);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_evict(const EvictArgs& a, int num_sms, cudaStream_t st) {
+    (void)num_sms;
+    if (a.B <= 0) return cudaSuccess;
+    const long long most = (long long)a.max_pages * a.ps, rows = (long long)a.B * a.H_kv;
+    unsigned cluster = 1;
+    while (cluster < kMaxCluster && (long long)cluster * kHeld < most) cluster *= 2;
+    const bool held = (long long)cluster * kHeld >= most;
+    cudaError_t e = launch_pdl_cluster(held ? choose_kernel<true> : choose_kernel<false>, dim3((unsigned)(rows * cluster)), dim3(kThreads), 0,
+                                       cluster, st, a);
+    if (e != cudaSuccess) return e;
+    // no sequence has more than `budget` tokens left
+    const int pages = (int)((most < a.budget ? most : a.budget) + a.ps - 1) / a.ps;
+    const long long items = rows * pages;
+    return launch_pdl(a.D == 128 ? move_kernel<128> : move_kernel<64>, dim3((unsigned)((items + 3) / 4)), dim3(128), 0, st, a, pages, items);
+}
+
+}  // namespace spd

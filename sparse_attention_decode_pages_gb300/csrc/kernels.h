@@ -31,6 +31,27 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
     return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
 
+// The same in clusters of `cluster` CTAs.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl_cluster(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, unsigned cluster,
+                               cudaStream_t st, Args&&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+}
+
 struct SummarizeArgs {
     const uint16_t* K;
     const int32_t* page_table;
@@ -186,6 +207,94 @@ struct SpecArgs {
 };
 cudaError_t launch_spec_accept(const SpecArgs& a, cudaStream_t st);
 size_t spec_smem_bytes(long long n);
+
+// The largest tree of drafted tokens (its masks are 64-bit words).
+constexpr int kTreeMax = 64;
+
+struct TreeAttnArgs {
+    const uint16_t* q;       // rows [B * T] of H_q * D, q_stride elements apart
+    const uint16_t* K;
+    const uint16_t* V;
+    const int32_t* page_table;
+    const int32_t* seq_lens;  // of the cache alone
+    const uint16_t* k_tree;  // rows [B * T] of H_kv * D
+    const uint16_t* v_tree;
+    long long q_stride, k_stride, v_stride;
+    const int32_t* parents;  // [B][T]
+    int B, H_q, H_kv, D, ps, max_pages, T;
+    long long num_phys;
+    float scale_log2;
+    uint16_t* o;
+    float* lse;
+    void* ws;
+    int num_sms;
+    unsigned* status;
+    unsigned long long wait_ns;
+};
+cudaError_t launch_tree_attn(const TreeAttnArgs& a, cudaStream_t st);
+size_t tree_attn_ws(int B, int H_kv, int G, int T, int D, int num_sms);
+
+struct TreeAcceptArgs {
+    const float* q;          // [B][T][n] target probabilities
+    const int32_t* draft;    // [B][T]
+    const int32_t* parents;  // [B][T]
+    const float* u_acc;      // [B][T]
+    const float* u_res;      // [B]
+    int32_t* n_path;         // [B]
+    int32_t* path;           // [B][T]
+    int32_t* tokens;         // [B][T]
+    int B, T;
+    long long n;
+    unsigned* status;
+};
+cudaError_t launch_spec_accept_tree(const TreeAcceptArgs& a, int num_sms, cudaStream_t st);
+
+struct AppendPathArgs {
+    AppendArgs append;  // T = nodes; k_new and v_new: node rows, k_stride and v_stride elements apart
+    long long k_stride, v_stride;
+    const int32_t* path;    // [B][T]
+    const int32_t* n_path;  // [B]
+    int32_t* new_lens;      // [B]
+};
+cudaError_t launch_append_path(const AppendPathArgs& a, cudaStream_t st);
+
+struct WeightsArgs {
+    const uint16_t* q;  // [B][T][H_q][D]
+    const float* lse;   // [B][T][H_q]
+    const uint16_t* K;
+    const int32_t* page_table;
+    const int32_t* seq_lens;
+    const int32_t* path;    // [B][T], with n_path [B]; NULL: all T rows in order
+    const int32_t* n_path;
+    const int32_t* sel;     // [B][H_kv][k_max], with nsel [B][H_kv]; NULL: every page
+    const int32_t* nsel;
+    int k_max;
+    int B, H_q, H_kv, D, ps, max_pages, T;
+    long long num_phys;
+    float decay, scale_log2;
+    const float* w_in;  // [B][H_kv][max_pages * ps] or NULL
+    float* w_out;
+    unsigned* status;
+};
+cudaError_t launch_weights_update(const WeightsArgs& a, cudaStream_t st);
+
+struct EvictArgs {
+    uint16_t* K;
+    uint16_t* V;
+    const int32_t* page_table;
+    const int32_t* seq_lens;
+    const int32_t* dst_table;
+    const float* w;  // [B][H_kv][max_pages * ps]
+    float* w_out;
+    int32_t* kept;   // [B][H_kv][budget]
+    uint16_t* summ;  // [B][H_kv][max_pages][2][D]
+    int32_t* new_lens;
+    int budget, n_sink, n_recent;
+    int B, H_kv, D, ps, max_pages;
+    long long num_phys;
+    unsigned* status;
+};
+cudaError_t launch_evict(const EvictArgs& a, int num_sms, cudaStream_t st);
 
 struct ScoreSelectArgs {
     const uint16_t* q;

@@ -1224,3 +1224,264 @@ SPD_API spd_status token_logprobs(int64_t rows, int32_t n_vocab, const void* log
     cudaError_t e = launch_token_logprobs(a, d->sms, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? SPD_OK : cuda_fail(e, "token_logprobs launch");
 }
+
+// ---------------------------------------------------------------- trees of drafted tokens
+
+// T and the rows of its nodes.
+static spd_status tree_rows(const spd_dims* dims, int32_t T, const spd_bf16* k_tree, int64_t k_stride,
+                            const spd_bf16* v_tree, int64_t v_stride) {
+    if (T < 1 || T > kTreeMax) return fail(SPD_ERR_UNSUPPORTED, "T = %d outside [1, %d]", T, kTreeMax);
+    if (dims->B == 0) return SPD_OK;
+    const int64_t row = (int64_t)dims->H_kv * dims->D;
+    if (!k_tree || !v_tree) return fail(SPD_ERR_INVALID_ARG, "NULL pointer argument");
+    if (!aligned16(k_tree) || !aligned16(v_tree)) return fail(SPD_ERR_INVALID_ARG, "k_tree and v_tree must be 16-byte aligned");
+    if (k_stride < row || k_stride % 8 || v_stride < row || v_stride % 8)
+        return fail(SPD_ERR_INVALID_ARG, "bad row strides (k_stride=%lld v_stride=%lld)", (long long)k_stride, (long long)v_stride);
+    return SPD_OK;
+}
+
+// One position for a token: in 32 signed bits, with room for a tile behind the last.
+static spd_status position_dims(const spd_dims* dims) {
+    if ((long long)dims->max_pages_per_seq * dims->page_size > (1LL << 30))
+        return fail(SPD_ERR_UNSUPPORTED, "max_pages_per_seq * page_size must be at most 2^30");
+    return SPD_OK;
+}
+
+static spd_status tree_attn_dims(const spd_dims* dims, int32_t T) {
+    spd_status st = check_dims(dims);
+    if (st == SPD_OK) st = position_dims(dims);
+    if (st != SPD_OK) return st;
+    if (T < 1 || T > kTreeMax) return fail(SPD_ERR_UNSUPPORTED, "T = %d outside [1, %d]", T, kTreeMax);
+    if ((long long)dims->B * dims->H_kv > 16384) return fail(SPD_ERR_UNSUPPORTED, "B * H_kv must be at most 16384");
+    return SPD_OK;
+}
+
+SPD_API size_t spd_tree_verify_workspace_size(const spd_dims* dims, int32_t T) {
+    if (tree_attn_dims(dims, T) != SPD_OK) return 0;
+    spd_status st = SPD_OK;
+    DevInfo* d = dev_info(&st);
+    return d ? tree_attn_ws(dims->B, dims->H_kv, dims->H_q / dims->H_kv, T, dims->D, d->sms) : 0;
+}
+
+SPD_API spd_status tree_verify_attn(const spd_dims* dims, int32_t T, const spd_bf16* q, int64_t q_stride,
+                                    const spd_bf16* K, const spd_bf16* V, const int32_t* page_table,
+                                    const int32_t* seq_lens, const spd_bf16* k_tree, int64_t k_stride,
+                                    const spd_bf16* v_tree, int64_t v_stride, const int32_t* parents,
+                                    float softmax_scale, spd_bf16* o, float* lse, void* ws, size_t ws_bytes,
+                                    void* stream) {
+    spd_status st = tree_attn_dims(dims, T);
+    if (st == SPD_OK) st = tree_rows(dims, T, k_tree, k_stride, v_tree, v_stride);
+    if (st != SPD_OK) return st;
+    const double scale_log2 = (double)softmax_scale * 1.4426950408889634;
+    if (!(fabs(scale_log2) <= 3.4e38)) return fail(SPD_ERR_INVALID_ARG, "softmax_scale must be finite, times log2(e) too");
+    if (dims->B == 0) return SPD_OK;
+    if (!q || !K || !V || !page_table || !seq_lens || !parents || !o) return fail(SPD_ERR_INVALID_ARG, "NULL pointer argument");
+    if (!aligned16(q) || !aligned16(K) || !aligned16(V) || !aligned16(o))
+        return fail(SPD_ERR_INVALID_ARG, "q, K, V and o must be 16-byte aligned");
+    if (q_stride < (int64_t)dims->H_q * dims->D || q_stride % 8)
+        return fail(SPD_ERR_INVALID_ARG, "bad row stride (q_stride=%lld)", (long long)q_stride);
+    DevInfo* d = dev_info(&st);
+    if (!d) return st;
+    const size_t need = tree_attn_ws(dims->B, dims->H_kv, dims->H_q / dims->H_kv, T, dims->D, d->sms);
+    if (!ws || ws_bytes < need) return fail(SPD_ERR_WORKSPACE, "workspace %zu bytes < %zu", ws_bytes, need);
+    if (!aligned16(ws)) return fail(SPD_ERR_INVALID_ARG, "ws must be 16-byte aligned");
+    TreeAttnArgs a = {};
+    a.q = q;
+    a.K = K;
+    a.V = V;
+    a.page_table = page_table;
+    a.seq_lens = seq_lens;
+    a.k_tree = k_tree;
+    a.v_tree = v_tree;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.parents = parents;
+    a.B = dims->B;
+    a.H_q = dims->H_q;
+    a.H_kv = dims->H_kv;
+    a.D = dims->D;
+    a.ps = dims->page_size;
+    a.max_pages = dims->max_pages_per_seq;
+    a.T = T;
+    a.num_phys = dims->num_phys_pages;
+    a.scale_log2 = (float)scale_log2;
+    a.o = o;
+    a.lse = lse;
+    a.ws = ws;
+    a.num_sms = d->sms;
+    a.status = d->status;
+    a.wait_ns = wait_limit_ns();
+    cudaError_t e = launch_tree_attn(a, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SPD_OK : cuda_fail(e, "tree_verify_attn launch");
+}
+
+SPD_API spd_status spec_accept_tree(int32_t B, int32_t T, int32_t n_vocab, const float* q_target, const int32_t* draft,
+                                    const int32_t* parents, const float* u_acc, const float* u_res, int32_t* n_path,
+                                    int32_t* path, int32_t* tokens, void* stream) {
+    if (B < 0) return fail(SPD_ERR_INVALID_ARG, "B < 0");
+    if (T < 1 || T > kTreeMax) return fail(SPD_ERR_UNSUPPORTED, "T = %d outside [1, %d]", T, kTreeMax);
+    if (n_vocab < 1 || n_vocab > (1 << 21)) return fail(SPD_ERR_UNSUPPORTED, "n_vocab = %d outside [1, 2^21]", n_vocab);
+    if ((int64_t)B * 16 >= (1LL << 31)) return fail(SPD_ERR_UNSUPPORTED, "B = %d is too large", B);
+    if (B == 0) return SPD_OK;
+    if (!q_target || !draft || !parents || !u_acc || !u_res || !n_path || !path || !tokens)
+        return fail(SPD_ERR_INVALID_ARG, "NULL pointer argument");
+    if (!aligned16(q_target)) return fail(SPD_ERR_INVALID_ARG, "q_target must be 16-byte aligned");
+    spd_status st;
+    DevInfo* d = dev_info(&st);
+    if (!d) return st;
+    TreeAcceptArgs a = {};
+    a.q = q_target;
+    a.draft = draft;
+    a.parents = parents;
+    a.u_acc = u_acc;
+    a.u_res = u_res;
+    a.n_path = n_path;
+    a.path = path;
+    a.tokens = tokens;
+    a.B = B;
+    a.T = T;
+    a.n = n_vocab;
+    a.status = d->status;
+    cudaError_t e = launch_spec_accept_tree(a, d->sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SPD_OK : cuda_fail(e, "spec_accept_tree launch");
+}
+
+SPD_API spd_status kv_append_path(const spd_dims* dims, int32_t T, spd_bf16* K, spd_bf16* V, const int32_t* page_table,
+                                  const int32_t* seq_lens, const spd_bf16* k_tree, int64_t k_stride,
+                                  const spd_bf16* v_tree, int64_t v_stride, const int32_t* path, const int32_t* n_path,
+                                  spd_bf16* summ, int32_t* new_lens, void* stream) {
+    spd_status st = check_dims(dims);
+    if (st != SPD_OK) return st;
+    st = tree_rows(dims, T, k_tree, k_stride, v_tree, v_stride);
+    if (st != SPD_OK || dims->B == 0) return st;
+    if (!K || !V || !page_table || !seq_lens || !path || !n_path || !summ || !new_lens)
+        return fail(SPD_ERR_INVALID_ARG, "NULL pointer argument");
+    if (!aligned16(K) || !aligned16(V) || !aligned16(summ))
+        return fail(SPD_ERR_INVALID_ARG, "K, V and summ must be 16-byte aligned");
+    if (new_lens == seq_lens) return fail(SPD_ERR_INVALID_ARG, "new_lens must not be seq_lens");
+    DevInfo* d = dev_info(&st);
+    if (!d) return st;
+    AppendPathArgs p = {};
+    AppendArgs& a = p.append;
+    a.K = K;
+    a.V = V;
+    a.page_table = page_table;
+    a.seq_lens = seq_lens;
+    a.k_new = k_tree;
+    a.v_new = v_tree;
+    a.summ = summ;
+    a.B = dims->B;
+    a.T = T;
+    a.H_kv = dims->H_kv;
+    a.D = dims->D;
+    a.ps = dims->page_size;
+    a.max_pages = dims->max_pages_per_seq;
+    a.num_phys = dims->num_phys_pages;
+    a.status = d->status;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.path = path;
+    p.n_path = n_path;
+    p.new_lens = new_lens;
+    cudaError_t e = launch_append_path(p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SPD_OK : cuda_fail(e, "kv_append_path launch");
+}
+
+// ---------------------------------------------------------------- eviction by attention weight
+
+SPD_API spd_status kv_weights_update(const spd_dims* dims, int32_t T, const spd_bf16* q, const float* lse,
+                                     const spd_bf16* K, const int32_t* page_table, const int32_t* seq_lens,
+                                     const int32_t* path, const int32_t* n_path, const int32_t* sel,
+                                     const int32_t* nsel, int32_t k_max, float decay, float softmax_scale,
+                                     const float* w_in, float* w_out, void* stream) {
+    spd_status st = check_dims(dims);
+    if (st == SPD_OK) st = position_dims(dims);
+    if (st != SPD_OK) return st;
+    if (T < 1 || T > kTreeMax) return fail(SPD_ERR_UNSUPPORTED, "T = %d outside [1, %d]", T, kTreeMax);
+    const double scale_log2 = (double)softmax_scale * 1.4426950408889634;
+    if (!(fabs(scale_log2) <= 3.4e38) || !(fabsf(decay) <= 3.4e38f))
+        return fail(SPD_ERR_INVALID_ARG, "decay and softmax_scale must be finite");
+    if ((path != nullptr) != (n_path != nullptr)) return fail(SPD_ERR_INVALID_ARG, "path and n_path go together");
+    if ((sel != nullptr) != (nsel != nullptr)) return fail(SPD_ERR_INVALID_ARG, "sel and nsel go together");
+    if (sel && k_max < 1) return fail(SPD_ERR_INVALID_ARG, "k_max < 1");
+    if ((long long)dims->B * dims->H_kv * (((long long)dims->max_pages_per_seq * dims->page_size >> 9) + 1) >= (1LL << 31))
+        return fail(SPD_ERR_UNSUPPORTED, "B * H_kv * max_pages_per_seq is too large");
+    if (dims->B == 0) return SPD_OK;
+    if (!q || !lse || !K || !page_table || !seq_lens || !w_out) return fail(SPD_ERR_INVALID_ARG, "NULL pointer argument");
+    if (!aligned16(q) || !aligned16(K)) return fail(SPD_ERR_INVALID_ARG, "q and K must be 16-byte aligned");
+    DevInfo* d = dev_info(&st);
+    if (!d) return st;
+    WeightsArgs a = {};
+    a.q = q;
+    a.lse = lse;
+    a.K = K;
+    a.page_table = page_table;
+    a.seq_lens = seq_lens;
+    a.path = path;
+    a.n_path = n_path;
+    a.sel = sel;
+    a.nsel = nsel;
+    a.k_max = k_max;
+    a.B = dims->B;
+    a.H_q = dims->H_q;
+    a.H_kv = dims->H_kv;
+    a.D = dims->D;
+    a.ps = dims->page_size;
+    a.max_pages = dims->max_pages_per_seq;
+    a.T = T;
+    a.num_phys = dims->num_phys_pages;
+    a.decay = decay;
+    a.scale_log2 = (float)scale_log2;
+    a.w_in = w_in;
+    a.w_out = w_out;
+    a.status = d->status;
+    cudaError_t e = launch_weights_update(a, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SPD_OK : cuda_fail(e, "kv_weights_update launch");
+}
+
+SPD_API spd_status kv_evict(const spd_dims* dims, int32_t budget, int32_t n_sink, int32_t n_recent, spd_bf16* K,
+                            spd_bf16* V, const int32_t* page_table, const int32_t* seq_lens, const float* weights,
+                            const int32_t* dst_table, int32_t* kept, float* weights_out, spd_bf16* summ,
+                            int32_t* new_lens, void* stream) {
+    spd_status st = check_dims(dims);
+    if (st == SPD_OK) st = position_dims(dims);
+    if (st != SPD_OK) return st;
+    if (budget < 1 || n_sink < 0 || n_recent < 0 || (int64_t)n_sink + n_recent > budget)
+        return fail(SPD_ERR_INVALID_ARG, "budget %d must be >= 1 and hold n_sink (%d) and n_recent (%d) tokens", budget, n_sink, n_recent);
+    const long long rows = (long long)dims->B * dims->H_kv;
+    if (rows * 8 >= (1LL << 31) || rows * dims->max_pages_per_seq >= (1LL << 31))
+        return fail(SPD_ERR_UNSUPPORTED, "B * H_kv * max_pages_per_seq is too large");
+    if (dims->B == 0) return SPD_OK;
+    if (!K || !V || !page_table || !seq_lens || !weights || !dst_table || !kept || !weights_out || !summ || !new_lens)
+        return fail(SPD_ERR_INVALID_ARG, "NULL pointer argument");
+    if (!aligned16(K) || !aligned16(V) || !aligned16(summ))
+        return fail(SPD_ERR_INVALID_ARG, "K, V and summ must be 16-byte aligned");
+    if (new_lens == seq_lens || weights_out == weights || dst_table == page_table)
+        return fail(SPD_ERR_INVALID_ARG, "new_lens, weights_out and dst_table must not be seq_lens, weights and page_table");
+    DevInfo* d = dev_info(&st);
+    if (!d) return st;
+    EvictArgs a = {};
+    a.K = K;
+    a.V = V;
+    a.page_table = page_table;
+    a.seq_lens = seq_lens;
+    a.dst_table = dst_table;
+    a.w = weights;
+    a.w_out = weights_out;
+    a.kept = kept;
+    a.summ = summ;
+    a.new_lens = new_lens;
+    a.budget = budget;
+    a.n_sink = n_sink;
+    a.n_recent = n_recent;
+    a.B = dims->B;
+    a.H_kv = dims->H_kv;
+    a.D = dims->D;
+    a.ps = dims->page_size;
+    a.max_pages = dims->max_pages_per_seq;
+    a.num_phys = dims->num_phys_pages;
+    a.status = d->status;
+    cudaError_t e = launch_evict(a, d->sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SPD_OK : cuda_fail(e, "kv_evict launch");
+}
