@@ -103,24 +103,6 @@ __device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t x, uint32_t 
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
-// Two multiply-adds, and two sums, as one instruction.
-__device__ __forceinline__ unsigned long long pair_of(float2 x) {
-    return (unsigned long long)__float_as_uint(x.y) << 32 | __float_as_uint(x.x);
-}
-__device__ __forceinline__ float2 of_pair(unsigned long long x) {
-    return make_float2(__uint_as_float((uint32_t)x), __uint_as_float((uint32_t)(x >> 32)));
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    unsigned long long d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(pair_of(a)), "l"(pair_of(b)), "l"(pair_of(c)));
-    return of_pair(d);
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    unsigned long long d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(pair_of(a)), "l"(pair_of(b)));
-    return of_pair(d);
-}
-
 template <int N>
 __device__ __forceinline__ void load_columns(uint32_t taddr, uint32_t (&v)[N]) {
     __syncwarp();

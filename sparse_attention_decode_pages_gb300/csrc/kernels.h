@@ -231,8 +231,13 @@ struct TreeAttnArgs {
     unsigned* status;
     unsigned long long wait_ns;
 };
-cudaError_t launch_tree_attn(const TreeAttnArgs& a, cudaStream_t st);
-size_t tree_attn_ws(int B, int H_kv, int G, int T, int D, int num_sms);
+// 64 channels by: a page's slots (k, v); a group's heads and nodes (q); the nodes (kt, vt).
+struct TreeMaps {
+    CUtensorMap k, v, q, kt, vt;
+};
+cudaError_t launch_tree_attn(const TreeAttnArgs& a, const TreeMaps& m, cudaStream_t st);
+size_t tree_attn_ws(int D, int num_sms);  // of a.ws
+int tree_nodes_per_tile(int T, int G);    // nodes in q's box
 
 struct TreeAcceptArgs {
     const float* q;          // [B][T][n] target probabilities

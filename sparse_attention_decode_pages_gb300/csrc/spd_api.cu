@@ -1256,11 +1256,46 @@ static spd_status tree_attn_dims(const spd_dims* dims, int32_t T) {
     return SPD_OK;
 }
 
+static spd_status tree_map(CUtensorMap* m, const void* base, int rank, const cuuint64_t* size, const cuuint64_t* stride,
+                           const cuuint32_t* box) {
+    spd_status st = SPD_OK;
+    EncodeTiledFn fn = encode_fn(&st);
+    if (!fn) return st;
+    const cuuint32_t step[5] = {1, 1, 1, 1, 1};
+    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base), size, stride, box, step,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? SPD_OK : fail(SPD_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+}
+
+// The views that the tree's attention copies boxes of, 64 channels (128 bytes) wide: pages as [page and KV head][half][slot],
+// queries as [half][row][head], nodes as [half][head][sequence][node] (what lies behind the last node arrives as zeros).
+static spd_status tree_maps(const TreeAttnArgs& a, TreeMaps* m) {
+    const cuuint64_t row = (cuuint64_t)a.D * 2, halves = (cuuint64_t)a.D / 64;
+    const cuuint64_t pages = (cuuint64_t)a.num_phys * a.H_kv;
+    const cuuint64_t kv_size[4] = {64, (cuuint64_t)a.ps, halves, pages ? pages : 1}, kv_stride[3] = {row, 128, row * a.ps};
+    const cuuint32_t kv_box[4] = {64, (cuuint32_t)a.ps, 1, 1};
+    spd_status st = tree_map(&m->k, a.K, 4, kv_size, kv_stride, kv_box);
+    if (st == SPD_OK) st = tree_map(&m->v, a.V, 4, kv_size, kv_stride, kv_box);
+    const int G = a.H_q / a.H_kv;
+    const cuuint64_t q_size[4] = {64, (cuuint64_t)a.H_q, (cuuint64_t)a.B * a.T, halves}, q_stride[3] = {row, (cuuint64_t)a.q_stride * 2, 128};
+    const cuuint32_t q_box[4] = {64, (cuuint32_t)G, (cuuint32_t)tree_nodes_per_tile(a.T, G), 1};
+    if (st == SPD_OK) st = tree_map(&m->q, a.q, 4, q_size, q_stride, q_box);
+    const cuuint32_t t_box[5] = {64, kTreeMax, 1, 1, 1};
+    for (int i = 0; i < 2 && st == SPD_OK; ++i) {
+        const cuuint64_t stride = (cuuint64_t)(i ? a.v_stride : a.k_stride) * 2;
+        const cuuint64_t t_size[5] = {64, (cuuint64_t)a.T, (cuuint64_t)a.B, (cuuint64_t)a.H_kv, halves};
+        const cuuint64_t t_stride[4] = {stride, stride * a.T, row, 128};
+        st = tree_map(i ? &m->vt : &m->kt, i ? a.v_tree : a.k_tree, 5, t_size, t_stride, t_box);
+    }
+    return st;
+}
+
 SPD_API size_t spd_tree_verify_workspace_size(const spd_dims* dims, int32_t T) {
     if (tree_attn_dims(dims, T) != SPD_OK) return 0;
     spd_status st = SPD_OK;
     DevInfo* d = dev_info(&st);
-    return d ? tree_attn_ws(dims->B, dims->H_kv, dims->H_q / dims->H_kv, T, dims->D, d->sms) : 0;
+    return d ? kTicketBytes + tree_attn_ws(dims->D, d->sms) : 0;
 }
 
 SPD_API spd_status tree_verify_attn(const spd_dims* dims, int32_t T, const spd_bf16* q, int64_t q_stride,
@@ -1282,7 +1317,7 @@ SPD_API spd_status tree_verify_attn(const spd_dims* dims, int32_t T, const spd_b
         return fail(SPD_ERR_INVALID_ARG, "bad row stride (q_stride=%lld)", (long long)q_stride);
     DevInfo* d = dev_info(&st);
     if (!d) return st;
-    const size_t need = tree_attn_ws(dims->B, dims->H_kv, dims->H_q / dims->H_kv, T, dims->D, d->sms);
+    const size_t need = kTicketBytes + tree_attn_ws(dims->D, d->sms);
     if (!ws || ws_bytes < need) return fail(SPD_ERR_WORKSPACE, "workspace %zu bytes < %zu", ws_bytes, need);
     if (!aligned16(ws)) return fail(SPD_ERR_INVALID_ARG, "ws must be 16-byte aligned");
     TreeAttnArgs a = {};
@@ -1308,11 +1343,14 @@ SPD_API spd_status tree_verify_attn(const spd_dims* dims, int32_t T, const spd_b
     a.scale_log2 = (float)scale_log2;
     a.o = o;
     a.lse = lse;
-    a.ws = ws;
+    a.ws = static_cast<char*>(ws) + kTicketBytes;  // behind the place of every call's tickets
     a.num_sms = d->sms;
     a.status = d->status;
     a.wait_ns = wait_limit_ns();
-    cudaError_t e = launch_tree_attn(a, static_cast<cudaStream_t>(stream));
+    TreeMaps m;
+    st = tree_maps(a, &m);
+    if (st != SPD_OK) return st;
+    cudaError_t e = launch_tree_attn(a, m, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? SPD_OK : cuda_fail(e, "tree_verify_attn launch");
 }
 

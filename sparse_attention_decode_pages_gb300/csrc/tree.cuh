@@ -6,12 +6,11 @@
 
 namespace spd {
 
-// By one warp: mask[v] = bits of v and its ancestors, or 0 for what is no node, from parents [T], T <= 64.
-// Lane i holds nodes i and i + 32; the paths double six times.  False where a parent is out of
-// range.
-__device__ __forceinline__ bool tree_masks(const int32_t* parents, int T, unsigned long long* mask) {
+// By one warp: bits of node v and its ancestors, or 0 for what is no node, from parents [T], T <= 64, for nodes
+// v = lane (m[0]) and v = lane + 32 (m[1]); the paths double six times.  False where a parent is
+// out of range.
+__device__ __forceinline__ bool tree_masks(const int32_t* parents, int T, unsigned long long (&m)[2]) {
     const int lane = threadIdx.x & 31;
-    unsigned long long m[2];
     int up[2];
     bool gone[2], bad = false;
 #pragma unroll
@@ -46,7 +45,7 @@ __device__ __forceinline__ bool tree_masks(const int32_t* parents, int T, unsign
             }
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) mask[lane + 32 * i] = gone[i] ? 0ull : m[i];
+    for (int i = 0; i < 2; ++i) m[i] = gone[i] ? 0ull : m[i];
     return !__any_sync(0xffffffffu, bad);
 }
 

@@ -1,101 +1,879 @@
 // tree_attn.cu -- attention of the nodes of a tree of drafted tokens over the paged cache, their
-// ancestors and themselves: the plain form, a warp a query row, a token a lane, one pass with the running
-// maximum and sum of the softmax.
+// ancestors and themselves.
+//
+// The R = T * G query rows of a (sequence, KV head) see the same cached tokens, so they are the rows of two
+// products on the 5th-generation tensor cores (tcgen05, bf16 in, fp32 out in tensor memory)
+//
+//   S = Q K^T      M = 128 rows, N = 128 tokens, K = channels;  Q and K in shared memory
+//   O += P V       M = 128 rows, N = channels, K = 128 tokens;  P in tensor memory, in S's place
+//
+// over tiles of 128 tokens, the tree's own nodes as the last one.  A thread of a softmax
+// warp has one row (a lane of tensor memory): its maximum, its sum and its weights need no other
+// thread.  Two streams of 128 rows take turns, so that one's softmax runs under the other's
+// products: more than 128 rows of a KV head are two row tiles over the same tokens, fewer are one row
+// tile whose streams take the even and the odd tiles of tokens and are joined at the end, in tensor
+// memory.
+//
+// The softmax goes by a reference that follows the row's maximum only when that has grown by 2^8 beyond it, so O
+// is rarely rescaled; sums are fp32, the weights that multiply V are rounded to bf16 (V's type,
+// as the products want them), 2^-9 of a weight at most and of either sign.
+//
+// One CTA an SM: a warp for copies, a warp for products, two warpgroups for the softmax.  Each page's
+// keys and values come by TMA, a box of 64 channels at a time.  The cache's end inside a page is a box that starts
+// above the page: what lies before it arrives as zeros, so the page's valid tokens come to lie at the box's
+// end and nothing past the sequence is ever read.
+//
+// The tiles of all (sequence, KV head, pair of row tiles) units in a row are cut into equal shares, one a CTA (the GPU knows
+// the lengths, the host does not); a unit that a border cuts leaves unnormalised partials, at most two a CTA, for
+// a second kernel to join.
+#include <atomic>
+
 #include "common.cuh"
 #include "kernels.h"
+#include "tcgen05.cuh"
 #include "tree.cuh"
 
 namespace spd {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kRows = 128;          // of a row tile
+constexpr int kTokens = 128;        // of a tile of tokens
+constexpr int kThreads = 384;       // two softmax warpgroups; a warp for copies, one for products, one for the nodes' values
+// Registers: 168 a thread at launch (64,512 of the SM's 65,536); of these the softmax warpgroups take 208 a
+// thread, the third keeps 80: 2 * 128 * 208 + 128 * 80 = 63,488.
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 80;
+static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "what the block was launched with");
+constexpr int kInfos = 16;          // tiles whose visible tokens are written down
+constexpr int kOdd = 8;             // pieces whose nodes with odd values are
+constexpr float kLag = 8.f;         // powers of two that a maximum may lie above the reference
 
 template <int D>
-__global__ void __launch_bounds__(32 * kWarps) tree_attn_kernel(const TreeAttnArgs a) {
-    __shared__ unsigned long long s_mask[kTreeMax];
-    __shared__ float s_q[kWarps][D];
-    __shared__ float s_p[kWarps][32];
-    __shared__ const bf16* s_v[kWarps][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+struct Cfg {
+    static constexpr int HALVES = D / 64;
+    static constexpr int HALF = kTokens * 128;  // 64 channels of a tile
+    static constexpr int TILE = HALVES * HALF;
+    static constexpr int STAGES = D == 128 ? 5 : 10;
+    static constexpr int OFF_Q = 0;             // two row tiles
+    static constexpr int OFF_RING = 2 * TILE;
+    static constexpr int OFF_INFO = OFF_RING + STAGES * TILE;  // uint16 [kInfos][8]: visible tokens of a tile
+    static constexpr int OFF_ML = OFF_INFO + kInfos * 16;      // float2 [128]: a stream's references and sums
+    static constexpr int OFF_BAR = OFF_ML + kRows * 8;         // uint64: full, empty, v_tree [STAGES], and ten more
+    static constexpr int SMEM = 1024 + OFF_BAR + (3 * STAGES + 10) * 8;
+    static_assert(SMEM <= 227 * 1024 && SMEM > 114 * 1024, "one CTA an SM");
+    // tensor memory: S (and P) and O of each stream
+    static constexpr int COL_S = 0, COL_O = 256, COLUMNS = 512;
+};
+
+// What a CTA leaves for the joining kernel: a unit that begins in its share and ends in another's.
+struct Cut {
+    int b, sub, pieces, pad;
+};
+
+// Partials: [slot][D / 4][256 rows] float4, then [slot][256 rows] (reference, sum); two slots a CTA, one for the unit
+// that its share begins in and one for the unit that it ends in.
+constexpr int kSlotRows = 256;
+__host__ __device__ constexpr size_t slot_bytes(int D) { return (size_t)kSlotRows * (D * 4 + 8); }
+
+struct Shape {
+    int G, tpt, row_tiles, pairs;  // heads of a group, nodes of a row tile, row tiles, units of a (sequence, KV head)
+};
+__host__ __device__ inline Shape shape_of(int T, int G) {
+    Shape s;
+    s.G = G;
+    s.tpt = min(kRows / G, T);
+    s.row_tiles = (T + s.tpt - 1) / s.tpt;
+    s.pairs = (s.row_tiles + 1) / 2;
+    return s;
+}
+
+// The part of a unit that lies in a CTA's share: tiles t0 .. t1 - 1 of its nt.
+struct Piece {
+    int b, sub, len, nt, t0, t1;
+};
+
+// Goes through the pieces of a share, one sequence's units after the other's.
+struct Walk {
+    int b, sub, t0, len, nt;
+    long long left;  // tiles
+    __device__ __forceinline__ void look(const TreeAttnArgs& a) {
+        len = a.seq_lens[b];
+        if (seq_pages(len, a.ps, a.max_pages) < 0) len = 0;
+        nt = (len + kTokens - 1) / kTokens + 1;
+    }
+    __device__ __forceinline__ bool next(const TreeAttnArgs& a, int subs, Piece& p) {
+        if (left <= 0) return false;
+        p.b = b;
+        p.sub = sub;
+        p.len = len;
+        p.nt = nt;
+        p.t0 = t0;
+        p.t1 = (int)min((long long)nt, t0 + left);
+        left -= p.t1 - p.t0;
+        t0 = 0;
+        if (++sub == subs) {
+            sub = 0;
+            if (left > 0) {
+                ++b;
+                look(a);
+            }
+        }
+        return true;
+    }
+};
+
+__device__ __forceinline__ void other_regs() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs)); }
+
+template <int S>
+struct Ring {
+    int slot = 0;
+    uint32_t parity = 0;
+    __device__ __forceinline__ void advance() {
+        if (++slot == S) {
+            slot = 0;
+            parity ^= 1u;
+        }
+    }
+};
+
+__device__ __forceinline__ long long share_begin(long long total, int ctas, int i) { return total * i / ctas; }
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    tree_kernel(const TreeAttnArgs a, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_kt,
+                const __grid_constant__ CUtensorMap map_vt) {
+    using C = Cfg<D>;
+    constexpr int STAGES = C::STAGES;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ long long s_scan[kThreads / 32];
+    __shared__ int s_b, s_off;
+    __shared__ uint32_t s_tmem;
+    __shared__ unsigned long long s_odd[kOdd];  // nodes of a piece's tree whose values are not all finite
+    uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+    uint64_t* empty = full + STAGES;
+    uint64_t* v_tree = empty + STAGES;  // the nodes' values have come; then they are looked over
+    uint64_t* q_full = v_tree + STAGES;
+    uint64_t* q_empty = q_full + 1;
+    uint64_t* s_full = q_empty + 1;  // [2] S is there, and the tile's visible tokens are written down
+    uint64_t* p_full = s_full + 2;   // [2] P is there
+    uint64_t* o_done = p_full + 2;   // [2] a piece's last product is done
+    uint64_t* level = o_done + 2;    // the softmax warps are as far as the others, where streams are joined
+    uint64_t* drain = level + 1;
+    uint16_t* info = reinterpret_cast<uint16_t*>(smem + C::OFF_INFO);
+    float2* s_ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    const Shape sh = shape_of(a.T, a.H_q / a.H_kv);
+    const int subs = a.H_kv * sh.pairs;
     const float NEG_INF = __int_as_float(0xff800000);
-    const int b = blockIdx.x / a.T, t = blockIdx.x % a.T;
-    const int G = a.H_q / a.H_kv;
+    const unsigned long long drain_ns = a.wait_ns > kDefaultWaitNs ? a.wait_ns : kDefaultWaitNs;
+
+    if (tid == 0) {
+        for (int i = 0; i < STAGES; ++i) {
+            mbar_init(full + i, 1);
+            mbar_init(empty + i, 1);
+            mbar_init(v_tree + i, 1);
+        }
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(s_full + i, 2);  // the product's completion, and the issuing thread
+            mbar_init(p_full + i, 4);
+            mbar_init(o_done + i, 2);  // as s_full
+        }
+        mbar_init(level, 8);
+        mbar_init(drain, 1);
+        mbar_fence_init();
+    }
     pdl_wait();
     pdl_trigger();
-    if (warp == 0 && !tree_masks(a.parents + (long long)b * a.T, a.T, s_mask) && lane == 0) raise_status(a.status, SPD_DEV_BAD_TREE);
-    __syncthreads();
-    int len = a.seq_lens[b];
-    unsigned long long mask = s_mask[t];
-    if (seq_pages(len, a.ps, a.max_pages) < 0) {
-        if (threadIdx.x == 0) raise_status(a.status, SPD_DEV_BAD_LEN);
-        mask = 0;
-    }
-    if (mask == 0) len = 0;
-    const bf16* K = reinterpret_cast<const bf16*>(a.K);
-    const bf16* V = reinterpret_cast<const bf16*>(a.V);
-    for (int hq = warp; hq < a.H_q; hq += kWarps) {
-        const int h = hq / G;
-        const bf16* q = reinterpret_cast<const bf16*>(a.q) + ((long long)b * a.T + t) * a.q_stride + (long long)hq * D;
-        __syncwarp();
-        for (int d = lane; d < D; d += 32) s_q[warp][d] = __bfloat162float(q[d]);
-        __syncwarp();
-        float m = NEG_INF, l = 0.f, o[D / 32] = {};
-        for (int t0 = 0; t0 < len + a.T; t0 += 32) {
-            const int i = t0 + lane;
-            const bf16 *k = nullptr, *v = nullptr;
-            if (i < len) {
-                const int p = a.page_table[(long long)b * a.max_pages + i / a.ps];
-                if (p < 0 || p >= a.num_phys) {
-                    raise_status(a.status, SPD_DEV_BAD_PAGE);
-                } else {
-                    const long long row = ((long long)p * a.H_kv + h) * a.ps + i % a.ps;
-                    k = K + row * D;
-                    v = V + row * D;
-                }
-            } else if (i < len + a.T && (mask >> (i - len) & 1)) {
-                const long long row = (long long)b * a.T + (i - len);
-                k = reinterpret_cast<const bf16*>(a.k_tree) + row * a.k_stride + h * D;
-                v = reinterpret_cast<const bf16*>(a.v_tree) + row * a.v_stride + h * D;
-            }
-            float s = NEG_INF;
-            if (k) {
-                s = 0.f;
-                for (int d = 0; d < D; ++d) s = fmaf(s_q[warp][d], __bfloat162float(k[d]), s);
-                s *= a.scale_log2;
-            }
-            float top = s;
-            for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-            const float now = fmaxf(m, top);
-            if (now == NEG_INF) continue;
-            const float corr = fast_exp2(m - now);
-            const float p = k ? fast_exp2(s - now) : 0.f;
-            float sum = p;
-            for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-            l = l * corr + sum;
-            m = now;
-            s_p[warp][lane] = p;
-            s_v[warp][lane] = v;
-            __syncwarp();
-            for (int j = 0; j < D / 32; ++j) o[j] *= corr;
-            for (int i2 = 0; i2 < 32; ++i2) {
-                const bf16* vv = s_v[warp][i2];
-                if (!vv) continue;
-                for (int j = 0; j < D / 32; ++j) o[j] = fmaf(s_p[warp][i2], __bfloat162float(vv[lane + 32 * j]), o[j]);
-            }
-            __syncwarp();
+
+    // this CTA's share: where it begins (sequence, and tile among that sequence's units) and how many tiles
+    {
+        const int per = (a.B + kThreads - 1) / kThreads;
+        const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
+        long long mine = 0;
+        auto tiles_of = [&](int b) {
+            const int len = a.seq_lens[b];
+            return (long long)(seq_pages(len, a.ps, a.max_pages) < 0 ? 1 : (len + kTokens - 1) / kTokens + 1) * subs;
+        };
+        for (int b = b0; b < b1; ++b) mine += tiles_of(b);
+        long long incl = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += y;
         }
-        const long long at = ((long long)b * a.T + t) * a.H_q + hq;
-        for (int j = 0; j < D / 32; ++j) reinterpret_cast<bf16*>(a.o)[at * D + lane + 32 * j] = __float2bfloat16_rn(l != 0.f ? o[j] / l : 0.f);
-        if (lane == 0 && a.lse) a.lse[at] = l != 0.f ? (m + log2f(l)) * kLn2 : NEG_INF;
+        if (lane == 31) s_scan[warp] = incl;
+        if (warp == 9) tmem_alloc(&s_tmem, C::COLUMNS);
+        tmem_fence_before();
+        __syncthreads();
+        tmem_fence_after();
+        long long total = 0, before = 0;
+        for (int i = 0; i < kThreads / 32; ++i) {
+            if (i == warp) before = total;
+            total += s_scan[i];
+        }
+        before += incl - mine;
+        const int ctas = (int)min((long long)gridDim.x, total);
+        const long long g0 = (int)blockIdx.x < ctas ? share_begin(total, ctas, blockIdx.x) : total;
+        const long long g1 = (int)blockIdx.x < ctas ? share_begin(total, ctas, blockIdx.x + 1) : total;
+        if (before <= g0 && g0 < before + mine) {
+            int b = b0;
+            while (g0 - before >= tiles_of(b)) before += tiles_of(b++);
+            s_b = b;
+            s_off = (int)(g0 - before);
+        }
+        __syncthreads();
+        Walk w;
+        w.left = g1 - g0;
+        w.b = w.sub = w.t0 = w.len = w.nt = 0;
+        if (w.left > 0) {
+            w.b = s_b;
+            w.look(a);
+            w.sub = s_off / w.nt;
+            w.t0 = s_off - w.sub * w.nt;
+        }
+        // a unit that begins here and ends behind the share: the joining kernel's work
+        Cut* cuts = reinterpret_cast<Cut*>(a.ws);
+        if (tid == 0) {
+            Cut cut = {0, 0, 0, 0};
+            Walk x = w;
+            Piece p;
+            long long at = g0;
+            while (x.next(a, subs, p)) {
+                if (p.t0 == 0 && p.t1 < p.nt) {
+                    int c = blockIdx.x;
+                    while (share_begin(total, ctas, c + 1) < at + p.nt) ++c;
+                    cut.b = p.b;
+                    cut.sub = p.sub;
+                    cut.pieces = c - (int)blockIdx.x + 1;
+                }
+                at += p.t1 - p.t0;
+            }
+            cuts[blockIdx.x] = cut;
+        }
+        float* part_o = reinterpret_cast<float*>(static_cast<char*>(a.ws) + ((size_t)gridDim.x * sizeof(Cut) + 255) / 256 * 256);
+        float2* part_ml = reinterpret_cast<float2*>(part_o + (size_t)2 * gridDim.x * kSlotRows * D);
+        const uint32_t tmem = s_tmem;
+        const uint32_t q_smem = smem_u32(smem + C::OFF_Q), ring_smem = smem_u32(smem + C::OFF_RING);
+
+        if (warp < 8) {
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+            // ======================================================== softmax
+            const int s = warp >> 2;               // the stream
+            const int row = (warp & 3) * 32 + lane;  // of its row tile
+            const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+            const uint32_t tm_s = tmem + C::COL_S + s * 128 + lanes, tm_o = tmem + C::COL_O + lanes;
+            const float scale = fmaxf(fabsf(a.scale_log2), 1e-37f);  // (0 would make -inf, a hidden token, a NaN)
+            const bool flip = a.scale_log2 < 0.f;
+            uint32_t s_parity = 0, o_parity = 0, level_parity = 0;
+            int tiles_done = 0, piece = -1;  // of the pieces before: their visible tokens' places
+            bool ok = true;
+            auto wait = [&](uint64_t* bar, uint32_t parity) {
+                ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, a.status, a.wait_ns));
+                return ok;
+            };
+            // a barrier of the eight softmax warps that no warp can be held at
+            auto all_level = [&]() {
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(level);
+                wait(level, level_parity);
+                level_parity ^= 1u;
+                tmem_fence_after();
+            };
+            int tree_b = -1;
+            unsigned long long tree[2] = {0, 0};
+            Piece p;
+            while (ok && w.next(a, subs, p)) {
+                const int h = p.sub / sh.pairs, mt = 2 * (p.sub - h * sh.pairs);
+                const bool two = mt + 1 < sh.row_tiles;
+                const int n = p.t1 - p.t0, step = two ? 1 : 2;
+                ++piece;
+                if (p.b != tree_b) {
+                    tree_masks(a.parents + (long long)p.b * a.T, a.T, tree);
+                    if (seq_pages(a.seq_lens[p.b], a.ps, a.max_pages) < 0) tree[0] = tree[1] = 0;
+                    tree_b = p.b;
+                }
+                const int node = (mt + (two ? s : 0)) * sh.tpt + row / sh.G;
+                const bool there = row < sh.tpt * sh.G && node < a.T;
+                const unsigned long long m_lo = __shfl_sync(0xffffffffu, tree[0], node & 31), m_hi = __shfl_sync(0xffffffffu, tree[1], node & 31);
+                const unsigned long long mask = !there ? 0 : node < 32 ? m_lo : m_hi;
+                float ref = NEG_INF;
+                float2 l0 = make_float2(0.f, 0.f), l1 = l0;
+                for (int j = two ? 0 : s; j < n; j += step) {
+                    const int t = p.t0 + j;
+                    if (!wait(s_full + s, s_parity)) break;
+                    s_parity ^= 1u;
+                    tmem_fence_after();
+                    uint32_t x[4][32];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) tmem_ld(tm_s + 32 * i, x[i]);
+                    uint4 seen = *reinterpret_cast<const uint4*>(info + ((tiles_done + j) & (kInfos - 1)) * 8);
+                    if (t == p.nt - 1) seen = make_uint4((uint32_t)mask, (uint32_t)(mask >> 32), 0u, 0u);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) tmem_loaded(x[i]);
+                    if (flip) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) x[i][c] ^= 0x80000000u;
+                    }
+                    if (__any_sync(0xffffffffu, (seen.x & seen.y & seen.z & seen.w) != 0xffffffffu)) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t bits = i == 0 ? seen.x : i == 1 ? seen.y : i == 2 ? seen.z : seen.w;
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                if (!(bits >> c & 1u)) x[i][c] = 0xff800000u;
+                        }
+                    }
+                    float top[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        top[i] = __uint_as_float(x[i][0]);
+#pragma unroll
+                        for (int c = 1; c < 31; c += 2) top[i] = fmaxf(top[i], fmaxf(__uint_as_float(x[i][c]), __uint_as_float(x[i][c + 1])));
+                        top[i] = fmaxf(top[i], __uint_as_float(x[i][31]));
+                    }
+                    const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
+                    const bool moves = most > ref + kLag;
+                    if (__any_sync(0xffffffffu, moves)) {
+                        const float now = moves ? most : ref;
+                        const float corr = moves ? fast_exp2(ref - now) : 1.f;
+                        ref = now;
+                        l0.x *= corr;
+                        l0.y *= corr;
+                        l1.x *= corr;
+                        l1.y *= corr;
+                        if (j >= step) {  // O of the tiles before; their products are done, as S's is
+#pragma unroll 1
+                            for (int i = 0; i < D; i += 16) {
+                                uint32_t o[16];
+                                tmem_ld(tm_o + s * 128 + i, o);
+                                tmem_wait_ld();
+                                tmem_loaded(o);
+#pragma unroll
+                                for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * corr);
+                                tmem_st(tm_o + s * 128 + i, o);
+                            }
+                        }
+                    }
+                    const float neg = ref == NEG_INF ? 0.f : -ref;
+                    const float2 scale2 = make_float2(scale, scale), neg2 = make_float2(neg, neg);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t w16[16];
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) {
+                            const float2 y = fma2(make_float2(__uint_as_float(x[i][2 * c]), __uint_as_float(x[i][2 * c + 1])), scale2, neg2);
+                            const float2 e = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+                            if (c & 1) l1 = add2(l1, e);
+                            else l0 = add2(l0, e);
+                            w16[c] = pack_bf16(e.x, e.y);
+                        }
+                        tmem_st(tm_s + 16 * i, w16);
+                    }
+                    tmem_wait_st();
+                    tmem_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(p_full + s);
+                }
+                if (!ok) break;
+                tiles_done += n;
+                float sum = l0.x + l0.y + (l1.x + l1.y);
+                const bool whole = p.t0 == 0 && p.t1 == p.nt;
+                // outputs, or the partial of slot 2 i (a unit that began before this share) or 2 i + 1
+                const int slot = 2 * (int)blockIdx.x + (p.t0 == 0 ? 1 : 0);
+                const long long out = ((long long)p.b * a.T + node) * a.H_q + h * sh.G + row % sh.G;
+                bf16* o_row = reinterpret_cast<bf16*>(a.o) + out * D;
+                float4* part = reinterpret_cast<float4*>(part_o) + (size_t)slot * kSlotRows * (D / 4) + (two ? s * kRows : 0) + row;
+                // values that are not finite, of the nodes that this row sees: added to columns c0 ... c0 + 15
+                auto give_back = [&](float (&o)[16], int c0) {
+                    unsigned long long odd = p.t1 == p.nt ? *reinterpret_cast<volatile unsigned long long*>(s_odd + (piece & (kOdd - 1))) & mask : 0;
+                    while (odd) {
+                        const int u = __ffsll((long long)odd) - 1;
+                        odd &= odd - 1;
+                        const bf16* v = reinterpret_cast<const bf16*>(a.v_tree) + ((long long)p.b * a.T + u) * a.v_stride + h * D + c0;
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) {
+                            const float x = __bfloat162float(v[c]);
+                            if (!(fabsf(x) <= 3.4e38f)) o[c] += x;
+                        }
+                    }
+                };
+                // 16 columns of this row's result, from column c0
+                auto put = [&](const float (&o)[16], int c0, float inv) {
+                    if (whole) {
+                        if (there) {
+#pragma unroll
+                            for (int c = 0; c < 16; c += 8) {
+                                uint4 v;
+                                v.x = pack_bf16(o[c] * inv, o[c + 1] * inv);
+                                v.y = pack_bf16(o[c + 2] * inv, o[c + 3] * inv);
+                                v.z = pack_bf16(o[c + 4] * inv, o[c + 5] * inv);
+                                v.w = pack_bf16(o[c + 6] * inv, o[c + 7] * inv);
+                                if (mask == 0) v = make_uint4(0, 0, 0, 0);
+                                *reinterpret_cast<uint4*>(o_row + c0 + c) = v;
+                            }
+                        }
+                    } else if (there) {
+#pragma unroll
+                        for (int c = 0; c < 16; c += 4) part[(size_t)((c0 + c) / 4) * kSlotRows] = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+                    }
+                };
+                auto put_ml = [&](float r, float total) {
+                    if (!there) return;
+                    if (whole) {
+                        if (a.lse) a.lse[out] = mask == 0 || total == 0.f ? NEG_INF : (r + log2f(total)) * kLn2;
+                    } else {
+                        part_ml[(size_t)slot * kSlotRows + (two ? s * kRows : 0) + row] = make_float2(r, mask == 0 ? 0.f : total);
+                    }
+                };
+                if (two) {
+                    if (!wait(o_done + s, o_parity)) break;
+                    o_parity ^= 1u;
+                    tmem_fence_after();
+                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll 1
+                    for (int c0 = 0; c0 < D; c0 += 16) {
+                        uint32_t o[16];
+                        tmem_ld(tm_o + s * 128 + c0, o);
+                        tmem_wait_ld();
+                        tmem_loaded(o);
+                        float v[16];
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) v[c] = mask == 0 ? 0.f : __uint_as_float(o[c]);
+                        give_back(v, c0);
+                        put(v, c0, inv);
+                    }
+                    put_ml(ref, sum);
+                    tmem_fence_before();
+                } else {
+                    // both streams' parts of the row: this warpgroup joins half of the channels
+                    if (s == 1) s_ml[row] = make_float2(ref, sum);
+                    if (s < n) {  // (the other stream's end is known behind the barrier)
+                        if (!wait(o_done + s, o_parity)) break;
+                        o_parity ^= 1u;
+                    }
+                    all_level();
+                    float2 ml0 = make_float2(ref, sum), ml1 = ml0;
+                    if (s == 0) {  // the other's, and in its place this one's
+                        ml1 = s_ml[row];
+                        s_ml[row] = ml0;
+                    }
+                    all_level();
+                    if (!ok) break;
+                    if (s == 1) ml0 = s_ml[row];
+                    const float r = fmaxf(ml0.x, ml1.x);
+                    const float w0 = ml0.x == NEG_INF ? 0.f : fast_exp2(ml0.x - r), w1 = ml1.x == NEG_INF ? 0.f : fast_exp2(ml1.x - r);
+                    // (a row of NaN logits alone has a sum of NaN and no reference)
+                    const float total = (ml0.x == NEG_INF ? ml0.y : ml0.y * w0) + (ml1.x == NEG_INF ? ml1.y : ml1.y * w1);
+                    const float inv = total == 0.f ? 0.f : 1.f / total;
+#pragma unroll 1
+                    for (int c0 = s * (D / 2); c0 < (s + 1) * (D / 2); c0 += 16) {
+                        uint32_t o0[16], o1[16];
+                        tmem_ld(tm_o + c0, o0);
+                        if (n > 1) tmem_ld(tm_o + 128 + c0, o1);
+                        tmem_wait_ld();
+                        tmem_loaded(o0);
+                        float v[16];
+                        if (n > 1) {
+                            tmem_loaded(o1);
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) v[c] = __uint_as_float(o0[c]) * w0 + __uint_as_float(o1[c]) * w1;
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) v[c] = __uint_as_float(o0[c]) * w0;
+                        }
+                        if (mask == 0) {
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) v[c] = 0.f;
+                        }
+                        give_back(v, c0);
+                        put(v, c0, inv);
+                    }
+                    if (s == 0) put_ml(r, total);
+                    all_level();  // both have read O and the references
+                }
+            }
+        } else if (warp == 8) {
+            other_regs();
+            // ======================================================== copies
+            const int ppt = kTokens / a.ps, lg_ps = __ffs(a.ps) - 1;  // pages of a tile
+            const int per_batch = 32 / ppt;                          // tiles of 32 page-table entries
+            const int oob = (int)max(1LL, a.num_phys * a.H_kv);      // a row of pages that is not there
+            Ring<STAGES> ring;
+            uint32_t q_parity = 1, v_parity = 0, v_items = 0;  // v_parity: of each slot's next; v_items: the last issued, bits
+            int issued = 0, n_info = 0;
+            bool ok = true, q_asked = false;
+            uint32_t q_last = 0;
+            Piece p;
+            while (ok && w.next(a, subs, p)) {
+                const int h = p.sub / sh.pairs, mt = 2 * (p.sub - h * sh.pairs);
+                const bool two = mt + 1 < sh.row_tiles;
+                const int n = p.t1 - p.t0;
+                const int P = (p.len + a.ps - 1) >> lg_ps;
+                if (p.t0 == 0 && p.sub == 0 && lane == 0) {
+                    if (seq_pages(a.seq_lens[p.b], a.ps, a.max_pages) < 0) raise_status(a.status, SPD_DEV_BAD_LEN);
+                }
+                // queries
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(q_empty, q_parity, a.status, a.wait_ns));
+                if (!ok) break;
+                const int row_bytes = sh.tpt * sh.G * 128;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(q_full, (two ? 2 : 1) * C::HALVES * row_bytes);
+                    for (int s = 0; s < (two ? 2 : 1); ++s)
+                        for (int x = 0; x < C::HALVES; ++x)
+                            tma_load_4d(smem + C::OFF_Q + s * C::TILE + x * C::HALF, &map_q, 0, h * sh.G, p.b * a.T + (mt + s) * sh.tpt, x, q_full);
+                }
+                q_asked = true;
+                q_last = q_parity ^ 1u;
+                q_parity ^= 1u;
+                // page-table entries: 32 at a time, of the tiles at hand, those before and the next
+                const int32_t* table = a.page_table + (long long)p.b * a.max_pages;
+                auto entries = [&](int batch) {
+                    const int e = batch * 32 + lane;
+                    int phys = -1;
+                    if (e < P) {
+                        phys = table[e];
+                        if (phys < 0 || phys >= a.num_phys) {
+                            raise_status(a.status, SPD_DEV_BAD_PAGE);
+                            phys = -1;
+                        }
+                    }
+                    return phys;
+                };
+                int batch = p.t0 / per_batch;
+                int cur = entries(batch), old = -1, nxt = entries(batch + 1);
+                for (int x = 0; x < 2 * n; ++x) {
+                    // two row tiles: K0 V0 K1 V1 ...; one: K0 K1 V0 K2 V1 ... (as the products take them)
+                    bool value;
+                    int j;
+                    if (two) {
+                        value = x & 1;
+                        j = x >> 1;
+                    } else {
+                        value = x == 2 * n - 1 || (x > 0 && !(x & 1));
+                        j = x == 2 * n - 1 ? n - 1 : value ? (x - 2) >> 1 : (x + 1) >> 1;
+                    }
+                    const int t = p.t0 + j;
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(empty + ring.slot, ring.parity ^ 1u, a.status, a.wait_ns));
+                    if (!ok) break;
+                    uint8_t* dst = smem + C::OFF_RING + ring.slot * C::TILE;
+                    uint64_t* bar = full + ring.slot;
+                    const CUtensorMap* map = value ? &map_v : &map_k;
+                    if (t < p.nt - 1) {
+                        if (t / per_batch > batch) {
+                            ++batch;
+                            old = cur;
+                            cur = nxt;
+                            nxt = entries(batch + 1);
+                        }
+                        const int ids = t / per_batch == batch ? cur : old;
+                        // lane i copies half i / ppt of page i % ppt
+                        const int i = lane & (ppt - 1), half = lane / ppt;
+                        const int page = t * ppt + i;
+                        const int phys = __shfl_sync(0xffffffffu, ids, page & 31);
+                        const int valid = min(a.ps, p.len - (page << lg_ps));  // its tokens (below 1: none)
+                        if (!value) {
+                            // 16 tokens a lane: a page's valid tokens are the last of its place in the tile
+                            const int gi = lane & 7, own = gi * 16 >> lg_ps;
+                            const int op = __shfl_sync(0xffffffffu, phys, own), ov = __shfl_sync(0xffffffffu, valid, own);
+                            const int hidden = (op < 0 || ov < 1 ? a.ps : a.ps - ov) - (gi * 16 & (a.ps - 1));
+                            const uint16_t bits = (uint16_t)(hidden <= 0 ? 0xffffu : hidden >= 16 ? 0u : 0xffffu << hidden);
+                            if (lane < 8) info[(n_info & (kInfos - 1)) * 8 + gi] = bits;
+                            ++n_info;
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_expect_tx(bar, C::TILE);
+                        __syncwarp();
+                        if (half < C::HALVES) {
+                            const bool there = phys >= 0 && valid > 0;
+                            tma_load_4d(dst + half * C::HALF + (i << lg_ps) * 128, map, 0, there ? valid - a.ps : 0, half,
+                                        there ? phys * a.H_kv + h : oob, bar);
+                        }
+                    } else {
+                        // the nodes: 64 rows, zeros behind the last
+                        uint64_t* to = value ? v_tree + ring.slot : bar;
+                        if (!value) ++n_info;
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(to, C::HALVES * 64 * 128);
+                            for (int half = 0; half < C::HALVES; ++half)
+                                tma_load_5d(dst + half * C::HALF, value ? &map_vt : &map_kt, 0, 0, p.b, h, half, to);
+                        }
+                    }
+                    const bool nodes = value && t == p.nt - 1;
+                    v_items = v_items << 1 | (nodes ? 1u : 0u);
+                    if (nodes) v_parity ^= 1u << ring.slot;
+                    ++issued;
+                    ring.advance();
+                }
+            }
+            // copies in flight land before their memory is given back
+            if (!ok) {
+                for (int at = max(0, issued - STAGES); at < issued; ++at) {
+                    const int slot = at % STAGES;
+                    if (v_items >> (issued - 1 - at) & 1u) mbar_wait_bounded(v_tree + slot, ~v_parity >> slot & 1u, a.status, drain_ns);
+                    else mbar_wait_bounded(full + slot, (uint32_t)(at / STAGES) & 1u, a.status, drain_ns);
+                }
+                if (q_asked) mbar_wait_bounded(q_full, q_last, a.status, drain_ns);
+            }
+        } else if (warp == 9) {
+            other_regs();
+            // ======================================================== products
+            constexpr uint32_t kIdescS = umma_idesc_bf16(kRows, kTokens, false, false);
+            constexpr uint32_t kIdescO = umma_idesc_bf16(kRows, D, false, true);
+            uint32_t q_parity = 0, p_parity = 0;  // (of both streams: bits)
+            int base = 0;  // items of the ring before this piece
+            bool ok = true;
+            auto wait = [&](uint64_t* bar, uint32_t parity) {
+                ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, a.status, a.wait_ns));
+                return ok;
+            };
+            auto wait_item = [&](int item) { return wait(full + item % STAGES, (uint32_t)(item / STAGES) & 1u); };
+            // S of stream s with row tile q and the keys of an item
+            auto keys = [&](int s, int q, int item) {
+                tmem_fence_after();
+                if (elect_one()) {
+                    const uint32_t k = ring_smem + item % STAGES * C::TILE;
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i)
+                        umma_f16_ss(tmem + C::COL_S + s * 128, umma_desc(q_smem + q * C::TILE + (i >> 2) * C::HALF + (i & 3) * 32, 0, 1024, kSwizzle128),
+                                    umma_desc(k + (i >> 2) * C::HALF + (i & 3) * 32, 0, 1024, kSwizzle128), kIdescS, i > 0);
+                    umma_commit(s_full + s);
+                    mbar_arrive(s_full + s);
+                }
+                __syncwarp();
+            };
+            auto values = [&](int s, int item, bool first, bool tree) {
+                tmem_fence_after();
+                if (elect_one()) {
+                    const uint32_t v = ring_smem + item % STAGES * C::TILE;
+                    const int steps = tree ? 4 : 8;
+                    for (int i = 0; i < steps; ++i)
+                        umma_f16_ts(tmem + C::COL_O + s * 128, tmem + C::COL_S + s * 128 + 8 * i,
+                                    umma_desc(v + i * 2048, C::HALF, 1024, kSwizzle128), kIdescO, !first || i > 0);
+                }
+                __syncwarp();
+            };
+            auto commit = [&](uint64_t* bar) {
+                if (elect_one()) umma_commit(bar);
+                __syncwarp();
+            };
+            auto last_product = [&](int s) {
+                if (elect_one()) {
+                    umma_commit(o_done + s);
+                    mbar_arrive(o_done + s);
+                }
+                __syncwarp();
+            };
+            auto wait_p = [&](int s) {
+                wait(p_full + s, p_parity >> s & 1u);
+                p_parity ^= 1u << s;
+                return ok;
+            };
+            Piece p;
+            while (ok && w.next(a, subs, p)) {
+                const int h = p.sub / sh.pairs, mt = 2 * (p.sub - h * sh.pairs);
+                const bool two = mt + 1 < sh.row_tiles;
+                const int n = p.t1 - p.t0;
+                if (!wait(q_full, q_parity)) break;
+                q_parity ^= 1u;
+                if (two) {
+                    if (!wait_item(base)) break;
+                    keys(0, 0, base);
+                    keys(1, 1, base);
+                    commit(empty + base % STAGES);
+                    if (n == 1) commit(q_empty);
+                    for (int i = 0; i < n && ok; ++i) {
+                        const int kn = base + 2 * i + 2, vi = base + 2 * i + 1;
+                        const bool tree = p.t0 + i == p.nt - 1;
+#pragma unroll
+                        for (int s = 0; s < 2; ++s) {
+                            if (!wait_p(s)) break;
+                            if (s == 0 && !wait_item(vi)) break;
+                            values(s, vi, i == 0, tree);
+                            if (s == 1) commit(empty + vi % STAGES);
+                            if (i + 1 < n) {
+                                if (s == 0 && !wait_item(kn)) break;
+                                keys(s, s, kn);
+                                if (s == 1) {
+                                    commit(empty + kn % STAGES);
+                                    if (i + 2 == n) commit(q_empty);
+                                }
+                            } else {
+                                last_product(s);
+                            }
+                        }
+                    }
+                } else {
+                    for (int j = 0; j < min(n, 2) && ok; ++j) {
+                        if (!wait_item(base + j)) break;
+                        keys(j, 0, base + j);
+                        commit(empty + (base + j) % STAGES);
+                        if (j + 1 == n) commit(q_empty);
+                    }
+                    for (int i = 0; i < n && ok; ++i) {
+                        const int s = i & 1, vi = base + min(2 * i + 2, 2 * n - 1), kn = base + 2 * i + 3;  // keys of tile i + 2
+                        if (!wait_p(s) || !wait_item(vi)) break;
+                        values(s, vi, i < 2, p.t0 + i == p.nt - 1);
+                        commit(empty + vi % STAGES);
+                        if (i + 2 < n) {
+                            if (!wait_item(kn)) break;
+                            keys(s, 0, kn);
+                            commit(empty + kn % STAGES);
+                            if (i + 3 == n) commit(q_empty);
+                        } else {
+                            last_product(s);
+                        }
+                    }
+                }
+                base += 2 * n;
+            }
+            if (!ok) {  // products in flight end before their memory is given back
+                commit(drain);
+                mbar_wait_bounded(drain, 0, a.status, drain_ns);
+            }
+        } else if (warp == 10) {
+            other_regs();
+            // ======================================================== the nodes' values
+            // A weight of 0 times an infinity or a NaN would reach rows that do not see the node: rows of what is
+            // no node (which may hold anything) and values that are not finite become 0 here, and the rows that see
+            // the latter get them back at the end.
+            uint32_t v_parity = 0;  // of each slot: bits
+            int base = 0, piece = 0;
+            Piece p;
+            while (w.next(a, subs, p)) {
+                base += 2 * (p.t1 - p.t0);
+                if (p.t1 == p.nt) {
+                    const int slot = (base - 1) % STAGES;
+                    unsigned long long m[2];
+                    if (!tree_masks(a.parents + (long long)p.b * a.T, a.T, m) && lane == 0 && p.sub == 0) raise_status(a.status, SPD_DEV_BAD_TREE);
+                    const unsigned long long gone = (unsigned long long)__ballot_sync(0xffffffffu, m[1] == 0) << 32 | __ballot_sync(0xffffffffu, m[0] == 0);
+                    if (!__all_sync(0xffffffffu, mbar_wait_bounded(v_tree + slot, v_parity >> slot & 1u, a.status, a.wait_ns))) break;
+                    v_parity ^= 1u << slot;
+                    uint8_t* rows = smem + C::OFF_RING + slot * C::TILE;
+                    unsigned long long odd = 0;
+#pragma unroll 4
+                    for (int i = 0; i < 2 * C::HALVES * 8; ++i) {
+                        // 16 bytes a lane: four rows an access
+                        const int y = i * 32 + lane, row = y >> 3 & 63;
+                        uint32_t* at = reinterpret_cast<uint32_t*>(rows + (y >> 9) * C::HALF + row * 128 + (y & 7) * 16);
+                        uint4 v = *reinterpret_cast<uint4*>(at);
+                        // an exponent of ones carries into the sign's place
+                        auto bad = [](uint32_t x) { return ((x & 0x7f807f80u) + 0x00800080u) & 0x80008000u; };
+                        const bool none = gone >> row & 1;
+                        const uint32_t any = bad(v.x) | bad(v.y) | bad(v.z) | bad(v.w);
+                        if (none || any) {
+                            auto clear = [&](uint32_t x) {
+                                const uint32_t b = bad(x);
+                                return none ? 0u : x & ~((b >> 15) * 0xffffu);
+                            };
+                            *reinterpret_cast<uint4*>(at) = make_uint4(clear(v.x), clear(v.y), clear(v.z), clear(v.w));
+                            if (!none) odd |= 1ull << row;
+                        }
+                    }
+                    odd = (unsigned long long)__reduce_or_sync(0xffffffffu, (uint32_t)(odd >> 32)) << 32 | __reduce_or_sync(0xffffffffu, (uint32_t)odd);
+                    if (lane == 0) s_odd[piece & (kOdd - 1)] = odd;
+                    async_proxy_fence();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(full + slot);
+                }
+                ++piece;
+            }
+        } else {
+            other_regs();  // the whole warpgroup gives registers back
+        }
     }
+    __syncwarp();
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    if (warp == 9) tmem_free(s_tmem, C::COLUMNS);
+}
+
+// Joins the partials of a unit that shares' borders cut: a thread has a row, a CTA 32 channels.
+template <int D>
+__global__ void __launch_bounds__(kSlotRows) join_kernel(const TreeAttnArgs a, int ctas) {
+    const float NEG_INF = __int_as_float(0xff800000);
+    pdl_wait();
+    pdl_trigger();
+    const Cut cut = reinterpret_cast<const Cut*>(a.ws)[blockIdx.x];
+    if (cut.pieces == 0) return;
+    const Shape sh = shape_of(a.T, a.H_q / a.H_kv);
+    const int h = cut.sub / sh.pairs, mt = 2 * (cut.sub - h * sh.pairs);
+    const int row = threadIdx.x & (kRows - 1), node = (mt + threadIdx.x / kRows) * sh.tpt + row / sh.G;
+    if (mt + (int)threadIdx.x / kRows >= sh.row_tiles || row >= sh.tpt * sh.G || node >= a.T) return;
+    const float* part_o = reinterpret_cast<const float*>(static_cast<const char*>(a.ws) + ((size_t)ctas * sizeof(Cut) + 255) / 256 * 256);
+    const float2* part_ml = reinterpret_cast<const float2*>(part_o + (size_t)2 * ctas * kSlotRows * D) + threadIdx.x;
+    const float4* part = reinterpret_cast<const float4*>(part_o) + threadIdx.x;
+    auto slot = [&](int i) { return (size_t)(2 * ((int)blockIdx.x + i) + (i == 0 ? 1 : 0)); };
+    float r = NEG_INF;
+    for (int i = 0; i < cut.pieces; ++i) r = fmaxf(r, part_ml[slot(i) * kSlotRows].x);
+    float total = 0.f;
+    float4 o[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < cut.pieces; ++i) {
+        const float2 ml = part_ml[slot(i) * kSlotRows];
+        const float w = ml.x == NEG_INF ? 0.f : fast_exp2(ml.x - r);
+        total += ml.x == NEG_INF ? ml.y : ml.y * w;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            const float4 v = part[(slot(i) * (D / 4) + blockIdx.y * 8 + c) * kSlotRows];
+            o[c].x = fmaf(v.x, w, o[c].x);
+            o[c].y = fmaf(v.y, w, o[c].y);
+            o[c].z = fmaf(v.z, w, o[c].z);
+            o[c].w = fmaf(v.w, w, o[c].w);
+        }
+    }
+    const float inv = total == 0.f ? 0.f : 1.f / total;
+    const long long out = ((long long)cut.b * a.T + node) * a.H_q + h * sh.G + row % sh.G;
+    uint4* to = reinterpret_cast<uint4*>(reinterpret_cast<bf16*>(a.o) + out * D + blockIdx.y * 32);
+#pragma unroll
+    for (int c = 0; c < 8; c += 2)
+        to[c / 2] = make_uint4(pack_bf16(o[c].x * inv, o[c].y * inv), pack_bf16(o[c].z * inv, o[c].w * inv),
+                               pack_bf16(o[c + 1].x * inv, o[c + 1].y * inv), pack_bf16(o[c + 1].z * inv, o[c + 1].w * inv));
+    if (blockIdx.y == 0 && a.lse) a.lse[out] = total == 0.f ? NEG_INF : (r + log2f(total)) * kLn2;
+}
+
+template <int D>
+cudaError_t launch(const TreeAttnArgs& a, const TreeMaps& m, int ctas, cudaStream_t st) {
+    static std::atomic<bool> known[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !known[dev].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(tree_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) known[dev].store(true, std::memory_order_release);
+    }
+    e = launch_pdl(tree_kernel<D>, dim3((unsigned)ctas), dim3(kThreads), Cfg<D>::SMEM, st, a, m.k, m.v, m.q, m.kt, m.vt);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(join_kernel<D>, dim3((unsigned)ctas, D / 32), dim3(kSlotRows), 0, st, a, ctas);
+}
+
+// CTAs: one an SM, or as many as there can be tiles.
+int grid_of(int B, int H_kv, int G, int T, int max_pages, int ps, int num_sms) {
+    const long long most = ((long long)max_pages * ps + kTokens - 1) / kTokens + 1;
+    const long long tiles = most * B * H_kv * shape_of(T, G).pairs;
+    return (int)(tiles < num_sms ? tiles : num_sms);
 }
 
 }  // namespace
 
-size_t tree_attn_ws(int B, int H_kv, int G, int T, int D, int num_sms) { return 256; }
+int tree_nodes_per_tile(int T, int G) { return shape_of(T, G).tpt; }
 
-cudaError_t launch_tree_attn(const TreeAttnArgs& a, cudaStream_t st) {
-    return launch_pdl(a.D == 128 ? tree_attn_kernel<128> : tree_attn_kernel<64>, dim3((unsigned)a.B * a.T), dim3(32 * kWarps), 0, st, a);
+size_t tree_attn_ws(int D, int num_sms) {
+    return ((size_t)num_sms * sizeof(Cut) + 255) / 256 * 256 + 2 * num_sms * slot_bytes(D);
+}
+
+cudaError_t launch_tree_attn(const TreeAttnArgs& a, const TreeMaps& m, cudaStream_t st) {
+    const int ctas = grid_of(a.B, a.H_kv, a.H_q / a.H_kv, a.T, a.max_pages, a.ps, a.num_sms);
+    return a.D == 128 ? launch<128>(a, m, ctas, st) : launch<64>(a, m, ctas, st);
 }
 
 }  // namespace spd

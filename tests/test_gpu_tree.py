@@ -459,3 +459,51 @@ def test_kv_append_path_skips_what_it_cannot_place(spd):
         y[int(pt[5, 0]), :, 14:16] = rows[5, :2].transpose(0, 1)
         assert torch.equal(x, y)
     assert bool((summ[[0, 1, 2, 3, 4, 6]] == 7.0).all()) and bool((summ[5, :, 1:] == 7.0).all()) and not bool((summ[5, :, 0] == 7.0).any())
+
+
+def test_tree_verify_attn_values_that_are_not_finite(spd):
+    """An infinite or NaN value of a node reaches the rows that see it, and no others; no-node rows reach none."""
+    rng = np.random.default_rng(31)
+    T, D = 6, 64
+    parents = np.array([-1, 0, 0, 1, 2, -2])
+    dims, lens, pt, K, V, q, k, v, parents = case(spd, rng, [140], T, 8, 2, D, 16, [parents], True)
+    clean = v.clone()
+    v[0, 1, 0, 5], v[0, 2, 0, 5], v[0, 2, 1, 63], v[0, 4, 0, 7] = float("inf"), float("-inf"), float("nan"), float("nan")
+    clean[0, 1, 0, 5] = clean[0, 2, 0, 5] = clean[0, 2, 1, 63] = clean[0, 4, 0, 7] = 0.0
+    args = (dev(pt), dev(lens), k)
+    o, lse = (host(x) for x in attend(spd, dims, T, q, K, V, *args, v, dev(parents.astype(np.int32))))
+    o2, lse2 = (host(x) for x in attend(spd, dims, T, q, K, V, *args, clean, dev(parents.astype(np.int32))))
+    assert np.array_equal(lse, lse2)
+    for hq in range(4):                       # head 0
+        for t in (1, 3):
+            o2[0, t, hq, 5] = np.inf
+        for t in (2, 4):
+            o2[0, t, hq, 5] = -np.inf
+        o2[0, 4, hq, 7] = np.nan
+        o2[0, [2, 4], 4 + hq, 63] = np.nan    # head 1
+    assert np.array_equal(o, o2, equal_nan=True)
+    assert spd.spd_device_status(clear=True) == 0
+
+
+@pytest.mark.parametrize("lens,T,H_q,H_kv,D", [([700, 300], 9, 8, 2, 128), ([700, 300], 64, 4, 1, 128), ([2000, 0], 50, 8, 1, 64)])
+def test_tree_verify_attn_with_waits_that_run_out(spd, lens, T, H_q, H_kv, D):
+    """A limit that no copy meets: the calls return with the timeout bit (or, should every copy be early, clean), all
+    of their waits over, and later calls with the usual limit are those of before."""
+    import torch
+    rng = np.random.default_rng(T)
+    dims, lens, pt, K, V, q, k, v, parents = case(spd, rng, lens, T, H_q, H_kv, D, 16, [ref.random_tree(rng, T, nodes=T - b) for b in range(2)])
+    args = (dims, T, q, K, V, dev(pt), dev(lens), k, v, dev(parents.astype(np.int32)))
+    first = attend(spd, *args)
+    assert spd.spd_device_status(clear=True) == 0
+    usual = spd.spd_wait_limit_ns()
+    try:
+        spd.spd_set_wait_limit_ns(1)
+        for _ in range(2):
+            attend(spd, *args)
+            torch.cuda.synchronize()
+            assert spd.spd_device_status(clear=True) & ~spd.DEV_TIMEOUT == 0
+    finally:
+        spd.spd_set_wait_limit_ns(usual)
+    for got, want in zip(attend(spd, *args), first):
+        assert torch.equal(got, want)
+    assert spd.spd_device_status(clear=True) == 0
