@@ -231,9 +231,10 @@ struct TreeAttnArgs {
     unsigned* status;
     unsigned long long wait_ns;
 };
-// 64 channels by: a page's slots (k, v); a group's heads and nodes (q); the nodes (kt, vt).
+// A page's keys or values of a KV head (k, v); eight slots of it by 64 channels (edge); 64 channels of a group's heads and
+// nodes (q), of the nodes (kt, vt).
 struct TreeMaps {
-    CUtensorMap k, v, q, kt, vt;
+    CUtensorMap k, v, k_edge, v_edge, q, kt, vt;
 };
 cudaError_t launch_tree_attn(const TreeAttnArgs& a, const TreeMaps& m, cudaStream_t st);
 size_t tree_attn_ws(int D, int num_sms);  // of a.ws

@@ -1268,15 +1268,20 @@ static spd_status tree_map(CUtensorMap* m, const void* base, int rank, const cuu
     return r == CUDA_SUCCESS ? SPD_OK : fail(SPD_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
 }
 
-// The views that the tree's attention copies boxes of, 64 channels (128 bytes) wide: pages as [page and KV head][half][slot],
+// The views that the tree's attention copies boxes of, 64 channels (128 bytes) wide: pages as [page and KV head][slot / 8][half][slot % 8] and [page and KV head][half][slot],
 // queries as [half][row][head], nodes as [half][head][sequence][node] (what lies behind the last node arrives as zeros).
 static spd_status tree_maps(const TreeAttnArgs& a, TreeMaps* m) {
     const cuuint64_t row = (cuuint64_t)a.D * 2, halves = (cuuint64_t)a.D / 64;
     const cuuint64_t pages = (cuuint64_t)a.num_phys * a.H_kv;
-    const cuuint64_t kv_size[4] = {64, (cuuint64_t)a.ps, halves, pages ? pages : 1}, kv_stride[3] = {row, 128, row * a.ps};
-    const cuuint32_t kv_box[4] = {64, (cuuint32_t)a.ps, 1, 1};
-    spd_status st = tree_map(&m->k, a.K, 4, kv_size, kv_stride, kv_box);
-    if (st == SPD_OK) st = tree_map(&m->v, a.V, 4, kv_size, kv_stride, kv_box);
+    const cuuint64_t n = pages ? pages : 1;
+    const cuuint64_t kv_size[5] = {64, 8, halves, (cuuint64_t)a.ps / 8, n}, kv_stride[4] = {row, 128, row * 8, row * a.ps};
+    const cuuint32_t kv_box[5] = {64, 8, (cuuint32_t)halves, (cuuint32_t)a.ps / 8, 1};
+    const cuuint64_t e_size[4] = {64, (cuuint64_t)a.ps, halves, n}, e_stride[3] = {row, 128, row * a.ps};
+    const cuuint32_t e_box[4] = {64, 8, 1, 1};
+    spd_status st = tree_map(&m->k, a.K, 5, kv_size, kv_stride, kv_box);
+    if (st == SPD_OK) st = tree_map(&m->v, a.V, 5, kv_size, kv_stride, kv_box);
+    if (st == SPD_OK) st = tree_map(&m->k_edge, a.K, 4, e_size, e_stride, e_box);
+    if (st == SPD_OK) st = tree_map(&m->v_edge, a.V, 4, e_size, e_stride, e_box);
     const int G = a.H_q / a.H_kv;
     const cuuint64_t q_size[4] = {64, (cuuint64_t)a.H_q, (cuuint64_t)a.B * a.T, halves}, q_stride[3] = {row, (cuuint64_t)a.q_stride * 2, 128};
     const cuuint32_t q_box[4] = {64, (cuuint32_t)G, (cuuint32_t)tree_nodes_per_tile(a.T, G), 1};

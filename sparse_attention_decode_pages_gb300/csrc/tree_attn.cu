@@ -18,10 +18,10 @@
 // is rarely rescaled; sums are fp32, the weights that multiply V are rounded to bf16 (V's type,
 // as the products want them), 2^-9 of a weight at most and of either sign.
 //
-// One CTA an SM: a warp for copies, a warp for products, two warpgroups for the softmax.  Each page's
-// keys and values come by TMA, a box of 64 channels at a time.  The cache's end inside a page is a box that starts
-// above the page: what lies before it arrives as zeros, so the page's valid tokens come to lie at the box's
-// end and nothing past the sequence is ever read.
+// One CTA an SM: two warpgroups for the softmax, and a warp each for the keys' copies, the values' copies, the products
+// and the nodes' values.  A page's keys or values of a KV head are one TMA box.  A sequence that ends inside a page has that page
+// copied eight slots at a time, by boxes that start above it: what lies before the page arrives as zeros, so its valid
+// tokens come to lie at the end of its place in the tile and nothing past the sequence is ever read.
 //
 // The tiles of all (sequence, KV head, pair of row tiles) units in a row are cut into equal shares, one a CTA (the GPU knows
 // the lengths, the host does not); a unit that a border cuts leaves unnormalised partials, at most two a CTA, for
@@ -38,7 +38,7 @@ namespace {
 
 constexpr int kRows = 128;          // of a row tile
 constexpr int kTokens = 128;        // of a tile of tokens
-constexpr int kThreads = 384;       // two softmax warpgroups; a warp for copies, one for products, one for the nodes' values
+constexpr int kThreads = 384;       // two softmax warpgroups and four warps
 // Registers: 168 a thread at launch (64,512 of the SM's 65,536); of these the softmax warpgroups take 208 a
 // thread, the third keeps 80: 2 * 128 * 208 + 128 * 80 = 63,488.
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 80;
@@ -52,6 +52,10 @@ struct Cfg {
     static constexpr int HALVES = D / 64;
     static constexpr int HALF = kTokens * 128;  // 64 channels of a tile
     static constexpr int TILE = HALVES * HALF;
+    // A tile of tokens: atoms of 8 tokens by 64 channels (1,024 bytes, 128-byte swizzle), a page's of all channels together, so
+    // that a page is one box: 8 tokens on and 64 channels on are these many bytes on.  Queries and the tree's nodes lie
+    // by 64 channels: [half][row].
+    static constexpr int GROUP = HALVES * 1024;
     static constexpr int STAGES = D == 128 ? 5 : 10;
     static constexpr int OFF_Q = 0;             // two row tiles
     static constexpr int OFF_RING = 2 * TILE;
@@ -123,25 +127,11 @@ struct Walk {
 
 __device__ __forceinline__ void other_regs() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs)); }
 
-template <int S>
-struct Ring {
-    int slot = 0;
-    uint32_t parity = 0;
-    __device__ __forceinline__ void advance() {
-        if (++slot == S) {
-            slot = 0;
-            parity ^= 1u;
-        }
-    }
-};
-
 __device__ __forceinline__ long long share_begin(long long total, int ctas, int i) { return total * i / ctas; }
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    tree_kernel(const TreeAttnArgs a, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
-                const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_kt,
-                const __grid_constant__ CUtensorMap map_vt) {
+    tree_kernel(const TreeAttnArgs a, const __grid_constant__ TreeMaps maps) {
     using C = Cfg<D>;
     constexpr int STAGES = C::STAGES;
     extern __shared__ uint8_t smem_raw[];
@@ -499,40 +489,41 @@ __global__ void __launch_bounds__(kThreads, 1)
                     all_level();  // both have read O and the references
                 }
             }
-        } else if (warp == 8) {
+        } else if (warp == 8 || warp == 11) {
             other_regs();
-            // ======================================================== copies
+            // ======================================================== copies: keys and queries, or values
+            const bool value = warp == 11;
             const int ppt = kTokens / a.ps, lg_ps = __ffs(a.ps) - 1;  // pages of a tile
             const int per_batch = 32 / ppt;                          // tiles of 32 page-table entries
             const int oob = (int)max(1LL, a.num_phys * a.H_kv);      // a row of pages that is not there
-            Ring<STAGES> ring;
-            uint32_t q_parity = 1, v_parity = 0, v_items = 0;  // v_parity: of each slot's next; v_items: the last issued, bits
-            int issued = 0, n_info = 0;
+            const CUtensorMap* map = value ? &maps.v : &maps.k;
+            const CUtensorMap* map_edge = value ? &maps.v_edge : &maps.k_edge;
+            uint32_t q_parity = 1, v_parity = 0;                // v_parity: of each slot's next nodes, bits
+            uint32_t asked = 0, asked_nodes = 0, asked_parity = 0;  // this warp's last copy to each slot, bits
+            int base = 0, n_info = 0;                            // items, and tiles, of the pieces before
             bool ok = true, q_asked = false;
-            uint32_t q_last = 0;
             Piece p;
             while (ok && w.next(a, subs, p)) {
                 const int h = p.sub / sh.pairs, mt = 2 * (p.sub - h * sh.pairs);
                 const bool two = mt + 1 < sh.row_tiles;
                 const int n = p.t1 - p.t0;
                 const int P = (p.len + a.ps - 1) >> lg_ps;
-                if (p.t0 == 0 && p.sub == 0 && lane == 0) {
-                    if (seq_pages(a.seq_lens[p.b], a.ps, a.max_pages) < 0) raise_status(a.status, SPD_DEV_BAD_LEN);
+                if (!value) {
+                    if (p.t0 == 0 && p.sub == 0 && lane == 0 && seq_pages(a.seq_lens[p.b], a.ps, a.max_pages) < 0)
+                        raise_status(a.status, SPD_DEV_BAD_LEN);
+                    // queries
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(q_empty, q_parity, a.status, a.wait_ns));
+                    if (!ok) break;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(q_full, (two ? 2 : 1) * C::HALVES * sh.tpt * sh.G * 128);
+                        for (int s = 0; s < (two ? 2 : 1); ++s)
+                            for (int x = 0; x < C::HALVES; ++x)
+                                tma_load_4d(smem + C::OFF_Q + s * C::TILE + x * C::HALF, &maps.q, 0, h * sh.G, p.b * a.T + (mt + s) * sh.tpt, x, q_full);
+                    }
+                    q_asked = true;
+                    q_parity ^= 1u;
                 }
-                // queries
-                ok = __all_sync(0xffffffffu, mbar_wait_bounded(q_empty, q_parity, a.status, a.wait_ns));
-                if (!ok) break;
-                const int row_bytes = sh.tpt * sh.G * 128;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(q_full, (two ? 2 : 1) * C::HALVES * row_bytes);
-                    for (int s = 0; s < (two ? 2 : 1); ++s)
-                        for (int x = 0; x < C::HALVES; ++x)
-                            tma_load_4d(smem + C::OFF_Q + s * C::TILE + x * C::HALF, &map_q, 0, h * sh.G, p.b * a.T + (mt + s) * sh.tpt, x, q_full);
-                }
-                q_asked = true;
-                q_last = q_parity ^ 1u;
-                q_parity ^= 1u;
-                // page-table entries: 32 at a time, of the tiles at hand, those before and the next
+                // page-table entries, 32 at a time
                 const int32_t* table = a.page_table + (long long)p.b * a.max_pages;
                 auto entries = [&](int batch) {
                     const int e = batch * 32 + lane;
@@ -547,34 +538,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                     return phys;
                 };
                 int batch = p.t0 / per_batch;
-                int cur = entries(batch), old = -1, nxt = entries(batch + 1);
-                for (int x = 0; x < 2 * n; ++x) {
-                    // two row tiles: K0 V0 K1 V1 ...; one: K0 K1 V0 K2 V1 ... (as the products take them)
-                    bool value;
-                    int j;
-                    if (two) {
-                        value = x & 1;
-                        j = x >> 1;
-                    } else {
-                        value = x == 2 * n - 1 || (x > 0 && !(x & 1));
-                        j = x == 2 * n - 1 ? n - 1 : value ? (x - 2) >> 1 : (x + 1) >> 1;
-                    }
-                    const int t = p.t0 + j;
-                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(empty + ring.slot, ring.parity ^ 1u, a.status, a.wait_ns));
+                int ids = entries(batch), nxt = entries(batch + 1);
+                for (int j = 0; j < n; ++j) {
+                    // the items' order, as the products take them: two row tiles K0 V0 K1 V1 ...; one K0 K1 V0 K2 V1 ...
+                    const int item = base + (two ? 2 * j + (value ? 1 : 0) : value ? min(2 * j + 2, 2 * n - 1) : max(0, 2 * j - 1));
+                    const int t = p.t0 + j, slot = item % STAGES;
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(empty + slot, ((uint32_t)(item / STAGES) & 1u) ^ 1u, a.status, a.wait_ns));
                     if (!ok) break;
-                    uint8_t* dst = smem + C::OFF_RING + ring.slot * C::TILE;
-                    uint64_t* bar = full + ring.slot;
-                    const CUtensorMap* map = value ? &map_v : &map_k;
+                    uint8_t* dst = smem + C::OFF_RING + slot * C::TILE;
+                    uint64_t* bar = full + slot;
                     if (t < p.nt - 1) {
                         if (t / per_batch > batch) {
                             ++batch;
-                            old = cur;
-                            cur = nxt;
+                            ids = nxt;
                             nxt = entries(batch + 1);
                         }
-                        const int ids = t / per_batch == batch ? cur : old;
-                        // lane i copies half i / ppt of page i % ppt
-                        const int i = lane & (ppt - 1), half = lane / ppt;
+                        // lane i copies page i
+                        const int i = lane & (ppt - 1);
                         const int page = t * ppt + i;
                         const int phys = __shfl_sync(0xffffffffu, ids, page & 31);
                         const int valid = min(a.ps, p.len - (page << lg_ps));  // its tokens (below 1: none)
@@ -590,36 +570,45 @@ __global__ void __launch_bounds__(kThreads, 1)
                         __syncwarp();
                         if (lane == 0) mbar_arrive_expect_tx(bar, C::TILE);
                         __syncwarp();
-                        if (half < C::HALVES) {
-                            const bool there = phys >= 0 && valid > 0;
-                            tma_load_4d(dst + half * C::HALF + (i << lg_ps) * 128, map, 0, there ? valid - a.ps : 0, half,
-                                        there ? phys * a.H_kv + h : oob, bar);
+                        const bool there = phys >= 0 && valid > 0;
+                        const unsigned cut = __ballot_sync(0xffffffffu, lane < ppt && there && valid < a.ps);
+                        if (lane < ppt && !(there && valid < a.ps))
+                            tma_load_5d(dst + (i << lg_ps) * (D * 2), map, 0, 0, 0, 0, there ? phys * a.H_kv + h : oob, bar);
+                        if (cut) {  // the sequence's last page, eight slots and 64 channels at a time
+                            const int e = __ffs((int)cut) - 1;
+                            const int ep = __shfl_sync(0xffffffffu, phys, e), ev = __shfl_sync(0xffffffffu, valid, e);
+                            const int grp = lane / C::HALVES, half = lane % C::HALVES;
+                            if (grp < a.ps >> 3)
+                                tma_load_4d(dst + (e << lg_ps) * (D * 2) + lane * 1024, map_edge, 0, grp * 8 + ev - a.ps, half, ep * a.H_kv + h, bar);
                         }
+                        asked_nodes &= ~(1u << slot);
                     } else {
                         // the nodes: 64 rows, zeros behind the last
-                        uint64_t* to = value ? v_tree + ring.slot : bar;
-                        if (!value) ++n_info;
+                        uint64_t* to = value ? v_tree + slot : bar;
+                        ++n_info;
                         if (lane == 0) {
                             mbar_arrive_expect_tx(to, C::HALVES * 64 * 128);
                             for (int half = 0; half < C::HALVES; ++half)
-                                tma_load_5d(dst + half * C::HALF, value ? &map_vt : &map_kt, 0, 0, p.b, h, half, to);
+                                tma_load_5d(dst + half * C::HALF, value ? &maps.vt : &maps.kt, 0, 0, p.b, h, half, to);
+                        }
+                        if (value) {
+                            asked_nodes |= 1u << slot;
+                            v_parity ^= 1u << slot;
                         }
                     }
-                    const bool nodes = value && t == p.nt - 1;
-                    v_items = v_items << 1 | (nodes ? 1u : 0u);
-                    if (nodes) v_parity ^= 1u << ring.slot;
-                    ++issued;
-                    ring.advance();
+                    asked |= 1u << slot;
+                    asked_parity = (asked_parity & ~(1u << slot)) | ((uint32_t)(item / STAGES) & 1u) << slot;
                 }
+                base += 2 * n;
             }
             // copies in flight land before their memory is given back
             if (!ok) {
-                for (int at = max(0, issued - STAGES); at < issued; ++at) {
-                    const int slot = at % STAGES;
-                    if (v_items >> (issued - 1 - at) & 1u) mbar_wait_bounded(v_tree + slot, ~v_parity >> slot & 1u, a.status, drain_ns);
-                    else mbar_wait_bounded(full + slot, (uint32_t)(at / STAGES) & 1u, a.status, drain_ns);
+                for (int i = 0; i < STAGES; ++i) {
+                    if (!(asked >> i & 1u)) continue;
+                    if (asked_nodes >> i & 1u) mbar_wait_bounded(v_tree + i, ~v_parity >> i & 1u, a.status, drain_ns);
+                    else mbar_wait_bounded(full + i, asked_parity >> i & 1u, a.status, drain_ns);
                 }
-                if (q_asked) mbar_wait_bounded(q_full, q_last, a.status, drain_ns);
+                if (q_asked) mbar_wait_bounded(q_full, q_parity, a.status, drain_ns);
             }
         } else if (warp == 9) {
             other_regs();
@@ -635,14 +624,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             auto wait_item = [&](int item) { return wait(full + item % STAGES, (uint32_t)(item / STAGES) & 1u); };
             // S of stream s with row tile q and the keys of an item
-            auto keys = [&](int s, int q, int item) {
+            auto keys = [&](int s, int q, int item, bool tree) {
                 tmem_fence_after();
                 if (elect_one()) {
                     const uint32_t k = ring_smem + item % STAGES * C::TILE;
+                    const uint32_t half = tree ? C::HALF : 1024, group = tree ? 1024 : C::GROUP;
 #pragma unroll
                     for (int i = 0; i < D / 16; ++i)
                         umma_f16_ss(tmem + C::COL_S + s * 128, umma_desc(q_smem + q * C::TILE + (i >> 2) * C::HALF + (i & 3) * 32, 0, 1024, kSwizzle128),
-                                    umma_desc(k + (i >> 2) * C::HALF + (i & 3) * 32, 0, 1024, kSwizzle128), kIdescS, i > 0);
+                                    umma_desc(k + (i >> 2) * half + (i & 3) * 32, 0, group, kSwizzle128), kIdescS, i > 0);
                     umma_commit(s_full + s);
                     mbar_arrive(s_full + s);
                 }
@@ -653,9 +643,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (elect_one()) {
                     const uint32_t v = ring_smem + item % STAGES * C::TILE;
                     const int steps = tree ? 4 : 8;
+                    const uint32_t half = tree ? C::HALF : 1024, group = tree ? 1024 : C::GROUP;
                     for (int i = 0; i < steps; ++i)
                         umma_f16_ts(tmem + C::COL_O + s * 128, tmem + C::COL_S + s * 128 + 8 * i,
-                                    umma_desc(v + i * 2048, C::HALF, 1024, kSwizzle128), kIdescO, !first || i > 0);
+                                    umma_desc(v + i * 2 * group, half, group, kSwizzle128), kIdescO, !first || i > 0);
                 }
                 __syncwarp();
             };
@@ -684,8 +675,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 q_parity ^= 1u;
                 if (two) {
                     if (!wait_item(base)) break;
-                    keys(0, 0, base);
-                    keys(1, 1, base);
+                    keys(0, 0, base, p.t0 == p.nt - 1);
+                    keys(1, 1, base, p.t0 == p.nt - 1);
                     commit(empty + base % STAGES);
                     if (n == 1) commit(q_empty);
                     for (int i = 0; i < n && ok; ++i) {
@@ -699,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (s == 1) commit(empty + vi % STAGES);
                             if (i + 1 < n) {
                                 if (s == 0 && !wait_item(kn)) break;
-                                keys(s, s, kn);
+                                keys(s, s, kn, p.t0 + i + 1 == p.nt - 1);
                                 if (s == 1) {
                                     commit(empty + kn % STAGES);
                                     if (i + 2 == n) commit(q_empty);
@@ -712,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else {
                     for (int j = 0; j < min(n, 2) && ok; ++j) {
                         if (!wait_item(base + j)) break;
-                        keys(j, 0, base + j);
+                        keys(j, 0, base + j, p.t0 + j == p.nt - 1);
                         commit(empty + (base + j) % STAGES);
                         if (j + 1 == n) commit(q_empty);
                     }
@@ -723,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         commit(empty + vi % STAGES);
                         if (i + 2 < n) {
                             if (!wait_item(kn)) break;
-                            keys(s, 0, kn);
+                            keys(s, 0, kn, p.t0 + i + 2 == p.nt - 1);
                             commit(empty + kn % STAGES);
                             if (i + 3 == n) commit(q_empty);
                         } else {
@@ -784,8 +775,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 ++piece;
             }
-        } else {
-            other_regs();  // the whole warpgroup gives registers back
         }
     }
     __syncwarp();
@@ -851,7 +840,7 @@ cudaError_t launch(const TreeAttnArgs& a, const TreeMaps& m, int ctas, cudaStrea
         if (e != cudaSuccess) return e;
         if (dev < 64) known[dev].store(true, std::memory_order_release);
     }
-    e = launch_pdl(tree_kernel<D>, dim3((unsigned)ctas), dim3(kThreads), Cfg<D>::SMEM, st, a, m.k, m.v, m.q, m.kt, m.vt);
+    e = launch_pdl(tree_kernel<D>, dim3((unsigned)ctas), dim3(kThreads), Cfg<D>::SMEM, st, a, m);
     if (e != cudaSuccess) return e;
     return launch_pdl(join_kernel<D>, dim3((unsigned)ctas, D / 32), dim3(kSlotRows), 0, st, a, ctas);
 }
