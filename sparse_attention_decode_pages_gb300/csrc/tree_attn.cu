@@ -93,15 +93,17 @@ __host__ __device__ inline Shape shape_of(int T, int G) {
 // The part of a unit that lies in a CTA's share: tiles t0 .. t1 - 1 of its nt.
 struct Piece {
     int b, sub, len, nt, t0, t1;
+    bool bad;  // a length that the page table has no room for: no tokens, no nodes
 };
 
 // Goes through the pieces of a share, one sequence's units after the other's.
 struct Walk {
     int b, sub, t0, len, nt;
+    bool bad;
     long long left;  // tiles
-    __device__ __forceinline__ void look(const TreeAttnArgs& a) {
-        len = a.seq_lens[b];
-        if (seq_pages(len, a.ps, a.max_pages) < 0) len = 0;
+    __device__ __forceinline__ void look(const TreeAttnArgs& a, int raw) {
+        bad = seq_pages(raw, a.ps, a.max_pages) < 0;
+        len = bad ? 0 : raw;
         nt = (len + kTokens - 1) / kTokens + 1;
     }
     __device__ __forceinline__ bool next(const TreeAttnArgs& a, int subs, Piece& p) {
@@ -110,16 +112,14 @@ struct Walk {
         p.sub = sub;
         p.len = len;
         p.nt = nt;
+        p.bad = bad;
         p.t0 = t0;
         p.t1 = (int)min((long long)nt, t0 + left);
         left -= p.t1 - p.t0;
         t0 = 0;
         if (++sub == subs) {
             sub = 0;
-            if (left > 0) {
-                ++b;
-                look(a);
-            }
+            if (left > 0) look(a, a.seq_lens[++b]);
         }
         return true;
     }
@@ -127,7 +127,21 @@ struct Walk {
 
 __device__ __forceinline__ void other_regs() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs)); }
 
-__device__ __forceinline__ long long share_begin(long long total, int ctas, int i) { return total * i / ctas; }
+// Where share i of `total` tiles begins: the first total % ctas shares have a tile more.
+struct Shares {
+    long long each;
+    int more;
+    __device__ __forceinline__ Shares(long long total, int ctas) {
+        if (total < 0x7fffffff) {
+            each = (int)total / ctas;
+            more = (int)total - (int)each * ctas;
+        } else {
+            each = total / ctas;
+            more = (int)(total - each * ctas);
+        }
+    }
+    __device__ __forceinline__ long long begin(int i) const { return each * i + min(i, more); }
+};
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -136,7 +150,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int STAGES = C::STAGES;
     extern __shared__ uint8_t smem_raw[];
     __shared__ long long s_scan[kThreads / 32];
-    __shared__ int s_b, s_off;
+    __shared__ int s_b, s_len;
+    __shared__ long long s_off;
     __shared__ uint32_t s_tmem;
     __shared__ unsigned long long s_odd[kOdd];  // nodes of a piece's tree whose values are not all finite
     uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
@@ -175,6 +190,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(drain, 1);
         mbar_fence_init();
     }
+    if (warp == 8 && elect_one()) {
+        tma_prefetch_desc(&maps.q);
+        tma_prefetch_desc(&maps.k);
+        tma_prefetch_desc(&maps.k_edge);
+        tma_prefetch_desc(&maps.kt);
+    }
+    if (warp == 11 && elect_one()) {
+        tma_prefetch_desc(&maps.v);
+        tma_prefetch_desc(&maps.v_edge);
+        tma_prefetch_desc(&maps.vt);
+    }
     pdl_wait();
     pdl_trigger();
 
@@ -182,12 +208,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     {
         const int per = (a.B + kThreads - 1) / kThreads;
         const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
-        long long mine = 0;
-        auto tiles_of = [&](int b) {
-            const int len = a.seq_lens[b];
+        auto tiles_of = [&](int len) {
             return (long long)(seq_pages(len, a.ps, a.max_pages) < 0 ? 1 : (len + kTokens - 1) / kTokens + 1) * subs;
         };
-        for (int b = b0; b < b1; ++b) mine += tiles_of(b);
+        int len = 0;  // of this thread's last sequence
+        long long mine = 0;
+        for (int b = b0; b < b1; ++b) {
+            len = a.seq_lens[b];
+            mine += tiles_of(len);
+        }
         long long incl = mine;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -199,49 +228,41 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_fence_before();
         __syncthreads();
         tmem_fence_after();
-        long long total = 0, before = 0;
-        for (int i = 0; i < kThreads / 32; ++i) {
-            if (i == warp) before = total;
-            total += s_scan[i];
+        long long sums = lane < kThreads / 32 ? s_scan[lane] : 0;
+#pragma unroll
+        for (int off = 1; off < 16; off <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, sums, off);
+            if (lane >= off) sums += y;
         }
-        before += incl - mine;
+        const long long total = __shfl_sync(0xffffffffu, sums, kThreads / 32 - 1);
+        long long before = __shfl_sync(0xffffffffu, sums, warp > 0 ? warp - 1 : 0);
+        before = (warp > 0 ? before : 0) + incl - mine;
         const int ctas = (int)min((long long)gridDim.x, total);
-        const long long g0 = (int)blockIdx.x < ctas ? share_begin(total, ctas, blockIdx.x) : total;
-        const long long g1 = (int)blockIdx.x < ctas ? share_begin(total, ctas, blockIdx.x + 1) : total;
+        const Shares shares(total, ctas);
+        const long long g0 = (int)blockIdx.x < ctas ? shares.begin(blockIdx.x) : total;
+        const long long g1 = (int)blockIdx.x < ctas ? shares.begin(blockIdx.x + 1) : total;
         if (before <= g0 && g0 < before + mine) {
             int b = b0;
-            while (g0 - before >= tiles_of(b)) before += tiles_of(b++);
+            if (per > 1) len = a.seq_lens[b];
+            while (g0 - before >= tiles_of(len)) {
+                before += tiles_of(len);
+                len = a.seq_lens[++b];
+            }
             s_b = b;
-            s_off = (int)(g0 - before);
+            s_off = g0 - before;
+            s_len = len;
         }
         __syncthreads();
         Walk w;
         w.left = g1 - g0;
         w.b = w.sub = w.t0 = w.len = w.nt = 0;
+        w.bad = false;
         if (w.left > 0) {
             w.b = s_b;
-            w.look(a);
-            w.sub = s_off / w.nt;
-            w.t0 = s_off - w.sub * w.nt;
-        }
-        // a unit that begins here and ends behind the share: the joining kernel's work
-        Cut* cuts = reinterpret_cast<Cut*>(a.ws);
-        if (tid == 0) {
-            Cut cut = {0, 0, 0, 0};
-            Walk x = w;
-            Piece p;
-            long long at = g0;
-            while (x.next(a, subs, p)) {
-                if (p.t0 == 0 && p.t1 < p.nt) {
-                    int c = blockIdx.x;
-                    while (share_begin(total, ctas, c + 1) < at + p.nt) ++c;
-                    cut.b = p.b;
-                    cut.sub = p.sub;
-                    cut.pieces = c - (int)blockIdx.x + 1;
-                }
-                at += p.t1 - p.t0;
-            }
-            cuts[blockIdx.x] = cut;
+            w.look(a, s_len);
+            const long long off = s_off;
+            w.sub = off < 0x7fffffff ? (int)off / w.nt : (int)(off / w.nt);
+            w.t0 = (int)(off - (long long)w.sub * w.nt);
         }
         float* part_o = reinterpret_cast<float*>(static_cast<char*>(a.ws) + ((size_t)gridDim.x * sizeof(Cut) + 255) / 256 * 256);
         float2* part_ml = reinterpret_cast<float2*>(part_o + (size_t)2 * gridDim.x * kSlotRows * D);
@@ -283,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++piece;
                 if (p.b != tree_b) {
                     tree_masks(a.parents + (long long)p.b * a.T, a.T, tree);
-                    if (seq_pages(a.seq_lens[p.b], a.ps, a.max_pages) < 0) tree[0] = tree[1] = 0;
+                    if (p.bad) tree[0] = tree[1] = 0;
                     tree_b = p.b;
                 }
                 const int node = (mt + (two ? s : 0)) * sh.tpt + row / sh.G;
@@ -405,7 +426,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 v.y = pack_bf16(o[c + 2] * inv, o[c + 3] * inv);
                                 v.z = pack_bf16(o[c + 4] * inv, o[c + 5] * inv);
                                 v.w = pack_bf16(o[c + 6] * inv, o[c + 7] * inv);
-                                if (mask == 0) v = make_uint4(0, 0, 0, 0);
                                 *reinterpret_cast<uint4*>(o_row + c0 + c) = v;
                             }
                         }
@@ -414,40 +434,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int c = 0; c < 16; c += 4) part[(size_t)((c0 + c) / 4) * kSlotRows] = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
                     }
                 };
-                auto put_ml = [&](float r, float total) {
-                    if (!there) return;
-                    if (whole) {
-                        if (a.lse) a.lse[out] = mask == 0 || total == 0.f ? NEG_INF : (r + log2f(total)) * kLn2;
-                    } else {
-                        part_ml[(size_t)slot * kSlotRows + (two ? s * kRows : 0) + row] = make_float2(r, mask == 0 ? 0.f : total);
-                    }
-                };
-                if (two) {
+                if (s < n || two) {  // (the other stream's end is known behind the barrier below)
                     if (!wait(o_done + s, o_parity)) break;
                     o_parity ^= 1u;
-                    tmem_fence_after();
-                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll 1
-                    for (int c0 = 0; c0 < D; c0 += 16) {
-                        uint32_t o[16];
-                        tmem_ld(tm_o + s * 128 + c0, o);
-                        tmem_wait_ld();
-                        tmem_loaded(o);
-                        float v[16];
-#pragma unroll
-                        for (int c = 0; c < 16; ++c) v[c] = mask == 0 ? 0.f : __uint_as_float(o[c]);
-                        give_back(v, c0);
-                        put(v, c0, inv);
-                    }
-                    put_ml(ref, sum);
-                    tmem_fence_before();
-                } else {
-                    // both streams' parts of the row: this warpgroup joins half of the channels
+                }
+                tmem_fence_after();
+                // the row's parts: this stream's, or both streams', of which this warpgroup joins half of the channels
+                float w0 = 1.f, w1 = 0.f;
+                if (!two) {
                     if (s == 1) s_ml[row] = make_float2(ref, sum);
-                    if (s < n) {  // (the other stream's end is known behind the barrier)
-                        if (!wait(o_done + s, o_parity)) break;
-                        o_parity ^= 1u;
-                    }
                     all_level();
                     float2 ml0 = make_float2(ref, sum), ml1 = ml0;
                     if (s == 0) {  // the other's, and in its place this one's
@@ -457,37 +452,50 @@ __global__ void __launch_bounds__(kThreads, 1)
                     all_level();
                     if (!ok) break;
                     if (s == 1) ml0 = s_ml[row];
-                    const float r = fmaxf(ml0.x, ml1.x);
-                    const float w0 = ml0.x == NEG_INF ? 0.f : fast_exp2(ml0.x - r), w1 = ml1.x == NEG_INF ? 0.f : fast_exp2(ml1.x - r);
+                    ref = fmaxf(ml0.x, ml1.x);
+                    w0 = ml0.x == NEG_INF ? 0.f : fast_exp2(ml0.x - ref);
+                    w1 = ml1.x == NEG_INF ? 0.f : fast_exp2(ml1.x - ref);
                     // (a row of NaN logits alone has a sum of NaN and no reference)
-                    const float total = (ml0.x == NEG_INF ? ml0.y : ml0.y * w0) + (ml1.x == NEG_INF ? ml1.y : ml1.y * w1);
-                    const float inv = total == 0.f ? 0.f : 1.f / total;
-#pragma unroll 1
-                    for (int c0 = s * (D / 2); c0 < (s + 1) * (D / 2); c0 += 16) {
-                        uint32_t o0[16], o1[16];
-                        tmem_ld(tm_o + c0, o0);
-                        if (n > 1) tmem_ld(tm_o + 128 + c0, o1);
-                        tmem_wait_ld();
-                        tmem_loaded(o0);
-                        float v[16];
-                        if (n > 1) {
-                            tmem_loaded(o1);
-#pragma unroll
-                            for (int c = 0; c < 16; ++c) v[c] = __uint_as_float(o0[c]) * w0 + __uint_as_float(o1[c]) * w1;
-                        } else {
-#pragma unroll
-                            for (int c = 0; c < 16; ++c) v[c] = __uint_as_float(o0[c]) * w0;
-                        }
-                        if (mask == 0) {
-#pragma unroll
-                            for (int c = 0; c < 16; ++c) v[c] = 0.f;
-                        }
-                        give_back(v, c0);
-                        put(v, c0, inv);
-                    }
-                    if (s == 0) put_ml(r, total);
-                    all_level();  // both have read O and the references
+                    sum = (ml0.x == NEG_INF ? ml0.y : ml0.y * w0) + (ml1.x == NEG_INF ? ml1.y : ml1.y * w1);
                 }
+                if (mask == 0) {
+                    sum = 0.f;
+                    ref = NEG_INF;
+                }
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                const uint32_t tm_a = tm_o + (two ? s * 128 : 0);
+                const int c_end = two ? D : (s + 1) * (D / 2);
+#pragma unroll 1
+                for (int c0 = two ? 0 : s * (D / 2); c0 < c_end; c0 += 16) {
+                    uint32_t oa[16], ob[16];
+                    tmem_ld(tm_a + c0, oa);
+                    if (!two && n > 1) tmem_ld(tm_o + 128 + c0, ob);
+                    tmem_wait_ld();
+                    tmem_loaded(oa);
+                    float v[16];
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) v[c] = __uint_as_float(oa[c]) * w0;
+                    if (!two && n > 1) {
+                        tmem_loaded(ob);
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) v[c] = fmaf(__uint_as_float(ob[c]), w1, v[c]);
+                    }
+                    if (mask == 0) {
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) v[c] = 0.f;
+                    }
+                    give_back(v, c0);
+                    put(v, c0, inv);
+                }
+                if ((two || s == 0) && there) {
+                    if (whole) {
+                        if (a.lse) a.lse[out] = sum == 0.f ? NEG_INF : (ref + log2f(sum)) * kLn2;
+                    } else {
+                        part_ml[(size_t)slot * kSlotRows + (two ? s * kRows : 0) + row] = make_float2(ref, sum);
+                    }
+                }
+                if (two) tmem_fence_before();
+                else all_level();  // both have read O and the references
             }
         } else if (warp == 8 || warp == 11) {
             other_regs();
@@ -508,9 +516,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool two = mt + 1 < sh.row_tiles;
                 const int n = p.t1 - p.t0;
                 const int P = (p.len + a.ps - 1) >> lg_ps;
+                // page-table entries, 32 at a time, asked for before the queries
+                const int32_t* table = a.page_table + (long long)p.b * a.max_pages;
+                auto ask = [&](int batch) {
+                    const int e = batch * 32 + lane;
+                    return e < P ? table[e] : -1;
+                };
+                auto checked = [&](int batch, int phys) {
+                    if (batch * 32 + lane < P && (phys < 0 || phys >= a.num_phys)) {
+                        raise_status(a.status, SPD_DEV_BAD_PAGE);
+                        phys = -1;
+                    }
+                    return phys;
+                };
+                int batch = p.t0 / per_batch;
+                int ids = ask(batch), nxt = ask(batch + 1);
                 if (!value) {
-                    if (p.t0 == 0 && p.sub == 0 && lane == 0 && seq_pages(a.seq_lens[p.b], a.ps, a.max_pages) < 0)
-                        raise_status(a.status, SPD_DEV_BAD_LEN);
+                    if (p.bad && p.sub == 0 && lane == 0) raise_status(a.status, SPD_DEV_BAD_LEN);
                     // queries
                     ok = __all_sync(0xffffffffu, mbar_wait_bounded(q_empty, q_parity, a.status, a.wait_ns));
                     if (!ok) break;
@@ -523,22 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     q_asked = true;
                     q_parity ^= 1u;
                 }
-                // page-table entries, 32 at a time
-                const int32_t* table = a.page_table + (long long)p.b * a.max_pages;
-                auto entries = [&](int batch) {
-                    const int e = batch * 32 + lane;
-                    int phys = -1;
-                    if (e < P) {
-                        phys = table[e];
-                        if (phys < 0 || phys >= a.num_phys) {
-                            raise_status(a.status, SPD_DEV_BAD_PAGE);
-                            phys = -1;
-                        }
-                    }
-                    return phys;
-                };
-                int batch = p.t0 / per_batch;
-                int ids = entries(batch), nxt = entries(batch + 1);
+                ids = checked(batch, ids);
                 for (int j = 0; j < n; ++j) {
                     // the items' order, as the products take them: two row tiles K0 V0 K1 V1 ...; one K0 K1 V0 K2 V1 ...
                     const int item = base + (two ? 2 * j + (value ? 1 : 0) : value ? min(2 * j + 2, 2 * n - 1) : max(0, 2 * j - 1));
@@ -550,8 +557,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (t < p.nt - 1) {
                         if (t / per_batch > batch) {
                             ++batch;
-                            ids = nxt;
-                            nxt = entries(batch + 1);
+                            ids = checked(batch, nxt);
+                            nxt = ask(batch + 1);
                         }
                         // lane i copies page i
                         const int i = lane & (ppt - 1);
@@ -731,6 +738,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (warp == 10) {
             other_regs();
             // ======================================================== the nodes' values
+            // first, a unit that begins here and ends behind the share is the joining kernel's work
+            if (lane == 0) {
+                Cut cut = {0, 0, 0, 0};
+                Walk x = w;
+                Piece p;
+                long long at = g0;
+                while (x.next(a, subs, p)) {
+                    if (p.t0 == 0 && p.t1 < p.nt) {
+                        int c = blockIdx.x;
+                        while (shares.begin(c + 1) < at + p.nt) ++c;
+                        cut.b = p.b;
+                        cut.sub = p.sub;
+                        cut.pieces = c - (int)blockIdx.x + 1;
+                    }
+                    at += p.t1 - p.t0;
+                }
+                reinterpret_cast<Cut*>(a.ws)[blockIdx.x] = cut;
+            }
+            __syncwarp();
             // A weight of 0 times an infinity or a NaN would reach rows that do not see the node: rows of what is
             // no node (which may hold anything) and values that are not finite become 0 here, and the rows that see
             // the latter get them back at the end.
@@ -784,48 +810,62 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 9) tmem_free(s_tmem, C::COLUMNS);
 }
 
-// Joins the partials of a unit that shares' borders cut: a thread has a row, a CTA 32 channels.
+// Joins the partials of a unit that shares' borders cut: a thread has eight channels of a row; eight partials are asked
+// for at once.
+constexpr int kJoinChannels = 8, kJoinAhead = 8;
 template <int D>
 __global__ void __launch_bounds__(kSlotRows) join_kernel(const TreeAttnArgs a, int ctas) {
     const float NEG_INF = __int_as_float(0xff800000);
+    const Shape sh = shape_of(a.T, a.H_q / a.H_kv);
+    const float* part_o = reinterpret_cast<const float*>(static_cast<const char*>(a.ws) + ((size_t)ctas * sizeof(Cut) + 255) / 256 * 256);
+    const float2* part_ml = reinterpret_cast<const float2*>(part_o + (size_t)2 * ctas * kSlotRows * D) + threadIdx.x;
+    const float4* part = reinterpret_cast<const float4*>(part_o) + blockIdx.y * 2 * kSlotRows + threadIdx.x;
     pdl_wait();
     pdl_trigger();
     const Cut cut = reinterpret_cast<const Cut*>(a.ws)[blockIdx.x];
     if (cut.pieces == 0) return;
-    const Shape sh = shape_of(a.T, a.H_q / a.H_kv);
     const int h = cut.sub / sh.pairs, mt = 2 * (cut.sub - h * sh.pairs);
     const int row = threadIdx.x & (kRows - 1), node = (mt + threadIdx.x / kRows) * sh.tpt + row / sh.G;
     if (mt + (int)threadIdx.x / kRows >= sh.row_tiles || row >= sh.tpt * sh.G || node >= a.T) return;
-    const float* part_o = reinterpret_cast<const float*>(static_cast<const char*>(a.ws) + ((size_t)ctas * sizeof(Cut) + 255) / 256 * 256);
-    const float2* part_ml = reinterpret_cast<const float2*>(part_o + (size_t)2 * ctas * kSlotRows * D) + threadIdx.x;
-    const float4* part = reinterpret_cast<const float4*>(part_o) + threadIdx.x;
-    auto slot = [&](int i) { return (size_t)(2 * ((int)blockIdx.x + i) + (i == 0 ? 1 : 0)); };
-    float r = NEG_INF;
-    for (int i = 0; i < cut.pieces; ++i) r = fmaxf(r, part_ml[slot(i) * kSlotRows].x);
-    float total = 0.f;
-    float4 o[8];
+    float r = NEG_INF, total = 0.f;
+    float4 o0 = make_float4(0.f, 0.f, 0.f, 0.f), o1 = o0;
+    for (int i0 = 0; i0 < cut.pieces; i0 += kJoinAhead) {
+        float2 ml[kJoinAhead];
+        float4 x[kJoinAhead], y[kJoinAhead];
 #pragma unroll
-    for (int c = 0; c < 8; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = 0; i < cut.pieces; ++i) {
-        const float2 ml = part_ml[slot(i) * kSlotRows];
-        const float w = ml.x == NEG_INF ? 0.f : fast_exp2(ml.x - r);
-        total += ml.x == NEG_INF ? ml.y : ml.y * w;
+        for (int k = 0; k < kJoinAhead; ++k) {
+            const int i = i0 + k;
+            // a unit's first partial is its CTA's second slot, the others are their CTAs' first
+            const size_t slot = (size_t)(2 * ((int)blockIdx.x + i) + (i == 0 ? 1 : 0));
+            ml[k] = make_float2(NEG_INF, 0.f);
+            x[k] = y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i < cut.pieces) {
+                ml[k] = part_ml[slot * kSlotRows];
+                x[k] = part[slot * (D / 4) * kSlotRows];
+                y[k] = part[(slot * (D / 4) + 1) * kSlotRows];
+            }
+        }
+        float now = r;
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-            const float4 v = part[(slot(i) * (D / 4) + blockIdx.y * 8 + c) * kSlotRows];
-            o[c].x = fmaf(v.x, w, o[c].x);
-            o[c].y = fmaf(v.y, w, o[c].y);
-            o[c].z = fmaf(v.z, w, o[c].z);
-            o[c].w = fmaf(v.w, w, o[c].w);
+        for (int k = 0; k < kJoinAhead; ++k) now = fmaxf(now, ml[k].x);
+        const float corr = r == NEG_INF ? 0.f : fast_exp2(r - now);
+        r = now;
+        total *= corr;
+        o0 = make_float4(o0.x * corr, o0.y * corr, o0.z * corr, o0.w * corr);
+        o1 = make_float4(o1.x * corr, o1.y * corr, o1.z * corr, o1.w * corr);
+#pragma unroll
+        for (int k = 0; k < kJoinAhead; ++k) {
+            const float w = ml[k].x == NEG_INF ? 0.f : fast_exp2(ml[k].x - r);
+            total += ml[k].x == NEG_INF ? ml[k].y : ml[k].y * w;  // (a row of NaN logits alone has no reference)
+            o0 = make_float4(fmaf(x[k].x, w, o0.x), fmaf(x[k].y, w, o0.y), fmaf(x[k].z, w, o0.z), fmaf(x[k].w, w, o0.w));
+            o1 = make_float4(fmaf(y[k].x, w, o1.x), fmaf(y[k].y, w, o1.y), fmaf(y[k].z, w, o1.z), fmaf(y[k].w, w, o1.w));
         }
     }
     const float inv = total == 0.f ? 0.f : 1.f / total;
     const long long out = ((long long)cut.b * a.T + node) * a.H_q + h * sh.G + row % sh.G;
-    uint4* to = reinterpret_cast<uint4*>(reinterpret_cast<bf16*>(a.o) + out * D + blockIdx.y * 32);
-#pragma unroll
-    for (int c = 0; c < 8; c += 2)
-        to[c / 2] = make_uint4(pack_bf16(o[c].x * inv, o[c].y * inv), pack_bf16(o[c].z * inv, o[c].w * inv),
-                               pack_bf16(o[c + 1].x * inv, o[c + 1].y * inv), pack_bf16(o[c + 1].z * inv, o[c + 1].w * inv));
+    *reinterpret_cast<uint4*>(reinterpret_cast<bf16*>(a.o) + out * D + blockIdx.y * kJoinChannels) =
+        make_uint4(pack_bf16(o0.x * inv, o0.y * inv), pack_bf16(o0.z * inv, o0.w * inv), pack_bf16(o1.x * inv, o1.y * inv),
+                   pack_bf16(o1.z * inv, o1.w * inv));
     if (blockIdx.y == 0 && a.lse) a.lse[out] = total == 0.f ? NEG_INF : (r + log2f(total)) * kLn2;
 }
 
@@ -842,7 +882,7 @@ cudaError_t launch(const TreeAttnArgs& a, const TreeMaps& m, int ctas, cudaStrea
     }
     e = launch_pdl(tree_kernel<D>, dim3((unsigned)ctas), dim3(kThreads), Cfg<D>::SMEM, st, a, m);
     if (e != cudaSuccess) return e;
-    return launch_pdl(join_kernel<D>, dim3((unsigned)ctas, D / 32), dim3(kSlotRows), 0, st, a, ctas);
+    return launch_pdl(join_kernel<D>, dim3((unsigned)ctas, D / kJoinChannels), dim3(kSlotRows), 0, st, a, ctas);
 }
 
 // CTAs: one an SM, or as many as there can be tiles.
