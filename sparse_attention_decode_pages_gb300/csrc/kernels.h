@@ -252,6 +252,7 @@ struct TreeAcceptArgs {
     int B, T;
     long long n;
     unsigned* status;
+    unsigned long long wait_ns;
 };
 cudaError_t launch_spec_accept_tree(const TreeAcceptArgs& a, int num_sms, cudaStream_t st);
 

@@ -1386,6 +1386,7 @@ SPD_API spd_status spec_accept_tree(int32_t B, int32_t T, int32_t n_vocab, const
     a.T = T;
     a.n = n_vocab;
     a.status = d->status;
+    a.wait_ns = wait_limit_ns();
     cudaError_t e = launch_spec_accept_tree(a, d->sms, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? SPD_OK : cuda_fail(e, "spec_accept_tree launch");
 }
