@@ -26,6 +26,7 @@ constexpr int kThreads = 1024, kWarps = kThreads / 32;
 constexpr int kKeys = 16;                     // keys of a thread
 constexpr int kMaxCluster = 8;
 constexpr int kHeld = kThreads * kKeys;       // tokens that a CTA holds
+constexpr int kFew = 1024;                    // keys that one warp goes on with
 
 // Larger weight, larger key; -0 as 0; NaN 0, below every number.
 __device__ __forceinline__ uint32_t weight_key(float w) { return w != w ? 0u : float_key(w + 0.f); }
@@ -33,12 +34,16 @@ __device__ __forceinline__ uint32_t weight_key(float w) { return w != w ? 0u : f
 // HELD: the cluster's registers hold the row.  Otherwise its CTAs go over parts of the row again and again.
 template <bool HELD>
 __global__ void __launch_bounds__(kThreads) choose_kernel(const EvictArgs a) {
-    __shared__ unsigned s_count[2][kMaxCluster][4];  // the CTAs' counts, in turn
-    __shared__ unsigned s_warp[kWarps][4];
+    __shared__ unsigned s_warp[2][kWarps][3];           // the warps' counts, in turn
+    __shared__ unsigned s_count[2][kMaxCluster][3];     // the CTAs' counts, in turn
+    __shared__ uint32_t s_few[kFew];                    // (the first CTA's) the keys that are left
+    __shared__ unsigned s_nfew;
+    __shared__ uint32_t s_found;
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank(), size = (int)cluster.num_blocks();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int row = blockIdx.x / size, b = row / a.H_kv;
+    if (tid == 0) s_nfew = 0;
     pdl_wait();
     pdl_trigger();
     const int len = a.seq_lens[b];
@@ -64,107 +69,166 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const EvictArgs a) {
     const int warps = size * kWarps;
     const int per = HELD ? kKeys : (int)(((long long)len + 32LL * warps - 1) / (32LL * warps));
     const long long base = (long long)(rank * kWarps + warp) * per * 32 + lane;
-    uint32_t key[kKeys];
-    auto key_at = [&](int i) {  // of the warp's i-th 32 tokens; what is not chosen by its weight has none (0)
+    // the key of the i-th of them; what is not chosen by its weight has none (0).  (Loads of any place, so that they go out together.)
+    auto key_at = [&](int i) {
         const long long t = base + 32LL * i;
-        return t >= lo && t < hi ? weight_key(__ldg(w + t)) : 0u;
+        const float x = __ldg(w + min(t, (long long)len - 1));
+        return t >= lo && t < hi ? weight_key(x) : 0u;
     };
+    uint32_t key[kKeys];
     if (HELD) {
 #pragma unroll
         for (int i = 0; i < kKeys; ++i) key[i] = key_at(i);
     }
-    // the cluster's counts of four kinds; the warps' own stay in s_warp
-    int turn = 0;
-    auto join = [&](unsigned (&n)[4]) {
+    // f(i, key) for each of this thread's tokens
+    auto each = [&](auto f) {
+        if (HELD) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) n[j] = __reduce_add_sync(0xffffffffu, n[j]);
-        if (lane == 0)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) s_warp[warp][j] = n[j];
-        __syncthreads();
-        if (warp < 4) {
-            const unsigned sum = __reduce_add_sync(0xffffffffu, s_warp[lane][warp]);
-            if (size == 1) {
-                if (lane == 0) s_count[turn][0][warp] = sum;
-            } else if (lane < size) {
-                *cluster.map_shared_rank(&s_count[turn][rank][warp], lane) = sum;
-            }
+            for (int i = 0; i < kKeys; ++i) f(i, key[i]);
+        } else {
+            for (int i = 0; i < per; ++i) f(i, key_at(i));
         }
-        if (size == 1) __syncthreads();
-        else cluster.sync();
+    };
+    // the cluster's three counts; the warps' own stay in s_warp[turn ^ 1], the CTAs' in s_count[turn ^ 1]
+    int turn = 0;
+    auto join = [&](unsigned (&n)[3]) {
+        if (HELD) {  // at most 512 each in a warp: one reduction of ten bits each
+            const unsigned all = __reduce_add_sync(0xffffffffu, n[0] | n[1] << 10 | n[2] << 20);
+            n[0] = all & 1023u;
+            n[1] = all >> 10 & 1023u;
+            n[2] = all >> 20;
+        } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            n[j] = 0;
-            for (int r = 0; r < size; ++r) n[j] += s_count[turn][r][j];
+            for (int j = 0; j < 3; ++j) n[j] = __reduce_add_sync(0xffffffffu, n[j]);
+        }
+        if (lane < 3) s_warp[turn][warp][lane] = lane == 0 ? n[0] : lane == 1 ? n[1] : n[2];
+        __syncthreads();
+        if (HELD && size == 1) {  // at most 16,384 each
+            const unsigned x = __reduce_add_sync(0xffffffffu, s_warp[turn][lane][0] | s_warp[turn][lane][1] << 16);
+            n[2] = __reduce_add_sync(0xffffffffu, s_warp[turn][lane][2]);
+            n[0] = x & 0xffffu;
+            n[1] = x >> 16;
+        } else {
+            if (warp < 3) {
+                const unsigned sum = __reduce_add_sync(0xffffffffu, s_warp[turn][lane][warp]);
+                if (lane < size) *cluster.map_shared_rank(&s_count[turn][rank][warp], lane) = sum;
+            }
+            cluster.sync();
+#pragma unroll
+            for (int j = 0; j < 3; ++j) {
+                n[j] = 0;
+                for (int r = 0; r < size; ++r) n[j] += s_count[turn][r][j];
+            }
         }
         turn ^= 1;
     };
     if (size > 1) cluster.sync();  // the other CTAs' shared memory is there
 
-    // the largest key that at least k tokens reach
+    // the largest key that at least k tokens reach: `found` so far, which at_found tokens reach, and above ones reach what lies
+    // behind its range
     uint32_t found = 0;
+    unsigned at_found = (unsigned)(hi - lo), above = 0;
     if (k > 0) {
+        int bit = 30;
 #pragma unroll 1
-        for (int bit = 30; bit >= 0; bit -= 2) {
+        for (; bit >= 0; bit -= 2) {
             const uint32_t c1 = found | 1u << bit, c2 = found | 2u << bit, c3 = found | 3u << bit;
-            unsigned n[4] = {0, 0, 0, 0};
-            if (HELD) {
-#pragma unroll
-                for (int i = 0; i < kKeys; ++i) {
-                    n[1] += key[i] >= c1;
-                    n[2] += key[i] >= c2;
-                    n[3] += key[i] >= c3;
-                }
-            } else {
-                for (int i = 0; i < per; ++i) {
-                    const uint32_t x = key_at(i);
-                    n[1] += x >= c1;
-                    n[2] += x >= c2;
-                    n[3] += x >= c3;
-                }
-            }
+            unsigned n[3] = {0, 0, 0};
+            each([&](int, uint32_t x) {
+                n[0] += x >= c1;
+                n[1] += x >= c2;
+                n[2] += x >= c3;
+            });
             join(n);
-            if (n[3] >= k) found = c3;
-            else if (n[2] >= k) found = c2;
-            else if (n[1] >= k) found = c1;
+            if (n[2] >= k) {
+                found = c3;
+                at_found = n[2];
+            } else if (n[1] >= k) {
+                found = c2;
+                at_found = n[1];
+                above = n[2];
+            } else if (n[0] >= k) {
+                found = c1;
+                at_found = n[0];
+                above = n[1];
+            } else {
+                above = n[0];
+            }
+            if (at_found - above <= kFew) break;
+        }
+        if (bit > 0) {
+            // few keys are left in the range: one warp goes on with them
+            unsigned* count = cluster.map_shared_rank(&s_nfew, 0);
+            uint32_t* few = cluster.map_shared_rank(s_few, 0);
+            each([&](int i, uint32_t x) {
+                const long long t = base + 32LL * i;
+                const bool mine = t >= lo && t < hi && x >> bit == found >> bit;
+                const unsigned m = __ballot_sync(0xffffffffu, mine);
+                if (m) {
+                    unsigned at = 0;
+                    if (lane == 0) at = atomicAdd(count, (unsigned)__popc(m));
+                    at = __shfl_sync(0xffffffffu, at, 0) + __popc(m & ((1u << lane) - 1u));
+                    if (mine && at < kFew) few[at] = x;
+                }
+            });
+            if (size > 1) cluster.sync();
+            else __syncthreads();
+            if (rank == 0 && warp == 0) {
+                uint32_t x[kFew / 32];
+                const unsigned n = min(s_nfew, (unsigned)kFew);
+#pragma unroll
+                for (int i = 0; i < kFew / 32; ++i) x[i] = 32 * i + lane < n ? s_few[32 * i + lane] : 0u;
+                const unsigned need = k - above;  // (at least one: those above are too few)
+#pragma unroll 1
+                for (bit -= 2; bit >= 0; bit -= 2) {
+                    const uint32_t c1 = found | 1u << bit, c2 = found | 2u << bit, c3 = found | 3u << bit;
+                    unsigned sum = 0, third = 0;
+#pragma unroll
+                    for (int i = 0; i < kFew / 32; ++i) {
+                        sum += (x[i] >= c1) + ((unsigned)(x[i] >= c2) << 16);
+                        third += x[i] >= c3;
+                    }
+                    sum = __reduce_add_sync(0xffffffffu, sum);
+                    third = __reduce_add_sync(0xffffffffu, third);
+                    if (third >= need) found = c3;
+                    else if (sum >> 16 >= need) found = c2;
+                    else if ((sum & 0xffffu) >= need) found = c1;
+                }
+                if (lane < size) *cluster.map_shared_rank(&s_found, lane) = found;
+            }
+            if (size > 1) cluster.sync();
+            else __syncthreads();
+            found = s_found;
         }
     } else {
         found = 0xffffffffu;  // no key reaches it: float_key gives at most 0xff800000 for a number
     }
 
     // how many stay without regard to ties, and how many tie, up to each warp
-    unsigned n[4] = {0, 0, 0, 0};
+    unsigned n[3] = {0, 0, 0};
     auto classify = [&](int i, uint32_t x, bool& stays, bool& ties) {
         const long long t = base + 32LL * i;
         const bool inner = t >= lo && t < hi;
         stays = (t < len && !inner) || (inner && x > found);
         ties = inner && k > 0 && x == found;
     };
-    auto tally = [&](int i, uint32_t x) {
+    each([&](int i, uint32_t x) {
         bool stays, ties;
         classify(i, x, stays, ties);
         n[0] += stays;
         n[1] += ties;
-    };
-    if (HELD) {
-#pragma unroll
-        for (int i = 0; i < kKeys; ++i) tally(i, key[i]);
-    } else {
-        for (int i = 0; i < per; ++i) tally(i, key_at(i));
-    }
+    });
     join(n);
     const unsigned need = (unsigned)a.budget - n[0];  // ties that stay: the first ones
-    unsigned stay_before = 0, tie_before = 0;
-    for (int r = 0; r < rank; ++r) {
-        stay_before += s_count[turn ^ 1][r][0];
-        tie_before += s_count[turn ^ 1][r][1];
-    }
-    for (int i = 0; i < warp; ++i) {
-        stay_before += s_warp[i][0];
-        tie_before += s_warp[i][1];
-    }
+    unsigned stay_before = __reduce_add_sync(0xffffffffu, lane < warp ? s_warp[turn ^ 1][lane][0] : 0u);
+    unsigned tie_before = __reduce_add_sync(0xffffffffu, lane < warp ? s_warp[turn ^ 1][lane][1] : 0u);
+    if (!(HELD && size == 1))
+        for (int r = 0; r < rank; ++r) {
+            stay_before += s_count[turn ^ 1][r][0];
+            tie_before += s_count[turn ^ 1][r][1];
+        }
     const unsigned below = (1u << lane) - 1u;
-    auto place = [&](int i, uint32_t x) {
+    each([&](int i, uint32_t x) {
         bool stays, ties;
         classify(i, x, stays, ties);
         const unsigned ms = __ballot_sync(0xffffffffu, stays), mt = __ballot_sync(0xffffffffu, ties);
@@ -173,13 +237,7 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const EvictArgs a) {
         if (stays || (ties && my_tie < need)) kept[stay_before + __popc(ms & below) + min(my_tie, need)] = (int)(base + 32LL * i);
         stay_before += __popc(ms);
         tie_before += __popc(mt);
-    };
-    if (HELD) {
-#pragma unroll
-        for (int i = 0; i < kKeys; ++i) place(i, key[i]);
-    } else {
-        for (int i = 0; i < per; ++i) place(i, key_at(i));
-    }
+    });
 }
 
 template <int D>
