@@ -28,8 +28,9 @@ constexpr int kMaxCluster = 8;
 constexpr int kHeld = kThreads * kKeys;       // tokens that a CTA holds
 constexpr int kFew = 1024;                    // keys that one warp goes on with
 
-// Larger weight, larger key; -0 as 0; NaN 0, below every number.
-__device__ __forceinline__ uint32_t weight_key(float w) { return w != w ? 0u : float_key(w + 0.f); }
+// Larger weight, larger key; -0 as 0; NaN below every number.  (No token: 0; one that stays whatever its weight: kAlways.)
+constexpr uint32_t kAlways = 0xffffffffu;
+__device__ __forceinline__ uint32_t weight_key(float w) { return w != w ? 1u : float_key(w + 0.f); }
 
 // HELD: the cluster's registers hold the row.  Otherwise its CTAs go over parts of the row again and again.
 template <bool HELD>
@@ -61,19 +62,18 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const EvictArgs a) {
         for (long long i = (long long)rank * kThreads + tid; i < len; i += (long long)size * kThreads) kept[i] = (int)i;
         return;
     }
-    const int lo = a.n_sink, hi = len - a.n_recent;  // tokens that are chosen by their weights
-    const unsigned k = (unsigned)(a.budget - a.n_sink - a.n_recent);
+    const unsigned k = (unsigned)a.budget;
     const float* w = a.w + (long long)row * a.max_pages * a.ps;
 
     // this warp's tokens: `per` times 32 consecutive ones
     const int warps = size * kWarps;
-    const int per = HELD ? kKeys : (int)(((long long)len + 32LL * warps - 1) / (32LL * warps));
-    const long long base = (long long)(rank * kWarps + warp) * per * 32 + lane;
-    // the key of the i-th of them; what is not chosen by its weight has none (0).  (Loads of any place, so that they go out together.)
+    const int per = HELD ? kKeys : (len + 32 * warps - 1) / (32 * warps);
+    const int base = (rank * kWarps + warp) * per * 32 + lane;
+    // the key of the i-th of them  (loads of any place, so that they go out together)
     auto key_at = [&](int i) {
-        const long long t = base + 32LL * i;
-        const float x = __ldg(w + min(t, (long long)len - 1));
-        return t >= lo && t < hi ? weight_key(x) : 0u;
+        const int t = base + 32 * i;
+        const float x = __ldg(w + min(t, len - 1));
+        return t >= len ? 0u : t < a.n_sink || t >= len - a.n_recent ? kAlways : weight_key(x);
     };
     uint32_t key[kKeys];
     if (HELD) {
@@ -127,99 +127,76 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const EvictArgs a) {
     // the largest key that at least k tokens reach: `found` so far, which at_found tokens reach, and above ones reach what lies
     // behind its range
     uint32_t found = 0;
-    unsigned at_found = (unsigned)(hi - lo), above = 0;
-    if (k > 0) {
-        int bit = 30;
+    unsigned at_found = (unsigned)len, above = 0;
+    int bit = 30;
 #pragma unroll 1
-        for (; bit >= 0; bit -= 2) {
-            const uint32_t c1 = found | 1u << bit, c2 = found | 2u << bit, c3 = found | 3u << bit;
-            unsigned n[3] = {0, 0, 0};
-            each([&](int, uint32_t x) {
-                n[0] += x >= c1;
-                n[1] += x >= c2;
-                n[2] += x >= c3;
-            });
-            join(n);
-            if (n[2] >= k) {
-                found = c3;
-                at_found = n[2];
-            } else if (n[1] >= k) {
-                found = c2;
-                at_found = n[1];
-                above = n[2];
-            } else if (n[0] >= k) {
-                found = c1;
-                at_found = n[0];
-                above = n[1];
-            } else {
-                above = n[0];
-            }
-            if (at_found - above <= kFew) break;
+    for (; bit >= 0; bit -= 2) {
+        const uint32_t c1 = found | 1u << bit, c2 = found | 2u << bit, c3 = found | 3u << bit;
+        unsigned n[3] = {0, 0, 0};
+        each([&](int, uint32_t x) {
+            n[0] += x >= c1;
+            n[1] += x >= c2;
+            n[2] += x >= c3;
+        });
+        join(n);
+        if (n[2] >= k) {
+            found = c3;
+            at_found = n[2];
+        } else if (n[1] >= k) {
+            found = c2;
+            at_found = n[1];
+            above = n[2];
+        } else if (n[0] >= k) {
+            found = c1;
+            at_found = n[0];
+            above = n[1];
+        } else {
+            above = n[0];
         }
-        if (bit > 0) {
-            // few keys are left in the range: one warp goes on with them
-            unsigned* count = cluster.map_shared_rank(&s_nfew, 0);
-            uint32_t* few = cluster.map_shared_rank(s_few, 0);
-            each([&](int i, uint32_t x) {
-                const long long t = base + 32LL * i;
-                const bool mine = t >= lo && t < hi && x >> bit == found >> bit;
-                const unsigned m = __ballot_sync(0xffffffffu, mine);
-                if (m) {
-                    unsigned at = 0;
-                    if (lane == 0) at = atomicAdd(count, (unsigned)__popc(m));
-                    at = __shfl_sync(0xffffffffu, at, 0) + __popc(m & ((1u << lane) - 1u));
-                    if (mine && at < kFew) few[at] = x;
-                }
+        if (at_found - above <= kFew) break;
+    }
+    if (bit > 0) {
+        // few keys are left in the range: one CTA goes on with one a thread, a bit and a barrier at a time
+        unsigned mine = 0;
+        each([&](int, uint32_t x) { mine += x >> bit == found >> bit && x != 0; });
+        unsigned at = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const unsigned y = __shfl_up_sync(0xffffffffu, at, off);
+            if (lane >= off) at += y;
+        }
+        unsigned all = __shfl_sync(0xffffffffu, at, 31);
+        if (lane == 0 && all) all = atomicAdd(cluster.map_shared_rank(&s_nfew, 0), all);
+        at += __shfl_sync(0xffffffffu, all, 0) - mine;
+        uint32_t* few = cluster.map_shared_rank(s_few, 0);
+        if (mine)
+            each([&](int, uint32_t x) {
+                if (x >> bit == found >> bit && x != 0 && at < kFew) few[at++] = x;
             });
-            if (size > 1) cluster.sync();
-            else __syncthreads();
-            if (rank == 0 && warp == 0) {
-                uint32_t x[kFew / 32];
-                const unsigned n = min(s_nfew, (unsigned)kFew);
-#pragma unroll
-                for (int i = 0; i < kFew / 32; ++i) x[i] = 32 * i + lane < n ? s_few[32 * i + lane] : 0u;
-                const unsigned need = k - above;  // (at least one: those above are too few)
+        if (size > 1) cluster.sync();
+        else __syncthreads();
+        if (rank == 0) {
+            const uint32_t x = tid < (int)min(s_nfew, (unsigned)kFew) ? s_few[tid] : 0u;
+            const int need = (int)(k - above);  // (at least one: those above are too few)
 #pragma unroll 1
-                for (bit -= 2; bit >= 0; bit -= 2) {
-                    const uint32_t c1 = found | 1u << bit, c2 = found | 2u << bit, c3 = found | 3u << bit;
-                    unsigned sum = 0, third = 0;
-#pragma unroll
-                    for (int i = 0; i < kFew / 32; ++i) {
-                        sum += (x[i] >= c1) + ((unsigned)(x[i] >= c2) << 16);
-                        third += x[i] >= c3;
-                    }
-                    sum = __reduce_add_sync(0xffffffffu, sum);
-                    third = __reduce_add_sync(0xffffffffu, third);
-                    if (third >= need) found = c3;
-                    else if (sum >> 16 >= need) found = c2;
-                    else if ((sum & 0xffffu) >= need) found = c1;
-                }
-                if (lane < size) *cluster.map_shared_rank(&s_found, lane) = found;
-            }
-            if (size > 1) cluster.sync();
-            else __syncthreads();
+            while (--bit >= 0)
+                if (__syncthreads_count(x >= (found | 1u << bit)) >= need) found |= 1u << bit;
+            if (size > 1 && tid < size) *cluster.map_shared_rank(&s_found, tid) = found;
+        }
+        if (size > 1) {
+            cluster.sync();
             found = s_found;
         }
-    } else {
-        found = 0xffffffffu;  // no key reaches it: float_key gives at most 0xff800000 for a number
     }
 
     // how many stay without regard to ties, and how many tie, up to each warp
     unsigned n[3] = {0, 0, 0};
-    auto classify = [&](int i, uint32_t x, bool& stays, bool& ties) {
-        const long long t = base + 32LL * i;
-        const bool inner = t >= lo && t < hi;
-        stays = (t < len && !inner) || (inner && x > found);
-        ties = inner && k > 0 && x == found;
-    };
-    each([&](int i, uint32_t x) {
-        bool stays, ties;
-        classify(i, x, stays, ties);
-        n[0] += stays;
-        n[1] += ties;
+    each([&](int, uint32_t x) {
+        n[0] += x > found;
+        n[1] += x == found;
     });
     join(n);
-    const unsigned need = (unsigned)a.budget - n[0];  // ties that stay: the first ones
+    const unsigned need = k - n[0];  // ties that stay: the first ones
     unsigned stay_before = __reduce_add_sync(0xffffffffu, lane < warp ? s_warp[turn ^ 1][lane][0] : 0u);
     unsigned tie_before = __reduce_add_sync(0xffffffffu, lane < warp ? s_warp[turn ^ 1][lane][1] : 0u);
     if (!(HELD && size == 1))
@@ -228,16 +205,23 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const EvictArgs a) {
             tie_before += s_count[turn ^ 1][r][1];
         }
     const unsigned below = (1u << lane) - 1u;
-    each([&](int i, uint32_t x) {
-        bool stays, ties;
-        classify(i, x, stays, ties);
-        const unsigned ms = __ballot_sync(0xffffffffu, stays), mt = __ballot_sync(0xffffffffu, ties);
-        const unsigned my_tie = tie_before + __popc(mt & below);
-        // kept ones before this token: those that stay, and ties up to `need`
-        if (stays || (ties && my_tie < need)) kept[stay_before + __popc(ms & below) + min(my_tie, need)] = (int)(base + 32LL * i);
-        stay_before += __popc(ms);
-        tie_before += __popc(mt);
-    });
+    if (need == n[1]) {  // every tie stays
+        unsigned before = stay_before + tie_before;
+        each([&](int i, uint32_t x) {
+            const unsigned m = __ballot_sync(0xffffffffu, x >= found);
+            if (x >= found) kept[before + __popc(m & below)] = base + 32 * i;
+            before += __popc(m);
+        });
+    } else {
+        each([&](int i, uint32_t x) {
+            const unsigned ms = __ballot_sync(0xffffffffu, x > found), mt = __ballot_sync(0xffffffffu, x == found);
+            const unsigned my_tie = tie_before + __popc(mt & below);
+            // kept ones before this token: those that stay, and ties up to `need`
+            if (x > found || (x == found && my_tie < need)) kept[stay_before + __popc(ms & below) + min(my_tie, need)] = base + 32 * i;
+            stay_before += __popc(ms);
+            tie_before += __popc(mt);
+        });
+    }
 }
 
 template <int D>
