@@ -282,8 +282,9 @@ struct WeightsArgs {
     const float* w_in;  // [B][H_kv][max_pages * ps] or NULL
     float* w_out;
     unsigned* status;
+    unsigned long long wait_ns;
 };
-cudaError_t launch_weights_update(const WeightsArgs& a, cudaStream_t st);
+cudaError_t launch_weights_update(const WeightsArgs& a, int num_sms, cudaStream_t st);
 
 struct EvictArgs {
     uint16_t* K;

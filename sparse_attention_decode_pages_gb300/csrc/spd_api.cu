@@ -1480,7 +1480,8 @@ SPD_API spd_status kv_weights_update(const spd_dims* dims, int32_t T, const spd_
     a.w_in = w_in;
     a.w_out = w_out;
     a.status = d->status;
-    cudaError_t e = launch_weights_update(a, static_cast<cudaStream_t>(stream));
+    a.wait_ns = wait_limit_ns();
+    cudaError_t e = launch_weights_update(a, d->sms, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? SPD_OK : cuda_fail(e, "kv_weights_update launch");
 }
 
