@@ -45,6 +45,10 @@ constexpr int kSoftmaxRegs = 208, kOtherRegs = 80;
 static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "what the block was launched with");
 constexpr int kInfos = 16;          // tiles whose visible tokens are written down
 constexpr int kOdd = 8;             // pieces whose nodes with odd values are
+// Units of which the SMs hold this many times as many are cut into parts of their own: the last part of a unit costs a CTA
+// 3 to 4 us (queries, first products, results) that a CTA with parts of two units pays twice; more units than this would leave
+// parts of very different lengths.
+constexpr int kFewUnits = 8;
 constexpr float kLag = 8.f;         // powers of two that a maximum may lie above the reference
 
 template <int D>
@@ -68,9 +72,10 @@ struct Cfg {
     static constexpr int COL_S = 0, COL_O = 256, COLUMNS = 512;
 };
 
-// What a CTA leaves for the joining kernel: a unit that begins in its share and ends in another's.
+// What a CTA leaves for the joining kernel: a unit that begins in its share and ends in another's (one for a CTA, or, where units are
+// few, for a unit).
 struct Cut {
-    int b, sub, pieces, pad;
+    int b, sub, pieces, cta;
 };
 
 // Partials: [slot][D / 4][256 rows] float4, then [slot][256 rows] (reference, sum); two slots a CTA, one for the unit
@@ -94,6 +99,14 @@ __host__ __device__ inline Shape shape_of(int T, int G) {
 struct Piece {
     int b, sub, len, nt, t0, t1;
     bool bad;  // a length that the page table has no room for: no tokens, no nodes
+};
+
+// Where a CTA's share begins, and what it is of: tile `at` of `total`, or (few units) the first of a unit's parts, which
+// `follow` CTAs hold the rest of.
+struct Share {
+    int b, sub, t0, len;
+    long long left, at, total;
+    int follow;
 };
 
 // Goes through the pieces of a share, one sequence's units after the other's.
@@ -145,13 +158,12 @@ struct Shares {
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    tree_kernel(const TreeAttnArgs a, const __grid_constant__ TreeMaps maps) {
+    tree_kernel(const TreeAttnArgs a, const __grid_constant__ TreeMaps maps, const bool few) {
     using C = Cfg<D>;
     constexpr int STAGES = C::STAGES;
     extern __shared__ uint8_t smem_raw[];
     __shared__ long long s_scan[kThreads / 32];
-    __shared__ int s_b, s_len;
-    __shared__ long long s_off;
+    __shared__ Share s_share;
     __shared__ uint32_t s_tmem;
     __shared__ unsigned long long s_odd[kOdd];  // nodes of a piece's tree whose values are not all finite
     uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
@@ -204,66 +216,98 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_wait();
     pdl_trigger();
 
-    // this CTA's share: where it begins (sequence, and tile among that sequence's units) and how many tiles
+    // This CTA's share: where it begins (unit and tile) and how many tiles, in shared memory (what every role would carry in
+    // registers otherwise costs the softmax its own).
     {
-        const int per = (a.B + kThreads - 1) / kThreads;
-        const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
-        auto tiles_of = [&](int len) {
-            return (long long)(seq_pages(len, a.ps, a.max_pages) < 0 ? 1 : (len + kTokens - 1) / kTokens + 1) * subs;
-        };
-        int len = 0;  // of this thread's last sequence
-        long long mine = 0;
-        for (int b = b0; b < b1; ++b) {
-            len = a.seq_lens[b];
-            mine += tiles_of(len);
-        }
-        long long incl = mine;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, incl, off);
-            if (lane >= off) incl += y;
-        }
-        if (lane == 31) s_scan[warp] = incl;
+        auto tiles_of = [&](int len) { return seq_pages(len, a.ps, a.max_pages) < 0 ? 1 : (len + kTokens - 1) / kTokens + 1; };
         if (warp == 9) tmem_alloc(&s_tmem, C::COLUMNS);
+        if (few) {
+            // A unit's tiles are cut into equal parts, about as many as its share of all tiles, so that no CTA goes from
+            // one unit to the next: one warp, a sequence a lane.
+            if (warp == 0) {
+                int len = 0, nt = 0;
+                if (lane < a.B) {
+                    len = a.seq_lens[lane];
+                    nt = tiles_of(len);
+                }
+                const int total = __reduce_add_sync(0xffffffffu, nt) * subs, units = a.B * subs;
+                const int parts = lane < a.B ? min(nt, 1 + (int)((unsigned)nt * (gridDim.x - units) / (unsigned)total)) : 0;
+                int incl = parts * subs;
+#pragma unroll
+                for (int off = 1; off < 32; off <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, incl, off);
+                    if (lane >= off) incl += y;
+                }
+                const unsigned mine = __ballot_sync(0xffffffffu, lane < a.B && (int)blockIdx.x < incl);
+                if (lane == (mine ? __ffs((int)mine) - 1 : 0)) {
+                    const int off = (int)blockIdx.x - (incl - parts * subs);
+                    Share x = {lane, 0, 0, len, 0, 0, 0, 0};
+                    if (mine) {
+                        x.sub = off / parts;
+                        const int part = off - x.sub * parts;
+                        x.t0 = (int)((unsigned)nt * part / parts);  // (at most 2^23 tiles, 256 parts)
+                        x.left = (int)((unsigned)nt * (part + 1) / parts) - x.t0;
+                        x.follow = part == 0 ? parts - 1 : 0;
+                    }
+                    s_share = x;
+                }
+            }
+        } else {
+            // all tiles in a row, in equal shares
+            const int per = (a.B + kThreads - 1) / kThreads;
+            const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
+            int len = 0;  // of this thread's last sequence
+            long long mine = 0;
+            for (int b = b0; b < b1; ++b) {
+                len = a.seq_lens[b];
+                mine += (long long)tiles_of(len) * subs;
+            }
+            long long incl = mine;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const long long y = __shfl_up_sync(0xffffffffu, incl, off);
+                if (lane >= off) incl += y;
+            }
+            if (lane == 31) s_scan[warp] = incl;
+            __syncthreads();
+            long long sums = lane < kThreads / 32 ? s_scan[lane] : 0;
+#pragma unroll
+            for (int off = 1; off < 16; off <<= 1) {
+                const long long y = __shfl_up_sync(0xffffffffu, sums, off);
+                if (lane >= off) sums += y;
+            }
+            const long long total = __shfl_sync(0xffffffffu, sums, kThreads / 32 - 1);
+            long long before = __shfl_sync(0xffffffffu, sums, warp > 0 ? warp - 1 : 0);
+            before = (warp > 0 ? before : 0) + incl - mine;
+            const int ctas = (int)min((long long)gridDim.x, total);
+            const bool any = (int)blockIdx.x < ctas;
+            const Shares shares(total, ctas);
+            const long long g0 = any ? shares.begin(blockIdx.x) : 0;
+            if (before <= g0 && g0 < before + mine) {  // one thread's
+                int b = b0;
+                if (per > 1) len = a.seq_lens[b];
+                long long at = before;
+                while (g0 - at >= (long long)tiles_of(len) * subs) {
+                    at += (long long)tiles_of(len) * subs;
+                    len = a.seq_lens[++b];
+                }
+                const long long off = g0 - at;
+                const int nt = tiles_of(len);
+                Share x = {b, 0, 0, len, any ? shares.begin(blockIdx.x + 1) - g0 : 0, g0, total, 0};
+                x.sub = off < 0x7fffffff ? (int)off / nt : (int)(off / nt);
+                x.t0 = (int)(off - (long long)x.sub * nt);
+                s_share = x;
+            }
+        }
         tmem_fence_before();
         __syncthreads();
         tmem_fence_after();
-        long long sums = lane < kThreads / 32 ? s_scan[lane] : 0;
-#pragma unroll
-        for (int off = 1; off < 16; off <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, sums, off);
-            if (lane >= off) sums += y;
-        }
-        const long long total = __shfl_sync(0xffffffffu, sums, kThreads / 32 - 1);
-        long long before = __shfl_sync(0xffffffffu, sums, warp > 0 ? warp - 1 : 0);
-        before = (warp > 0 ? before : 0) + incl - mine;
-        const int ctas = (int)min((long long)gridDim.x, total);
-        const Shares shares(total, ctas);
-        const long long g0 = (int)blockIdx.x < ctas ? shares.begin(blockIdx.x) : total;
-        const long long g1 = (int)blockIdx.x < ctas ? shares.begin(blockIdx.x + 1) : total;
-        if (before <= g0 && g0 < before + mine) {
-            int b = b0;
-            if (per > 1) len = a.seq_lens[b];
-            while (g0 - before >= tiles_of(len)) {
-                before += tiles_of(len);
-                len = a.seq_lens[++b];
-            }
-            s_b = b;
-            s_off = g0 - before;
-            s_len = len;
-        }
-        __syncthreads();
         Walk w;
-        w.left = g1 - g0;
-        w.b = w.sub = w.t0 = w.len = w.nt = 0;
-        w.bad = false;
-        if (w.left > 0) {
-            w.b = s_b;
-            w.look(a, s_len);
-            const long long off = s_off;
-            w.sub = off < 0x7fffffff ? (int)off / w.nt : (int)(off / w.nt);
-            w.t0 = (int)(off - (long long)w.sub * w.nt);
-        }
+        w.b = s_share.b;
+        w.sub = s_share.sub;
+        w.t0 = s_share.t0;
+        w.left = s_share.left;
+        w.look(a, s_share.len);
         float* part_o = reinterpret_cast<float*>(static_cast<char*>(a.ws) + ((size_t)gridDim.x * sizeof(Cut) + 255) / 256 * 256);
         float2* part_ml = reinterpret_cast<float2*>(part_o + (size_t)2 * gridDim.x * kSlotRows * D);
         const uint32_t tmem = s_tmem;
@@ -740,21 +784,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ======================================================== the nodes' values
             // first, a unit that begins here and ends behind the share is the joining kernel's work
             if (lane == 0) {
-                Cut cut = {0, 0, 0, 0};
-                Walk x = w;
-                Piece p;
-                long long at = g0;
-                while (x.next(a, subs, p)) {
-                    if (p.t0 == 0 && p.t1 < p.nt) {
-                        int c = blockIdx.x;
-                        while (shares.begin(c + 1) < at + p.nt) ++c;
-                        cut.b = p.b;
-                        cut.sub = p.sub;
-                        cut.pieces = c - (int)blockIdx.x + 1;
+                Cut* cuts = reinterpret_cast<Cut*>(a.ws);
+                if (few) {
+                    if (w.left > 0 && w.t0 == 0) {
+                        const int parts = s_share.follow + 1;
+                        cuts[w.b * subs + w.sub] = {w.b, w.sub, parts > 1 ? parts : 0, (int)blockIdx.x};
                     }
-                    at += p.t1 - p.t0;
+                } else {
+                    Cut cut = {0, 0, 0, (int)blockIdx.x};
+                    Walk x = w;
+                    Piece p;
+                    long long at = s_share.at;
+                    const Shares shares(s_share.total, (int)min((long long)gridDim.x, s_share.total));
+                    while (x.next(a, subs, p)) {
+                        if (p.t0 == 0 && p.t1 < p.nt) {
+                            int c = blockIdx.x;
+                            while (shares.begin(c + 1) < at + p.nt) ++c;
+                            cut = {p.b, p.sub, c - (int)blockIdx.x + 1, (int)blockIdx.x};
+                        }
+                        at += p.t1 - p.t0;
+                    }
+                    cuts[blockIdx.x] = cut;
                 }
-                reinterpret_cast<Cut*>(a.ws)[blockIdx.x] = cut;
             }
             __syncwarp();
             // A weight of 0 times an infinity or a NaN would reach rows that do not see the node: rows of what is
@@ -810,7 +861,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 9) tmem_free(s_tmem, C::COLUMNS);
 }
 
-// Joins the partials of a unit that shares' borders cut: a thread has eight channels of a row; eight partials are asked
+// Joins the partials of the units that shares' borders cut: a thread has eight channels of a row; eight partials are asked
 // for at once.
 constexpr int kJoinChannels = 8, kJoinAhead = 8;
 template <int D>
@@ -819,10 +870,11 @@ __global__ void __launch_bounds__(kSlotRows) join_kernel(const TreeAttnArgs a, i
     const Shape sh = shape_of(a.T, a.H_q / a.H_kv);
     const float* part_o = reinterpret_cast<const float*>(static_cast<const char*>(a.ws) + ((size_t)ctas * sizeof(Cut) + 255) / 256 * 256);
     const float2* part_ml = reinterpret_cast<const float2*>(part_o + (size_t)2 * ctas * kSlotRows * D) + threadIdx.x;
-    const float4* part = reinterpret_cast<const float4*>(part_o) + blockIdx.y * 2 * kSlotRows + threadIdx.x;
+    const int group = blockIdx.x % (D / kJoinChannels);
+    const float4* part = reinterpret_cast<const float4*>(part_o) + group * 2 * kSlotRows + threadIdx.x;
     pdl_wait();
     pdl_trigger();
-    const Cut cut = reinterpret_cast<const Cut*>(a.ws)[blockIdx.x];
+    const Cut cut = reinterpret_cast<const Cut*>(a.ws)[blockIdx.x / (D / kJoinChannels)];
     if (cut.pieces == 0) return;
     const int h = cut.sub / sh.pairs, mt = 2 * (cut.sub - h * sh.pairs);
     const int row = threadIdx.x & (kRows - 1), node = (mt + threadIdx.x / kRows) * sh.tpt + row / sh.G;
@@ -836,7 +888,7 @@ __global__ void __launch_bounds__(kSlotRows) join_kernel(const TreeAttnArgs a, i
         for (int k = 0; k < kJoinAhead; ++k) {
             const int i = i0 + k;
             // a unit's first partial is its CTA's second slot, the others are their CTAs' first
-            const size_t slot = (size_t)(2 * ((int)blockIdx.x + i) + (i == 0 ? 1 : 0));
+            const size_t slot = (size_t)(2 * (cut.cta + i) + (i == 0 ? 1 : 0));
             ml[k] = make_float2(NEG_INF, 0.f);
             x[k] = y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (i < cut.pieces) {
@@ -863,10 +915,10 @@ __global__ void __launch_bounds__(kSlotRows) join_kernel(const TreeAttnArgs a, i
     }
     const float inv = total == 0.f ? 0.f : 1.f / total;
     const long long out = ((long long)cut.b * a.T + node) * a.H_q + h * sh.G + row % sh.G;
-    *reinterpret_cast<uint4*>(reinterpret_cast<bf16*>(a.o) + out * D + blockIdx.y * kJoinChannels) =
+    *reinterpret_cast<uint4*>(reinterpret_cast<bf16*>(a.o) + out * D + group * kJoinChannels) =
         make_uint4(pack_bf16(o0.x * inv, o0.y * inv), pack_bf16(o0.z * inv, o0.w * inv), pack_bf16(o1.x * inv, o1.y * inv),
                    pack_bf16(o1.z * inv, o1.w * inv));
-    if (blockIdx.y == 0 && a.lse) a.lse[out] = total == 0.f ? NEG_INF : (r + log2f(total)) * kLn2;
+    if (group == 0 && a.lse) a.lse[out] = total == 0.f ? NEG_INF : (r + log2f(total)) * kLn2;
 }
 
 template <int D>
@@ -880,9 +932,12 @@ cudaError_t launch(const TreeAttnArgs& a, const TreeMaps& m, int ctas, cudaStrea
         if (e != cudaSuccess) return e;
         if (dev < 64) known[dev].store(true, std::memory_order_release);
     }
-    e = launch_pdl(tree_kernel<D>, dim3((unsigned)ctas), dim3(kThreads), Cfg<D>::SMEM, st, a, m);
+    const long long units = (long long)a.B * a.H_kv * shape_of(a.T, a.H_q / a.H_kv).pairs;
+    const bool few = a.B <= 32 && units * kFewUnits <= ctas;
+    e = launch_pdl(tree_kernel<D>, dim3((unsigned)ctas), dim3(kThreads), Cfg<D>::SMEM, st, a, m, few);
     if (e != cudaSuccess) return e;
-    return launch_pdl(join_kernel<D>, dim3((unsigned)ctas, D / kJoinChannels), dim3(kSlotRows), 0, st, a, ctas);
+    const long long cuts = few ? units : ctas;
+    return launch_pdl(join_kernel<D>, dim3((unsigned)(cuts * (D / kJoinChannels))), dim3(kSlotRows), 0, st, a, ctas);
 }
 
 // CTAs: one an SM, or as many as there can be tiles.
