@@ -1,18 +1,22 @@
 // evict.cu -- shortens the cache to the tokens of the largest attention weights.
 //
-// Two kernels.  The first chooses: of a (sequence, KV head)'s tokens the first n_sink, the newest
-// n_recent, and the k others of the largest weights.  A weight becomes a 32-bit key in the
-// order of the numbers; the key of the k-th largest is found two bits at a time, from the highest, by
-// counting the keys that reach each of three candidates.  The keys stay in registers meanwhile: 16 a thread,
-// 16,384 tokens a CTA, and a cluster of CTAs for longer rows (the counts are joined through
-// distributed shared memory); rows beyond that are read anew for each count.  Tokens with a larger
-// key stay, and of those with that very key the lowest positions.  A warp holds consecutive tokens, 32 a
-// register, so one scan of the warps' counts and ballots give every kept token its place.
+// Two kernels.  The first chooses: of a (sequence, KV head)'s tokens the first n_sink, the newest n_recent, and the
+// others of the largest weights.  A weight becomes a 32-bit key in the order of the numbers (above all numbers for the
+// tokens that always stay); the largest key that `budget` tokens reach is found two bits at a time, from the highest, by counting
+// the keys that reach each of three candidates, until few keys are left in the range; those go on alone, one a thread, a bit and
+// a barrier that counts at a time.  Tokens with a larger key stay, and of those with that very key the lowest positions.  A warp
+// has consecutive tokens, so one scan of the warps' counts and ballots give every kept token its place.
+// What bounds it is a count's latency: three CTAs an SM where rows are many, clusters of up to eight CTAs a row, their counts joined
+// through distributed shared memory, where rows are few or long (the choice for 512 rows of 8K-16K tokens: 52 us; keys in
+// registers, one CTA of 1,024 threads an SM: 89; 8 rows of 65,521: 23 us).  The keys stay in shared memory; rows beyond
+// 8 x 49,152 tokens are read anew for each count.
 //
 // The second moves: a warp takes a new page of a KV head, 16 tokens at a time, all their keys' and values' rows in flight at
-// once, and forms the page's minima and maxima on the way.  It is bound by memory: each kept row
-// is read once and written once.
+// once, and forms the page's minima and maxima on the way.  It is bound by memory: each kept row is read once and written
+// once (512 heads' 4,096 tokens, 2.2 GB: 357 us, 91 % of the measured copy peak).
 #include <cooperative_groups.h>
+
+#include <atomic>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -22,19 +26,20 @@ namespace cg = cooperative_groups;
 namespace spd {
 namespace {
 
-constexpr int kThreads = 1024, kWarps = kThreads / 32;
-constexpr int kKeys = 16;                     // keys of a thread
+constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kHeld = kThreads * kKeys;       // tokens that a CTA holds
-constexpr int kFew = 1024;                    // keys that one warp goes on with
+constexpr int kHeld = 49152, kHeldMany = 18432;  // tokens that a CTA holds: alone on an SM, and three on an SM
+constexpr int kFew = kThreads;                   // keys that one CTA goes on with, one a thread
 
 // Larger weight, larger key; -0 as 0; NaN below every number.  (No token: 0; one that stays whatever its weight: kAlways.)
 constexpr uint32_t kAlways = 0xffffffffu;
 __device__ __forceinline__ uint32_t weight_key(float w) { return w != w ? 1u : float_key(w + 0.f); }
 
-// HELD: the cluster's registers hold the row.  Otherwise its CTAs go over parts of the row again and again.
+// HELD: the cluster's shared memory holds the row's keys, `room` tokens a CTA.  Otherwise its CTAs go over parts of the row again
+// and again.
 template <bool HELD>
 __global__ void __launch_bounds__(kThreads) choose_kernel(const EvictArgs a) {
+    extern __shared__ __align__(16) uint32_t s_key[];
     __shared__ unsigned s_warp[2][kWarps][3];           // the warps' counts, in turn
     __shared__ unsigned s_count[2][kMaxCluster][3];     // the CTAs' counts, in turn
     __shared__ uint32_t s_few[kFew];                    // (the first CTA's) the keys that are left
@@ -65,34 +70,42 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const EvictArgs a) {
     const unsigned k = (unsigned)a.budget;
     const float* w = a.w + (long long)row * a.max_pages * a.ps;
 
-    // this warp's tokens: `per` times 32 consecutive ones
+    // this warp's tokens: `per` (a multiple of four) times 32 consecutive ones
     const int warps = size * kWarps;
-    const int per = HELD ? kKeys : (len + 32 * warps - 1) / (32 * warps);
+    const int per = ((len + 32 * warps - 1) / (32 * warps) + 3) & ~3;
     const int base = (rank * kWarps + warp) * per * 32 + lane;
-    // the key of the i-th of them  (loads of any place, so that they go out together)
-    auto key_at = [&](int i) {
-        const int t = base + 32 * i;
-        const float x = __ldg(w + min(t, len - 1));
-        return t >= len ? 0u : t < a.n_sink || t >= len - a.n_recent ? kAlways : weight_key(x);
-    };
-    uint32_t key[kKeys];
+    auto key_of = [&](int t, float x) { return t >= len ? 0u : t < a.n_sink || t >= len - a.n_recent ? kAlways : weight_key(x); };
+    // (loads of any place, so that they go out together)
+    auto weight_at = [&](int t) { return __ldg(w + min(t, len - 1)); };
+    uint32_t* keys = s_key + warp * per * 32;
     if (HELD) {
+        for (int i = 0; i < per; i += 4) {
+            float x[4];
 #pragma unroll
-        for (int i = 0; i < kKeys; ++i) key[i] = key_at(i);
+            for (int j = 0; j < 4; ++j) x[j] = weight_at(base + 32 * (i + j));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) keys[32 * (i + j) + lane] = key_of(base + 32 * (i + j), x[j]);
+        }
+        __syncwarp();
     }
-    // f(i, key) for each of this thread's tokens
+    // f(key) for each of this warp's tokens, in any order
     auto each = [&](auto f) {
         if (HELD) {
-#pragma unroll
-            for (int i = 0; i < kKeys; ++i) f(i, key[i]);
+            for (int i = 0; i < per / 4; ++i) {
+                const uint4 x = *reinterpret_cast<const uint4*>(keys + 128 * i + 4 * lane);
+                f(x.x);
+                f(x.y);
+                f(x.z);
+                f(x.w);
+            }
         } else {
-            for (int i = 0; i < per; ++i) f(i, key_at(i));
+            for (int i = 0; i < per; ++i) f(key_of(base + 32 * i, weight_at(base + 32 * i)));
         }
     };
     // the cluster's three counts; the warps' own stay in s_warp[turn ^ 1], the CTAs' in s_count[turn ^ 1]
     int turn = 0;
     auto join = [&](unsigned (&n)[3]) {
-        if (HELD) {  // at most 512 each in a warp: one reduction of ten bits each
+        if (per <= 31) {  // at most 992 each in a warp: one reduction of ten bits each
             const unsigned all = __reduce_add_sync(0xffffffffu, n[0] | n[1] << 10 | n[2] << 20);
             n[0] = all & 1023u;
             n[1] = all >> 10 & 1023u;
@@ -103,14 +116,12 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const EvictArgs a) {
         }
         if (lane < 3) s_warp[turn][warp][lane] = lane == 0 ? n[0] : lane == 1 ? n[1] : n[2];
         __syncthreads();
-        if (HELD && size == 1) {  // at most 16,384 each
-            const unsigned x = __reduce_add_sync(0xffffffffu, s_warp[turn][lane][0] | s_warp[turn][lane][1] << 16);
-            n[2] = __reduce_add_sync(0xffffffffu, s_warp[turn][lane][2]);
-            n[0] = x & 0xffffu;
-            n[1] = x >> 16;
+        if (size == 1) {
+#pragma unroll
+            for (int j = 0; j < 3; ++j) n[j] = __reduce_add_sync(0xffffffffu, lane < kWarps ? s_warp[turn][lane][j] : 0u);
         } else {
             if (warp < 3) {
-                const unsigned sum = __reduce_add_sync(0xffffffffu, s_warp[turn][lane][warp]);
+                const unsigned sum = __reduce_add_sync(0xffffffffu, lane < kWarps ? s_warp[turn][lane][warp] : 0u);
                 if (lane < size) *cluster.map_shared_rank(&s_count[turn][rank][warp], lane) = sum;
             }
             cluster.sync();
@@ -133,7 +144,7 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const EvictArgs a) {
     for (; bit >= 0; bit -= 2) {
         const uint32_t c1 = found | 1u << bit, c2 = found | 2u << bit, c3 = found | 3u << bit;
         unsigned n[3] = {0, 0, 0};
-        each([&](int, uint32_t x) {
+        each([&](uint32_t x) {
             n[0] += x >= c1;
             n[1] += x >= c2;
             n[2] += x >= c3;
@@ -158,7 +169,7 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const EvictArgs a) {
     if (bit > 0) {
         // few keys are left in the range: one CTA goes on with one a thread, a bit and a barrier at a time
         unsigned mine = 0;
-        each([&](int, uint32_t x) { mine += x >> bit == found >> bit && x != 0; });
+        each([&](uint32_t x) { mine += x >> bit == found >> bit && x != 0; });
         unsigned at = mine;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -170,7 +181,7 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const EvictArgs a) {
         at += __shfl_sync(0xffffffffu, all, 0) - mine;
         uint32_t* few = cluster.map_shared_rank(s_few, 0);
         if (mine)
-            each([&](int, uint32_t x) {
+            each([&](uint32_t x) {
                 if (x >> bit == found >> bit && x != 0 && at < kFew) few[at++] = x;
             });
         if (size > 1) cluster.sync();
@@ -191,7 +202,7 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const EvictArgs a) {
 
     // how many stay without regard to ties, and how many tie, up to each warp
     unsigned n[3] = {0, 0, 0};
-    each([&](int, uint32_t x) {
+    each([&](uint32_t x) {
         n[0] += x > found;
         n[1] += x == found;
     });
@@ -199,28 +210,29 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const EvictArgs a) {
     const unsigned need = k - n[0];  // ties that stay: the first ones
     unsigned stay_before = __reduce_add_sync(0xffffffffu, lane < warp ? s_warp[turn ^ 1][lane][0] : 0u);
     unsigned tie_before = __reduce_add_sync(0xffffffffu, lane < warp ? s_warp[turn ^ 1][lane][1] : 0u);
-    if (!(HELD && size == 1))
+    if (size > 1)
         for (int r = 0; r < rank; ++r) {
             stay_before += s_count[turn ^ 1][r][0];
             tie_before += s_count[turn ^ 1][r][1];
         }
     const unsigned below = (1u << lane) - 1u;
-    if (need == n[1]) {  // every tie stays
-        unsigned before = stay_before + tie_before;
-        each([&](int i, uint32_t x) {
+    const bool all_ties = need == n[1];
+    unsigned before = stay_before + tie_before;
+    for (int i = 0; i < per; ++i) {
+        const int t = base + 32 * i;
+        const uint32_t x = HELD ? keys[32 * i + lane] : key_of(t, weight_at(t));
+        if (all_ties) {
             const unsigned m = __ballot_sync(0xffffffffu, x >= found);
-            if (x >= found) kept[before + __popc(m & below)] = base + 32 * i;
+            if (x >= found) kept[before + __popc(m & below)] = t;
             before += __popc(m);
-        });
-    } else {
-        each([&](int i, uint32_t x) {
+        } else {
             const unsigned ms = __ballot_sync(0xffffffffu, x > found), mt = __ballot_sync(0xffffffffu, x == found);
             const unsigned my_tie = tie_before + __popc(mt & below);
             // kept ones before this token: those that stay, and ties up to `need`
-            if (x > found || (x == found && my_tie < need)) kept[stay_before + __popc(ms & below) + min(my_tie, need)] = base + 32 * i;
+            if (x > found || (x == found && my_tie < need)) kept[stay_before + __popc(ms & below) + min(my_tie, need)] = t;
             stay_before += __popc(ms);
             tie_before += __popc(mt);
-        });
+        }
     }
 }
 
@@ -309,14 +321,30 @@ __global__ void __launch_bounds__(128) move_kernel(const EvictArgs a, int pages,
 }  // namespace
 
 cudaError_t launch_evict(const EvictArgs& a, int num_sms, cudaStream_t st) {
-    (void)num_sms;
     if (a.B <= 0) return cudaSuccess;
     const long long most = (long long)a.max_pages * a.ps, rows = (long long)a.B * a.H_kv;
+    // CTAs of a row: with rows enough to fill the SMs, as few as hold it, three on an SM where that is enough; with fewer, up to two CTAs an
+    // SM in all
     unsigned cluster = 1;
-    while (cluster < kMaxCluster && (long long)cluster * kHeld < most) cluster *= 2;
-    const bool held = (long long)cluster * kHeld >= most;
-    cudaError_t e = launch_pdl_cluster(held ? choose_kernel<true> : choose_kernel<false>, dim3((unsigned)(rows * cluster)), dim3(kThreads), 0,
-                                       cluster, st, a);
+    auto holds = [&](int held) { return (long long)cluster * held >= most; };
+    if (rows >= num_sms) {
+        while (cluster < kMaxCluster && !holds(kHeldMany)) cluster *= 2;
+    } else {
+        while (cluster < kMaxCluster && (!holds(kHeld) || (long long)(2 * cluster) * rows <= 2 * num_sms)) cluster *= 2;
+    }
+    const bool held = holds(kHeld);
+    // (a warp's tokens are a multiple of 128)
+    const long long room = ((most + cluster * kWarps - 1) / (cluster * kWarps) + 127) / 128 * 128 * kWarps;
+    const size_t smem = held ? (size_t)room * sizeof(uint32_t) : 0;
+    static std::atomic<bool> known[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && (dev >= 64 || !known[dev].load(std::memory_order_acquire))) {
+        e = cudaFuncSetAttribute(choose_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)((kHeld + 128 * kWarps) * sizeof(uint32_t)));
+        if (e == cudaSuccess && dev < 64) known[dev].store(true, std::memory_order_release);
+    }
+    if (e != cudaSuccess) return e;
+    e = launch_pdl_cluster(held ? choose_kernel<true> : choose_kernel<false>, dim3((unsigned)(rows * cluster)), dim3(kThreads), smem, cluster, st, a);
     if (e != cudaSuccess) return e;
     // no sequence has more than `budget` tokens left
     const int pages = (int)((most < a.budget ? most : a.budget) + a.ps - 1) / a.ps;
