@@ -99,6 +99,7 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const EvictArgs a) {
                 f(x.w);
             }
         } else {
+#pragma unroll 8
             for (int i = 0; i < per; ++i) f(key_of(base + 32 * i, weight_at(base + 32 * i)));
         }
     };

@@ -357,3 +357,84 @@ def test_a_round_with_trees_and_eviction_as_it_is_used(spd):
             stay = kept[b, h].cpu().numpy()
             j = np.arange(budget)
             assert np.array_equal(host(K)[dst[b, j // ps], h, j % ps], keys[stay, h])
+
+
+def test_kv_evict_rows_beyond_shared_memory(spd):
+    """A row that no cluster holds."""
+    evict(spd, np.random.default_rng(4), [400001, 3000], 4096, 4, 500, 1, 64, 64, 0, "ties")
+
+
+@pytest.mark.parametrize("longest", [700, 20011])
+def test_kv_evict_many_rows(spd, longest):
+    """More (sequence, KV head) rows than SMs: one CTA a row, and clusters of two."""
+    rng = np.random.default_rng(longest)
+    evict(spd, rng, [longest, *rng.integers(0, 400, 40)], 150, 2, 30, 4, 64, 32, 0, "usual")
+
+
+def test_kv_weights_update_of_a_long_row(spd):
+    """2^30 - 3 tokens of one page: the weights of the first, of some in the middle, and of the newest, which is fresh."""
+    import torch
+    ps, D, n = 64, 64, (1 << 30) - 3
+    pages = 1 << 24
+    if torch.cuda.mem_get_info()[0] < 20 << 30:
+        pytest.skip("needs 20 GB of device memory")
+    rng = np.random.default_rng(2)
+    dims = spd.dims_of(1, 3, 1, D, ps, pages, 1)
+    K = bf(rng.standard_normal((1, 1, ps, D)))
+    pt = torch.zeros((1, pages), dtype=torch.int32, device="cuda")
+    w = torch.ones((1, 1, pages * ps), device="cuda")
+    q, lse = bf(rng.standard_normal((1, 1, 3, D))), dev(np.array([[[5.0, 6.0, 7.0]]], np.float32))
+    spd.kv_weights_update(dims, 1, q, lse, K, pt, torch.tensor([n], dtype=torch.int32, device="cuda"), w, w_in=w, decay=0.5)
+    assert spd.spd_device_status(clear=True) == 0
+    total, spread = ref.weights(host(q)[0], lse.cpu().numpy()[0].astype(np.float64), host(K)[0, 0], D ** -0.5, ps)
+    got = w[0, 0]
+    for t0 in (0, 1 << 20, (1 << 29) + 64, (1 << 30) - 64):
+        block = host(got[t0: t0 + ps])
+        stop = min(ps, n - t0)
+        fresh = n - 1 - t0
+        check_weights(block, np.ones(ps), 0.5, fresh, stop, total[:stop], spread[:stop], 3, t0)
+    assert got[n:].tolist() == [1.0] * 3
+
+
+def test_caches_past_4_gib(spd):
+    """Pages whose byte offset passes 32 bits: tree verification, append, weights and eviction between the cache's two ends."""
+    import torch
+    rng = np.random.default_rng(40)
+    ps, H, D, T = 64, 8, 128, 5
+    n = (5 << 30) // (H * ps * D * 2)
+    lens, pt, mp, m, K, V = paged(rng, [150, 70], ps, H, D)
+    far = np.where(pt >= 0, n - 1 - pt, -1).astype(np.int32)      # the same pages at the end of a large cache
+    far[:, -1] = [n - 1 - m, n - 2 - m]                          # a spare page each, for what is appended
+    big_K, big_V = (torch.zeros((n, H, ps, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    for p in range(m):
+        big_K[n - 1 - p], big_V[n - 1 - p] = K[p], V[p]
+    q, k, v = (bf(rng.standard_normal((2, T, h, D))) for h in (2 * H, H, H))
+    parents = dev(np.tile(np.array([-1, 0, 0, 1, 2], np.int32), (2, 1)))
+    results = []
+    for cache_K, cache_V, table, pages in ((K, V, pt, m), (big_K, big_V, far, n)):
+        if pages == m:  # with the spare pages and those of the eviction behind the others
+            extra = torch.zeros((6, H, ps, D), dtype=torch.bfloat16, device="cuda")
+            cache_K, cache_V, pages = torch.cat([cache_K, extra]), torch.cat([cache_V, extra]), m + 6
+            table = table.copy()
+            table[:, -1] = [m, m + 1]
+            dst = np.array([[m + 2, m + 3], [m + 4, m + 5]], np.int32)
+        else:
+            dst = np.array([[0, n // 2], [1, n // 2 + 1]], np.int32)
+        dims = spd.dims_of(2, 2 * H, H, D, ps, table.shape[1], pages)
+        dst_table = np.full_like(table, -1)
+        dst_table[:, :2] = dst
+        o, lse = torch.empty_like(q), torch.empty((2, T, 2 * H), device="cuda")
+        d_pt, d_lens = dev(table), dev(lens)
+        spd.tree_verify_attn(dims, T, q, cache_K, cache_V, d_pt, d_lens, k, v, parents, o, spd.workspace(spd.spd_tree_verify_workspace_size(dims, T)), lse=lse)
+        path, count = dev(np.array([[0, 1, 3, -1, -1], [0, 2, -1, -1, -1]], np.int32)), dev(np.array([3, 2], np.int32))
+        summ = torch.zeros((2, H, table.shape[1], 2, D), dtype=torch.bfloat16, device="cuda")
+        new, new2 = (torch.zeros(2, dtype=torch.int32, device="cuda") for _ in range(2))
+        spd.kv_append_path(dims, T, cache_K, cache_V, d_pt, d_lens, k, v, path, count, summ, new)
+        w, w2 = (torch.zeros((2, H, table.shape[1] * ps), device="cuda") for _ in range(2))
+        spd.kv_weights_update(dims, T, q, lse, cache_K, d_pt, new, w, path=path, n_path=count)
+        kept = torch.full((2, H, 100), -1, dtype=torch.int32, device="cuda")
+        spd.kv_evict(dims, 100, 4, 20, cache_K, cache_V, d_pt, new, w, dev(dst_table), kept, w2, summ, new2)
+        assert spd.spd_device_status(clear=True) == 0
+        results.append([o, lse, new, w, kept, w2, new2] + [x[dev(dst.reshape(-1).astype(np.int64))] for x in (cache_K, cache_V)])
+    for x, y in zip(*results):
+        assert torch.equal(x, y)

@@ -507,3 +507,59 @@ def test_tree_verify_attn_with_waits_that_run_out(spd, lens, T, H_q, H_kv, D):
     for got, want in zip(attend(spd, *args), first):
         assert torch.equal(got, want)
     assert spd.spd_device_status(clear=True) == 0
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_tree_verify_attn_of_any_shape(spd, seed):
+    """Heads, nodes, pages, lengths and trees drawn together, several sequences to none."""
+    rng = np.random.default_rng(1000 + seed)
+    H_kv = int(rng.integers(1, 5))
+    G, T, D, ps = int(rng.integers(1, 9)), int(rng.integers(1, 65)), int(rng.choice([64, 128])), int(rng.choice([16, 32, 64]))
+    B = int(rng.integers(1, 7))
+    lens = rng.integers(0, int(rng.choice([20, 300, 900])), B)
+    trees = [ref.random_tree(rng, T, str(rng.choice(["chain", "wide", "random"])), int(rng.integers(0, T + 1))) for _ in range(B)]
+    check_case(spd, *case(spd, rng, lens, T, G * H_kv, H_kv, D, ps, trees, bool(rng.integers(2))), rows=set(rng.integers(0, T, 6).tolist()))
+
+
+def test_tree_verify_attn_on_two_streams_at_once(spd):
+    """Calls that overlap, each with a workspace of its own: the bits of calls by themselves."""
+    import torch
+    rng = np.random.default_rng(12)
+    calls = []
+    for T, D in ((30, 128), (7, 64)):
+        dims, lens, pt, K, V, q, k, v, parents = case(spd, rng, rng.integers(500, 4000, 30), T, 8, 2, D, 16, [ref.random_tree(rng, T) for _ in range(30)])
+        calls.append((dims, T, q, K, V, dev(pt), dev(lens), k, v, dev(parents.astype(np.int32))))
+    want = [attend(spd, *c) for c in calls]
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    out = []
+    for _ in range(4):
+        for c, s in zip(calls, streams):
+            with torch.cuda.stream(s):
+                out.append(attend(spd, *c))
+    torch.cuda.synchronize()
+    for i, got in enumerate(out):
+        for x, y in zip(got, want[i % 2]):
+            assert torch.equal(x, y)
+    assert spd.spd_device_status(clear=True) == 0
+
+
+def test_tree_verify_attn_the_longest_sequence(spd):
+    """2^30 - 5 tokens, all but the last page one and the same: the last token, whose weight is e^40 times the others', decides;
+    what lies behind it is NaN."""
+    import torch
+    ps, D, n = 16, 64, (1 << 30) - 5
+    pages = 1 << 26
+    dims = spd.dims_of(1, 2, 1, D, ps, pages, 2)
+    K, V = torch.zeros((2, 1, ps, D), dtype=torch.bfloat16, device="cuda"), torch.ones((2, 1, ps, D), dtype=torch.bfloat16, device="cuda")
+    last = (n - 1) % ps
+    K[1, 0, last], V[1, 0, last] = 5.0, 5.0
+    K[1, 0, last + 1:], V[1, 0, last + 1:] = float("nan"), float("inf")
+    pt = torch.zeros((1, pages), dtype=torch.int32, device="cuda")
+    pt[0, -1] = 1
+    q = torch.ones((1, 2, 2, D), dtype=torch.bfloat16, device="cuda")   # logits 40 (scale 1 / 8) and 0
+    k, v = torch.zeros((1, 2, 1, D), dtype=torch.bfloat16, device="cuda"), torch.zeros((1, 2, 1, D), dtype=torch.bfloat16, device="cuda")
+    o, lse = attend(spd, dims, 2, q, K, V, pt, torch.tensor([n], dtype=torch.int32, device="cuda"), k, v, dev(np.array([[-1, 0]], np.int32)))
+    assert spd.spd_device_status(clear=True) == 0
+    # the others' share of the weight is 2^30 e^-40 = 4.6e-9
+    assert np.abs(host(o) - 5.0).max() <= 5 * 2.0 ** -8 and np.abs(host(lse) - 40.0).max() <= 40 * 2.0 ** -20
