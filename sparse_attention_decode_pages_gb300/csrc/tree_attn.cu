@@ -83,15 +83,24 @@ struct Cut {
 constexpr int kSlotRows = 256;
 __host__ __device__ constexpr size_t slot_bytes(int D) { return (size_t)kSlotRows * (D * 4 + 8); }
 
+// What follows from T, G and the page size, worked out once by the host (a division costs a CTA's start more than it looks).
 struct Shape {
-    int G, tpt, row_tiles, pairs;  // heads of a group, nodes of a row tile, row tiles, units of a (sequence, KV head)
+    int G, tpt, row_tiles, pairs;  // heads of a group, nodes of a row tile, row tiles (up to 4), units of a (sequence, KV head) (1 or 2)
+    int lg_ps;                     // log2 of the page size
+    __device__ __forceinline__ int pages(int len, int max_pages) const {  // as seq_pages
+        if (len < 0 || (long long)len > (long long)max_pages << lg_ps) return -1;
+        return (int)(((unsigned)len + (1u << lg_ps) - 1) >> lg_ps);
+    }
+    __device__ __forceinline__ int head(int sub) const { return sub >> (pairs - 1); }
+    __device__ __forceinline__ int first_tile(int sub) const { return 2 * (sub & (pairs - 1)); }
 };
-__host__ __device__ inline Shape shape_of(int T, int G) {
+inline Shape shape_of(int T, int G, int ps) {
     Shape s;
     s.G = G;
-    s.tpt = min(kRows / G, T);
+    s.tpt = kRows / G < T ? kRows / G : T;
     s.row_tiles = (T + s.tpt - 1) / s.tpt;
     s.pairs = (s.row_tiles + 1) / 2;
+    s.lg_ps = ps == 16 ? 4 : ps == 32 ? 5 : 6;
     return s;
 }
 
@@ -114,12 +123,12 @@ struct Walk {
     int b, sub, t0, len, nt;
     bool bad;
     long long left;  // tiles
-    __device__ __forceinline__ void look(const TreeAttnArgs& a, int raw) {
-        bad = seq_pages(raw, a.ps, a.max_pages) < 0;
+    __device__ __forceinline__ void look(const TreeAttnArgs& a, const Shape& sh, int raw) {
+        bad = sh.pages(raw, a.max_pages) < 0;
         len = bad ? 0 : raw;
         nt = (len + kTokens - 1) / kTokens + 1;
     }
-    __device__ __forceinline__ bool next(const TreeAttnArgs& a, int subs, Piece& p) {
+    __device__ __forceinline__ bool next(const TreeAttnArgs& a, const Shape& sh, Piece& p) {
         if (left <= 0) return false;
         p.b = b;
         p.sub = sub;
@@ -130,9 +139,9 @@ struct Walk {
         p.t1 = (int)min((long long)nt, t0 + left);
         left -= p.t1 - p.t0;
         t0 = 0;
-        if (++sub == subs) {
+        if (++sub == a.H_kv * sh.pairs) {
             sub = 0;
-            if (left > 0) look(a, a.seq_lens[++b]);
+            if (left > 0) look(a, sh, a.seq_lens[++b]);
         }
         return true;
     }
@@ -158,7 +167,7 @@ struct Shares {
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    tree_kernel(const TreeAttnArgs a, const __grid_constant__ TreeMaps maps, const bool few) {
+    tree_kernel(const TreeAttnArgs a, const __grid_constant__ TreeMaps maps, const Shape sh, const bool few) {
     using C = Cfg<D>;
     constexpr int STAGES = C::STAGES;
     extern __shared__ uint8_t smem_raw[];
@@ -180,7 +189,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint16_t* info = reinterpret_cast<uint16_t*>(smem + C::OFF_INFO);
     float2* s_ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-    const Shape sh = shape_of(a.T, a.H_q / a.H_kv);
     const int subs = a.H_kv * sh.pairs;
     const float NEG_INF = __int_as_float(0xff800000);
     const unsigned long long drain_ns = a.wait_ns > kDefaultWaitNs ? a.wait_ns : kDefaultWaitNs;
@@ -219,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // This CTA's share: where it begins (unit and tile) and how many tiles, in shared memory (what every role would carry in
     // registers otherwise costs the softmax its own).
     {
-        auto tiles_of = [&](int len) { return seq_pages(len, a.ps, a.max_pages) < 0 ? 1 : (len + kTokens - 1) / kTokens + 1; };
+        auto tiles_of = [&](int len) { return sh.pages(len, a.max_pages) < 0 ? 1 : (len + kTokens - 1) / kTokens + 1; };
         if (warp == 9) tmem_alloc(&s_tmem, C::COLUMNS);
         if (few) {
             // A unit's tiles are cut into equal parts, about as many as its share of all tiles, so that no CTA goes from
@@ -307,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         w.sub = s_share.sub;
         w.t0 = s_share.t0;
         w.left = s_share.left;
-        w.look(a, s_share.len);
+        w.look(a, sh, s_share.len);
         float* part_o = reinterpret_cast<float*>(static_cast<char*>(a.ws) + ((size_t)gridDim.x * sizeof(Cut) + 255) / 256 * 256);
         float2* part_ml = reinterpret_cast<float2*>(part_o + (size_t)2 * gridDim.x * kSlotRows * D);
         const uint32_t tmem = s_tmem;
@@ -341,8 +349,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             int tree_b = -1;
             unsigned long long tree[2] = {0, 0};
             Piece p;
-            while (ok && w.next(a, subs, p)) {
-                const int h = p.sub / sh.pairs, mt = 2 * (p.sub - h * sh.pairs);
+            while (ok && w.next(a, sh, p)) {
+                const int h = sh.head(p.sub), mt = sh.first_tile(p.sub);
                 const bool two = mt + 1 < sh.row_tiles;
                 const int n = p.t1 - p.t0, step = two ? 1 : 2;
                 ++piece;
@@ -545,8 +553,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             other_regs();
             // ======================================================== copies: keys and queries, or values
             const bool value = warp == 11;
-            const int ppt = kTokens / a.ps, lg_ps = __ffs(a.ps) - 1;  // pages of a tile
-            const int per_batch = 32 / ppt;                          // tiles of 32 page-table entries
+            const int lg_ps = sh.lg_ps, ppt = kTokens >> lg_ps;  // pages of a tile
+            const int lg_batch = lg_ps - 2;                      // 32 page-table entries are 2^lg_batch tiles
             const int oob = (int)max(1LL, a.num_phys * a.H_kv);      // a row of pages that is not there
             const CUtensorMap* map = value ? &maps.v : &maps.k;
             const CUtensorMap* map_edge = value ? &maps.v_edge : &maps.k_edge;
@@ -555,8 +563,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             int base = 0, n_info = 0;                            // items, and tiles, of the pieces before
             bool ok = true, q_asked = false;
             Piece p;
-            while (ok && w.next(a, subs, p)) {
-                const int h = p.sub / sh.pairs, mt = 2 * (p.sub - h * sh.pairs);
+            while (ok && w.next(a, sh, p)) {
+                const int h = sh.head(p.sub), mt = sh.first_tile(p.sub);
                 const bool two = mt + 1 < sh.row_tiles;
                 const int n = p.t1 - p.t0;
                 const int P = (p.len + a.ps - 1) >> lg_ps;
@@ -573,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     return phys;
                 };
-                int batch = p.t0 / per_batch;
+                int batch = p.t0 >> lg_batch;
                 int ids = ask(batch), nxt = ask(batch + 1);
                 if (!value) {
                     if (p.bad && p.sub == 0 && lane == 0) raise_status(a.status, SPD_DEV_BAD_LEN);
@@ -599,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint8_t* dst = smem + C::OFF_RING + slot * C::TILE;
                     uint64_t* bar = full + slot;
                     if (t < p.nt - 1) {
-                        if (t / per_batch > batch) {
+                        if (t >> lg_batch > batch) {
                             ++batch;
                             ids = checked(batch, nxt);
                             nxt = ask(batch + 1);
@@ -718,8 +726,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return ok;
             };
             Piece p;
-            while (ok && w.next(a, subs, p)) {
-                const int h = p.sub / sh.pairs, mt = 2 * (p.sub - h * sh.pairs);
+            while (ok && w.next(a, sh, p)) {
+                const int h = sh.head(p.sub), mt = sh.first_tile(p.sub);
                 const bool two = mt + 1 < sh.row_tiles;
                 const int n = p.t1 - p.t0;
                 if (!wait(q_full, q_parity)) break;
@@ -796,7 +804,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     Piece p;
                     long long at = s_share.at;
                     const Shares shares(s_share.total, (int)min((long long)gridDim.x, s_share.total));
-                    while (x.next(a, subs, p)) {
+                    while (x.next(a, sh, p)) {
                         if (p.t0 == 0 && p.t1 < p.nt) {
                             int c = blockIdx.x;
                             while (shares.begin(c + 1) < at + p.nt) ++c;
@@ -814,7 +822,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t v_parity = 0;  // of each slot: bits
             int base = 0, piece = 0;
             Piece p;
-            while (w.next(a, subs, p)) {
+            while (w.next(a, sh, p)) {
                 base += 2 * (p.t1 - p.t0);
                 if (p.t1 == p.nt) {
                     const int slot = (base - 1) % STAGES;
@@ -865,9 +873,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // for at once.
 constexpr int kJoinChannels = 8, kJoinAhead = 8;
 template <int D>
-__global__ void __launch_bounds__(kSlotRows) join_kernel(const TreeAttnArgs a, int ctas) {
+__global__ void __launch_bounds__(kSlotRows) join_kernel(const TreeAttnArgs a, const Shape sh, int ctas) {
     const float NEG_INF = __int_as_float(0xff800000);
-    const Shape sh = shape_of(a.T, a.H_q / a.H_kv);
     const float* part_o = reinterpret_cast<const float*>(static_cast<const char*>(a.ws) + ((size_t)ctas * sizeof(Cut) + 255) / 256 * 256);
     const float2* part_ml = reinterpret_cast<const float2*>(part_o + (size_t)2 * ctas * kSlotRows * D) + threadIdx.x;
     const int group = blockIdx.x % (D / kJoinChannels);
@@ -876,7 +883,7 @@ __global__ void __launch_bounds__(kSlotRows) join_kernel(const TreeAttnArgs a, i
     pdl_trigger();
     const Cut cut = reinterpret_cast<const Cut*>(a.ws)[blockIdx.x / (D / kJoinChannels)];
     if (cut.pieces == 0) return;
-    const int h = cut.sub / sh.pairs, mt = 2 * (cut.sub - h * sh.pairs);
+    const int h = sh.head(cut.sub), mt = sh.first_tile(cut.sub);
     const int row = threadIdx.x & (kRows - 1), node = (mt + threadIdx.x / kRows) * sh.tpt + row / sh.G;
     if (mt + (int)threadIdx.x / kRows >= sh.row_tiles || row >= sh.tpt * sh.G || node >= a.T) return;
     float r = NEG_INF, total = 0.f;
@@ -932,24 +939,25 @@ cudaError_t launch(const TreeAttnArgs& a, const TreeMaps& m, int ctas, cudaStrea
         if (e != cudaSuccess) return e;
         if (dev < 64) known[dev].store(true, std::memory_order_release);
     }
-    const long long units = (long long)a.B * a.H_kv * shape_of(a.T, a.H_q / a.H_kv).pairs;
+    const Shape sh = shape_of(a.T, a.H_q / a.H_kv, a.ps);
+    const long long units = (long long)a.B * a.H_kv * sh.pairs;
     const bool few = a.B <= 32 && units * kFewUnits <= ctas;
-    e = launch_pdl(tree_kernel<D>, dim3((unsigned)ctas), dim3(kThreads), Cfg<D>::SMEM, st, a, m, few);
+    e = launch_pdl(tree_kernel<D>, dim3((unsigned)ctas), dim3(kThreads), Cfg<D>::SMEM, st, a, m, sh, few);
     if (e != cudaSuccess) return e;
     const long long cuts = few ? units : ctas;
-    return launch_pdl(join_kernel<D>, dim3((unsigned)(cuts * (D / kJoinChannels))), dim3(kSlotRows), 0, st, a, ctas);
+    return launch_pdl(join_kernel<D>, dim3((unsigned)(cuts * (D / kJoinChannels))), dim3(kSlotRows), 0, st, a, sh, ctas);
 }
 
 // CTAs: one an SM, or as many as there can be tiles.
 int grid_of(int B, int H_kv, int G, int T, int max_pages, int ps, int num_sms) {
     const long long most = ((long long)max_pages * ps + kTokens - 1) / kTokens + 1;
-    const long long tiles = most * B * H_kv * shape_of(T, G).pairs;
+    const long long tiles = most * B * H_kv * shape_of(T, G, ps).pairs;
     return (int)(tiles < num_sms ? tiles : num_sms);
 }
 
 }  // namespace
 
-int tree_nodes_per_tile(int T, int G) { return shape_of(T, G).tpt; }
+int tree_nodes_per_tile(int T, int G) { return shape_of(T, G, 16).tpt; }
 
 size_t tree_attn_ws(int D, int num_sms) {
     return ((size_t)num_sms * sizeof(Cut) + 255) / 256 * 256 + 2 * num_sms * slot_bytes(D);
