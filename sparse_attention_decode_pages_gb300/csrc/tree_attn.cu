@@ -683,15 +683,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             auto wait_item = [&](int item) { return wait(full + item % STAGES, (uint32_t)(item / STAGES) & 1u); };
             // S of stream s with row tile q and the keys of an item
+            // (Descriptors count in 16 bytes: the steps' are sums.  Loops rolled but for two steps: unrolled at every place, what they share is kept
+            // in registers that the softmax then spills, 571 us against 565.)
             auto keys = [&](int s, int q, int item, bool tree) {
                 tmem_fence_after();
                 if (elect_one()) {
-                    const uint32_t k = ring_smem + item % STAGES * C::TILE;
-                    const uint32_t half = tree ? C::HALF : 1024, group = tree ? 1024 : C::GROUP;
-#pragma unroll
+                    const uint32_t half = (tree ? C::HALF : 1024) >> 4;
+                    const uint64_t dq = umma_desc(q_smem + q * C::TILE, 0, 1024, kSwizzle128);
+                    const uint64_t dk = umma_desc(ring_smem + item % STAGES * C::TILE, 0, tree ? 1024 : C::GROUP, kSwizzle128);
+#pragma unroll (D / 64)
                     for (int i = 0; i < D / 16; ++i)
-                        umma_f16_ss(tmem + C::COL_S + s * 128, umma_desc(q_smem + q * C::TILE + (i >> 2) * C::HALF + (i & 3) * 32, 0, 1024, kSwizzle128),
-                                    umma_desc(k + (i >> 2) * half + (i & 3) * 32, 0, group, kSwizzle128), kIdescS, i > 0);
+                        umma_f16_ss(tmem + C::COL_S + s * 128, dq + (((i >> 2) * C::HALF + (i & 3) * 32) >> 4), dk + ((i >> 2) * half + (i & 3) * 2),
+                                    kIdescS, i > 0);
                     umma_commit(s_full + s);
                     mbar_arrive(s_full + s);
                 }
@@ -700,12 +703,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto values = [&](int s, int item, bool first, bool tree) {
                 tmem_fence_after();
                 if (elect_one()) {
-                    const uint32_t v = ring_smem + item % STAGES * C::TILE;
+                    const uint32_t group = tree ? 1024 : C::GROUP;
+                    const uint64_t dv = umma_desc(ring_smem + item % STAGES * C::TILE, tree ? C::HALF : 1024, group, kSwizzle128);
                     const int steps = tree ? 4 : 8;
-                    const uint32_t half = tree ? C::HALF : 1024, group = tree ? 1024 : C::GROUP;
+#pragma unroll 2
                     for (int i = 0; i < steps; ++i)
-                        umma_f16_ts(tmem + C::COL_O + s * 128, tmem + C::COL_S + s * 128 + 8 * i,
-                                    umma_desc(v + i * 2 * group, half, group, kSwizzle128), kIdescO, !first || i > 0);
+                        umma_f16_ts(tmem + C::COL_O + s * 128, tmem + C::COL_S + s * 128 + 8 * i, dv + i * (2 * group >> 4), kIdescO, !first || i > 0);
                 }
                 __syncwarp();
             };
