@@ -284,7 +284,8 @@ struct WeightsArgs {
     unsigned* status;
     unsigned long long wait_ns;
 };
-cudaError_t launch_weights_update(const WeightsArgs& a, int num_sms, cudaStream_t st);
+// map: boxes of 16 rows of K.
+cudaError_t launch_weights_update(const WeightsArgs& a, const CUtensorMap& map, int num_sms, cudaStream_t st);
 
 struct EvictArgs {
     uint16_t* K;

@@ -92,15 +92,15 @@ EncodeTiledFn encode_fn(spd_status* st) {
 
 // 3-D view of a paged K or V cache: x = 64 channels (128 bytes), y = rows
 // (num_phys * H_kv * ps of D bf16, stride 2D bytes), z = the D / 64 halves of a
-// row (stride 128 bytes).  One box = a page's ps rows of one KV head, laid out
-// in shared memory as [half][row][64] with the 128-byte swizzle.
-spd_status kv_map(CUtensorMap* m, const void* base, const spd_dims* d) {
+// row (stride 128 bytes).  One box = a page's ps rows of one KV head (or `rows` of
+// them), laid out in shared memory as [half][row][64] with the 128-byte swizzle.
+spd_status kv_map(CUtensorMap* m, const void* base, const spd_dims* d, int rows = 0) {
     spd_status st = SPD_OK;
     EncodeTiledFn fn = encode_fn(&st);
     if (!fn) return st;
     cuuint64_t gdim[3] = {64, (cuuint64_t)d->num_phys_pages * d->H_kv * d->page_size, (cuuint64_t)d->D / 64};
     cuuint64_t gstride[2] = {(cuuint64_t)d->D * 2, 128};
-    cuuint32_t box[3] = {64, (cuuint32_t)d->page_size, (cuuint32_t)d->D / 64};
+    cuuint32_t box[3] = {64, (cuuint32_t)(rows ? rows : d->page_size), (cuuint32_t)d->D / 64};
     cuuint32_t estride[3] = {1, 1, 1};
     CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), gdim, gstride, box, estride,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -1481,7 +1481,12 @@ SPD_API spd_status kv_weights_update(const spd_dims* dims, int32_t T, const spd_
     a.w_out = w_out;
     a.status = d->status;
     a.wait_ns = wait_limit_ns();
-    cudaError_t e = launch_weights_update(a, d->sms, static_cast<cudaStream_t>(stream));
+    spd_dims k = *dims;
+    if (k.num_phys_pages < 1) k.num_phys_pages = 1;  // (a view of nothing is none; no page of it is read)
+    CUtensorMap map;
+    st = kv_map(&map, K, &k, 16);
+    if (st != SPD_OK) return st;
+    cudaError_t e = launch_weights_update(a, map, d->sms, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? SPD_OK : cuda_fail(e, "kv_weights_update launch");
 }
 

@@ -16,7 +16,7 @@
 //
 // The softmax goes by a reference that follows the row's maximum only when that has grown by 2^8 beyond it, so O
 // is rarely rescaled; sums are fp32, the weights that multiply V are rounded to bf16 (V's type,
-// as the products want them), 2^-9 of a weight at most and of either sign.
+// as the products want them), 2^-8 of a weight at most and of either sign.
 //
 // One CTA an SM: two warpgroups for the softmax, and a warp each for the keys' copies, the values' copies, the products
 // and the nodes' values.  A page's keys or values of a KV head are one TMA box.  A sequence that ends inside a page has that page

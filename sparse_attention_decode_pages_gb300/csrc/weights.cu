@@ -7,11 +7,12 @@
 // bounds it (the values are not needed).
 //
 // A CTA takes a run of tokens of one (sequence, KV head), a warp 16 of them at a time: 16 tokens' keys of a page
-// are one piece of memory, brought to a ring of the warp's own by a bulk copy, two of them in flight, 24 warps an SM (64 sequences
-// of 8K-16K tokens, paths of up to 7 nodes: 292 us, 5.7 TB/s; three in flight of 16 warps 295; by loads to registers 399).
-// They are the A operand of mma.m16n8k16: lane (g, c) = (lane / 4, lane % 4) reads 16 bytes, channels
-// 32 i + 8 c ..., of tokens g and g + 8; the contraction's order of channels that this gives is the one in which the
-// queries, the B operand, are read.  Eight query rows at a time the scores of the 16 tokens are weighed and summed
+// come to a ring of the warp's own as one TMA box, two of them in flight, 24 warps an SM (64 sequences
+// of 8K-16K tokens, paths of up to 7 nodes: 260 us, 94 % of the measured copy peak; as plain rows of 256 bytes, two on the same
+// banks, 300; by loads to registers 399).
+// They are the A operand of mma.m16n8k16: lane (g, c) = (lane / 4, lane % 4) reads 16-byte pieces 2 c and 2 c + 1 of
+// 64 channels of tokens g and g + 8, which with the box's 128-byte swizzle lie on different banks; the contraction's order of
+// channels that this gives is the one in which the queries, the B operand, are read.  Eight query rows at a time the scores of the 16 tokens are weighed and summed
 // in the lanes, over the four lanes of a token at the end.
 #include <atomic>
 
@@ -27,10 +28,11 @@ constexpr size_t kMostSmem = 226 * 1024;
 constexpr int kLeastRun = 16 * kWarps, kMostRun = 32 * kLeastRun;  // tokens of a CTA: up to 32 tiles a warp, one a lane
 
 template <int D, bool SEL>
-__global__ void __launch_bounds__(kThreads, 3) weights_kernel(const WeightsArgs a, int rows_padded, int runs, int run_tokens) {
+__global__ void __launch_bounds__(kThreads, 3) weights_kernel(const WeightsArgs a, const __grid_constant__ CUtensorMap map, int rows_padded, int runs, int run_tokens) {
     constexpr int TILE = 16 * D * 2;
     constexpr int QROW = D * 2 + 16;  // bytes of a query row in shared memory: rows on different banks
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
     uint8_t* s_q = smem + kWarps * kStages * TILE;                       // [rows_padded][QROW]
     float* s_lse = reinterpret_cast<float*>(s_q + rows_padded * QROW);   // lse * log2(e); +inf: adds nothing
     int* s_lim = reinterpret_cast<int*>(s_lse + rows_padded);            // the last position that a row sees
@@ -111,7 +113,7 @@ __global__ void __launch_bounds__(kThreads, 3) weights_kernel(const WeightsArgs 
         if (lane == 0) {
             const int at = (t0 + (warp + kWarps * i) * 16) % a.ps;
             mbar_arrive_expect_tx(&s_full[warp][slot], TILE);
-            bulk_load(ring + slot * TILE, a.K + (((long long)phys * a.H_kv + h) * a.ps + at) * D, TILE, &s_full[warp][slot]);
+            tma_load_3d(ring + slot * TILE, &map, 0, (phys * a.H_kv + h) * a.ps + at, 0, &s_full[warp][slot]);
         }
     };
     unsigned todo = there;  // tiles to ask for
@@ -151,10 +153,20 @@ __global__ void __launch_bounds__(kThreads, 3) weights_kernel(const WeightsArgs 
         __shared__ unsigned s_there[kWarps];
         if (lane == 0) s_there[warp] = there;
         __syncthreads();
-        for (int i = tid; i < min(run_tokens, len - t0); i += kThreads) {
-            const int tile = i >> 4;
-            if (!(s_there[tile & (kWarps - 1)] >> (tile / kWarps) & 1u))
-                a.w_out[wrow + i] = a.w_in && t0 + i < fresh ? a.decay * a.w_in[wrow + i] : 0.f;
+        const int end = min(run_tokens, len - t0);
+        constexpr int kAhead = 8;  // (w_in may be w_out: loads do not move before stores by themselves)
+        for (int i0 = tid; i0 < end; i0 += kAhead * kThreads) {
+            float w[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int i = i0 + k * kThreads;
+                w[k] = a.w_in && i < end && t0 + i < fresh ? a.w_in[wrow + i] : 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int i = i0 + k * kThreads, tile = i >> 4;
+                if (i < end && !(s_there[tile & (kWarps - 1)] >> (tile / kWarps) & 1u)) a.w_out[wrow + i] = a.decay * w[k];
+            }
         }
     }
     // lane i < 16: the old weight of token i of a tile, asked for a tile ahead
@@ -176,11 +188,11 @@ __global__ void __launch_bounds__(kThreads, 3) weights_kernel(const WeightsArgs 
             if (!ok) break;
             there &= ~(1u << i);
             uint4 k[D / 32][2];
-            const uint8_t* src = ring + slot * TILE + g * (D * 2) + c * 16;
+            const uint8_t* src = ring + slot * TILE;
 #pragma unroll
             for (int x = 0; x < D / 32; ++x) {
-                k[x][0] = *reinterpret_cast<const uint4*>(src + x * 64);
-                k[x][1] = *reinterpret_cast<const uint4*>(src + x * 64 + 8 * D * 2);
+                k[x][0] = *reinterpret_cast<const uint4*>(src + (x >> 1) * 2048 + swz128(g, 2 * c + (x & 1)));
+                k[x][1] = *reinterpret_cast<const uint4*>(src + (x >> 1) * 2048 + 1024 + swz128(g, 2 * c + (x & 1)));
             }
             __syncwarp();  // the tile has been read
             ask_next(slot);
@@ -193,10 +205,10 @@ __global__ void __launch_bounds__(kThreads, 3) weights_kernel(const WeightsArgs 
             const bool all = t0 + at + 15 <= fresh;  // every row sees every token
             for (int j = 0; j < groups; ++j) {
                 float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};  // (two chains of products)
-                const uint8_t* q = s_q + (j * 8 + g) * QROW + c * 16;
+                const uint8_t* q = s_q + (j * 8 + g) * QROW + c * 32;
 #pragma unroll
                 for (int x = 0; x < D / 32; ++x) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(q + x * 64);
+                    const uint4 v = *reinterpret_cast<const uint4*>(q + (x >> 1) * 128 + (x & 1) * 16);
                     const uint32_t a0[4] = {k[x][0].x, k[x][1].x, k[x][0].y, k[x][1].y};
                     const uint32_t a1[4] = {k[x][0].z, k[x][1].z, k[x][0].w, k[x][1].w};
                     mma_bf16(s[0], a0, v.x, v.y);
@@ -238,11 +250,11 @@ __global__ void __launch_bounds__(kThreads, 3) weights_kernel(const WeightsArgs 
 }
 
 template <int D>
-cudaError_t launch(const WeightsArgs& a, int num_sms, cudaStream_t st) {
+cudaError_t launch(const WeightsArgs& a, const CUtensorMap& map, int num_sms, cudaStream_t st) {
     static std::atomic<bool> known[64][2];
     const int padded = (a.T * (a.H_q / a.H_kv) + 7) / 8 * 8;
-    const size_t smem = (size_t)kWarps * kStages * 16 * D * 2 + (size_t)padded * (D * 2 + 16 + 8);
-    static_assert(kWarps * kStages * 16 * D * 2 + 8 * kTreeMax * (D * 2 + 16 + 8) <= kMostSmem, "512 query rows fit");
+    const size_t smem = 1024 + (size_t)kWarps * kStages * 16 * D * 2 + (size_t)padded * (D * 2 + 16 + 8);
+    static_assert(1024 + kWarps * kStages * 16 * D * 2 + 8 * kTreeMax * (D * 2 + 16 + 8) <= kMostSmem, "512 query rows fit");
     auto* kern = a.sel ? weights_kernel<D, true> : weights_kernel<D, false>;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -258,14 +270,14 @@ cudaError_t launch(const WeightsArgs& a, int num_sms, cudaStream_t st) {
     // two rounds of two CTAs an SM, or more (8 sequences of 2K-4K tokens, 7 nodes: 21.8 us; for four rounds 27.6; 64 of 8K-16K: the same)
     while (run > kLeastRun && rows * runs_of(run) < 4 * num_sms) run /= 2;
     const long long runs = runs_of(run);
-    return launch_pdl(kern, dim3((unsigned)(rows * runs)), dim3(kThreads), smem, st, a, padded, (int)runs, run);
+    return launch_pdl(kern, dim3((unsigned)(rows * runs)), dim3(kThreads), smem, st, a, map, padded, (int)runs, run);
 }
 
 }  // namespace
 
-cudaError_t launch_weights_update(const WeightsArgs& a, int num_sms, cudaStream_t st) {
+cudaError_t launch_weights_update(const WeightsArgs& a, const CUtensorMap& map, int num_sms, cudaStream_t st) {
     if (a.B <= 0) return cudaSuccess;
-    return a.D == 128 ? launch<128>(a, num_sms, st) : launch<64>(a, num_sms, st);
+    return a.D == 128 ? launch<128>(a, map, num_sms, st) : launch<64>(a, map, num_sms, st);
 }
 
 }  // namespace spd
