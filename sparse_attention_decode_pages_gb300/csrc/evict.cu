@@ -243,7 +243,6 @@ __global__ void __launch_bounds__(128) move_kernel(const EvictArgs a, int pages,
     constexpr int ACC = 16 / RPI;                    // accesses for 16 tokens
     const int lane = threadIdx.x & 31;
     const long long item = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-    pdl_wait();
     pdl_trigger();
     if (item >= items) return;
     const int page = (int)(item % pages);
@@ -350,7 +349,13 @@ cudaError_t launch_evict(const EvictArgs& a, int num_sms, cudaStream_t st) {
     // no sequence has more than `budget` tokens left
     const int pages = (int)((most < a.budget ? most : a.budget) + a.ps - 1) / a.ps;
     const long long items = rows * pages;
-    return launch_pdl(a.D == 128 ? move_kernel<128> : move_kernel<64>, dim3((unsigned)((items + 3) / 4)), dim3(128), 0, st, a, pages, items);
+    // An ordinary launch: the rows in flight need the L1 that an SM with the choice's shared memory gives back only once it is empty
+    // (64 sequences of 8K-16K tokens: 413 us; 483 with CTAs that are there early).
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((items + 3) / 4));
+    cfg.blockDim = dim3(128);
+    cfg.stream = st;
+    return cudaLaunchKernelEx(&cfg, a.D == 128 ? move_kernel<128> : move_kernel<64>, a, pages, items);
 }
 
 }  // namespace spd
