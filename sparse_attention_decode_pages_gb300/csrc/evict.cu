@@ -243,6 +243,7 @@ __global__ void __launch_bounds__(128) move_kernel(const EvictArgs a, int pages,
     constexpr int ACC = 16 / RPI;                    // accesses for 16 tokens
     const int lane = threadIdx.x & 31;
     const long long item = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+    pdl_wait();
     pdl_trigger();
     if (item >= items) return;
     const int page = (int)(item % pages);
@@ -349,13 +350,16 @@ cudaError_t launch_evict(const EvictArgs& a, int num_sms, cudaStream_t st) {
     // no sequence has more than `budget` tokens left
     const int pages = (int)((most < a.budget ? most : a.budget) + a.ps - 1) / a.ps;
     const long long items = rows * pages;
-    // An ordinary launch: the rows in flight need the L1 that an SM with the choice's shared memory gives back only once it is empty
-    // (64 sequences of 8K-16K tokens: 413 us; 483 with CTAs that are there early).
+    const dim3 grid((unsigned)((items + 3) / 4));
+    auto move = a.D == 128 ? move_kernel<128> : move_kernel<64>;
+    if (rows < num_sms) return launch_pdl(move, grid, dim3(128), 0, st, a, pages, items);
+    // Where the choice fills the SMs, an ordinary launch: the rows in flight need the L1 that an SM gives back only once it has no
+    // shared memory in use (64 sequences of 8K-16K tokens: 413 us; 483 with CTAs that are there early; 8 rows of 65,521: @ us, @)
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((items + 3) / 4));
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(128);
     cfg.stream = st;
-    return cudaLaunchKernelEx(&cfg, a.D == 128 ? move_kernel<128> : move_kernel<64>, a, pages, items);
+    return cudaLaunchKernelEx(&cfg, move, a, pages, items);
 }
 
 }  // namespace spd
