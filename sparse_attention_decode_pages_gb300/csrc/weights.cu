@@ -13,7 +13,8 @@
 // They are the A operand of mma.m16n8k16: lane (g, c) = (lane / 4, lane % 4) reads 16-byte pieces 2 c and 2 c + 1 of
 // 64 channels of tokens g and g + 8, which with the box's 128-byte swizzle lie on different banks; the contraction's order of
 // channels that this gives is the one in which the queries, the B operand, are read.  Eight query rows at a time the scores of the 16 tokens are weighed and summed
-// in the lanes, over the four lanes of a token at the end.
+// in the lanes, over the four lanes of a token at the end.  (At the memory's rate with mma.sync, so nothing would be won by the
+// products in tensor memory, whose 128 rows a query tile seldom fills.)
 #include <atomic>
 
 #include "common.cuh"
@@ -267,7 +268,8 @@ cudaError_t launch(const WeightsArgs& a, const CUtensorMap& map, int num_sms, cu
     const long long most = (long long)a.max_pages * a.ps, rows = (long long)a.B * a.H_kv;
     auto runs_of = [&](int run) { return (most + run - 1) / run; };
     int run = kMostRun;
-    // two rounds of two CTAs an SM, or more (8 sequences of 2K-4K tokens, 7 nodes: 21.8 us; for four rounds 27.6; 64 of 8K-16K: the same)
+    // two rounds of two CTAs an SM, or more (8 sequences of 2K-4K tokens, 7 nodes: 17.2 us; as plain rows 21.2, for four
+    // rounds 27.6; 64 of 8K-16K: the same)
     while (run > kLeastRun && rows * runs_of(run) < 4 * num_sms) run /= 2;
     const long long runs = runs_of(run);
     return launch_pdl(kern, dim3((unsigned)(rows * runs)), dim3(kThreads), smem, st, a, map, padded, (int)runs, run);
