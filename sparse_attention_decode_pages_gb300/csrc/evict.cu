@@ -2,13 +2,13 @@
 //
 // Two kernels.  The first chooses: of a (sequence, KV head)'s tokens the first n_sink, the newest n_recent, and the
 // others of the largest weights.  A weight becomes a 32-bit key in the order of the numbers (above all numbers for the
-// tokens that always stay); the largest key that `budget` tokens reach is found two bits at a time, from the highest, by counting
-// the keys that reach each of three candidates, until few keys are left in the range; those go on alone, one a thread, a bit and
-// a barrier that counts at a time.  Tokens with a larger key stay, and of those with that very key the lowest positions.  A warp
+// tokens that always stay); the largest key that `budget` tokens reach is found by counting, as the keys come in, those with each
+// of the 2,048 values of their upper 11 bits, then two bits at a time by counting those that reach each of three candidates, until
+// few keys are left in the range; those go on alone, one a thread, a bit and a barrier that counts at a time.  Tokens with a larger key stay, and of those with that very key the lowest positions.  A warp
 // has consecutive tokens, so one scan of the warps' counts and ballots give every kept token its place.
 // What bounds it is a count's latency: three CTAs an SM where rows are many, clusters of up to eight CTAs a row, their counts joined
-// through distributed shared memory, where rows are few or long (the choice for 512 rows of 8K-16K tokens: 52 us; keys in
-// registers, one CTA of 1,024 threads an SM: 89; 8 rows of 65,521: 23 us).  The keys stay in shared memory; rows beyond
+// through distributed shared memory, where rows are few or long (the choice for 512 rows of 8K-16K tokens: 33 us, 8 rows of 65,521:
+// 12; without the count of the upper bits 52 and 21, with keys in registers, one CTA of 1,024 threads an SM, 89 and 32).  The keys stay in shared memory; rows beyond
 // 8 x 49,152 tokens are read anew for each count.
 //
 // The second moves: a warp takes a new page of a KV head, 16 tokens at a time, all their keys' and values' rows in flight at
@@ -28,8 +28,10 @@ namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kHeld = 49152, kHeldMany = 18432;  // tokens that a CTA holds: alone on an SM, and three on an SM
+constexpr int kHeld = 49152, kHeldMany = 16384;  // tokens that a CTA holds: alone on an SM, and three on an SM
 constexpr int kFew = kThreads;                   // keys that one CTA goes on with, one a thread
+constexpr int kBinShift = 21, kBins = 1 << (32 - kBinShift);  // of the first count: keys' sign, exponent and two bits
+static_assert(kBins == 4 * kThreads, "four bins a thread");
 
 // Larger weight, larger key; -0 as 0; NaN below every number.  (No token: 0; one that stays whatever its weight: kAlways.)
 constexpr uint32_t kAlways = 0xffffffffu;
@@ -43,6 +45,8 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const EvictArgs a) {
     __shared__ unsigned s_warp[2][kWarps][3];           // the warps' counts, in turn
     __shared__ unsigned s_count[2][kMaxCluster][3];     // the CTAs' counts, in turn
     __shared__ uint32_t s_few[kFew];                    // (the first CTA's) the keys that are left
+    __shared__ __align__(16) unsigned s_bin[kBins];     // (in descending order of their keys)
+    __shared__ unsigned s_cut[3];                       // the bin of the largest key wanted, keys from it on, keys above it
     __shared__ unsigned s_nfew;
     __shared__ uint32_t s_found;
     cg::cluster_group cluster = cg::this_cluster();
@@ -74,16 +78,40 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const EvictArgs a) {
     const int per = ((len + 32 * warps - 1) / (32 * warps) + 3) & ~3;
     const int base = (rank * kWarps + warp) * per * 32 + lane;
     auto key_of = [&](int t, float x) { return t >= len ? 0u : t < a.n_sink || t >= len - a.n_recent ? kAlways : weight_key(x); };
-    // (loads of any place, so that they go out together)
     auto weight_at = [&](int t) { return __ldg(w + min(t, len - 1)); };
     uint32_t* keys = s_key + warp * per * 32;
+    auto count_bin = [&](uint32_t x) {
+        if (x) atomicAdd(s_bin + (kBins - 1 - (x >> kBinShift)), 1u);
+    };
+    reinterpret_cast<uint4*>(s_bin)[tid] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
     if (HELD) {
-        for (int i = 0; i < per; i += 4) {
-            float x[4];
+        // 128 tokens at a time, four a lane (a row's room is a multiple of 16, so none lies past its end)
+        const bool vec = (reinterpret_cast<uintptr_t>(a.w) & 15) == 0;
+        const int first = (rank * kWarps + warp) * per * 32 + 4 * lane, last = a.max_pages * a.ps - 4;
+        for (int i = 0; i < per; i += 16) {
+            float4 x[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) x[j] = weight_at(base + 32 * (i + j));
+            for (int j = 0; j < 4; ++j) {
+                const float* from = w + min(first + 32 * i + 128 * j, last);
+                x[j] = vec ? __ldg(reinterpret_cast<const float4*>(from)) : make_float4(__ldg(from), __ldg(from + 1), __ldg(from + 2), __ldg(from + 3));
+            }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) keys[32 * (i + j) + lane] = key_of(base + 32 * (i + j), x[j]);
+            for (int j = 0; j < 4; ++j) {
+                const int t = first + 32 * i + 128 * j;
+                if (i + 4 * j >= per) break;
+                uint4 y;
+                if (__all_sync(0xffffffffu, t >= a.n_sink && t + 3 < len - a.n_recent)) {
+                    y = make_uint4(weight_key(x[j].x), weight_key(x[j].y), weight_key(x[j].z), weight_key(x[j].w));
+                } else {
+                    y = make_uint4(key_of(t, x[j].x), key_of(t + 1, x[j].y), key_of(t + 2, x[j].z), key_of(t + 3, x[j].w));
+                }
+                *reinterpret_cast<uint4*>(keys + 32 * i + 128 * j + 4 * lane) = y;
+                count_bin(y.x);
+                count_bin(y.y);
+                count_bin(y.z);
+                count_bin(y.w);
+            }
         }
         __syncwarp();
     }
@@ -133,16 +161,55 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const EvictArgs a) {
         }
         turn ^= 1;
     };
-    if (size > 1) cluster.sync();  // the other CTAs' shared memory is there
+    if (!HELD) each(count_bin);
+    if (size > 1) cluster.sync();
+    else __syncthreads();
 
-    // the largest key that at least k tokens reach: `found` so far, which at_found tokens reach, and above ones reach what lies
-    // behind its range
-    uint32_t found = 0;
-    unsigned at_found = (unsigned)len, above = 0;
-    int bit = 30;
+    // the bin of the largest key that at least k tokens reach: thread i has the i-th four bins
+    {
+        uint4 y = reinterpret_cast<const uint4*>(s_bin)[tid];
+        for (int r = 1; r < size; ++r) {
+            const uint4 z = reinterpret_cast<const uint4*>(cluster.map_shared_rank(s_bin, (rank + r) & (size - 1)))[tid];
+            y.x += z.x;
+            y.y += z.y;
+            y.z += z.z;
+            y.w += z.w;
+        }
+        const unsigned mine = y.x + y.y + y.z + y.w;
+        unsigned upto = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const unsigned z = __shfl_up_sync(0xffffffffu, upto, off);
+            if (lane >= off) upto += z;
+        }
+        if (lane == 31) s_warp[1][warp][0] = upto;
+        __syncthreads();
+        upto += __reduce_add_sync(0xffffffffu, lane < warp ? s_warp[1][lane][0] : 0u);
+        unsigned above = upto - mine;
+        if (above < k && upto >= k) {
+            const unsigned n[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (above < k && above + n[j] >= k) {
+                    s_cut[0] = kBins - 1 - (4 * tid + j);
+                    s_cut[1] = above + n[j];
+                    s_cut[2] = above;
+                }
+                above += n[j];
+            }
+        }
+        __syncthreads();
+    }
+
+    // that key: `found` so far, which at_found tokens reach, and above ones reach what lies behind its range
+    uint32_t found = s_cut[0] << kBinShift;
+    unsigned at_found = s_cut[1], above = s_cut[2];
+    int bit = kBinShift;
 #pragma unroll 1
-    for (; bit >= 0; bit -= 2) {
-        const uint32_t c1 = found | 1u << bit, c2 = found | 2u << bit, c3 = found | 3u << bit;
+    while (at_found - above > kFew && bit > 0) {
+        const bool last = bit == 1;  // a single bit is left: the three are one
+        bit = last ? 0 : bit - 2;
+        const uint32_t c1 = found | 1u << bit, c2 = last ? c1 : found | 2u << bit, c3 = last ? c1 : found | 3u << bit;
         unsigned n[3] = {0, 0, 0};
         each([&](uint32_t x) {
             n[0] += x >= c1;
@@ -164,7 +231,6 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const EvictArgs a) {
         } else {
             above = n[0];
         }
-        if (at_found - above <= kFew) break;
     }
     if (bit > 0) {
         // few keys are left in the range: one CTA goes on with one a thread, a bit and a barrier at a time
@@ -345,7 +411,7 @@ cudaError_t launch_evict(const EvictArgs& a, int num_sms, cudaStream_t st) {
     }
     if (e != cudaSuccess) return e;
     // (an ordinary launch: CTAs that wait with their shared memory behind a call's move, or another kernel, take its L1; a run of such
-    // calls over 8 rows of 65,521 tokens 45.2 -> 34.8 us each)
+    // calls over 8 rows of 65,521 tokens: 10 us less each, 27 us now)
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(rows * cluster));
     cfg.blockDim = dim3(kThreads);
@@ -366,8 +432,8 @@ cudaError_t launch_evict(const EvictArgs& a, int num_sms, cudaStream_t st) {
     auto move = a.D == 128 ? move_kernel<128> : move_kernel<64>;
     if (rows < num_sms) return launch_pdl(move, grid, dim3(128), 0, st, a, pages, items);
     // Where the choice fills the SMs, an ordinary launch too: the rows in flight need the L1 that an SM gives back only once it has
-    // no shared memory in use (64 sequences of 8K-16K tokens: 410 us; 475 with CTAs that are there early.  8 rows of 65,521, one
-    // call by itself: 41 us early, 45 so)
+    // no shared memory in use (64 sequences of 8K-16K tokens: 65 us less than with CTAs that are there early, 393 us now.  8 rows of
+    // 65,521, one call by itself: 4 us more)
     cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(128);
