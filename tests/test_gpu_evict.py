@@ -438,3 +438,43 @@ def test_caches_past_4_gib(spd):
         results.append([o, lse, new, w, kept, w2, new2] + [x[dev(dst.reshape(-1).astype(np.int64))] for x in (cache_K, cache_V)])
     for x, y in zip(*results):
         assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("length", [5000, 16000, 60001, 400003])
+@pytest.mark.parametrize("values", [2, 3, 2048, 1 << 21])
+def test_kv_evict_weights_that_differ_in_their_last_bits(spd, monkeypatch, length, values):
+    """Keys with the same upper bits, more of them than go on alone, down to the last bit."""
+    def close(rng, kind, shape):
+        return (np.uint32(0x3F800000) + rng.integers(0, values, shape).astype(np.uint32)).view(np.float32) * np.float32(kind)
+    monkeypatch.setitem(globals(), "weights_of", close)
+    rng = np.random.default_rng(length + values)
+    evict(spd, rng, [length, 700], length // 2, 3, 100, 1, 64, 64, 0, 1)
+    evict(spd, rng, [length], length - 700, 0, 0, 1, 64, 64, 0, -1)
+
+
+def test_kv_evict_weights_at_any_address(spd):
+    """Weights that start at no multiple of 16 bytes."""
+    import torch
+    rng = np.random.default_rng(8)
+    lens, budget, H, D, ps = [1001, 40, 333], 100, 2, 64, 16
+    lens, pt, mp, n, K, V = paged(rng, lens, ps, H, D)
+    B = len(lens)
+    dst = np.full_like(pt, -1)
+    dst[:, :7] = n + np.arange(B * 7).reshape(B, 7)
+    K, V = (torch.cat([x, bf(rng.standard_normal((B * 7 + 1, H, ps, D)))]) for x in (K, V))
+    w = rng.random((B, H, mp * ps)).astype(np.float32)
+    dims = spd.dims_of(B, H, H, D, ps, mp, K.shape[0])
+    for off in (1, 2, 3):
+        at = torch.full((w.size + 4,), 9.0, device="cuda")[off: off + w.size].view(w.shape)
+        at.copy_(dev(w))
+        kept = torch.full((B, H, budget), -9, dtype=torch.int32, device="cuda")
+        w_out = torch.full((w.size + 4,), 5.0, device="cuda")[off: off + w.size].view(w.shape)
+        summ = torch.zeros((B, H, mp, 2, D), dtype=torch.bfloat16, device="cuda")
+        new_lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+        spd.kv_evict(dims, budget, 4, 10, K, V, dev(pt), dev(lens), at, dev(dst), kept, w_out, summ, new_lens)
+        assert spd.spd_device_status(clear=True) == 0
+        for b in range(B):
+            for h in range(H):
+                stay = ref.kept(w[b, h], lens[b], budget, 4, 10)
+                assert np.array_equal(kept[b, h, : len(stay)].cpu().numpy(), stay)
+                assert np.array_equal(w_out[b, h, : len(stay)].cpu().numpy(), w[b, h, stay])
