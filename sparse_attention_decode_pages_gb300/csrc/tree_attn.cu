@@ -878,31 +878,54 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 9) tmem_free(s_tmem, C::COLUMNS);
 }
 
-// Joins the partials of the units that shares' borders cut: a thread has eight channels of a row; eight partials are asked
-// for at once.
-constexpr int kJoinChannels = 8, kJoinAhead = 8;
-template <int D>
-__global__ void __launch_bounds__(kSlotRows) join_kernel(const TreeAttnArgs a, const Shape sh, int ctas) {
+// Joins the partials of the units that shares' borders cut.  A thread has eight channels of a row and asks for eight partials at
+// once.  A CTA has 2^lg_rows rows, `chunks` of which cover a unit; what is left of its threads goes over the partials in turn
+// (SPLIT: few units, in many parts each) or has other channels.  (One sequence of 23,545 tokens with two KV heads, in 76 parts
+// each: 16.6 us for the whole call, 27.5 where a thread goes over all partials of a row; 64 sequences of 1,024, 15 nodes, in two
+// or three parts: 60 us, 5 more with splits.)
+constexpr int kJoinChannels = 8, kJoinAhead = 8, kJoinThreads = 256;
+template <int D, bool SPLIT>
+__global__ void __launch_bounds__(kJoinThreads, SPLIT ? 3 : 4) join_kernel(const TreeAttnArgs a, const Shape sh, int ctas, int lg_rows, int chunks) {
+    __shared__ float4 s_o[SPLIT ? kJoinThreads : 1][2];
+    __shared__ float2 s_ml[SPLIT ? kJoinThreads : 1];
     const float NEG_INF = __int_as_float(0xff800000);
+    const int rows = 1 << lg_rows, others = kJoinThreads >> lg_rows, other = threadIdx.x >> lg_rows;
+    const int splits = SPLIT ? others : 1, split = SPLIT ? other : 0;
+    const int groups = SPLIT ? 1 : others;  // eight channels each
+    const int blocks = D / kJoinChannels / groups, chunk = blockIdx.x % (unsigned)chunks, block = blockIdx.x / (unsigned)chunks;
+    const int unit = block / blocks, group = (block - unit * blocks) * groups + (SPLIT ? 0 : other);
+    const int at = (chunk << lg_rows) + (int)(threadIdx.x & (rows - 1));  // of the unit's two row tiles
     const float* part_o = reinterpret_cast<const float*>(static_cast<const char*>(a.ws) + ((size_t)ctas * sizeof(Cut) + 255) / 256 * 256);
-    const float2* part_ml = reinterpret_cast<const float2*>(part_o + (size_t)2 * ctas * kSlotRows * D) + threadIdx.x;
-    const int group = blockIdx.x % (D / kJoinChannels);
-    const float4* part = reinterpret_cast<const float4*>(part_o) + group * 2 * kSlotRows + threadIdx.x;
+    const float2* part_ml = reinterpret_cast<const float2*>(part_o + (size_t)2 * ctas * kSlotRows * D) + at;
+    const float4* part = reinterpret_cast<const float4*>(part_o) + group * 2 * kSlotRows + at;
     pdl_wait();
     pdl_trigger();
-    const Cut cut = reinterpret_cast<const Cut*>(a.ws)[blockIdx.x / (D / kJoinChannels)];
+    const Cut cut = reinterpret_cast<const Cut*>(a.ws)[unit];
     if (cut.pieces == 0) return;
     const int h = sh.head(cut.sub), mt = sh.first_tile(cut.sub);
-    const int row = threadIdx.x & (kRows - 1), node = (mt + threadIdx.x / kRows) * sh.tpt + row / sh.G;
-    if (mt + (int)threadIdx.x / kRows >= sh.row_tiles || row >= sh.tpt * sh.G || node >= a.T) return;
+    const int row = at & (kRows - 1), node = (mt + at / kRows) * sh.tpt + row / sh.G;
+    const bool valid = mt + at / kRows < sh.row_tiles && row < sh.tpt * sh.G && node < a.T;
     float r = NEG_INF, total = 0.f;
     float4 o0 = make_float4(0.f, 0.f, 0.f, 0.f), o1 = o0;
-    for (int i0 = 0; i0 < cut.pieces; i0 += kJoinAhead) {
+    auto add = [&](float now, float m, float l, float4 x, float4 y) {
+        const float w = m == NEG_INF ? 0.f : fast_exp2(m - now);
+        total += m == NEG_INF ? l : l * w;  // (a row of NaN logits alone has no reference)
+        o0 = make_float4(fmaf(x.x, w, o0.x), fmaf(x.y, w, o0.y), fmaf(x.z, w, o0.z), fmaf(x.w, w, o0.w));
+        o1 = make_float4(fmaf(y.x, w, o1.x), fmaf(y.y, w, o1.y), fmaf(y.z, w, o1.z), fmaf(y.w, w, o1.w));
+    };
+    auto follow = [&](float now) {
+        const float corr = r == NEG_INF ? 0.f : fast_exp2(r - now);
+        total = r == NEG_INF ? total : total * corr;
+        r = now;
+        o0 = make_float4(o0.x * corr, o0.y * corr, o0.z * corr, o0.w * corr);
+        o1 = make_float4(o1.x * corr, o1.y * corr, o1.z * corr, o1.w * corr);
+    };
+    for (int i0 = split; valid && i0 < cut.pieces; i0 += kJoinAhead * splits) {
         float2 ml[kJoinAhead];
         float4 x[kJoinAhead], y[kJoinAhead];
 #pragma unroll
         for (int k = 0; k < kJoinAhead; ++k) {
-            const int i = i0 + k;
+            const int i = i0 + k * splits;
             // a unit's first partial is its CTA's second slot, the others are their CTAs' first
             const size_t slot = (size_t)(2 * (cut.cta + i) + (i == 0 ? 1 : 0));
             ml[k] = make_float2(NEG_INF, 0.f);
@@ -916,19 +939,24 @@ __global__ void __launch_bounds__(kSlotRows) join_kernel(const TreeAttnArgs a, c
         float now = r;
 #pragma unroll
         for (int k = 0; k < kJoinAhead; ++k) now = fmaxf(now, ml[k].x);
-        const float corr = r == NEG_INF ? 0.f : fast_exp2(r - now);
-        r = now;
-        total *= corr;
-        o0 = make_float4(o0.x * corr, o0.y * corr, o0.z * corr, o0.w * corr);
-        o1 = make_float4(o1.x * corr, o1.y * corr, o1.z * corr, o1.w * corr);
+        follow(now);
 #pragma unroll
-        for (int k = 0; k < kJoinAhead; ++k) {
-            const float w = ml[k].x == NEG_INF ? 0.f : fast_exp2(ml[k].x - r);
-            total += ml[k].x == NEG_INF ? ml[k].y : ml[k].y * w;  // (a row of NaN logits alone has no reference)
-            o0 = make_float4(fmaf(x[k].x, w, o0.x), fmaf(x[k].y, w, o0.y), fmaf(x[k].z, w, o0.z), fmaf(x[k].w, w, o0.w));
-            o1 = make_float4(fmaf(y[k].x, w, o1.x), fmaf(y[k].y, w, o1.y), fmaf(y[k].z, w, o1.z), fmaf(y[k].w, w, o1.w));
-        }
+        for (int k = 0; k < kJoinAhead; ++k) add(now, ml[k].x, ml[k].y, x[k], y[k]);
     }
+    if (SPLIT) {
+        if (split > 0) {
+            s_o[threadIdx.x][0] = o0;
+            s_o[threadIdx.x][1] = o1;
+            s_ml[threadIdx.x] = make_float2(r, total);
+        }
+        __syncthreads();
+        if (split > 0) return;
+        float now = r;
+        for (int i = threadIdx.x + rows; i < kJoinThreads; i += rows) now = fmaxf(now, s_ml[i].x);
+        follow(now);
+        for (int i = threadIdx.x + rows; i < kJoinThreads; i += rows) add(now, s_ml[i].x, s_ml[i].y, s_o[i][0], s_o[i][1]);
+    }
+    if (!valid) return;
     const float inv = total == 0.f ? 0.f : 1.f / total;
     const long long out = ((long long)cut.b * a.T + node) * a.H_q + h * sh.G + row % sh.G;
     *reinterpret_cast<uint4*>(reinterpret_cast<bf16*>(a.o) + out * D + group * kJoinChannels) =
@@ -954,7 +982,13 @@ cudaError_t launch(const TreeAttnArgs& a, const TreeMaps& m, int ctas, cudaStrea
     e = launch_pdl(tree_kernel<D>, dim3((unsigned)ctas), dim3(kThreads), Cfg<D>::SMEM, st, a, m, sh, few);
     if (e != cudaSuccess) return e;
     const long long cuts = few ? units : ctas;
-    return launch_pdl(join_kernel<D>, dim3((unsigned)(cuts * (D / kJoinChannels))), dim3(kSlotRows), 0, st, a, sh, ctas);
+    // no more rows a CTA than there are; and where units are few, splits until a thread has eight partials or the GPU is full
+    const int rows = sh.row_tiles == 1 ? sh.tpt * sh.G : kSlotRows;
+    int lg = 5;
+    auto chunks = [&] { return (rows + (1 << lg) - 1) >> lg; };
+    auto blocks = [&] { return cuts * chunks() * (D / kJoinChannels) / (few ? 1 : kJoinThreads >> lg); };
+    while (lg < 8 && chunks() > 1 && (!few || blocks() > 4 * a.num_sms || ctas <= units * kJoinAhead * (kJoinThreads >> (lg + 1)))) ++lg;
+    return launch_pdl(few ? join_kernel<D, true> : join_kernel<D, false>, dim3((unsigned)blocks()), dim3(kJoinThreads), 0, st, a, sh, ctas, lg, chunks());
 }
 
 // CTAs: one an SM, or as many as there can be tiles.
