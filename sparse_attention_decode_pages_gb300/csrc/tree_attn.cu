@@ -51,10 +51,14 @@ constexpr int kSoftmaxRegs = 208, kOtherRegs = 80;
 static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "what the block was launched with");
 constexpr int kInfos = 16;          // tiles whose visible tokens are written down
 constexpr int kOdd = 8;             // pieces whose nodes with odd values are
-// Units of which the SMs hold this many times as many are cut into parts of their own: the last part of a unit costs a CTA
-// 3 to 4 us (queries, first products, results) that a CTA with parts of two units pays twice; more units than this would leave
-// parts of very different lengths.
-constexpr int kFewUnits = 8;
+// Units of which the SMs hold this many times as many are cut into parts of their own, so that no CTA has parts of two
+// (3 sequences of 14,000 tokens, 61 nodes: 46 us against 51); more units than this leave parts of too different lengths, or CTAs
+// without one (8 sequences of 8,000, 8 nodes: 55.6 us so, 51.2 in equal shares).
+constexpr int kFewUnits = 4;
+// What a unit costs a CTA beside its tiles (queries, first products, results), in tiles: so many are counted in front of its own
+// where equal shares are cut, or a CTA with many short units would hold up the others (12 sequences of 0 to 16,000 tokens, 61 nodes:
+// 119 -> 88 us; 64 of 0 to 2,000, 64 nodes: 121 -> 88; with five instead of three the same).
+constexpr int kUnitTiles = 3;
 constexpr float kLag = 8.f;         // powers of two that a maximum may lie above the reference
 
 template <int D>
@@ -116,40 +120,43 @@ struct Piece {
     bool bad;  // a length that the page table has no room for: no tokens, no nodes
 };
 
-// Where a CTA's share begins, and what it is of: tile `at` of `total`, or (few units) the first of a unit's parts, which
-// `follow` CTAs hold the rest of.
+// Where a CTA's share begins, counted with kUnitTiles in front of each unit's, and what it is of: tile `at` of `total`, or (few
+// units) the first of a unit's parts, which `follow` CTAs hold the rest of.
 struct Share {
     int b, sub, t0, len;
     long long left, at, total;
     int follow;
 };
 
-// Goes through the pieces of a share, one sequence's units after the other's.
+// Goes through the pieces of a share, one sequence's units after the other's (t0 and left counted as the share).
 struct Walk {
     int b, sub, t0, len, nt;
     bool bad;
-    long long left;  // tiles
+    long long left;
     __device__ __forceinline__ void look(const TreeAttnArgs& a, const Shape& sh, int raw) {
         bad = sh.pages(raw, a.max_pages) < 0;
         len = bad ? 0 : raw;
         nt = (len + kTokens - 1) / kTokens + 1;
     }
     __device__ __forceinline__ bool next(const TreeAttnArgs& a, const Shape& sh, Piece& p) {
-        if (left <= 0) return false;
-        p.b = b;
-        p.sub = sub;
-        p.len = len;
-        p.nt = nt;
-        p.bad = bad;
-        p.t0 = t0;
-        p.t1 = (int)min((long long)nt, t0 + left);
-        left -= p.t1 - p.t0;
-        t0 = 0;
-        if (++sub == a.H_kv * sh.pairs) {
-            sub = 0;
-            if (left > 0) look(a, sh, a.seq_lens[++b]);
+        while (left > 0) {
+            p.b = b;
+            p.sub = sub;
+            p.len = len;
+            p.nt = nt;
+            p.bad = bad;
+            const int end = (int)min((long long)nt + kUnitTiles, t0 + left);
+            p.t0 = max(0, t0 - kUnitTiles);
+            p.t1 = max(0, end - kUnitTiles);
+            left -= end - t0;
+            t0 = 0;
+            if (++sub == a.H_kv * sh.pairs) {
+                sub = 0;
+                if (left > 0) look(a, sh, a.seq_lens[++b]);
+            }
+            if (p.t0 < p.t1) return true;
         }
-        return true;
+        return false;
     }
 };
 
@@ -236,16 +243,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto tiles_of = [&](int len) { return sh.pages(len, a.max_pages) < 0 ? 1 : (len + kTokens - 1) / kTokens + 1; };
         if (warp == 9) tmem_alloc(&s_tmem, C::COLUMNS);
         if (few) {
-            // A unit's tiles are cut into equal parts, about as many as its share of all tiles, so that no CTA goes from
-            // one unit to the next: one warp, a sequence a lane.
+            // A unit's tiles are cut into equal parts, none of more tiles than there have to be for all parts to find a CTA, so
+            // that no CTA goes from one unit to the next: one warp, a sequence a lane.
             if (warp == 0) {
                 int len = 0, nt = 0;
                 if (lane < a.B) {
                     len = a.seq_lens[lane];
                     nt = tiles_of(len);
                 }
-                const int total = __reduce_add_sync(0xffffffffu, nt) * subs, units = a.B * subs;
-                const int parts = lane < a.B ? min(nt, 1 + (int)((unsigned)nt * (gridDim.x - units) / (unsigned)total)) : 0;
+                int most = max(1, (__reduce_add_sync(0xffffffffu, nt) * subs + (int)gridDim.x - 1) / (int)gridDim.x), parts;
+                for (;; most += 1 + (most >> 4)) {  // (ends where every unit is one part at the latest: there are more CTAs)
+                    parts = (nt + most - 1) / most;
+                    if (__reduce_add_sync(0xffffffffu, parts) * subs <= (int)gridDim.x) break;
+                }
                 int incl = parts * subs;
 #pragma unroll
                 for (int off = 1; off < 32; off <<= 1) {
@@ -259,8 +269,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (mine) {
                         x.sub = off / parts;
                         const int part = off - x.sub * parts;
-                        x.t0 = (int)((unsigned)nt * part / parts);  // (at most 2^23 tiles, 256 parts)
-                        x.left = (int)((unsigned)nt * (part + 1) / parts) - x.t0;
+                        const int t0 = (int)((unsigned)nt * part / parts);  // (at most 2^23 tiles, 256 parts)
+                        x.t0 = t0 + kUnitTiles;
+                        x.left = (int)((unsigned)nt * (part + 1) / parts) - t0;
                         x.follow = part == 0 ? parts - 1 : 0;
                     }
                     s_share = x;
@@ -268,13 +279,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         } else {
             // all tiles in a row, in equal shares
+            auto cost_of = [&](int len) { return tiles_of(len) + kUnitTiles; };
             const int per = (a.B + kThreads - 1) / kThreads;
             const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
             int len = 0;  // of this thread's last sequence
             long long mine = 0;
             for (int b = b0; b < b1; ++b) {
                 len = a.seq_lens[b];
-                mine += (long long)tiles_of(len) * subs;
+                mine += (long long)cost_of(len) * subs;
             }
             long long incl = mine;
 #pragma unroll
@@ -301,12 +313,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 int b = b0;
                 if (per > 1) len = a.seq_lens[b];
                 long long at = before;
-                while (g0 - at >= (long long)tiles_of(len) * subs) {
-                    at += (long long)tiles_of(len) * subs;
+                while (g0 - at >= (long long)cost_of(len) * subs) {
+                    at += (long long)cost_of(len) * subs;
                     len = a.seq_lens[++b];
                 }
                 const long long off = g0 - at;
-                const int nt = tiles_of(len);
+                const int nt = cost_of(len);
                 Share x = {b, 0, 0, len, any ? shares.begin(blockIdx.x + 1) - g0 : 0, g0, total, 0};
                 x.sub = off < 0x7fffffff ? (int)off / nt : (int)(off / nt);
                 x.t0 = (int)(off - (long long)x.sub * nt);
@@ -803,7 +815,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) {
                 Cut* cuts = reinterpret_cast<Cut*>(a.ws);
                 if (few) {
-                    if (w.left > 0 && w.t0 == 0) {
+                    if (w.left > 0 && w.t0 == kUnitTiles) {
                         const int parts = s_share.follow + 1;
                         cuts[w.b * subs + w.sub] = {w.b, w.sub, parts > 1 ? parts : 0, (int)blockIdx.x};
                     }
@@ -811,15 +823,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     Cut cut = {0, 0, 0, (int)blockIdx.x};
                     Walk x = w;
                     Piece p;
-                    long long at = s_share.at;
                     const Shares shares(s_share.total, (int)min((long long)gridDim.x, s_share.total));
                     while (x.next(a, sh, p)) {
                         if (p.t0 == 0 && p.t1 < p.nt) {
+                            const long long end = s_share.at + (w.left - x.left) + (p.nt - p.t1);  // of the unit
                             int c = blockIdx.x;
-                            while (shares.begin(c + 1) < at + p.nt) ++c;
+                            while (shares.begin(c + 1) < end) ++c;
                             cut = {p.b, p.sub, c - (int)blockIdx.x + 1, (int)blockIdx.x};
                         }
-                        at += p.t1 - p.t0;
                     }
                     cuts[blockIdx.x] = cut;
                 }
