@@ -168,6 +168,7 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const EvictArgs a) {
     // the bin of the largest key that at least k tokens reach: thread i has the i-th four bins
     {
         uint4 y = reinterpret_cast<const uint4*>(s_bin)[tid];
+#pragma unroll 4
         for (int r = 1; r < size; ++r) {
             const uint4 z = reinterpret_cast<const uint4*>(cluster.map_shared_rank(s_bin, (rank + r) & (size - 1)))[tid];
             y.x += z.x;
@@ -430,8 +431,8 @@ cudaError_t launch_evict(const EvictArgs& a, int num_sms, cudaStream_t st) {
     const long long items = rows * pages;
     const dim3 grid((unsigned)((items + 3) / 4));
     auto move = a.D == 128 ? move_kernel<128> : move_kernel<64>;
-    if (rows < num_sms) return launch_pdl(move, grid, dim3(128), 0, st, a, pages, items);
-    // Where the choice fills the SMs, an ordinary launch too: the rows in flight need the L1 that an SM gives back only once it has
+    if (rows < num_sms && items <= 48 * num_sms) return launch_pdl(move, grid, dim3(128), 0, st, a, pages, items);
+    // Where the choice or the move fills the SMs, an ordinary launch too: the rows in flight need the L1 that an SM gives back only once it has
     // no shared memory in use (64 sequences of 8K-16K tokens: 65 us less than with CTAs that are there early, 393 us now.  8 rows of
     // 65,521, one call by itself: 4 us more)
     cfg = {};
