@@ -125,6 +125,7 @@ __global__ void __launch_bounds__(kThreads, 3) weights_kernel(const WeightsArgs 
     };
     for (int i = 0; i < kStages; ++i) ask_next(i);
 
+    bool dead = false;
     for (int i = tid; i < groups * 8 * (D / 8); i += kThreads) {
         const int r = i / (D / 8), ch = i % (D / 8), t = r / G;
         uint4 v = make_uint4(0, 0, 0, 0);
@@ -136,8 +137,9 @@ __global__ void __launch_bounds__(kThreads, 3) weights_kernel(const WeightsArgs 
             v = __ldg(reinterpret_cast<const uint4*>(a.q + at * D) + ch);
             if (ch == 0) {
                 lse = a.lse[at] * kLog2e;
+                dead |= lse == -INF;
                 if (lse == -INF) lse = INF;
-                lim = fresh + t;
+                else lim = fresh + t;
             }
         }
         *reinterpret_cast<uint4*>(s_q + r * QROW + ch * 16) = v;
@@ -146,7 +148,9 @@ __global__ void __launch_bounds__(kThreads, 3) weights_kernel(const WeightsArgs 
             s_lim[r] = lim;
         }
     }
-    __syncthreads();
+    // rows that add nothing see no token (an infinite key would make NaN of them): those that fill up the last group, and others
+    const bool none_dead = !__syncthreads_or(dead);
+    const int filled = R & 7 ? groups - 1 : -1;
 
     const long long wrow = (long long)row * a.max_pages * a.ps + t0;
     if (SEL) {
@@ -203,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 3) weights_kernel(const WeightsArgs 
             }
             float sum0 = 0.f, sum1 = 0.f;  // of tokens g and g + 8
             const int p0 = t0 + at + g;
-            const bool all = t0 + at + 15 <= fresh;  // every row sees every token
+            const bool all = none_dead && t0 + at + 15 <= fresh;  // every row sees every token
             for (int j = 0; j < groups; ++j) {
                 float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};  // (two chains of products)
                 const uint8_t* q = s_q + (j * 8 + g) * QROW + c * 32;
@@ -219,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 3) weights_kernel(const WeightsArgs 
                 float e[4];
 #pragma unroll
                 for (int x = 0; x < 4; ++x) e[x] = fast_exp2(fmaf(s[0][x] + s[1][x], a.scale_log2, x & 1 ? -lse.y : -lse.x));
-                if (!all) {
+                if (!all || j == filled) {
                     const int2 lim = *reinterpret_cast<const int2*>(s_lim + j * 8 + 2 * c);
                     if (p0 > lim.x) e[0] = 0.f;
                     if (p0 > lim.y) e[1] = 0.f;

@@ -478,3 +478,33 @@ def test_kv_evict_weights_at_any_address(spd):
                 stay = ref.kept(w[b, h], lens[b], budget, 4, 10)
                 assert np.array_equal(kept[b, h, : len(stay)].cpu().numpy(), stay)
                 assert np.array_equal(w_out[b, h, : len(stay)].cpu().numpy(), w[b, h, stay])
+
+
+@pytest.mark.parametrize("T,G", [(2, 3), (5, 8), (8, 1)])
+def test_kv_weights_update_keys_and_rows_that_are_not_finite(spd, T, G):
+    """Rows of lse = -inf add nothing, whatever their queries hold; a key of -inf logits gets nothing from any row, one of +inf
+    logits infinity, a NaN key NaN, and no other token is touched by them."""
+    import torch
+    rng = np.random.default_rng(T)
+    D, ps, length = 64, 16, 200
+    lens, pt, mp, n, K, V = paged(rng, [length], ps, 1, D)
+    q = np.abs(host(bf(rng.standard_normal((1, T, G, D)))))
+    lse = rng.uniform(4, 9, (1, T, G)).astype(np.float32)
+    for t, value in ((20, float("-inf")), (40, float("inf")), (41, float("nan"))):
+        K[int(pt[0, t // ps]), 0, t % ps, 0] = value
+    dead = [(0, 0), (T - 1, G - 1)]
+    for (t, g), value in zip(dead, (np.nan, np.inf)):
+        lse[0, t, g], q[0, t, g] = -np.inf, value
+    keys = context(lens, pt, host(K), ps, 0)[:, 0]
+    w_in = rng.uniform(0, 2, (1, 1, mp * ps)).astype(np.float32)
+    out = torch.full((1, 1, mp * ps), 5.0, device="cuda")
+    spd.kv_weights_update(spd.dims_of(1, G, 1, D, ps, mp, n), T, bf(q), dev(lse), K, dev(pt), dev(lens), out, w_in=dev(w_in), decay=0.5)
+    assert spd.spd_device_status(clear=True) == 0
+    got = host(out)[0, 0]
+    assert got[20] == 0.5 * w_in[0, 0, 20] and np.isposinf(got[40]) and np.isnan(got[41])
+    finite = keys.copy()
+    finite[[20, 40, 41]] = 0
+    q[0, [t for t, g in dead], [g for t, g in dead]] = 0
+    total, spread = ref.weights(host(bf(q))[0], lse[0].astype(np.float64), finite, D ** -0.5, length - T)
+    rest = np.delete(np.arange(length), [20, 40, 41])
+    check_weights(got[rest], w_in[0, 0][rest], 0.5, length - T - 3, len(rest), total[rest], spread[rest], T * G, T)
