@@ -28,10 +28,10 @@
 // a second kernel to join.
 //
 // What bounds it (32 / 8 heads of 128 channels): memory up to 128 rows a KV head (64 sequences of 8K-16K tokens, 15 nodes:
-// 477 us, the measured copy rate).  With 256 rows (64 nodes) 560 us, 1,480 TFLOP/s, in a short run: a pair of tiles takes
+// 474 us, the measured copy rate).  With 256 rows (64 nodes) 557 us, 1,490 TFLOP/s, in a short run: a pair of tiles takes
 // 3,325 cycles, its products 2,048 of them, and their operands and copies keep shared memory busy for as many; in a long one
-// the power limit, 667 us at an SM clock of 1.46 GHz.  One sequence of 131,001 tokens, 61 nodes: 108 us; of 1,003, 8 nodes:
-// 14.4 us, the latency of the two kernels.
+// the power limit, 610 to 667 us at an SM clock of 1.46 to 1.6 GHz.  One sequence of 131,001 tokens, 61 nodes: 98 us; of 1,003, 8
+// nodes: 10.5 us, the latency of the two kernels.
 #include <atomic>
 
 #include "common.cuh"
