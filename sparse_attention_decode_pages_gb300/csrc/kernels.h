@@ -284,7 +284,8 @@ struct WeightsArgs {
     unsigned* status;
     unsigned long long wait_ns;
 };
-// map: boxes of 16 rows of K.
+// Whether many query rows make it go by tiles of 128 tokens; map: then boxes of a page of K as tree_verify_attn's, else of 16 rows.
+bool weights_by_tiles(int T, int G, bool selected);
 cudaError_t launch_weights_update(const WeightsArgs& a, const CUtensorMap& map, int num_sms, cudaStream_t st);
 
 struct EvictArgs {

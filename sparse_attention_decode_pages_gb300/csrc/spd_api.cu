@@ -1268,18 +1268,24 @@ static spd_status tree_map(CUtensorMap* m, const void* base, int rank, const cuu
     return r == CUDA_SUCCESS ? SPD_OK : fail(SPD_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
 }
 
+// Pages of keys or values as boxes of atoms, 8 slots by 64 channels: [page and KV head][slot / 8][half][slot % 8], n of them.
+static spd_status page_map(CUtensorMap* m, const void* base, int D, int ps, cuuint64_t n) {
+    const cuuint64_t row = (cuuint64_t)D * 2, halves = (cuuint64_t)D / 64;
+    const cuuint64_t size[5] = {64, 8, halves, (cuuint64_t)ps / 8, n}, stride[4] = {row, 128, row * 8, row * ps};
+    const cuuint32_t box[5] = {64, 8, (cuuint32_t)halves, (cuuint32_t)ps / 8, 1};
+    return tree_map(m, base, 5, size, stride, box);
+}
+
 // The views that the tree's attention copies boxes of, 64 channels (128 bytes) wide: pages as [page and KV head][slot / 8][half][slot % 8] and [page and KV head][half][slot],
 // queries as [half][row][head], nodes as [half][head][sequence][node] (what lies behind the last node arrives as zeros).
 static spd_status tree_maps(const TreeAttnArgs& a, TreeMaps* m) {
     const cuuint64_t row = (cuuint64_t)a.D * 2, halves = (cuuint64_t)a.D / 64;
     const cuuint64_t pages = (cuuint64_t)a.num_phys * a.H_kv;
     const cuuint64_t n = pages ? pages : 1;
-    const cuuint64_t kv_size[5] = {64, 8, halves, (cuuint64_t)a.ps / 8, n}, kv_stride[4] = {row, 128, row * 8, row * a.ps};
-    const cuuint32_t kv_box[5] = {64, 8, (cuuint32_t)halves, (cuuint32_t)a.ps / 8, 1};
     const cuuint64_t e_size[4] = {64, (cuuint64_t)a.ps, halves, n}, e_stride[3] = {row, 128, row * a.ps};
     const cuuint32_t e_box[4] = {64, 8, 1, 1};
-    spd_status st = tree_map(&m->k, a.K, 5, kv_size, kv_stride, kv_box);
-    if (st == SPD_OK) st = tree_map(&m->v, a.V, 5, kv_size, kv_stride, kv_box);
+    spd_status st = page_map(&m->k, a.K, a.D, a.ps, n);
+    if (st == SPD_OK) st = page_map(&m->v, a.V, a.D, a.ps, n);
     if (st == SPD_OK) st = tree_map(&m->k_edge, a.K, 4, e_size, e_stride, e_box);
     if (st == SPD_OK) st = tree_map(&m->v_edge, a.V, 4, e_size, e_stride, e_box);
     const int G = a.H_q / a.H_kv;
@@ -1484,7 +1490,8 @@ SPD_API spd_status kv_weights_update(const spd_dims* dims, int32_t T, const spd_
     spd_dims k = *dims;
     if (k.num_phys_pages < 1) k.num_phys_pages = 1;  // (a view of nothing is none; no page of it is read)
     CUtensorMap map;
-    st = kv_map(&map, K, &k, 16);
+    st = weights_by_tiles(T, dims->H_q / dims->H_kv, sel != nullptr) ? page_map(&map, K, k.D, k.page_size, dims->num_phys_pages ? (cuuint64_t)k.num_phys_pages * k.H_kv : 1)
+                                                                      : kv_map(&map, K, &k, 16);
     if (st != SPD_OK) return st;
     cudaError_t e = launch_weights_update(a, map, d->sms, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? SPD_OK : cuda_fail(e, "kv_weights_update launch");

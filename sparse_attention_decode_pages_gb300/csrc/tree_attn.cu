@@ -678,15 +678,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 base += 2 * n;
             }
-            // copies in flight land before their memory is given back
-            if (!ok) {
-                for (int i = 0; i < STAGES; ++i) {
-                    if (!(asked >> i & 1u)) continue;
-                    if (asked_nodes >> i & 1u) mbar_wait_bounded(v_tree + i, ~v_parity >> i & 1u, a.status, drain_ns);
-                    else mbar_wait_bounded(full + i, asked_parity >> i & 1u, a.status, drain_ns);
-                }
-                if (q_asked) mbar_wait_bounded(q_full, q_parity, a.status, drain_ns);
+            // copies land before their memory is given back, also where the products no longer wait for them
+            for (int i = 0; i < STAGES; ++i) {
+                if (!(asked >> i & 1u)) continue;
+                if (asked_nodes >> i & 1u) mbar_wait_bounded(v_tree + i, ~v_parity >> i & 1u, a.status, drain_ns);
+                else mbar_wait_bounded(full + i, asked_parity >> i & 1u, a.status, drain_ns);
             }
+            if (q_asked) mbar_wait_bounded(q_full, q_parity, a.status, drain_ns);
         } else if (warp == 9) {
             other_regs();
             // ======================================================== products

@@ -38,6 +38,10 @@ WEIGHTS = [  # lens, T, H_q, H_kv, D, ps, path, with old weights, pages selected
     ([100, 3, 1500], 3, 5, 5, 128, 16, True, True, 0),
     ([1600, 20, 7], 1, 8, 2, 128, 16, False, True, 9),
     ([1600, 500], 4, 3, 1, 64, 64, False, True, 5),
+    ([200, 16, 900], 16, 8, 2, 64, 16, True, True, 0),
+    ([129, 1300], 20, 14, 2, 128, 32, False, True, 0),
+    ([700, 128, 64], 11, 3, 1, 128, 64, True, False, 0),
+    ([4500, 0, 63], 63, 5, 1, 64, 16, True, True, 0),
 ]
 
 
@@ -508,3 +512,35 @@ def test_kv_weights_update_keys_and_rows_that_are_not_finite(spd, T, G):
     total, spread = ref.weights(host(bf(q))[0], lse[0].astype(np.float64), finite, D ** -0.5, length - T)
     rest = np.delete(np.arange(length), [20, 40, 41])
     check_weights(got[rest], w_in[0, 0][rest], 0.5, length - T - 3, len(rest), total[rest], spread[rest], T * G, T)
+
+
+@pytest.mark.parametrize("T,pages", [(2, 0), (40, 0), (3, 4)])
+def test_kv_weights_update_with_waits_that_run_out(spd, T, pages):
+    """A limit of 1 ns: the call ends, and the next one with the usual limit gives a clean one's bits."""
+    import torch
+    rng = np.random.default_rng(T)
+    H_q, H_kv, D, ps = 8, 2, 128, 16
+    lens, pt, mp, n, K, V = paged(rng, [3000, 200, 40], ps, H_kv, D)
+    dims = spd.dims_of(3, H_q, H_kv, D, ps, mp, n)
+    q, lse = bf(rng.standard_normal((3, T, H_q, D))), dev(rng.uniform(4, 9, (3, T, H_q)).astype(np.float32))
+    args = {}
+    if pages:
+        args = dict(sel=dev(np.tile(np.array([0, 1, 2], np.int32), (3, H_kv, 1))), nsel=dev(np.full((3, H_kv), 3, np.int32)))
+
+    def update():
+        w = torch.zeros((3, H_kv, mp * ps), device="cuda")
+        spd.kv_weights_update(dims, T, q, lse, K, dev(pt), dev(lens), w, **args)
+        torch.cuda.synchronize()
+        return w
+
+    first = update()
+    assert spd.spd_device_status(clear=True) == 0
+    usual = spd.spd_wait_limit_ns()
+    try:
+        spd.spd_set_wait_limit_ns(1)
+        for _ in range(3):
+            update()
+            assert spd.spd_device_status(clear=True) & ~spd.DEV_TIMEOUT == 0
+    finally:
+        spd.spd_set_wait_limit_ns(usual)
+    assert torch.equal(update(), first) and spd.spd_device_status(clear=True) == 0
