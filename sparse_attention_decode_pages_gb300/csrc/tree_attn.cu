@@ -579,6 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t q_parity = 1, v_parity = 0;                // v_parity: of each slot's next nodes, bits
             uint32_t asked = 0, asked_nodes = 0, asked_parity = 0;  // this warp's last copy to each slot, bits
             int base = 0, n_info = 0;                            // items, and tiles, of the pieces before
+            int asked_item = 0;                                  // lane i: of slot i
             bool ok = true, q_asked = false;
             Piece p;
             while (ok && w.next(a, sh, p)) {
@@ -674,13 +675,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     asked |= 1u << slot;
+                    if (lane == slot) asked_item = item;
                     asked_parity = (asked_parity & ~(1u << slot)) | ((uint32_t)(item / STAGES) & 1u) << slot;
                 }
                 base += 2 * n;
             }
-            // copies land before their memory is given back, also where the products no longer wait for them
+            // copies land before their memory is given back, also where the products no longer wait for them.  (Where all have
+            // been asked for, the other warp's later item in a slot has this one's behind it, and the barrier two phases on.)
             for (int i = 0; i < STAGES; ++i) {
-                if (!(asked >> i & 1u)) continue;
+                if (!(asked >> i & 1u) || (ok && __shfl_sync(0xffffffffu, asked_item, i) < base - STAGES)) continue;
                 if (asked_nodes >> i & 1u) mbar_wait_bounded(v_tree + i, ~v_parity >> i & 1u, a.status, drain_ns);
                 else mbar_wait_bounded(full + i, asked_parity >> i & 1u, a.status, drain_ns);
             }

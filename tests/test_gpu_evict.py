@@ -544,3 +544,27 @@ def test_kv_weights_update_with_waits_that_run_out(spd, T, pages):
     finally:
         spd.spd_set_wait_limit_ns(usual)
     assert torch.equal(update(), first) and spd.spd_device_status(clear=True) == 0
+
+
+def test_kv_weights_update_of_a_long_row_many_queries(spd):
+    """2^30 - 3 tokens of one page and 18 query rows."""
+    import torch
+    ps, D, T, n = 64, 64, 6, (1 << 30) - 3
+    pages = 1 << 24
+    if torch.cuda.mem_get_info()[0] < 20 << 30:
+        pytest.skip("needs 20 GB of device memory")
+    rng = np.random.default_rng(3)
+    dims = spd.dims_of(1, 3, 1, D, ps, pages, 1)
+    K = bf(rng.standard_normal((1, 1, ps, D)))
+    pt = torch.zeros((1, pages), dtype=torch.int32, device="cuda")
+    w = torch.ones((1, 1, pages * ps), device="cuda")
+    q, lse = bf(rng.standard_normal((1, T, 3, D))), dev(rng.uniform(5, 8, (1, T, 3)).astype(np.float32))
+    spd.kv_weights_update(dims, T, q, lse, K, pt, torch.tensor([n], dtype=torch.int32, device="cuda"), w, w_in=w, decay=0.5)
+    assert spd.spd_device_status(clear=True) == 0
+    got = w[0, 0]
+    for t0 in (0, 1 << 20, (1 << 29) + 64, (1 << 30) - 64):
+        block = host(got[t0: t0 + ps])
+        stop, fresh = min(ps, n - t0), n - T - t0
+        total, spread = ref.weights(host(q)[0], lse.cpu().numpy()[0].astype(np.float64), host(K)[0, 0], D ** -0.5, min(fresh, ps))
+        check_weights(block, np.ones(ps), 0.5, fresh, stop, total[:stop], spread[:stop], 3 * T, t0)
+    assert got[n:].tolist() == [1.0] * 3
