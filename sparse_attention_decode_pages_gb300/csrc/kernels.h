@@ -284,8 +284,9 @@ struct WeightsArgs {
     unsigned* status;
     unsigned long long wait_ns;
 };
-// Whether many query rows make it go by tiles of 128 tokens; map: then boxes of a page of K as tree_verify_attn's, else of 16 rows.
-bool weights_by_tiles(int T, int G, bool selected);
+// Whether it goes by tiles of 128 tokens (many query rows, or a table for `most` tokens that is wide); map: then boxes of a page of K as
+// tree_verify_attn's, else of 16 rows.
+bool weights_by_tiles(int T, int G, bool selected, long long most);
 cudaError_t launch_weights_update(const WeightsArgs& a, const CUtensorMap& map, int num_sms, cudaStream_t st);
 
 struct EvictArgs {

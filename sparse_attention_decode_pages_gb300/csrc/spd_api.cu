@@ -1490,7 +1490,8 @@ SPD_API spd_status kv_weights_update(const spd_dims* dims, int32_t T, const spd_
     spd_dims k = *dims;
     if (k.num_phys_pages < 1) k.num_phys_pages = 1;  // (a view of nothing is none; no page of it is read)
     CUtensorMap map;
-    st = weights_by_tiles(T, dims->H_q / dims->H_kv, sel != nullptr) ? page_map(&map, K, k.D, k.page_size, dims->num_phys_pages ? (cuuint64_t)k.num_phys_pages * k.H_kv : 1)
+    st = weights_by_tiles(T, dims->H_q / dims->H_kv, sel != nullptr, (long long)k.max_pages_per_seq * k.page_size)
+             ? page_map(&map, K, k.D, k.page_size, dims->num_phys_pages ? (cuuint64_t)k.num_phys_pages * k.H_kv : 1)
                                                                       : kv_map(&map, K, &k, 16);
     if (st != SPD_OK) return st;
     cudaError_t e = launch_weights_update(a, map, d->sms, static_cast<cudaStream_t>(stream));

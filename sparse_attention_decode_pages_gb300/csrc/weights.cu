@@ -28,6 +28,9 @@ constexpr int kStages = 2;  // of a warp's ring
 // many heads 75 -> 47; one sequence of 1,000, 28 rows 4.2 -> 4.8.  (16 rows: 87.4 / 82.6, but 64 sequences of 1 to 2,000 tokens 28.1 / 31.3,
 // and one of 4,099 with 4 rows 6.4 / 8.3, which is the commonest call.)
 constexpr int kFewRows = 16;
+// So do any rows where the page table has room for this many tokens: few rows' runs follow the table's width (4 rows, 8 sequences of
+// 4,000 tokens in a table for 131,072: 36 us, so 28; one of 131,001: 55, so 49).
+constexpr int kWideTable = 32768;
 constexpr size_t kMostSmem = 226 * 1024;
 constexpr int kLeastRun = 16 * kWarps, kMostRun = 32 * kLeastRun;  // tokens of a CTA: up to 32 tiles a warp, one a lane
 
@@ -272,7 +275,7 @@ struct Tiles {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kTileThreads, 2) tiles_kernel(const WeightsArgs a, const __grid_constant__ CUtensorMap map, int rows_padded, int runs, int) {
+__global__ void __launch_bounds__(kTileThreads, 2) tiles_kernel(const WeightsArgs a, const __grid_constant__ CUtensorMap map, int rows_padded, int runs, int parts) {
     using C = Tiles<D>;
     constexpr int STAGES = C::STAGES;
     extern __shared__ uint8_t smem_raw[];
@@ -309,8 +312,9 @@ __global__ void __launch_bounds__(kTileThreads, 2) tiles_kernel(const WeightsArg
         return;
     }
     // the sequence's tokens in equal runs whatever the table's width (4,000 tokens in a table for 131,072: 6.4 us; in runs of that
-    // width's 19.8), no longer ones than the host has counted on
-    const int run_tokens = max(2 * kTileTokens, ((len + runs - 1) / runs + kTileTokens - 1) / kTileTokens * kTileTokens), t0 = run * run_tokens;
+    // width's 19.8): as many as fill the GPU, or of 1,024 tokens, and no more than there are CTAs
+    const int many = min(runs, max(parts, (len + 1023) >> 10));
+    const int run_tokens = max(2 * kTileTokens, ((len + many - 1) / many + kTileTokens - 1) / kTileTokens * kTileTokens), t0 = run * run_tokens;
     if (t0 >= len) return;
     if (warp == 9) tmem_alloc(&s_tmem, 2 * kTileRows);
     const int fresh = len - N;  // the first token without a weight of its own
@@ -472,7 +476,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) tiles_kernel(const WeightsArg
 template <int D>
 cudaError_t launch(const WeightsArgs& a, const CUtensorMap& map, int num_sms, cudaStream_t st) {
     static std::atomic<bool> known[64][3];
-    const bool tiles = weights_by_tiles(a.T, a.H_q / a.H_kv, a.sel != nullptr);
+    const bool tiles = weights_by_tiles(a.T, a.H_q / a.H_kv, a.sel != nullptr, (long long)a.max_pages * a.ps);
     const int kind = tiles ? 2 : a.sel ? 1 : 0, step = tiles ? 16 : 8;
     const int padded = (a.T * (a.H_q / a.H_kv) + step - 1) / step * step;
     size_t smem = 1024 + (size_t)kWarps * kStages * 16 * D * 2 + (size_t)padded * (D * 2 + 16 + 8);
@@ -493,13 +497,18 @@ cudaError_t launch(const WeightsArgs& a, const CUtensorMap& map, int num_sms, cu
     // two rounds of two CTAs an SM, or more (8 sequences of 2K-4K tokens, 4 rows: 17 us; for four rounds 27.6; 64 of 8K-16K: the same);
     // of the tiles' CTAs, which start more slowly, one an SM (8 sequences of 2K-4K tokens, 28 rows: 15.7 us; two an SM 17.9, four 21.5)
     while (run > (tiles ? 2 * kTileTokens : kLeastRun) && rows * runs_of(run) < (tiles ? 1 : 4) * num_sms) run /= 2;
-    const long long runs = runs_of(run);
-    return launch_pdl(kern, dim3((unsigned)(rows * runs)), dim3(tiles ? kTileThreads : kThreads), smem, st, a, map, padded, (int)runs, run);
+    long long runs = runs_of(run), parts = run;
+    if (tiles) {  // (a CTA without tokens costs some 0.1 us on each SM: a wide table's rows have fewer CTAs, with longer runs)
+        parts = (2 * num_sms + rows - 1) / rows;
+        const long long enough = 16LL * num_sms / rows > parts ? 16LL * num_sms / rows : parts;
+        if (runs > enough) runs = enough;
+    }
+    return launch_pdl(kern, dim3((unsigned)(rows * runs)), dim3(tiles ? kTileThreads : kThreads), smem, st, a, map, padded, (int)runs, (int)parts);
 }
 
 }  // namespace
 
-bool weights_by_tiles(int T, int G, bool selected) { return !selected && T * G > kFewRows; }
+bool weights_by_tiles(int T, int G, bool selected, long long most) { return !selected && (T * G > kFewRows || most >= kWideTable); }
 
 cudaError_t launch_weights_update(const WeightsArgs& a, const CUtensorMap& map, int num_sms, cudaStream_t st) {
     if (a.B <= 0) return cudaSuccess;
