@@ -33,7 +33,7 @@ __device__ __forceinline__ u64 fixed40(float v) {
 // or +inf, so a result below 2^30 is always the exact floor(2^40 v).
 __device__ __forceinline__ unsigned fixed40_u32(float v) { return __float2uint_rz(v * 1099511627776.0f); }
 
-// floor(u * total) for a float u in [0, 1), exactly: u = m * 2^-shift
+// floor(u * total) for a float u >= 0, exactly: u = m * 2^-shift.  2^64 and more: 2^64 - 1, past any total.
 __device__ __forceinline__ u64 scaled_floor(float u, u64 total) {
     const unsigned bits = __float_as_uint(u);
     const unsigned E = (bits >> 23) & 0xffu;
@@ -50,6 +50,7 @@ __device__ __forceinline__ u64 scaled_floor(float u, u64 total) {
     const u64 lo = m * total, hi = __umul64hi(m, total);
     if (shift >= 128) return 0ull;
     if (shift >= 64) return hi >> (shift - 64);
+    if (hi >> shift) return ~0ull;
     return (lo >> shift) | (hi << (64 - shift));
 }
 

@@ -1,0 +1,42 @@
+"""Tree verification and acceptance where few calls go: numbers of one and more, short wait limits, many sequences, many parts,
+long sums."""
+import numpy as np
+import pytest
+
+from tests import tree_reference as ref
+from tests.test_gpu_rope import dev, host
+from tests.test_gpu_tree import attend, case, check_accept, check_case
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def spd():
+    import sparse_attention_decode_pages_gb300 as spd
+    spd.spd_device_status(clear=True)
+    return spd
+
+
+@pytest.mark.parametrize("u", [1.0, 8.0, 2.0 ** 21, 2.0 ** 22, 1.5 * 2.0 ** 22, 2.0 ** 23, 3e38])
+def test_spec_accept_tree_numbers_of_one_and_more(spd, u):
+    """A number of 1 or more takes no child and draws the last token of positive weight, also where its product with the
+    row's sum passes 64 bits (2^22 times four weights of 2^40 is 2^64)."""
+    T, n = 3, 7
+    q = np.zeros((3, T, n), np.float32)
+    q[0, :, :4] = 1.0
+    q[1, :, :5] = 1.0
+    q[2, :, 2] = 0.75
+    draft, parents = np.tile([0, 2, 1], (3, 1)), np.tile([-1, 0, 0], (3, 1))
+    got = check_accept(spd, q, draft, parents, np.full((3, T), u, np.float32), np.full(3, u, np.float32))
+    assert got[0].tolist() == [1, 1, 1] and got[2][:, 0].tolist() == [3, 4, -1]
+    assert spd.spd_device_status(clear=True) == 0
+
+
+@pytest.mark.parametrize("u", [4.0, 8.0, 24.0])
+def test_spec_accept_tree_numbers_of_one_and_more_long_rows(spd, u):
+    """Row sums of 2^61, the largest there are."""
+    n = 1 << 21
+    q = np.ones((1, 2, n), np.float32)
+    q[0, 1] = 0.0
+    got = check_accept(spd, q, np.array([[0, 5]]), np.array([[-1, 0]]), np.full((1, 2), u, np.float32), np.float32([u]))
+    assert got[0][0] == 1 and got[2][0, 0] == n - 1
