@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) accept_tree_kernel(TreeAccept
     // elements of a warp's run: whole loads
     const int run = ((n + W - 1) / W + kStep - 1) / kStep * kStep;
     const int first = me * run, last = min(n, first + run);
-    const unsigned long long limit = a.wait_ns > kDefaultWaitNs ? a.wait_ns : kDefaultWaitNs;
+    auto limit = [&]() { return a.wait_ns > kDefaultWaitNs ? a.wait_ns : kDefaultWaitNs; };
     if (tid < 2) mbar_init(s_bar + tid, 1);
     if (VEC && lane < kStages) mbar_init(&s_full[warp][lane], 1);
     mbar_fence_init();
@@ -110,6 +110,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) accept_tree_kernel(TreeAccept
     pdl_trigger();
 
     bool ok = true;
+    int flying = 0;  // chunks asked for and not seen yet, from the ring's slot on
     const int chunks = VEC && last > first ? (last - first + kChunk - 1) / kChunk : 0;
     float* ring = ring_all + warp * (kStages * kChunk);
     int slot = 0;  // of the ring's next chunk
@@ -123,24 +124,35 @@ __global__ void __launch_bounds__(kThreads, kCtas) accept_tree_kernel(TreeAccept
         bulk_load(ring + to * kChunk, rows + (long long)node * n + x, bytes, &s_full[warp][to]);
     };
     auto ask_first = [&](int node) {
-        if (VEC && lane == 0)
+        if (!VEC) return;
+        if (lane == 0)
             for (int c = 0; c < min(kStages, chunks); ++c) ask(node, c, (slot + c) % kStages);
+        flying = min(kStages, chunks);
     };
     auto next_chunk = [&]() {
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&s_full[warp][slot], parity, a.status, limit));
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&s_full[warp][slot], parity, a.status, a.wait_ns));
+        return ok;
     };
     auto advance = [&]() {
+        --flying;
         if (++slot == kStages) {
             slot = 0;
             parity ^= 1u;
+        }
+    };
+    // copies land before their memory is given back, also those that nobody reads
+    auto drain = [&]() {
+        while (flying > 0) {
+            mbar_wait_bounded(&s_full[warp][slot], parity, a.status, limit());
+            advance();
         }
     };
     // this warp's part of a row's sum; the first chunks have been asked for
     auto run_sum = [&](int node) {
         u64 sum = 0;
         if (VEC) {
-            for (int c = 0; c < chunks && ok; ++c) {
-                next_chunk();
+            for (int c = 0; c < chunks; ++c) {
+                if (!next_chunk()) break;
                 const int left = last - first - c * kChunk;
                 float4 v[kChunk / kStep];
 #pragma unroll
@@ -149,7 +161,10 @@ __global__ void __launch_bounds__(kThreads, kCtas) accept_tree_kernel(TreeAccept
                     if (i * kStep + lane * 4 < left) v[i] = *reinterpret_cast<const float4*>(ring + slot * kChunk + i * kStep + lane * 4);
                 }
                 __syncwarp();  // the chunk has been read
-                if (lane == 0 && c + kStages < chunks) ask(node, c + kStages, slot);
+                if (c + kStages < chunks) {
+                    if (lane == 0) ask(node, c + kStages, slot);
+                    ++flying;
+                }
                 GridSum g;
 #pragma unroll
                 for (int i = 0; i < kChunk / kStep; ++i) {
@@ -202,6 +217,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) accept_tree_kernel(TreeAccept
             a.tokens[(long long)b * T + tid] = -1;
             if (tid == 0) a.n_path[b] = 0;
         }
+        drain();
         return;
     }
 
@@ -228,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) accept_tree_kernel(TreeAccept
             w2[i] = child && tk[i] >= 0 ? s_w[c] : 0;
         }
         const int guess = kids[0] ? __ffs((int)kids[0]) - 1 : kids[1] ? __ffs((int)kids[1]) + 31 : -1;
-        if (guess >= 0 && count > 0) ask_first(guess);  // (the first rows of all sequences have the memory to themselves)
+        if (ok && guess >= 0 && count > 0) ask_first(guess);  // (the first rows of all sequences have the memory to themselves)
         for (unsigned k = kids[0]; k; k &= k - 1) {
             const int c = __ffs((int)k) - 1, x = __shfl_sync(0xffffffffu, tk[0], c);
 #pragma unroll
@@ -246,8 +262,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) accept_tree_kernel(TreeAccept
             pre[1] = all + in - w2[1];
             all += __shfl_sync(0xffffffffu, in, 31);
         }
-        // (never a shorter limit than the usual one: what is on its way to a CTA lands before it ends)
-        ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(s_bar + turn, (uint32_t)count >> 1 & 1u, a.status, limit));
+        // (never a shorter limit than the usual one: a sum that is on its way to a CTA lands before it ends)
+        ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(s_bar + turn, (uint32_t)count >> 1 & 1u, a.status, limit()));
         if (!ok) break;
         u64 total = 0;
         for (int i = lane; i < W; i += 32) total += s_sums[turn][i];
@@ -268,15 +284,14 @@ __global__ void __launch_bounds__(kThreads, kCtas) accept_tree_kernel(TreeAccept
             if (lane + 32 * i == count) my_path[i] = node;
         ++count;
         left = total - all;
-        if (VEC && guess >= 0 && count > 1 && next != guess)  // what was asked for in vain
-            for (int c = 0; c < min(kStages, chunks) && ok; ++c) {
-                next_chunk();
-                advance();
-            }
-        if (next < 0 || !ok) break;
+        if (next < 0) break;
+        if (next != guess)  // what was asked for in vain
+            while (flying > 0 && next_chunk()) advance();
         node = next;
-        if (next != guess || count == 1) ask_first(next);
-        sum = run_sum(next);
+        if (ok) {
+            if (next != guess || count == 1) ask_first(next);
+            sum = run_sum(next);
+        }
     }
 
     if (ok && rank == 0 && warp == 0) {
@@ -361,6 +376,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) accept_tree_kernel(TreeAccept
             }
         }
     }
+    drain();
     cluster.sync();  // no CTA ends while another may still send to it
 }
 

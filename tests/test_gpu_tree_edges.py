@@ -40,3 +40,48 @@ def test_spec_accept_tree_numbers_of_one_and_more_long_rows(spd, u):
     q[0, 1] = 0.0
     got = check_accept(spd, q, np.array([[0, 5]]), np.array([[-1, 0]]), np.full((1, 2), u, np.float32), np.float32([u]))
     assert got[0][0] == 1 and got[2][0, 0] == n - 1
+
+
+def walks(B, T, n):
+    """Arguments of spec_accept_tree with walks of several steps, made on the GPU."""
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    q = torch.rand((B, T, n), generator=gen, device="cuda") ** 8
+    draft = torch.randint(0, n, (B, T), generator=gen, device="cuda")
+    parents = torch.clamp(torch.arange(T, device="cuda") - 1, min=-1) // 2
+    parents[0] = -1
+    parents = parents.repeat(B, 1)
+    for x in range(1, T):  # a token proposed weighs more than all others together
+        q[torch.arange(B), parents[:, x], draft[:, x]] = 0.3 * n
+    q /= q.sum(2, keepdim=True)
+    u_acc, u_res = (torch.rand(shape, generator=gen, device="cuda") for shape in ((B, T), (B,)))
+    return q, draft.to(torch.int32), parents.to(torch.int32).contiguous(), u_acc, u_res
+
+
+def accepted(spd, *args):
+    import torch
+    B, T = args[1].shape
+    out = [torch.full(shape, -9, dtype=torch.int32, device="cuda") for shape in ((B,), (B, T), (B, T))]
+    spd.spec_accept_tree(*args, *out)
+    return out
+
+
+@pytest.mark.parametrize("B,T,n", [(64, 15, 151936), (3, 8, 151936), (400, 5, 32000), (20, 6, 4099)])
+def test_spec_accept_tree_with_waits_that_run_out(spd, B, T, n):
+    """A limit that no copy meets: the calls return with the timeout bit (or, should every copy be early, clean), and later calls
+    with the usual limit are those of before."""
+    import torch
+    args = walks(B, T, n)
+    want = accepted(spd, *args)
+    assert spd.spd_device_status(clear=True) == 0 and int(want[0].max()) > 2  # (five nodes in pairs are three deep)
+    usual = spd.spd_wait_limit_ns()
+    try:
+        spd.spd_set_wait_limit_ns(1)
+        for _ in range(2):
+            accepted(spd, *args)
+            assert spd.spd_device_status(clear=True) & ~spd.DEV_TIMEOUT == 0
+    finally:
+        spd.spd_set_wait_limit_ns(usual)
+    for got, x in zip(accepted(spd, *args), want):
+        assert torch.equal(got, x)
+    assert spd.spd_device_status(clear=True) == 0
