@@ -622,7 +622,8 @@ spd_status tree_verify_attn(const spd_dims *dims, int32_t T, const spd_bf16 *q, 
  * nodes, then -1; tokens int32 [B][T], what follows each of them (the next one's draft, at last
  * the drawn token), then -1.  Where node 0 is not a root, n_path = 0 and all else is -1.
  * A draft outside [0, n_vocab) that is tried is not taken and sets SPD_DEV_BAD_TOKEN.
- * Waits of a sequence's CTAs for one another have the default limit at least (SPD_DEV_TIMEOUT behind it).
+ * A sequence with a copy that does not come within the limit keeps its n_path, path and tokens as they were (SPD_DEV_TIMEOUT);
+ * waits of a sequence's CTAs for one another have the default limit at least.
  * Supported: 1 <= T <= 64, 1 <= n_vocab <= 2^21, B * 16 < 2^31; q_target 16-byte aligned.
  */
 spd_status spec_accept_tree(int32_t B, int32_t T, int32_t n_vocab, const float *q_target,

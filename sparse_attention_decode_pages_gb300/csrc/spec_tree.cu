@@ -54,13 +54,23 @@ __device__ __forceinline__ float4 load4(const float* row, long long x, long long
     return v;
 }
 
-// The sum of the lanes' numbers below 2^62: 22 bits at a time, each by one reduction.
-__device__ __forceinline__ u64 warp_sum(u64 v) {
+// The sum of the lanes' numbers below 2^62: 22 bits at a time, each by one reduction; top: what their bits from 44 on add up to.
+__device__ __forceinline__ u64 warp_sum(u64 v, unsigned& top) {
     const unsigned m = (1u << 22) - 1u;
     const unsigned a = __reduce_add_sync(0xffffffffu, (unsigned)v & m), b = __reduce_add_sync(0xffffffffu, (unsigned)(v >> 22) & m);
-    const unsigned c = __reduce_add_sync(0xffffffffu, (unsigned)(v >> 44));
-    return a + ((u64)b << 22) + ((u64)c << 44);
+    top = __reduce_add_sync(0xffffffffu, (unsigned)(v >> 44));
+    return a + ((u64)b << 22) + ((u64)top << 44);
 }
+__device__ __forceinline__ u64 warp_sum(u64 v) {
+    unsigned top;
+    return warp_sum(v, top);
+}
+
+// What a warp sends that has no sum, because its copies were late.  A row's sum is at most 2^61, so a total above that (by its
+// bits from 44 on) has one in it; a lane adds up four at most, 2^64 - 2^62.
+constexpr u64 kNoSum = 3ull << 60;
+constexpr unsigned kMostTop = 1u << 17;
+static_assert(kMaxWarps / 32 <= 4, "a lane's sums");
 
 // The sum of the lanes up to this one.
 __device__ __forceinline__ u64 warp_scan(u64 v, int lane) {
@@ -110,7 +120,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) accept_tree_kernel(TreeAccept
     pdl_trigger();
 
     bool ok = true;
-    int flying = 0;  // chunks asked for and not seen yet, from the ring's slot on
+    int flying = 0;  // chunks that were asked for and that no sum waits for, from the ring's slot on
     const int chunks = VEC && last > first ? (last - first + kChunk - 1) / kChunk : 0;
     float* ring = ring_all + warp * (kStages * kChunk);
     int slot = 0;  // of the ring's next chunk
@@ -124,17 +134,14 @@ __global__ void __launch_bounds__(kThreads, kCtas) accept_tree_kernel(TreeAccept
         bulk_load(ring + to * kChunk, rows + (long long)node * n + x, bytes, &s_full[warp][to]);
     };
     auto ask_first = [&](int node) {
-        if (!VEC) return;
-        if (lane == 0)
+        if (VEC && lane == 0)
             for (int c = 0; c < min(kStages, chunks); ++c) ask(node, c, (slot + c) % kStages);
-        flying = min(kStages, chunks);
     };
     auto next_chunk = [&]() {
         ok = __all_sync(0xffffffffu, mbar_wait_bounded(&s_full[warp][slot], parity, a.status, a.wait_ns));
         return ok;
     };
     auto advance = [&]() {
-        --flying;
         if (++slot == kStages) {
             slot = 0;
             parity ^= 1u;
@@ -142,7 +149,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) accept_tree_kernel(TreeAccept
     };
     // copies land before their memory is given back, also those that nobody reads
     auto drain = [&]() {
-        while (flying > 0) {
+        for (; flying > 0; --flying) {
             mbar_wait_bounded(&s_full[warp][slot], parity, a.status, limit());
             advance();
         }
@@ -152,7 +159,10 @@ __global__ void __launch_bounds__(kThreads, kCtas) accept_tree_kernel(TreeAccept
         u64 sum = 0;
         if (VEC) {
             for (int c = 0; c < chunks; ++c) {
-                if (!next_chunk()) break;
+                if (!next_chunk()) {
+                    flying = min(kStages, chunks - c);
+                    break;
+                }
                 const int left = last - first - c * kChunk;
                 float4 v[kChunk / kStep];
 #pragma unroll
@@ -161,10 +171,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) accept_tree_kernel(TreeAccept
                     if (i * kStep + lane * 4 < left) v[i] = *reinterpret_cast<const float4*>(ring + slot * kChunk + i * kStep + lane * 4);
                 }
                 __syncwarp();  // the chunk has been read
-                if (c + kStages < chunks) {
-                    if (lane == 0) ask(node, c + kStages, slot);
-                    ++flying;
-                }
+                if (lane == 0 && c + kStages < chunks) ask(node, c + kStages, slot);
                 GridSum g;
 #pragma unroll
                 for (int i = 0; i < kChunk / kStep; ++i) {
@@ -230,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) accept_tree_kernel(TreeAccept
         const int turn = count & 1;
         const uint32_t bar = smem_u32(s_bar + turn);
         if (tid == 0) mbar_arrive_expect_tx(s_bar + turn, W * 8);
-        if (lane < size) send(remote(smem_u32(s_sums[turn] + me), lane), sum, remote(bar, lane));
+        if (lane < size) send(remote(smem_u32(s_sums[turn] + me), lane), ok ? sum : kNoSum, remote(bar, lane));
         // while the sums are on their way: this lane's two nodes, if they are children of the node
         int tk[2];
         unsigned kids[2];
@@ -244,7 +251,10 @@ __global__ void __launch_bounds__(kThreads, kCtas) accept_tree_kernel(TreeAccept
             w2[i] = child && tk[i] >= 0 ? s_w[c] : 0;
         }
         const int guess = kids[0] ? __ffs((int)kids[0]) - 1 : kids[1] ? __ffs((int)kids[1]) + 31 : -1;
-        if (ok && guess >= 0 && count > 0) ask_first(guess);  // (the first rows of all sequences have the memory to themselves)
+        if (ok && guess >= 0 && count > 0) {  // (the first rows of all sequences have the memory to themselves)
+            ask_first(guess);
+            flying = min(kStages, chunks);
+        }
         for (unsigned k = kids[0]; k; k &= k - 1) {
             const int c = __ffs((int)k) - 1, x = __shfl_sync(0xffffffffu, tk[0], c);
 #pragma unroll
@@ -267,7 +277,10 @@ __global__ void __launch_bounds__(kThreads, kCtas) accept_tree_kernel(TreeAccept
         if (!ok) break;
         u64 total = 0;
         for (int i = lane; i < W; i += 32) total += s_sums[turn][i];
-        total = warp_sum(total);
+        unsigned top;
+        total = warp_sum(total, top);
+        ok = top <= kMostTop;  // (the same for all warps of the cluster)
+        if (!ok) break;
         // the children in order: each is tried on what the earlier ones leave
         const unsigned p0 = __ballot_sync(0xffffffffu, w2[0] && scaled_floor(s_u[lane], total - pre[0]) < w2[0]);
         unsigned p1 = 0;
@@ -286,9 +299,10 @@ __global__ void __launch_bounds__(kThreads, kCtas) accept_tree_kernel(TreeAccept
         left = total - all;
         if (next < 0) break;
         if (next != guess)  // what was asked for in vain
-            while (flying > 0 && next_chunk()) advance();
+            for (; flying > 0 && next_chunk(); --flying) advance();
         node = next;
         if (ok) {
+            flying = 0;
             if (next != guess || count == 1) ask_first(next);
             sum = run_sum(next);
         }

@@ -85,3 +85,25 @@ def test_spec_accept_tree_with_waits_that_run_out(spd, B, T, n):
     for got, x in zip(accepted(spd, *args), want):
         assert torch.equal(got, x)
     assert spd.spd_device_status(clear=True) == 0
+
+
+@pytest.mark.parametrize("B,T,n", [(64, 15, 151936), (3, 8, 151936), (400, 5, 32000)])
+@pytest.mark.parametrize("limit_ns", [1, 3000])
+def test_spec_accept_tree_writes_nothing_of_a_sequence_whose_copies_are_late(spd, B, T, n, limit_ns):
+    """Whatever the limit, a sequence's outputs are those of the usual one, or left as they were with the timeout bit set."""
+    args = walks(B, T, n)
+    want = [x.cpu().numpy() for x in accepted(spd, *args)]
+    assert spd.spd_device_status(clear=True) == 0
+    usual = spd.spd_wait_limit_ns()
+    try:
+        spd.spd_set_wait_limit_ns(limit_ns)
+        for _ in range(6):
+            got = [x.cpu().numpy() for x in accepted(spd, *args)]
+            status = spd.spd_device_status(clear=True)
+            late = got[0] == -9
+            assert np.all(got[1][late] == -9) and np.all(got[2][late] == -9)
+            for x, y in zip(got, want):
+                assert np.array_equal(x[~late], y[~late])
+            assert status == (spd.DEV_TIMEOUT if late.any() else 0), (status, late.sum())
+    finally:
+        spd.spd_set_wait_limit_ns(usual)
