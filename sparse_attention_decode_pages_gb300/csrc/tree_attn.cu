@@ -188,6 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ Share s_share;
     __shared__ uint32_t s_tmem;
     __shared__ unsigned long long s_odd[kOdd];  // nodes of a piece's tree whose values are not all finite
+    __shared__ int s_asked;                     // tiles whose values have been asked for
     uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
     uint64_t* empty = full + STAGES;
@@ -222,6 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(level, 8);
         mbar_init(drain, 1);
         mbar_fence_init();
+        s_asked = 0;
     }
     if (warp == 8 && elect_one()) {
         tma_prefetch_desc(&maps.q);
@@ -675,6 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     asked |= 1u << slot;
+                    if (value && lane == 0) *reinterpret_cast<volatile int*>(&s_asked) = base / 2 + j + 1;
                     if (lane == slot) asked_item = item;
                     asked_parity = (asked_parity & ~(1u << slot)) | ((uint32_t)(item / STAGES) & 1u) << slot;
                 }
@@ -842,6 +845,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the latter get them back at the end.
             uint32_t v_parity = 0;  // of each slot: bits
             int base = 0, piece = 0;
+            // A piece's nodes come behind all of its tiles: the limit counts from the last tile that was asked for.
+            auto wait_nodes = [&](uint64_t* bar, uint32_t parity) {
+                int asked = -1;
+                unsigned long long since = 0;
+                while (!mbar_try_wait(bar, parity)) {
+                    const int now_asked = *reinterpret_cast<volatile int*>(&s_asked);
+                    const unsigned long long now = globaltimer_ns();
+                    if (now_asked != asked) {
+                        asked = now_asked;
+                        since = now;
+                    } else if (now - since > a.wait_ns) {
+                        raise_status(a.status, SPD_DEV_TIMEOUT);
+                        return false;
+                    }
+                }
+                return true;
+            };
             Piece p;
             while (w.next(a, sh, p)) {
                 base += 2 * (p.t1 - p.t0);
@@ -850,7 +870,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     unsigned long long m[2];
                     if (!tree_masks(a.parents + (long long)p.b * a.T, a.T, m) && lane == 0 && p.sub == 0) raise_status(a.status, SPD_DEV_BAD_TREE);
                     const unsigned long long gone = (unsigned long long)__ballot_sync(0xffffffffu, m[1] == 0) << 32 | __ballot_sync(0xffffffffu, m[0] == 0);
-                    if (!__all_sync(0xffffffffu, mbar_wait_bounded(v_tree + slot, v_parity >> slot & 1u, a.status, a.wait_ns))) break;
+                    if (!__all_sync(0xffffffffu, wait_nodes(v_tree + slot, v_parity >> slot & 1u))) break;
                     v_parity ^= 1u << slot;
                     uint8_t* rows = smem + C::OFF_RING + slot * C::TILE;
                     unsigned long long odd = 0;

@@ -107,3 +107,36 @@ def test_spec_accept_tree_writes_nothing_of_a_sequence_whose_copies_are_late(spd
             assert status == (spd.DEV_TIMEOUT if late.any() else 0), (status, late.sum())
     finally:
         spd.spd_set_wait_limit_ns(usual)
+
+
+def test_tree_verify_attn_a_limit_shorter_than_a_part(spd):
+    """A limit is one of a single wait: a part of 65,536 tokens takes many times the limit, no copy in it does."""
+    import torch
+    B, T, H_q, H_kv, D, ps, n = 19, 32, 64, 8, 128, 16, 65536
+    dims = spd.dims_of(B, H_q, H_kv, D, ps, n // ps, n // ps)
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    r = lambda *shape: torch.randn(shape, generator=gen, device="cuda", dtype=torch.bfloat16)
+    K, V = r(n // ps, H_kv, ps, D), r(n // ps, H_kv, ps, D)
+    pt = torch.arange(n // ps, dtype=torch.int32, device="cuda").repeat(B, 1)  # all sequences over the same pages
+    lens = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    parents = dev(np.tile(ref.random_tree(np.random.default_rng(0), T).astype(np.int32), (B, 1)))
+    args = (dims, T, r(B, T, H_q, D), K, V, pt, lens, r(B, T, H_kv, D), r(B, T, H_kv, D), parents)
+    ws = spd.workspace(spd.spd_tree_verify_workspace_size(dims, T))
+    want = attend(spd, *args, ws=ws)
+    begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    begin.record()
+    attend(spd, *args, ws=ws)
+    end.record()
+    assert spd.spd_device_status(clear=True) == 0
+    limit_ns = 200_000
+    assert begin.elapsed_time(end) * 1e6 > 2 * limit_ns  # (one part a CTA)
+    usual = spd.spd_wait_limit_ns()
+    try:
+        spd.spd_set_wait_limit_ns(limit_ns)
+        for _ in range(3):
+            got = attend(spd, *args, ws=ws)
+            assert spd.spd_device_status(clear=True) == 0
+            for x, y in zip(got, want):
+                assert torch.equal(x, y)
+    finally:
+        spd.spd_set_wait_limit_ns(usual)
