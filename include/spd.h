@@ -590,8 +590,7 @@ spd_status token_logprobs(int64_t rows, int32_t n_vocab, const void *logits, int
  * What is no node may hold anything in its rows of q, k_tree and v_tree, and what lies in a page behind the length
  * may too; a node's infinities and NaN reach only the rows that see it, those of a cached value every row of its
  * sequence and head.
- * Many cached tokens of one sequence and head that one CTA goes over (more of them where the call has many rows) lower the
- * sums of values of one sign: by 0.01 % at 2^17 tokens, 0.07 % at 2^20.
+ * The sums of values of one sign come out low by up to 0.01 % where a sequence is long, whatever its length.
  * Supported: 1 <= T <= 64, B * H_kv <= 16384, max_pages_per_seq * page_size <= 2^30.  The workspace needs no zeros.
  */
 size_t spd_tree_verify_workspace_size(const spd_dims *dims, int32_t T);

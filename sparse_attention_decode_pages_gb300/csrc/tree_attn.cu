@@ -15,8 +15,10 @@
 // memory.
 //
 // The softmax goes by a reference that follows the row's maximum only when that has grown by 2^8 beyond it, so O
-// is rarely rescaled; sums are fp32, the weights that multiply V are rounded to bf16 (V's type,
-// as the products want them), 2^-8 of a weight at most and of either sign.
+// is rarely rescaled; sums are fp32, a tile's by itself first, the weights that multiply V are rounded to bf16 (V's type,
+// as the products want them), 2^-8 of a weight at most and of either sign.  O adds up in tensor memory for 65,536 tokens of a stream and
+// then in an fp32 sum in the workspace, or what the tensor cores cut grows with the length (means of 2^20 tokens were up to 0.4 % low,
+// of 2^24 6 %; now 0.01 %, at no cost: a pass over O in 512 tiles).
 //
 // One CTA an SM: two warpgroups for the softmax, and a warp each for the keys' copies, the values' copies, the products
 // and the nodes' values.  A page's keys or values of a KV head are one TMA box.  A sequence that ends inside a page has that page
@@ -60,6 +62,9 @@ constexpr int kFewUnits = 4;
 // 119 -> 88 us; 64 of 0 to 2,000, 64 nodes: 121 -> 88; with five instead of three the same).
 constexpr int kUnitTiles = 3;
 constexpr float kLag = 8.f;         // powers of two that a maximum may lie above the reference
+// Tiles of a stream whose products add up in tensor memory (a power of two).  The tensor cores cut what lies about 2^-25 below a sum,
+// so O goes to an fp32 sum in the workspace every so many and starts again.
+constexpr int kAside = 512;
 
 template <int D>
 struct Cfg {
@@ -383,8 +388,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool there = row < sh.tpt * sh.G && node < a.T;
                 const unsigned long long m_lo = __shfl_sync(0xffffffffu, tree[0], node & 31), m_hi = __shfl_sync(0xffffffffu, tree[1], node & 31);
                 const unsigned long long mask = !there ? 0 : node < 32 ? m_lo : m_hi;
-                float ref = NEG_INF;
-                float2 l0 = make_float2(0.f, 0.f), l1 = l0;
+                float ref = NEG_INF, sum = 0.f;
+                // outputs, or the partial of slot 2 i (a unit that began before this share) or 2 i + 1; until then what this row has put aside
+                const int slot = 2 * (int)blockIdx.x + (p.t0 == 0 ? 1 : 0);
+                auto aside = [&]() { return reinterpret_cast<float4*>(part_o) + (size_t)slot * kSlotRows * (D / 4) + s * kRows + row; };
+                auto aside_ml = [&]() { return part_ml + (size_t)slot * kSlotRows + s * kRows + row; };
                 for (int j = two ? 0 : s; j < n; j += step) {
                     const int t = p.t0 + j;
                     if (!wait(s_full + s, s_parity)) break;
@@ -423,15 +431,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
                     const bool moves = most > ref + kLag;
-                    if (__any_sync(0xffffffffu, moves)) {
+                    const int i_s = j >> (step - 1);  // the stream's tile
+                    const bool full_up = i_s > 0 && (i_s & (kAside - 1)) == 0;
+                    if (full_up || __any_sync(0xffffffffu, moves)) {
                         const float now = moves ? most : ref;
                         const float corr = moves ? fast_exp2(ref - now) : 1.f;
                         ref = now;
-                        l0.x *= corr;
-                        l0.y *= corr;
-                        l1.x *= corr;
-                        l1.y *= corr;
-                        if (j >= step) {  // O of the tiles before; their products are done, as S's is
+                        sum *= corr;
+                        if (full_up) {  // put aside, at the new reference; the next product starts from nothing
+                            const bool more = i_s > kAside;
+                            const float2 ml = more ? *aside_ml() : make_float2(NEG_INF, 0.f);
+                            const float w = ml.x == NEG_INF ? 0.f : fast_exp2(ml.x - ref);
+                            *aside_ml() = make_float2(ref, sum + (ml.x == NEG_INF ? ml.y : ml.y * w));
+                            sum = 0.f;
+                            float4* at = aside();
+#pragma unroll 1
+                            for (int i = 0; i < D; i += 16) {
+                                uint32_t o[16];
+                                tmem_ld(tm_o + s * 128 + i, o);
+                                tmem_wait_ld();
+                                tmem_loaded(o);
+#pragma unroll
+                                for (int c = 0; c < 16; c += 4, at += kSlotRows) {
+                                    const float4 x = more ? *at : make_float4(0.f, 0.f, 0.f, 0.f);
+                                    *at = make_float4(fmaf(__uint_as_float(o[c]), corr, x.x * w), fmaf(__uint_as_float(o[c + 1]), corr, x.y * w),
+                                                      fmaf(__uint_as_float(o[c + 2]), corr, x.z * w), fmaf(__uint_as_float(o[c + 3]), corr, x.w * w));
+                                }
+                            }
+                        } else if (j >= step) {  // O of the tiles before; their products are done, as S's is
 #pragma unroll 1
                             for (int i = 0; i < D; i += 16) {
                                 uint32_t o[16];
@@ -446,6 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     const float neg = ref == NEG_INF ? 0.f : -ref;
                     const float2 scale2 = make_float2(scale, scale), neg2 = make_float2(neg, neg);
+                    float2 l0 = make_float2(0.f, 0.f), l1 = l0;  // of this tile
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         uint32_t w16[16];
@@ -463,13 +491,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(p_full + s);
+                    sum += l0.x + l0.y + (l1.x + l1.y);
                 }
                 if (!ok) break;
                 tiles_done += n;
-                float sum = l0.x + l0.y + (l1.x + l1.y);
                 const bool whole = p.t0 == 0 && p.t1 == p.nt;
-                // outputs, or the partial of slot 2 i (a unit that began before this share) or 2 i + 1
-                const int slot = 2 * (int)blockIdx.x + (p.t0 == 0 ? 1 : 0);
                 const long long out = ((long long)p.b * a.T + node) * a.H_q + h * sh.G + row % sh.G;
                 bf16* o_row = reinterpret_cast<bf16*>(a.o) + out * D;
                 float4* part = reinterpret_cast<float4*>(part_o) + (size_t)slot * kSlotRows * (D / 4) + (two ? s * kRows : 0) + row;
@@ -511,6 +537,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                     o_parity ^= 1u;
                 }
                 tmem_fence_after();
+                if ((two ? n : (n - s + 1) >> 1) > kAside) {  // what was put aside, back to O
+                    const float2 ml = *aside_ml();
+                    const float w = ml.x == NEG_INF ? 0.f : fast_exp2(ml.x - ref);
+                    sum += ml.x == NEG_INF ? ml.y : ml.y * w;
+                    const float4* at = aside();
+#pragma unroll 1
+                    for (int i = 0; i < D; i += 16) {
+                        uint32_t o[16];
+                        tmem_ld(tm_o + s * 128 + i, o);
+                        tmem_wait_ld();
+                        tmem_loaded(o);
+#pragma unroll
+                        for (int c = 0; c < 16; c += 4, at += kSlotRows) {
+                            const float4 x = *at;
+                            o[c] = __float_as_uint(fmaf(x.x, w, __uint_as_float(o[c])));
+                            o[c + 1] = __float_as_uint(fmaf(x.y, w, __uint_as_float(o[c + 1])));
+                            o[c + 2] = __float_as_uint(fmaf(x.z, w, __uint_as_float(o[c + 2])));
+                            o[c + 3] = __float_as_uint(fmaf(x.w, w, __uint_as_float(o[c + 3])));
+                        }
+                        tmem_st(tm_o + s * 128 + i, o);
+                    }
+                    tmem_wait_st();
+                }
                 // the row's parts: this stream's, or both streams', of which this warpgroup joins half of the channels
                 float w0 = 1.f, w1 = 0.f;
                 if (!two) {
@@ -770,7 +819,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int s = 0; s < 2; ++s) {
                             if (!wait_p(s)) break;
                             if (s == 0 && !wait_item(vi)) break;
-                            values(s, vi, i == 0, tree);
+                            values(s, vi, (i & (kAside - 1)) == 0, tree);
                             if (s == 1) commit(empty + vi % STAGES);
                             if (i + 1 < n) {
                                 if (s == 0 && !wait_item(kn)) break;
@@ -794,7 +843,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = 0; i < n && ok; ++i) {
                         const int s = i & 1, vi = base + min(2 * i + 2, 2 * n - 1), kn = base + 2 * i + 3;  // keys of tile i + 2
                         if (!wait_p(s) || !wait_item(vi)) break;
-                        values(s, vi, i < 2, p.t0 + i == p.nt - 1);
+                        values(s, vi, ((i >> 1) & (kAside - 1)) == 0, p.t0 + i == p.nt - 1);
                         commit(empty + vi % STAGES);
                         if (i + 2 < n) {
                             if (!wait_item(kn)) break;

@@ -5,7 +5,7 @@ import pytest
 
 from tests import tree_reference as ref
 from tests.test_gpu_rope import dev, host
-from tests.test_gpu_tree import attend, case, check_accept, check_case
+from tests.test_gpu_tree import attend, case, check_accept, check_case, check_node
 
 pytestmark = pytest.mark.gpu
 
@@ -140,3 +140,89 @@ def test_tree_verify_attn_a_limit_shorter_than_a_part(spd):
                 assert torch.equal(x, y)
     finally:
         spd.spd_set_wait_limit_ns(usual)
+
+
+@pytest.mark.parametrize("lg_tokens,low,T,G,D", [(17, 1e-4, 32, 8, 64), (20, 7e-4, 32, 8, 64), (22, 1e-4, 32, 8, 64), (21, 1e-4, 29, 8, 128),
+                                                 (20, 1e-4, 4, 4, 128), (22, 1e-4, 5, 3, 64)])
+def test_tree_verify_attn_long_sums_of_one_sign(spd, lg_tokens, low, T, G, D):
+    """Equal logits over 2^17 and more tokens that one CTA goes over: channel c's mean is 1 + m / 64 * 2^-7 for an m that grows with c,
+    so a result is 1 + 2^-7 where the mean, less what the tensor cores cut (`low` of it at most), is above 1 + 2^-8, and 1 where it
+    is below.  (Sums that lose their small parts give 1 everywhere.)"""
+    import torch
+    B, ps, n = 152, 64, 1 << lg_tokens
+    dims = spd.dims_of(B, G, 1, D, ps, n // ps, 1)
+    K = torch.zeros((1, 1, ps, D), dtype=torch.bfloat16, device="cuda")
+    m = np.arange(D) * 64 // D
+    V = (1.0 + (torch.arange(ps, device="cuda")[:, None] < dev(m)) * 2.0 ** -7).to(torch.bfloat16)[None, None].contiguous()
+    pt = torch.zeros((B, n // ps), dtype=torch.int32, device="cuda")
+    lens = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    q = torch.ones((B, T, G, D), dtype=torch.bfloat16, device="cuda")
+    k, v = torch.full((B, T, 1, D), -100.0, dtype=torch.bfloat16, device="cuda"), torch.zeros((B, T, 1, D), dtype=torch.bfloat16, device="cuda")
+    parents = dev(np.tile(np.arange(-1, T - 1, dtype=np.int32), (B, 1)))
+    o, lse = attend(spd, dims, T, q, K, V, pt, lens, k, v, parents)
+    assert spd.spd_device_status(clear=True) == 0
+    mean = 1.0 + m / 64 * 2.0 ** -7
+    o = host(o)
+    assert np.all(np.isin(o, [1.0, 1.0 + 2.0 ** -7]))
+    assert np.all(o[..., mean * (1 - low) > 1.0 + 2.0 ** -8] == 1.0 + 2.0 ** -7)
+    assert np.all(o[..., mean < 1.0 + 2.0 ** -8] == 1.0)
+    # n weights of 1 add up exactly below 2^24; log2 is off by an ulp (2^-19 at most), its product with ln 2 is rounded
+    assert np.abs(host(lse) - lg_tokens * np.log(2.0)).max() <= lg_tokens * 2.0 ** -22
+
+
+@pytest.mark.parametrize("T,G,D,B", [(32, 8, 64, 152), (4, 2, 128, 152), (32, 8, 128, 100), (7, 2, 64, 90)])
+def test_tree_verify_attn_long_sums_of_weights_below_one(spd, T, G, D, B):
+    """2^22 - 5 tokens, one of 64 of them with a larger logit: weights of 0.7 add up as they should, from one reference to a
+    later one (the last token's logit is 15 above all others)."""
+    import torch
+    ps, n = 64, (1 << 22) - 5
+    pages = -(-n // ps)
+    dims = spd.dims_of(B, G, 1, D, ps, pages, 2)
+    K, V = torch.zeros((2, 1, ps, D), dtype=torch.bfloat16, device="cuda"), torch.ones((2, 1, ps, D), dtype=torch.bfloat16, device="cuda")
+    K[:, 0, 0] = 0.35 / D ** 0.5
+    K[1, 0, (n - 1) % ps] = 15.0 / D ** 0.5
+    pt = torch.zeros((B, pages), dtype=torch.int32, device="cuda")
+    pt[:, -1] = 1
+    lens = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    q = torch.ones((B, T, G, D), dtype=torch.bfloat16, device="cuda")
+    k, v = torch.full((B, T, 1, D), -100.0, dtype=torch.bfloat16, device="cuda"), torch.zeros((B, T, 1, D), dtype=torch.bfloat16, device="cuda")
+    o, lse = attend(spd, dims, T, q, K, V, pt, lens, k, v, dev(np.tile(np.arange(-1, T - 1, dtype=np.int32), (B, 1))))
+    assert spd.spd_device_status(clear=True) == 0
+    z = host(K)[:, 0].sum(-1) * D ** -0.5
+    count = np.array([(pages - 1), 1])[:, None] * np.ones(ps)
+    count[1, (n - 1) % ps + 1:] = 0
+    want = np.log((count * np.exp(z)).sum())
+    # logits: D exact products; the exponent's and ex2's 2^-22 and 2^-24 * 15 each; sums of 36 in a tile, 512 tiles, 64 of these
+    # sums and two streams, each off by 2^-24 at most; log2 and its product
+    assert np.abs(host(lse) - want).max() <= (36 + 512 + 64 + 2) * 2.0 ** -24 + 16 * 2.0 ** -22 + 22 * 2.0 ** -22
+    # values of 1: the weights' rounding (2^-9 of each), the tensor cores' cut (1e-4) and the result's rounding
+    assert np.abs(host(o) - 1.0).max() <= 2.0 ** -9 + 1e-4 + 2.0 ** -8
+
+
+@pytest.mark.parametrize("T,G,D,B", [(32, 8, 64, 110), (5, 4, 128, 110)])
+def test_tree_verify_attn_long_sequences_of_any_values(spd, T, G, D, B):
+    """200,001 tokens for each of many sequences (all over the same pages), logits that rise and fall along them, shares that cut
+    most of the sequences."""
+    import torch
+    rng = np.random.default_rng(T)
+    ps, n = 64, 200001
+    pages = -(-n // ps)
+    dims = spd.dims_of(B, G, 1, D, ps, pages, pages)
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    r = lambda *shape: torch.randn(shape, generator=gen, device="cuda", dtype=torch.bfloat16)
+    K, V = r(pages, 1, ps, D), r(pages, 1, ps, D)
+    K *= (1.5 + torch.sin(torch.arange(pages, device="cuda") / 300.0))[:, None, None, None].to(torch.bfloat16)
+    V[pages // 3: pages // 2] += 1.0
+    table = rng.permutation(pages).astype(np.int32)
+    parents = ref.random_tree(rng, T)
+    q, k, v = r(B, T, G, D), r(B, T, 1, D), r(B, T, 1, D)
+    o, lse = attend(spd, dims, T, q, K, V, dev(np.tile(table, (B, 1))), torch.full((B,), n, dtype=torch.int32, device="cuda"), k, v,
+                    dev(np.tile(parents.astype(np.int32), (B, 1))))
+    assert spd.spd_device_status(clear=True) == 0
+    ck, cv = (host(x)[table, 0].reshape(-1, D)[:n] for x in (K, V))
+    sees = ref.sees(parents)
+    for b in (0, 1, B // 2, B - 1):
+        keys, values = (np.concatenate([c, host(x[b, :, 0])]) for c, x in ((ck, k), (cv, v)))
+        for t, hq in ((0, 0), (T - 1, G - 1)):
+            seen = np.concatenate([np.ones(n, bool), sees[t]])
+            check_node(host(o[b, t, hq]), float(lse[b, t, hq]), host(q[b, t, hq]), keys, values, D ** -0.5, seen, (b, t, hq))
