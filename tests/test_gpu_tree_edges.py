@@ -142,6 +142,53 @@ def test_tree_verify_attn_a_limit_shorter_than_a_part(spd):
         spd.spd_set_wait_limit_ns(usual)
 
 
+@pytest.mark.parametrize("B", [385, 800])
+def test_tree_verify_attn_more_sequences_than_a_cta_has_threads(spd, B):
+    """Short sequences of unequal lengths, several empty: a thread's run of them where shares are cut."""
+    rng = np.random.default_rng(B)
+    lens = np.where(rng.random(B) < 0.2, 0, rng.integers(0, 200, B))
+    lens[[0, -1]] = 0, 1500
+    T = 3
+    trees = [ref.random_tree(rng, T, "random", int(rng.integers(0, T + 1))) for _ in range(B)]
+    check_case(spd, *case(spd, rng, lens, T, 2, 1, 64, 16, trees))
+
+
+def test_tree_verify_attn_a_bad_length_among_many_sequences(spd):
+    """The rows of a sequence that the page table has no room for are of no node, all others' bits are those without it."""
+    import torch
+    rng = np.random.default_rng(5)
+    B, T = 500, 4
+    lens = rng.integers(0, 150, B)
+    trees = [ref.random_tree(rng, T) for _ in range(B)]
+    dims, lens, pt, K, V, q, k, v, parents = case(spd, rng, lens, T, 4, 2, 64, 16, trees)
+    args = (dims, T, q, K, V, dev(pt))
+    rest = (k, v, dev(parents.astype(np.int32)))
+    room = pt.shape[1] * 16
+    clean = lens.copy()
+    clean[[7, 250, 499]] = 0
+    bad = clean.copy()
+    bad[[7, 250, 499]] = room + 1, -1, 2 ** 31 - 1
+    want = attend(spd, *args, dev(clean), *rest)
+    assert spd.spd_device_status(clear=True) == 0
+    o, lse = attend(spd, *args, dev(bad), *rest)
+    assert spd.spd_device_status(clear=True) == spd.DEV_BAD_LEN
+    assert bool((o[[7, 250, 499]] == 0).all()) and bool(torch.isneginf(lse[[7, 250, 499]]).all())
+    good = np.setdiff1d(np.arange(B), [7, 250, 499])
+    assert torch.equal(o[good], want[0][good]) and torch.equal(lse[good], want[1][good])
+
+
+@pytest.mark.parametrize("lens,T,H_q,H_kv,D,ps,rows", [
+    ([23545], 51, 8, 2, 128, 16, {0, 17, 50}),      # two units in 76 parts each
+    ([18001], 3, 2, 1, 64, 32, None),               # one in 142
+    ([40003, 300, 0], 33, 4, 1, 128, 64, {0, 31, 32}),
+])
+def test_tree_verify_attn_units_in_many_parts(spd, lens, T, H_q, H_kv, D, ps, rows):
+    """Tens of partials of a row, joined by several threads each."""
+    rng = np.random.default_rng(T)
+    trees = [ref.random_tree(rng, T) for _ in lens]
+    check_case(spd, *case(spd, rng, lens, T, H_q, H_kv, D, ps, trees), rows=rows)
+
+
 @pytest.mark.parametrize("lg_tokens,low,T,G,D", [(17, 1e-4, 32, 8, 64), (20, 7e-4, 32, 8, 64), (22, 1e-4, 32, 8, 64), (21, 1e-4, 29, 8, 128),
                                                  (20, 1e-4, 4, 4, 128), (22, 1e-4, 5, 3, 64)])
 def test_tree_verify_attn_long_sums_of_one_sign(spd, lg_tokens, low, T, G, D):
