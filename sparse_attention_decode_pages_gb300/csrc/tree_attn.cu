@@ -94,9 +94,16 @@ struct Cut {
 };
 
 // Partials: [slot][D / 4][256 rows] float4, then [slot][256 rows] (reference, sum); two slots a CTA, one for the unit
-// that its share begins in and one for the unit that it ends in.
+// that its share begins in and one for the unit that it ends in.  A reference that is NaN: the CTA gave up, and the unit's rows
+// are left as they were.
 constexpr int kSlotRows = 256;
 __host__ __device__ constexpr size_t slot_bytes(int D) { return (size_t)kSlotRows * (D * 4 + 8); }
+__device__ __forceinline__ float* part_o_of(void* ws, int ctas) {
+    return reinterpret_cast<float*>(static_cast<char*>(ws) + ((size_t)ctas * sizeof(Cut) + 255) / 256 * 256);
+}
+__device__ __forceinline__ float2* part_ml_of(void* ws, int ctas, int D) {
+    return reinterpret_cast<float2*>(part_o_of(ws, ctas) + (size_t)2 * ctas * kSlotRows * D);
+}
 
 // What follows from T, G and the page size, worked out once by the host (a division costs a CTA's start more than it looks).
 struct Shape {
@@ -194,6 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ uint32_t s_tmem;
     __shared__ unsigned long long s_odd[kOdd];  // nodes of a piece's tree whose values are not all finite
     __shared__ int s_asked;                     // tiles whose values have been asked for
+    __shared__ int s_gave_up;                   // a softmax warp's wait has run out
     uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
     uint64_t* empty = full + STAGES;
@@ -229,6 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(drain, 1);
         mbar_fence_init();
         s_asked = 0;
+        s_gave_up = 0;
     }
     if (warp == 8 && elect_one()) {
         tma_prefetch_desc(&maps.q);
@@ -341,8 +350,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         w.t0 = s_share.t0;
         w.left = s_share.left;
         w.look(a, sh, s_share.len);
-        float* part_o = reinterpret_cast<float*>(static_cast<char*>(a.ws) + ((size_t)gridDim.x * sizeof(Cut) + 255) / 256 * 256);
-        float2* part_ml = reinterpret_cast<float2*>(part_o + (size_t)2 * gridDim.x * kSlotRows * D);
+        float* part_o = part_o_of(a.ws, (int)gridDim.x);
+        float2* part_ml = part_ml_of(a.ws, (int)gridDim.x, D);
         const uint32_t tmem = s_tmem;
         const uint32_t q_smem = smem_u32(smem + C::OFF_Q), ring_smem = smem_u32(smem + C::OFF_RING);
 
@@ -362,8 +371,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, a.status, a.wait_ns));
                 return ok;
             };
-            // a barrier of the eight softmax warps that no warp can be held at
+            // a barrier of the eight softmax warps that no warp can be held at (a warp that has given up is counted no more)
             auto all_level = [&]() {
+                if (!ok) return;
                 tmem_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(level);
@@ -618,6 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (two) tmem_fence_before();
                 else all_level();  // both have read O and the references
             }
+            if (!ok && lane == 0) *reinterpret_cast<volatile int*>(&s_gave_up) = 1;
         } else if (warp == 8 || warp == 11) {
             other_regs();
             // ======================================================== copies: keys and queries, or values
@@ -957,6 +968,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tmem_fence_after();
     if (warp == 9) tmem_free(s_tmem, C::COLUMNS);
+    if (s_gave_up && tid < kSlotRows) {  // what is in this CTA's slots is not joined
+        float2* ml = part_ml_of(a.ws, (int)gridDim.x, D) + (size_t)2 * blockIdx.x * kSlotRows + tid;
+        ml[0] = ml[kSlotRows] = make_float2(__int_as_float(0x7fffffff), 0.f);
+    }
 }
 
 // Joins the partials of the units that shares' borders cut.  A thread has eight channels of a row and asks for eight partials at
@@ -976,9 +991,8 @@ __global__ void __launch_bounds__(kJoinThreads, SPLIT ? 3 : 4) join_kernel(const
     const int blocks = D / kJoinChannels / groups, chunk = blockIdx.x % (unsigned)chunks, block = blockIdx.x / (unsigned)chunks;
     const int unit = block / blocks, group = (block - unit * blocks) * groups + (SPLIT ? 0 : other);
     const int at = (chunk << lg_rows) + (int)(threadIdx.x & (rows - 1));  // of the unit's two row tiles
-    const float* part_o = reinterpret_cast<const float*>(static_cast<const char*>(a.ws) + ((size_t)ctas * sizeof(Cut) + 255) / 256 * 256);
-    const float2* part_ml = reinterpret_cast<const float2*>(part_o + (size_t)2 * ctas * kSlotRows * D) + at;
-    const float4* part = reinterpret_cast<const float4*>(part_o) + group * 2 * kSlotRows + at;
+    const float2* part_ml = part_ml_of(a.ws, ctas, D) + at;
+    const float4* part = reinterpret_cast<const float4*>(part_o_of(a.ws, ctas)) + group * 2 * kSlotRows + at;
     pdl_wait();
     pdl_trigger();
     const Cut cut = reinterpret_cast<const Cut*>(a.ws)[unit];
@@ -987,6 +1001,7 @@ __global__ void __launch_bounds__(kJoinThreads, SPLIT ? 3 : 4) join_kernel(const
     const int row = at & (kRows - 1), node = (mt + at / kRows) * sh.tpt + row / sh.G;
     const bool valid = mt + at / kRows < sh.row_tiles && row < sh.tpt * sh.G && node < a.T;
     float r = NEG_INF, total = 0.f;
+    bool gone = false;  // a part is not there
     float4 o0 = make_float4(0.f, 0.f, 0.f, 0.f), o1 = o0;
     auto add = [&](float now, float m, float l, float4 x, float4 y) {
         const float w = m == NEG_INF ? 0.f : fast_exp2(m - now);
@@ -1019,7 +1034,10 @@ __global__ void __launch_bounds__(kJoinThreads, SPLIT ? 3 : 4) join_kernel(const
         }
         float now = r;
 #pragma unroll
-        for (int k = 0; k < kJoinAhead; ++k) now = fmaxf(now, ml[k].x);
+        for (int k = 0; k < kJoinAhead; ++k) {
+            now = fmaxf(now, ml[k].x);
+            gone |= ml[k].x != ml[k].x;
+        }
         follow(now);
 #pragma unroll
         for (int k = 0; k < kJoinAhead; ++k) add(now, ml[k].x, ml[k].y, x[k], y[k]);
@@ -1028,16 +1046,19 @@ __global__ void __launch_bounds__(kJoinThreads, SPLIT ? 3 : 4) join_kernel(const
         if (split > 0) {
             s_o[threadIdx.x][0] = o0;
             s_o[threadIdx.x][1] = o1;
-            s_ml[threadIdx.x] = make_float2(r, total);
+            s_ml[threadIdx.x] = make_float2(gone ? __int_as_float(0x7fffffff) : r, total);
         }
         __syncthreads();
         if (split > 0) return;
         float now = r;
-        for (int i = threadIdx.x + rows; i < kJoinThreads; i += rows) now = fmaxf(now, s_ml[i].x);
+        for (int i = threadIdx.x + rows; i < kJoinThreads; i += rows) {
+            now = fmaxf(now, s_ml[i].x);
+            gone |= s_ml[i].x != s_ml[i].x;
+        }
         follow(now);
         for (int i = threadIdx.x + rows; i < kJoinThreads; i += rows) add(now, s_ml[i].x, s_ml[i].y, s_o[i][0], s_o[i][1]);
     }
-    if (!valid) return;
+    if (!valid || gone) return;
     const float inv = total == 0.f ? 0.f : 1.f / total;
     const long long out = ((long long)cut.b * a.T + node) * a.H_q + h * sh.G + row % sh.G;
     *reinterpret_cast<uint4*>(reinterpret_cast<bf16*>(a.o) + out * D + group * kJoinChannels) =

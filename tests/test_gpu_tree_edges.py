@@ -142,6 +142,39 @@ def test_tree_verify_attn_a_limit_shorter_than_a_part(spd):
         spd.spd_set_wait_limit_ns(usual)
 
 
+@pytest.mark.parametrize("lens,T,H_q,H_kv,D", [([700, 300], 9, 8, 2, 128), ([700, 300], 64, 4, 1, 128), ([2000, 0], 50, 8, 1, 64),
+                                               ([9000], 5, 4, 1, 64), (list(range(0, 4000, 50)), 20, 8, 2, 128), (list(range(0, 4000, 50)), 50, 8, 2, 64)])
+@pytest.mark.parametrize("limit_ns", [1, 1500])
+def test_tree_verify_attn_writes_nothing_of_parts_that_are_late(spd, lens, T, H_q, H_kv, D, limit_ns):
+    """Whatever the limit, each output is the usual one's or left as it was (with the timeout bit set), also where partials are
+    joined and the workspace holds those of another call."""
+    import torch
+    rng = np.random.default_rng(T)
+    dims, lens, pt, K, V, q, k, v, parents = case(spd, rng, lens, T, H_q, H_kv, D, 16, [ref.random_tree(rng, T) for _ in lens])
+    args = (dims, T, q, K, V, dev(pt), dev(lens), k, v, dev(parents.astype(np.int32)))
+    ws = spd.workspace(spd.spd_tree_verify_workspace_size(dims, T))
+    want = attend(spd, *args, ws=ws)
+    other = (dims, T, torch.randn_like(q.contiguous()), *args[3:])
+    assert spd.spd_device_status(clear=True) == 0
+    usual = spd.spd_wait_limit_ns()
+    for _ in range(8):
+        attend(spd, *other, ws=ws)
+        torch.cuda.synchronize()
+        try:
+            spd.spd_set_wait_limit_ns(limit_ns)
+            got = attend(spd, *args, ws=ws)  # (outputs that begin as NaN)
+            status = spd.spd_device_status(clear=True)
+        finally:
+            spd.spd_set_wait_limit_ns(usual)
+        missing = [torch.isnan(x) for x in got]
+        for x, y, m in zip(got, want, missing):
+            assert torch.equal(x[~m], y[~m])
+        assert status in (0, spd.DEV_TIMEOUT) and (status or not any(bool(m.any()) for m in missing))
+    for x, y in zip(attend(spd, *args, ws=ws), want):
+        assert torch.equal(x, y)
+    assert spd.spd_device_status(clear=True) == 0
+
+
 @pytest.mark.parametrize("B", [385, 800])
 def test_tree_verify_attn_more_sequences_than_a_cta_has_threads(spd, B):
     """Short sequences of unequal lengths, several empty: a thread's run of them where shares are cut."""
