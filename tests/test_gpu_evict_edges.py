@@ -83,6 +83,46 @@ def test_kv_weights_update_wide_tables_and_paths_with_selections(spd, lens, T, H
     update(spd, np.random.default_rng(T * 5 + pages), lens, T, H_q, H_kv, D, ps, tokens, with_path, pages)
 
 
+@pytest.mark.parametrize("T,pages,tokens", [(2, 0, 0), (40, 0, 0), (3, 40, 0), (1, 0, 65536)])
+@pytest.mark.parametrize("limit_ns", [1, 1500])
+def test_kv_weights_update_writes_nothing_of_tokens_that_are_late(spd, T, pages, tokens, limit_ns):
+    """Whatever the limit, a weight is the usual one or left as it was, with the timeout bit set."""
+    import torch
+    rng = np.random.default_rng(T)
+    H_q, H_kv, D, ps = 8, 2, 128, 16
+    lens, pt, mp, n, K, V = paged(rng, rng.integers(T, 6000, 40), ps, H_kv, D)
+    B = len(lens)
+    if tokens // ps > mp:
+        pt = np.concatenate([pt, np.full((B, tokens // ps - mp), -1, np.int32)], 1)
+        mp = tokens // ps
+    q, lse = bf(rng.standard_normal((B, T, H_q, D))), dev(rng.uniform(4, 9, (B, T, H_q)).astype(np.float32))
+    args = {}
+    if pages:
+        nsel = np.minimum(pages, -(-lens // ps))[:, None].repeat(H_kv, 1).astype(np.int32)
+        args = dict(sel=dev(np.tile(np.arange(pages, dtype=np.int32), (B, H_kv, 1))), nsel=dev(nsel))
+    w_in = torch.rand((B, H_kv, mp * ps), device="cuda")
+    d_pt, d_lens = dev(pt), dev(lens)
+
+    def update():
+        w = torch.full_like(w_in, -1.0)
+        spd.kv_weights_update(spd.dims_of(B, H_q, H_kv, D, ps, mp, n), T, q, lse, K, d_pt, d_lens, w, w_in=w_in, **args)
+        return w, spd.spd_device_status(clear=True)
+
+    want, status = update()
+    assert status == 0
+    usual = spd.spd_wait_limit_ns()
+    try:
+        spd.spd_set_wait_limit_ns(limit_ns)
+        for _ in range(6):
+            got, status = update()
+            left = (got == -1.0) & (want != -1.0)
+            assert torch.equal(got[~left], want[~left])
+            assert status in (0, spd.DEV_TIMEOUT) and (status or not bool(left.any()))
+    finally:
+        spd.spd_set_wait_limit_ns(usual)
+    assert torch.equal(update()[0], want)
+
+
 @pytest.mark.parametrize("spare", [0, 4000])
 def test_kv_evict_of_sequences_that_share_pages(spd, spare):
     """Three sequences begin with the same physical pages; each keeps its own choice of them, and they stay as they were."""
