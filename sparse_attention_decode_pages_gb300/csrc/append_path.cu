@@ -5,8 +5,9 @@
 // As the append of consecutive tokens: one CTA for a (sequence, touched page), one warp a KV head, every
 // row of the page visited once.  Rows of the path are read from the nodes' rows and stored
 // into the cache, older ones are read from it, and the channel-wise minima and maxima are formed on the
-// way.  What is read from the cache and what is written are different rows.  Bound by latency (length, path, page
-// table, rows, one behind the other): 2.7 us for one path, 8.3 us for 256 out of trees of 64 nodes.
+// way.  What is read from the cache and what is written are different rows.  Up to about 128 paths it is bound by latency (length, path,
+// page table, rows, one behind the other): 2.7 us for one path in a run of calls, 3.5 for 64, 3.8 for 128; behind that by
+// rounds of CTAs, of which a sequence has as many as its tree could touch pages: 5.9 for 256 paths out of 64 nodes, 5.4 out of 8.
 #include "common.cuh"
 #include "kernels.h"
 

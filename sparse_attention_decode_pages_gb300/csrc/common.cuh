@@ -37,7 +37,8 @@ __device__ __forceinline__ unsigned long long globaltimer_ns() {
     return t;
 }
 
-// Programmatic dependent launch.  Every kernel of the library is launched so
+// Programmatic dependent launch.  Every kernel of the library but the eviction's
+// choice and its larger moves (evict.cu says why) is launched so
 // that it may start while the previous kernel on the stream finishes; before
 // its first access to global memory it waits for that kernel (and so, in
 // turn, everything before it) to complete, and early on it lets the next

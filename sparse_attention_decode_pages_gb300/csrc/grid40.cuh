@@ -57,7 +57,7 @@ __device__ __forceinline__ u64 scaled_floor(float u, u64 total) {
 // Sums of floor(2^40 v) of many values of any size, at four multiply-adds for two of them and no conversion:
 // with t = v 2^20 + 2^23 rounded towards zero, t - 2^23 is floor(2^20 v) and also lies in t's low bits; what it leaves of
 // v is exact, and its next 20 bits are found the same way.  Values above 1 count as 1, negative ones and NaN as
-// 0.  take() is good for 4,096 values before total().
+// 0.  take() is good for 4,095 values before total() (4,096 ones are 2^32).
 struct GridSum {
     unsigned hi = 0, lo = 0, n = 0;
     __device__ __forceinline__ void take(float2 v) {

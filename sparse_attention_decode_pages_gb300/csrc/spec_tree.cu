@@ -14,8 +14,9 @@
 // there counts), every warp adds up the W sums and tries the children, a lane each, all warps alike, and goes on to
 // the next row.  Two sets of sums in turn suffice: a warp sends those of step k + 2 when it has every warp's of step k + 1,
 // which that warp sent after it had read step k's.  At the end the runs' sums tell which warp holds the drawn
-// token; it reads its run once more.  (64 sequences of 151,936 tokens, trees of 31 nodes, walks of up to 11 steps: 37 to 40 us, a
-// step 3.5; one sequence, 8 nodes: 7.7 us.)
+// token; it reads its run once more.  (64 sequences of 151,936 tokens, inputs that are not in the L2: one node, that is one row's sum and the
+// draw, 19 us; trees of 8 nodes, longest walks of 4 or 5, 34; of 31 nodes, longest walks of 5 to 11, 43: the start is nearly half, a
+// further step 2 to 5 us.  One sequence, 8 nodes: 8.1 us, 9.6 cold.)
 #include <cooperative_groups.h>
 
 #include <atomic>
@@ -397,8 +398,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) accept_tree_kernel(TreeAccept
 }  // namespace
 
 // CTAs of a cluster: as many as let every sequence's cluster run at once, up to 16.  One sequence of a 151,936-token
-// vocabulary, 8 / 16 CTAs: 13.1 / 11.4 us; 19: 17.6 / 18.5; 64, trees of 31 nodes, walks of up to 11: 4 / 8 / 16 CTAs 50.6 / 45.1 / 44.9;
-// 150: 2 / 4 CTAs 67.7 / 73.7; 400 sequences, 32,000 tokens: 1 / 2 / 4 CTAs 39.6 / 39.1 / 43.3.
+// vocabulary, 4 / 8 / 16 CTAs: 13.9 / 10.9 / 9.5 us; 19: 22.3 / 16.8 / 19.6; 64, trees of 31 nodes: 47.1 / 45.7 / 43.0; 150: 2 / 4 / 8 CTAs
+// 63.9 / 70.0 / 55.5; 400 sequences, 32,000 tokens: 1 / 2 / 4 CTAs 47.8 / 35.7 / 38.9.  (So twice as many would be the better rule for
+// most batches, by up to a quarter.)
 cudaError_t launch_spec_accept_tree(const TreeAcceptArgs& a, int num_sms, cudaStream_t st) {
     static std::atomic<bool> known[64][2];
     if (a.B <= 0) return cudaSuccess;

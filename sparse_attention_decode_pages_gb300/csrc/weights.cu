@@ -263,7 +263,8 @@ __global__ void __launch_bounds__(kThreads, 3) weights_kernel(const WeightsArgs 
 // The same for many query rows: S = K Q^T on the 5th-generation tensor cores, M = 128 tokens by N = up to 128 rows, K = channels, so
 // that a thread has one token (a lane of tensor memory) and adds up its rows' weights by itself.  Eight warps do that, four a
 // tile of tokens, two tiles in turn; a warp copies the keys, a page a box, and one issues the products.  Two CTAs an SM.
-// Bound by memory up to 128 rows, by the exponentials (16 an SM and cycle) behind that.
+// Bound by memory up to 128 rows (16 sequences of 16,384 tokens, 64 rows 93 us, 128 rows 105); behind that a tile's turns of products and
+// weights follow one another (256 rows 246, 512 rows 472: 15 exponentials an SM and ns, a quarter of what an SM can).
 constexpr int kTileThreads = 320, kTileTokens = 128, kTileRows = 128;
 constexpr size_t kTileLeastSmem = 78 * 1024;  // no third CTA on an SM, whose tensor memory two share
 template <int D>
