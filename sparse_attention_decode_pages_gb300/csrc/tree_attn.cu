@@ -33,7 +33,7 @@
 // 467 to 476 us, the measured copy rate).  With 256 rows (64 nodes) the hand-overs between softmax and products: a pair of tiles takes
 // 3,325 cycles, its products 2,048 of them, and their operands and copies keep shared memory busy for as many.  598 to 633 us in a
 // run of ten calls, 634 to 683 in longer ones, where the power limit takes the SM clock to 1.46 to 1.6 GHz as well; at that clock a large
-// library product does 1,718 TFLOP/s, this 1,243 (557 us in runs of a few calls).  One sequence of 131,001 tokens, 61 nodes: 102 us, 108
+// library product does 1,718 TFLOP/s, this 1,243.  One sequence of 131,001 tokens, 61 nodes: 102 us, 108
 // with cold inputs, 110 to 116 in long runs; of 1,003, 8 nodes: 11.5 us, 15 cold, the latency of the two kernels.  With heads of 64
 // channels a tile's softmax is as long and its products half: 64 nodes 430 to 437 us (bytes: 239), 15 nodes 262, 131,001 tokens 84.
 #include <atomic>
